@@ -9,3 +9,5 @@ from .scan import (abi_version, bwd_workspace_bytes, causal_conv1d,  # noqa: F40
                    ssd_chunk_scan, ssd_chunk_state, ssd_decode_step, ssd_dt_cumsum,
                    ssd_scan, ssd_scan_bwd, ssd_scan_fwd, ssd_scan_fwd_host, ssd_state_passing,
                    workspace_bytes)
+from .block import (add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_fwd,  # noqa: F401
+                    block_abi_version, gated_rmsnorm, gated_rmsnorm_bwd, gated_rmsnorm_fwd)

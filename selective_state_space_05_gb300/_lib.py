@@ -72,6 +72,20 @@ SIGNATURES = {
                                _vp]),
 }
 
+# include/ssd_block.h
+SIGNATURES.update({
+    "ssd_block_abi_version": (_i, []),
+    "ssd_add_rmsnorm_fwd": (_i, [_vp, _vp, _vp, _vp, _f, _i64, _i, _i, _i, _vp, _vp, _vp]),
+    "ssd_add_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i]),
+    "ssd_add_rmsnorm_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _f, _i64, _i, _i, _i, _vp, _vp,
+                                 _vp, _vp, _vp, _sz, _vp]),
+    "ssd_gated_rmsnorm_fwd": (_i, [_vp, _st, _vp, _st, _vp, _f, _i64, _i64, _i, _i, _i, _i, _vp,
+                                   _vp]),
+    "ssd_gated_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i64, _i, _i]),
+    "ssd_gated_rmsnorm_bwd": (_i, [_vp, _vp, _st, _vp, _st, _vp, _f, _i64, _i64, _i, _i, _i, _i,
+                                   _vp, _vp, _st, _vp, _vp, _sz, _vp]),
+})
+
 _LIB = None
 
 

@@ -1,0 +1,600 @@
+// RMSNorms of the block: with the residual stream before it, with the gate
+// after its scan, forward and backward.
+//
+// Both are bound by HBM: a forward reads its inputs and writes its outputs
+// once, and so does a backward, which keeps the row it normalises in
+// registers.  One team of warps holds a row (add) or a channel group of a row
+// (gated), eight elements to a slot, so each statistic is one sum over the
+// team.  With n = r * s, s = 1 / sqrt(mean r^2 + eps), g = w dy, the backward
+//   dr = s (g - n mean(g n)) = s (g - r s^2 mean(g r))
+// needs mean r^2 and mean g r, which are summed together: one exchange.
+// The parameters' gradients sum over rows: each team walks rows a grid apart
+// and keeps its columns' sums in registers, writes them once to the
+// workspace, and launch_column_sum joins the teams in a fixed order.
+#include <stdio.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/ssd_block.h"
+#include "ssd_common.cuh"
+#include "ssd_row.cuh"
+
+namespace ssd {
+namespace row {
+
+int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    n = n > 0 ? n : 152;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace row
+
+namespace norm {
+
+constexpr int kFwdWarps = 32, kBwdWarps = 16;   // most warps a row
+
+using row::kVec;
+using row::load_slot;
+using row::store_slot;
+
+// ---------------------------------------------------------------- add_rmsnorm
+
+template <typename T, typename R, bool VEC, int S>
+__global__ void __launch_bounds__(1024)
+    add_fwd_kernel(const T* __restrict__ x, const R* residual, const float* __restrict__ scale,
+                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int warps,
+                   T* __restrict__ y, R* rout) {
+  __shared__ row::TeamSums sums;
+  const int nt = warps * 32;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / nt) + team;
+  const bool live = r < rows;
+  float v[S][kVec];
+  float ss = 0.f;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (live) {
+      load_slot<VEC>(x + r * dim, s, t, nt, dim, v[s]);
+      if (scale) {
+        float c[kVec];
+        load_slot<VEC>(scale, s, t, nt, dim, c);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[s][j] *= c[j];
+      }
+      if (residual) {
+        float q[kVec];
+        load_slot<VEC>(residual + r * dim, s, t, nt, dim, q);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[s][j] += q[j];
+      }
+      store_slot<VEC>(rout + r * dim, s, t, nt, dim, v[s]);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        v[s][j] = row::stored(v[s][j], (const R*)nullptr);
+        ss = fmaf(v[s][j], v[s][j], ss);
+      }
+    }
+  }
+  const float rstd = rsqrtf(row::team_sum2(ss, 0.f, sums, 0, team, warps).x / (float)dim + eps);
+  if (!live) return;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    float w[kVec];
+    load_slot<VEC>(weight, s, t, nt, dim, w);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[s][j] = v[s][j] * rstd * w[j];
+    store_slot<VEC>(y + r * dim, s, t, nt, dim, v[s]);
+  }
+}
+
+// Partial sums of team q of the grid: part[q * 2 * dim + c] for dweight, and
+// dim further for dscale.
+template <typename T, typename R, bool VEC, int S>
+__global__ void __launch_bounds__(kBwdWarps * 32)
+    add_bwd_kernel(const T* __restrict__ dy, const R* dres_out, const R* __restrict__ rin,
+                   const T* __restrict__ x, const float* __restrict__ scale,
+                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int warps,
+                   T* __restrict__ dx, R* dres, float* __restrict__ part) {
+  __shared__ row::TeamSums sums;
+  const int nt = warps * 32;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
+  float dw[S][kVec], ds[S][kVec];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) dw[s][j] = ds[s][j] = 0.f;
+  int buf = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < rows; r0 += (int64_t)gridDim.x * teams) {
+    const int64_t r = r0 + team;
+    const bool live = r < rows;
+    float rv[S][kVec], g[S][kVec];
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (live) {
+        float w[kVec];
+        load_slot<VEC>(rin + r * dim, s, t, nt, dim, rv[s]);
+        load_slot<VEC>(dy + r * dim, s, t, nt, dim, g[s]);
+        load_slot<VEC>(weight, s, t, nt, dim, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          c1 = fmaf(rv[s][j], rv[s][j], c1);
+          c2 = fmaf(g[s][j] * w[j], rv[s][j], c2);
+        }
+      }
+    }
+    const float2 c = row::team_sum2(c1, c2, sums, buf, team, warps);
+    buf ^= 1;
+    if (!live) continue;
+    const float rstd = rsqrtf(c.x / (float)dim + eps);
+    const float k = rstd * rstd * (c.y / (float)dim);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float w[kVec], d[kVec];
+      load_slot<VEC>(weight, s, t, nt, dim, w);
+      if (dres_out) {
+        load_slot<VEC>(dres_out + r * dim, s, t, nt, dim, d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) d[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        dw[s][j] = fmaf(g[s][j], rv[s][j] * rstd, dw[s][j]);
+        d[j] = fmaf(rstd, fmaf(-rv[s][j], k, g[s][j] * w[j]), d[j]);
+      }
+      if (dres) store_slot<VEC>(dres + r * dim, s, t, nt, dim, d);
+      if (scale) {
+        float xv[kVec], sc[kVec];
+        load_slot<VEC>(x + r * dim, s, t, nt, dim, xv);
+        load_slot<VEC>(scale, s, t, nt, dim, sc);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          ds[s][j] = fmaf(d[j], xv[j], ds[s][j]);
+          d[j] *= sc[j];
+        }
+      }
+      if (dx) store_slot<VEC>(dx + r * dim, s, t, nt, dim, d);
+    }
+  }
+  float* p = part + ((int64_t)blockIdx.x * teams + team) * 2 * dim;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    store_slot<VEC>(p, s, t, nt, dim, dw[s]);
+    if (scale) store_slot<VEC>(p + dim, s, t, nt, dim, ds[s]);
+  }
+}
+
+// -------------------------------------------------------------- gated_rmsnorm
+
+struct Rows {   // rows of [batch, seqlen, ...] views
+  uint32_t rows, seqlen;
+  TokStride y, z, dz;
+};
+__device__ __forceinline__ int64_t row_off(const TokStride& s, uint32_t r, uint32_t seqlen) {
+  const uint32_t b = r / seqlen;
+  return (int64_t)b * s.b + (int64_t)(r - b * seqlen) * s.t;
+}
+
+template <typename T, bool VEC, int S>
+__global__ void __launch_bounds__(1024)
+    gated_fwd_kernel(const T* y, const T* __restrict__ z, const float* __restrict__ weight,
+                     float eps, Rows rw, int dim, int gs, int warps, int before, T* out) {
+  __shared__ row::TeamSums sums;
+  const int nt = warps * 32;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / nt) + team;
+  const bool live = r < rw.rows;
+  const int c0 = blockIdx.y * gs;
+  float v[S][kVec], gate[S][kVec];
+  float ss = 0.f;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (live) {
+      load_slot<VEC>(y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, v[s]);
+      if (z) {
+        load_slot<VEC>(z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, gate[s]);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) gate[s][j] *= row::sigmoid_f(gate[s][j]);
+        if (!before) {
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) v[s][j] *= gate[s][j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) ss = fmaf(v[s][j], v[s][j], ss);
+    }
+  }
+  const float rstd = rsqrtf(row::team_sum2(ss, 0.f, sums, 0, team, warps).x / (float)gs + eps);
+  if (!live) return;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    float w[kVec];
+    load_slot<VEC>(weight + c0, s, t, nt, gs, w);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      v[s][j] = v[s][j] * rstd * w[j];
+      if (z && before) v[s][j] *= gate[s][j];
+    }
+    store_slot<VEC>(out + r * dim + c0, s, t, nt, gs, v[s]);
+  }
+}
+
+// With e = silu(z) (1 without z), e' its derivative, s = 1 / rms:
+//   gate first:  u = y e,  g = w dout,  du = s (g - u s^2 mean(g u)),
+//                dy = du e,  dz = du y e',  dw = sum dout u s
+//   norm first:  g = w dout e,  dy = s (g - y s^2 mean(g y)),
+//                dz = dout w y s e',  dw = sum dout e y s
+// Partial dweight of team q of the grid's x: part[q * dim + c].
+template <typename T, bool VEC, int S>
+__global__ void __launch_bounds__(kBwdWarps * 32)
+    gated_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ y, const T* __restrict__ z,
+                     const float* __restrict__ weight, float eps, Rows rw, int dim, int gs,
+                     int warps, int before, T* __restrict__ dy, T* __restrict__ dz,
+                     float* __restrict__ part) {
+  __shared__ row::TeamSums sums;
+  const int nt = warps * 32;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
+  const int c0 = blockIdx.y * gs;
+  float dw[S][kVec];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) dw[s][j] = 0.f;
+  int buf = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < rw.rows;
+       r0 += (int64_t)gridDim.x * teams) {
+    const int64_t r = r0 + team;
+    const bool live = r < rw.rows;
+    float yv[S][kVec], zv[S][kVec], go[S][kVec];
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (live) {
+        float w[kVec];
+        load_slot<VEC>(y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, yv[s]);
+        load_slot<VEC>(dout + r * dim + c0, s, t, nt, gs, go[s]);
+        if (z) load_slot<VEC>(z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, zv[s]);
+        load_slot<VEC>(weight + c0, s, t, nt, gs, w);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          const float e = z ? zv[s][j] * row::sigmoid_f(zv[s][j]) : 1.f;
+          const float u = before ? yv[s][j] : yv[s][j] * e;
+          const float g = before ? go[s][j] * w[j] * e : go[s][j] * w[j];
+          c1 = fmaf(u, u, c1);
+          c2 = fmaf(g, u, c2);
+        }
+      }
+    }
+    const float2 c = row::team_sum2(c1, c2, sums, buf, team, warps);
+    buf ^= 1;
+    if (!live) continue;
+    const float rstd = rsqrtf(c.x / (float)gs + eps);
+    const float k = rstd * rstd * (c.y / (float)gs);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      float w[kVec], dyv[kVec], dzv[kVec];
+      load_slot<VEC>(weight + c0, s, t, nt, gs, w);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float sg = z ? row::sigmoid_f(zv[s][j]) : 1.f;
+        const float e = z ? zv[s][j] * sg : 1.f;
+        const float de = z ? sg * (1.f + zv[s][j] * (1.f - sg)) : 0.f;
+        const float gw = go[s][j] * w[j];
+        if (before) {
+          const float n = yv[s][j] * rstd;
+          dyv[j] = rstd * fmaf(-yv[s][j], k, gw * e);
+          dzv[j] = gw * n * de;
+          dw[s][j] = fmaf(go[s][j] * e, n, dw[s][j]);
+        } else {
+          const float u = yv[s][j] * e;
+          const float du = rstd * fmaf(-u, k, gw);
+          dyv[j] = du * e;
+          dzv[j] = du * yv[s][j] * de;
+          dw[s][j] = fmaf(go[s][j], u * rstd, dw[s][j]);
+        }
+      }
+      store_slot<VEC>(dy + r * dim + c0, s, t, nt, gs, dyv);
+      if (z)
+        store_slot<VEC>(dz + row_off(rw.dz, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, dzv);
+    }
+  }
+  float* p = part + ((int64_t)blockIdx.x * teams + team) * dim + c0;
+#pragma unroll
+  for (int s = 0; s < S; ++s) store_slot<VEC>(p, s, t, nt, gs, dw[s]);
+}
+
+// ----------------------------------------------------------------- column sum
+
+constexpr int kSumRows = 8;
+
+// 32 columns a CTA, kSumRows warps that walk the rows kSumRows apart.
+__global__ void __launch_bounds__(32 * kSumRows)
+    column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t ld, int64_t n,
+                      float* __restrict__ out) {
+  __shared__ float acc[kSumRows][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < n) {
+#pragma unroll 4
+    for (int64_t r = w; r < rows; r += kSumRows) s += part[r * ld + c];
+  }
+  acc[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < n) {
+#pragma unroll
+    for (int i = 1; i < kSumRows; ++i) s += acc[i][lane];
+    out[c] = s;
+  }
+}
+
+// Teams at once in a CTA whose row takes one warp, and the CTAs of a
+// backward's grid an SM; the workspace holds one partial row a team.
+constexpr int kTeams = 4;
+constexpr int kBwdCtasPerSm = 4;
+
+int64_t bwd_ctas(int64_t rows, const row::Shape& sh, int groups) {
+  const int64_t need = (rows + sh.teams - 1) / sh.teams;
+  const int64_t most = std::max<int64_t>(1, (int64_t)row::sm_count() * kBwdCtasPerSm / groups);
+  return std::min(need, most);
+}
+
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+int bad(int code, const char* msg) { return set_error(code, msg); }
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return SSD_OK;
+  char m[256];
+  snprintf(m, sizeof(m), "%s launch: %s", what, cudaGetErrorString(e));
+  return set_error(SSD_ERR_CUDA, m);
+}
+
+bool known(ssd_dtype_t t) { return t == SSD_DTYPE_F32 || t == SSD_DTYPE_BF16; }
+size_t esize(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
+bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int check_add(int64_t rows, int dim, float eps, ssd_dtype_t dt, ssd_dtype_t rt) {
+  if (!known(dt) || !known(rt)) return bad(SSD_ERR_ARG, "unknown dtype");
+  if (dt == SSD_DTYPE_F32 && rt != SSD_DTYPE_F32)
+    return bad(SSD_ERR_ARG, "an fp32 x takes an fp32 residual");
+  if (rows < 1 || dim < 1) return bad(SSD_ERR_ARG, "rows and dim must be >= 1");
+  if (rows > 2147483647LL) return bad(SSD_ERR_UNSUPPORTED, "rows must be below 2^31");
+  if (dim > row::kMaxRow) return bad(SSD_ERR_UNSUPPORTED, "dim must be at most 16384");
+  if (!(eps >= 0.f)) return bad(SSD_ERR_ARG, "eps must be >= 0");
+  return SSD_OK;
+}
+
+int check_gated(int64_t batch, int64_t seqlen, int dim, int gs, float eps, ssd_dtype_t dt) {
+  if (!known(dt)) return bad(SSD_ERR_ARG, "unknown dtype");
+  if (batch < 1 || seqlen < 1 || dim < 1 || gs < 1 || dim % gs != 0)
+    return bad(SSD_ERR_ARG, "batch, seqlen, dim >= 1 and group_size dividing dim are required");
+  if (batch > 2147483647LL || seqlen > 2147483647LL || batch * seqlen > 2147483647LL)
+    return bad(SSD_ERR_UNSUPPORTED, "batch * seqlen must be below 2^31");
+  if (gs > row::kMaxRow) return bad(SSD_ERR_UNSUPPORTED, "group_size must be at most 16384");
+  if (dim / gs > 65535) return bad(SSD_ERR_UNSUPPORTED, "at most 65535 groups");
+  if (!(eps >= 0.f)) return bad(SSD_ERR_ARG, "eps must be >= 0");
+  return SSD_OK;
+}
+
+bool bad_stride(const ssd_stride_t& s) {
+  return s.batch < 0 || s.token < 0 || s.batch > (1LL << 40) || s.token > (1LL << 40);
+}
+bool wide_stride(const ssd_stride_t& s, size_t e) {
+  return (s.batch * (int64_t)e) % 16 == 0 && (s.token * (int64_t)e) % 16 == 0;
+}
+
+}  // namespace norm
+
+cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
+                              cudaStream_t st) {
+  norm::column_sum_kernel<<<(unsigned)((n + 31) / 32), 32 * norm::kSumRows, 0, st>>>(part, rows,
+                                                                                     ld, n, out);
+  return cudaGetLastError();
+}
+
+}  // namespace ssd
+
+using namespace ssd;
+using namespace ssd::norm;
+
+// Launches the wide or one-element instance with the shape's slots.
+#define SSD_NORM_FWD(LAUNCH)       \
+  do {                             \
+    if (vec && sh.slots == 1) LAUNCH(true, 1);  \
+    else if (vec) LAUNCH(true, 2);              \
+    else if (sh.slots == 1) LAUNCH(false, 1);   \
+    else LAUNCH(false, 2);                      \
+  } while (0)
+#define SSD_NORM_BWD(LAUNCH)       \
+  do {                             \
+    if (vec && sh.slots == 1) LAUNCH(true, 1);      \
+    else if (vec && sh.slots == 2) LAUNCH(true, 2); \
+    else if (vec) LAUNCH(true, 4);                  \
+    else if (sh.slots == 1) LAUNCH(false, 1);       \
+    else if (sh.slots == 2) LAUNCH(false, 2);       \
+    else LAUNCH(false, 4);                          \
+  } while (0)
+
+extern "C" {
+
+int ssd_block_abi_version(void) { return SSD_BLOCK_ABI_VERSION; }
+
+int ssd_add_rmsnorm_fwd(const void* x, const void* residual, const float* scale,
+                        const float* weight, float eps, int64_t rows, int dim, ssd_dtype_t dtype,
+                        ssd_dtype_t residual_dtype, void* y, void* residual_out, void* stream) {
+  const int c = check_add(rows, dim, eps, dtype, residual_dtype);
+  if (c != SSD_OK) return c;
+  if (!x || !weight || !y || !residual_out)
+    return bad(SSD_ERR_NULL, "x, weight, y and residual_out are required");
+  const size_t e = esize(dtype), re = esize(residual_dtype);
+  if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(residual, re) ||
+      !aligned_to(residual_out, re) || !aligned_to(weight, 4) || !aligned_to(scale, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  const bool vec = dim % kVec == 0 && row::wide(x) && row::wide(residual) && row::wide(y) &&
+                   row::wide(residual_out) && row::wide(scale) && row::wide(weight);
+  const row::Shape sh = row::shape_for(dim, kFwdWarps, kTeams);
+  const unsigned grid = (unsigned)((rows + sh.teams - 1) / sh.teams);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  using bf = __nv_bfloat16;
+#define SSD_ADD_FWD(T, R, V, S)                                                              \
+  add_fwd_kernel<T, R, V, S><<<grid, sh.threads(), 0, st>>>(                                 \
+      static_cast<const T*>(x), static_cast<const R*>(residual), scale, weight, eps,         \
+      (uint32_t)rows, dim, sh.warps, static_cast<T*>(y), static_cast<R*>(residual_out))
+#define SSD_ADD_FWD_FF(V, S) SSD_ADD_FWD(float, float, V, S)
+#define SSD_ADD_FWD_BF(V, S) SSD_ADD_FWD(bf, float, V, S)
+#define SSD_ADD_FWD_BB(V, S) SSD_ADD_FWD(bf, bf, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_ADD_FWD_FF);
+  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_ADD_FWD_BF);
+  else SSD_NORM_FWD(SSD_ADD_FWD_BB);
+  return launched("add_rmsnorm_fwd");
+}
+
+size_t ssd_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int dim) {
+  if (check_add(rows, dim, 0.f, SSD_DTYPE_F32, SSD_DTYPE_F32) != SSD_OK) return 0;
+  const row::Shape sh = row::shape_for(dim, kBwdWarps, kTeams);
+  return up256((size_t)bwd_ctas(rows, sh, 1) * sh.teams * 2 * dim * sizeof(float));
+}
+
+int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* residual_out,
+                        const void* x, const float* scale, const float* weight, float eps,
+                        int64_t rows, int dim, ssd_dtype_t dtype, ssd_dtype_t residual_dtype,
+                        void* dx, void* dresidual, float* dweight, float* dscale, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const int c = check_add(rows, dim, eps, dtype, residual_dtype);
+  if (c != SSD_OK) return c;
+  if (!dy || !residual_out || !weight || !dweight || !workspace)
+    return bad(SSD_ERR_NULL, "dy, residual_out, weight, dweight and workspace are required");
+  if ((scale != nullptr) != (dscale != nullptr) || (scale && !x))
+    return bad(SSD_ERR_NULL, "scale takes x and dscale, and dscale takes scale");
+  const size_t e = esize(dtype), re = esize(residual_dtype);
+  if (!aligned_to(dy, e) || !aligned_to(x, e) || !aligned_to(dx, e) ||
+      !aligned_to(dresidual_out, re) || !aligned_to(residual_out, re) ||
+      !aligned_to(dresidual, re) || !aligned_to(weight, 4) || !aligned_to(scale, 4) ||
+      !aligned_to(dweight, 4) || !aligned_to(dscale, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (!aligned_to(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace: 256-byte aligned");
+  if (workspace_bytes < ssd_add_rmsnorm_bwd_workspace_bytes(rows, dim))
+    return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const bool vec = dim % kVec == 0 && row::wide(dy) && row::wide(dresidual_out) &&
+                   row::wide(residual_out) && row::wide(x) && row::wide(dx) &&
+                   row::wide(dresidual) && row::wide(scale) && row::wide(weight);
+  const row::Shape sh = row::shape_for(dim, kBwdWarps, kTeams);
+  const unsigned grid = (unsigned)bwd_ctas(rows, sh, 1);
+  float* part = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  using bf = __nv_bfloat16;
+#define SSD_ADD_BWD(T, R, V, S)                                                               \
+  add_bwd_kernel<T, R, V, S><<<grid, sh.threads(), 0, st>>>(                                  \
+      static_cast<const T*>(dy), static_cast<const R*>(dresidual_out),                        \
+      static_cast<const R*>(residual_out), static_cast<const T*>(x), scale, weight, eps,      \
+      (uint32_t)rows, dim, sh.warps, static_cast<T*>(dx), static_cast<R*>(dresidual), part)
+#define SSD_ADD_BWD_FF(V, S) SSD_ADD_BWD(float, float, V, S)
+#define SSD_ADD_BWD_BF(V, S) SSD_ADD_BWD(bf, float, V, S)
+#define SSD_ADD_BWD_BB(V, S) SSD_ADD_BWD(bf, bf, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_ADD_BWD_FF);
+  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_ADD_BWD_BF);
+  else SSD_NORM_BWD(SSD_ADD_BWD_BB);
+  const int64_t prow = (int64_t)grid * sh.teams;
+  launch_column_sum(part, prow, 2 * dim, dim, dweight, st);
+  if (dscale) launch_column_sum(part + dim, prow, 2 * dim, dim, dscale, st);
+  return launched("add_rmsnorm_bwd");
+}
+
+int ssd_gated_rmsnorm_fwd(const void* y, ssd_stride_t y_stride, const void* z,
+                          ssd_stride_t z_stride, const float* weight, float eps, int64_t batch,
+                          int64_t seqlen, int dim, int group_size, int norm_before_gate,
+                          ssd_dtype_t dtype, void* out, void* stream) {
+  const int c = check_gated(batch, seqlen, dim, group_size, eps, dtype);
+  if (c != SSD_OK) return c;
+  if (!y || !weight || !out) return bad(SSD_ERR_NULL, "y, weight and out are required");
+  const size_t e = esize(dtype);
+  if (!aligned_to(y, e) || !aligned_to(z, e) || !aligned_to(out, e) || !aligned_to(weight, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (bad_stride(y_stride) || (z && bad_stride(z_stride)))
+    return bad(SSD_ERR_ARG, "strides must be in [0, 2^40]");
+  const bool vec = group_size % kVec == 0 && row::wide(y) && row::wide(z) && row::wide(out) &&
+                   row::wide(weight) && wide_stride(y_stride, e) &&
+                   (!z || wide_stride(z_stride, e));
+  const row::Shape sh = row::shape_for(group_size, kFwdWarps, kTeams);
+  Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
+             {z_stride.batch, z_stride.token}, {0, 0}};
+  const dim3 grid((unsigned)((rw.rows + (int64_t)sh.teams - 1) / sh.teams),
+                  (unsigned)(dim / group_size));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define SSD_GATED_FWD(T, V, S)                                                             \
+  gated_fwd_kernel<T, V, S><<<grid, sh.threads(), 0, st>>>(                                \
+      static_cast<const T*>(y), static_cast<const T*>(z), weight, eps, rw, dim, group_size, \
+      sh.warps, norm_before_gate, static_cast<T*>(out))
+#define SSD_GATED_FWD_F(V, S) SSD_GATED_FWD(float, V, S)
+#define SSD_GATED_FWD_B(V, S) SSD_GATED_FWD(__nv_bfloat16, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_GATED_FWD_F);
+  else SSD_NORM_FWD(SSD_GATED_FWD_B);
+  return launched("gated_rmsnorm_fwd");
+}
+
+size_t ssd_gated_rmsnorm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int dim,
+                                             int group_size) {
+  if (check_gated(batch, seqlen, dim, group_size, 0.f, SSD_DTYPE_F32) != SSD_OK) return 0;
+  const row::Shape sh = row::shape_for(group_size, kBwdWarps, kTeams);
+  return up256((size_t)bwd_ctas(batch * seqlen, sh, dim / group_size) * sh.teams * dim *
+               sizeof(float));
+}
+
+int ssd_gated_rmsnorm_bwd(const void* dout, const void* y, ssd_stride_t y_stride, const void* z,
+                          ssd_stride_t z_stride, const float* weight, float eps, int64_t batch,
+                          int64_t seqlen, int dim, int group_size, int norm_before_gate,
+                          ssd_dtype_t dtype, void* dy, void* dz, ssd_stride_t dz_stride,
+                          float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  const int c = check_gated(batch, seqlen, dim, group_size, eps, dtype);
+  if (c != SSD_OK) return c;
+  if (!dout || !y || !weight || !dy || !dweight || !workspace)
+    return bad(SSD_ERR_NULL, "dout, y, weight, dy, dweight and workspace are required");
+  if ((z != nullptr) != (dz != nullptr)) return bad(SSD_ERR_NULL, "z and dz come together");
+  const size_t e = esize(dtype);
+  if (!aligned_to(dout, e) || !aligned_to(y, e) || !aligned_to(z, e) || !aligned_to(dy, e) ||
+      !aligned_to(dz, e) || !aligned_to(weight, 4) || !aligned_to(dweight, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (!aligned_to(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace: 256-byte aligned");
+  if (bad_stride(y_stride) || (z && (bad_stride(z_stride) || bad_stride(dz_stride))))
+    return bad(SSD_ERR_ARG, "strides must be in [0, 2^40]");
+  if (z && ((seqlen > 1 && dz_stride.token < dim) || (batch > 1 && dz_stride.batch < dim)))
+    return bad(SSD_ERR_ARG, "dz: tokens must not overlap");
+  if (workspace_bytes < ssd_gated_rmsnorm_bwd_workspace_bytes(batch, seqlen, dim, group_size))
+    return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const bool vec = group_size % kVec == 0 && row::wide(dout) && row::wide(y) && row::wide(z) &&
+                   row::wide(dy) && row::wide(dz) && row::wide(weight) &&
+                   wide_stride(y_stride, e) &&
+                   (!z || (wide_stride(z_stride, e) && wide_stride(dz_stride, e)));
+  const row::Shape sh = row::shape_for(group_size, kBwdWarps, kTeams);
+  Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
+             {z_stride.batch, z_stride.token}, {dz_stride.batch, dz_stride.token}};
+  const dim3 grid((unsigned)bwd_ctas(rw.rows, sh, dim / group_size),
+                  (unsigned)(dim / group_size));
+  float* part = static_cast<float*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define SSD_GATED_BWD(T, V, S)                                                                \
+  gated_bwd_kernel<T, V, S><<<grid, sh.threads(), 0, st>>>(                                   \
+      static_cast<const T*>(dout), static_cast<const T*>(y), static_cast<const T*>(z), weight, \
+      eps, rw, dim, group_size, sh.warps, norm_before_gate, static_cast<T*>(dy),               \
+      static_cast<T*>(dz), part)
+#define SSD_GATED_BWD_F(V, S) SSD_GATED_BWD(float, V, S)
+#define SSD_GATED_BWD_B(V, S) SSD_GATED_BWD(__nv_bfloat16, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_GATED_BWD_F);
+  else SSD_NORM_BWD(SSD_GATED_BWD_B);
+  launch_column_sum(part, (int64_t)grid.x * sh.teams, dim, dim, dweight, st);
+  return launched("gated_rmsnorm_bwd");
+}
+
+}  // extern "C"

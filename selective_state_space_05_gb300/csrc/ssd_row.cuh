@@ -1,0 +1,175 @@
+// Helpers shared by the row-wise kernels of the block's operators: a team of
+// warps that holds one row (or one channel group of a row) in registers,
+// eight elements to a slot, and the sum over the rows of partial parameter
+// gradients.
+#pragma once
+
+#include "ssd_common.cuh"
+
+namespace ssd {
+namespace row {
+
+constexpr int kVec = 8;   // elements per slot: one 16-byte bf16 or two fp32 vectors
+constexpr int kMaxWarps = 32;
+
+__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
+
+__device__ __forceinline__ void unpack(uint4 w, float (&v)[kVec]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Column of element j of slot s for thread t of a team of nt.  VEC: a slot is
+// eight consecutive columns (one wide access); otherwise a slot's elements are
+// nt apart, so that the team's one-element accesses are consecutive.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int s, int j, int t, int nt) {
+  return VEC ? (s * nt + t) * kVec + j : (s * kVec + j) * nt + t;
+}
+
+// Slot s of a row of n elements; zeros past n (n is a multiple of 8 if VEC).
+template <bool VEC>
+__device__ __forceinline__ void load_slot(const float* p, int s, int t, int nt, int n,
+                                          float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(s, 0, t, nt);
+    if (c < n) {
+      const float4 a = *reinterpret_cast<const float4*>(p + c);
+      const float4 b = *reinterpret_cast<const float4*>(p + c + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int c = col_of<false>(s, j, t, nt);
+      v[j] = c < n ? p[c] : 0.f;
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_slot(const __nv_bfloat16* p, int s, int t, int nt, int n,
+                                          float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(s, 0, t, nt);
+    unpack(c < n ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int c = col_of<false>(s, j, t, nt);
+      v[j] = c < n ? __bfloat162float(p[c]) : 0.f;
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_slot(float* p, int s, int t, int nt, int n,
+                                           const float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(s, 0, t, nt);
+    if (c < n) {
+      *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int c = col_of<false>(s, j, t, nt);
+      if (c < n) p[c] = v[j];
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_slot(__nv_bfloat16* p, int s, int t, int nt, int n,
+                                           const float (&v)[kVec]) {
+  if constexpr (VEC) {
+    const int c = col_of<true>(s, 0, t, nt);
+    if (c < n) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int c = col_of<false>(s, j, t, nt);
+      if (c < n) p[c] = __float2bfloat16_rn(v[j]);
+    }
+  }
+}
+
+// The value as it is stored in type T.
+__device__ __forceinline__ float stored(float v, const float*) { return v; }
+__device__ __forceinline__ float stored(float v, const __nv_bfloat16*) {
+  return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+// Sums of a and b over a team of `warps` consecutive warps (team `team` of
+// the CTA), to every thread of it.  Every thread of the CTA calls it the same
+// number of times; `buf` alternates between 0 and 1 from call to call, so
+// that one barrier a call is enough: a slow reader of one call's sums is past
+// the next call's barrier before their place is written again.
+struct TeamSums {
+  float2 part[2][kMaxWarps];
+};
+__device__ __forceinline__ float2 team_sum2(float a, float b, TeamSums& sm, int buf, int team,
+                                            int warps) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, off);
+    b += __shfl_xor_sync(0xffffffffu, b, off);
+  }
+  if (warps == 1) return make_float2(a, b);
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) sm.part[buf][warp] = make_float2(a, b);
+  __syncthreads();
+  float2 s = make_float2(0.f, 0.f);
+  for (int i = 0; i < warps; ++i) {
+    const float2 p = sm.part[buf][team * warps + i];
+    s.x += p.x;
+    s.y += p.y;
+  }
+  return s;
+}
+
+// How a row of n elements is laid over threads: `warps` warps a row with
+// `slots` slots of eight elements each, `teams` rows at once in a CTA.
+constexpr int kMaxRow = 16384;
+struct Shape {
+  int warps, slots, teams;
+  int threads() const { return warps * teams * 32; }
+};
+// At most max_warps (16 or 32) warps a row: the forwards hold one row (32), the
+// backwards three and the parameters' sums (16, so that a thread may use 128
+// registers).
+inline Shape shape_for(int n, int max_warps, int teams_of_one) {
+  const int vecs = (n + kVec - 1) / kVec, cap = max_warps * 32;
+  Shape s;
+  s.slots = vecs <= cap ? 1 : vecs <= 2 * cap ? 2 : 4;   // n <= kMaxRow
+  s.warps = (vecs + 32 * s.slots - 1) / (32 * s.slots);
+  s.teams = s.warps >= teams_of_one ? 1 : teams_of_one / s.warps;
+  return s;
+}
+
+inline bool wide(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+int sm_count();
+
+}  // namespace row
+
+// out[c] = sum over r < rows of part[r * ld + c], c < n, in a fixed order.
+cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
+                              cudaStream_t st);
+
+}  // namespace ssd

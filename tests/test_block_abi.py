@@ -1,0 +1,91 @@
+"""The block operators' C ABI on the CPU: what each call refuses, before
+anything touches a GPU (the addresses below are never dereferenced), and the
+workspace queries."""
+import math
+
+import pytest
+
+from selective_state_space_05_gb300 import _lib
+
+BF, F32 = _lib.SSD_DTYPE_BF16, _lib.SSD_DTYPE_F32
+ARG, NULL, ALIGN, UNSUPPORTED, WORKSPACE = -1, -2, -3, -4, -5
+S = _lib.Stride
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from selective_state_space_05_gb300 import build
+    build.build()
+    return _lib.load()
+
+
+def caller(lib, name, **defaults):
+    fn = getattr(lib, name)
+
+    def call(**kw):
+        assert not set(kw) - set(defaults), kw
+        return fn(*{**defaults, **kw}.values())
+    return call
+
+
+def test_block_abi_version(lib):
+    assert lib.ssd_block_abi_version() == 1
+
+
+def test_add_rmsnorm_refusals(lib):
+    f = caller(lib, "ssd_add_rmsnorm_fwd", x=16, residual=16, scale=None, weight=16, eps=1e-5,
+               rows=4, dim=8, dtype=BF, rdtype=F32, y=16, rout=16, stream=None)
+    assert f(dtype=9) == ARG and f(rdtype=-1) == ARG
+    assert f(dtype=F32, rdtype=BF) == ARG and b"fp32 residual" in lib.ssd_last_error()
+    assert f(rows=0) == ARG and f(dim=0) == ARG and f(rows=-3) == ARG
+    assert f(eps=-1.0) == ARG and f(eps=math.nan) == ARG
+    assert f(rows=2 ** 31) == UNSUPPORTED and f(dim=16385) == UNSUPPORTED
+    for k in ("x", "weight", "y", "rout"):
+        assert f(**{k: None}) == NULL, k
+    assert f(x=17) == ALIGN and f(residual=18) == ALIGN and f(weight=6) == ALIGN
+    ws = lib.ssd_add_rmsnorm_bwd_workspace_bytes(4, 8)
+    assert ws >= 4 * 2 * 8 * 4 and ws % 256 == 0
+    assert lib.ssd_add_rmsnorm_bwd_workspace_bytes(0, 8) == 0
+    assert lib.ssd_add_rmsnorm_bwd_workspace_bytes(4, 16385) == 0
+    b = caller(lib, "ssd_add_rmsnorm_bwd", dy=16, dro=16, ro=16, x=16, scale=16, weight=16,
+               eps=1e-5, rows=4, dim=8, dtype=BF, rdtype=F32, dx=16, dres=16, dw=16, ds=16,
+               ws=256, wsb=1 << 20, stream=None)
+    assert b(rows=0) == ARG and b(dim=16385) == UNSUPPORTED
+    for k in ("dy", "ro", "weight", "dw", "ws", "ds", "x"):
+        assert b(**{k: None}) == NULL, k
+    assert b(scale=None) == NULL            # dscale without scale
+    assert b(ws=128) == ALIGN and b(dy=1) == ALIGN and b(dres=2) == ALIGN
+    assert b(wsb=ws - 1) == WORKSPACE
+
+
+def test_gated_rmsnorm_refusals(lib):
+    f = caller(lib, "ssd_gated_rmsnorm_fwd", y=16, ys=S(32, 8), z=16, zs=S(32, 8), weight=16,
+               eps=1e-5, batch=2, seqlen=4, dim=8, gs=8, before=0, dtype=BF, out=16, stream=None)
+    assert f(dtype=5) == ARG and f(gs=3) == ARG and f(gs=0) == ARG and f(seqlen=0) == ARG
+    assert f(batch=0) == ARG and f(eps=-0.5) == ARG
+    assert f(ys=S(-1, 8)) == ARG and f(zs=S(32, -8)) == ARG
+    assert f(batch=2 ** 20, seqlen=2 ** 11) == UNSUPPORTED
+    assert f(dim=16392, gs=16392) == UNSUPPORTED and f(dim=65536, gs=1) == UNSUPPORTED
+    for k in ("y", "weight", "out"):
+        assert f(**{k: None}) == NULL, k
+    assert f(z=17) == ALIGN
+    ws = lib.ssd_gated_rmsnorm_bwd_workspace_bytes(2, 4, 8, 8)
+    assert ws > 0 and lib.ssd_gated_rmsnorm_bwd_workspace_bytes(2, 4, 8, 3) == 0
+    b = caller(lib, "ssd_gated_rmsnorm_bwd", dout=16, y=16, ys=S(32, 8), z=16, zs=S(32, 8),
+               weight=16, eps=1e-5, batch=2, seqlen=4, dim=8, gs=8, before=0, dtype=BF, dy=16,
+               dz=16, dzs=S(32, 8), dw=16, ws=256, wsb=1 << 20, stream=None)
+    assert b(gs=3) == ARG and b(dzs=S(32, 4)) == ARG and b(dzs=S(4, 8)) == ARG
+    for k in ("dout", "y", "weight", "dy", "dw", "ws", "z", "dz"):
+        assert b(**{k: None}) == NULL, k
+    assert b(ws=16) == ALIGN and b(wsb=ws - 1) == WORKSPACE
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+
+    import selective_state_space_05_gb300 as ssd
+    x, w = torch.zeros(2, 8), torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA"):
+        ssd.add_rmsnorm_fwd(x, None, w)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        ssd.gated_rmsnorm_fwd(x.half(), None, w)
