@@ -106,6 +106,74 @@ int ssd_gated_rmsnorm_bwd(const void *dout, const void *y, ssd_stride_t y_stride
                           void *dz, ssd_stride_t dz_stride, float *dweight,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Backward of ssd_causal_conv1d (ssd_scan.h) for the upstream gradient dout of
+ * its out, the forward's other arguments as they were.  With pre = the
+ * forward's value before act, recomputed, and dpre = dout * act'(pre):
+ *   dx[b,s,c]    = sum_k weight[c,k] dpre[b, s+width-1-k, c]
+ *   dweight[c,k] = sum_{b,t} dpre[b,t,c] x[b, t-width+1+k, c]
+ *   dbias[c]     = sum_{b,t} dpre[b,t,c]
+ * over the taps that the forward counts (inside the sequence and, with
+ * seq_idx, in token t's document).
+ *   dout, x, dx  [batch, seqlen, channels] x dtype, channels dense, with
+ *                strides as for the forward's x (multiples of 16 bytes); dx may
+ *                be a slice of the projection's gradient, and must not overlap
+ *                x or dout
+ *   dweight      [channels, width] float;  dbias [channels] float or NULL
+ * All written, not accumulated.  channels a multiple of 8, width 1..8; dout,
+ * x and dx 16-byte aligned. */
+size_t ssd_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen,
+                                             int channels, int width);
+int ssd_causal_conv1d_bwd(const void *dout, ssd_stride_t dout_stride,
+                          const void *x, ssd_stride_t x_stride,
+                          const float *weight, const float *bias,
+                          const int32_t *seq_idx, int64_t batch, int64_t seqlen,
+                          int channels, int width, int silu, ssd_dtype_t dtype,
+                          void *dx, ssd_stride_t dx_stride, float *dweight,
+                          float *dbias, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/* One token of the conv per batch row, next to ssd_decode_step:
+ *   out[b,c] = act(bias[c] + sum_{k<width-1} weight[c,k] conv_state[b,k,c]
+ *                  + weight[c,width-1] x[b,c])
+ * and conv_state, the last width-1 inputs of the sequence, oldest first,
+ * moves on by one (in place).  After a prompt it is the prompt's last width-1
+ * inputs (zeros before its start).
+ *   x           [batch, channels] x dtype, rows x_row_stride elements apart
+ *               (a multiple of 16 bytes), e.g. a slice of the projection
+ *   conv_state  [batch, width-1, channels] x dtype (NULL for width 1)
+ *   out         [batch, channels] x dtype, dense
+ * channels a multiple of 8, width 1..8; x, conv_state, out 16-byte aligned. */
+int ssd_causal_conv1d_step(const void *x, int64_t x_row_stride, void *conv_state,
+                           const float *weight, const float *bias, int64_t batch,
+                           int channels, int width, int silu, ssd_dtype_t dtype,
+                           void *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Global gradient norm over many tensors, and clipping by it:
+ *   norm = sqrt(sum over tensors and elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + eps))
+ * grads, sizes, dtypes, outs, out_dtypes are HOST arrays of `count` entries,
+ * read during the call only: device addresses (aligned to their element),
+ * element counts (0 allowed: the tensor is left out) and ssd_dtype_t values,
+ * which may differ from tensor to tensor.  outs NULL: in place; else each
+ * tensor's clipped values go to its own output, of out_dtypes (NULL: the
+ * gradient's own type).  Tensors must not overlap one another.
+ * norm: one float on the device (written).  Squares are summed in fp32 within
+ * a chunk and in double beyond it, and in double throughout where a square
+ * would leave the fp32 range.  A norm that is not finite is not special: an
+ * infinite one gives the factor 0 (and NaN where g is infinite), a NaN one
+ * gives NaN everywhere.  count may be 0 (norm = 0).  max_norm, eps >= 0. */
+size_t ssd_clip_grads_workspace_bytes(int count);
+int ssd_grad_norm(const void *const *grads, const int64_t *sizes,
+                  const int32_t *dtypes, int count, float *norm,
+                  void *workspace, size_t workspace_bytes, void *stream);
+int ssd_clip_grads(const void *const *grads, const int64_t *sizes,
+                   const int32_t *dtypes, int count, void *const *outs,
+                   const int32_t *out_dtypes, float max_norm, float eps,
+                   float *norm, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -84,6 +84,13 @@ SIGNATURES.update({
     "ssd_gated_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i64, _i, _i]),
     "ssd_gated_rmsnorm_bwd": (_i, [_vp, _vp, _st, _vp, _st, _vp, _f, _i64, _i64, _i, _i, _i, _i,
                                    _vp, _vp, _st, _vp, _vp, _sz, _vp]),
+    "ssd_causal_conv1d_bwd_workspace_bytes": (_sz, [_i64, _i64, _i, _i]),
+    "ssd_causal_conv1d_bwd": (_i, [_vp, _st, _vp, _st, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _i,
+                                   _vp, _st, _vp, _vp, _vp, _sz, _vp]),
+    "ssd_causal_conv1d_step": (_i, [_vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _vp]),
+    "ssd_clip_grads_workspace_bytes": (_sz, [_i]),
+    "ssd_grad_norm": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "ssd_clip_grads": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f, _f, _vp, _vp, _sz, _vp]),
 })
 
 _LIB = None

@@ -1,6 +1,7 @@
 """Python binding of the block operators' C ABI (include/ssd_block.h): the
 residual RMSNorm before a block and the gated grouped RMSNorm after its scan,
-with their backwards and a differentiable form of each.
+with their backwards and a differentiable form of each, the causal conv1d's
+backward and one-token step, and gradient clipping.
 
 Argument marshalling only, as in scan.py.  Each operator comes as
 ``<name>_fwd`` and ``<name>_bwd`` (explicit, usable on any stream and inside a
@@ -10,6 +11,7 @@ capturing ``Tensor.backward`` ties the graph to autograd's own streams.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
@@ -276,3 +278,186 @@ def gated_rmsnorm(y: torch.Tensor, z: Optional[torch.Tensor], weight: torch.Tens
     """gated_rmsnorm_fwd as a differentiable torch function: gradients for y,
     z and weight."""
     return _GatedRMSNorm.apply(y, z, weight, group_size, eps, norm_before_gate)
+
+
+# --- causal conv1d: backward, one token --------------------------------------
+
+def causal_conv1d_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                      bias: Optional[torch.Tensor] = None, *,
+                      seq_idx: Optional[torch.Tensor] = None, activation: Optional[str] = "silu",
+                      dx: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of causal_conv1d (ssd_causal_conv1d_bwd) for the upstream
+    gradient dout; dout and x [batch, seqlen, channels] may be strided views
+    with dense channels, and dx may be given as one (e.g. a slice of the
+    projection's gradient).  Returns dx (x's dtype), dweight [channels, width]
+    and dbias [channels] (fp32; None without bias)."""
+    dt = _float_dtype(x, "x")
+    if activation not in (None, "silu"):
+        raise ValueError("activation must be None or 'silu'")
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, channels]")
+    Bsz, L, Cn = x.shape
+    dev = x.device
+    _need_rows(x, "x", x.dtype, None, dev)
+    _need_rows(dout, "dout", x.dtype, x.shape, dev)
+    W = weight.shape[-1]
+    _need(weight, "weight", torch.float32, (Cn, W), dev)
+    _need(bias, "bias", torch.float32, (Cn,), dev, optional=True)
+    _need(seq_idx, "seq_idx", torch.int32, (Bsz, L), dev, optional=True)
+    st = _stream_of(stream, dev)
+    if dx is None:
+        dx = _empty(x.shape, x.dtype, dev, stream)
+    _need_rows(dx, "dx", x.dtype, x.shape, dev)
+    lib = _lib.load()
+    ws, ws_bytes, hold = _workspace(
+        int(lib.ssd_causal_conv1d_bwd_workspace_bytes(Bsz, L, Cn, W)), workspace, dev, stream)
+    dw = _empty((Cn, W), torch.float32, dev, stream)
+    db = None if bias is None else _empty((Cn,), torch.float32, dev, stream)
+    _lib.check(lib.ssd_causal_conv1d_bwd(
+        _ptr(dout), _stride3(dout), _ptr(x), _stride3(x), _ptr(weight), _ptr(bias), _ptr(seq_idx),
+        Bsz, L, Cn, W, int(activation == "silu"), dt, _ptr(dx), _stride3(dx), _ptr(dw), _ptr(db),
+        ws, ws_bytes, st))
+    return dict(dx=dx, dweight=dw, dbias=db)
+
+
+def causal_conv1d_step(x: torch.Tensor, conv_state: Optional[torch.Tensor], weight: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of causal_conv1d per batch row (ssd_causal_conv1d_step): x
+    [batch, channels] (rows may be strided); conv_state [batch, width - 1,
+    channels], the sequence's last inputs, oldest first, moved on in place
+    (None for width 1).  Returns out [batch, channels]."""
+    dt = _float_dtype(x, "x")
+    if activation not in (None, "silu"):
+        raise ValueError("activation must be None or 'silu'")
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, channels]")
+    Bsz, Cn = x.shape
+    dev = x.device
+    _need_rows(x, "x", x.dtype, None, dev)
+    W = weight.shape[-1]
+    _need(weight, "weight", torch.float32, (Cn, W), dev)
+    _need(bias, "bias", torch.float32, (Cn,), dev, optional=True)
+    _need(conv_state, "conv_state", x.dtype, (Bsz, W - 1, Cn), dev, optional=W == 1)
+    st = _stream_of(stream, dev)
+    if out is None:
+        out = _empty((Bsz, Cn), x.dtype, dev, stream)
+    else:
+        _need(out, "out", x.dtype, (Bsz, Cn), dev)
+    _lib.check(_lib.load().ssd_causal_conv1d_step(
+        x.data_ptr(), x.stride(0), _ptr(conv_state) if W > 1 else None, weight.data_ptr(),
+        _ptr(bias), Bsz, Cn, W, int(activation == "silu"), dt, out.data_ptr(), st))
+    return out
+
+
+class CausalConv1d(torch.autograd.Function):
+    """causal_conv1d forward (scan.causal_conv1d), causal_conv1d_bwd backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, seq_idx, activation):
+        from .scan import causal_conv1d
+        ctx.save_for_backward(x, weight, bias, seq_idx)
+        ctx.activation = activation
+        return causal_conv1d(x, weight, bias, seq_idx=seq_idx, activation=activation)
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, bias, seq_idx = ctx.saved_tensors
+        g = causal_conv1d_bwd(dout.contiguous(), x, weight, bias, seq_idx=seq_idx,
+                              activation=ctx.activation)
+        return g["dx"], g["dweight"], g["dbias"], None, None
+
+
+# --- gradient norm and clipping ----------------------------------------------
+
+def _storage_dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one block of memory (in any order of its
+    dimensions), so that an element-wise pass may walk the block."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if s != want:
+            return False
+        want *= n
+    return True
+
+
+def _tensor_table(tensors, name):
+    codes = []
+    for t in tensors:
+        code = _DT.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name}: tensors must be float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensors must be CUDA tensors")
+        if not _storage_dense(t):
+            raise ValueError(f"{name}: tensors must be dense")
+        codes.append(code)
+    n = len(tensors)
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int32 * n)(*codes))
+
+
+def _grad_list(grads):
+    grads = [grads] if isinstance(grads, torch.Tensor) else [g for g in grads if g is not None]
+    if not grads:
+        raise ValueError("no gradients given")
+    dev = grads[0].device
+    if any(g.device != dev for g in grads):
+        raise ValueError("the gradients must be on one device")
+    return grads, dev
+
+
+def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The 2-norm over all elements of a tensor or an iterable of tensors
+    (fp32 and bf16, None entries skipped; ssd_grad_norm), as a 0-d fp32
+    tensor on their device."""
+    grads, dev = _grad_list(grads)
+    ptrs, codes = _tensor_table(grads, "grads")
+    n = len(grads)
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    st = _stream_of(stream, dev)
+    lib = _lib.load()
+    ws, ws_bytes, hold = _workspace(int(lib.ssd_clip_grads_workspace_bytes(n)), workspace, dev,
+                                    stream)
+    norm = _empty((), torch.float32, dev, stream)
+    _lib.check(lib.ssd_grad_norm(ptrs, sizes, codes, n, norm.data_ptr(), ws, ws_bytes, st))
+    return norm
+
+
+def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scales the gradients (a tensor or an iterable, None entries skipped) by
+    min(1, max_norm / (norm + eps)) with their common 2-norm
+    (ssd_clip_grads): in place, or into `out`, one tensor for each gradient
+    that is not None, of the same shape and fp32 or bf16 (e.g. fp32 for an
+    optimizer that keeps bf16 gradients' clipped values so).  No host
+    synchronisation.  Returns the norm before clipping, 0-d fp32."""
+    grads, dev = _grad_list(grads)
+    ptrs, codes = _tensor_table(grads, "grads")
+    n = len(grads)
+    outs = out_codes = None
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else [o for o in out if o is not None]
+        if len(out) != n:
+            raise ValueError(f"out has {len(out)} tensors for {n} gradients")
+        for o, g in zip(out, grads):
+            if o.shape != g.shape or o.device != dev or (
+                    o.stride() != g.stride()
+                    and not (o.is_contiguous() and g.is_contiguous())):
+                raise ValueError("out must match its gradient's shape, strides and device")
+        outs, out_codes = _tensor_table(out, "out")
+    written = [p for p, g in zip(outs or ptrs, grads) if g.numel()]
+    if len(set(written)) != len(written):
+        raise ValueError("a tensor to write is given twice")
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    st = _stream_of(stream, dev)
+    lib = _lib.load()
+    ws, ws_bytes, hold = _workspace(int(lib.ssd_clip_grads_workspace_bytes(n)), workspace, dev,
+                                    stream)
+    norm = _empty((), torch.float32, dev, stream)
+    _lib.check(lib.ssd_clip_grads(ptrs, sizes, codes, n, outs, out_codes, float(max_norm),
+                                  float(eps), norm.data_ptr(), ws, ws_bytes, st))
+    return norm

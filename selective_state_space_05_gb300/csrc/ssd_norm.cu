@@ -320,21 +320,23 @@ constexpr int kSumRows = 8;
 // 32 columns a CTA, kSumRows warps that walk the rows kSumRows apart.
 __global__ void __launch_bounds__(32 * kSumRows)
     column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t ld, int64_t n,
-                      float* __restrict__ out) {
+                      float* __restrict__ out, int64_t n2, float* __restrict__ out2) {
   __shared__ float acc[kSumRows][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < n) {
+  const bool in = c < n + n2;
+  if (in) {
 #pragma unroll 4
     for (int64_t r = w; r < rows; r += kSumRows) s += part[r * ld + c];
   }
   acc[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < n) {
+  if (w == 0 && in) {
 #pragma unroll
     for (int i = 1; i < kSumRows; ++i) s += acc[i][lane];
-    out[c] = s;
+    if (c < n) out[c] = s;
+    else out2[c - n] = s;
   }
 }
 
@@ -398,9 +400,9 @@ bool wide_stride(const ssd_stride_t& s, size_t e) {
 }  // namespace norm
 
 cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
-                              cudaStream_t st) {
-  norm::column_sum_kernel<<<(unsigned)((n + 31) / 32), 32 * norm::kSumRows, 0, st>>>(part, rows,
-                                                                                     ld, n, out);
+                              int64_t n2, float* out2, cudaStream_t st) {
+  norm::column_sum_kernel<<<(unsigned)((n + n2 + 31) / 32), 32 * norm::kSumRows, 0, st>>>(
+      part, rows, ld, n, out, n2, out2);
   return cudaGetLastError();
 }
 
@@ -507,8 +509,7 @@ int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* r
   else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_ADD_BWD_BF);
   else SSD_NORM_BWD(SSD_ADD_BWD_BB);
   const int64_t prow = (int64_t)grid * sh.teams;
-  launch_column_sum(part, prow, 2 * dim, dim, dweight, st);
-  if (dscale) launch_column_sum(part + dim, prow, 2 * dim, dim, dscale, st);
+  launch_column_sum(part, prow, 2 * dim, dim, dweight, dscale ? dim : 0, dscale, st);
   return launched("add_rmsnorm_bwd");
 }
 
@@ -593,7 +594,7 @@ int ssd_gated_rmsnorm_bwd(const void* dout, const void* y, ssd_stride_t y_stride
 #define SSD_GATED_BWD_B(V, S) SSD_GATED_BWD(__nv_bfloat16, V, S)
   if (dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_GATED_BWD_F);
   else SSD_NORM_BWD(SSD_GATED_BWD_B);
-  launch_column_sum(part, (int64_t)grid.x * sh.teams, dim, dim, dweight, st);
+  launch_column_sum(part, (int64_t)grid.x * sh.teams, dim, dim, dweight, 0, nullptr, st);
   return launched("gated_rmsnorm_bwd");
 }
 

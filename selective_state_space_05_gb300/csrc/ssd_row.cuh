@@ -168,8 +168,9 @@ int sm_count();
 
 }  // namespace row
 
-// out[c] = sum over r < rows of part[r * ld + c], c < n, in a fixed order.
+// Column sums in a fixed order: s[c] = sum over r < rows of part[r * ld + c] for
+// c < n + n2; the first n go to out, the next n2 to out2.
 cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
-                              cudaStream_t st);
+                              int64_t n2, float* out2, cudaStream_t st);
 
 }  // namespace ssd

@@ -367,7 +367,14 @@ def causal_conv1d(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     """Causal depthwise conv1d over tokens (ssd_causal_conv1d): x [batch,
     seqlen, channels] (a strided view such as the xBC slice of zxbcdt is
     fine), weight [channels, width] fp32, bias [channels] fp32.  Returns a
-    dense [batch, seqlen, channels] tensor of x's dtype."""
+    dense [batch, seqlen, channels] tensor of x's dtype.  Differentiable in
+    x, weight and bias (its backward is causal_conv1d_bwd) unless out or
+    stream is given."""
+    if (out is None and stream is None and torch.is_grad_enabled()
+            and (x.requires_grad or weight.requires_grad
+                 or (bias is not None and bias.requires_grad))):
+        from .block import CausalConv1d
+        return CausalConv1d.apply(x, weight, bias, seq_idx, activation)
     if x.dtype not in _DT:
         raise ValueError("x must be float32 or bfloat16")
     if activation not in (None, "silu"):

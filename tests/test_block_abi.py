@@ -89,3 +89,50 @@ def test_binding_refuses_host_tensors():
         ssd.add_rmsnorm_fwd(x, None, w)
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         ssd.gated_rmsnorm_fwd(x.half(), None, w)
+
+
+def test_conv_refusals(lib):
+    d = dict(dout=16, dos=S(64, 16), x=16, xs=S(64, 16), weight=16, bias=16, seq=16, batch=2,
+             seqlen=4, channels=16, width=4, silu=1, dtype=BF, dx=16, dxs=S(64, 16), dw=16, db=16,
+             ws=256, wsb=1 << 20, stream=None)
+    f = caller(lib, "ssd_causal_conv1d_bwd", **d)
+    assert f(dtype=2) == ARG and f(batch=0) == ARG and f(seqlen=0) == ARG and f(batch=65536) == ARG
+    assert f(channels=12) == UNSUPPORTED and f(width=9) == UNSUPPORTED and f(width=0) == UNSUPPORTED
+    for k in ("dout", "x", "weight", "dx", "dw", "ws"):
+        assert f(**{k: None}) == NULL, k
+    assert f(x=8) == ALIGN and f(dx=24) == ALIGN and f(ws=16) == ALIGN
+    assert f(xs=S(64, 20)) == ALIGN and f(dos=S(64, 8)) == ALIGN and f(dxs=S(60, 16)) == ALIGN
+    assert f(dxs=S(0, 16)) == ARG
+    ws = lib.ssd_causal_conv1d_bwd_workspace_bytes(2, 4, 16, 4)
+    assert ws >= 2 * 16 * 5 * 4 and f(wsb=ws - 1) == WORKSPACE
+    assert lib.ssd_causal_conv1d_bwd_workspace_bytes(2, 4, 12, 4) == 0
+    g = caller(lib, "ssd_causal_conv1d_step", x=16, xs=16, state=16, weight=16, bias=None, batch=2,
+               channels=16, width=4, silu=1, dtype=BF, out=16, stream=None)
+    assert g(batch=0) == ARG and g(channels=4) == UNSUPPORTED and g(width=9) == UNSUPPORTED
+    for k in ("x", "state", "weight", "out"):
+        assert g(**{k: None}) == NULL, k
+    assert g(x=8) == ALIGN and g(xs=20) == ALIGN and g(state=24) == ALIGN
+
+
+def test_clip_refusals(lib):
+    import ctypes
+
+    def arr(t, *v):
+        return (t * len(v))(*v)
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    d = dict(g=arr(P, 16, 18), n=arr(I64, 4, 4), gt=arr(I32, F32, BF), count=2, outs=None, ot=None,
+             max_norm=1.0, eps=1e-6, norm=16, ws=256, wsb=1 << 20, stream=None)
+    f = caller(lib, "ssd_clip_grads", **d)
+    assert f(count=-1) == ARG and f(max_norm=-1.0) == ARG and f(max_norm=math.nan) == ARG
+    assert f(eps=-1.0) == ARG and f(n=arr(I64, 4, -1)) == ARG and f(gt=arr(I32, F32, 7)) == ARG
+    assert f(n=arr(I64, 4, 2 ** 45)) == UNSUPPORTED
+    for k in ("g", "n", "gt", "norm", "ws"):
+        assert f(**{k: None}) == NULL, k
+    assert f(g=arr(P, 16, None)) == NULL
+    assert f(outs=arr(P, 16, None)) == NULL
+    assert f(g=arr(P, 18, 18)) == ALIGN and f(g=arr(P, 16, 17)) == ALIGN
+    assert f(outs=arr(P, 16, 18), ot=arr(I32, F32, F32)) == ALIGN
+    assert f(norm=18) == ALIGN and f(ws=16) == ALIGN
+    ws = lib.ssd_clip_grads_workspace_bytes(2)
+    assert f(wsb=ws - 1) == WORKSPACE and lib.ssd_clip_grads_workspace_bytes(-1) == 0
+    assert lib.ssd_clip_grads_workspace_bytes(2000) > ws
