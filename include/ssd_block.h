@@ -174,6 +174,65 @@ int ssd_clip_grads(const void *const *grads, const int64_t *sizes,
                    float *norm, void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Projection with bias, activation and residual in one pass:
+ *   pre = x W^T + bias,   out = act(pre) + residual
+ *   x         [rows, in_features] x dtype, rows x_row_stride elements apart
+ *   weight    [out_features, in_features] x dtype, dense
+ *   bias      [out_features] x dtype, or NULL
+ *   residual  [rows, out_features] fp32 or x dtype (residual_dtype), rows
+ *             residual_row_stride elements apart, or NULL
+ *   out       [rows, out_features] dense, of the residual's type, or the x
+ *             dtype without one (written; may be the residual if it is dense)
+ *   pre       [rows, out_features] dense, or NULL: the value before act, which
+ *             the backward of an activation reads.  For bf16 it is kept in
+ *             IEEE half (11 bits in the same 2 bytes: act' depends on pre by
+ *             its absolute value only, so the half's range is enough: beyond
+ *             it both activations are flat), for fp32 in fp32.
+ * Sums in fp32 (bf16 products on the tensor cores; fp32 operands are split
+ * into three bf16 parts each and their six leading products summed, about
+ * fp32 accuracy).  SSD_ACT_GELU is v * Phi(v).
+ * Any sizes and element-aligned pointers; bf16 operands whose rows are not all
+ * 16-byte aligned (x, weight: in_features or the stride not a multiple of 8)
+ * and fp32 ones are first laid out in the workspace.
+ * aligned (workspace queries): nonzero if x (and for the backward dout and
+ * weight) are 16-byte aligned and x_row_stride is a multiple of 8.
+ * rows <= 2^30, features <= 2^24.
+ *
+ * Backward for the upstream gradient dout of out ([rows, out_features] dense,
+ * x dtype or fp32; also the residual's gradient, which needs no call):
+ *   dpre = dout * act'(pre),  dx = dpre W,  dweight = dpre^T x,
+ *   dbias = sum_rows dpre
+ * dx [rows, in_features], dweight [out_features, in_features], dbias
+ * [out_features], each x dtype, dense, or NULL (not computed); all written,
+ * not accumulated.  For bf16, dpre is rounded to bf16 for the two products
+ * (their operands' type) but not for dbias.
+ * dout_as_is (workspace query): nonzero if there is no activation and dout has
+ * the x dtype.  A wait inside the product kernel is bounded; ssd_scan_status
+ * tells whether one gave up.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_activation_t;
+
+size_t ssd_linear_fwd_workspace_bytes(int64_t rows, int in_features,
+                                      int out_features, ssd_dtype_t dtype,
+                                      int aligned);
+int ssd_linear_fwd(const void *x, int64_t x_row_stride, const void *weight,
+                   const void *bias, const void *residual,
+                   int64_t residual_row_stride, int64_t rows, int in_features,
+                   int out_features, ssd_activation_t activation,
+                   ssd_dtype_t dtype, ssd_dtype_t residual_dtype, void *out,
+                   void *pre, void *workspace, size_t workspace_bytes,
+                   void *stream);
+size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int in_features,
+                                      int out_features, ssd_dtype_t dtype,
+                                      int aligned, int dout_as_is);
+int ssd_linear_bwd(const void *dout, ssd_dtype_t dout_dtype, const void *x,
+                   int64_t x_row_stride, const void *weight, const void *pre,
+                   int64_t rows, int in_features, int out_features,
+                   ssd_activation_t activation, ssd_dtype_t dtype, void *dx,
+                   void *dweight, void *dbias, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,4 +11,5 @@ from .scan import (abi_version, bwd_workspace_bytes, causal_conv1d,  # noqa: F40
                    workspace_bytes)
 from .block import (add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_fwd,  # noqa: F401
                     block_abi_version, causal_conv1d_bwd, causal_conv1d_step, clip_grads,
-                    gated_rmsnorm, gated_rmsnorm_bwd, gated_rmsnorm_fwd, grad_norm)
+                    gated_rmsnorm, gated_rmsnorm_bwd, gated_rmsnorm_fwd, grad_norm, linear,
+                    linear_bwd, linear_fwd)

@@ -88,6 +88,12 @@ SIGNATURES.update({
     "ssd_causal_conv1d_bwd": (_i, [_vp, _st, _vp, _st, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _i,
                                    _vp, _st, _vp, _vp, _vp, _sz, _vp]),
     "ssd_causal_conv1d_step": (_i, [_vp, _i64, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _vp]),
+    "ssd_linear_fwd_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i]),
+    "ssd_linear_fwd": (_i, [_vp, _i64, _vp, _vp, _vp, _i64, _i64, _i, _i, _i, _i, _i, _vp, _vp,
+                            _vp, _sz, _vp]),
+    "ssd_linear_bwd_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i, _i]),
+    "ssd_linear_bwd": (_i, [_vp, _i, _vp, _i64, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _vp, _vp,
+                            _vp, _sz, _vp]),
     "ssd_clip_grads_workspace_bytes": (_sz, [_i]),
     "ssd_grad_norm": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
     "ssd_clip_grads": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _f, _f, _vp, _vp, _sz, _vp]),

@@ -1,7 +1,8 @@
 """Python binding of the block operators' C ABI (include/ssd_block.h): the
 residual RMSNorm before a block and the gated grouped RMSNorm after its scan,
-with their backwards and a differentiable form of each, the causal conv1d's
-backward and one-token step, and gradient clipping.
+the projections with bias, activation and residual in their epilogue, with
+their backwards and a differentiable form of each, the causal conv1d's backward
+and one-token step, and gradient clipping.
 
 Argument marshalling only, as in scan.py.  Each operator comes as
 ``<name>_fwd`` and ``<name>_bwd`` (explicit, usable on any stream and inside a
@@ -367,6 +368,170 @@ class CausalConv1d(torch.autograd.Function):
         g = causal_conv1d_bwd(dout.contiguous(), x, weight, bias, seq_idx=seq_idx,
                               activation=ctx.activation)
         return g["dx"], g["dweight"], g["dbias"], None, None
+
+
+# --- projections --------------------------------------------------------------
+
+_ACT = {None: 0, "silu": 1, "gelu": 2}
+_PRE = {torch.bfloat16: torch.float16, torch.float32: torch.float32}
+
+
+def _act_code(activation) -> int:
+    code = _ACT.get(activation)
+    if code is None:
+        raise ValueError("activation must be None, 'silu' or 'gelu'")
+    return code
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """The one stride between the rows of t seen as [rows, features]."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: each row must be dense")
+    if t.is_contiguous() or t.dim() == 1:
+        return t.shape[-1]
+    step, want = None, None
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = want = s
+        if s != want:
+            raise ValueError(f"{name}: its rows must be evenly spaced")
+        want = s * n
+    return t.shape[-1] if step is None else step
+
+
+def _aligned(t: torch.Tensor, stride: int) -> bool:
+    return t.data_ptr() % 16 == 0 and stride % 8 == 0
+
+
+def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+               activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+               save_pre: bool = False, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None):
+    """out = act(x W^T + bias) + residual (ssd_linear_fwd).  x [..., in]
+    (evenly spaced dense rows, e.g. a slice of a wider tensor), weight [out,
+    in] and bias [out] of x's dtype; activation None, "silu" or "gelu";
+    residual [..., out] fp32 or x's dtype, also evenly spaced; out may be the
+    residual.  Returns out (the residual's dtype, x's without one), or (out,
+    pre) with save_pre: the value before the activation for linear_bwd (fp16
+    for bf16, fp32 for fp32)."""
+    dt = _float_dtype(x, "x")
+    act = _act_code(activation)
+    dev, xd = x.device, x.dtype
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    K = x.shape[-1]
+    N = weight.shape[0]
+    _need(weight, "weight", xd, (N, K), dev)
+    _need(bias, "bias", xd, (N,), dev, optional=True)
+    shape = x.shape[:-1] + (N,)
+    sx = _row_stride(x, "x")
+    sr, rt = 0, dt
+    if residual is not None:
+        if residual.shape != shape or residual.device != dev:
+            raise ValueError(f"residual must have shape {tuple(shape)} on {dev}")
+        rt = _float_dtype(residual, "residual")
+        sr = _row_stride(residual, "residual")
+    st = _stream_of(stream, dev)
+    od = xd if residual is None else residual.dtype
+    if out is None:
+        out = _empty(shape, od, dev, stream)
+    else:
+        _need(out, "out", od, shape, dev)
+    pre = _empty(shape, _PRE[xd], dev, stream) if save_pre else None
+    rows = x.numel() // K if K else 0
+    lib = _lib.load()
+    ws, ws_bytes, hold = _workspace(
+        int(lib.ssd_linear_fwd_workspace_bytes(
+            rows, K, N, dt, int(_aligned(x, sx) and weight.data_ptr() % 16 == 0))),
+        workspace, dev, stream)
+    _lib.check(lib.ssd_linear_fwd(
+        x.data_ptr(), sx, weight.data_ptr(), _ptr(bias), _ptr(residual), sr, rows, K, N, act, dt,
+        rt, out.data_ptr(), _ptr(pre), ws, ws_bytes, st))
+    return (out, pre) if save_pre else out
+
+
+def linear_bwd(dout: torch.Tensor, x: Optional[torch.Tensor], weight: Optional[torch.Tensor], *,
+               activation: Optional[str] = None, pre: Optional[torch.Tensor] = None,
+               need_dx: bool = True, need_dweight: bool = True, need_dbias: bool = False,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of linear_fwd (ssd_linear_bwd) for the dense upstream
+    gradient dout, fp32 or x's dtype (dout is the residual's gradient as
+    well).  pre is the forward's, with an activation.  Returns dx, dweight and
+    dbias in x's dtype, None where not asked for."""
+    given = x if x is not None else weight
+    if given is None:
+        raise ValueError("x or weight is required")
+    dt = _float_dtype(given, "x")
+    act = _act_code(activation)
+    dev, xd = dout.device, given.dtype
+    dd = _float_dtype(dout, "dout")
+    _need(dout, "dout", device=dev)
+    N, K = dout.shape[-1], given.shape[-1]
+    rows = dout.numel() // N if N else 0
+    shape = dout.shape[:-1] + (K,)
+    if need_dx:
+        _need(weight, "weight", xd, (N, K), dev)
+    sx = K
+    if need_dweight:
+        if x is None or x.shape != shape or x.device != dev:
+            raise ValueError(f"x must have shape {tuple(shape)} on {dev}")
+        sx = _row_stride(x, "x")
+    if activation is not None:
+        _need(pre, "pre", _PRE[xd], dout.shape, dev)
+    st = _stream_of(stream, dev)
+    lib = _lib.load()
+    aligned = (dout.data_ptr() % 16 == 0 and (not need_dx or weight.data_ptr() % 16 == 0)
+               and (not need_dweight or _aligned(x, sx)))
+    ws, ws_bytes, hold = _workspace(
+        int(lib.ssd_linear_bwd_workspace_bytes(rows, K, N, dt, int(aligned),
+                                               int(act == 0 and dd == dt))),
+        workspace, dev, stream)
+    dx = _empty(shape, xd, dev, stream) if need_dx else None
+    dw = _empty((N, K), xd, dev, stream) if need_dweight else None
+    db = _empty((N,), xd, dev, stream) if need_dbias else None
+    _lib.check(lib.ssd_linear_bwd(
+        dout.data_ptr(), dd, x.data_ptr() if need_dweight else None, sx,
+        weight.data_ptr() if need_dx else None, _ptr(pre) if act else None, rows, K, N, act, dt,
+        _ptr(dx), _ptr(dw), _ptr(db), ws, ws_bytes, st))
+    return dict(dx=dx, dweight=dw, dbias=db)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        save = activation is not None and any(ctx.needs_input_grad[:3])
+        got = linear_fwd(x, weight, bias, activation=activation, residual=residual, save_pre=save)
+        out, pre = got if save else (got, None)
+        ctx.save_for_backward(x if ctx.needs_input_grad[1] else None,
+                              weight if ctx.needs_input_grad[0] else None, pre)
+        ctx.activation, ctx.like = activation, (x.dtype, x.shape[-1])
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, weight, pre = ctx.saved_tensors
+        nx, nw, nb, nr = ctx.needs_input_grad[:4]
+        dout = dout.contiguous()
+        g = dict(dx=None, dweight=None, dbias=None)
+        if nx or nw or nb:
+            # dbias alone needs neither operand: an empty one tells the type
+            given = x if x is not None else weight
+            if given is None:
+                given = torch.empty((0, ctx.like[1]), dtype=ctx.like[0], device=dout.device)
+            g = linear_bwd(dout, x if x is not None else given, weight,
+                           activation=ctx.activation, pre=pre, need_dx=nx, need_dweight=nw,
+                           need_dbias=nb)
+        return g["dx"], g["dweight"], g["dbias"], dout if nr else None, None
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+           activation: Optional[str] = None,
+           residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """linear_fwd as a differentiable torch function: gradients for x,
+    weight, bias and residual."""
+    return _Linear.apply(x, weight, bias, residual, activation)
 
 
 # --- gradient norm and clipping ----------------------------------------------

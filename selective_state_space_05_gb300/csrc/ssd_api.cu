@@ -282,6 +282,14 @@ int ssd_scan_status(int reset, void* stream) {
   e = ssd::tc32_status(reset, static_cast<cudaStream_t>(stream), &bits32);
   if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
   bits |= bits32;
+  int bits_linear = 0;
+  e = ssd::linear_status(reset, static_cast<cudaStream_t>(stream), &bits_linear);
+  if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
+  if (bits_linear != 0)
+    return fail(SSD_ERR_TIMEOUT,
+                "a projection's launch gave up a bounded wait (error bits 0x%x: 1 barrier, 2 "
+                "drain); its outputs are not valid",
+                bits_linear);
   if (bits != 0)
     return fail(SSD_ERR_TIMEOUT,
                 "a tensor-core scan launch gave up a bounded wait (error bits 0x%x: 1 barrier, "

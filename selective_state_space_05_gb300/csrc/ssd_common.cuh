@@ -148,6 +148,8 @@ cudaError_t launch_cb_tc32(const float* B, const float* C, const Dims& d, float*
                            cudaStream_t st);
 // Status bits of their bounded waits (8: a wait gave up), as fused_status.
 int tc32_status(int reset, cudaStream_t st, int* bits);
+// The same for the projections' product kernel (ssd_linear.cu).
+int linear_status(int reset, cudaStream_t st, int* bits);
 
 // Device-wide status of the fused kernel's bounded waits: the error bits
 // recorded since the last reset into *bits (0: none); synchronises st.

@@ -1,0 +1,1051 @@
+// Projections of the block: out = act(x W^T + bias) + residual, and its
+// backward dx = dpre W, dW = dpre^T x, dbias = sum dpre, dpre = dout act'(pre).
+//
+// All three products are one kernel, D[m,n] = sum_k A[m,k] B[n,k], on the
+// tensor cores (tcgen05, accumulators in TMEM, operand tiles by TMA with the
+// 128-byte swizzle).  An operand is read where it lies: K-major (x and W of
+// the forward, dpre of dx) or MN-major (W of dx, dpre and x of dW), so nothing
+// is transposed.
+//
+// fp32 runs on the same kernel: each operand is split beforehand into three
+// bf16 planes hi + mid + lo, which hold its 24-bit significand exactly, and
+// the six products down to 2^-24 (hi hi, hi mid, mid hi, mid mid, hi lo,
+// lo hi) are more K steps of the same sum, the smallest first.
+//
+// The kernel is persistent: one CTA an SM walks output tiles of 128 x BN; one
+// thread issues the TMA loads, one the MMAs, and four warps take finished
+// accumulators out of TMEM (two, so that the next tile's MMAs run meanwhile),
+// turn them through shared memory so that rows are written in whole sectors,
+// and apply bias, activation and residual on the way.  Where there are few
+// tiles, K is split over CTAs: each writes its partial sums in fp32 and a
+// second kernel adds them in a fixed order and applies the same epilogue.
+//
+// A few rows (decoding) are bound by the weight's bytes: skinny_kernel streams
+// W through registers once, all of its loads in flight, with mma.sync for bf16
+// (the weight's rows are the MMA's 16 rows, the tokens its 8 columns) and fp32
+// FMAs for fp32.
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "../../include/ssd_block.h"
+#include "ssd_common.cuh"
+#include "ssd_row.cuh"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+namespace linear {
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kThreads = 192;             // warp 0: TMA, 1: MMA, 2-5: epilogue
+constexpr int kPitch = 36;                // floats a row of the epilogue's 32 x 32 block: 16-byte
+                                          // row accesses of eight lanes hit all 32 banks
+constexpr unsigned long long kWaitNs = 2000000000ull;   // limit of any single wait: 2 s
+constexpr uint32_t kSleepNs = 20000;
+
+// Sticky status of this device: nonzero once a wait gave up (ssd_scan_status).
+__device__ int g_status_linear;
+
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+enum { kNone = 0, kF32 = 1, kBf16 = 2, kF16 = 3 };
+
+// What happens to a sum on its way out: out = act(sum + bias) + res, and pre =
+// sum + bias where the backward will want it.
+struct Epilogue {
+  const void* bias;
+  const void* res;
+  void* out;
+  void* pre;
+  int64_t res_ld, out_ld;
+  uint8_t bias_t, res_t, out_t, pre_t, act;
+  bool wide;   // four columns at once: every row of every tensor stays aligned for it
+};
+
+__device__ __forceinline__ float act_f(int act, float v) {
+  if (act == kActSilu) return v * row::sigmoid_f(v);
+  if (act == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678f));
+  return v;
+}
+__device__ __forceinline__ float dact_f(int act, float v) {
+  if (act == kActSilu) {
+    const float s = row::sigmoid_f(v);
+    return s * (1.f + v * (1.f - s));
+  }
+  if (act == kActGelu)
+    return 0.5f * (1.f + erff(v * 0.70710678f)) + v * 0.39894228f * __expf(-0.5f * v * v);
+  return 1.f;
+}
+
+// The half that pre is kept in: beyond its range act' is flat, so the largest
+// half stands for it (an infinity would make silu' a NaN).
+__device__ __forceinline__ float half_range(float v) {
+  return v > 65504.f ? 65504.f : v < -65504.f ? -65504.f : v;   // NaN stays
+}
+
+__device__ __forceinline__ float get1(const void* p, int t, int64_t i) {
+  if (t == kF32) return static_cast<const float*>(p)[i];
+  if (t == kF16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void put1(void* p, int t, int64_t i, float v) {
+  if (t == kF32) static_cast<float*>(p)[i] = v;
+  else if (t == kF16) static_cast<__half*>(p)[i] = __float2half_rn(half_range(v));
+  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ void get4(const void* p, int t, int64_t i, float (&v)[4]) {
+  if (t == kF32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void put4(void* p, int t, int64_t i, const float (&v)[4]) {
+  if (t == kF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (t == kF16) {
+    const __half2 a = __floats2half2_rn(half_range(v[0]), half_range(v[1]));
+    const __half2 b = __floats2half2_rn(half_range(v[2]), half_range(v[3]));
+    *reinterpret_cast<uint2*>(static_cast<__half*>(p) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
+        make_uint2(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]));
+  }
+}
+
+// Sums of row m, columns n .. n + 3 (those below N).  v is finished in place.
+__device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int64_t n, int64_t N,
+                                        float (&v)[4]) {
+  if (e.wide) {
+    if (n >= N) return;
+    if (e.bias) {
+      float b[4];
+      get4(e.bias, e.bias_t, n, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += b[i];
+    }
+    if (e.pre) put4(e.pre, e.pre_t, m * N + n, v);
+    if (e.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_f(e.act, v[i]);
+    }
+    if (e.res) {
+      float r[4];
+      get4(e.res, e.res_t, m * e.res_ld + n, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += r[i];
+    }
+    put4(e.out, e.out_t, m * e.out_ld + n, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n + i >= N) return;
+      float s = v[i] + (e.bias ? get1(e.bias, e.bias_t, n + i) : 0.f);
+      if (e.pre) put1(e.pre, e.pre_t, m * N + n + i, s);
+      s = act_f(e.act, s);
+      if (e.res) s += get1(e.res, e.res_t, m * e.res_ld + n + i);
+      put1(e.out, e.out_t, m * e.out_ld + n + i, s);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the product
+
+struct Gemm {
+  int64_t M, N;
+  int kblocks;        // K in steps of kBK
+  int pairs;          // products of planes: 1, or 6 for fp32
+  int tiles_m, tiles_n, splits, steps_per_split;
+  int group_m;        // tiles of M walked together (L2 reuse)
+  float* partial;     // [splits][M][N] where splits > 1
+  Epilogue e;
+};
+
+// The planes of the q-th product of an fp32 sum, smallest first.
+__device__ __forceinline__ void planes_of(int pairs, int q, int& a, int& b) {
+  if (pairs == 1) {
+    a = b = 0;
+    return;
+  }
+  switch (q) {
+    case 0: a = 0; b = 2; break;
+    case 1: a = 2; b = 0; break;
+    case 2: a = 1; b = 1; break;
+    case 3: a = 0; b = 1; break;
+    case 4: a = 1; b = 0; break;
+    default: a = 0; b = 0; break;
+  }
+}
+
+template <int BN>
+struct Cfg {
+  static constexpr int kStageA = kBM * kBK * 2, kStageB = BN * kBK * 2;
+  static constexpr int kStages = 192 * 1024 / (kStageA + kStageB);
+  static constexpr uint32_t kTmemCols = 2 * BN;   // 128, 256 or 512
+};
+
+template <int BN>
+struct alignas(1024) Smem {
+  unsigned char a[Cfg<BN>::kStages][Cfg<BN>::kStageA];
+  unsigned char b[Cfg<BN>::kStages][Cfg<BN>::kStageB];
+  float turn[4][32 * kPitch];
+  uint64_t full[Cfg<BN>::kStages], empty[Cfg<BN>::kStages], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Smem<256>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<64>) + 1024 <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Waits for a phase; gives up after kWaitNs, or soon after another role of the
+// CTA gave up.  Returns whether the phase completed.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int* abort) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  for (;;) {
+    if (tc::mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+    if (*reinterpret_cast<volatile int*>(abort)) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *reinterpret_cast<volatile int*>(abort) = 1;
+      atomicOr(&g_status_linear, 1);
+      return false;
+    }
+  }
+}
+// For work of its own that is still in flight at the end: not cut short by an abort.
+__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = now_ns();
+  while (!tc::mbar_try_wait_sleep(bar, parity, kSleepNs))
+    if (now_ns() - t0 > kWaitNs) {
+      atomicOr(&g_status_linear, 2);
+      return;
+    }
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// One stage's tile of an operand: ROWS rows of M or N from r0, kBK of K from k0.
+template <int ROWS, bool MN>
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int r0, int k0, int plane) {
+  if constexpr (MN) {
+#pragma unroll
+    for (int j = 0; j < ROWS / 64; ++j)
+      tma_load_3d(dst + j * (kBK * 128), map, bar, r0 + 64 * j, k0, plane);
+  } else {
+    tma_load_3d(dst, map, bar, k0, r0, plane);
+  }
+}
+template <bool MN>
+__device__ __forceinline__ uint64_t tile_desc(const unsigned char* p) {
+  return MN ? tc::sdesc_sw128(tc::smem_u32(p), kBK * 128, 1024)
+            : tc::sdesc_sw128(tc::smem_u32(p), 16, 1024);
+}
+
+// Work item -> tile and split.  Tiles run down group_m rows of tiles before
+// the next column, so that the CTAs at work at one time share operands in L2.
+__device__ __forceinline__ void tile_of(const Gemm& p, int item, int& tm, int& tn, int& split) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  split = item / tiles;
+  const int t = item - split * tiles;
+  const int per = p.group_m * p.tiles_n;
+  const int g = t / per, r = t - g * per;
+  const int gm = min(p.group_m, p.tiles_m - g * p.group_m);
+  tm = g * p.group_m + r % gm;
+  tn = r / gm;
+}
+
+template <int BN, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                const __grid_constant__ Gemm p) {
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ unsigned char raw[];
+  Smem<BN>& s = *reinterpret_cast<Smem<BN>*>(
+      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int items = p.tiles_m * p.tiles_n * p.splits;
+  const int all_steps = p.kblocks * p.pairs;
+
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < S; ++i) {
+      tc::mbar_init(&s.full[i], 1);
+      tc::mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.tfull[i], 1);
+      tc::mbar_init(&s.tempty[i], 4);
+    }
+    tc::mbar_init(&s.drain, 1);
+    tc::mbar_fence_init();
+    s.abort = 0;
+    tc::tma_prefetch_desc(&ma);
+    tc::tma_prefetch_desc(&mb);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&s.tmem, C::kTmemCols);
+    tc::tmem_relinquish();
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        int tm, tn, split;
+        tile_of(p, it, tm, tn, split);
+        const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_phase(&s.empty[st], ph ^ 1, &s.abort)) {
+            ok = false;
+            break;
+          }
+          const int q = k / p.kblocks;
+          int pa, pb;
+          planes_of(p.pairs, q, pa, pb);
+          const int kk = (k - q * p.kblocks) * kBK;
+          tc::mbar_arrive_expect_tx(&s.full[st], C::kStageA + C::kStageB);
+          load_tile<kBM, AMN>(s.a[st], &ma, &s.full[st], tm * kBM, kk, pa);
+          load_tile<BN, BMN>(s.b[st], &mb, &s.full[st], tn * BN, kk, pb);
+          ++issued;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {   // no copy outlives the CTA
+        for (int i = max(0, issued - S); i < issued; ++i)
+          wait_drain(&s.full[i % S], (i / S) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(kBM, BN, AMN, BMN);
+      int st = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x, ++n) {
+        int tm, tn, split;
+        tile_of(p, it, tm, tn, split);
+        const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+        const int buf = n & 1;
+        if (!wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort)) break;
+        tc::fence_after_sync();
+        for (int k = k0; k < k1; ++k) {
+          if (!wait_phase(&s.full[st], ph, &s.abort)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint64_t da = tile_desc<AMN>(s.a[st]), db = tile_desc<BMN>(s.b[st]);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            tc::mma_ss(tmem + buf * BN, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2),
+                       idesc, k > k0 || kk > 0);
+          tc::mma_commit(&s.empty[st]);
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) tc::mma_commit(&s.tfull[buf]);
+      }
+      // every MMA has finished before the operands' memory and TMEM are given back
+      tc::mma_commit(&s.drain);
+      wait_drain(&s.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;   // this warp's quarter of the TMEM lanes
+    float* turn = s.turn[warp - 2];
+    int n = 0;
+    for (int it = blockIdx.x; it < items; it += gridDim.x, ++n) {
+      int tm, tn, split;
+      tile_of(p, it, tm, tn, split);
+      const int buf = n & 1;
+      // one verdict for the warp: the TMEM loads below take all of its lanes
+      if (!__all_sync(0xffffffffu, wait_phase(&s.tfull[buf], (n >> 1) & 1, &s.abort))) break;
+      tc::fence_after_sync();
+      const int64_t m0 = (int64_t)tm * kBM + q * 32;
+      const int64_t n0 = (int64_t)tn * BN;
+      const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
+      float* part = p.splits > 1 ? p.partial + (int64_t)split * p.M * p.N : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        if (n0 + c >= p.N) break;
+        uint32_t r[32];
+        tc::tmem_ld32(tmem + buf * BN + c + (static_cast<uint32_t>(q * 32) << 16), r);
+        tc::tmem_ld_wait_regs(r);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(turn + lane * kPitch + 4 * i) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        __syncwarp();
+        const int64_t col = n0 + c + 4 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          if (rr < rows) {
+            const float4 f = *reinterpret_cast<const float4*>(turn + rr * kPitch + 4 * (lane & 7));
+            float v[4] = {f.x, f.y, f.z, f.w};
+            if (part) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (col + j < p.N) part[(m0 + rr) * p.N + col + j] = v[j];
+            } else {
+              finish4(p.e, m0 + rr, col, p.N, v);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s.tempty[buf]);
+    }
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// Adds the partial sums of split K, in order, and finishes them.
+__global__ void __launch_bounds__(256)
+    join_kernel(const float* __restrict__ part, int splits, int64_t M, int64_t N,
+                const __grid_constant__ Epilogue e) {
+  const int64_t per_row = (N + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= M * per_row) return;
+  const int64_t m = i / per_row, n = (i - m * per_row) * 4;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + (s * M + m) * N + n;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < N) v[j] += p[j];
+  }
+  finish4(e, m, n, N, v);
+}
+
+// ------------------------------------------------------- operands made ready
+
+// src (times act'(pre)) as bf16 planes [planes][R][ld] (planes 0: none), and
+// its column sums over this CTA's rows (colsum: [gridDim.y][C], or null).
+// Three planes hold an fp32 value exactly: each takes the next 8 bits of its
+// significand, rounded, the next one the remainder.
+struct Prep {
+  const void* src;
+  const void* pre;
+  __nv_bfloat16* out;
+  float* colsum;
+  int64_t R, src_ld, ld, rows_per;
+  int C;
+  uint8_t src_t, pre_t, act, planes;
+};
+__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ Prep p) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.C) return;
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per, r1 = min(r0 + p.rows_per, p.R);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int64_t r = r0; r < r1; ++r) {
+    float v = get1(p.src, p.src_t, r * p.src_ld + c);
+    if (p.pre) v *= dact_f(p.act, get1(p.pre, p.pre_t, r * p.C + c));
+    sum += v;
+    __nv_bfloat16* o = p.out + r * p.ld + c;
+    for (int k = 0; k < p.planes; ++k) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      *o = h;
+      o += p.R * p.ld;
+      v -= __bfloat162float(h);
+    }
+  }
+  if (p.colsum) p.colsum[(int64_t)blockIdx.y * p.C + c] = sum;
+}
+
+// out[c] = sum over r of part[r][c], rounded once to out's type.
+__global__ void __launch_bounds__(256)
+    sum_rows_kernel(const float* __restrict__ part, int rows, int C, void* out, int out_t) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= C) return;
+  float s = 0.f;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) s += part[(int64_t)r * C + c];
+  put1(out, out_t, c, s);
+}
+
+// ------------------------------------------------------------------- few rows
+
+constexpr int kSkinnyThreads = 256, kSkinnyWarps = 8;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 rows of W a CTA against NT x 8 tokens.  The warps take steps of 32 of K
+// in turn.  Each lane loads 16 consecutive bytes of a row: the MMA's K index
+// is permuted within the step, alike for W and x, which leaves the sum as it
+// is.  K a multiple of 8, rows 16-byte aligned.
+template <int NT>
+__global__ void __launch_bounds__(kSkinnyThreads)
+    skinny_bf16_kernel(const __nv_bfloat16* __restrict__ x, int64_t sx,
+                       const __nv_bfloat16* __restrict__ w, int M, int64_t N, int K,
+                       const __grid_constant__ Epilogue e) {
+  __shared__ float acc[kSkinnyWarps][16][NT * 8 + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const bool lo = n0 + g < N, hi = n0 + g + 8 < N;
+  const __nv_bfloat16* w0 = w + (n0 + g) * K;
+  const __nv_bfloat16* w1 = w0 + (int64_t)8 * K;
+  float d[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int k = (warp * 4 + t) * 8; k < K + t * 8; k += kSkinnyWarps * 32) {   // uniform trip count
+    const bool in = k < K;
+    const uint4 a = in && lo ? *reinterpret_cast<const uint4*>(w0 + k) : zero;
+    const uint4 b = in && hi ? *reinterpret_cast<const uint4*>(w1 + k) : zero;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int m = i * 8 + g;
+      const uint4 v = in && m < M ? *reinterpret_cast<const uint4*>(x + m * sx + k) : zero;
+      mma16816(d[i], a.x, b.x, a.y, b.y, v.x, v.y);
+      mma16816(d[i], a.z, b.z, a.w, b.w, v.z, v.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    acc[warp][g][i * 8 + 2 * t] = d[i][0];
+    acc[warp][g][i * 8 + 2 * t + 1] = d[i][1];
+    acc[warp][g + 8][i * 8 + 2 * t] = d[i][2];
+    acc[warp][g + 8][i * 8 + 2 * t + 1] = d[i][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * 8 * 4; i += kSkinnyThreads) {
+    const int m = i >> 2, c = (i & 3) * 4;
+    if (m >= M) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < kSkinnyWarps; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += acc[q][c + j][m];
+    finish4(e, m, n0 + c, N, v);
+  }
+}
+
+// fp32: a warp takes four rows of W against up to 8 tokens.  K a multiple of
+// 4, rows 16-byte aligned.
+constexpr int kF32Rows = 4;
+__global__ void __launch_bounds__(kSkinnyThreads)
+    skinny_f32_kernel(const float* __restrict__ x, int64_t sx, const float* __restrict__ w, int M,
+                      int64_t N, int K, const __grid_constant__ Epilogue e) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t n0 = ((int64_t)blockIdx.x * kSkinnyWarps + warp) * kF32Rows;
+  if (n0 >= N) return;
+  float acc[8][kF32Rows];
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int j = 0; j < kF32Rows; ++j) acc[m][j] = 0.f;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = lane * 4; k < K; k += 128) {
+    float4 wv[kF32Rows];
+#pragma unroll
+    for (int j = 0; j < kF32Rows; ++j)
+      wv[j] = n0 + j < N ? *reinterpret_cast<const float4*>(w + (n0 + j) * K + k) : zero;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      if (m < M) {
+        const float4 xv = *reinterpret_cast<const float4*>(x + m * sx + k);
+#pragma unroll
+        for (int j = 0; j < kF32Rows; ++j)
+          acc[m][j] = fmaf(xv.x, wv[j].x, fmaf(xv.y, wv[j].y, fmaf(xv.z, wv[j].z, fmaf(xv.w, wv[j].w, acc[m][j]))));
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    if (m >= M) break;
+#pragma unroll
+    for (int j = 0; j < kF32Rows; ++j)
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+        acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], off);
+    if (lane == 0) finish4(e, m, n0, N, acc[m]);
+  }
+}
+
+// ------------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+int bad(int code, const char* msg) { return set_error(code, msg); }
+int cuda_bad(cudaError_t e, const char* what) {
+  char m[256];
+  snprintf(m, sizeof(m), "%s: %s", what, cudaGetErrorString(e));
+  return set_error(SSD_ERR_CUDA, m);
+}
+bool al(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// An operand in memory: `rows` rows of `cols` bf16, ld apart, `planes` of them
+// rows * ld apart.
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+  int planes;
+};
+
+// box: kBK x tile rows of a K-major operand, 64 x kBK of an MN-major one.
+bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2,
+                                 (cuuint64_t)(o.planes > 1 ? o.rows * o.ld * 2 : o.ld * 2)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? kBK : tile_rows), 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a product of M x N with `steps` K steps is cut: tile width and splits.
+struct Plan {
+  int bn, splits, steps_per;
+};
+Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs) {
+  const int sms = row::sm_count();
+  const int steps = (int)((K + kBK - 1) / kBK) * pairs;
+  Plan best = {256, 1, steps};
+  double best_cost = 1e30;
+  for (int bn = 64; bn <= 256; bn *= 2) {
+    const int64_t tiles = ((M + kBM - 1) / kBM) * ((N + bn - 1) / bn);
+    const double step = bn == 256 ? 1.0 : bn == 128 ? 0.6 : 0.42;
+    const double fixed = 6.0 + 8.0 * bn / 256;   // pipeline fill and the last epilogue
+    for (int splits = 1; splits <= 16; splits *= 2) {
+      const int per = (steps + splits - 1) / splits;
+      if (splits > 1 && per < 4) break;
+      const int64_t waves = (tiles * splits + sms - 1) / sms;
+      double cost = waves * per * step + fixed;
+      // partial sums are written, read and joined by another launch
+      if (splits > 1) cost += 12.0 + (double)M * N * (splits * 2 + 1) * 4 / 1.5e6;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {bn, splits, per};
+      }
+    }
+  }
+  best.splits = (steps + best.steps_per - 1) / best.steps_per;
+  return best;
+}
+size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
+  return p.splits > 1 ? up256((size_t)p.splits * M * N * sizeof(float)) : 0;
+}
+
+template <int BN, bool AMN, bool BMN>
+cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid,
+                        cudaStream_t st) {
+  const size_t smem = sizeof(Smem<BN>) + 1024;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(gemm_kernel<BN, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  gemm_kernel<BN, AMN, BMN><<<grid, kThreads, smem, st>>>(ma, mb, g);
+  return cudaGetLastError();
+}
+
+// D[M,N] = sum over K and planes, finished by e; part: partial_bytes of the plan.
+int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int64_t N, int64_t K,
+         const Epilogue& e, float* part, cudaStream_t st) {
+  const int pairs = a.planes == 3 ? 6 : 1;
+  const Plan pl = plan_for(M, N, K, pairs);
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, pl.bn))
+    return bad(SSD_ERR_CUDA, "linear: a tensor map could not be made");
+  Gemm g = {};
+  g.M = M;
+  g.N = N;
+  g.kblocks = (int)((K + kBK - 1) / kBK);
+  g.pairs = pairs;
+  g.tiles_m = (int)((M + kBM - 1) / kBM);
+  g.tiles_n = (int)((N + pl.bn - 1) / pl.bn);
+  g.splits = pl.splits;
+  g.steps_per_split = pl.steps_per;
+  g.group_m = 8;
+  g.partial = part;
+  g.e = e;
+  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int grid = (int)std::min<int64_t>(items, row::sm_count());
+  cudaError_t err;
+#define SSD_GEMM(BN)                                                          \
+  err = amn ? launch_gemm<BN, true, true>(ma, mb, g, grid, st)                \
+            : bmn ? launch_gemm<BN, false, true>(ma, mb, g, grid, st)         \
+                  : launch_gemm<BN, false, false>(ma, mb, g, grid, st)
+  if (pl.bn == 256) SSD_GEMM(256);
+  else if (pl.bn == 128) SSD_GEMM(128);
+  else SSD_GEMM(64);
+#undef SSD_GEMM
+  if (err != cudaSuccess) return cuda_bad(err, "linear launch");
+  if (pl.splits > 1) {
+    const int64_t n = M * ((N + 3) / 4);
+    join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, pl.splits, M, N, e);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return cuda_bad(err, "linear join launch");
+  }
+  return SSD_OK;
+}
+
+int type_of(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? kBf16 : kF32; }
+size_t esize(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
+
+// Rows of a column-sum / plane pass a CTA; bounded by the grid's y limit.
+int64_t prep_rows_per(int64_t R, int C) {
+  const int64_t cols = (C + 255) / 256;
+  const int64_t want = std::max<int64_t>(1, (int64_t)row::sm_count() * 8 / cols);
+  return std::max<int64_t>(std::max<int64_t>(8, (R + want - 1) / want), (R + 65534) / 65535);
+}
+int64_t prep_parts(int64_t R, int C) {
+  const int64_t per = prep_rows_per(R, C);
+  return (R + per - 1) / per;
+}
+int64_t padded(int64_t c) { return (c + 7) & ~(int64_t)7; }
+size_t planes_bytes(int64_t R, int64_t C, int planes) {
+  return up256((size_t)planes * R * padded(C) * 2);
+}
+
+// src as operand planes at `out`; column sums to colsum if not null.
+cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const void* pre, int pre_t,
+                 int act, int planes, void* out, float* colsum, cudaStream_t st) {
+  Prep p = {};
+  p.src = src;
+  p.pre = pre;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.colsum = colsum;
+  p.R = R;
+  p.src_ld = ld;
+  p.ld = padded(C);
+  p.rows_per = prep_rows_per(R, C);
+  p.C = C;
+  p.src_t = (uint8_t)src_t;
+  p.pre_t = (uint8_t)pre_t;
+  p.act = (uint8_t)act;
+  p.planes = (uint8_t)planes;
+  const dim3 grid((unsigned)((C + 255) / 256), (unsigned)prep_parts(R, C));
+  prep_kernel<<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+int check_sizes(int64_t rows, int in_f, int out_f, ssd_dtype_t dt) {
+  if (dt != SSD_DTYPE_F32 && dt != SSD_DTYPE_BF16) return bad(SSD_ERR_ARG, "unknown dtype");
+  if (rows < 1 || in_f < 1 || out_f < 1)
+    return bad(SSD_ERR_ARG, "rows, in_features and out_features must be >= 1");
+  if (rows > (1LL << 30) || in_f > (1 << 24) || out_f > (1 << 24))
+    return bad(SSD_ERR_UNSUPPORTED, "rows above 2^30 or features above 2^24");
+  // tiles (of 128 x 64) are counted in 31 bits
+  for (const int64_t t : {((rows + 127) / 128) * ((int64_t)(std::max(in_f, out_f) + 63) / 64),
+                          (((int64_t)out_f + 127) / 128) * (((int64_t)in_f + 63) / 64)})
+    if (t * 16 > 0x7fffffff) return bad(SSD_ERR_UNSUPPORTED, "the product is too large");
+  return SSD_OK;
+}
+
+// Whether a bf16 matrix can be read by TMA where it lies.
+bool in_place(const void* p, int64_t ld, ssd_dtype_t dt) {
+  return dt == SSD_DTYPE_BF16 && al(p, 16) && ld % 8 == 0 && ld < (1LL << 38);
+}
+
+// rows up to which the weight is streamed through registers
+constexpr int kSkinnyBf16 = 16, kSkinnyF32 = 8;
+
+bool skinny(const void* x, int64_t sx, const void* w, int64_t rows, int K, ssd_dtype_t dt) {
+  if (dt == SSD_DTYPE_BF16)
+    return rows <= kSkinnyBf16 && K % 8 == 0 && al(x, 16) && al(w, 16) && (rows == 1 || sx % 8 == 0);
+  return rows <= kSkinnyF32 && K % 4 == 0 && al(x, 16) && al(w, 16) && (rows == 1 || sx % 4 == 0);
+}
+
+// every row of a tensor starts on a multiple of four elements
+bool wide4(const void* p, int64_t ld, size_t e) { return al(p, 4 * e) && ld % 4 == 0; }
+
+size_t fwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w) {
+  const int planes = dt == SSD_DTYPE_F32 ? 3 : 1;
+  size_t b = partial_bytes(plan_for(rows, N, K, planes == 3 ? 6 : 1), rows, N);
+  if (pack_x) b += planes_bytes(rows, K, planes);
+  if (pack_w) b += planes_bytes(N, K, planes);
+  return b;
+}
+size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w, bool pack_d) {
+  const int planes = dt == SSD_DTYPE_F32 ? 3 : 1, pairs = planes == 3 ? 6 : 1;
+  size_t b = std::max(partial_bytes(plan_for(rows, K, N, pairs), rows, K),
+                      partial_bytes(plan_for(N, K, rows, pairs), N, K));
+  b += up256((size_t)prep_parts(rows, N) * N * sizeof(float));
+  if (pack_x) b += planes_bytes(rows, K, planes);
+  if (pack_w) b += planes_bytes(N, K, planes);
+  if (pack_d) b += planes_bytes(rows, N, planes);
+  return b;
+}
+
+}  // namespace linear
+
+int linear_status(int reset, cudaStream_t st, int* bits) {
+  int h = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&h, linear::g_status_linear, sizeof(int), 0,
+                                            cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && reset && h != 0) {
+    static const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(linear::g_status_linear, &zero, sizeof(int), 0,
+                                cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
+  *bits = h;
+  return (int)e;
+}
+
+}  // namespace ssd
+
+using namespace ssd;
+using namespace ssd::linear;
+
+extern "C" {
+
+size_t ssd_linear_fwd_workspace_bytes(int64_t rows, int in_features, int out_features,
+                                      ssd_dtype_t dtype, int aligned) {
+  if (check_sizes(rows, in_features, out_features, dtype) != SSD_OK) return 0;
+  const bool pack = dtype == SSD_DTYPE_F32 || !aligned || in_features % 8 != 0;
+  // a strided x may be aligned while a weight of odd rows is not; the sum is enough for both
+  return std::max<size_t>(256, fwd_bytes(rows, in_features, out_features, dtype, pack, pack));
+}
+
+int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, const void* bias,
+                   const void* residual, int64_t residual_row_stride, int64_t rows, int in_features,
+                   int out_features, ssd_activation_t activation, ssd_dtype_t dtype,
+                   ssd_dtype_t residual_dtype, void* out, void* pre, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  const int c = check_sizes(rows, in_features, out_features, dtype);
+  if (c != SSD_OK) return c;
+  if (activation < SSD_ACT_NONE || activation > SSD_ACT_GELU)
+    return bad(SSD_ERR_ARG, "unknown activation");
+  if (residual && residual_dtype != dtype && residual_dtype != SSD_DTYPE_F32)
+    return bad(SSD_ERR_ARG, "the residual is fp32 or of the x dtype");
+  if (!x || !weight || !out) return bad(SSD_ERR_NULL, "x, weight and out are required");
+  const size_t e = esize(dtype), re = residual ? esize(residual_dtype) : e;
+  if (!al(x, e) || !al(weight, e) || !al(bias, e) || !al(residual, re) || !al(out, re) ||
+      !al(pre, dtype == SSD_DTYPE_BF16 ? 2 : 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (rows > 1 && (x_row_stride < in_features || (residual && residual_row_stride < out_features) ||
+                   x_row_stride > (1LL << 40) || residual_row_stride > (1LL << 40)))
+    return bad(SSD_ERR_ARG, "row strides must be at least the features, and below 2^40");
+  const int64_t K = in_features, N = out_features;
+  const int64_t sx = rows > 1 ? x_row_stride : padded(K);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Epilogue ep = {};
+  ep.bias = bias;
+  ep.bias_t = (uint8_t)type_of(dtype);
+  ep.res = residual;
+  ep.res_t = (uint8_t)type_of(residual_dtype);
+  ep.res_ld = rows > 1 ? residual_row_stride : padded(N);
+  ep.out = out;
+  ep.out_t = (uint8_t)type_of(residual ? residual_dtype : dtype);
+  ep.out_ld = N;
+  ep.pre = pre;
+  ep.pre_t = dtype == SSD_DTYPE_BF16 ? kF16 : kF32;
+  ep.act = (uint8_t)activation;
+  ep.wide = N % 4 == 0 && al(bias, 4 * e) && al(out, 4 * re) &&
+            al(pre, dtype == SSD_DTYPE_BF16 ? 8 : 16) &&
+            (!residual || wide4(residual, ep.res_ld, re));
+  if (skinny(x, sx, weight, rows, in_features, dtype)) {
+    if (dtype == SSD_DTYPE_BF16) {
+      const auto* xb = static_cast<const __nv_bfloat16*>(x);
+      const auto* wb = static_cast<const __nv_bfloat16*>(weight);
+      const unsigned grid = (unsigned)((N + 15) / 16);
+      if (rows <= 8)
+        skinny_bf16_kernel<1><<<grid, kSkinnyThreads, 0, st>>>(xb, sx, wb, (int)rows, N,
+                                                               in_features, ep);
+      else
+        skinny_bf16_kernel<2><<<grid, kSkinnyThreads, 0, st>>>(xb, sx, wb, (int)rows, N,
+                                                               in_features, ep);
+    } else {
+      const unsigned grid = (unsigned)((N + kSkinnyWarps * kF32Rows - 1) / (kSkinnyWarps * kF32Rows));
+      skinny_f32_kernel<<<grid, kSkinnyThreads, 0, st>>>(static_cast<const float*>(x), sx,
+                                                         static_cast<const float*>(weight),
+                                                         (int)rows, N, in_features, ep);
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? SSD_OK : cuda_bad(err, "linear launch");
+  }
+  const bool pack_x = !in_place(x, sx, dtype), pack_w = !in_place(weight, K, dtype);
+  if (!al(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace: 256-byte aligned");
+  const size_t need = fwd_bytes(rows, in_features, out_features, dtype, pack_x, pack_w);
+  if (need > 0 && !workspace) return bad(SSD_ERR_NULL, "workspace is required");
+  if (workspace_bytes < need) return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const int planes = dtype == SSD_DTYPE_F32 ? 3 : 1;
+  char* ws = static_cast<char*>(workspace);
+  Operand a = {x, rows, K, sx, 1}, b = {weight, N, K, K, 1};
+  if (pack_x) {
+    const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
+                                 nullptr, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
+    a = {ws, rows, K, padded(K), planes};
+    ws += planes_bytes(rows, K, planes);
+  }
+  if (pack_w) {
+    const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
+                                 ws, nullptr, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
+    b = {ws, N, K, padded(K), planes};
+    ws += planes_bytes(N, K, planes);
+  }
+  return gemm(a, false, b, false, rows, N, K, ep, reinterpret_cast<float*>(ws), st);
+}
+
+size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int in_features, int out_features,
+                                      ssd_dtype_t dtype, int aligned, int dout_as_is) {
+  if (check_sizes(rows, in_features, out_features, dtype) != SSD_OK) return 0;
+  const bool pack = dtype == SSD_DTYPE_F32 || !aligned;
+  return std::max<size_t>(
+      256, bwd_bytes(rows, in_features, out_features, dtype, pack || in_features % 8 != 0,
+                     pack || in_features % 8 != 0, pack || !dout_as_is || out_features % 8 != 0));
+}
+
+int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int64_t x_row_stride,
+                   const void* weight, const void* pre, int64_t rows, int in_features,
+                   int out_features, ssd_activation_t activation, ssd_dtype_t dtype, void* dx,
+                   void* dweight, void* dbias, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  const int c = check_sizes(rows, in_features, out_features, dtype);
+  if (c != SSD_OK) return c;
+  if (activation < SSD_ACT_NONE || activation > SSD_ACT_GELU)
+    return bad(SSD_ERR_ARG, "unknown activation");
+  if (dout_dtype != dtype && dout_dtype != SSD_DTYPE_F32)
+    return bad(SSD_ERR_ARG, "dout is fp32 or of the x dtype");
+  const bool act = activation != SSD_ACT_NONE;
+  if (!dout || (dweight && !x) || (dx && !weight) || (act && !pre) || !workspace)
+    return bad(SSD_ERR_NULL,
+               "dout and workspace, x for dweight, weight for dx and pre with an activation are "
+               "required");
+  const size_t e = esize(dtype);
+  if (!al(dout, esize(dout_dtype)) || !al(x, e) || !al(weight, e) || !al(dx, e) || !al(dweight, e) ||
+      !al(dbias, e) || !al(pre, dtype == SSD_DTYPE_BF16 ? 2 : 4) || !al(workspace, 256))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element (workspace: 256 bytes)");
+  if (rows > 1 && x && (x_row_stride < in_features || x_row_stride > (1LL << 40)))
+    return bad(SSD_ERR_ARG, "row strides must be at least the features, and below 2^40");
+  const int64_t K = in_features, N = out_features;
+  const int64_t sx = rows > 1 ? x_row_stride : padded(K);
+  const bool pack_x = dweight && !in_place(x, sx, dtype);
+  const bool pack_w = dx && !in_place(weight, K, dtype);
+  const bool products = dx || dweight;
+  const bool pack_d = products && (act || dout_dtype != dtype || !in_place(dout, N, dtype));
+  if (workspace_bytes < bwd_bytes(rows, in_features, out_features, dtype, pack_x, pack_w, pack_d))
+    return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const int planes = dtype == SSD_DTYPE_F32 ? 3 : 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  float* colsum = reinterpret_cast<float*>(ws);
+  ws += up256((size_t)prep_parts(rows, out_features) * N * sizeof(float));
+  Operand d = {dout, rows, N, N, 1}, w = {weight, N, K, K, 1}, xo = {x, rows, K, sx, 1};
+  if (pack_d || dbias) {
+    const cudaError_t err =
+        prep(dout, type_of(dout_dtype), N, rows, out_features, act ? pre : nullptr,
+             dtype == SSD_DTYPE_BF16 ? kF16 : kF32, activation, pack_d ? planes : 0, ws,
+             dbias ? colsum : nullptr, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
+    if (pack_d) {
+      d = {ws, rows, N, padded(N), planes};
+      ws += planes_bytes(rows, N, planes);
+    }
+    if (dbias) {
+      sum_rows_kernel<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(
+          colsum, (int)prep_parts(rows, out_features), out_features, dbias, type_of(dtype));
+      const cudaError_t err2 = cudaGetLastError();
+      if (err2 != cudaSuccess) return cuda_bad(err2, "linear dbias launch");
+    }
+  }
+  if (pack_w) {
+    const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
+                                 ws, nullptr, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
+    w = {ws, N, K, padded(K), planes};
+    ws += planes_bytes(N, K, planes);
+  }
+  if (pack_x) {
+    const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
+                                 nullptr, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
+    xo = {ws, rows, K, padded(K), planes};
+    ws += planes_bytes(rows, K, planes);
+  }
+  Epilogue ep = {};
+  ep.out_t = (uint8_t)type_of(dtype);
+  ep.out_ld = K;
+  float* part = reinterpret_cast<float*>(ws);
+  if (dx) {
+    ep.out = dx;
+    ep.wide = K % 4 == 0 && al(dx, 4 * e);
+    const int r = gemm(d, false, w, true, rows, K, N, ep, part, st);
+    if (r != SSD_OK) return r;
+  }
+  if (dweight) {
+    ep.out = dweight;
+    ep.wide = K % 4 == 0 && al(dweight, 4 * e);
+    return gemm(d, true, xo, true, N, K, rows, ep, part, st);
+  }
+  return SSD_OK;
+}
+
+}  // extern "C"

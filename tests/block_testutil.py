@@ -16,14 +16,14 @@ def half_step(dtype) -> float:
     return 0.0 if dtype == torch.float32 else torch.finfo(dtype).eps / 2
 
 
-def assert_within(got, ref, mag, ops, what=""):
-    """|got - ref| <= half a step of got's type * |ref| + ops * 2^-24 * mag,
-    element by element; NaN where ref is NaN."""
+def assert_within(got, ref, mag, ops, what="", extra=0.0):
+    """|got - ref| <= half a step of got's type * |ref| + ops * 2^-24 * mag +
+    extra, element by element; NaN where ref is NaN."""
     half = half_step(got.dtype)
     got = got.detach().double().cpu()
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{what}: NaNs differ"
-    e32 = ops * U32 * mag * (1 + half)
+    e32 = (ops * U32 * mag + extra) * (1 + half)
     tiny = 2.0 ** -126   # below the normal range nothing is claimed
     bad = ((got - ref).abs() > half * ref.abs() + e32 + tiny) & ~torch.isnan(ref)
     if bad.any():

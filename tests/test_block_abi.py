@@ -136,3 +136,39 @@ def test_clip_refusals(lib):
     ws = lib.ssd_clip_grads_workspace_bytes(2)
     assert f(wsb=ws - 1) == WORKSPACE and lib.ssd_clip_grads_workspace_bytes(-1) == 0
     assert lib.ssd_clip_grads_workspace_bytes(2000) > ws
+
+
+def test_linear_refusals(lib):
+    d = dict(x=16, sx=64, weight=16, bias=16, res=16, sr=32, rows=40, k=64, n=32, act=0, dtype=BF,
+             rdtype=F32, out=16, pre=None, ws=256, wsb=1 << 30, stream=None)
+    f = caller(lib, "ssd_linear_fwd", **d)
+    assert f(dtype=3) == ARG and f(act=3) == ARG and f(act=-1) == ARG
+    assert f(rows=0) == ARG and f(k=0) == ARG and f(n=-1) == ARG
+    assert f(dtype=F32, rdtype=BF) == ARG
+    assert f(sx=63) == ARG and f(sr=31) == ARG and f(sx=2 ** 41) == ARG
+    assert f(rows=2 ** 31) == UNSUPPORTED and f(k=2 ** 25) == UNSUPPORTED
+    assert f(rows=2 ** 30, n=2 ** 24) == UNSUPPORTED
+    for k in ("x", "weight", "out"):
+        assert f(**{k: None}) == NULL, k
+    assert f(x=17) == ALIGN and f(bias=17) == ALIGN and f(res=18) == ALIGN and f(pre=17) == ALIGN
+    assert f(ws=128) == ALIGN
+    # operands that are laid out in the workspace need it
+    assert f(x=18, wsb=0) == WORKSPACE and f(x=18, ws=None) == NULL
+    q = lib.ssd_linear_fwd_workspace_bytes
+    assert q(0, 64, 32, BF, 1) == 0 and q(40, 64, 32, 9, 1) == 0
+    big = 40000   # enough rows for no split
+    assert q(big, 64, 256, BF, 1) == 256
+    assert q(big, 64, 256, BF, 0) >= (big * 64 + 256 * 64) * 2
+    assert q(big, 65, 256, BF, 1) >= (big + 256) * 72 * 2
+    assert q(big, 64, 256, F32, 1) >= 3 * (big + 256) * 64 * 2
+    b = caller(lib, "ssd_linear_bwd", dout=16, ddt=BF, x=16, sx=64, weight=16, pre=None, rows=40,
+               k=64, n=32, act=0, dtype=BF, dx=16, dw=16, db=16, ws=256, wsb=1 << 30, stream=None)
+    assert b(ddt=7) == ARG and b(dtype=F32, ddt=BF) == ARG and b(act=4) == ARG and b(rows=0) == ARG
+    assert b(sx=60) == ARG
+    for k in ("dout", "x", "weight", "ws"):
+        assert b(**{k: None}) == NULL, k
+    assert b(act=1) == NULL                       # an activation needs pre
+    assert b(dout=17) == ALIGN and b(dw=1) == ALIGN and b(ws=64) == ALIGN
+    assert b(wsb=16) == WORKSPACE
+    assert lib.ssd_linear_bwd_workspace_bytes(40, 64, 32, BF, 1, 1) > 0
+    assert lib.ssd_linear_bwd_workspace_bytes(40, 0, 32, BF, 1, 1) == 0
