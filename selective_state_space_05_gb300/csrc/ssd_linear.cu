@@ -13,10 +13,10 @@
 // lo hi) are more K steps of the same sum, the smallest first.
 //
 // The kernel is persistent: one CTA an SM walks output tiles of 128 x BN; one
-// thread issues the TMA loads, one the MMAs, and four warps take finished
-// accumulators out of TMEM (two, so that the next tile's MMAs run meanwhile),
-// turn them through shared memory so that rows are written in whole sectors,
-// and apply bias, activation and residual on the way.  Where there are few
+// thread issues the TMA loads, one the MMAs, and eight warps take finished
+// accumulators out of TMEM (two, so that the next MMAs run meanwhile) into
+// registers, turn them through shared memory so that rows are written in whole
+// sectors, and apply bias, activation and residual on the way.  Where there are few
 // tiles, K is split over CTAs: each writes its partial sums in fp32 and a
 // second kernel adds them in a fixed order and applies the same epilogue.
 //
@@ -41,9 +41,13 @@ namespace ssd {
 namespace linear {
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kThreads = 192;             // warp 0: TMA, 1: MMA, 2-5: epilogue
-constexpr int kPitch = 36;                // floats a row of the epilogue's 32 x 32 block: 16-byte
-                                          // row accesses of eight lanes hit all 32 banks
+constexpr int kEpiWarps = 8;              // two a quarter of the TMEM lanes: half the columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0: TMA, 1: MMA, then the epilogue
+// K steps that one TMEM accumulator takes where the result is kept in fp32.
+// The tensor core's fp32 sum rounds towards zero at every MMA, an error that
+// grows with their number (relative 3.9e-6 after 320 MMAs, K = 5120, measured);
+// sums of 64 MMAs are added up in registers, to nearest, instead.
+constexpr int kExactSteps = 16;
 constexpr unsigned long long kWaitNs = 2000000000ull;   // limit of any single wait: 2 s
 constexpr uint32_t kSleepNs = 20000;
 
@@ -120,9 +124,26 @@ __device__ __forceinline__ void put4(void* p, int t, int64_t i, const float (&v)
   }
 }
 
+// The residual at row m, columns n .. n + 3 (zeros past N, and without one).
+// Apart from finish4, so that a thread has all of its loads in flight before
+// its first store (the output may be the residual's memory).
+__device__ __forceinline__ void residual4(const Epilogue& e, int64_t m, int64_t n, int64_t N,
+                                          float (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = 0.f;
+  if (!e.res) return;
+  if (e.wide) {
+    if (n < N) get4(e.res, e.res_t, m * e.res_ld + n, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) r[i] = get1(e.res, e.res_t, m * e.res_ld + n + i);
+  }
+}
+
 // Sums of row m, columns n .. n + 3 (those below N).  v is finished in place.
 __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int64_t n, int64_t N,
-                                        float (&v)[4]) {
+                                        float (&v)[4], const float (&res)[4]) {
   if (e.wide) {
     if (n >= N) return;
     if (e.bias) {
@@ -136,12 +157,9 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int64_t n,
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = act_f(e.act, v[i]);
     }
-    if (e.res) {
-      float r[4];
-      get4(e.res, e.res_t, m * e.res_ld + n, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += r[i];
-    }
+    for (int i = 0; i < 4; ++i)
+      if (e.res) v[i] += res[i];
     put4(e.out, e.out_t, m * e.out_ld + n, v);
   } else {
 #pragma unroll
@@ -150,9 +168,21 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int64_t n,
       float s = v[i] + (e.bias ? get1(e.bias, e.bias_t, n + i) : 0.f);
       if (e.pre) put1(e.pre, e.pre_t, m * N + n + i, s);
       s = act_f(e.act, s);
-      if (e.res) s += get1(e.res, e.res_t, m * e.res_ld + n + i);
+      if (e.res) s += res[i];
       put1(e.out, e.out_t, m * e.out_ld + n + i, s);
     }
+  }
+}
+
+// Four columns of a split's partial sums.
+__device__ __forceinline__ void partial4(float* part, int64_t at, int64_t n, int64_t N,
+                                         const float (&v)[4]) {
+  if ((N & 3) == 0) {
+    if (n < N) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) part[at + i] = v[i];
   }
 }
 
@@ -164,6 +194,7 @@ struct Gemm {
   int pairs;          // products of planes: 1, or 6 for fp32
   int tiles_m, tiles_n, splits, steps_per_split;
   int group_m;        // tiles of M walked together (L2 reuse)
+  int run;            // K steps an accumulator takes before it is added to the registers'
   float* partial;     // [splits][M][N] where splits > 1
   Epilogue e;
 };
@@ -195,7 +226,7 @@ template <int BN>
 struct alignas(1024) Smem {
   unsigned char a[Cfg<BN>::kStages][Cfg<BN>::kStageA];
   unsigned char b[Cfg<BN>::kStages][Cfg<BN>::kStageB];
-  float turn[4][32 * kPitch];
+  float turn[kEpiWarps][32 * 16], res[kEpiWarps][32 * 16];
   uint64_t full[Cfg<BN>::kStages], empty[Cfg<BN>::kStages], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
@@ -295,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.tfull[i], 1);
-      tc::mbar_init(&s.tempty[i], 4);
+      tc::mbar_init(&s.tempty[i], kEpiWarps);
     }
     tc::mbar_init(&s.drain, 1);
     tc::mbar_fence_init();
@@ -353,31 +384,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       int st = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int it = blockIdx.x; it < items && ok; it += gridDim.x, ++n) {
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
         int tm, tn, split;
         tile_of(p, it, tm, tn, split);
         const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
-        const int buf = n & 1;
-        if (!wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort)) break;
-        tc::fence_after_sync();
-        for (int k = k0; k < k1; ++k) {
-          if (!wait_phase(&s.full[st], ph, &s.abort)) {
-            ok = false;
-            break;
-          }
+        for (int r0 = k0; r0 < k1 && ok; r0 += p.run, ++n) {
+          const int r1 = min(r0 + p.run, k1), buf = n & 1;
+          ok = wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort);
           tc::fence_after_sync();
-          const uint64_t da = tile_desc<AMN>(s.a[st]), db = tile_desc<BMN>(s.b[st]);
+          for (int k = r0; k < r1 && ok; ++k) {
+            ok = wait_phase(&s.full[st], ph, &s.abort);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t da = tile_desc<AMN>(s.a[st]), db = tile_desc<BMN>(s.b[st]);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc::mma_ss(tmem + buf * BN, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2),
-                       idesc, k > k0 || kk > 0);
-          tc::mma_commit(&s.empty[st]);
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              tc::mma_ss(tmem + buf * BN, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2),
+                         idesc, k > r0 || kk > 0);
+            tc::mma_commit(&s.empty[st]);
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
+            }
           }
+          if (ok) tc::mma_commit(&s.tfull[buf]);
         }
-        if (ok) tc::mma_commit(&s.tfull[buf]);
       }
       // every MMA has finished before the operands' memory and TMEM are given back
       tc::mma_commit(&s.drain);
@@ -386,51 +417,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3;   // this warp's quarter of the TMEM lanes
+    constexpr int kCols = BN / 2;   // and its columns: half of the tile's
+    const int c0 = ((warp - 2) >> 2) * kCols;
     float* turn = s.turn[warp - 2];
+    float* kept = s.res[warp - 2] + 4 * lane;   // this lane's residual, four rows' pieces
     int n = 0;
-    for (int it = blockIdx.x; it < items; it += gridDim.x, ++n) {
+    bool ok = true;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
       int tm, tn, split;
       tile_of(p, it, tm, tn, split);
-      const int buf = n & 1;
-      // one verdict for the warp: the TMEM loads below take all of its lanes
-      if (!__all_sync(0xffffffffu, wait_phase(&s.tfull[buf], (n >> 1) & 1, &s.abort))) break;
-      tc::fence_after_sync();
+      const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+      float acc[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+      for (int r0 = k0; r0 < k1; r0 += p.run, ++n) {
+        const int buf = n & 1;
+        // one verdict for the warp: the TMEM loads below take all of its lanes
+        ok = __all_sync(0xffffffffu, wait_phase(&s.tfull[buf], (n >> 1) & 1, &s.abort));
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          uint32_t r[16];
+          tc::tmem_ld16(tmem + buf * BN + c0 + c + (static_cast<uint32_t>(q * 32) << 16), r);
+          tc::tmem_ld_wait_regs(r);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(r[i]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.tempty[buf]);
+      }
+      if (!ok) break;
+      // rows by lane -> 8 rows of four lanes at a time, 16 columns a turn; the
+      // 16-byte pieces of a row are exchanged by its number so that both
+      // directions reach all banks
       const int64_t m0 = (int64_t)tm * kBM + q * 32;
-      const int64_t n0 = (int64_t)tn * BN;
+      const int64_t n0 = (int64_t)tn * BN + c0;
       const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
-      float* part = p.splits > 1 ? p.partial + (int64_t)split * p.M * p.N : nullptr;
+      const int rr = lane >> 2, cc = lane & 3;
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        const int64_t col = n0 + c + 4 * cc;
+        if (n0 + c < p.N) {
+          if (p.splits == 1 && p.e.res) {
+            float res[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (8 * i + rr < rows) residual4(p.e, m0 + 8 * i + rr, col, p.N, res[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(kept + i * 128) =
+                  make_float4(res[i][0], res[i][1], res[i][2], res[i][3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(turn + lane * 16 + 4 * (i ^ ((lane >> 1) & 3))) =
+                make_float4(acc[c + 4 * i], acc[c + 4 * i + 1], acc[c + 4 * i + 2],
+                            acc[c + 4 * i + 3]);
+          __syncwarp();
+          // (rolled: unrolled copies of the epilogue would cost acc its registers)
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        if (n0 + c >= p.N) break;
-        uint32_t r[32];
-        tc::tmem_ld32(tmem + buf * BN + c + (static_cast<uint32_t>(q * 32) << 16), r);
-        tc::tmem_ld_wait_regs(r);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(turn + lane * kPitch + 4 * i) =
-              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-        __syncwarp();
-        const int64_t col = n0 + c + 4 * (lane & 7);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3);
-          if (rr < rows) {
-            const float4 f = *reinterpret_cast<const float4*>(turn + rr * kPitch + 4 * (lane & 7));
+          for (int r = rr; r < rows; r += 8) {
+            const float4 f =
+                *reinterpret_cast<const float4*>(turn + r * 16 + 4 * (cc ^ ((r >> 1) & 3)));
             float v[4] = {f.x, f.y, f.z, f.w};
-            if (part) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (col + j < p.N) part[(m0 + rr) * p.N + col + j] = v[j];
+            if (p.splits > 1) {
+              partial4(p.partial, ((int64_t)split * p.M + m0 + r) * p.N + col, col, p.N, v);
             } else {
-              finish4(p.e, m0 + rr, col, p.N, v);
+              const float4 k = *reinterpret_cast<const float4*>(kept + (r >> 3) * 128);
+              const float res[4] = {k.x, k.y, k.z, k.w};
+              finish4(p.e, m0 + r, col, p.N, v, res);
             }
           }
         }
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&s.tempty[buf]);
     }
   }
   __syncthreads();
@@ -446,14 +508,21 @@ __global__ void __launch_bounds__(256)
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= M * per_row) return;
   const int64_t m = i / per_row, n = (i - m * per_row) * 4;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  float v[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
+  residual4(e, m, n, N, res);
+#pragma unroll 4
   for (int s = 0; s < splits; ++s) {
     const float* p = part + (s * M + m) * N + n;
+    if ((N & 3) == 0) {
+      const float4 f = *reinterpret_cast<const float4*>(p);
+      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (n + j < N) v[j] += p[j];
+      for (int j = 0; j < 4; ++j)
+        if (n + j < N) v[j] += p[j];
+    }
   }
-  finish4(e, m, n, N, v);
+  finish4(e, m, n, N, v, res);
 }
 
 // ------------------------------------------------------- operands made ready
@@ -561,12 +630,13 @@ __global__ void __launch_bounds__(kSkinnyThreads)
   for (int i = threadIdx.x; i < NT * 8 * 4; i += kSkinnyThreads) {
     const int m = i >> 2, c = (i & 3) * 4;
     if (m >= M) continue;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
+    residual4(e, m, n0 + c, N, res);
 #pragma unroll
     for (int q = 0; q < kSkinnyWarps; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += acc[q][c + j][m];
-    finish4(e, m, n0 + c, N, v);
+    finish4(e, m, n0 + c, N, v, res);
   }
 }
 
@@ -609,7 +679,11 @@ __global__ void __launch_bounds__(kSkinnyThreads)
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1)
         acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], off);
-    if (lane == 0) finish4(e, m, n0, N, acc[m]);
+    if (lane == 0) {
+      float res[4];
+      residual4(e, m, n0, N, res);
+      finish4(e, m, n0, N, acc[m], res);
+    }
   }
 }
 
@@ -729,6 +803,7 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.splits = pl.splits;
   g.steps_per_split = pl.steps_per;
   g.group_m = 8;
+  g.run = e.out_t == kF32 ? kExactSteps : pl.steps_per;
   g.partial = part;
   g.e = e;
   const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
