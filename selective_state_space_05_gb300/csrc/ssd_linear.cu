@@ -12,7 +12,11 @@
 // the six products down to 2^-24 (hi hi, hi mid, mid hi, mid mid, hi lo,
 // lo hi) are more K steps of the same sum, the smallest first.
 //
-// The kernel is persistent: one CTA an SM walks output tiles of 128 x BN; one
+// The kernel is persistent.  A pair of CTAs on two SMs walks output tiles of
+// 256 x BN (cta_group::2: each SM reads half of B's tile, which the shared
+// memory's bandwidth needs: with 128 x 256 tiles on one SM, 96 KB a K step are
+// written and read in 512 tensor cycles, and it reached 1.5 PFLOP/s); small
+// products take 128 x BN tiles on single CTAs.  In a CTA one
 // thread issues the TMA loads, one the MMAs, and eight warps take finished
 // accumulators out of TMEM (two, so that the next MMAs run meanwhile) into
 // registers, turn them through shared memory so that rows are written in whole
@@ -215,25 +219,30 @@ __device__ __forceinline__ void planes_of(int pairs, int q, int& a, int& b) {
   }
 }
 
-template <int BN>
+// CG CTAs work on a tile of CG * kBM x BN: a CTA holds kBM rows of A and BN / CG
+// rows of B.
+template <int CG, int BN>
 struct Cfg {
-  static constexpr int kStageA = kBM * kBK * 2, kStageB = BN * kBK * 2;
+  static constexpr int kRowsB = BN / CG;
+  static constexpr int kStageA = kBM * kBK * 2, kStageB = kRowsB * kBK * 2;
   static constexpr int kStages = 192 * 1024 / (kStageA + kStageB);
   static constexpr uint32_t kTmemCols = 2 * BN;   // 128, 256 or 512
 };
 
-template <int BN>
+template <int CG, int BN>
 struct alignas(1024) Smem {
-  unsigned char a[Cfg<BN>::kStages][Cfg<BN>::kStageA];
-  unsigned char b[Cfg<BN>::kStages][Cfg<BN>::kStageB];
+  using C = Cfg<CG, BN>;
+  unsigned char a[C::kStages][C::kStageA];
+  unsigned char b[C::kStages][C::kStageB];
   float turn[kEpiWarps][32 * 16], res[kEpiWarps][32 * 16];
-  uint64_t full[Cfg<BN>::kStages], empty[Cfg<BN>::kStages], tfull[2], tempty[2], drain;
+  uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Smem<256>) + 1024 <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<64>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<2, 256>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<2, 128>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<1, 128>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<1, 64>) + 1024 <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -266,25 +275,17 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                            int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-
 // One stage's tile of an operand: ROWS rows of M or N from r0, kBK of K from k0.
-template <int ROWS, bool MN>
+// bar: the barrier, for a CTA pair as a shared::cluster address.
+template <int CG, int ROWS, bool MN>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar,
-                                          int r0, int k0, int plane) {
-  if constexpr (MN) {
+                                          uint32_t pair_bar, int r0, int k0, int plane) {
 #pragma unroll
-    for (int j = 0; j < ROWS / 64; ++j)
-      tma_load_3d(dst + j * (kBK * 128), map, bar, r0 + 64 * j, k0, plane);
-  } else {
-    tma_load_3d(dst, map, bar, k0, r0, plane);
+  for (int j = 0; j < (MN ? ROWS / 64 : 1); ++j) {
+    unsigned char* to = dst + j * (kBK * 128);
+    const int x = MN ? r0 + 64 * j : k0, y = MN ? k0 : r0;
+    if constexpr (CG == 2) tc::tma_load_3d_pair(to, map, pair_bar, x, y, plane);
+    else tc::tma_load_3d(to, map, bar, x, y, plane);
   }
 }
 template <bool MN>
@@ -306,16 +307,21 @@ __device__ __forceinline__ void tile_of(const Gemm& p, int item, int& tm, int& t
   tn = r / gm;
 }
 
-template <int BN, bool AMN, bool BMN>
-__global__ void __launch_bounds__(kThreads, 1)
+// A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
+// leader's `full`; the leader issues the MMAs and signals `empty` and `tfull`
+// of both; both CTAs' epilogues arrive on the leader's `tempty`.
+template <int CG, int BN, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ Gemm p) {
-  using C = Cfg<BN>;
+  using C = Cfg<CG, BN>;
   constexpr int S = C::kStages;
   extern __shared__ unsigned char raw[];
-  Smem<BN>& s = *reinterpret_cast<Smem<BN>*>(
+  Smem<CG, BN>& s = *reinterpret_cast<Smem<CG, BN>*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)tc::cluster_rank() : 0;
+  const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   const int items = p.tiles_m * p.tiles_n * p.splits;
   const int all_steps = p.kblocks * p.pairs;
 
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.tfull[i], 1);
-      tc::mbar_init(&s.tempty[i], kEpiWarps);
+      tc::mbar_init(&s.tempty[i], CG * kEpiWarps);
     }
     tc::mbar_init(&s.drain, 1);
     tc::mbar_fence_init();
@@ -335,11 +341,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tma_prefetch_desc(&mb);
   }
   if (warp == 1) {
-    tc::tmem_alloc(&s.tmem, C::kTmemCols);
-    tc::tmem_relinquish();
+    if constexpr (CG == 2) {
+      tc::tmem_alloc_pair(&s.tmem, C::kTmemCols);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(&s.tmem, C::kTmemCols);
+      tc::tmem_relinquish();
+    }
     tc::fence_before_sync();
   }
   __syncthreads();
+  if constexpr (CG == 2) tc::cluster_sync();   // the peer's barriers are ready
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
 
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       int issued = 0;
       bool ok = true;
-      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      for (int it = first; it < items && ok; it += stride) {
         int tm, tn, split;
         tile_of(p, it, tm, tn, split);
         const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
@@ -362,9 +374,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           int pa, pb;
           planes_of(p.pairs, q, pa, pb);
           const int kk = (k - q * p.kblocks) * kBK;
-          tc::mbar_arrive_expect_tx(&s.full[st], C::kStageA + C::kStageB);
-          load_tile<kBM, AMN>(s.a[st], &ma, &s.full[st], tm * kBM, kk, pa);
-          load_tile<BN, BMN>(s.b[st], &mb, &s.full[st], tn * BN, kk, pb);
+          if (rank == 0)
+            tc::mbar_arrive_expect_tx(&s.full[st], CG * (C::kStageA + C::kStageB));
+          const uint32_t bar = CG == 2 ? tc::mapa(&s.full[st], 0) : 0;
+          load_tile<CG, kBM, AMN>(s.a[st], &ma, &s.full[st], bar, (tm * CG + rank) * kBM, kk, pa);
+          load_tile<CG, C::kRowsB, BMN>(s.b[st], &mb, &s.full[st], bar,
+                                        tn * BN + rank * C::kRowsB, kk, pb);
           ++issued;
           if (++st == S) {
             st = 0;
@@ -372,19 +387,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) {   // no copy outlives the CTA
+      // no copy outlives the CTA (a pair's are counted by the leader, which
+      // both CTAs wait for at the end)
+      if (!ok && rank == 0) {
         for (int i = max(0, issued - S); i < issued; ++i)
           wait_drain(&s.full[i % S], (i / S) & 1);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16(kBM, BN, AMN, BMN);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = tc::idesc_bf16(CG * kBM, BN, AMN, BMN);
+      auto commit = [](uint64_t* bar) {
+        if constexpr (CG == 2) tc::mma_commit_pair(bar);
+        else tc::mma_commit(bar);
+      };
       int st = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      for (int it = first; it < items && ok; it += stride) {
         int tm, tn, split;
         tile_of(p, it, tm, tn, split);
         const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
@@ -398,22 +419,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             const uint64_t da = tile_desc<AMN>(s.a[st]), db = tile_desc<BMN>(s.b[st]);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              tc::mma_ss(tmem + buf * BN, da + kk * (AMN ? 128 : 2), db + kk * (BMN ? 128 : 2),
-                         idesc, k > r0 || kk > 0);
-            tc::mma_commit(&s.empty[st]);
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              const uint64_t a = da + kk * (AMN ? 128 : 2), b = db + kk * (BMN ? 128 : 2);
+              if constexpr (CG == 2)
+                tc::mma_ss_pair(tmem + buf * BN, a, b, idesc, k > r0 || kk > 0);
+              else
+                tc::mma_ss(tmem + buf * BN, a, b, idesc, k > r0 || kk > 0);
+            }
+            commit(&s.empty[st]);
             if (++st == S) {
               st = 0;
               ph ^= 1;
             }
           }
-          if (ok) tc::mma_commit(&s.tfull[buf]);
+          if (ok) commit(&s.tfull[buf]);
         }
       }
       // every MMA has finished before the operands' memory and TMEM are given back
-      tc::mma_commit(&s.drain);
-      wait_drain(&s.drain, 0);
+      commit(&s.drain);
     }
+    // (in a pair the leader's commits arrive at the peer's barriers too: its
+    // memory stays until the last of them has)
+    if (lane == 0) wait_drain(&s.drain, 0);
     __syncwarp();
   } else {
     const int q = warp & 3;   // this warp's quarter of the TMEM lanes
@@ -423,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* kept = s.res[warp - 2] + 4 * lane;   // this lane's residual, four rows' pieces
     int n = 0;
     bool ok = true;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = first; it < items; it += stride) {
       int tm, tn, split;
       tile_of(p, it, tm, tn, split);
       const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
@@ -446,13 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s.tempty[buf]);
+        if (lane == 0) {
+          if constexpr (CG == 2) tc::mbar_arrive_cluster(tc::mapa(&s.tempty[buf], 0));
+          else tc::mbar_arrive(&s.tempty[buf]);
+        }
       }
       if (!ok) break;
       // rows by lane -> 8 rows of four lanes at a time, 16 columns a turn; the
       // 16-byte pieces of a row are exchanged by its number so that both
       // directions reach all banks
-      const int64_t m0 = (int64_t)tm * kBM + q * 32;
+      const int64_t m0 = ((int64_t)tm * CG + rank) * kBM + q * 32;
       const int64_t n0 = (int64_t)tn * BN + c0;
       const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
       const int rr = lane >> 2, cc = lane & 3;
@@ -497,7 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem, C::kTmemCols);
+  if constexpr (CG == 2) {
+    tc::cluster_sync();   // nothing of the peer's is needed or written any more
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, C::kTmemCols);
+  } else {
+    if (warp == 1) tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
 }
 
 // Adds the partial sums of split K, in order, and finishes them.
@@ -736,27 +771,33 @@ bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
 
 // How a product of M x N with `steps` K steps is cut: tile width and splits.
 struct Plan {
-  int bn, splits, steps_per;
+  int cg, bn, splits, steps_per;
 };
 Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs) {
   const int sms = row::sm_count();
   const int steps = (int)((K + kBK - 1) / kBK) * pairs;
-  Plan best = {256, 1, steps};
+  // tile shapes and the time of one K step, in units of the largest tile's
+  struct Tile {
+    int cg, bn;
+    double step;
+  };
+  constexpr Tile kTiles[] = {{2, 256, 1.0}, {2, 128, 0.62}, {1, 128, 0.6}, {1, 64, 0.42}};
+  Plan best = {2, 256, 1, steps};
   double best_cost = 1e30;
-  for (int bn = 64; bn <= 256; bn *= 2) {
-    const int64_t tiles = ((M + kBM - 1) / kBM) * ((N + bn - 1) / bn);
-    const double step = bn == 256 ? 1.0 : bn == 128 ? 0.6 : 0.42;
-    const double fixed = 6.0 + 8.0 * bn / 256;   // pipeline fill and the last epilogue
+  for (const Tile& t : kTiles) {
+    const int64_t tiles = ((M + kBM * t.cg - 1) / (kBM * t.cg)) * ((N + t.bn - 1) / t.bn);
+    const double fixed = 6.0 + 8.0 * t.bn / 256;   // pipeline fill and the last epilogue
     for (int splits = 1; splits <= 16; splits *= 2) {
       const int per = (steps + splits - 1) / splits;
       if (splits > 1 && per < 4) break;
-      const int64_t waves = (tiles * splits + sms - 1) / sms;
-      double cost = waves * per * step + fixed;
+      const int64_t at_once = sms / t.cg;
+      const int64_t waves = (tiles * splits + at_once - 1) / at_once;
+      double cost = waves * per * t.step + fixed;
       // partial sums are written, read and joined by another launch
       if (splits > 1) cost += 12.0 + (double)M * N * (splits * 2 + 1) * 4 / 1.5e6;
       if (cost < best_cost) {
         best_cost = cost;
-        best = {bn, splits, per};
+        best = {t.cg, t.bn, splits, per};
       }
     }
   }
@@ -767,21 +808,51 @@ size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? up256((size_t)p.splits * M * N * sizeof(float)) : 0;
 }
 
-template <int BN, bool AMN, bool BMN>
-cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g, int grid,
-                        cudaStream_t st) {
-  const size_t smem = sizeof(Smem<BN>) + 1024;
-  static std::atomic<bool> done[64];
+// Persistent CTAs (or pairs) of a kernel that fit the device at once, cached
+// per device; the first call also opts in to its shared memory.
+template <int CG, int BN, bool AMN, bool BMN>
+cudaError_t resident(int* n) {
+  static std::atomic<int> cached[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(gemm_kernel<BN, AMN, BMN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+  const bool known = dev >= 0 && dev < 64;
+  *n = known ? cached[dev].load(std::memory_order_acquire) : 0;
+  if (*n > 0) return cudaSuccess;
+  const size_t smem = sizeof(Smem<CG, BN>) + 1024;
+  auto* kernel = gemm_kernel<CG, BN, AMN, BMN>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  *n = row::sm_count() / CG;
+  if (CG > 1) {   // some SMs may have no partner
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(row::sm_count() / CG * CG);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = CG;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int most = 0;
+    e = cudaOccupancyMaxActiveClusters(&most, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+    if (most > 0) *n = std::min(*n, most);
   }
-  gemm_kernel<BN, AMN, BMN><<<grid, kThreads, smem, st>>>(ma, mb, g);
+  if (known) cached[dev].store(*n, std::memory_order_release);
+  return cudaSuccess;
+}
+
+template <int CG, int BN, bool AMN, bool BMN>
+cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g,
+                        cudaStream_t st) {
+  int at_once = 0;
+  const cudaError_t e = resident<CG, BN, AMN, BMN>(&at_once);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int grid = CG * (int)std::min<int64_t>(items, at_once);
+  gemm_kernel<CG, BN, AMN, BMN><<<grid, kThreads, sizeof(Smem<CG, BN>) + 1024, st>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
@@ -791,31 +862,30 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   const int pairs = a.planes == 3 ? 6 : 1;
   const Plan pl = plan_for(M, N, K, pairs);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, pl.bn))
+  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, pl.bn / pl.cg))
     return bad(SSD_ERR_CUDA, "linear: a tensor map could not be made");
   Gemm g = {};
   g.M = M;
   g.N = N;
   g.kblocks = (int)((K + kBK - 1) / kBK);
   g.pairs = pairs;
-  g.tiles_m = (int)((M + kBM - 1) / kBM);
+  g.tiles_m = (int)((M + kBM * pl.cg - 1) / (kBM * pl.cg));
   g.tiles_n = (int)((N + pl.bn - 1) / pl.bn);
   g.splits = pl.splits;
   g.steps_per_split = pl.steps_per;
-  g.group_m = 8;
+  g.group_m = 8 / pl.cg;
   g.run = e.out_t == kF32 ? kExactSteps : pl.steps_per;
   g.partial = part;
   g.e = e;
-  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int grid = (int)std::min<int64_t>(items, row::sm_count());
   cudaError_t err;
-#define SSD_GEMM(BN)                                                          \
-  err = amn ? launch_gemm<BN, true, true>(ma, mb, g, grid, st)                \
-            : bmn ? launch_gemm<BN, false, true>(ma, mb, g, grid, st)         \
-                  : launch_gemm<BN, false, false>(ma, mb, g, grid, st)
-  if (pl.bn == 256) SSD_GEMM(256);
-  else if (pl.bn == 128) SSD_GEMM(128);
-  else SSD_GEMM(64);
+#define SSD_GEMM(CG, BN)                                                      \
+  err = amn ? launch_gemm<CG, BN, true, true>(ma, mb, g, st)            \
+            : bmn ? launch_gemm<CG, BN, false, true>(ma, mb, g, st)     \
+                  : launch_gemm<CG, BN, false, false>(ma, mb, g, st)
+  if (pl.cg == 2 && pl.bn == 256) SSD_GEMM(2, 256);
+  else if (pl.cg == 2) SSD_GEMM(2, 128);
+  else if (pl.bn == 128) SSD_GEMM(1, 128);
+  else SSD_GEMM(1, 64);
 #undef SSD_GEMM
   if (err != cudaSuccess) return cuda_bad(err, "linear launch");
   if (pl.splits > 1) {
