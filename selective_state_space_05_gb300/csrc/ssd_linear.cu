@@ -70,7 +70,8 @@ struct Epilogue {
   void* pre;
   int64_t res_ld, out_ld;
   uint8_t bias_t, res_t, out_t, pre_t, act;
-  bool wide;   // four columns at once: every row of every tensor stays aligned for it
+  bool wide;    // four columns at once: every row of every tensor stays aligned for it
+  bool wide8;   // eight
 };
 
 __device__ __forceinline__ float act_f(int act, float v) {
@@ -178,15 +179,32 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int64_t n,
   }
 }
 
-// Four columns of a split's partial sums.
-__device__ __forceinline__ void partial4(float* part, int64_t at, int64_t n, int64_t N,
-                                         const float (&v)[4]) {
-  if ((N & 3) == 0) {
-    if (n < N) *reinterpret_cast<float4*>(part + at) = make_float4(v[0], v[1], v[2], v[3]);
+// Eight consecutive elements (16-byte accesses).
+__device__ __forceinline__ void get8(const void* p, int t, float (&v)[8]) {
+  if (t == kF32) {
+    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
+    row::unpack(*static_cast<const uint4*>(p), v);
+  }
+}
+__device__ __forceinline__ void put8(void* p, int t, const float (&v)[8]) {
+  if (t == kF32) {
+    static_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    static_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < N) part[at + i] = v[i];
+    for (int i = 0; i < 4; ++i) {
+      if (t == kF16) {
+        const __half2 h = __floats2half2_rn(half_range(v[2 * i]), half_range(v[2 * i + 1]));
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        u[i] = tc::pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      }
+    }
+    *static_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -197,6 +215,8 @@ struct Gemm {
   int kblocks;        // K in steps of kBK
   int pairs;          // products of planes: 1, or 6 for fp32
   int tiles_m, tiles_n, splits, steps_per_split;
+  int bn;             // tile width, a multiple of 32 up to 256
+  int stages;         // operand tiles in flight
   int group_m;        // tiles of M walked together (L2 reuse)
   int run;            // K steps an accumulator takes before it is added to the registers'
   float* partial;     // [splits][M][N] where splits > 1
@@ -220,29 +240,25 @@ __device__ __forceinline__ void planes_of(int pairs, int q, int& a, int& b) {
 }
 
 // CG CTAs work on a tile of CG * kBM x BN: a CTA holds kBM rows of A and BN / CG
-// rows of B.
-template <int CG, int BN>
-struct Cfg {
-  static constexpr int kRowsB = BN / CG;
-  static constexpr int kStageA = kBM * kBK * 2, kStageB = kRowsB * kBK * 2;
-  static constexpr int kStages = 192 * 1024 / (kStageA + kStageB);
-  static constexpr uint32_t kTmemCols = 2 * BN;   // 128, 256 or 512
-};
+// rows of B (whole blocks of 64 where B is MN-major).
+constexpr int kStageA = kBM * kBK * 2;
+constexpr int kOperandBytes = 192 * 1024, kMaxStages = 10;
+__host__ __device__ constexpr int rows_b(int cg, int bn, bool mn) {
+  return mn ? (bn / cg + 63) / 64 * 64 : bn / cg;
+}
+__host__ __device__ constexpr int stage_b(int cg, int bn, bool mn) {
+  return rows_b(cg, bn, mn) * kBK * 2;
+}
+constexpr uint32_t kTmemCols = 512;   // two accumulators of up to 256 columns
 
-template <int CG, int BN>
 struct alignas(1024) Smem {
-  using C = Cfg<CG, BN>;
-  unsigned char a[C::kStages][C::kStageA];
-  unsigned char b[C::kStages][C::kStageB];
-  float turn[kEpiWarps][32 * 16], res[kEpiWarps][32 * 16];
-  uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
+  unsigned char operands[kOperandBytes];   // stages of A's tile, then B's
+  float turn[kEpiWarps][32 * 32];
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Smem<2, 256>) + 1024 <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<2, 128>) + 1024 <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<1, 128>) + 1024 <= 227 * 1024, "shared memory");
-static_assert(sizeof(Smem<1, 64>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
@@ -275,13 +291,15 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// One stage's tile of an operand: ROWS rows of M or N from r0, kBK of K from k0.
-// bar: the barrier, for a CTA pair as a shared::cluster address.
-template <int CG, int ROWS, bool MN>
+// One stage's tile of an operand: `rows` (at most MOST) rows of M or N from r0,
+// kBK of K from k0.  bar: the barrier, for a CTA pair as a shared::cluster
+// address.
+template <int CG, int MOST, bool MN>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar,
-                                          uint32_t pair_bar, int r0, int k0, int plane) {
+                                          uint32_t pair_bar, int rows, int r0, int k0, int plane) {
 #pragma unroll
-  for (int j = 0; j < (MN ? ROWS / 64 : 1); ++j) {
+  for (int j = 0; j < (MN ? MOST / 64 : 1); ++j) {
+    if (MN && 64 * j >= rows) break;
     unsigned char* to = dst + j * (kBK * 128);
     const int x = MN ? r0 + 64 * j : k0, y = MN ? k0 : r0;
     if constexpr (CG == 2) tc::tma_load_3d_pair(to, map, pair_bar, x, y, plane);
@@ -310,15 +328,14 @@ __device__ __forceinline__ void tile_of(const Gemm& p, int item, int& tm, int& t
 // A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
 // leader's `full`; the leader issues the MMAs and signals `empty` and `tfull`
 // of both; both CTAs' epilogues arrive on the leader's `tempty`.
-template <int CG, int BN, bool AMN, bool BMN>
+template <int CG, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ Gemm p) {
-  using C = Cfg<CG, BN>;
-  constexpr int S = C::kStages;
   extern __shared__ unsigned char raw[];
-  Smem<CG, BN>& s = *reinterpret_cast<Smem<CG, BN>*>(
-      (reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int S = p.stages, BN = p.bn;
+  const int rowsB = rows_b(CG, BN, BMN), stage = kStageA + rowsB * kBK * 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)tc::cluster_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
@@ -342,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   }
   if (warp == 1) {
     if constexpr (CG == 2) {
-      tc::tmem_alloc_pair(&s.tmem, C::kTmemCols);
+      tc::tmem_alloc_pair(&s.tmem, kTmemCols);
       tc::tmem_relinquish_pair();
     } else {
-      tc::tmem_alloc(&s.tmem, C::kTmemCols);
+      tc::tmem_alloc(&s.tmem, kTmemCols);
       tc::tmem_relinquish();
     }
     tc::fence_before_sync();
@@ -355,53 +372,65 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
 
+  // The TMA and MMA warps run their loops converged, one elected lane issuing:
+  // descriptors and coordinates then live in uniform registers.  (With the
+  // loops inside one lane's branch, a K step's four MMAs and their commit took
+  // about 500 cycles to issue, as long as the MMAs themselves.)
   if (warp == 0) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      int issued = 0;
-      bool ok = true;
-      for (int it = first; it < items && ok; it += stride) {
-        int tm, tn, split;
-        tile_of(p, it, tm, tn, split);
-        const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
-        for (int k = k0; k < k1; ++k) {
-          if (!wait_phase(&s.empty[st], ph ^ 1, &s.abort)) {
-            ok = false;
-            break;
-          }
-          const int q = k / p.kblocks;
-          int pa, pb;
-          planes_of(p.pairs, q, pa, pb);
-          const int kk = (k - q * p.kblocks) * kBK;
+    int st = 0;
+    uint32_t ph = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int it = first; it < items && ok; it += stride) {
+      int tm, tn, split;
+      tile_of(p, it, tm, tn, split);
+      const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+      int q = k0 / p.kblocks, kb = k0 - q * p.kblocks;   // product of planes, K step in it
+      int pa, pb;
+      planes_of(p.pairs, q, pa, pb);
+      for (int k = k0; k < k1; ++k) {
+        if (kb == p.kblocks) {
+          kb = 0;
+          planes_of(p.pairs, ++q, pa, pb);
+        }
+        const int kk = kb++ * kBK;
+        ok = __all_sync(0xffffffffu, wait_phase(&s.empty[st], ph ^ 1, &s.abort));
+        if (!ok) break;
+        if (tc::elect_one()) {
           if (rank == 0)
-            tc::mbar_arrive_expect_tx(&s.full[st], CG * (C::kStageA + C::kStageB));
+            tc::mbar_arrive_expect_tx(&s.full[st], CG * stage);
           const uint32_t bar = CG == 2 ? tc::mapa(&s.full[st], 0) : 0;
-          load_tile<CG, kBM, AMN>(s.a[st], &ma, &s.full[st], bar, (tm * CG + rank) * kBM, kk, pa);
-          load_tile<CG, C::kRowsB, BMN>(s.b[st], &mb, &s.full[st], bar,
-                                        tn * BN + rank * C::kRowsB, kk, pb);
-          ++issued;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+          unsigned char* at = s.operands + st * stage;
+          load_tile<CG, kBM, AMN>(at, &ma, &s.full[st], bar, kBM, (tm * CG + rank) * kBM, kk, pa);
+          load_tile<CG, 256 / CG, BMN>(at + kStageA, &mb, &s.full[st], bar, rowsB,
+                             tn * BN + rank * (BN / CG), kk, pb);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      // no copy outlives the CTA (a pair's are counted by the leader, which
-      // both CTAs wait for at the end)
-      if (!ok && rank == 0) {
-        for (int i = max(0, issued - S); i < issued; ++i)
-          wait_drain(&s.full[i % S], (i / S) & 1);
-      }
+    }
+    // no copy outlives the CTA (a pair's are counted by the leader, which
+    // both CTAs wait for at the end)
+    if (!ok && rank == 0) {
+      for (int i = max(0, issued - S); i < issued; ++i)
+        wait_drain(&s.full[i % S], (i / S) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = tc::idesc_bf16(CG * kBM, BN, AMN, BMN);
+    if (rank == 0) {
+      const uint32_t idesc = tc::idesc_bf16(CG * kBM, BN, AMN, BMN);
       auto commit = [](uint64_t* bar) {
-        if constexpr (CG == 2) tc::mma_commit_pair(bar);
-        else tc::mma_commit(bar);
+        if (tc::elect_one()) {
+          if constexpr (CG == 2) tc::mma_commit_pair(bar);
+          else tc::mma_commit(bar);
+        }
+        __syncwarp();
       };
+      const uint64_t da0 = tile_desc<AMN>(s.operands), db0 = tile_desc<BMN>(s.operands + kStageA);
       int st = 0, n = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -411,21 +440,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
         const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
         for (int r0 = k0; r0 < k1 && ok; r0 += p.run, ++n) {
           const int r1 = min(r0 + p.run, k1), buf = n & 1;
-          ok = wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort);
+          ok = __all_sync(0xffffffffu,
+                          wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort));
           tc::fence_after_sync();
           for (int k = r0; k < r1 && ok; ++k) {
-            ok = wait_phase(&s.full[st], ph, &s.abort);
+            ok = __all_sync(0xffffffffu, wait_phase(&s.full[st], ph, &s.abort));
             if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t da = tile_desc<AMN>(s.a[st]), db = tile_desc<BMN>(s.b[st]);
+            // (descriptors count 16-byte units)
+            const uint64_t da = da0 + st * (stage >> 4), db = db0 + st * (stage >> 4);
+            if (tc::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              const uint64_t a = da + kk * (AMN ? 128 : 2), b = db + kk * (BMN ? 128 : 2);
-              if constexpr (CG == 2)
-                tc::mma_ss_pair(tmem + buf * BN, a, b, idesc, k > r0 || kk > 0);
-              else
-                tc::mma_ss(tmem + buf * BN, a, b, idesc, k > r0 || kk > 0);
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                const uint64_t a = da + kk * (AMN ? 128 : 2), b = db + kk * (BMN ? 128 : 2);
+                if constexpr (CG == 2)
+                  tc::mma_ss_pair(tmem + buf * 256, a, b, idesc, k > r0 || kk > 0);
+                else
+                  tc::mma_ss(tmem + buf * 256, a, b, idesc, k > r0 || kk > 0);
+              }
             }
+            __syncwarp();
             commit(&s.empty[st]);
             if (++st == S) {
               st = 0;
@@ -440,98 +474,186 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     }
     // (in a pair the leader's commits arrive at the peer's barriers too: its
     // memory stays until the last of them has)
-    if (lane == 0) wait_drain(&s.drain, 0);
+    wait_drain(&s.drain, 0);
     __syncwarp();
   } else {
-    const int q = warp & 3;   // this warp's quarter of the TMEM lanes
-    constexpr int kCols = BN / 2;   // and its columns: half of the tile's
-    const int c0 = ((warp - 2) >> 2) * kCols;
+    // a quarter of the TMEM lanes and every other 32 columns
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     float* turn = s.turn[warp - 2];
-    float* kept = s.res[warp - 2] + 4 * lane;   // this lane's residual, four rows' pieces
     int n = 0;
     bool ok = true;
     for (int it = first; it < items; it += stride) {
       int tm, tn, split;
       tile_of(p, it, tm, tn, split);
       const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
-      float acc[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-      for (int r0 = k0; r0 < k1; r0 += p.run, ++n) {
-        const int buf = n & 1;
-        // one verdict for the warp: the TMEM loads below take all of its lanes
-        ok = __all_sync(0xffffffffu, wait_phase(&s.tfull[buf], (n >> 1) & 1, &s.abort));
-        if (!ok) break;
+      auto filled = [&](int i) {   // one verdict for the warp: TMEM loads take all of its lanes
+        const bool r =
+            __all_sync(0xffffffffu, wait_phase(&s.tfull[i & 1], (i >> 1) & 1, &s.abort));
         tc::fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          uint32_t r[16];
-          tc::tmem_ld16(tmem + buf * BN + c0 + c + (static_cast<uint32_t>(q * 32) << 16), r);
-          tc::tmem_ld_wait_regs(r);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] += __uint_as_float(r[i]);
-        }
+        return r;
+      };
+      auto release = [&](int i) {
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (CG == 2) tc::mbar_arrive_cluster(tc::mapa(&s.tempty[buf], 0));
-          else tc::mbar_arrive(&s.tempty[buf]);
+          if constexpr (CG == 2) tc::mbar_arrive_cluster(tc::mapa(&s.tempty[i & 1], 0));
+          else tc::mbar_arrive(&s.tempty[i & 1]);
         }
-      }
-      if (!ok) break;
-      // rows by lane -> 8 rows of four lanes at a time, 16 columns a turn; the
-      // 16-byte pieces of a row are exchanged by its number so that both
-      // directions reach all banks
-      const int64_t m0 = ((int64_t)tm * CG + rank) * kBM + q * 32;
-      const int64_t n0 = (int64_t)tn * BN + c0;
-      const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
-      const int rr = lane >> 2, cc = lane & 3;
+      };
+      if (k1 - k0 > p.run) {
+        // the runs' sums in registers; their total goes back to the last run's
+        // place in TMEM
+        float acc[4][32];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 16) {
-        const int64_t col = n0 + c + 4 * cc;
-        if (n0 + c < p.N) {
-          if (p.splits == 1 && p.e.res) {
-            float res[4][4];
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (8 * i + rr < rows) residual4(p.e, m0 + 8 * i + rr, col, p.N, res[i]);
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
+        for (int r0 = k0; r0 < k1; r0 += p.run, ++n) {
+          ok = filled(n);
+          if (!ok) break;
+          const uint32_t at = tmem + (n & 1) * 256 + lanes;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(kept + i * 128) =
-                  make_float4(res[i][0], res[i][1], res[i][2], res[i][3]);
-          }
-          __syncwarp();
+          for (int c = 0; c < 4; ++c) {
+            const int col = (2 * c + half) * 32;
+            if (col < BN) {
+              uint32_t r[32];
+              tc::tmem_ld32(at + col, r);
+              tc::tmem_ld_wait_regs(r);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(turn + lane * 16 + 4 * (i ^ ((lane >> 1) & 3))) =
-                make_float4(acc[c + 4 * i], acc[c + 4 * i + 1], acc[c + 4 * i + 2],
-                            acc[c + 4 * i + 3]);
-          __syncwarp();
-          // (rolled: unrolled copies of the epilogue would cost acc its registers)
-#pragma unroll 1
-          for (int r = rr; r < rows; r += 8) {
-            const float4 f =
-                *reinterpret_cast<const float4*>(turn + r * 16 + 4 * (cc ^ ((r >> 1) & 3)));
-            float v[4] = {f.x, f.y, f.z, f.w};
-            if (p.splits > 1) {
-              partial4(p.partial, ((int64_t)split * p.M + m0 + r) * p.N + col, col, p.N, v);
-            } else {
-              const float4 k = *reinterpret_cast<const float4*>(kept + (r >> 3) * 128);
-              const float res[4] = {k.x, k.y, k.z, k.w};
-              finish4(p.e, m0 + r, col, p.N, v, res);
+              for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
             }
           }
+          if (r0 + p.run < k1) release(n);
+        }
+        if (!ok) break;
+        --n;
+        const uint32_t at = tmem + (n & 1) * 256 + lanes;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = (2 * c + half) * 32;
+          if (col < BN) {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(acc[c][i]);
+            tc::tmem_st32(at + col, r);
+          }
+        }
+        tc::tmem_st_wait();
+      } else {
+        ok = filled(n);
+        if (!ok) break;
+      }
+      // Rows by lane become eight rows of four lanes at a time, eight columns a
+      // lane.  The 16-byte pieces of a row are exchanged by its number, so that
+      // both directions reach all banks.
+      const uint32_t at = tmem + (n & 1) * 256 + lanes;
+      const int64_t m0 = ((int64_t)tm * CG + rank) * kBM + q * 32;
+      const int64_t n0 = (int64_t)tn * BN;
+      const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
+      const int rr = lane >> 2, cc = lane & 3;
+      const bool parts = p.splits > 1;
+      void* const out = parts ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.e.out;
+      const int out_t = parts ? kF32 : p.e.out_t;
+      const int64_t out_ld = parts ? p.N : p.e.out_ld;
+      const int oe = out_t == kF32 ? 4 : 2;
+      const bool wide = parts ? (p.N & 7) == 0 : p.e.wide8;
+      const bool plain = parts || (!p.e.bias && !p.e.pre && !p.e.res && p.e.act == kActNone);
+#pragma unroll 1
+      for (int c = half * 32; c < BN; c += 64) {
+        uint32_t r[32];
+        __syncwarp();
+        tc::tmem_ld32(at + c, r);
+        tc::tmem_ld_wait_regs(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(turn + lane * 32 + 4 * (i ^ (lane & 7))) =
+              make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        __syncwarp();
+        auto sums = [&](int r, float (&v)[8]) {
+          const float4 x = *reinterpret_cast<const float4*>(turn + r * 32 + 4 * ((2 * cc) ^ (r & 7)));
+          const float4 y =
+              *reinterpret_cast<const float4*>(turn + r * 32 + 4 * ((2 * cc + 1) ^ (r & 7)));
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+          v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        };
+        const int64_t col = n0 + c + 8 * cc;
+        if (wide && col < p.N) {
+          char* o = static_cast<char*>(out) + ((m0 + rr) * out_ld + col) * oe;
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (8 * i + rr < rows) {
+                float v[8];
+                sums(8 * i + rr, v);
+                put8(o + 8 * i * out_ld * oe, out_t, v);
+              }
+            }
+          } else {
+            float bias[8], res[4][8];
+            if (p.e.bias)
+              get8(static_cast<const char*>(p.e.bias) + col * (p.e.bias_t == kF32 ? 4 : 2),
+                   p.e.bias_t, bias);
+            if (p.e.res) {   // all of them in flight before the first store
+              const int re = p.e.res_t == kF32 ? 4 : 2;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (8 * i + rr < rows)
+                  get8(static_cast<const char*>(p.e.res) +
+                           ((m0 + 8 * i + rr) * p.e.res_ld + col) * re,
+                       p.e.res_t, res[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (8 * i + rr < rows) {
+                float v[8];
+                sums(8 * i + rr, v);
+                if (p.e.bias) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[j] += bias[j];
+                }
+                if (p.e.pre)
+                  put8(static_cast<char*>(p.e.pre) +
+                           ((m0 + 8 * i + rr) * p.N + col) * (p.e.pre_t == kF32 ? 4 : 2),
+                       p.e.pre_t, v);
+                if (p.e.act != kActNone) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[j] = act_f(p.e.act, v[j]);
+                }
+                if (p.e.res) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) v[j] += res[i][j];
+                }
+                put8(o + 8 * i * out_ld * oe, out_t, v);
+              }
+            }
+          }
+        } else if (!wide && n0 + c + lane < p.N) {   // a column a lane, row by row
+          const int64_t cl = n0 + c + lane;
+          const float b = !parts && p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r) {
+            float v = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
+            if (!plain) {
+              if (p.e.pre) put1(p.e.pre, p.e.pre_t, (m0 + r) * p.N + cl, v);
+              v = act_f(p.e.act, v);
+              if (p.e.res) v += get1(p.e.res, p.e.res_t, (m0 + r) * p.e.res_ld + cl);
+            }
+            put1(out, out_t, (m0 + r) * out_ld + cl, v);
+          }
         }
       }
+      release(n);
+      ++n;
     }
   }
   __syncthreads();
   tc::fence_after_sync();
   if constexpr (CG == 2) {
     tc::cluster_sync();   // nothing of the peer's is needed or written any more
-    if (warp == 1) tc::tmem_dealloc_pair(tmem, C::kTmemCols);
+    if (warp == 1) tc::tmem_dealloc_pair(tmem, kTmemCols);
   } else {
-    if (warp == 1) tc::tmem_dealloc(tmem, C::kTmemCols);
+    if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -769,39 +891,44 @@ bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product of M x N with `steps` K steps is cut: tile width and splits.
+// How a product of M x N with `steps` K steps is cut: CTAs a tile, tile width
+// and splits of K.
 struct Plan {
   int cg, bn, splits, steps_per;
 };
-Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs) {
+// A model of its time in microseconds, over all tile widths (multiples of 32)
+// and splits.  A K step takes the tensor cores 2 BN cycles, and the shared
+// memory the time to write and read the step's tiles at 128 bytes a cycle
+// (measured: 528 cycles for 256 x 256 on a pair, 524 for 128 x 128 on one CTA).
+Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
   const int sms = row::sm_count();
   const int steps = (int)((K + kBK - 1) / kBK) * pairs;
-  // tile shapes and the time of one K step, in units of the largest tile's
-  struct Tile {
-    int cg, bn;
-    double step;
-  };
-  constexpr Tile kTiles[] = {{2, 256, 1.0}, {2, 128, 0.62}, {1, 128, 0.6}, {1, 64, 0.42}};
+  constexpr double kGhz = 1.9, kL2Gbs = 16e3, kHbmGbs = 6e3;
+  const double hbm_us = ((double)(M + N) * K * 2 * (pairs > 1 ? 3 : 1)) / kHbmGbs * 1e-3;
   Plan best = {2, 256, 1, steps};
-  double best_cost = 1e30;
-  for (const Tile& t : kTiles) {
-    const int64_t tiles = ((M + kBM * t.cg - 1) / (kBM * t.cg)) * ((N + t.bn - 1) / t.bn);
-    const double fixed = 6.0 + 8.0 * t.bn / 256;   // pipeline fill and the last epilogue
-    for (int splits = 1; splits <= 16; splits *= 2) {
-      const int per = (steps + splits - 1) / splits;
-      if (splits > 1 && per < 4) break;
-      const int64_t at_once = sms / t.cg;
-      const int64_t waves = (tiles * splits + at_once - 1) / at_once;
-      double cost = waves * per * t.step + fixed;
-      // partial sums are written, read and joined by another launch
-      if (splits > 1) cost += 12.0 + (double)M * N * (splits * 2 + 1) * 4 / 1.5e6;
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {t.cg, t.bn, splits, per};
+  double best_us = 1e30;
+  for (int cg = 1; cg <= 2; ++cg) {
+    for (int bn = 32; bn <= 256; bn += 32) {
+      if (bmn && bn % (64 * cg) != 0) continue;   // whole blocks of an MN-major B
+      const int64_t tiles = ((M + kBM * cg - 1) / (kBM * cg)) * ((N + bn - 1) / bn);
+      const double step_bytes = kStageA + stage_b(cg, bn, bmn);   // a CTA's
+      const double step = std::max(2.0 * bn, 2.0 * step_bytes / 128) * 1e-3 / kGhz;
+      for (int splits = 1; splits <= 16; ++splits) {
+        const int per = (steps + splits - 1) / splits;
+        if (splits > 1 && (per < 8 || (steps + per - 1) / per != splits)) continue;
+        const int64_t at_once = sms / cg, items = tiles * splits;
+        const int64_t waves = (items + at_once - 1) / at_once;
+        double us = std::max(waves * per * step, items * per * step_bytes * cg / kL2Gbs * 1e-3);
+        us = std::max(us, hbm_us) + 3.0 + 2.0 * bn / 256;   // fill, last epilogue
+        // partial sums are written, read and joined by another launch
+        if (splits > 1) us += 3.0 + (double)M * N * splits * 2 * 4 / 5e6;
+        if (us < best_us) {
+          best_us = us;
+          best = {cg, bn, splits, per};
+        }
       }
     }
   }
-  best.splits = (steps + best.steps_per - 1) / best.steps_per;
   return best;
 }
 size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
@@ -810,7 +937,7 @@ size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
 
 // Persistent CTAs (or pairs) of a kernel that fit the device at once, cached
 // per device; the first call also opts in to its shared memory.
-template <int CG, int BN, bool AMN, bool BMN>
+template <int CG, bool AMN, bool BMN>
 cudaError_t resident(int* n) {
   static std::atomic<int> cached[64];
   int dev = 0;
@@ -819,8 +946,8 @@ cudaError_t resident(int* n) {
   const bool known = dev >= 0 && dev < 64;
   *n = known ? cached[dev].load(std::memory_order_acquire) : 0;
   if (*n > 0) return cudaSuccess;
-  const size_t smem = sizeof(Smem<CG, BN>) + 1024;
-  auto* kernel = gemm_kernel<CG, BN, AMN, BMN>;
+  const size_t smem = sizeof(Smem) + 1024;
+  auto* kernel = gemm_kernel<CG, AMN, BMN>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   *n = row::sm_count() / CG;
@@ -844,15 +971,15 @@ cudaError_t resident(int* n) {
   return cudaSuccess;
 }
 
-template <int CG, int BN, bool AMN, bool BMN>
+template <int CG, bool AMN, bool BMN>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g,
                         cudaStream_t st) {
   int at_once = 0;
-  const cudaError_t e = resident<CG, BN, AMN, BMN>(&at_once);
+  const cudaError_t e = resident<CG, AMN, BMN>(&at_once);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
   const int grid = CG * (int)std::min<int64_t>(items, at_once);
-  gemm_kernel<CG, BN, AMN, BMN><<<grid, kThreads, sizeof(Smem<CG, BN>) + 1024, st>>>(ma, mb, g);
+  gemm_kernel<CG, AMN, BMN><<<grid, kThreads, sizeof(Smem) + 1024, st>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
@@ -860,9 +987,9 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
 int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int64_t N, int64_t K,
          const Epilogue& e, float* part, cudaStream_t st) {
   const int pairs = a.planes == 3 ? 6 : 1;
-  const Plan pl = plan_for(M, N, K, pairs);
+  const Plan pl = plan_for(M, N, K, pairs, bmn);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, pl.bn / pl.cg))
+  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, rows_b(pl.cg, pl.bn, bmn)))
     return bad(SSD_ERR_CUDA, "linear: a tensor map could not be made");
   Gemm g = {};
   g.M = M;
@@ -873,19 +1000,19 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.tiles_n = (int)((N + pl.bn - 1) / pl.bn);
   g.splits = pl.splits;
   g.steps_per_split = pl.steps_per;
+  g.bn = pl.bn;
+  g.stages = std::min(kMaxStages, kOperandBytes / (kStageA + stage_b(pl.cg, pl.bn, bmn)));
   g.group_m = 8 / pl.cg;
   g.run = e.out_t == kF32 ? kExactSteps : pl.steps_per;
   g.partial = part;
   g.e = e;
   cudaError_t err;
-#define SSD_GEMM(CG, BN)                                                      \
-  err = amn ? launch_gemm<CG, BN, true, true>(ma, mb, g, st)            \
-            : bmn ? launch_gemm<CG, BN, false, true>(ma, mb, g, st)     \
-                  : launch_gemm<CG, BN, false, false>(ma, mb, g, st)
-  if (pl.cg == 2 && pl.bn == 256) SSD_GEMM(2, 256);
-  else if (pl.cg == 2) SSD_GEMM(2, 128);
-  else if (pl.bn == 128) SSD_GEMM(1, 128);
-  else SSD_GEMM(1, 64);
+#define SSD_GEMM(CG)                                                      \
+  err = amn ? launch_gemm<CG, true, true>(ma, mb, g, st)                  \
+            : bmn ? launch_gemm<CG, false, true>(ma, mb, g, st)           \
+                  : launch_gemm<CG, false, false>(ma, mb, g, st)
+  if (pl.cg == 2) SSD_GEMM(2);
+  else SSD_GEMM(1);
 #undef SSD_GEMM
   if (err != cudaSuccess) return cuda_bad(err, "linear launch");
   if (pl.splits > 1) {
@@ -969,15 +1096,15 @@ bool wide4(const void* p, int64_t ld, size_t e) { return al(p, 4 * e) && ld % 4 
 
 size_t fwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w) {
   const int planes = dt == SSD_DTYPE_F32 ? 3 : 1;
-  size_t b = partial_bytes(plan_for(rows, N, K, planes == 3 ? 6 : 1), rows, N);
+  size_t b = partial_bytes(plan_for(rows, N, K, planes == 3 ? 6 : 1, false), rows, N);
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
   return b;
 }
 size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w, bool pack_d) {
   const int planes = dt == SSD_DTYPE_F32 ? 3 : 1, pairs = planes == 3 ? 6 : 1;
-  size_t b = std::max(partial_bytes(plan_for(rows, K, N, pairs), rows, K),
-                      partial_bytes(plan_for(N, K, rows, pairs), N, K));
+  size_t b = std::max(partial_bytes(plan_for(rows, K, N, pairs, true), rows, K),
+                      partial_bytes(plan_for(N, K, rows, pairs, true), N, K));
   b += up256((size_t)prep_parts(rows, N) * N * sizeof(float));
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
@@ -1054,6 +1181,8 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
   ep.wide = N % 4 == 0 && al(bias, 4 * e) && al(out, 4 * re) &&
             al(pre, dtype == SSD_DTYPE_BF16 ? 8 : 16) &&
             (!residual || wide4(residual, ep.res_ld, re));
+  ep.wide8 = N % 8 == 0 && al(bias, 16) && al(out, 16) && al(pre, 16) &&
+             (!residual || (al(residual, 16) && ep.res_ld % 8 == 0));
   if (skinny(x, sx, weight, rows, in_features, dtype)) {
     if (dtype == SSD_DTYPE_BF16) {
       const auto* xb = static_cast<const __nv_bfloat16*>(x);
@@ -1182,12 +1311,14 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   if (dx) {
     ep.out = dx;
     ep.wide = K % 4 == 0 && al(dx, 4 * e);
+    ep.wide8 = K % 8 == 0 && al(dx, 16);
     const int r = gemm(d, false, w, true, rows, K, N, ep, part, st);
     if (r != SSD_OK) return r;
   }
   if (dweight) {
     ep.out = dweight;
     ep.wide = K % 4 == 0 && al(dweight, 4 * e);
+    ep.wide8 = K % 8 == 0 && al(dweight, 16);
     return gemm(d, true, xo, true, N, K, rows, ep, part, st);
   }
   return SSD_OK;
