@@ -195,8 +195,10 @@ int ssd_clip_grads(const void *const *grads, const int64_t *sizes,
  * Any sizes and element-aligned pointers; bf16 operands whose rows are not all
  * 16-byte aligned (x, weight: in_features or the stride not a multiple of 8)
  * and fp32 ones are first laid out in the workspace.
- * aligned (workspace queries): nonzero if x (and for the backward dout and
- * weight) are 16-byte aligned and x_row_stride is a multiple of 8.
+ * The forward's workspace may be 0 bytes (workspace NULL): so it is where
+ * operands are read where they lie and the sums are not split.
+ * aligned (workspace queries): nonzero if x, weight (and for the backward dout)
+ * are 16-byte aligned and x_row_stride is a multiple of 8.
  * rows <= 2^30, features <= 2^24.
  *
  * Backward for the upstream gradient dout of out ([rows, out_features] dense,

@@ -13,21 +13,45 @@ capturing ``Tensor.backward`` ties the graph to autograd's own streams.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional
 
 import torch
 
 from . import _lib
-from .scan import _DT, _need, _ptr, _token_dense
+from .scan import _DT, _need, _ptr
+
+_F32 = torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_fn = {}
+
+
+def _call(name):
+    """The library's function, looked up once."""
+    f = _fn.get(name)
+    if f is None:
+        f = _fn[name] = getattr(_lib.load(), name)
+    return f
+
+
+def _chk(t, name, dtype, shape, dev) -> None:
+    """A dense tensor of this dtype, shape and device (the checks of _need in
+    one expression: a call of a few microseconds has several of them)."""
+    if not (t is not None and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
 
 
 def _stream_of(stream, dev) -> int:
     """The cudaStream_t of `stream`, or of dev's current stream."""
-    if dev.index != torch.cuda.current_device():
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    if dev.index != _current_device():
         raise ValueError(f"tensors are on {dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev.index)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -45,9 +69,10 @@ def _empty(shape, dtype, dev, stream) -> torch.Tensor:
 def _workspace(need: int, given: Optional[torch.Tensor], dev, stream):
     """(pointer, bytes, tensor that owns it) of a workspace of `need` bytes."""
     if given is None:
-        given = _empty(max(need, 256), torch.uint8, dev, stream)
-    else:
-        _need(given, "workspace", device=dev)
+        need = max(need, 256)
+        given = _empty((need,), torch.uint8, dev, stream)
+        return given.data_ptr(), need, given
+    _need(given, "workspace", device=dev)
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
@@ -74,30 +99,34 @@ def add_rmsnorm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: t
     dtype, or None (then r = scale * x, of residual_dtype, default x's);
     weight, scale [dim] fp32.  residual_out may be residual (in place).
     Returns (y, residual_out)."""
+    xd = x.dtype
     dt = _float_dtype(x, "x")
     dev, shape = x.device, x.shape
-    dim = shape[-1] if x.dim() else 0
-    _need(x, "x", device=dev)
+    dim = shape[-1] if shape else 0
     if residual is not None:
         residual_dtype = residual.dtype
+        _chk(residual, "residual", residual_dtype, shape, dev)
     elif residual_dtype is None:
-        residual_dtype = x.dtype if residual_out is None else residual_out.dtype
-    _need(residual, "residual", residual_dtype, shape, dev, optional=True)
-    _need(weight, "weight", torch.float32, (dim,), dev)
-    _need(scale, "scale", torch.float32, (dim,), dev, optional=True)
+        residual_dtype = xd if residual_out is None else residual_out.dtype
+    _chk(x, "x", xd, shape, dev)
+    _chk(weight, "weight", _F32, (dim,), dev)
+    if scale is not None:
+        _chk(scale, "scale", _F32, (dim,), dev)
     st = _stream_of(stream, dev)
     if out is None:
-        out = _empty(shape, x.dtype, dev, stream)
+        out = _empty(shape, xd, dev, stream)
     else:
-        _need(out, "out", x.dtype, shape, dev)
+        _chk(out, "out", xd, shape, dev)
     if residual_out is None:
         residual_out = _empty(shape, residual_dtype, dev, stream)
     else:
-        _need(residual_out, "residual_out", residual_dtype, shape, dev)
-    _lib.check(_lib.load().ssd_add_rmsnorm_fwd(
-        _ptr(x), _ptr(residual), _ptr(scale), _ptr(weight), float(eps),
+        _chk(residual_out, "residual_out", residual_dtype, shape, dev)
+    code = _call("ssd_add_rmsnorm_fwd")(
+        x.data_ptr(), _ptr(residual), _ptr(scale), weight.data_ptr(), eps,
         x.numel() // dim if dim else 0, dim, dt, _float_dtype(residual_out, "residual"),
-        _ptr(out), _ptr(residual_out), st))
+        out.data_ptr(), residual_out.data_ptr(), st)
+    if code:
+        _lib.check(code)
     return out, residual_out
 
 
@@ -114,25 +143,25 @@ def add_rmsnorm_bwd(dy: torch.Tensor, dresidual_out: Optional[torch.Tensor],
     dt = _float_dtype(dy, "dy")
     dev, shape = dy.device, dy.shape
     dim = shape[-1] if dy.dim() else 0
-    f32 = torch.float32
-    _need(dy, "dy", device=dev)
-    _need(residual_out, "residual_out", None, shape, dev)
+    f32 = _F32
+    _chk(dy, "dy", dy.dtype, shape, dev)
     rt = _float_dtype(residual_out, "residual_out")
-    _need(dresidual_out, "dresidual_out", residual_out.dtype, shape, dev, optional=True)
-    _need(weight, "weight", f32, (dim,), dev)
-    _need(scale, "scale", f32, (dim,), dev, optional=True)
+    _chk(residual_out, "residual_out", residual_out.dtype, shape, dev)
+    if dresidual_out is not None:
+        _chk(dresidual_out, "dresidual_out", residual_out.dtype, shape, dev)
+    _chk(weight, "weight", f32, (dim,), dev)
     if scale is not None:
-        _need(x, "x", dy.dtype, shape, dev)
+        _chk(scale, "scale", f32, (dim,), dev)
+        _chk(x, "x", dy.dtype, shape, dev)
     st = _stream_of(stream, dev)
     rows = dy.numel() // dim if dim else 0
-    lib = _lib.load()
-    ws, ws_bytes, hold = _workspace(int(lib.ssd_add_rmsnorm_bwd_workspace_bytes(rows, dim)),
+    ws, ws_bytes, hold = _workspace(_call("ssd_add_rmsnorm_bwd_workspace_bytes")(rows, dim),
                                     workspace, dev, stream)
     dx = _empty(shape, dy.dtype, dev, stream) if need_dx else None
     dres = _empty(shape, residual_out.dtype, dev, stream) if need_dresidual else None
     dw = _empty((dim,), f32, dev, stream)
     ds = None if scale is None else _empty((dim,), f32, dev, stream)
-    _lib.check(lib.ssd_add_rmsnorm_bwd(
+    _lib.check(_call("ssd_add_rmsnorm_bwd")(
         _ptr(dy), _ptr(dresidual_out), _ptr(residual_out), None if scale is None else _ptr(x),
         _ptr(scale), _ptr(weight), float(eps), rows, dim, dt, rt, _ptr(dx), _ptr(dres), _ptr(dw),
         _ptr(ds), ws, ws_bytes, st))
@@ -170,26 +199,42 @@ def add_rmsnorm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch
 
 # --- gated grouped RMSNorm ---------------------------------------------------
 
-def _rows3(t: torch.Tensor) -> torch.Tensor:
-    """[..., dim] as [batch, seqlen, dim] without a copy of dense channels."""
-    if t.dim() == 3:
-        return t
-    if t.dim() == 2:
-        return t.unsqueeze(0)
-    if t.dim() == 1:
-        return t.view(1, 1, -1) if t.is_contiguous() else t.reshape(1, 1, -1)
-    return t.view(1, -1, t.shape[-1]) if t.is_contiguous() else t.flatten(0, -3)
-
-
-def _stride3(t: Optional[torch.Tensor]) -> _lib.Stride:
-    return _lib.Stride(0, 0) if t is None else _lib.Stride(t.stride(0), t.stride(1))
-
-
-def _need_rows(t, name, dtype, shape, dev) -> None:
-    """A [..., dim] tensor whose channels are dense; other strides are free."""
-    _need(t, name, dtype, shape, dev, strided=True)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _rows(t: torch.Tensor, name: str):
+    """(batch, seqlen, strides) of a [..., channels] tensor with dense
+    channels, whose rows are batch x seqlen at two strides."""
+    shape, st = t.shape, t.stride()
+    n = len(shape)
+    if n == 0 or (shape[-1] > 1 and st[-1] != 1):
         raise ValueError(f"{name}: the channels of a token must be dense")
+    if n == 3:
+        return shape[0], shape[1], _lib.Stride(st[0], st[1])
+    if n == 2:
+        return 1, shape[0], _lib.Stride(0, st[0])
+    if n == 1:
+        return 1, 1, _lib.Stride(0, shape[0])
+    # more: the outer dimensions have to be one evenly spaced dimension
+    want = None
+    for k, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if k == 1:
+            continue
+        if want is not None and s != want:
+            raise ValueError(f"{name}: its rows must have one batch and one token stride")
+        want = (s if want is None else want) * k
+    batch = math.prod(shape[:-2])
+    inner = next((s for k, s in zip(reversed(shape[:-2]), reversed(st[:-2])) if k > 1), 0)
+    return batch, shape[-2], _lib.Stride(inner, st[-2])
+
+
+def _chk_rows(t, name, dtype, shape, dev):
+    """_rows of a tensor of this dtype, shape and device."""
+    if not (t is not None and t.dtype is dtype and t.shape == shape and t.device == dev):
+        if t is not None and t.is_cuda and t.device == dev and t.dtype is dtype:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        _need(t, name, dtype, shape, dev, strided=True)
+    return _rows(t, name)
+
+
+_NO_STRIDE = _lib.Stride(0, 0)
 
 
 def gated_rmsnorm_fwd(y: torch.Tensor, z: Optional[torch.Tensor], weight: torch.Tensor, *,
@@ -202,21 +247,25 @@ def gated_rmsnorm_fwd(y: torch.Tensor, z: Optional[torch.Tensor], weight: torch.
     dense, e.g. z a slice of the input projection; weight [dim] fp32.
     Returns a dense tensor of y's shape and dtype."""
     dt = _float_dtype(y, "y")
-    dev, shape, dim = y.device, y.shape, y.shape[-1]
-    _need_rows(y, "y", y.dtype, None, dev)
+    yd, dev, shape = y.dtype, y.device, y.shape
+    B, L, sy = _chk_rows(y, "y", yd, shape, dev)
+    dim = shape[-1]
+    sz, zp = _NO_STRIDE, None
     if z is not None:
-        _need_rows(z, "z", y.dtype, shape, dev)
-    _need(weight, "weight", torch.float32, (dim,), dev)
+        sz = _chk_rows(z, "z", yd, shape, dev)[2]
+        zp = z.data_ptr()
+    _chk(weight, "weight", _F32, (dim,), dev)
     st = _stream_of(stream, dev)
     if out is None:
-        out = _empty(shape, y.dtype, dev, stream)
+        out = _empty(shape, yd, dev, stream)
     else:
-        _need(out, "out", y.dtype, shape, dev)
-    y3, z3 = _rows3(y), None if z is None else _rows3(z)
-    _lib.check(_lib.load().ssd_gated_rmsnorm_fwd(
-        _ptr(y3), _stride3(y3), _ptr(z3), _stride3(z3), _ptr(weight), float(eps), y3.shape[0],
-        y3.shape[1], dim, dim if group_size is None else int(group_size),
-        int(bool(norm_before_gate)), dt, _ptr(out), st))
+        _chk(out, "out", yd, shape, dev)
+    code = _call("ssd_gated_rmsnorm_fwd")(
+        y.data_ptr(), sy, zp, sz, weight.data_ptr(), eps, B, L, dim,
+        dim if group_size is None else group_size, 1 if norm_before_gate else 0, dt,
+        out.data_ptr(), st)
+    if code:
+        _lib.check(code)
     return out
 
 
@@ -230,32 +279,29 @@ def gated_rmsnorm_bwd(dout: torch.Tensor, y: torch.Tensor, z: Optional[torch.Ten
     slice of the projection's gradient).  Returns dy (dense), dz (None without
     z) in y's dtype and dweight (fp32)."""
     dt = _float_dtype(y, "y")
-    dev, shape, dim = y.device, y.shape, y.shape[-1]
-    _need_rows(y, "y", y.dtype, None, dev)
-    _need(dout, "dout", y.dtype, shape, dev)
+    yd, dev, shape = y.dtype, y.device, y.shape
+    B, L, sy = _chk_rows(y, "y", yd, shape, dev)
+    dim = shape[-1]
+    _chk(dout, "dout", yd, shape, dev)
+    _chk(weight, "weight", _F32, (dim,), dev)
+    st = _stream_of(stream, dev)
+    sz = sdz = _NO_STRIDE
     if z is not None:
-        _need_rows(z, "z", y.dtype, shape, dev)
+        sz = _chk_rows(z, "z", yd, shape, dev)[2]
         if dz is None:
-            dz = _empty(shape, y.dtype, dev, stream)
-        _need_rows(dz, "dz", y.dtype, shape, dev)
+            dz = _empty(shape, yd, dev, stream)
+        sdz = _chk_rows(dz, "dz", yd, shape, dev)[2]
     elif dz is not None:
         raise ValueError("dz is given without z")
-    _need(weight, "weight", torch.float32, (dim,), dev)
-    st = _stream_of(stream, dev)
-    gs = dim if group_size is None else int(group_size)
-    y3, z3, dz3 = _rows3(y), None if z is None else _rows3(z), None if z is None else _rows3(dz)
-    if dz3 is not None and dz3.data_ptr() != dz.data_ptr():
-        raise ValueError("dz: its rows must have one batch and one token stride")
-    B, L = y3.shape[:2]
-    lib = _lib.load()
-    ws, ws_bytes, hold = _workspace(
-        int(lib.ssd_gated_rmsnorm_bwd_workspace_bytes(B, L, dim, gs)), workspace, dev, stream)
-    dy = _empty(shape, y.dtype, dev, stream)
-    dw = _empty((dim,), torch.float32, dev, stream)
-    _lib.check(lib.ssd_gated_rmsnorm_bwd(
-        _ptr(dout), _ptr(y3), _stride3(y3), _ptr(z3), _stride3(z3), _ptr(weight), float(eps), B,
-        L, dim, gs, int(bool(norm_before_gate)), dt, _ptr(dy), _ptr(dz3), _stride3(dz3), _ptr(dw),
-        ws, ws_bytes, st))
+    gs = dim if group_size is None else group_size
+    ws, ws_bytes, hold = _workspace(_call("ssd_gated_rmsnorm_bwd_workspace_bytes")(B, L, dim, gs),
+                                    workspace, dev, stream)
+    dy = _empty(shape, yd, dev, stream)
+    dw = _empty((dim,), _F32, dev, stream)
+    _lib.check(_call("ssd_gated_rmsnorm_bwd")(
+        dout.data_ptr(), y.data_ptr(), sy, _ptr(z), sz, weight.data_ptr(), eps, B, L, dim, gs,
+        1 if norm_before_gate else 0, dt, dy.data_ptr(), _ptr(dz), sdz, dw.data_ptr(), ws,
+        ws_bytes, st))
     return dict(dy=dy, dz=dz, dweight=dw)
 
 
@@ -298,27 +344,28 @@ def causal_conv1d_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         raise ValueError("activation must be None or 'silu'")
     if x.dim() != 3:
         raise ValueError("x must be [batch, seqlen, channels]")
-    Bsz, L, Cn = x.shape
-    dev = x.device
-    _need_rows(x, "x", x.dtype, None, dev)
-    _need_rows(dout, "dout", x.dtype, x.shape, dev)
+    shape, xd, dev = x.shape, x.dtype, x.device
+    Bsz, L, Cn = shape
+    sx = _chk_rows(x, "x", xd, shape, dev)[2]
+    sd = _chk_rows(dout, "dout", xd, shape, dev)[2]
     W = weight.shape[-1]
-    _need(weight, "weight", torch.float32, (Cn, W), dev)
-    _need(bias, "bias", torch.float32, (Cn,), dev, optional=True)
-    _need(seq_idx, "seq_idx", torch.int32, (Bsz, L), dev, optional=True)
+    _chk(weight, "weight", _F32, (Cn, W), dev)
+    if bias is not None:
+        _chk(bias, "bias", _F32, (Cn,), dev)
+    if seq_idx is not None:
+        _chk(seq_idx, "seq_idx", torch.int32, (Bsz, L), dev)
     st = _stream_of(stream, dev)
     if dx is None:
-        dx = _empty(x.shape, x.dtype, dev, stream)
-    _need_rows(dx, "dx", x.dtype, x.shape, dev)
-    lib = _lib.load()
+        dx = _empty(shape, xd, dev, stream)
+    so = _chk_rows(dx, "dx", xd, shape, dev)[2]
     ws, ws_bytes, hold = _workspace(
-        int(lib.ssd_causal_conv1d_bwd_workspace_bytes(Bsz, L, Cn, W)), workspace, dev, stream)
-    dw = _empty((Cn, W), torch.float32, dev, stream)
-    db = None if bias is None else _empty((Cn,), torch.float32, dev, stream)
-    _lib.check(lib.ssd_causal_conv1d_bwd(
-        _ptr(dout), _stride3(dout), _ptr(x), _stride3(x), _ptr(weight), _ptr(bias), _ptr(seq_idx),
-        Bsz, L, Cn, W, int(activation == "silu"), dt, _ptr(dx), _stride3(dx), _ptr(dw), _ptr(db),
-        ws, ws_bytes, st))
+        _call("ssd_causal_conv1d_bwd_workspace_bytes")(Bsz, L, Cn, W), workspace, dev, stream)
+    dw = _empty((Cn, W), _F32, dev, stream)
+    db = None if bias is None else _empty((Cn,), _F32, dev, stream)
+    _lib.check(_call("ssd_causal_conv1d_bwd")(
+        dout.data_ptr(), sd, x.data_ptr(), sx, weight.data_ptr(), _ptr(bias), _ptr(seq_idx), Bsz,
+        L, Cn, W, int(activation == "silu"), dt, dx.data_ptr(), so, dw.data_ptr(), _ptr(db), ws,
+        ws_bytes, st))
     return dict(dx=dx, dweight=dw, dbias=db)
 
 
@@ -334,21 +381,26 @@ def causal_conv1d_step(x: torch.Tensor, conv_state: Optional[torch.Tensor], weig
         raise ValueError("activation must be None or 'silu'")
     if x.dim() != 2:
         raise ValueError("x must be [batch, channels]")
-    Bsz, Cn = x.shape
-    dev = x.device
-    _need_rows(x, "x", x.dtype, None, dev)
+    shape, xd, dev = x.shape, x.dtype, x.device
+    Bsz, Cn = shape
+    if Cn > 1 and x.stride(1) != 1:
+        raise ValueError("x: the channels of a token must be dense")
     W = weight.shape[-1]
-    _need(weight, "weight", torch.float32, (Cn, W), dev)
-    _need(bias, "bias", torch.float32, (Cn,), dev, optional=True)
-    _need(conv_state, "conv_state", x.dtype, (Bsz, W - 1, Cn), dev, optional=W == 1)
+    _chk(weight, "weight", _F32, (Cn, W), dev)
+    if bias is not None:
+        _chk(bias, "bias", _F32, (Cn,), dev)
+    if W > 1:
+        _chk(conv_state, "conv_state", xd, (Bsz, W - 1, Cn), dev)
     st = _stream_of(stream, dev)
     if out is None:
-        out = _empty((Bsz, Cn), x.dtype, dev, stream)
+        out = _empty(shape, xd, dev, stream)
     else:
-        _need(out, "out", x.dtype, (Bsz, Cn), dev)
-    _lib.check(_lib.load().ssd_causal_conv1d_step(
-        x.data_ptr(), x.stride(0), _ptr(conv_state) if W > 1 else None, weight.data_ptr(),
-        _ptr(bias), Bsz, Cn, W, int(activation == "silu"), dt, out.data_ptr(), st))
+        _chk(out, "out", xd, shape, dev)
+    code = _call("ssd_causal_conv1d_step")(
+        x.data_ptr(), x.stride(0), conv_state.data_ptr() if W > 1 else None, weight.data_ptr(),
+        _ptr(bias), Bsz, Cn, W, 1 if activation == "silu" else 0, dt, out.data_ptr(), st)
+    if code:
+        _lib.check(code)
     return out
 
 
@@ -419,12 +471,12 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     dt = _float_dtype(x, "x")
     act = _act_code(activation)
     dev, xd = x.device, x.dtype
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
     K = x.shape[-1]
     N = weight.shape[0]
-    _need(weight, "weight", xd, (N, K), dev)
-    _need(bias, "bias", xd, (N,), dev, optional=True)
+    st = _stream_of(stream, dev)
+    _chk(weight, "weight", xd, (N, K), dev)
+    if bias is not None:
+        _chk(bias, "bias", xd, (N,), dev)
     shape = x.shape[:-1] + (N,)
     sx = _row_stride(x, "x")
     sr, rt = 0, dt
@@ -433,22 +485,23 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
             raise ValueError(f"residual must have shape {tuple(shape)} on {dev}")
         rt = _float_dtype(residual, "residual")
         sr = _row_stride(residual, "residual")
-    st = _stream_of(stream, dev)
     od = xd if residual is None else residual.dtype
     if out is None:
         out = _empty(shape, od, dev, stream)
     else:
-        _need(out, "out", od, shape, dev)
+        _chk(out, "out", od, shape, dev)
     pre = _empty(shape, _PRE[xd], dev, stream) if save_pre else None
     rows = x.numel() // K if K else 0
-    lib = _lib.load()
-    ws, ws_bytes, hold = _workspace(
-        int(lib.ssd_linear_fwd_workspace_bytes(
-            rows, K, N, dt, int(_aligned(x, sx) and weight.data_ptr() % 16 == 0))),
-        workspace, dev, stream)
-    _lib.check(lib.ssd_linear_fwd(
-        x.data_ptr(), sx, weight.data_ptr(), _ptr(bias), _ptr(residual), sr, rows, K, N, act, dt,
-        rt, out.data_ptr(), _ptr(pre), ws, ws_bytes, st))
+    xp, wp = x.data_ptr(), weight.data_ptr()
+    need = _call("ssd_linear_fwd_workspace_bytes")(
+        rows, K, N, dt, 1 if (xp | wp) % 16 == 0 and sx % 8 == 0 else 0)
+    ws, ws_bytes, hold = (None, 0, None) if need == 0 and workspace is None and rows > 0 else \
+        _workspace(need, workspace, dev, stream)
+    code = _call("ssd_linear_fwd")(
+        xp, sx, wp, _ptr(bias), _ptr(residual), sr, rows, K, N, act, dt, rt, out.data_ptr(),
+        _ptr(pre), ws, ws_bytes, st)
+    if code:
+        _lib.check(code)
     return (out, pre) if save_pre else out
 
 
@@ -467,31 +520,30 @@ def linear_bwd(dout: torch.Tensor, x: Optional[torch.Tensor], weight: Optional[t
     act = _act_code(activation)
     dev, xd = dout.device, given.dtype
     dd = _float_dtype(dout, "dout")
-    _need(dout, "dout", device=dev)
+    st = _stream_of(stream, dev)
+    _chk(dout, "dout", dout.dtype, dout.shape, dev)
     N, K = dout.shape[-1], given.shape[-1]
     rows = dout.numel() // N if N else 0
     shape = dout.shape[:-1] + (K,)
     if need_dx:
-        _need(weight, "weight", xd, (N, K), dev)
+        _chk(weight, "weight", xd, (N, K), dev)
     sx = K
     if need_dweight:
         if x is None or x.shape != shape or x.device != dev:
             raise ValueError(f"x must have shape {tuple(shape)} on {dev}")
         sx = _row_stride(x, "x")
     if activation is not None:
-        _need(pre, "pre", _PRE[xd], dout.shape, dev)
-    st = _stream_of(stream, dev)
-    lib = _lib.load()
+        _chk(pre, "pre", _PRE[xd], dout.shape, dev)
     aligned = (dout.data_ptr() % 16 == 0 and (not need_dx or weight.data_ptr() % 16 == 0)
                and (not need_dweight or _aligned(x, sx)))
     ws, ws_bytes, hold = _workspace(
-        int(lib.ssd_linear_bwd_workspace_bytes(rows, K, N, dt, int(aligned),
-                                               int(act == 0 and dd == dt))),
+        _call("ssd_linear_bwd_workspace_bytes")(rows, K, N, dt, int(aligned),
+                                                int(act == 0 and dd == dt)),
         workspace, dev, stream)
     dx = _empty(shape, xd, dev, stream) if need_dx else None
     dw = _empty((N, K), xd, dev, stream) if need_dweight else None
     db = _empty((N,), xd, dev, stream) if need_dbias else None
-    _lib.check(lib.ssd_linear_bwd(
+    _lib.check(_call("ssd_linear_bwd")(
         dout.data_ptr(), dd, x.data_ptr() if need_dweight else None, sx,
         weight.data_ptr() if need_dx else None, _ptr(pre) if act else None, rows, K, N, act, dt,
         _ptr(dx), _ptr(dw), _ptr(db), ws, ws_bytes, st))
@@ -549,20 +601,21 @@ def _storage_dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _tensor_table(tensors, name):
-    codes = []
+def _tensor_table(tensors, name, dev):
+    """Host arrays of the tensors' addresses and dtype codes."""
+    codes, ptrs = [], []
     for t in tensors:
         code = _DT.get(t.dtype)
         if code is None:
             raise ValueError(f"{name}: tensors must be float32 or bfloat16, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensors must be CUDA tensors")
-        if not _storage_dense(t):
+        if t.device != dev:
+            raise ValueError(f"{name}: a tensor is on {t.device}, expected {dev}")
+        if not (t.is_contiguous() or _storage_dense(t)):
             raise ValueError(f"{name}: tensors must be dense")
         codes.append(code)
-    n = len(tensors)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int32 * n)(*codes))
+        ptrs.append(t.data_ptr())
+    n = len(ptrs)
+    return ptrs, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int32 * n)(*codes)
 
 
 def _grad_list(grads):
@@ -570,8 +623,8 @@ def _grad_list(grads):
     if not grads:
         raise ValueError("no gradients given")
     dev = grads[0].device
-    if any(g.device != dev for g in grads):
-        raise ValueError("the gradients must be on one device")
+    if dev.type != "cuda":
+        raise ValueError("the gradients must be CUDA tensors")
     return grads, dev
 
 
@@ -580,15 +633,14 @@ def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None, stream=None) -
     (fp32 and bf16, None entries skipped; ssd_grad_norm), as a 0-d fp32
     tensor on their device."""
     grads, dev = _grad_list(grads)
-    ptrs, codes = _tensor_table(grads, "grads")
+    _, ptrs, codes = _tensor_table(grads, "grads", dev)
     n = len(grads)
     sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
     st = _stream_of(stream, dev)
-    lib = _lib.load()
-    ws, ws_bytes, hold = _workspace(int(lib.ssd_clip_grads_workspace_bytes(n)), workspace, dev,
+    ws, ws_bytes, hold = _workspace(_call("ssd_clip_grads_workspace_bytes")(n), workspace, dev,
                                     stream)
-    norm = _empty((), torch.float32, dev, stream)
-    _lib.check(lib.ssd_grad_norm(ptrs, sizes, codes, n, norm.data_ptr(), ws, ws_bytes, st))
+    norm = _empty((), _F32, dev, stream)
+    _lib.check(_call("ssd_grad_norm")(ptrs, sizes, codes, n, norm.data_ptr(), ws, ws_bytes, st))
     return norm
 
 
@@ -601,7 +653,7 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
     optimizer that keeps bf16 gradients' clipped values so).  No host
     synchronisation.  Returns the norm before clipping, 0-d fp32."""
     grads, dev = _grad_list(grads)
-    ptrs, codes = _tensor_table(grads, "grads")
+    where, ptrs, codes = _tensor_table(grads, "grads", dev)
     n = len(grads)
     outs = out_codes = None
     if out is not None:
@@ -609,20 +661,20 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors for {n} gradients")
         for o, g in zip(out, grads):
-            if o.shape != g.shape or o.device != dev or (
-                    o.stride() != g.stride()
-                    and not (o.is_contiguous() and g.is_contiguous())):
-                raise ValueError("out must match its gradient's shape, strides and device")
-        outs, out_codes = _tensor_table(out, "out")
-    written = [p for p, g in zip(outs or ptrs, grads) if g.numel()]
-    if len(set(written)) != len(written):
-        raise ValueError("a tensor to write is given twice")
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+            if o.shape != g.shape or not (o.is_contiguous() and g.is_contiguous()
+                                          or o.stride() == g.stride()):
+                raise ValueError("out must match its gradient's shape and strides")
+        where, outs, out_codes = _tensor_table(out, "out", dev)
+    counts = [g.numel() for g in grads]
+    if len(set(where)) != n:
+        written = [p for p, k in zip(where, counts) if k]
+        if len(set(written)) != len(written):
+            raise ValueError("a tensor to write is given twice")
+    sizes = (ctypes.c_int64 * n)(*counts)
     st = _stream_of(stream, dev)
-    lib = _lib.load()
-    ws, ws_bytes, hold = _workspace(int(lib.ssd_clip_grads_workspace_bytes(n)), workspace, dev,
+    ws, ws_bytes, hold = _workspace(_call("ssd_clip_grads_workspace_bytes")(n), workspace, dev,
                                     stream)
-    norm = _empty((), torch.float32, dev, stream)
-    _lib.check(lib.ssd_clip_grads(ptrs, sizes, codes, n, outs, out_codes, float(max_norm),
-                                  float(eps), norm.data_ptr(), ws, ws_bytes, st))
+    norm = _empty((), _F32, dev, stream)
+    _lib.check(_call("ssd_clip_grads")(ptrs, sizes, codes, n, outs, out_codes, max_norm, eps,
+                                       norm.data_ptr(), ws, ws_bytes, st))
     return norm

@@ -1139,9 +1139,11 @@ extern "C" {
 size_t ssd_linear_fwd_workspace_bytes(int64_t rows, int in_features, int out_features,
                                       ssd_dtype_t dtype, int aligned) {
   if (check_sizes(rows, in_features, out_features, dtype) != SSD_OK) return 0;
-  const bool pack = dtype == SSD_DTYPE_F32 || !aligned || in_features % 8 != 0;
-  // a strided x may be aligned while a weight of odd rows is not; the sum is enough for both
-  return std::max<size_t>(256, fwd_bytes(rows, in_features, out_features, dtype, pack, pack));
+  const bool odd = !aligned || in_features % 8 != 0;
+  if (!odd && rows <= (dtype == SSD_DTYPE_BF16 ? kSkinnyBf16 : kSkinnyF32)) return 0;
+  // (a strided x may be aligned while a weight of odd rows is not: the sum is enough for both)
+  const bool pack = dtype == SSD_DTYPE_F32 || odd;
+  return fwd_bytes(rows, in_features, out_features, dtype, pack, pack);
 }
 
 int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, const void* bias,
