@@ -27,7 +27,10 @@ namespace clip {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;      // elements
-constexpr int kCtasPerSm = 8;
+// CTAs an SM: reading alone wants all the loads that fit, reading and writing
+// together fewer (645M bf16 values into fp32: 634 us with 5, 776 with 8, 700
+// with 4; stores that leave the L2 first were no faster).
+constexpr int kNormCtas = 8, kScaleCtas = 5;
 constexpr int kSmall = 48, kLarge = 768;   // tensors a launch: 1.3 KB or 20.7 KB of parameters
 
 template <int N>
@@ -73,19 +76,22 @@ __device__ __forceinline__ double block_sum(double v) {
 struct SquareSum {
   float f = 0.f;    // of the current chunk
   double d = 0.0;
+  // Eight values at once.  Their fp32 sum is taken where it is neither too large
+  // nor so small that squares lost to underflow could matter to it.
   __device__ __forceinline__ void add8(const float (&v)[row::kVec]) {
-    float big = 0.f, small = 0.f;
+    float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < row::kVec; ++j) {
-      big = fmaxf(big, fabsf(v[j]));
-      small = fmaxf(small, fabsf(v[j]) < 0x1p-60f ? fabsf(v[j]) : 0.f);
-    }
-    if (big < 0x1p60f && small == 0.f) {
-#pragma unroll
-      for (int j = 0; j < row::kVec; ++j) f = fmaf(v[j], v[j], f);
+    for (int j = 0; j < row::kVec; ++j) s = fmaf(v[j], v[j], s);
+    if (s >= 0x1p-80f && s < 0x1p120f) {
+      f += s;
     } else {
+      float big = 0.f;
 #pragma unroll
-      for (int j = 0; j < row::kVec; ++j) d += (double)v[j] * (double)v[j];
+      for (int j = 0; j < row::kVec; ++j) big = fmaxf(big, fabsf(v[j]));
+      if (s != 0.f || big != 0.f) {   // (a NaN is in s)
+#pragma unroll
+        for (int j = 0; j < row::kVec; ++j) d += (double)v[j] * (double)v[j];
+      }
     }
   }
   __device__ __forceinline__ void add1(float v) { d += (double)v * (double)v; }
@@ -204,8 +210,8 @@ __global__ void __launch_bounds__(kThreads)
 
 int bad(int code, const char* msg) { return set_error(code, msg); }
 
-int grid_of(uint32_t chunks) {
-  return (int)std::min<int64_t>(chunks, (int64_t)row::sm_count() * kCtasPerSm);
+int grid_of(uint32_t chunks, int ctas_per_sm) {
+  return (int)std::min<int64_t>(chunks, (int64_t)row::sm_count() * ctas_per_sm);
 }
 
 // Fills the next launch's table from tensor `k` on; returns the tensor after
@@ -241,7 +247,7 @@ int run(const void* const* g, const int64_t* n, const int32_t* gt, int count, vo
   for (int k = 0; k < count;) {
     k = fill(t, k, count, g, n, gt, clipping ? to : nullptr, out ? ot : nullptr);
     if (t.chunks == 0) break;
-    const int grid = grid_of(t.chunks);
+    const int grid = grid_of(t.chunks, kNormCtas);
     square_sum_kernel<N><<<grid, kThreads, 0, st>>>(t, part + parts);
     parts += grid;
   }
@@ -252,7 +258,7 @@ int run(const void* const* g, const int64_t* n, const int32_t* gt, int count, vo
     for (int k = 0; k < count;) {
       k = fill(t, k, count, g, n, gt, to, out ? ot : nullptr);
       if (t.chunks == 0) break;
-      scale_kernel<N><<<grid_of(t.chunks), kThreads, 0, st>>>(t, part, parts, max_norm, eps,
+      scale_kernel<N><<<grid_of(t.chunks, kScaleCtas), kThreads, 0, st>>>(t, part, parts, max_norm, eps,
                                                               in_place, first ? norm : nullptr);
       first = false;
     }
@@ -300,7 +306,7 @@ size_t ssd_clip_grads_workspace_bytes(int count) {
   if (count < 0) return 0;
   // one double per CTA of each launch
   const size_t launches = (size_t)count / kSmall + 1;
-  return (launches * ssd::row::sm_count() * kCtasPerSm * sizeof(double) + 255) & ~(size_t)255;
+  return (launches * ssd::row::sm_count() * kNormCtas * sizeof(double) + 255) & ~(size_t)255;
 }
 
 int ssd_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int count,

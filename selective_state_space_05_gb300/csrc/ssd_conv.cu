@@ -7,7 +7,7 @@
 // Bound by HBM: x and dout are read once and dx is written once.  One thread
 // walks a range of tokens of four channels with the filter, the last W inputs
 // and the W unfinished dx in registers (rings with compile-time slots: the
-// walk is unrolled W times), the next W tokens' loads in flight; pre is
+// walk is unrolled W times); pre is
 // recomputed from the inputs, which are read anyway.  A range reads W-1 tokens
 // of its neighbours on either side.  The filter's gradient is summed over the
 // range in registers, written once per range and joined by
@@ -27,7 +27,7 @@ constexpr int kMaxW = 8;
 constexpr int kCh = 4;          // channels a thread
 constexpr int kThreads = 128;
 constexpr int kMinRange = 32;   // tokens: the halo of W-1 on either side stays small
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 5, kCtasPerSmSeq = 4;   // that registers leave room for
 
 struct Raw4 {   // one token's kCh channels as loaded
   uint4 v;
@@ -57,24 +57,47 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&v)[kCh]) {
                                             *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// Asynchronous copy of one token's kCh channels into this thread's own place in
+// shared memory (8 bytes of bf16, 16 of fp32).
+template <int BYTES>
+__device__ __forceinline__ void copy_ahead(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "n"(BYTES)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // grid (channel blocks, ranges, batch).  part: [batch * ranges][C * W + C],
-// the range's dweight, then its dbias.
-template <typename T, int W>
+// the range's dweight, then its dbias.  SEQ: with seq_idx.
+// x and dout of the next kAhead tokens are on their way through shared memory,
+// each thread copying and reading its own channels only (no barrier); with the
+// loads held in registers instead, W tokens ahead, the warps waited for them
+// (4 of 8 stalls).
+template <typename T, int W, bool SEQ>
 __global__ void __launch_bounds__(kThreads)
     conv_bwd_kernel(const T* __restrict__ x, TokStride sx, const T* __restrict__ dout,
                     TokStride sdo, const float* __restrict__ w, const float* __restrict__ bias,
                     const int32_t* __restrict__ seq_idx, int64_t L, int64_t range, int C, int silu,
                     T* __restrict__ dx, TokStride sdx, float* __restrict__ part) {
+  constexpr int kBytes = kCh * sizeof(T);
+  constexpr int kAhead = 64 / kBytes * 2;   // 16 or 8 tokens: 32 KB a CTA
+  __shared__ alignas(16) unsigned char ring[2][kAhead][kThreads][kBytes];
   const int c0 = (blockIdx.x * kThreads + threadIdx.x) * kCh;
   if (c0 >= C) return;
   const int64_t b = blockIdx.z;
   const int64_t t0 = (int64_t)blockIdx.y * range;
   const int64_t t1 = t0 + range < L ? t0 + range : L;
   const int64_t tend = t1 + W - 1 < L ? t1 + W - 1 : L;   // dx of the last tokens needs these
-  const T* xb = x + b * sx.b + c0;
-  const T* db = dout + b * sdo.b + c0;
-  T* dxb = dx + b * sdx.b + c0;
-  const int32_t* sq = seq_idx ? seq_idx + b * L : nullptr;
+  const int n = (int)(tend - t0), own = (int)(t1 - t0);
+  const T* xb = x + b * sx.b + c0 + t0 * sx.t;
+  const T* db = dout + b * sdo.b + c0 + t0 * sdo.t;
+  T* dxb = dx + b * sdx.b + c0 + (t0 - (W - 1)) * sdx.t;   // the token finished at step 0
+  const int32_t* sq = SEQ ? seq_idx + b * L + t0 : nullptr;
   float wt[W][kCh], bv[kCh], dw[W][kCh], dbv[kCh];
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
@@ -86,10 +109,21 @@ __global__ void __launch_bounds__(kThreads)
       dw[k][i] = 0.f;
     }
   }
+  const T *xp = xb, *dp = db;   // of the next token to copy
+  auto ahead = [&](int i) {     // token i of the range, if it is one
+    if (i < n) {
+      copy_ahead<kBytes>(ring[0][i % kAhead][threadIdx.x], xp);
+      copy_ahead<kBytes>(ring[1][i % kAhead][threadIdx.x], dp);
+      xp += sx.t;
+      dp += sdo.t;
+    }
+    copy_commit();
+  };
+  for (int i = 0; i < kAhead; ++i) ahead(i);
   // rings: token t0 + n W + u sits in slot u; the W-1 tokens before t0 in
   // slots 1 .. W-1
   float xr[W][kCh], dr[W][kCh];
-  int qr[W];
+  int qr[W], qn[W];   // documents of the window, and of the next W tokens
 #pragma unroll
   for (int u = 0; u < W; ++u) {
     qr[u] = 0;
@@ -98,37 +132,34 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t t = t0 - W + u;
     if (u > 0 && t >= 0) {
       Raw4 r;
-      raw4(xb + t * sx.t, r);
+      raw4(xb + (u - W) * sx.t, r);
       val4(r, (const T*)nullptr, xr[u]);
-      if (sq) qr[u] = sq[t];
+      if (SEQ) qr[u] = sq[u - W];
     }
+    if (SEQ) qn[u] = u < n ? sq[u] : 0;
   }
-  Raw4 nx[W], nd[W];   // the next W tokens as loaded
-#pragma unroll
-  for (int u = 0; u < W; ++u)
-    if (t0 + u < tend) {
-      raw4(xb + (t0 + u) * sx.t, nx[u]);
-      raw4(db + (t0 + u) * sdo.t, nd[u]);
-    }
-  for (int64_t tb = t0; tb < tend; tb += W) {
+  for (int tb = 0; tb < n; tb += W) {
 #pragma unroll
     for (int u = 0; u < W; ++u) {
-      const int64_t t = tb + u;
-      if (t < tend) {
+      const int t = tb + u;
+      if (t < n) {
+        copy_wait<kAhead - 1>();
+        Raw4 rx, rd;
+        raw4(reinterpret_cast<const T*>(ring[0][t % kAhead][threadIdx.x]), rx);
+        raw4(reinterpret_cast<const T*>(ring[1][t % kAhead][threadIdx.x]), rd);
         float g[kCh], pre[kCh];
-        val4(nx[u], (const T*)nullptr, xr[u]);
-        val4(nd[u], (const T*)nullptr, g);
-        if (t + W < tend) {
-          raw4(xb + (t + W) * sx.t, nx[u]);
-          raw4(db + (t + W) * sdo.t, nd[u]);
+        val4(rx, (const T*)nullptr, xr[u]);
+        val4(rd, (const T*)nullptr, g);
+        if (SEQ) {
+          qr[u] = qn[u];
+          qn[u] = t + W < n ? sq[t + W] : 0;
         }
-        if (sq) qr[u] = sq[t];
 #pragma unroll
         for (int i = 0; i < kCh; ++i) pre[i] = bv[i];
         bool same[W];   // lag j: token t - j is in t's document (or before the sequence, where x = 0)
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-          same[j] = qr[(u - j + W) % W] == qr[u];
+          same[j] = !SEQ || qr[(u - j + W) % W] == qr[u];
           if (same[j]) {
 #pragma unroll
             for (int i = 0; i < kCh; ++i)
@@ -139,38 +170,45 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
           for (int i = 0; i < kCh; ++i) {
             const float s = row::sigmoid_f(pre[i]);
-            g[i] *= s * (1.f + pre[i] * (1.f - s));
+            g[i] *= fmaf(s * pre[i], 1.f - s, s);
           }
         }
 #pragma unroll
         for (int i = 0; i < kCh; ++i) dr[u][i] = 0.f;
-        const bool mine = t < t1;
 #pragma unroll
         for (int j = 0; j < W; ++j) {
           if (same[j]) {
 #pragma unroll
-            for (int i = 0; i < kCh; ++i) {
+            for (int i = 0; i < kCh; ++i)
               dr[(u - j + W) % W][i] = fmaf(wt[W - 1 - j][i], g[i], dr[(u - j + W) % W][i]);
-              if (mine) dw[W - 1 - j][i] = fmaf(g[i], xr[(u - j + W) % W][i], dw[W - 1 - j][i]);
-            }
           }
         }
-        if (mine) {
+        if (t < own) {   // the tokens after the range are its neighbour's
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            if (same[j]) {
+#pragma unroll
+              for (int i = 0; i < kCh; ++i)
+                dw[W - 1 - j][i] = fmaf(g[i], xr[(u - j + W) % W][i], dw[W - 1 - j][i]);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kCh; ++i) dbv[i] += g[i];
         }
-        const int64_t s = t - (W - 1);   // finished: no later token reads it
-        if (s >= t0) put4(dxb + s * sdx.t, dr[(u + 1) % W]);
+        if (t >= W - 1) put4(dxb, dr[(u + 1) % W]);   // token t - (W-1): no later one reads it
+        dxb += sdx.t;
+        ahead(t + kAhead);   // into the place just read
       }
     }
   }
   // tokens whose readers end with the sequence
 #pragma unroll
   for (int u = 0; u < W; ++u) {
-    // the last token of slot u: the largest t < tend with (t - t0) % W == u
-    const int64_t t = t0 + u + (tend - t0 - u + W - 1) / W * W - W;
-    if (t0 + u < tend && t < t1 && t > tend - W) put4(dxb + t * sdx.t, dr[u]);
+    // the last token of slot u: the largest t < n with t % W == u
+    const int t = u + (n - u + W - 1) / W * W - W;
+    if (u < n && t < own && t > n - W) put4(dxb + (int64_t)(t - (n - (W - 1))) * sdx.t, dr[u]);
   }
+  copy_wait<0>();
   float* p = part + (b * gridDim.y + blockIdx.y) * ((int64_t)C * (W + 1));
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
@@ -215,17 +253,21 @@ __global__ void __launch_bounds__(kThreads)
 
 int channel_blocks(int C) { return (C / kCh + kThreads - 1) / kThreads; }
 
-// Tokens a range: enough ranges to give every SM kCtasPerSm CTAs, none
-// shorter than kMinRange.
-int64_t range_of(int64_t batch, int64_t seqlen, int C) {
-  const int64_t want = std::max<int64_t>(
-      1, (int64_t)row::sm_count() * kCtasPerSm / (channel_blocks(C) * batch));
+// Tokens a range: as many ranges as fill the SMs once or twice, whichever leaves
+// fewer places empty (8 x 4096 tokens x 5376 channels with documents: 285 us in
+// two rounds, 309 in one of 528 of 608 places), none shorter than kMinRange.
+int64_t range_of(int64_t batch, int64_t seqlen, int C, bool seq) {
+  const int64_t places = (int64_t)row::sm_count() * (seq ? kCtasPerSmSeq : kCtasPerSm);
+  const int64_t per = channel_blocks(C) * batch;   // CTAs of one range
+  int64_t want = std::max<int64_t>(1, places / per);
+  const int64_t twice = 2 * places / per;
+  if (twice * per > 2 * (want * per) + places / 10) want = twice;
   int64_t r = (seqlen + want - 1) / want;
   r = std::max<int64_t>(r, kMinRange);
   return std::max(r, (seqlen + 65534) / 65535);
 }
-int64_t ranges_of(int64_t batch, int64_t seqlen, int C) {
-  const int64_t r = range_of(batch, seqlen, C);
+int64_t ranges_of(int64_t batch, int64_t seqlen, int C, bool seq) {
+  const int64_t r = range_of(batch, seqlen, C, seq);
   return (seqlen + r - 1) / r;
 }
 
@@ -245,7 +287,7 @@ int check(int64_t batch, int64_t seqlen, int C, int W, ssd_dtype_t dt) {
     return bad(SSD_ERR_ARG, "batch (1..65535), seqlen and channels must be >= 1");
   if (C % 8 != 0) return bad(SSD_ERR_UNSUPPORTED, "channels must be a multiple of 8");
   if (W < 1 || W > kMaxW) return bad(SSD_ERR_UNSUPPORTED, "width must be in [1, 8]");
-  if (seqlen > (1LL << 40)) return bad(SSD_ERR_UNSUPPORTED, "seqlen too large");
+  if (seqlen >= (1LL << 31)) return bad(SSD_ERR_UNSUPPORTED, "seqlen too large");
   return SSD_OK;
 }
 
@@ -278,7 +320,9 @@ extern "C" {
 size_t ssd_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int channels,
                                              int width) {
   if (check(batch, seqlen, channels, width, SSD_DTYPE_F32) != SSD_OK) return 0;
-  const size_t n = (size_t)(batch * ranges_of(batch, seqlen, channels)) * channels * (width + 1);
+  const int64_t most = std::max(ranges_of(batch, seqlen, channels, false),
+                                ranges_of(batch, seqlen, channels, true));
+  const size_t n = (size_t)(batch * most) * channels * (width + 1);
   return (n * sizeof(float) + 255) & ~(size_t)255;
 }
 
@@ -304,7 +348,7 @@ int ssd_causal_conv1d_bwd(const void* dout, ssd_stride_t dout_stride, const void
     return bad(SSD_ERR_ARG, "dx: batch rows must not overlap");
   if (workspace_bytes < ssd_causal_conv1d_bwd_workspace_bytes(batch, seqlen, channels, width))
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
-  const int64_t range = range_of(batch, seqlen, channels);
+  const int64_t range = range_of(batch, seqlen, channels, seq_idx != nullptr);
   const int64_t ranges = (seqlen + range - 1) / range;
   const dim3 grid((unsigned)channel_blocks(channels), (unsigned)ranges, (unsigned)batch);
   float* part = static_cast<float*>(workspace);
@@ -312,7 +356,8 @@ int ssd_causal_conv1d_bwd(const void* dout, ssd_stride_t dout_stride, const void
   const TokStride sx = {x_stride.batch, x_stride.token}, sd = {dout_stride.batch, dout_stride.token},
                   so = {dx_stride.batch, dx_stride.token};
 #define SSD_CONV_BWD(T, W)                                                                     \
-  conv_bwd_kernel<T, W><<<grid, kThreads, 0, st>>>(                                            \
+  (seq_idx ? conv_bwd_kernel<T, W, true> : conv_bwd_kernel<T, W, false>)                       \
+  <<<grid, kThreads, 0, st>>>(                                                                 \
       static_cast<const T*>(x), sx, static_cast<const T*>(dout), sd, weight, bias, seq_idx,    \
       seqlen, range, channels, silu, static_cast<T*>(dx), so, part)
 #define SSD_CONV_BWD_F(W) SSD_CONV_BWD(float, W)

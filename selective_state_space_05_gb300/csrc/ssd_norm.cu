@@ -40,30 +40,36 @@ int sm_count() {
 
 namespace norm {
 
-constexpr int kFwdWarps = 32, kBwdWarps = 16;   // most warps a row
-
 using row::kVec;
 using row::load_slot;
+using row::Slot;
 using row::store_slot;
+
+constexpr int kMaxThreads = row::kRowThreads;
 
 // ---------------------------------------------------------------- add_rmsnorm
 
 template <typename T, typename R, bool VEC, int S>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kMaxThreads)
     add_fwd_kernel(const T* __restrict__ x, const R* residual, const float* __restrict__ scale,
-                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int warps,
+                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int nt,
                    T* __restrict__ y, R* rout) {
   __shared__ row::TeamSums sums;
-  const int nt = warps * 32;
-  const int team = threadIdx.x / nt, t = threadIdx.x % nt;
-  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / nt) + team;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
+  const int64_t r = (int64_t)blockIdx.x * teams + team;
   const bool live = r < rows;
-  float v[S][kVec];
-  float ss = 0.f;
+  float v[S][kVec], ss[1] = {0.f};
+  if (live) {
+    Slot<T, VEC> xs[S];
+    Slot<R, VEC> rs[S];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (live) {
-      load_slot<VEC>(x + r * dim, s, t, nt, dim, v[s]);
+    for (int s = 0; s < S; ++s) {
+      xs[s].load(x + r * dim, s, t, nt, dim);
+      if (residual) rs[s].load(residual + r * dim, s, t, nt, dim);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      xs[s].get(v[s]);
       if (scale) {
         float c[kVec];
         load_slot<VEC>(scale, s, t, nt, dim, c);
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(1024)
       }
       if (residual) {
         float q[kVec];
-        load_slot<VEC>(residual + r * dim, s, t, nt, dim, q);
+        rs[s].get(q);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) v[s][j] += q[j];
       }
@@ -80,12 +86,13 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
         v[s][j] = row::stored(v[s][j], (const R*)nullptr);
-        ss = fmaf(v[s][j], v[s][j], ss);
+        ss[0] = fmaf(v[s][j], v[s][j], ss[0]);
       }
     }
   }
-  const float rstd = rsqrtf(row::team_sum2(ss, 0.f, sums, 0, team, warps).x / (float)dim + eps);
+  row::team_sum(ss, sums, 0, team, nt);
   if (!live) return;
+  const float rstd = rsqrtf(ss[0] / (float)dim + eps);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     float w[kVec];
@@ -97,15 +104,14 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Partial sums of team q of the grid: part[q * 2 * dim + c] for dweight, and
-// dim further for dscale.
+// dim further for dscale.  All of a row's loads are in flight before its sums.
 template <typename T, typename R, bool VEC, int S>
-__global__ void __launch_bounds__(kBwdWarps * 32)
+__global__ void __launch_bounds__(kMaxThreads)
     add_bwd_kernel(const T* __restrict__ dy, const R* dres_out, const R* __restrict__ rin,
                    const T* __restrict__ x, const float* __restrict__ scale,
-                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int warps,
+                   const float* __restrict__ weight, float eps, uint32_t rows, int dim, int nt,
                    T* __restrict__ dx, R* dres, float* __restrict__ part) {
   __shared__ row::TeamSums sums;
-  const int nt = warps * 32;
   const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
   float dw[S][kVec], ds[S][kVec];
 #pragma unroll
@@ -116,46 +122,56 @@ __global__ void __launch_bounds__(kBwdWarps * 32)
   for (int64_t r0 = (int64_t)blockIdx.x * teams; r0 < rows; r0 += (int64_t)gridDim.x * teams) {
     const int64_t r = r0 + team;
     const bool live = r < rows;
-    float rv[S][kVec], g[S][kVec];
-    float c1 = 0.f, c2 = 0.f;
+    Slot<R, VEC> rs[S], dr[S];
+    Slot<T, VEC> gs[S], xs[S];
+    float c[2] = {0.f, 0.f};
+    if (live) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (live) {
-        float w[kVec];
-        load_slot<VEC>(rin + r * dim, s, t, nt, dim, rv[s]);
-        load_slot<VEC>(dy + r * dim, s, t, nt, dim, g[s]);
+      for (int s = 0; s < S; ++s) {
+        rs[s].load(rin + r * dim, s, t, nt, dim);
+        gs[s].load(dy + r * dim, s, t, nt, dim);
+        if (dres_out) dr[s].load(dres_out + r * dim, s, t, nt, dim);
+        if (scale) xs[s].load(x + r * dim, s, t, nt, dim);
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        float w[kVec], rv[kVec], g[kVec];
         load_slot<VEC>(weight, s, t, nt, dim, w);
+        rs[s].get(rv);
+        gs[s].get(g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          c1 = fmaf(rv[s][j], rv[s][j], c1);
-          c2 = fmaf(g[s][j] * w[j], rv[s][j], c2);
+          c[0] = fmaf(rv[j], rv[j], c[0]);
+          c[1] = fmaf(g[j] * w[j], rv[j], c[1]);
         }
       }
     }
-    const float2 c = row::team_sum2(c1, c2, sums, buf, team, warps);
+    row::team_sum(c, sums, buf, team, nt);
     buf ^= 1;
     if (!live) continue;
-    const float rstd = rsqrtf(c.x / (float)dim + eps);
-    const float k = rstd * rstd * (c.y / (float)dim);
+    const float rstd = rsqrtf(c[0] / (float)dim + eps);
+    const float k = rstd * rstd * (c[1] / (float)dim);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      float w[kVec], d[kVec];
+      float w[kVec], rv[kVec], g[kVec], d[kVec];
       load_slot<VEC>(weight, s, t, nt, dim, w);
+      rs[s].get(rv);
+      gs[s].get(g);
       if (dres_out) {
-        load_slot<VEC>(dres_out + r * dim, s, t, nt, dim, d);
+        dr[s].get(d);
       } else {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) d[j] = 0.f;
       }
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        dw[s][j] = fmaf(g[s][j], rv[s][j] * rstd, dw[s][j]);
-        d[j] = fmaf(rstd, fmaf(-rv[s][j], k, g[s][j] * w[j]), d[j]);
+        dw[s][j] = fmaf(g[j], rv[j] * rstd, dw[s][j]);
+        d[j] = fmaf(rstd, fmaf(-rv[j], k, g[j] * w[j]), d[j]);
       }
       if (dres) store_slot<VEC>(dres + r * dim, s, t, nt, dim, d);
       if (scale) {
         float xv[kVec], sc[kVec];
-        load_slot<VEC>(x + r * dim, s, t, nt, dim, xv);
+        xs[s].get(xv);
         load_slot<VEC>(scale, s, t, nt, dim, sc);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
@@ -176,46 +192,57 @@ __global__ void __launch_bounds__(kBwdWarps * 32)
 
 // -------------------------------------------------------------- gated_rmsnorm
 
-struct Rows {   // rows of [batch, seqlen, ...] views
+struct Rows {   // rows of [batch, seqlen, ...] views; seqlen 0: one stride (the token's) for all
   uint32_t rows, seqlen;
   TokStride y, z, dz;
 };
 __device__ __forceinline__ int64_t row_off(const TokStride& s, uint32_t r, uint32_t seqlen) {
+  if (seqlen == 0) return r * s.t;
   const uint32_t b = r / seqlen;
   return (int64_t)b * s.b + (int64_t)(r - b * seqlen) * s.t;
 }
 
-template <typename T, bool VEC, int S>
-__global__ void __launch_bounds__(1024)
+// What the gate does: nothing (no z), before the norm, after it.
+enum { kNoGate = 0, kGateFirst = 1, kNormFirst = 2 };
+
+template <typename T, bool VEC, int S, int MODE>
+__global__ void __launch_bounds__(kMaxThreads)
     gated_fwd_kernel(const T* y, const T* __restrict__ z, const float* __restrict__ weight,
-                     float eps, Rows rw, int dim, int gs, int warps, int before, T* out) {
+                     float eps, Rows rw, int dim, int gs, int nt, T* out) {
   __shared__ row::TeamSums sums;
-  const int nt = warps * 32;
-  const int team = threadIdx.x / nt, t = threadIdx.x % nt;
-  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / nt) + team;
-  const bool live = r < rw.rows;
+  const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
   const int c0 = blockIdx.y * gs;
-  float v[S][kVec], gate[S][kVec];
-  float ss = 0.f;
+  const int64_t r = (int64_t)blockIdx.x * teams + team;
+  const bool live = r < rw.rows;
+  float v[S][kVec], gate[S][kVec], ss[1] = {0.f};
+  if (live) {
+    Slot<T, VEC> ys[S], zs[S];
+    const T* yr = y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0;
+    const T* zr = MODE != kNoGate ? z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0 : nullptr;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (live) {
-      load_slot<VEC>(y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, v[s]);
-      if (z) {
-        load_slot<VEC>(z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, gate[s]);
+    for (int s = 0; s < S; ++s) {
+      ys[s].load(yr, s, t, nt, gs);
+      if (MODE != kNoGate) zs[s].load(zr, s, t, nt, gs);
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      ys[s].get(v[s]);
+      if (MODE != kNoGate) {
+        zs[s].get(gate[s]);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) gate[s][j] *= row::sigmoid_f(gate[s][j]);
-        if (!before) {
+        if (MODE == kGateFirst) {
 #pragma unroll
           for (int j = 0; j < kVec; ++j) v[s][j] *= gate[s][j];
         }
       }
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) ss = fmaf(v[s][j], v[s][j], ss);
+      for (int j = 0; j < kVec; ++j) ss[0] = fmaf(v[s][j], v[s][j], ss[0]);
     }
   }
-  const float rstd = rsqrtf(row::team_sum2(ss, 0.f, sums, 0, team, warps).x / (float)gs + eps);
+  row::team_sum(ss, sums, 0, team, nt);
   if (!live) return;
+  const float rstd = rsqrtf(ss[0] / (float)gs + eps);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     float w[kVec];
@@ -223,7 +250,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       v[s][j] = v[s][j] * rstd * w[j];
-      if (z && before) v[s][j] *= gate[s][j];
+      if (MODE == kNormFirst) v[s][j] *= gate[s][j];
     }
     store_slot<VEC>(out + r * dim + c0, s, t, nt, gs, v[s]);
   }
@@ -234,15 +261,16 @@ __global__ void __launch_bounds__(1024)
 //                dy = du e,  dz = du y e',  dw = sum dout u s
 //   norm first:  g = w dout e,  dy = s (g - y s^2 mean(g y)),
 //                dz = dout w y s e',  dw = sum dout e y s
-// Partial dweight of team q of the grid's x: part[q * dim + c].
-template <typename T, bool VEC, int S>
-__global__ void __launch_bounds__(kBwdWarps * 32)
+// Partial dweight of team q of the grid's x: part[q * dim + c].  The operands
+// stay packed and the sigmoid is taken twice: holding its fp32 values as well
+// would halve the rows in flight.
+template <typename T, bool VEC, int S, int MODE>
+__global__ void __launch_bounds__(kMaxThreads)
     gated_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ y, const T* __restrict__ z,
                      const float* __restrict__ weight, float eps, Rows rw, int dim, int gs,
-                     int warps, int before, T* __restrict__ dy, T* __restrict__ dz,
+                     int nt, T* __restrict__ dy, T* __restrict__ dz,
                      float* __restrict__ part) {
   __shared__ row::TeamSums sums;
-  const int nt = warps * 32;
   const int team = threadIdx.x / nt, t = threadIdx.x % nt, teams = blockDim.x / nt;
   const int c0 = blockIdx.y * gs;
   float dw[S][kVec];
@@ -255,57 +283,68 @@ __global__ void __launch_bounds__(kBwdWarps * 32)
        r0 += (int64_t)gridDim.x * teams) {
     const int64_t r = r0 + team;
     const bool live = r < rw.rows;
-    float yv[S][kVec], zv[S][kVec], go[S][kVec];
-    float c1 = 0.f, c2 = 0.f;
+    Slot<T, VEC> ys[S], zs[S], os[S];
+    float c[2] = {0.f, 0.f};
+    if (live) {
+      const T* yr = y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0;
+      const T* zr = MODE != kNoGate ? z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0 : nullptr;
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (live) {
-        float w[kVec];
-        load_slot<VEC>(y + row_off(rw.y, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, yv[s]);
-        load_slot<VEC>(dout + r * dim + c0, s, t, nt, gs, go[s]);
-        if (z) load_slot<VEC>(z + row_off(rw.z, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, zv[s]);
+      for (int s = 0; s < S; ++s) {
+        ys[s].load(yr, s, t, nt, gs);
+        os[s].load(dout + r * dim + c0, s, t, nt, gs);
+        if (MODE != kNoGate) zs[s].load(zr, s, t, nt, gs);
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        float w[kVec], yv[kVec], zv[kVec], go[kVec];
         load_slot<VEC>(weight + c0, s, t, nt, gs, w);
+        ys[s].get(yv);
+        os[s].get(go);
+        if (MODE != kNoGate) zs[s].get(zv);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          const float e = z ? zv[s][j] * row::sigmoid_f(zv[s][j]) : 1.f;
-          const float u = before ? yv[s][j] : yv[s][j] * e;
-          const float g = before ? go[s][j] * w[j] * e : go[s][j] * w[j];
-          c1 = fmaf(u, u, c1);
-          c2 = fmaf(g, u, c2);
+          const float e = MODE != kNoGate ? zv[j] * row::sigmoid_f(zv[j]) : 1.f;
+          const float u = MODE == kNormFirst ? yv[j] : yv[j] * e;
+          const float g = MODE == kNormFirst ? go[j] * w[j] * e : go[j] * w[j];
+          c[0] = fmaf(u, u, c[0]);
+          c[1] = fmaf(g, u, c[1]);
         }
       }
     }
-    const float2 c = row::team_sum2(c1, c2, sums, buf, team, warps);
+    row::team_sum(c, sums, buf, team, nt);
     buf ^= 1;
     if (!live) continue;
-    const float rstd = rsqrtf(c.x / (float)gs + eps);
-    const float k = rstd * rstd * (c.y / (float)gs);
+    const float rstd = rsqrtf(c[0] / (float)gs + eps);
+    const float k = rstd * rstd * (c[1] / (float)gs);
+    T* dzr = MODE != kNoGate ? dz + row_off(rw.dz, (uint32_t)r, rw.seqlen) + c0 : nullptr;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      float w[kVec], dyv[kVec], dzv[kVec];
+      float w[kVec], yv[kVec], zv[kVec], go[kVec], dyv[kVec], dzv[kVec];
       load_slot<VEC>(weight + c0, s, t, nt, gs, w);
+      ys[s].get(yv);
+      os[s].get(go);
+      if (MODE != kNoGate) zs[s].get(zv);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float sg = z ? row::sigmoid_f(zv[s][j]) : 1.f;
-        const float e = z ? zv[s][j] * sg : 1.f;
-        const float de = z ? sg * (1.f + zv[s][j] * (1.f - sg)) : 0.f;
-        const float gw = go[s][j] * w[j];
-        if (before) {
-          const float n = yv[s][j] * rstd;
-          dyv[j] = rstd * fmaf(-yv[s][j], k, gw * e);
+        const float sg = MODE != kNoGate ? row::sigmoid_f(zv[j]) : 1.f;
+        const float e = MODE != kNoGate ? zv[j] * sg : 1.f;
+        const float de = MODE != kNoGate ? fmaf(sg, 1.f - e, e) : 0.f;   // e = z sg
+        const float gw = go[j] * w[j];
+        if constexpr (MODE == kNormFirst) {
+          const float n = yv[j] * rstd;
+          dyv[j] = rstd * fmaf(-yv[j], k, gw * e);
           dzv[j] = gw * n * de;
-          dw[s][j] = fmaf(go[s][j] * e, n, dw[s][j]);
+          dw[s][j] = fmaf(go[j] * e, n, dw[s][j]);
         } else {
-          const float u = yv[s][j] * e;
+          const float u = yv[j] * e;
           const float du = rstd * fmaf(-u, k, gw);
           dyv[j] = du * e;
-          dzv[j] = du * yv[s][j] * de;
-          dw[s][j] = fmaf(go[s][j], u * rstd, dw[s][j]);
+          dzv[j] = du * yv[j] * de;
+          dw[s][j] = fmaf(go[j], u * rstd, dw[s][j]);
         }
       }
       store_slot<VEC>(dy + r * dim + c0, s, t, nt, gs, dyv);
-      if (z)
-        store_slot<VEC>(dz + row_off(rw.dz, (uint32_t)r, rw.seqlen) + c0, s, t, nt, gs, dzv);
+      if (MODE != kNoGate) store_slot<VEC>(dzr, s, t, nt, gs, dzv);
     }
   }
   float* p = part + ((int64_t)blockIdx.x * teams + team) * dim + c0;
@@ -315,40 +354,46 @@ __global__ void __launch_bounds__(kBwdWarps * 32)
 
 // ----------------------------------------------------------------- column sum
 
-constexpr int kSumRows = 8;
-
-// 32 columns a CTA, kSumRows warps that walk the rows kSumRows apart.
-__global__ void __launch_bounds__(32 * kSumRows)
+// 32 columns a CTA, ROWS warps that walk the rows ROWS apart.
+template <int ROWS>
+__global__ void __launch_bounds__(32 * ROWS)
     column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t ld, int64_t n,
                       float* __restrict__ out, int64_t n2, float* __restrict__ out2) {
-  __shared__ float acc[kSumRows][32];
+  __shared__ float acc[ROWS][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   const bool in = c < n + n2;
   if (in) {
-#pragma unroll 4
-    for (int64_t r = w; r < rows; r += kSumRows) s += part[r * ld + c];
+#pragma unroll 8
+    for (int64_t r = w; r < rows; r += ROWS) s += part[r * ld + c];
   }
   acc[w][lane] = s;
   __syncthreads();
   if (w == 0 && in) {
 #pragma unroll
-    for (int i = 1; i < kSumRows; ++i) s += acc[i][lane];
+    for (int i = 1; i < ROWS; ++i) s += acc[i][lane];
     if (c < n) out[c] = s;
     else out2[c - n] = s;
   }
 }
 
-// Teams at once in a CTA whose row takes one warp, and the CTAs of a
-// backward's grid an SM; the workspace holds one partial row a team.
-constexpr int kTeams = 4;
-constexpr int kBwdCtasPerSm = 4;
+// Slots a thread, by what a kernel holds of each (norm first: the gate too).
+constexpr int kAddFwdSlots = 4, kAddBwdSlots = 2;
+constexpr int gated_fwd_slots(ssd_dtype_t dt, bool norm_first) {
+  return dt == SSD_DTYPE_BF16 && !norm_first ? 4 : 2;
+}
+constexpr int gated_bwd_slots(ssd_dtype_t dt) { return dt == SSD_DTYPE_BF16 ? 4 : 2; }
 
-int64_t bwd_ctas(int64_t rows, const row::Shape& sh, int groups) {
+// A backward's grid holds the CTAs that its registers let run at once: more
+// would be a second, nearly empty round (2560 channels: 366 us instead of 276),
+// fewer leave loads out of flight.  Its workspace holds one partial row a team.
+constexpr int kAddWarps = 24, kGatedWarps = 32, kManySlotsWarps = 16;   // warps an SM
+int64_t bwd_ctas(int64_t rows, const row::Shape& sh, int groups, int warps_of_one_slot) {
+  const int warps = sh.slots == 1 ? warps_of_one_slot : kManySlotsWarps;
   const int64_t need = (rows + sh.teams - 1) / sh.teams;
-  const int64_t most = std::max<int64_t>(1, (int64_t)row::sm_count() * kBwdCtasPerSm / groups);
-  return std::min(need, most);
+  const int64_t per_sm = std::max(1, warps / (sh.threads() / 32));
+  return std::min(need, std::max<int64_t>(1, row::sm_count() * per_sm / groups));
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -393,6 +438,10 @@ int check_gated(int64_t batch, int64_t seqlen, int dim, int gs, float eps, ssd_d
 bool bad_stride(const ssd_stride_t& s) {
   return s.batch < 0 || s.token < 0 || s.batch > (1LL << 40) || s.token > (1LL << 40);
 }
+// all rows of [batch, seqlen] one stride apart
+bool even(const ssd_stride_t& s, int64_t batch, int64_t seqlen) {
+  return batch == 1 || s.batch == seqlen * s.token;
+}
 bool wide_stride(const ssd_stride_t& s, size_t e) {
   return (s.batch * (int64_t)e) % 16 == 0 && (s.token * (int64_t)e) % 16 == 0;
 }
@@ -401,8 +450,13 @@ bool wide_stride(const ssd_stride_t& s, size_t e) {
 
 cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
                               int64_t n2, float* out2, cudaStream_t st) {
-  norm::column_sum_kernel<<<(unsigned)((n + n2 + 31) / 32), 32 * norm::kSumRows, 0, st>>>(
-      part, rows, ld, n, out, n2, out2);
+  // many rows: more of them at once (1024 rows of 1280 columns: 22 us with 8
+  // warps, whose loads wait for one another)
+  const unsigned grid = (unsigned)((n + n2 + 31) / 32);
+  if (rows >= 128)
+    norm::column_sum_kernel<32><<<grid, 1024, 0, st>>>(part, rows, ld, n, out, n2, out2);
+  else
+    norm::column_sum_kernel<8><<<grid, 256, 0, st>>>(part, rows, ld, n, out, n2, out2);
   return cudaGetLastError();
 }
 
@@ -412,21 +466,23 @@ using namespace ssd;
 using namespace ssd::norm;
 
 // Launches the wide or one-element instance with the shape's slots.
-#define SSD_NORM_FWD(LAUNCH)       \
-  do {                             \
-    if (vec && sh.slots == 1) LAUNCH(true, 1);  \
-    else if (vec) LAUNCH(true, 2);              \
-    else if (sh.slots == 1) LAUNCH(false, 1);   \
-    else LAUNCH(false, 2);                      \
+#define SSD_NORM_SLOTS(LAUNCH, V)    \
+  switch (sh.slots) {                \
+    case 1: LAUNCH(V, 1); break;     \
+    case 2: LAUNCH(V, 2); break;     \
+    case 3: LAUNCH(V, 3); break;     \
+    default: LAUNCH(V, 4); break;    \
+  }
+#define SSD_GATED_MODE(LAUNCH, T, V, S)                      \
+  do {                                                       \
+    if (!z) LAUNCH(T, V, S, kNoGate);                        \
+    else if (norm_before_gate) LAUNCH(T, V, S, kNormFirst);  \
+    else LAUNCH(T, V, S, kGateFirst);                        \
   } while (0)
-#define SSD_NORM_BWD(LAUNCH)       \
-  do {                             \
-    if (vec && sh.slots == 1) LAUNCH(true, 1);      \
-    else if (vec && sh.slots == 2) LAUNCH(true, 2); \
-    else if (vec) LAUNCH(true, 4);                  \
-    else if (sh.slots == 1) LAUNCH(false, 1);       \
-    else if (sh.slots == 2) LAUNCH(false, 2);       \
-    else LAUNCH(false, 4);                          \
+#define SSD_NORM_PICK(LAUNCH)              \
+  do {                                     \
+    if (vec) SSD_NORM_SLOTS(LAUNCH, true)  \
+    else SSD_NORM_SLOTS(LAUNCH, false)     \
   } while (0)
 
 extern "C" {
@@ -446,27 +502,27 @@ int ssd_add_rmsnorm_fwd(const void* x, const void* residual, const float* scale,
     return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
   const bool vec = dim % kVec == 0 && row::wide(x) && row::wide(residual) && row::wide(y) &&
                    row::wide(residual_out) && row::wide(scale) && row::wide(weight);
-  const row::Shape sh = row::shape_for(dim, kFwdWarps, kTeams);
+  const row::Shape sh = row::shape_for(dim, kAddFwdSlots);
   const unsigned grid = (unsigned)((rows + sh.teams - 1) / sh.teams);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf = __nv_bfloat16;
 #define SSD_ADD_FWD(T, R, V, S)                                                              \
   add_fwd_kernel<T, R, V, S><<<grid, sh.threads(), 0, st>>>(                                 \
       static_cast<const T*>(x), static_cast<const R*>(residual), scale, weight, eps,         \
-      (uint32_t)rows, dim, sh.warps, static_cast<T*>(y), static_cast<R*>(residual_out))
+      (uint32_t)rows, dim, sh.nt, static_cast<T*>(y), static_cast<R*>(residual_out))
 #define SSD_ADD_FWD_FF(V, S) SSD_ADD_FWD(float, float, V, S)
 #define SSD_ADD_FWD_BF(V, S) SSD_ADD_FWD(bf, float, V, S)
 #define SSD_ADD_FWD_BB(V, S) SSD_ADD_FWD(bf, bf, V, S)
-  if (dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_ADD_FWD_FF);
-  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_ADD_FWD_BF);
-  else SSD_NORM_FWD(SSD_ADD_FWD_BB);
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_ADD_FWD_FF);
+  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_ADD_FWD_BF);
+  else SSD_NORM_PICK(SSD_ADD_FWD_BB);
   return launched("add_rmsnorm_fwd");
 }
 
 size_t ssd_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int dim) {
   if (check_add(rows, dim, 0.f, SSD_DTYPE_F32, SSD_DTYPE_F32) != SSD_OK) return 0;
-  const row::Shape sh = row::shape_for(dim, kBwdWarps, kTeams);
-  return up256((size_t)bwd_ctas(rows, sh, 1) * sh.teams * 2 * dim * sizeof(float));
+  const row::Shape sh = row::shape_for(dim, kAddBwdSlots);
+  return up256((size_t)bwd_ctas(rows, sh, 1, kAddWarps) * sh.teams * 2 * dim * sizeof(float));
 }
 
 int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* residual_out,
@@ -492,8 +548,8 @@ int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* r
   const bool vec = dim % kVec == 0 && row::wide(dy) && row::wide(dresidual_out) &&
                    row::wide(residual_out) && row::wide(x) && row::wide(dx) &&
                    row::wide(dresidual) && row::wide(scale) && row::wide(weight);
-  const row::Shape sh = row::shape_for(dim, kBwdWarps, kTeams);
-  const unsigned grid = (unsigned)bwd_ctas(rows, sh, 1);
+  const row::Shape sh = row::shape_for(dim, kAddBwdSlots);
+  const unsigned grid = (unsigned)bwd_ctas(rows, sh, 1, kAddWarps);
   float* part = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf = __nv_bfloat16;
@@ -501,13 +557,13 @@ int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* r
   add_bwd_kernel<T, R, V, S><<<grid, sh.threads(), 0, st>>>(                                  \
       static_cast<const T*>(dy), static_cast<const R*>(dresidual_out),                        \
       static_cast<const R*>(residual_out), static_cast<const T*>(x), scale, weight, eps,      \
-      (uint32_t)rows, dim, sh.warps, static_cast<T*>(dx), static_cast<R*>(dresidual), part)
+      (uint32_t)rows, dim, sh.nt, static_cast<T*>(dx), static_cast<R*>(dresidual), part)
 #define SSD_ADD_BWD_FF(V, S) SSD_ADD_BWD(float, float, V, S)
 #define SSD_ADD_BWD_BF(V, S) SSD_ADD_BWD(bf, float, V, S)
 #define SSD_ADD_BWD_BB(V, S) SSD_ADD_BWD(bf, bf, V, S)
-  if (dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_ADD_BWD_FF);
-  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_ADD_BWD_BF);
-  else SSD_NORM_BWD(SSD_ADD_BWD_BB);
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_ADD_BWD_FF);
+  else if (residual_dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_ADD_BWD_BF);
+  else SSD_NORM_PICK(SSD_ADD_BWD_BB);
   const int64_t prow = (int64_t)grid * sh.teams;
   launch_column_sum(part, prow, 2 * dim, dim, dweight, dscale ? dim : 0, dscale, st);
   return launched("add_rmsnorm_bwd");
@@ -528,29 +584,33 @@ int ssd_gated_rmsnorm_fwd(const void* y, ssd_stride_t y_stride, const void* z,
   const bool vec = group_size % kVec == 0 && row::wide(y) && row::wide(z) && row::wide(out) &&
                    row::wide(weight) && wide_stride(y_stride, e) &&
                    (!z || wide_stride(z_stride, e));
-  const row::Shape sh = row::shape_for(group_size, kFwdWarps, kTeams);
+  const row::Shape sh = row::shape_for(group_size, gated_fwd_slots(dtype, z && norm_before_gate));
   Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
              {z_stride.batch, z_stride.token}, {0, 0}};
+  if (even(y_stride, batch, seqlen) && (!z || even(z_stride, batch, seqlen))) rw.seqlen = 0;
   const dim3 grid((unsigned)((rw.rows + (int64_t)sh.teams - 1) / sh.teams),
                   (unsigned)(dim / group_size));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define SSD_GATED_FWD(T, V, S)                                                             \
-  gated_fwd_kernel<T, V, S><<<grid, sh.threads(), 0, st>>>(                                \
+#define SSD_GATED_FWD(T, V, S, MODE)                                                       \
+  gated_fwd_kernel<T, V, S, MODE><<<grid, sh.threads(), 0, st>>>(                          \
       static_cast<const T*>(y), static_cast<const T*>(z), weight, eps, rw, dim, group_size, \
-      sh.warps, norm_before_gate, static_cast<T*>(out))
-#define SSD_GATED_FWD_F(V, S) SSD_GATED_FWD(float, V, S)
-#define SSD_GATED_FWD_B(V, S) SSD_GATED_FWD(__nv_bfloat16, V, S)
-  if (dtype == SSD_DTYPE_F32) SSD_NORM_FWD(SSD_GATED_FWD_F);
-  else SSD_NORM_FWD(SSD_GATED_FWD_B);
+      sh.nt, static_cast<T*>(out))
+#define SSD_GATED_FWD_F(V, S) SSD_GATED_MODE(SSD_GATED_FWD, float, V, S)
+#define SSD_GATED_FWD_B(V, S) SSD_GATED_MODE(SSD_GATED_FWD, __nv_bfloat16, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_GATED_FWD_F);
+  else SSD_NORM_PICK(SSD_GATED_FWD_B);
   return launched("gated_rmsnorm_fwd");
 }
 
 size_t ssd_gated_rmsnorm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int dim,
                                              int group_size) {
   if (check_gated(batch, seqlen, dim, group_size, 0.f, SSD_DTYPE_F32) != SSD_OK) return 0;
-  const row::Shape sh = row::shape_for(group_size, kBwdWarps, kTeams);
-  return up256((size_t)bwd_ctas(batch * seqlen, sh, dim / group_size) * sh.teams * dim *
-               sizeof(float));
+  size_t most = 0;   // of the two dtypes' layouts
+  for (const ssd_dtype_t dt : {SSD_DTYPE_F32, SSD_DTYPE_BF16}) {
+    const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dt));
+    most = std::max(most, (size_t)(bwd_ctas(batch * seqlen, sh, dim / group_size, kGatedWarps) * sh.teams));
+  }
+  return up256(most * dim * sizeof(float));
 }
 
 int ssd_gated_rmsnorm_bwd(const void* dout, const void* y, ssd_stride_t y_stride, const void* z,
@@ -578,22 +638,24 @@ int ssd_gated_rmsnorm_bwd(const void* dout, const void* y, ssd_stride_t y_stride
                    row::wide(dy) && row::wide(dz) && row::wide(weight) &&
                    wide_stride(y_stride, e) &&
                    (!z || (wide_stride(z_stride, e) && wide_stride(dz_stride, e)));
-  const row::Shape sh = row::shape_for(group_size, kBwdWarps, kTeams);
+  const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dtype));
   Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
              {z_stride.batch, z_stride.token}, {dz_stride.batch, dz_stride.token}};
-  const dim3 grid((unsigned)bwd_ctas(rw.rows, sh, dim / group_size),
+  if (even(y_stride, batch, seqlen) &&
+      (!z || (even(z_stride, batch, seqlen) && even(dz_stride, batch, seqlen))))
+    rw.seqlen = 0;
+  const dim3 grid((unsigned)bwd_ctas(rw.rows, sh, dim / group_size, kGatedWarps),
                   (unsigned)(dim / group_size));
   float* part = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define SSD_GATED_BWD(T, V, S)                                                                \
-  gated_bwd_kernel<T, V, S><<<grid, sh.threads(), 0, st>>>(                                   \
+#define SSD_GATED_BWD(T, V, S, MODE)                                                          \
+  gated_bwd_kernel<T, V, S, MODE><<<grid, sh.threads(), 0, st>>>(                             \
       static_cast<const T*>(dout), static_cast<const T*>(y), static_cast<const T*>(z), weight, \
-      eps, rw, dim, group_size, sh.warps, norm_before_gate, static_cast<T*>(dy),               \
-      static_cast<T*>(dz), part)
-#define SSD_GATED_BWD_F(V, S) SSD_GATED_BWD(float, V, S)
-#define SSD_GATED_BWD_B(V, S) SSD_GATED_BWD(__nv_bfloat16, V, S)
-  if (dtype == SSD_DTYPE_F32) SSD_NORM_BWD(SSD_GATED_BWD_F);
-  else SSD_NORM_BWD(SSD_GATED_BWD_B);
+      eps, rw, dim, group_size, sh.nt, static_cast<T*>(dy), static_cast<T*>(dz), part)
+#define SSD_GATED_BWD_F(V, S) SSD_GATED_MODE(SSD_GATED_BWD, float, V, S)
+#define SSD_GATED_BWD_B(V, S) SSD_GATED_MODE(SSD_GATED_BWD, __nv_bfloat16, V, S)
+  if (dtype == SSD_DTYPE_F32) SSD_NORM_PICK(SSD_GATED_BWD_F);
+  else SSD_NORM_PICK(SSD_GATED_BWD_B);
   launch_column_sum(part, (int64_t)grid.x * sh.teams, dim, dim, dweight, 0, nullptr, st);
   return launched("gated_rmsnorm_bwd");
 }

@@ -10,9 +10,18 @@ namespace ssd {
 namespace row {
 
 constexpr int kVec = 8;   // elements per slot: one 16-byte bf16 or two fp32 vectors
-constexpr int kMaxWarps = 32;
+constexpr int kMaxWarps = 16;   // of a CTA of row teams
 
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + __expf(-v)); }
+// 1 / (1 + 2^(-v log2 e)) in four instructions: both SFU operations flush
+// subnormals, where the sigmoid is 0 or 1 to fp32 anyway (relative error of
+// each about 2^-22; with expf and a division the gated backward was bound by
+// its instructions).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
 
 __device__ __forceinline__ void unpack(uint4 w, float (&v)[kVec]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -115,50 +124,83 @@ __device__ __forceinline__ float stored(float v, const __nv_bfloat16*) {
   return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-// Sums of a and b over a team of `warps` consecutive warps (team `team` of
-// the CTA), to every thread of it.  Every thread of the CTA calls it the same
-// number of times; `buf` alternates between 0 and 1 from call to call, so
-// that one barrier a call is enough: a slow reader of one call's sums is past
-// the next call's barrier before their place is written again.
-struct TeamSums {
-  float2 part[2][kMaxWarps];
-};
-__device__ __forceinline__ float2 team_sum2(float a, float b, TeamSums& sm, int buf, int team,
-                                            int warps) {
+// A slot as it was loaded: bf16 stays packed (four registers) until its values
+// are used, so that a thread can hold several rows' operands at once.
+template <typename T, bool VEC>
+struct Slot {
+  float v[kVec];
+  __device__ __forceinline__ void load(const T* p, int s, int t, int nt, int n) {
+    load_slot<VEC>(p, s, t, nt, n, v);
+  }
+  __device__ __forceinline__ void get(float (&o)[kVec]) const {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, off);
-    b += __shfl_xor_sync(0xffffffffu, b, off);
+    for (int j = 0; j < kVec; ++j) o[j] = v[j];
   }
-  if (warps == 1) return make_float2(a, b);
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) sm.part[buf][warp] = make_float2(a, b);
+};
+template <>
+struct Slot<__nv_bfloat16, true> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int s, int t, int nt, int n) {
+    const int c = col_of<true>(s, 0, t, nt);
+    u = c < n ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&o)[kVec]) const { unpack(u, o); }
+};
+
+// Sums of K values over a team of nt consecutive threads (8, 16 or whole
+// warps; team `team` of the CTA), to every thread of it.  Every thread of the
+// CTA calls it the same number of times; `buf` alternates between 0 and 1 from
+// call to call, so that one barrier a call is enough: a slow reader of one
+// call's sums is past the next call's barrier before their place is written
+// again.
+struct TeamSums {
+  float part[2][2][kMaxWarps];
+};
+template <int K>
+__device__ __forceinline__ void team_sum(float (&a)[K], TeamSums& sm, int buf, int team, int nt) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    if (off < nt) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], off);
+    }
+  if (nt <= 32) return;
+  const int warp = threadIdx.x >> 5, warps = nt >> 5;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) sm.part[buf][k][warp] = a[k];
+  }
   __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-  for (int i = 0; i < warps; ++i) {
-    const float2 p = sm.part[buf][team * warps + i];
-    s.x += p.x;
-    s.y += p.y;
-  }
-  return s;
+#pragma unroll
+  for (int k = 0; k < K; ++k) a[k] = 0.f;
+  for (int i = 0; i < warps; ++i)
+#pragma unroll
+    for (int k = 0; k < K; ++k) a[k] += sm.part[buf][k][team * warps + i];
 }
 
-// How a row of n elements is laid over threads: `warps` warps a row with
-// `slots` slots of eight elements each, `teams` rows at once in a CTA.
-constexpr int kMaxRow = 16384;
+// How a row of n elements is laid over threads: nt threads a row (8, 16 or
+// whole warps) with `slots` slots of eight elements each, `teams` rows at once
+// in a CTA.  Among up to `most` slots a thread the fullest threads are taken,
+// and then the fewest, whose sums cost least to exchange; four slots where
+// sixteen warps need them.
+constexpr int kMaxRow = 16384, kRowThreads = 512, kTeamThreads = 256;
 struct Shape {
-  int warps, slots, teams;
-  int threads() const { return warps * teams * 32; }
+  int nt, slots, teams;
+  int threads() const { return nt * teams; }
 };
-// At most max_warps (16 or 32) warps a row: the forwards hold one row (32), the
-// backwards three and the parameters' sums (16, so that a thread may use 128
-// registers).
-inline Shape shape_for(int n, int max_warps, int teams_of_one) {
-  const int vecs = (n + kVec - 1) / kVec, cap = max_warps * 32;
-  Shape s;
-  s.slots = vecs <= cap ? 1 : vecs <= 2 * cap ? 2 : 4;   // n <= kMaxRow
-  s.warps = (vecs + 32 * s.slots - 1) / (32 * s.slots);
-  s.teams = s.warps >= teams_of_one ? 1 : teams_of_one / s.warps;
+inline Shape shape_for(int n, int most) {
+  const int vecs = (n + kVec - 1) / kVec;
+  if (vecs > kRowThreads * most) most = 4;   // n <= kMaxRow
+  Shape s = {0, 0, 0};
+  for (int k = 1; k <= most; ++k) {
+    const int need = (vecs + k - 1) / k;
+    const int nt = need <= 8 ? 8 : need <= 16 ? 16 : (need + 31) / 32 * 32;
+    if (nt <= kRowThreads && (s.nt == 0 || nt * k <= s.nt * s.slots)) {
+      s.nt = nt;
+      s.slots = k;
+    }
+  }
+  s.teams = s.nt >= kTeamThreads ? 1 : kTeamThreads / s.nt;
   return s;
 }
 
