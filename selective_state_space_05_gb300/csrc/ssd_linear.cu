@@ -185,6 +185,15 @@ __device__ __forceinline__ void get8(const void* p, int t, float (&v)[8]) {
     const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else if (t == kF16) {
+    const uint4 w = *static_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
   } else {
     row::unpack(*static_cast<const uint4*>(p), v);
   }
@@ -501,6 +510,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           else tc::mbar_arrive(&s.tempty[i & 1]);
         }
       };
+      if (p.e.res && p.splits == 1) {
+        // the residual on its way to L2 while the sums are made: a row a lane
+        const int64_t m = ((int64_t)tm * CG + rank) * kBM + q * 32 + lane;
+        if (m < p.M)
+          for (int c = half * 32; c < BN; c += 64) {
+            const int64_t n = (int64_t)tn * BN + c;
+            if (n < p.N)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                  static_cast<const char*>(p.e.res) +
+                  (m * p.e.res_ld + n) * (p.e.res_t == kF32 ? 4 : 2)));
+          }
+      }
       if (k1 - k0 > p.run) {
         // the runs' sums in registers; their total goes back to the last run's
         // place in TMEM
@@ -718,20 +739,72 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ Prep 
   if (p.colsum) p.colsum[(int64_t)blockIdx.y * p.C + c] = sum;
 }
 
+// The same with eight consecutive columns a thread (C and the strides multiples
+// of 8, 16-byte aligned): 17M fp32 values into planes take about a quarter of
+// the one-column form's time, whose 2-byte stores go to three planes.
+__global__ void __launch_bounds__(128) prep8_kernel(const __grid_constant__ Prep p) {
+  const int c = (blockIdx.x * 128 + threadIdx.x) * 8;
+  if (c >= p.C) return;
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per, r1 = min(r0 + p.rows_per, p.R);
+  const int se = p.src_t == kF32 ? 4 : 2, pe = p.pre_t == kF32 ? 4 : 2;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+#pragma unroll 2
+  for (int64_t r = r0; r < r1; ++r) {
+    float v[8];
+    get8(static_cast<const char*>(p.src) + (r * p.src_ld + c) * se, p.src_t, v);
+    if (p.pre) {
+      float q[8];
+      get8(static_cast<const char*>(p.pre) + (r * p.C + c) * pe, p.pre_t, q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= dact_f(p.act, q[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    __nv_bfloat16* o = p.out + r * p.ld + c;
+    for (int k = 0; k < p.planes; ++k) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u[j] = tc::pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        v[2 * j] -= __uint_as_float(u[j] << 16);
+        v[2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+      o += p.R * p.ld;
+    }
+  }
+  if (p.colsum) {
+    float4* q = reinterpret_cast<float4*>(p.colsum + (int64_t)blockIdx.y * p.C + c);
+    q[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    q[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+  }
+}
+
 // out[c] = sum over r of part[r][c], rounded once to out's type.
 __global__ void __launch_bounds__(256)
     sum_rows_kernel(const float* __restrict__ part, int rows, int C, void* out, int out_t) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= C) return;
+  __shared__ float acc[8][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) s += part[(int64_t)r * C + c];
-  put1(out, out_t, c, s);
+  if (c < C) {
+#pragma unroll 8
+    for (int r = w; r < rows; r += 8) s += part[(int64_t)r * C + c];
+  }
+  acc[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < C) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += acc[i][lane];
+    put1(out, out_t, c, s);
+  }
 }
 
 // ------------------------------------------------------------------- few rows
 
-constexpr int kSkinnyThreads = 256, kSkinnyWarps = 8;
+constexpr int kSkinnyThreads = 256, kSkinnyWarps = 8;   // (16 warps for few rows of W)
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -746,12 +819,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // in turn.  Each lane loads 16 consecutive bytes of a row: the MMA's K index
 // is permuted within the step, alike for W and x, which leaves the sum as it
 // is.  K a multiple of 8, rows 16-byte aligned.
-template <int NT>
-__global__ void __launch_bounds__(kSkinnyThreads)
+template <int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32)
     skinny_bf16_kernel(const __nv_bfloat16* __restrict__ x, int64_t sx,
                        const __nv_bfloat16* __restrict__ w, int M, int64_t N, int K,
                        const __grid_constant__ Epilogue e) {
-  __shared__ float acc[kSkinnyWarps][16][NT * 8 + 1];
+  __shared__ float acc[WARPS][16][NT * 8 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
   const bool lo = n0 + g < N, hi = n0 + g + 8 < N;
@@ -764,7 +837,7 @@ __global__ void __launch_bounds__(kSkinnyThreads)
     for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-  for (int k = (warp * 4 + t) * 8; k < K + t * 8; k += kSkinnyWarps * 32) {   // uniform trip count
+  for (int k = (warp * 4 + t) * 8; k < K + t * 8; k += WARPS * 32) {   // uniform trip count
     const bool in = k < K;
     const uint4 a = in && lo ? *reinterpret_cast<const uint4*>(w0 + k) : zero;
     const uint4 b = in && hi ? *reinterpret_cast<const uint4*>(w1 + k) : zero;
@@ -784,64 +857,77 @@ __global__ void __launch_bounds__(kSkinnyThreads)
     acc[warp][g + 8][i * 8 + 2 * t + 1] = d[i][3];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < NT * 8 * 4; i += kSkinnyThreads) {
+  for (int i = threadIdx.x; i < NT * 8 * 4; i += WARPS * 32) {
     const int m = i >> 2, c = (i & 3) * 4;
     if (m >= M) continue;
     float v[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
     residual4(e, m, n0 + c, N, res);
 #pragma unroll
-    for (int q = 0; q < kSkinnyWarps; ++q)
+    for (int q = 0; q < WARPS; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += acc[q][c + j][m];
     finish4(e, m, n0 + c, N, v, res);
   }
 }
 
-// fp32: a warp takes four rows of W against up to 8 tokens.  K a multiple of
-// 4, rows 16-byte aligned.
+// fp32: a CTA takes four rows of W against up to 8 tokens, its warps steps of
+// 128 of K in turn (so that x is read once a CTA).  The 32 sums are folded over
+// the lanes: each halving keeps half of them in either half of the lanes, and
+// lane m * 4 + j ends up with token m, row j.  K a multiple of 4, rows 16-byte
+// aligned.
 constexpr int kF32Rows = 4;
 __global__ void __launch_bounds__(kSkinnyThreads)
     skinny_f32_kernel(const float* __restrict__ x, int64_t sx, const float* __restrict__ w, int M,
                       int64_t N, int K, const __grid_constant__ Epilogue e) {
+  __shared__ float part[kSkinnyWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t n0 = ((int64_t)blockIdx.x * kSkinnyWarps + warp) * kF32Rows;
-  if (n0 >= N) return;
-  float acc[8][kF32Rows];
+  const int64_t n0 = (int64_t)blockIdx.x * kF32Rows;
+  float acc[32];
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int j = 0; j < kF32Rows; ++j) acc[m][j] = 0.f;
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int k = lane * 4; k < K; k += 128) {
-    float4 wv[kF32Rows];
+  for (int k = (warp * 32 + lane) * 4; k < K; k += kSkinnyWarps * 128) {
+    float4 wv[kF32Rows], xv[8];
 #pragma unroll
     for (int j = 0; j < kF32Rows; ++j)
       wv[j] = n0 + j < N ? *reinterpret_cast<const float4*>(w + (n0 + j) * K + k) : zero;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      if (m < M) {
-        const float4 xv = *reinterpret_cast<const float4*>(x + m * sx + k);
+    for (int m = 0; m < 8; ++m)
+      xv[m] = m < M ? *reinterpret_cast<const float4*>(x + m * sx + k) : zero;
 #pragma unroll
-        for (int j = 0; j < kF32Rows; ++j)
-          acc[m][j] = fmaf(xv.x, wv[j].x, fmaf(xv.y, wv[j].y, fmaf(xv.z, wv[j].z, fmaf(xv.w, wv[j].w, acc[m][j]))));
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int j = 0; j < kF32Rows; ++j) {
+        float& a = acc[m * 4 + j];
+        a = fmaf(xv[m].x, wv[j].x, a);
+        a = fmaf(xv[m].y, wv[j].y, a);
+        a = fmaf(xv[m].z, wv[j].z, a);
+        a = fmaf(xv[m].w, wv[j].w, a);
       }
-    }
   }
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    if (m >= M) break;
+  for (int off = 16; off > 0; off >>= 1) {
+    const bool up = lane & off;
 #pragma unroll
-    for (int j = 0; j < kF32Rows; ++j)
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1)
-        acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], off);
-    if (lane == 0) {
-      float res[4];
-      residual4(e, m, n0, N, res);
-      finish4(e, m, n0, N, acc[m], res);
+    for (int i = 0; i < off; ++i) {
+      const float keep = up ? acc[i + off] : acc[i], give = up ? acc[i] : acc[i + off];
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
     }
   }
+  part[warp][lane] = acc[0];
+  __syncthreads();
+  if (warp > 0) return;
+  float v = 0.f;
+#pragma unroll
+  for (int q = 0; q < kSkinnyWarps; ++q) v += part[q][lane];
+  const int m = lane >> 2;
+  const int64_t n = n0 + (lane & 3);
+  if (m >= M || n >= N) return;
+  if (e.bias) v += get1(e.bias, e.bias_t, n);
+  if (e.pre) put1(e.pre, e.pre_t, m * N + n, v);
+  v = act_f(e.act, v);
+  if (e.res) v += get1(e.res, e.res_t, m * e.res_ld + n);
+  put1(e.out, e.out_t, m * e.out_ld + n, v);
 }
 
 // ------------------------------------------------------------------- host side
@@ -881,9 +967,15 @@ struct Operand {
 bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.planes};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2,
-                                 (cuuint64_t)(o.planes > 1 ? o.rows * o.ld * 2 : o.ld * 2)};
+  // Loads from a map of less than 128 KB are slower (M = 17, K = 2560, N = 10576:
+  // 31 us instead of 24), so a small operand's map is given a second plane past
+  // that size, which no load's coordinates reach.
+  const bool small = o.planes == 1 && o.rows * o.ld * 2 < 131072;
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows,
+                              (cuuint64_t)(small ? 2 : o.planes)};
+  const cuuint64_t strides[2] = {
+      (cuuint64_t)o.ld * 2,
+      (cuuint64_t)(small ? 131072 : o.planes > 1 ? o.rows * o.ld * 2 : o.ld * 2)};
   const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? kBK : tile_rows), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, es,
@@ -921,7 +1013,7 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
         double us = std::max(waves * per * step, items * per * step_bytes * cg / kL2Gbs * 1e-3);
         us = std::max(us, hbm_us) + 3.0 + 2.0 * bn / 256;   // fill, last epilogue
         // partial sums are written, read and joined by another launch
-        if (splits > 1) us += 3.0 + (double)M * N * splits * 2 * 4 / 5e6;
+        if (splits > 1) us += 6.0 + (double)M * N * splits * 2 * 4 / 5e6;
         if (us < best_us) {
           best_us = us;
           best = {cg, bn, splits, per};
@@ -1027,11 +1119,12 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
 int type_of(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? kBf16 : kF32; }
 size_t esize(ssd_dtype_t t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
 
-// Rows of a column-sum / plane pass a CTA; bounded by the grid's y limit.
+// Rows of a plane / column-sum pass a CTA: about eight CTAs of 128 threads an
+// SM; bounded by the grid's y limit.
 int64_t prep_rows_per(int64_t R, int C) {
-  const int64_t cols = (C + 255) / 256;
+  const int64_t cols = (C + 1023) / 1024;
   const int64_t want = std::max<int64_t>(1, (int64_t)row::sm_count() * 8 / cols);
-  return std::max<int64_t>(std::max<int64_t>(8, (R + want - 1) / want), (R + 65534) / 65535);
+  return std::max<int64_t>(std::max<int64_t>(4, (R + want - 1) / want), (R + 65534) / 65535);
 }
 int64_t prep_parts(int64_t R, int C) {
   const int64_t per = prep_rows_per(R, C);
@@ -1059,8 +1152,11 @@ cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const
   p.pre_t = (uint8_t)pre_t;
   p.act = (uint8_t)act;
   p.planes = (uint8_t)planes;
-  const dim3 grid((unsigned)((C + 255) / 256), (unsigned)prep_parts(R, C));
-  prep_kernel<<<grid, 256, 0, st>>>(p);
+  const unsigned parts = (unsigned)prep_parts(R, C);
+  if (C % 8 == 0 && ld % 8 == 0 && al(src, 16) && al(pre, 16))
+    prep8_kernel<<<dim3((unsigned)((C + 1023) / 1024), parts), 128, 0, st>>>(p);
+  else
+    prep_kernel<<<dim3((unsigned)((C + 255) / 256), parts), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -1082,13 +1178,18 @@ bool in_place(const void* p, int64_t ld, ssd_dtype_t dt) {
   return dt == SSD_DTYPE_BF16 && al(p, 16) && ld % 8 == 0 && ld < (1LL << 38);
 }
 
-// rows up to which the weight is streamed through registers
-constexpr int kSkinnyBf16 = 16, kSkinnyF32 = 8;
+// Rows for which the weight is streamed through registers.  Every CTA reads all
+// of x, so beyond 8 rows x has to be small (64 KB).
+constexpr int kSkinnyBf16 = 32, kSkinnyF32 = 8;
+bool few_rows(int64_t rows, int K, ssd_dtype_t dt) {
+  if (dt == SSD_DTYPE_F32) return rows <= kSkinnyF32;
+  return rows <= 8 || (rows <= kSkinnyBf16 && rows * K <= 32768);
+}
 
 bool skinny(const void* x, int64_t sx, const void* w, int64_t rows, int K, ssd_dtype_t dt) {
-  if (dt == SSD_DTYPE_BF16)
-    return rows <= kSkinnyBf16 && K % 8 == 0 && al(x, 16) && al(w, 16) && (rows == 1 || sx % 8 == 0);
-  return rows <= kSkinnyF32 && K % 4 == 0 && al(x, 16) && al(w, 16) && (rows == 1 || sx % 4 == 0);
+  const int unit = dt == SSD_DTYPE_BF16 ? 8 : 4;   // elements of a 16-byte load
+  return few_rows(rows, K, dt) && K % unit == 0 && al(x, 16) && al(w, 16) &&
+         (rows == 1 || sx % unit == 0);
 }
 
 // every row of a tensor starts on a multiple of four elements
@@ -1140,7 +1241,7 @@ size_t ssd_linear_fwd_workspace_bytes(int64_t rows, int in_features, int out_fea
                                       ssd_dtype_t dtype, int aligned) {
   if (check_sizes(rows, in_features, out_features, dtype) != SSD_OK) return 0;
   const bool odd = !aligned || in_features % 8 != 0;
-  if (!odd && rows <= (dtype == SSD_DTYPE_BF16 ? kSkinnyBf16 : kSkinnyF32)) return 0;
+  if (!odd && few_rows(rows, in_features, dtype)) return 0;
   // (a strided x may be aligned while a weight of odd rows is not: the sum is enough for both)
   const bool pack = dtype == SSD_DTYPE_F32 || odd;
   return fwd_bytes(rows, in_features, out_features, dtype, pack, pack);
@@ -1190,14 +1291,23 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
       const auto* xb = static_cast<const __nv_bfloat16*>(x);
       const auto* wb = static_cast<const __nv_bfloat16*>(weight);
       const unsigned grid = (unsigned)((N + 15) / 16);
-      if (rows <= 8)
-        skinny_bf16_kernel<1><<<grid, kSkinnyThreads, 0, st>>>(xb, sx, wb, (int)rows, N,
-                                                               in_features, ep);
-      else
-        skinny_bf16_kernel<2><<<grid, kSkinnyThreads, 0, st>>>(xb, sx, wb, (int)rows, N,
-                                                               in_features, ep);
+      // one CTA an SM or fewer: twice the warps, for the loads in flight
+      const bool few = N < 16 * 2 * (int64_t)row::sm_count();
+#define SSD_SKINNY(NT)                                                                          \
+  if (few)                                                                                      \
+    skinny_bf16_kernel<NT, 16><<<grid, 512, 0, st>>>(xb, sx, wb, (int)rows, N, in_features, ep); \
+  else                                                                                          \
+    skinny_bf16_kernel<NT, 8><<<grid, 256, 0, st>>>(xb, sx, wb, (int)rows, N, in_features, ep)
+      if (rows <= 8) {
+        SSD_SKINNY(1);
+      } else if (rows <= 16) {
+        SSD_SKINNY(2);
+      } else {
+        SSD_SKINNY(4);
+      }
+#undef SSD_SKINNY
     } else {
-      const unsigned grid = (unsigned)((N + kSkinnyWarps * kF32Rows - 1) / (kSkinnyWarps * kF32Rows));
+      const unsigned grid = (unsigned)((N + kF32Rows - 1) / kF32Rows);
       skinny_f32_kernel<<<grid, kSkinnyThreads, 0, st>>>(static_cast<const float*>(x), sx,
                                                          static_cast<const float*>(weight),
                                                          (int)rows, N, in_features, ep);
@@ -1286,7 +1396,7 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
       ws += planes_bytes(rows, N, planes);
     }
     if (dbias) {
-      sum_rows_kernel<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(
+      sum_rows_kernel<<<(unsigned)((N + 31) / 32), 256, 0, st>>>(
           colsum, (int)prep_parts(rows, out_features), out_features, dbias, type_of(dtype));
       const cudaError_t err2 = cudaGetLastError();
       if (err2 != cudaSuccess) return cuda_bad(err2, "linear dbias launch");
