@@ -97,6 +97,43 @@ def test_linear(case):
     _check(M, K, N, dt, act, x, w, b, r, do, out, pre, got)
 
 
+# rows, in, out that the product kernel cuts differently: single CTAs and pairs,
+# tiles 32 to 256 wide, one to sixteen splits of K, several rounds of tiles,
+# sums in one run and in several (an fp32 residual keeps the sum exact)
+TILES = [(700, 512, 1500), (2500, 640, 700), (3000, 4096, 520), (260, 8192, 264),
+         (513, 2048, 1032), (100, 2100, 4200), (5000, 136, 5000), (40, 24000, 40),
+         (1999, 1000, 3001)]
+
+
+@pytest.mark.parametrize("rt", [None, F32])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("shape", TILES, ids=str)
+def test_tiles(shape, dt, rt):
+    import selective_state_space_05_gb300 as ssd
+    M, K, N = shape
+    g = torch.Generator("cuda").manual_seed(M + K + N)
+
+    def r(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    x, w, b = r(M, K).to(dt), (r(N, K) * K ** -0.5).to(dt), r(N).to(dt)
+    res = None if rt is None else r(M, N)
+    do = r(M, N).to(rt or dt)
+    out = ssd.linear_fwd(x, w, b, residual=res)
+    got = ssd.linear_bwd(do, x, w, need_dbias=True)
+    ssd.scan_status()
+    X, W, D = x.double(), w.double(), do.double()
+    ref, mag = X @ W.t() + b.double(), X.abs() @ W.abs().t() + b.double().abs()
+    if res is not None:
+        ref, mag = ref + res.double(), mag + res.double().abs()
+    bt.assert_within(out, ref.cpu(), mag.cpu(), _ops(K), "out")
+    # an fp32 upstream gradient is rounded to bf16 for the two products
+    e = 2.0 ** -8 if dt == BF and do.dtype == F32 else 0.0
+    for k, v, m, n in (("dx", D @ W, D.abs() @ W.abs(), N), ("dweight", D.t() @ X,
+                                                             D.abs().t() @ X.abs(), M)):
+        bt.assert_within(got[k], v.cpu(), m.cpu(), _ops(n), k, e * m.cpu())
+    bt.assert_within(got["dbias"], D.sum(0).cpu(), D.abs().sum(0).cpu(), M + 64, "dbias")
+
+
 @pytest.mark.parametrize("case", [(40, 64, 72, BF, True, None, F32), (5, 64, 72, BF, True, None, BF),
                                   (40, 64, 72, F32, False, None, F32), (5, 40, 9, F32, True, None, F32)],
                          ids=str)
