@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 // stay packed and the sigmoid is taken twice: holding its fp32 values as well
 // would halve the rows in flight.
 template <typename T, bool VEC, int S, int MODE>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1)   // (one slot: 64 registers)
     gated_bwd_kernel(const T* __restrict__ dout, const T* __restrict__ y, const T* __restrict__ z,
                      const float* __restrict__ weight, float eps, Rows rw, int dim, int gs,
                      int nt, T* __restrict__ dy, T* __restrict__ dz,
