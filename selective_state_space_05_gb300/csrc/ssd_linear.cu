@@ -582,6 +582,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       const bool plain = parts || (!p.e.bias && !p.e.pre && !p.e.res && p.e.act == kActNone);
 #pragma unroll 1
       for (int c = half * 32; c < BN; c += 64) {
+        const int64_t col = n0 + c + 8 * cc;
+        const bool in = wide && col < p.N;
+        // the residual first: its loads are in flight during the TMEM load, all
+        // of them before the first store
+        float res[4][8];
+        if (!plain && in && p.e.res) {
+          const int re = p.e.res_t == kF32 ? 4 : 2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (8 * i + rr < rows)
+              get8(static_cast<const char*>(p.e.res) + ((m0 + 8 * i + rr) * p.e.res_ld + col) * re,
+                   p.e.res_t, res[i]);
+        }
         uint32_t r[32];
         __syncwarp();
         tc::tmem_ld32(at + c, r);
@@ -598,32 +611,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
           v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
         };
-        const int64_t col = n0 + c + 8 * cc;
-        if (wide && col < p.N) {
+        if (in) {
           char* o = static_cast<char*>(out) + ((m0 + rr) * out_ld + col) * oe;
-          if (plain) {
+          const int64_t step = 8 * out_ld * oe;
+          if (plain) {   // all of the sums read, then all stored
+            float v[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (8 * i + rr < rows) {
-                float v[8];
-                sums(8 * i + rr, v);
-                put8(o + 8 * i * out_ld * oe, out_t, v);
-              }
+            for (int i = 0; i < 4; ++i) sums(8 * i + rr, v[i]);
+            if (out_t == kF32) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (8 * i + rr < rows) put8(o + i * step, kF32, v[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (8 * i + rr < rows) put8(o + i * step, kBf16, v[i]);
             }
           } else {
-            float bias[8], res[4][8];
+            float bias[8];
             if (p.e.bias)
               get8(static_cast<const char*>(p.e.bias) + col * (p.e.bias_t == kF32 ? 4 : 2),
                    p.e.bias_t, bias);
-            if (p.e.res) {   // all of them in flight before the first store
-              const int re = p.e.res_t == kF32 ? 4 : 2;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (8 * i + rr < rows)
-                  get8(static_cast<const char*>(p.e.res) +
-                           ((m0 + 8 * i + rr) * p.e.res_ld + col) * re,
-                       p.e.res_t, res[i]);
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (8 * i + rr < rows) {
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] += res[i][j];
                 }
-                put8(o + 8 * i * out_ld * oe, out_t, v);
+                put8(o + i * step, out_t, v);
               }
             }
           }
