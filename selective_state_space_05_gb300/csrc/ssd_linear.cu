@@ -20,9 +20,10 @@
 // thread issues the TMA loads, one the MMAs, and eight warps take finished
 // accumulators out of TMEM (two, so that the next MMAs run meanwhile) into
 // registers, turn them through shared memory so that rows are written in whole
-// sectors, and apply bias, activation and residual on the way.  Where there are few
-// tiles, K is split over CTAs: each writes its partial sums in fp32 and a
-// second kernel adds them in a fixed order and applies the same epilogue.
+// sectors, and apply bias, activation and residual on the way.  Tiles that would
+// fill the SMs only partly are split along K over them: each split writes its
+// partial sums in fp32 and a second kernel adds them in a fixed order and applies
+// the same epilogue.
 //
 // A few rows (decoding) are bound by the weight's bytes: skinny_kernel streams
 // W through registers once, all of its loads in flight, with mma.sync for bf16
@@ -223,12 +224,14 @@ struct Gemm {
   int64_t M, N;
   int kblocks;        // K in steps of kBK
   int pairs;          // products of planes: 1, or 6 for fp32
-  int tiles_m, tiles_n, splits, steps_per_split;
+  int tiles_m, tiles_n;
+  int full;           // tiles [0, full) are computed whole, the others ("the tail") in
+  int splits, steps_per_split;   // splits of K each, joined afterwards where splits > 1
   int bn;             // tile width, a multiple of 32 up to 256
   int stages;         // operand tiles in flight
   int group_m;        // tiles of M walked together (L2 reuse)
   int run;            // K steps an accumulator takes before it is added to the registers'
-  float* partial;     // [splits][M][N] where splits > 1
+  float* partial;     // [tail tile][splits][rows of a tile][bn] where splits > 1
   Epilogue e;
 };
 
@@ -321,17 +324,36 @@ __device__ __forceinline__ uint64_t tile_desc(const unsigned char* p) {
             : tc::sdesc_sw128(tc::smem_u32(p), 16, 1024);
 }
 
-// Work item -> tile and split.  Tiles run down group_m rows of tiles before
-// the next column, so that the CTAs at work at one time share operands in L2.
-__device__ __forceinline__ void tile_of(const Gemm& p, int item, int& tm, int& tn, int& split) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  split = item / tiles;
-  const int t = item - split * tiles;
+// Tile number -> its place.  Tiles run down group_m rows of tiles before the
+// next column, so that the CTAs at work at one time share operands in L2.
+__host__ __device__ __forceinline__ void place_of(const Gemm& p, int t, int& tm, int& tn) {
   const int per = p.group_m * p.tiles_n;
   const int g = t / per, r = t - g * per;
-  const int gm = min(p.group_m, p.tiles_m - g * p.group_m);
+  const int left = p.tiles_m - g * p.group_m, gm = left < p.group_m ? left : p.group_m;
   tm = g * p.group_m + r % gm;
   tn = r / gm;
+}
+
+// A work item: a whole tile, or one split of a tail tile; the K steps [k0, k1).
+struct Item {
+  int tm, tn, k0, k1;
+  int part;   // of the tail: its place in `partial`; -1: finished here
+};
+__device__ __forceinline__ Item item_of(const Gemm& p, int item, int all_steps) {
+  Item w;
+  w.k0 = 0;
+  w.k1 = all_steps;
+  w.part = -1;
+  int t = item;
+  if (item >= p.full && p.splits > 1) {
+    const int j = item - p.full, q = j / p.splits, split = j - q * p.splits;
+    t = p.full + q;
+    w.part = j;
+    w.k0 = split * p.steps_per_split;
+    w.k1 = min(w.k0 + p.steps_per_split, all_steps);
+  }
+  place_of(p, t, w.tm, w.tn);
+  return w;
 }
 
 // A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
@@ -348,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)tc::cluster_rank() : 0;
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
-  const int items = p.tiles_m * p.tiles_n * p.splits;
+  const int items = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   const int all_steps = p.kblocks * p.pairs;
 
   if (warp == 0 && lane == 0) {
@@ -391,9 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     int issued = 0;
     bool ok = true;
     for (int it = first; it < items && ok; it += stride) {
-      int tm, tn, split;
-      tile_of(p, it, tm, tn, split);
-      const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+      const Item w = item_of(p, it, all_steps);
+      const int tm = w.tm, tn = w.tn, k0 = w.k0, k1 = w.k1;
       int q = k0 / p.kblocks, kb = k0 - q * p.kblocks;   // product of planes, K step in it
       int pa, pb;
       planes_of(p.pairs, q, pa, pb);
@@ -444,9 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int it = first; it < items && ok; it += stride) {
-        int tm, tn, split;
-        tile_of(p, it, tm, tn, split);
-        const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+        const Item w = item_of(p, it, all_steps);
+        const int k0 = w.k0, k1 = w.k1;
         for (int r0 = k0; r0 < k1 && ok; r0 += p.run, ++n) {
           const int r1 = min(r0 + p.run, k1), buf = n & 1;
           ok = __all_sync(0xffffffffu,
@@ -493,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     int n = 0;
     bool ok = true;
     for (int it = first; it < items; it += stride) {
-      int tm, tn, split;
-      tile_of(p, it, tm, tn, split);
-      const int k0 = split * p.steps_per_split, k1 = min(k0 + p.steps_per_split, all_steps);
+      const Item w = item_of(p, it, all_steps);
+      const int tm = w.tm, tn = w.tn, k0 = w.k0, k1 = w.k1;
+      const bool parts = w.part >= 0;
       auto filled = [&](int i) {   // one verdict for the warp: TMEM loads take all of its lanes
         const bool r =
             __all_sync(0xffffffffu, wait_phase(&s.tfull[i & 1], (i >> 1) & 1, &s.abort));
@@ -510,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           else tc::mbar_arrive(&s.tempty[i & 1]);
         }
       };
-      if (p.e.res && p.splits == 1) {
+      if (p.e.res && !parts) {
         // the residual on its way to L2 while the sums are made: a row a lane
         const int64_t m = ((int64_t)tm * CG + rank) * kBM + q * 32 + lane;
         if (m < p.M)
@@ -571,19 +591,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       const uint32_t at = tmem + (n & 1) * 256 + lanes;
       const int64_t m0 = ((int64_t)tm * CG + rank) * kBM + q * 32;
       const int64_t n0 = (int64_t)tn * BN;
-      const int rows = (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
+      const int rows = parts ? 32 : (int)min((int64_t)32, p.M - m0);   // <= 0: none of this warp's
       const int rr = lane >> 2, cc = lane & 3;
-      const bool parts = p.splits > 1;
-      void* const out = parts ? static_cast<void*>(p.partial + (int64_t)split * p.M * p.N) : p.e.out;
       const int out_t = parts ? kF32 : p.e.out_t;
-      const int64_t out_ld = parts ? p.N : p.e.out_ld;
+      const int64_t out_ld = parts ? BN : p.e.out_ld;
       const int oe = out_t == kF32 ? 4 : 2;
-      const bool wide = parts ? (p.N & 7) == 0 : p.e.wide8;
+      // this lane's place in the tile's first row and column block
+      char* const base =
+          parts ? reinterpret_cast<char*>(
+                      p.partial + (((int64_t)w.part * CG + rank) * kBM + q * 32 + rr) * BN + 8 * cc)
+                : static_cast<char*>(p.e.out) + ((m0 + rr) * out_ld + n0 + 8 * cc) * oe;
+      const bool wide = parts || p.e.wide8;
       const bool plain = parts || (!p.e.bias && !p.e.pre && !p.e.res && p.e.act == kActNone);
 #pragma unroll 1
       for (int c = half * 32; c < BN; c += 64) {
         const int64_t col = n0 + c + 8 * cc;
-        const bool in = wide && col < p.N;
+        const bool in = wide && (parts || col < p.N);
         // the residual first: its loads are in flight during the TMEM load, all
         // of them before the first store
         float res[4][8];
@@ -612,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
         };
         if (in) {
-          char* o = static_cast<char*>(out) + ((m0 + rr) * out_ld + col) * oe;
+          char* o = base + c * oe;
           const int64_t step = 8 * out_ld * oe;
           if (plain) {   // all of the sums read, then all stored
             float v[4][8];
@@ -659,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           }
         } else if (!wide && n0 + c + lane < p.N) {   // a column a lane, row by row
           const int64_t cl = n0 + c + lane;
-          const float b = !parts && p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
+          const float b = p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
 #pragma unroll 4
           for (int r = 0; r < rows; ++r) {
             float v = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
@@ -668,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
               v = act_f(p.e.act, v);
               if (p.e.res) v += get1(p.e.res, p.e.res_t, (m0 + r) * p.e.res_ld + cl);
             }
-            put1(out, out_t, (m0 + r) * out_ld + cl, v);
+            put1(p.e.out, out_t, (m0 + r) * out_ld + cl, v);
           }
         }
       }
@@ -686,29 +709,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   }
 }
 
-// Adds the partial sums of split K, in order, and finishes them.
-__global__ void __launch_bounds__(256)
-    join_kernel(const float* __restrict__ part, int splits, int64_t M, int64_t N,
-                const __grid_constant__ Epilogue e) {
-  const int64_t per_row = (N + 3) / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= M * per_row) return;
-  const int64_t m = i / per_row, n = (i - m * per_row) * 4;
+// Adds the partial sums of the tail's tiles, in order, and finishes them: four
+// columns a thread, a tile a blockIdx.y.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Gemm p, int rows) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= rows * p.bn) return;
+  const int r = i / p.bn, c = i - r * p.bn;
+  int tm, tn;
+  place_of(p, p.full + blockIdx.y, tm, tn);
+  const int64_t m = (int64_t)tm * rows + r, n = (int64_t)tn * p.bn + c;
+  if (m >= p.M || n >= p.N) return;
   float v[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
-  residual4(e, m, n, N, res);
+  residual4(p.e, m, n, p.N, res);
+  const float* part = p.partial + (int64_t)blockIdx.y * p.splits * rows * p.bn + i;
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float* p = part + (s * M + m) * N + n;
-    if ((N & 3) == 0) {
-      const float4 f = *reinterpret_cast<const float4*>(p);
-      v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < N) v[j] += p[j];
-    }
+  for (int s = 0; s < p.splits; ++s) {
+    const float4 f = *reinterpret_cast<const float4*>(part + (int64_t)s * rows * p.bn);
+    v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
   }
-  finish4(e, m, n, N, v, res);
+  finish4(p.e, m, n, p.N, v, res);
 }
 
 // ------------------------------------------------------- operands made ready
@@ -991,21 +1010,26 @@ bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product of M x N with `steps` K steps is cut: CTAs a tile, tile width
-// and splits of K.
+// How a product of M x N with `steps` K steps is cut: CTAs a tile, tile width,
+// the tiles computed whole, and the splits of K of the others.
 struct Plan {
-  int cg, bn, splits, steps_per;
+  int cg, bn, full, tail, splits, steps_per;
+  size_t partial_bytes() const {
+    return splits > 1 ? (size_t)tail * splits * cg * kBM * bn * sizeof(float) : 0;
+  }
 };
-// A model of its time in microseconds, over all tile widths (multiples of 32)
-// and splits.  A K step takes the tensor cores 2 BN cycles, and the shared
+// A model of its time in microseconds, over all tile widths (multiples of 32).
+// Tiles fill the SMs in rounds; the last, incomplete round's tiles may be split
+// along K over the SMs that it would leave idle (4096 x 10576 x 2560: 160 tiles
+// on 76 pairs).  A K step takes the tensor cores 2 BN cycles, and the shared
 // memory the time to write and read the step's tiles at 128 bytes a cycle
 // (measured: 528 cycles for 256 x 256 on a pair, 524 for 128 x 128 on one CTA).
 Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
   const int sms = row::sm_count();
   const int steps = (int)((K + kBK - 1) / kBK) * pairs;
-  constexpr double kGhz = 1.9, kL2Gbs = 16e3, kHbmGbs = 6e3;
+  constexpr double kGhz = 1.9, kL2Gbs = 16e3, kHbmGbs = 6e3, kJoinUs = 8.0, kJoinGbs = 5e3;
   const double hbm_us = ((double)(M + N) * K * 2 * (pairs > 1 ? 3 : 1)) / kHbmGbs * 1e-3;
-  Plan best = {2, 256, 1, steps};
+  Plan best = {2, 256, 1, 0, 1, steps};
   double best_us = 1e30;
   for (int cg = 1; cg <= 2; ++cg) {
     for (int bn = 32; bn <= 256; bn += 32) {
@@ -1013,26 +1037,27 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
       const int64_t tiles = ((M + kBM * cg - 1) / (kBM * cg)) * ((N + bn - 1) / bn);
       const double step_bytes = kStageA + stage_b(cg, bn, bmn);   // a CTA's
       const double step = std::max(2.0 * bn, 2.0 * step_bytes / 128) * 1e-3 / kGhz;
+      const int64_t at_once = sms / cg, rounds = tiles / at_once, tail = tiles % at_once;
+      const double l2_us = tiles * steps * step_bytes * cg / kL2Gbs * 1e-3;
       for (int splits = 1; splits <= 16; ++splits) {
         const int per = (steps + splits - 1) / splits;
-        if (splits > 1 && (per < 8 || (steps + per - 1) / per != splits)) continue;
-        const int64_t at_once = sms / cg, items = tiles * splits;
-        const int64_t waves = (items + at_once - 1) / at_once;
-        double us = std::max(waves * per * step, items * per * step_bytes * cg / kL2Gbs * 1e-3);
-        us = std::max(us, hbm_us) + 3.0 + 2.0 * bn / 256;   // fill, last epilogue
+        if (splits > 1 && (tail == 0 || tail * splits > at_once || per < 8 ||
+                           (steps + per - 1) / per != splits))
+          continue;
+        double us = (rounds * steps + (tail > 0 ? per : 0)) * step;
+        us = std::max(std::max(us, l2_us), hbm_us) + 3.0 + 2.0 * bn / 256;   // fill, last epilogue
         // partial sums are written, read and joined by another launch
-        if (splits > 1) us += 6.0 + (double)M * N * splits * 2 * 4 / 5e6;
+        if (splits > 1)
+          us += kJoinUs + (double)tail * cg * kBM * bn * splits * 8 / kJoinGbs * 1e-3;
         if (us < best_us) {
           best_us = us;
-          best = {cg, bn, splits, per};
+          best = {cg, bn, (int)(splits > 1 ? tiles - tail : tiles), (int)(splits > 1 ? tail : 0),
+                  splits, per};
         }
       }
     }
   }
   return best;
-}
-size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
-  return p.splits > 1 ? up256((size_t)p.splits * M * N * sizeof(float)) : 0;
 }
 
 // Persistent CTAs (or pairs) of a kernel that fit the device at once, cached
@@ -1077,13 +1102,13 @@ cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   int at_once = 0;
   const cudaError_t e = resident<CG, AMN, BMN>(&at_once);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int64_t items = g.full + ((int64_t)g.tiles_m * g.tiles_n - g.full) * g.splits;
   const int grid = CG * (int)std::min<int64_t>(items, at_once);
   gemm_kernel<CG, AMN, BMN><<<grid, kThreads, sizeof(Smem) + 1024, st>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
-// D[M,N] = sum over K and planes, finished by e; part: partial_bytes of the plan.
+// D[M,N] = sum over K and planes, finished by e; part: the plan's partial_bytes.
 int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int64_t N, int64_t K,
          const Epilogue& e, float* part, cudaStream_t st) {
   const int pairs = a.planes == 3 ? 6 : 1;
@@ -1098,12 +1123,13 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.pairs = pairs;
   g.tiles_m = (int)((M + kBM * pl.cg - 1) / (kBM * pl.cg));
   g.tiles_n = (int)((N + pl.bn - 1) / pl.bn);
+  g.full = pl.full;
   g.splits = pl.splits;
   g.steps_per_split = pl.steps_per;
   g.bn = pl.bn;
   g.stages = std::min(kMaxStages, kOperandBytes / (kStageA + stage_b(pl.cg, pl.bn, bmn)));
   g.group_m = 8 / pl.cg;
-  g.run = e.out_t == kF32 ? kExactSteps : pl.steps_per;
+  g.run = e.out_t == kF32 ? kExactSteps : g.kblocks * pairs;
   g.partial = part;
   g.e = e;
   cudaError_t err;
@@ -1116,8 +1142,9 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
 #undef SSD_GEMM
   if (err != cudaSuccess) return cuda_bad(err, "linear launch");
   if (pl.splits > 1) {
-    const int64_t n = M * ((N + 3) / 4);
-    join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, pl.splits, M, N, e);
+    const int rows = kBM * pl.cg;
+    join_kernel<<<dim3((unsigned)((rows * pl.bn / 4 + 255) / 256), (unsigned)pl.tail), 256, 0, st>>>(
+        g, rows);
     err = cudaGetLastError();
     if (err != cudaSuccess) return cuda_bad(err, "linear join launch");
   }
@@ -1205,15 +1232,15 @@ bool wide4(const void* p, int64_t ld, size_t e) { return al(p, 4 * e) && ld % 4 
 
 size_t fwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w) {
   const int planes = dt == SSD_DTYPE_F32 ? 3 : 1;
-  size_t b = partial_bytes(plan_for(rows, N, K, planes == 3 ? 6 : 1, false), rows, N);
+  size_t b = up256(plan_for(rows, N, K, planes == 3 ? 6 : 1, false).partial_bytes());
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
   return b;
 }
 size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w, bool pack_d) {
   const int planes = dt == SSD_DTYPE_F32 ? 3 : 1, pairs = planes == 3 ? 6 : 1;
-  size_t b = std::max(partial_bytes(plan_for(rows, K, N, pairs, true), rows, K),
-                      partial_bytes(plan_for(N, K, rows, pairs, true), N, K));
+  size_t b = up256(std::max(plan_for(rows, K, N, pairs, true).partial_bytes(),
+                            plan_for(N, K, rows, pairs, true).partial_bytes()));
   b += up256((size_t)prep_parts(rows, N) * N * sizeof(float));
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
