@@ -12,8 +12,9 @@ capturing ``Tensor.backward`` ties the graph to autograd's own streams.
 """
 from __future__ import annotations
 
-import ctypes
+import array
 import math
+import operator
 from typing import Optional
 
 import torch
@@ -591,8 +592,6 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
 def _storage_dense(t: torch.Tensor) -> bool:
     """Whether t's elements fill one block of memory (in any order of its
     dimensions), so that an element-wise pass may walk the block."""
-    if t.is_contiguous():
-        return True
     want = 1
     for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
         if s != want:
@@ -601,21 +600,31 @@ def _storage_dense(t: torch.Tensor) -> bool:
     return True
 
 
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 def _tensor_table(tensors, name, dev):
-    """Host arrays of the tensors' addresses and dtype codes."""
-    codes, ptrs = [], []
-    for t in tensors:
-        code = _DT.get(t.dtype)
-        if code is None:
-            raise ValueError(f"{name}: tensors must be float32 or bfloat16, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name}: a tensor is on {t.device}, expected {dev}")
-        if not (t.is_contiguous() or _storage_dense(t)):
-            raise ValueError(f"{name}: tensors must be dense")
-        codes.append(code)
-        ptrs.append(t.data_ptr())
-    n = len(ptrs)
-    return ptrs, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int32 * n)(*codes)
+    """Addresses of the tensors and their dtypes' codes (array.array), and
+    whether all are contiguous.  (A model has hundreds of gradients: each check
+    is one map over them.)"""
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, tensors))
+    try:
+        codes = array.array("i", map(_DT.__getitem__, map(_dtype_of, tensors)))
+    except KeyError as e:
+        raise ValueError(f"{name}: tensors must be float32 or bfloat16, got {e.args[0]}") from None
+    if set(map(torch.Tensor.get_device, tensors)) != {dev.index}:
+        raise ValueError(f"{name}: the tensors must be on {dev}")
+    contiguous = all(map(torch.Tensor.is_contiguous, tensors))
+    if not contiguous:
+        for t in tensors:
+            if not (t.is_contiguous() or t.numel() == 0 or _storage_dense(t)):
+                raise ValueError(f"{name}: tensors must be dense")
+    return ptrs, codes, contiguous
+
+
+def _address(a) -> int:
+    """Where an array.array's items are (host memory; the array must live)."""
+    return a.buffer_info()[0]
 
 
 def _grad_list(grads):
@@ -633,14 +642,14 @@ def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None, stream=None) -
     (fp32 and bf16, None entries skipped; ssd_grad_norm), as a 0-d fp32
     tensor on their device."""
     grads, dev = _grad_list(grads)
-    _, ptrs, codes = _tensor_table(grads, "grads", dev)
+    ptrs, codes, _ = _tensor_table(grads, "grads", dev)
     n = len(grads)
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    sizes = array.array("q", map(torch.Tensor.numel, grads))
     st = _stream_of(stream, dev)
     ws, ws_bytes, hold = _workspace(_call("ssd_clip_grads_workspace_bytes")(n), workspace, dev,
                                     stream)
     norm = _empty((), _F32, dev, stream)
-    _lib.check(_call("ssd_grad_norm")(ptrs, sizes, codes, n, norm.data_ptr(), ws, ws_bytes, st))
+    _lib.check(_call("ssd_grad_norm")(_address(ptrs), _address(sizes), _address(codes), n, norm.data_ptr(), ws, ws_bytes, st))
     return norm
 
 
@@ -653,28 +662,30 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
     optimizer that keeps bf16 gradients' clipped values so).  No host
     synchronisation.  Returns the norm before clipping, 0-d fp32."""
     grads, dev = _grad_list(grads)
-    where, ptrs, codes = _tensor_table(grads, "grads", dev)
+    ptrs, codes, dense = _tensor_table(grads, "grads", dev)
     n = len(grads)
-    outs = out_codes = None
+    sizes = array.array("q", map(torch.Tensor.numel, grads))
+    written, outs, out_codes = ptrs, None, None
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else [o for o in out if o is not None]
         if len(out) != n:
             raise ValueError(f"out has {len(out)} tensors for {n} gradients")
-        for o, g in zip(out, grads):
-            if o.shape != g.shape or not (o.is_contiguous() and g.is_contiguous()
-                                          or o.stride() == g.stride()):
-                raise ValueError("out must match its gradient's shape and strides")
-        where, outs, out_codes = _tensor_table(out, "out", dev)
-    counts = [g.numel() for g in grads]
-    if len(set(where)) != n:
-        written = [p for p, k in zip(where, counts) if k]
-        if len(set(written)) != len(written):
+        outs, out_codes, dense_out = _tensor_table(out, "out", dev)
+        written = outs
+        if list(map(_shape_of, out)) != list(map(_shape_of, grads)) or (
+                not (dense and dense_out)
+                and any(o.stride() != g.stride() for o, g in zip(out, grads))):
+            raise ValueError("out must match its gradient's shape and strides")
+    if len(set(written)) != n:
+        full = [p for p, k in zip(written, sizes) if k]
+        if len(set(full)) != len(full):
             raise ValueError("a tensor to write is given twice")
-    sizes = (ctypes.c_int64 * n)(*counts)
     st = _stream_of(stream, dev)
     ws, ws_bytes, hold = _workspace(_call("ssd_clip_grads_workspace_bytes")(n), workspace, dev,
                                     stream)
     norm = _empty((), _F32, dev, stream)
-    _lib.check(_call("ssd_clip_grads")(ptrs, sizes, codes, n, outs, out_codes, max_norm, eps,
-                                       norm.data_ptr(), ws, ws_bytes, st))
+    _lib.check(_call("ssd_clip_grads")(
+        _address(ptrs), _address(sizes), _address(codes), n,
+        None if outs is None else _address(outs), None if outs is None else _address(out_codes),
+        max_norm, eps, norm.data_ptr(), ws, ws_bytes, st))
     return norm

@@ -31,7 +31,7 @@ constexpr int kChunk = 16384;      // elements
 // together fewer (645M bf16 values into fp32: 634 us with 5, 776 with 8, 700
 // with 4; stores that leave the L2 first were no faster).
 constexpr int kNormCtas = 8, kScaleCtas = 5;
-constexpr int kSmall = 48, kLarge = 768;   // tensors a launch: 1.3 KB or 20.7 KB of parameters
+constexpr int kSmall = 48, kLarge = 768;   // tensors a launch: 1.5 KB or 23 KB of parameters
 
 template <int N>
 struct Table {
