@@ -39,7 +39,7 @@ int ssd_block_abi_version(void);
  *   residual      [rows, dim] residual_dtype, or NULL (= 0)
  *   scale         [dim] float, or NULL (= 1)
  *   weight        [dim] float
- *   y             [rows, dim] x dtype (written)
+ *   y             [rows, dim] x dtype (written; no other tensor's memory)
  *   residual_out  [rows, dim] residual_dtype (written; may be residual)
  * residual_dtype is fp32 or the x dtype.  rows in [1, 2^31), dim in
  * [1, 16384], any value; 16-byte aligned rows (dim a multiple of 8) take wide
@@ -183,7 +183,8 @@ int ssd_clip_grads(const void *const *grads, const int64_t *sizes,
  *   residual  [rows, out_features] fp32 or x dtype (residual_dtype), rows
  *             residual_row_stride elements apart, or NULL
  *   out       [rows, out_features] dense, of the residual's type, or the x
- *             dtype without one (written; may be the residual if it is dense)
+ *             dtype without one (written; may be the residual if it is dense,
+ *             and must not overlap anything else)
  *   pre       [rows, out_features] dense, or NULL: the value before act, which
  *             the backward of an activation reads.  For bf16 it is kept in
  *             IEEE half (11 bits in the same 2 bytes: act' depends on pre by

@@ -18,6 +18,7 @@ import operator
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .scan import _DT, _need, _ptr
@@ -180,6 +181,7 @@ class _AddRMSNorm(torch.autograd.Function):
         return y, r
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dr):
         r, weight, x, scale = ctx.saved_tensors
         if dy is None:
@@ -314,6 +316,7 @@ class _GatedRMSNorm(torch.autograd.Function):
         return gated_rmsnorm_fwd(y, z, weight, **ctx.opts)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, z, weight = ctx.saved_tensors
         g = gated_rmsnorm_bwd(dout.contiguous(), y, z, weight, **ctx.opts)
@@ -416,6 +419,7 @@ class CausalConv1d(torch.autograd.Function):
         return causal_conv1d(x, weight, bias, seq_idx=seq_idx, activation=activation)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x, weight, bias, seq_idx = ctx.saved_tensors
         g = causal_conv1d_bwd(dout.contiguous(), x, weight, bias, seq_idx=seq_idx,
@@ -563,6 +567,7 @@ class _Linear(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         x, weight, pre = ctx.saved_tensors
         nx, nw, nb, nr = ctx.needs_input_grad[:4]
@@ -600,7 +605,7 @@ def _storage_dense(t: torch.Tensor) -> bool:
     return True
 
 
-_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _tensor_table(tensors, name, dev):
@@ -658,9 +663,9 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
     """Scales the gradients (a tensor or an iterable, None entries skipped) by
     min(1, max_norm / (norm + eps)) with their common 2-norm
     (ssd_clip_grads): in place, or into `out`, one tensor for each gradient
-    that is not None, of the same shape and fp32 or bf16 (e.g. fp32 for an
-    optimizer that keeps bf16 gradients' clipped values so).  No host
-    synchronisation.  Returns the norm before clipping, 0-d fp32."""
+    that is not None, of its size and fp32 or bf16 (e.g. fp32 for an optimizer
+    that takes bf16 gradients' clipped values so).  No host synchronisation.
+    Returns the norm before clipping, 0-d fp32."""
     grads, dev = _grad_list(grads)
     ptrs, codes, dense = _tensor_table(grads, "grads", dev)
     n = len(grads)
@@ -672,10 +677,12 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
             raise ValueError(f"out has {len(out)} tensors for {n} gradients")
         outs, out_codes, dense_out = _tensor_table(out, "out", dev)
         written = outs
-        if list(map(_shape_of, out)) != list(map(_shape_of, grads)) or (
+        if array.array("q", map(torch.Tensor.numel, out)) != sizes or (
                 not (dense and dense_out)
-                and any(o.stride() != g.stride() for o, g in zip(out, grads))):
-            raise ValueError("out must match its gradient's shape and strides")
+                and any(o.shape != g.shape or o.stride() != g.stride()
+                        for o, g in zip(out, grads))):
+            raise ValueError("out must match its gradient's size (shape and strides, unless all "
+                             "tensors are contiguous)")
     if len(set(written)) != n:
         full = [p for p, k in zip(written, sizes) if k]
         if len(set(full)) != len(full):

@@ -218,6 +218,53 @@ __device__ __forceinline__ void put8(void* p, int t, const float (&v)[8]) {
   }
 }
 
+// v[r] to element at + r * ld of p, r < rows.
+__device__ __forceinline__ void put_column(void* p, int t, int64_t at, int64_t ld, int rows,
+                                           const float (&v)[32]) {
+  if (t == kF32) {
+    float* q = static_cast<float*>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      if (r < rows) q[r * ld] = v[r];
+  } else if (t == kF16) {
+    __half* q = static_cast<__half*>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      if (r < rows) q[r * ld] = __float2half_rn(half_range(v[r]));
+  } else {
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      if (r < rows) q[r * ld] = __float2bfloat16_rn(v[r]);
+  }
+}
+
+// Columns col .. col + 7 of a row whose tensors are aligned for eight columns
+// (whole) or for four; more: whether the second four are below N.
+__device__ __forceinline__ void get8(const void* p, int t, bool whole, bool more, float (&v)[8]) {
+  if (whole) {
+    get8(p, t, v);
+    return;
+  }
+  float a[4], b[4] = {0.f, 0.f, 0.f, 0.f};
+  get4(p, t, 0, a);
+  if (more) get4(p, t, 4, b);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
+  }
+}
+__device__ __forceinline__ void put8(void* p, int t, bool whole, bool more, const float (&v)[8]) {
+  if (whole) {
+    put8(p, t, v);
+    return;
+  }
+  const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+  put4(p, t, 0, a);
+  if (more) put4(p, t, 4, b);
+}
+
 // ------------------------------------------------------------------ the product
 
 struct Gemm {
@@ -601,12 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           parts ? reinterpret_cast<char*>(
                       p.partial + (((int64_t)w.part * CG + rank) * kBM + q * 32 + rr) * BN + 8 * cc)
                 : static_cast<char*>(p.e.out) + ((m0 + rr) * out_ld + n0 + 8 * cc) * oe;
-      const bool wide = parts || p.e.wide8;
+      const bool whole = parts || p.e.wide8, wide = whole || p.e.wide;
       const bool plain = parts || (!p.e.bias && !p.e.pre && !p.e.res && p.e.act == kActNone);
 #pragma unroll 1
       for (int c = half * 32; c < BN; c += 64) {
         const int64_t col = n0 + c + 8 * cc;
-        const bool in = wide && (parts || col < p.N);
+        const bool in = wide && (parts || col < p.N), more = parts || col + 4 < p.N;
         // the residual first: its loads are in flight during the TMEM load, all
         // of them before the first store
         float res[4][8];
@@ -616,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           for (int i = 0; i < 4; ++i)
             if (8 * i + rr < rows)
               get8(static_cast<const char*>(p.e.res) + ((m0 + 8 * i + rr) * p.e.res_ld + col) * re,
-                   p.e.res_t, res[i]);
+                   p.e.res_t, whole, more, res[i]);
         }
         uint32_t r[32];
         __syncwarp();
@@ -644,17 +691,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
             if (out_t == kF32) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (8 * i + rr < rows) put8(o + i * step, kF32, v[i]);
+                if (8 * i + rr < rows) put8(o + i * step, kF32, whole, more, v[i]);
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (8 * i + rr < rows) put8(o + i * step, kBf16, v[i]);
+                if (8 * i + rr < rows) put8(o + i * step, kBf16, whole, more, v[i]);
             }
           } else {
             float bias[8];
             if (p.e.bias)
               get8(static_cast<const char*>(p.e.bias) + col * (p.e.bias_t == kF32 ? 4 : 2),
-                   p.e.bias_t, bias);
+                   p.e.bias_t, whole, more, bias);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if (8 * i + rr < rows) {
@@ -667,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
                 if (p.e.pre)
                   put8(static_cast<char*>(p.e.pre) +
                            ((m0 + 8 * i + rr) * p.N + col) * (p.e.pre_t == kF32 ? 4 : 2),
-                       p.e.pre_t, v);
+                       p.e.pre_t, whole, more, v);
                 if (p.e.act != kActNone) {
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] = act_f(p.e.act, v[j]);
@@ -676,22 +723,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] += res[i][j];
                 }
-                put8(o + i * step, out_t, v);
+                put8(o + i * step, out_t, whole, more, v);
               }
             }
           }
-        } else if (!wide && n0 + c + lane < p.N) {   // a column a lane, row by row
+        } else if (!wide) {   // a column a lane: all of a step's rows before the next step
           const int64_t cl = n0 + c + lane;
-          const float b = p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
-#pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
-            float v = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
-            if (!plain) {
-              if (p.e.pre) put1(p.e.pre, p.e.pre_t, (m0 + r) * p.N + cl, v);
-              v = act_f(p.e.act, v);
-              if (p.e.res) v += get1(p.e.res, p.e.res_t, (m0 + r) * p.e.res_ld + cl);
+          if (cl < p.N) {
+            float v[32];
+            const float b = p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              v[r] = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
+            if (p.e.pre) put_column(p.e.pre, p.e.pre_t, m0 * p.N + cl, p.N, rows, v);
+            if (p.e.act != kActNone) {
+#pragma unroll
+              for (int r = 0; r < 32; ++r) v[r] = act_f(p.e.act, v[r]);
             }
-            put1(p.e.out, out_t, (m0 + r) * out_ld + cl, v);
+            if (p.e.res) {
+              const int64_t at0 = m0 * p.e.res_ld + cl;
+              if (p.e.res_t == kF32) {
+                const float* q = static_cast<const float*>(p.e.res) + at0;
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                  if (r < rows) v[r] += q[r * p.e.res_ld];
+              } else {
+                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.e.res) + at0;
+#pragma unroll
+                for (int r = 0; r < 32; ++r)
+                  if (r < rows) v[r] += __bfloat162float(q[r * p.e.res_ld]);
+              }
+            }
+            put_column(p.e.out, out_t, m0 * out_ld + cl, out_ld, rows, v);
           }
         }
       }
@@ -745,67 +808,108 @@ struct Prep {
   int C;
   uint8_t src_t, pre_t, act, planes;
 };
-__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ Prep p) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.C) return;
-  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per, r1 = min(r0 + p.rows_per, p.R);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int64_t r = r0; r < r1; ++r) {
-    float v = get1(p.src, p.src_t, r * p.src_ld + c);
-    if (p.pre) v *= dact_f(p.act, get1(p.pre, p.pre_t, r * p.C + c));
-    sum += v;
-    __nv_bfloat16* o = p.out + r * p.ld + c;
-    for (int k = 0; k < p.planes; ++k) {
-      const __nv_bfloat16 h = __float2bfloat16_rn(v);
-      *o = h;
-      o += p.R * p.ld;
-      v -= __bfloat162float(h);
-    }
+// Eight consecutive elements from an address that is aligned to its element
+// only: the aligned 16-byte words that hold them (none past `end`, the end of
+// the row, is touched), moved down by the offset in steps of 2, 1 and 1/2 words.
+__device__ __forceinline__ void get8_any(const void* p, int t, const void* end, float (&v)[8]) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), base = a & ~(uintptr_t)15;
+  const uint4* q = reinterpret_cast<const uint4*>(base);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int off = (int)(a & 15) >> 2, n = t == kF32 ? 3 : 2;   // in words; 16-byte words needed
+  uint32_t u[12];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint4 w =
+        i < n && reinterpret_cast<uintptr_t>(q + i) < reinterpret_cast<uintptr_t>(end) ? q[i] : zero;
+    u[4 * i] = w.x; u[4 * i + 1] = w.y; u[4 * i + 2] = w.z; u[4 * i + 3] = w.w;
   }
-  if (p.colsum) p.colsum[(int64_t)blockIdx.y * p.C + c] = sum;
+  if (off & 2) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) u[i] = u[i + 2];
+  }
+  if (off & 1) {
+#pragma unroll
+    for (int i = 0; i < 9; ++i) u[i] = u[i + 1];
+  }
+  if (t == kF32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+    return;
+  }
+  if (a & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
+  }
+  if (t == kF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+    row::unpack(make_uint4(u[0], u[1], u[2], u[3]), v);
+  }
 }
 
-// The same with eight consecutive columns a thread (C and the strides multiples
-// of 8, 16-byte aligned): 17M fp32 values into planes take about a quarter of
-// the one-column form's time, whose 2-byte stores go to three planes.
-__global__ void __launch_bounds__(128) prep8_kernel(const __grid_constant__ Prep p) {
+// Eight consecutive columns a thread; ANY: rows of any alignment and length.
+template <bool ANY>
+__global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep p) {
   const int c = (blockIdx.x * 128 + threadIdx.x) * 8;
   if (c >= p.C) return;
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per, r1 = min(r0 + p.rows_per, p.R);
   const int se = p.src_t == kF32 ? 4 : 2, pe = p.pre_t == kF32 ? 4 : 2;
+  const int left = p.C - c;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
-#pragma unroll 2
-  for (int64_t r = r0; r < r1; ++r) {
-    float v[8];
-    get8(static_cast<const char*>(p.src) + (r * p.src_ld + c) * se, p.src_t, v);
-    if (p.pre) {
-      float q[8];
-      get8(static_cast<const char*>(p.pre) + (r * p.C + c) * pe, p.pre_t, q);
+  // kAhead rows' loads before the first store (which may not be moved over loads)
+  constexpr int kAhead = 4;
+  for (int64_t rb = r0; rb < r1; rb += kAhead) {
+    float v[kAhead][8], q[kAhead][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= dact_f(p.act, q[j]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t r = min(rb + i, r1 - 1);
+      const char* src = static_cast<const char*>(p.src) + (r * p.src_ld + c) * se;
+      if (ANY) get8_any(src, p.src_t, src + (int64_t)left * se, v[i]);
+      else get8(src, p.src_t, v[i]);
+    }
+    if (p.pre) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t r = min(rb + i, r1 - 1);
+        const char* pre = static_cast<const char*>(p.pre) + (r * p.C + c) * pe;
+        if (ANY) get8_any(pre, p.pre_t, pre + (int64_t)left * pe, q[i]);
+        else get8(pre, p.pre_t, q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= dact_f(p.act, q[i][j]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    __nv_bfloat16* o = p.out + r * p.ld + c;
-    for (int k = 0; k < p.planes; ++k) {
-      uint32_t u[4];
+    for (int i = 0; i < kAhead; ++i) {
+      if (rb + i >= r1) break;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        u[j] = tc::pack_bf16x2(v[2 * j], v[2 * j + 1]);
-        v[2 * j] -= __uint_as_float(u[j] << 16);
-        v[2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
+      for (int j = 0; j < 8; ++j) sum[j] += v[i][j];
+      __nv_bfloat16* o = p.out + (rb + i) * p.ld + c;   // (ld is a multiple of 8: the pad may be written)
+      for (int k = 0; k < p.planes; ++k) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          u[j] = tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1]);
+          v[i][2 * j] -= __uint_as_float(u[j] << 16);
+          v[i][2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+        o += p.R * p.ld;
       }
-      *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-      o += p.R * p.ld;
     }
   }
   if (p.colsum) {
-    float4* q = reinterpret_cast<float4*>(p.colsum + (int64_t)blockIdx.y * p.C + c);
-    q[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-    q[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) p.colsum[(int64_t)blockIdx.y * p.C + c + j] = sum[j];
   }
 }
 
@@ -1188,10 +1292,11 @@ cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const
   p.act = (uint8_t)act;
   p.planes = (uint8_t)planes;
   const unsigned parts = (unsigned)prep_parts(R, C);
+  const dim3 grid((unsigned)((C + 1023) / 1024), parts);
   if (C % 8 == 0 && ld % 8 == 0 && al(src, 16) && al(pre, 16))
-    prep8_kernel<<<dim3((unsigned)((C + 1023) / 1024), parts), 128, 0, st>>>(p);
+    prep_kernel<false><<<grid, 128, 0, st>>>(p);
   else
-    prep_kernel<<<dim3((unsigned)((C + 255) / 256), parts), 256, 0, st>>>(p);
+    prep_kernel<true><<<grid, 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -379,11 +379,16 @@ __global__ void __launch_bounds__(32 * ROWS)
 }
 
 // Slots a thread, by what a kernel holds of each (norm first: the gate too).
-constexpr int kAddFwdSlots = 4, kAddBwdSlots = 2;
-constexpr int gated_fwd_slots(ssd_dtype_t dt, bool norm_first) {
-  return dt == SSD_DTYPE_BF16 && !norm_first ? 4 : 2;
+// One-element accesses hold every operand unpacked: one slot in the backwards,
+// where two would spill (10224 x 2417 in fp32: 291 us).
+constexpr int kAddFwdSlots = 4;
+constexpr int add_bwd_slots(bool vec) { return vec ? 2 : 1; }
+constexpr int gated_fwd_slots(ssd_dtype_t dt, bool norm_first, bool vec) {
+  return dt == SSD_DTYPE_BF16 && !norm_first && vec ? 4 : 2;
 }
-constexpr int gated_bwd_slots(ssd_dtype_t dt) { return dt == SSD_DTYPE_BF16 ? 4 : 2; }
+constexpr int gated_bwd_slots(ssd_dtype_t dt, bool vec) {
+  return !vec ? 1 : dt == SSD_DTYPE_BF16 ? 4 : 2;
+}
 
 // A backward's grid holds the CTAs that its registers let run at once: more
 // would be a second, nearly empty round (2560 channels: 366 us instead of 276),
@@ -394,6 +399,9 @@ int64_t bwd_ctas(int64_t rows, const row::Shape& sh, int groups, int warps_of_on
   const int64_t need = (rows + sh.teams - 1) / sh.teams;
   const int64_t per_sm = std::max(1, warps / (sh.threads() / 32));
   return std::min(need, std::max<int64_t>(1, row::sm_count() * per_sm / groups));
+}
+int64_t add_bwd_ctas(int64_t rows, const row::Shape& sh, bool vec) {
+  return bwd_ctas(rows, sh, 1, vec ? kAddWarps : kManySlotsWarps);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -521,8 +529,12 @@ int ssd_add_rmsnorm_fwd(const void* x, const void* residual, const float* scale,
 
 size_t ssd_add_rmsnorm_bwd_workspace_bytes(int64_t rows, int dim) {
   if (check_add(rows, dim, 0.f, SSD_DTYPE_F32, SSD_DTYPE_F32) != SSD_OK) return 0;
-  const row::Shape sh = row::shape_for(dim, kAddBwdSlots);
-  return up256((size_t)bwd_ctas(rows, sh, 1, kAddWarps) * sh.teams * 2 * dim * sizeof(float));
+  int64_t most = 0;   // of the layouts for aligned rows and others
+  for (const bool vec : {false, true}) {
+    const row::Shape sh = row::shape_for(dim, add_bwd_slots(vec));
+    most = std::max(most, add_bwd_ctas(rows, sh, vec) * sh.teams);
+  }
+  return up256((size_t)most * 2 * dim * sizeof(float));
 }
 
 int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* residual_out,
@@ -548,8 +560,8 @@ int ssd_add_rmsnorm_bwd(const void* dy, const void* dresidual_out, const void* r
   const bool vec = dim % kVec == 0 && row::wide(dy) && row::wide(dresidual_out) &&
                    row::wide(residual_out) && row::wide(x) && row::wide(dx) &&
                    row::wide(dresidual) && row::wide(scale) && row::wide(weight);
-  const row::Shape sh = row::shape_for(dim, kAddBwdSlots);
-  const unsigned grid = (unsigned)bwd_ctas(rows, sh, 1, kAddWarps);
+  const row::Shape sh = row::shape_for(dim, add_bwd_slots(vec));
+  const unsigned grid = (unsigned)add_bwd_ctas(rows, sh, vec);
   float* part = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf = __nv_bfloat16;
@@ -584,7 +596,7 @@ int ssd_gated_rmsnorm_fwd(const void* y, ssd_stride_t y_stride, const void* z,
   const bool vec = group_size % kVec == 0 && row::wide(y) && row::wide(z) && row::wide(out) &&
                    row::wide(weight) && wide_stride(y_stride, e) &&
                    (!z || wide_stride(z_stride, e));
-  const row::Shape sh = row::shape_for(group_size, gated_fwd_slots(dtype, z && norm_before_gate));
+  const row::Shape sh = row::shape_for(group_size, gated_fwd_slots(dtype, z && norm_before_gate, vec));
   Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
              {z_stride.batch, z_stride.token}, {0, 0}};
   if (even(y_stride, batch, seqlen) && (!z || even(z_stride, batch, seqlen))) rw.seqlen = 0;
@@ -605,9 +617,10 @@ int ssd_gated_rmsnorm_fwd(const void* y, ssd_stride_t y_stride, const void* z,
 size_t ssd_gated_rmsnorm_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int dim,
                                              int group_size) {
   if (check_gated(batch, seqlen, dim, group_size, 0.f, SSD_DTYPE_F32) != SSD_OK) return 0;
-  size_t most = 0;   // of the two dtypes' layouts
-  for (const ssd_dtype_t dt : {SSD_DTYPE_F32, SSD_DTYPE_BF16}) {
-    const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dt));
+  size_t most = 0;   // of the layouts for one slot, two and four
+  for (int i = 0; i < 3; ++i) {
+    const ssd_dtype_t dt = i == 2 ? SSD_DTYPE_BF16 : SSD_DTYPE_F32;
+    const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dt, i > 0));
     most = std::max(most, (size_t)(bwd_ctas(batch * seqlen, sh, dim / group_size, kGatedWarps) * sh.teams));
   }
   return up256(most * dim * sizeof(float));
@@ -638,7 +651,7 @@ int ssd_gated_rmsnorm_bwd(const void* dout, const void* y, ssd_stride_t y_stride
                    row::wide(dy) && row::wide(dz) && row::wide(weight) &&
                    wide_stride(y_stride, e) &&
                    (!z || (wide_stride(z_stride, e) && wide_stride(dz_stride, e)));
-  const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dtype));
+  const row::Shape sh = row::shape_for(group_size, gated_bwd_slots(dtype, vec));
   Rows rw = {(uint32_t)(batch * seqlen), (uint32_t)seqlen, {y_stride.batch, y_stride.token},
              {z_stride.batch, z_stride.token}, {dz_stride.batch, dz_stride.token}};
   if (even(y_stride, batch, seqlen) &&
