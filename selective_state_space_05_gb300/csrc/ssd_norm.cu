@@ -3,14 +3,22 @@
 //
 // Both are bound by HBM: a forward reads its inputs and writes its outputs
 // once, and so does a backward, which keeps the row it normalises in
-// registers.  One team of warps holds a row (add) or a channel group of a row
-// (gated), eight elements to a slot, so each statistic is one sum over the
-// team.  With n = r * s, s = 1 / sqrt(mean r^2 + eps), g = w dy, the backward
+// registers, packed as it was loaded.  A team of threads (8 to 512) holds a row
+// (add) or a channel group of a row (gated), eight elements to a slot and up to
+// four slots a thread, so each statistic is one sum over the team, and a row
+// that one warp holds needs no barrier.  With n = r * s,
+// s = 1 / sqrt(mean r^2 + eps), g = w dy, the backward
 //   dr = s (g - n mean(g n)) = s (g - r s^2 mean(g r))
 // needs mean r^2 and mean g r, which are summed together: one exchange.
 // The parameters' gradients sum over rows: each team walks rows a grid apart
 // and keeps its columns' sums in registers, writes them once to the
 // workspace, and launch_column_sum joins the teams in a fixed order.
+//
+// Measured on one GB300 (6.69 TB/s copy), 32768 rows: add_rmsnorm of 2560
+// channels (bf16, fp32 residual) forward 149 us = 6.77 TB/s, backward with scale
+// 274 us = 5.5 TB/s; gated_rmsnorm of 5120 channels (bf16) in 8 groups forward
+// 193 us = 5.2 TB/s, backward 337 us = 5.0 TB/s, where it issues 70 % of the
+// cycles: exponentials, reciprocals and the conversions of five operands.
 #include <stdio.h>
 
 #include <algorithm>
