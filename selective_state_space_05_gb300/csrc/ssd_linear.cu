@@ -226,23 +226,10 @@ __device__ __forceinline__ void put8(void* p, int t, const float (&v)[8]) {
 
 // v[r] to element at + r * ld of p, r < rows.
 __device__ __forceinline__ void put_column(void* p, int t, int64_t at, int64_t ld, int rows,
-                                           const float (&v)[32]) {
-  if (t == kF32) {
-    float* q = static_cast<float*>(p) + at;
+                                           const float (&v)[8]) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r)
-      if (r < rows) q[r * ld] = v[r];
-  } else if (t == kF16) {
-    __half* q = static_cast<__half*>(p) + at;
-#pragma unroll
-    for (int r = 0; r < 32; ++r)
-      if (r < rows) q[r * ld] = __float2half_rn(half_range(v[r]));
-  } else {
-    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
-#pragma unroll
-    for (int r = 0; r < 32; ++r)
-      if (r < rows) q[r * ld] = __float2bfloat16_rn(v[r]);
-  }
+  for (int r = 0; r < 8; ++r)
+    if (r < rows) put1(p, t, at + r * ld, v[r]);
 }
 
 // Columns col .. col + 7 of a row whose tensors are aligned for eight columns
@@ -412,7 +399,10 @@ __device__ __forceinline__ Item item_of(const Gemm& p, int item, int all_steps) 
 // A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
 // leader's `full`; the leader issues the MMAs and signals `empty` and `tfull`
 // of both; both CTAs' epilogues arrive on the leader's `tempty`.
-template <int CG, bool AMN, bool BMN>
+// EXACT: sums in runs of p.run K steps (fp32 results); PLAIN: no bias, pre,
+// activation or residual.  Apart, because one kernel with all of it was 150 KB
+// of code and spilled.
+template <int CG, bool AMN, bool BMN, bool EXACT, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const __grid_constant__ Gemm p) {
@@ -425,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   const int items = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   const int all_steps = p.kblocks * p.pairs;
+  const int run = EXACT ? p.run : all_steps;   // K steps of one accumulator
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S; ++i) {
@@ -520,8 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       for (int it = first; it < items && ok; it += stride) {
         const Item w = item_of(p, it, all_steps);
         const int k0 = w.k0, k1 = w.k1;
-        for (int r0 = k0; r0 < k1 && ok; r0 += p.run, ++n) {
-          const int r1 = min(r0 + p.run, k1), buf = n & 1;
+        for (int r0 = k0; r0 < k1 && ok; r0 += run, ++n) {
+          const int r1 = min(r0 + run, k1), buf = n & 1;
           ok = __all_sync(0xffffffffu,
                           wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort));
           tc::fence_after_sync();
@@ -583,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
           else tc::mbar_arrive(&s.tempty[i & 1]);
         }
       };
-      if (p.e.res && !parts) {
+      const bool has_res = !PLAIN && p.e.res && !parts;
+      if (has_res) {
         // the residual on its way to L2 while the sums are made: a row a lane
         const int64_t m = ((int64_t)tm * CG + rank) * kBM + q * 32 + lane;
         if (m < p.M)
@@ -595,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
                   (m * p.e.res_ld + n) * (p.e.res_t == kF32 ? 4 : 2)));
           }
       }
-      if (k1 - k0 > p.run) {
+      if (EXACT && k1 - k0 > p.run) {
         // the runs' sums in registers; their total goes back to the last run's
         // place in TMEM
         float acc[4][32];
@@ -655,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
                       p.partial + (((int64_t)w.part * CG + rank) * kBM + q * 32 + rr) * BN + 8 * cc)
                 : static_cast<char*>(p.e.out) + ((m0 + rr) * out_ld + n0 + 8 * cc) * oe;
       const bool whole = parts || p.e.wide8, wide = whole || p.e.wide;
-      const bool plain = parts || (!p.e.bias && !p.e.pre && !p.e.res && p.e.act == kActNone);
+      const bool plain = PLAIN || parts;
 #pragma unroll 1
       for (int c = half * 32; c < BN; c += 64) {
         const int64_t col = n0 + c + 8 * cc;
@@ -663,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
         // the residual first: its loads are in flight during the TMEM load, all
         // of them before the first store
         float res[4][8];
-        if (!plain && in && p.e.res) {
+        if (in && has_res) {
           const int re = p.e.res_t == kF32 ? 4 : 2;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -725,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] = act_f(p.e.act, v[j]);
                 }
-                if (p.e.res) {
+                if (has_res) {
 #pragma unroll
                   for (int j = 0; j < 8; ++j) v[j] += res[i][j];
                 }
@@ -733,34 +725,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
               }
             }
           }
-        } else if (!wide) {   // a column a lane: all of a step's rows before the next step
+        } else if (!wide) {   // a column a lane, eight rows at a time
           const int64_t cl = n0 + c + lane;
           if (cl < p.N) {
-            float v[32];
-            const float b = p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
+            const float b = !PLAIN && p.e.bias ? get1(p.e.bias, p.e.bias_t, cl) : 0.f;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+              float v[8];
 #pragma unroll
-            for (int r = 0; r < 32; ++r)
-              v[r] = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
-            if (p.e.pre) put_column(p.e.pre, p.e.pre_t, m0 * p.N + cl, p.N, rows, v);
-            if (p.e.act != kActNone) {
-#pragma unroll
-              for (int r = 0; r < 32; ++r) v[r] = act_f(p.e.act, v[r]);
-            }
-            if (p.e.res) {
-              const int64_t at0 = m0 * p.e.res_ld + cl;
-              if (p.e.res_t == kF32) {
-                const float* q = static_cast<const float*>(p.e.res) + at0;
-#pragma unroll
-                for (int r = 0; r < 32; ++r)
-                  if (r < rows) v[r] += q[r * p.e.res_ld];
-              } else {
-                const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.e.res) + at0;
-#pragma unroll
-                for (int r = 0; r < 32; ++r)
-                  if (r < rows) v[r] += __bfloat162float(q[r * p.e.res_ld]);
+              for (int i = 0; i < 8; ++i) {
+                const int r = r0 + i;
+                v[i] = turn[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
               }
+              const int left = rows - r0;
+              if constexpr (!PLAIN) {
+                if (p.e.pre)
+                  put_column(p.e.pre, p.e.pre_t, (m0 + r0) * p.N + cl, p.N, left, v);
+                if (p.e.act != kActNone) {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[i] = act_f(p.e.act, v[i]);
+                }
+                if (has_res) {
+                  float res[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    res[i] =
+                        i < left ? get1(p.e.res, p.e.res_t, (m0 + r0 + i) * p.e.res_ld + cl) : 0.f;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[i] += res[i];
+                }
+              }
+              put_column(p.e.out, out_t, (m0 + r0) * out_ld + cl, out_ld, left, v);
             }
-            put_column(p.e.out, out_t, m0 * out_ld + cl, out_ld, rows, v);
           }
         }
       }
@@ -1133,7 +1129,8 @@ struct Plan {
 // along K over the SMs that it would leave idle (4096 x 10576 x 2560: 160 tiles
 // on 76 pairs).  A K step takes the tensor cores 2 BN cycles, and the shared
 // memory the time to write and read the step's tiles at 128 bytes a cycle
-// (measured: 528 cycles for 256 x 256 on a pair, 524 for 128 x 128 on one CTA).
+// (measured: 528 cycles for 256 x 256 on a pair, 524 for 128 x 128 on one CTA), and the MMA warp
+// 350 to 400 cycles to issue.
 Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
   const int sms = row::sm_count();
   const int steps = (int)((K + kBK - 1) / kBK) * pairs;
@@ -1146,7 +1143,7 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
       if (bmn && bn % (64 * cg) != 0) continue;   // whole blocks of an MN-major B
       const int64_t tiles = ((M + kBM * cg - 1) / (kBM * cg)) * ((N + bn - 1) / bn);
       const double step_bytes = kStageA + stage_b(cg, bn, bmn);   // a CTA's
-      const double step = std::max(2.0 * bn, 2.0 * step_bytes / 128) * 1e-3 / kGhz;
+      const double step = std::max({2.0 * bn, 2.0 * step_bytes / 128, 380.0}) * 1e-3 / kGhz;
       const int64_t at_once = sms / cg, rounds = tiles / at_once, tail = tiles % at_once;
       const double l2_us = tiles * steps * step_bytes * cg / kL2Gbs * 1e-3;
       for (int splits = 1; splits <= 16; ++splits) {
@@ -1172,7 +1169,7 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
 
 // Persistent CTAs (or pairs) of a kernel that fit the device at once, cached
 // per device; the first call also opts in to its shared memory.
-template <int CG, bool AMN, bool BMN>
+template <int CG, bool AMN, bool BMN, bool EXACT, bool PLAIN>
 cudaError_t resident(int* n) {
   static std::atomic<int> cached[64];
   int dev = 0;
@@ -1182,7 +1179,7 @@ cudaError_t resident(int* n) {
   *n = known ? cached[dev].load(std::memory_order_acquire) : 0;
   if (*n > 0) return cudaSuccess;
   const size_t smem = sizeof(Smem) + 1024;
-  auto* kernel = gemm_kernel<CG, AMN, BMN>;
+  auto* kernel = gemm_kernel<CG, AMN, BMN, EXACT, PLAIN>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   *n = row::sm_count() / CG;
@@ -1206,15 +1203,16 @@ cudaError_t resident(int* n) {
   return cudaSuccess;
 }
 
-template <int CG, bool AMN, bool BMN>
+template <int CG, bool AMN, bool BMN, bool EXACT, bool PLAIN>
 cudaError_t launch_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm& g,
                         cudaStream_t st) {
   int at_once = 0;
-  const cudaError_t e = resident<CG, AMN, BMN>(&at_once);
+  const cudaError_t e = resident<CG, AMN, BMN, EXACT, PLAIN>(&at_once);
   if (e != cudaSuccess) return e;
   const int64_t items = g.full + ((int64_t)g.tiles_m * g.tiles_n - g.full) * g.splits;
   const int grid = CG * (int)std::min<int64_t>(items, at_once);
-  gemm_kernel<CG, AMN, BMN><<<grid, kThreads, sizeof(Smem) + 1024, st>>>(ma, mb, g);
+  gemm_kernel<CG, AMN, BMN, EXACT, PLAIN>
+      <<<grid, kThreads, sizeof(Smem) + 1024, st>>>(ma, mb, g);
   return cudaGetLastError();
 }
 
@@ -1239,17 +1237,23 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.bn = pl.bn;
   g.stages = std::min(kMaxStages, kOperandBytes / (kStageA + stage_b(pl.cg, pl.bn, bmn)));
   g.group_m = 8 / pl.cg;
-  g.run = e.out_t == kF32 ? kExactSteps : g.kblocks * pairs;
+  g.run = kExactSteps;
   g.partial = part;
   g.e = e;
+  const bool exact = e.out_t == kF32;
+  const bool plain = !e.bias && !e.pre && !e.res && e.act == kActNone;
   cudaError_t err;
-#define SSD_GEMM(CG)                                                      \
-  err = amn ? launch_gemm<CG, true, true>(ma, mb, g, st)                  \
-            : bmn ? launch_gemm<CG, false, true>(ma, mb, g, st)           \
-                  : launch_gemm<CG, false, false>(ma, mb, g, st)
-  if (pl.cg == 2) SSD_GEMM(2);
-  else SSD_GEMM(1);
-#undef SSD_GEMM
+  // (the backward's products are plain)
+#define SSD_GEMM_AS(CG, EXACT)                                                               \
+  err = amn   ? launch_gemm<CG, true, true, EXACT, true>(ma, mb, g, st)                      \
+        : bmn ? launch_gemm<CG, false, true, EXACT, true>(ma, mb, g, st)                     \
+        : plain ? launch_gemm<CG, false, false, EXACT, true>(ma, mb, g, st)                  \
+                : launch_gemm<CG, false, false, EXACT, false>(ma, mb, g, st)
+  if (pl.cg == 2 && exact) SSD_GEMM_AS(2, true);
+  else if (pl.cg == 2) SSD_GEMM_AS(2, false);
+  else if (exact) SSD_GEMM_AS(1, true);
+  else SSD_GEMM_AS(1, false);
+#undef SSD_GEMM_AS
   if (err != cudaSuccess) return cuda_bad(err, "linear launch");
   if (pl.splits > 1) {
     const int rows = kBM * pl.cg;
