@@ -31,10 +31,12 @@
 // fp32 FMAs for fp32.
 //
 // Measured on one GB300 (bf16, of 1885 TFLOP/s for a library product):
-// 32768 x 2560 -> 10576 forward 935 us (1.90 PFLOP/s, the tensor pipe 90 % active
-// in a capture), dx 937 us, dW 988-1080 us; 1021 x 5120 -> 2560 into an fp32
+// 32768 x 2560 -> 10576 forward 915 us (1.94 PFLOP/s, the tensor pipe 90 % active
+// in a capture), dx 923 us, dW 1020-1087 us; 1021 x 5120 -> 2560 into an fp32
 // residual 35 us, where 64 of 76 pairs hold one tile each and its last epilogue
 // has nothing to hide behind; 8 x 2560 -> 10576 10.3 us (5.3 TB/s of weight).
+// fp32, 4095 x 2048 -> 4384: forward 271 us, dx 298, dW 282 with the splitting
+// into planes (six bf16 products: 1.63, 1.48 and 1.56 PFLOP/s of them).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <stdio.h>
@@ -1126,15 +1128,16 @@ struct Plan {
 };
 // A model of its time in microseconds, over all tile widths (multiples of 32).
 // Tiles fill the SMs in rounds; the last, incomplete round's tiles may be split
-// along K over the SMs that it would leave idle (4096 x 10576 x 2560: 160 tiles
-// on 76 pairs).  A K step takes the tensor cores 2 BN cycles, and the shared
-// memory the time to write and read the step's tiles at 128 bytes a cycle
-// (measured: 528 cycles for 256 x 256 on a pair, 524 for 128 x 128 on one CTA), and the MMA warp
-// 350 to 400 cycles to issue.
+// along K over the SMs that it would leave idle (dx of 4096 x 10576 -> 2560: 160
+// tiles on 76 pairs), in one round of splits or several (8192 rows: 16 tiles
+// left in four splits, 247 us instead of 271).  A K step takes the tensor cores
+// 2 BN cycles, the shared memory the time to write and read the step's tiles at
+// 128 bytes a cycle (measured: 528 cycles for 256 x 256 on a pair, 524 for
+// 128 x 128 on one CTA), and the MMA warp 350 to 400 cycles to issue.
 Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
   const int sms = row::sm_count();
   const int steps = (int)((K + kBK - 1) / kBK) * pairs;
-  constexpr double kGhz = 1.9, kL2Gbs = 16e3, kHbmGbs = 6e3, kJoinUs = 8.0, kJoinGbs = 5e3;
+  constexpr double kGhz = 1.9, kL2Gbs = 20e3, kHbmGbs = 6e3, kJoinUs = 8.0, kJoinGbs = 5e3;
   const double hbm_us = ((double)(M + N) * K * 2 * (pairs > 1 ? 3 : 1)) / kHbmGbs * 1e-3;
   Plan best = {2, 256, 1, 0, 1, steps};
   double best_us = 1e30;
@@ -1148,10 +1151,9 @@ Plan plan_for(int64_t M, int64_t N, int64_t K, int pairs, bool bmn) {
       const double l2_us = tiles * steps * step_bytes * cg / kL2Gbs * 1e-3;
       for (int splits = 1; splits <= 16; ++splits) {
         const int per = (steps + splits - 1) / splits;
-        if (splits > 1 && (tail == 0 || tail * splits > at_once || per < 8 ||
-                           (steps + per - 1) / per != splits))
-          continue;
-        double us = (rounds * steps + (tail > 0 ? per : 0)) * step;
+        if (splits > 1 && (tail == 0 || per < 8 || (steps + per - 1) / per != splits)) continue;
+        const int64_t parts = (tail * splits + at_once - 1) / at_once;   // rounds of splits
+        double us = (rounds * steps + parts * per) * step;
         us = std::max(std::max(us, l2_us), hbm_us) + 3.0 + 2.0 * bn / 256;   // fill, last epilogue
         // partial sums are written, read and joined by another launch
         if (splits > 1)

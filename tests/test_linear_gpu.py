@@ -98,11 +98,11 @@ def test_linear(case):
 
 
 # rows, in, out that the product kernel cuts differently: single CTAs and pairs,
-# tiles 32 to 256 wide, one to sixteen splits of K, several rounds of tiles,
+# tiles 32 to 256 wide, one to sixteen splits of K, several rounds of tiles and of splits,
 # sums in one run and in several (an fp32 residual keeps the sum exact)
 TILES = [(700, 512, 1500), (2500, 640, 700), (3000, 4096, 520), (260, 8192, 264),
          (513, 2048, 1032), (100, 2100, 4200), (5000, 136, 5000), (40, 24000, 40),
-         (1999, 1000, 3001)]
+         (1999, 1000, 3001), (611, 2100, 3591)]
 
 
 @pytest.mark.parametrize("rt", [None, F32])
