@@ -31,8 +31,8 @@
 // fp32 FMAs for fp32.
 //
 // Measured on one GB300 (bf16, of 1885 TFLOP/s for a library product):
-// 32768 x 2560 -> 10576 forward 915 us (1.94 PFLOP/s, the tensor pipe 90 % active
-// in a capture), dx 923 us, dW 1020-1087 us; 1021 x 5120 -> 2560 into an fp32
+// 32768 x 2560 -> 10576 forward 915-943 us (1.94-1.88 PFLOP/s, the tensor pipe 93 %
+// active in a capture), dx 923-943 us, dW 997-1054 us; 1021 x 5120 -> 2560 into an fp32
 // residual 35 us, where 64 of 76 pairs hold one tile each and its last epilogue
 // has nothing to hide behind; 8 x 2560 -> 10576 10.3 us (5.3 TB/s of weight).
 // fp32, 4095 x 2048 -> 4384: forward 271 us, dx 298, dW 282 with the splitting
