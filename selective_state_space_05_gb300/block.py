@@ -654,7 +654,8 @@ def grad_norm(grads, *, workspace: Optional[torch.Tensor] = None, stream=None) -
     ws, ws_bytes, hold = _workspace(_call("ssd_clip_grads_workspace_bytes")(n), workspace, dev,
                                     stream)
     norm = _empty((), _F32, dev, stream)
-    _lib.check(_call("ssd_grad_norm")(_address(ptrs), _address(sizes), _address(codes), n, norm.data_ptr(), ws, ws_bytes, st))
+    _lib.check(_call("ssd_grad_norm")(
+        _address(ptrs), _address(sizes), _address(codes), n, norm.data_ptr(), ws, ws_bytes, st))
     return norm
 
 
