@@ -1005,7 +1005,7 @@ __global__ void __launch_bounds__(WARPS * 32)
   }
 }
 
-// fp32: a CTA takes four rows of W against up to 8 tokens, its warps steps of
+// fp32: a CTA takes four rows of W against 8 tokens, its warps steps of
 // 128 of K in turn (so that x is read once a CTA).  The 32 sums are folded over
 // the lanes: each halving keeps half of them in either half of the lanes, and
 // lane m * 4 + j ends up with token m, row j.  K a multiple of 4, rows 16-byte
@@ -1016,7 +1016,9 @@ __global__ void __launch_bounds__(kSkinnyThreads)
                       int64_t N, int K, const __grid_constant__ Epilogue e) {
   __shared__ float part[kSkinnyWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t n0 = (int64_t)blockIdx.x * kF32Rows;
+  const int64_t n0 = (int64_t)blockIdx.x * kF32Rows, m0 = (int64_t)blockIdx.y * 8;
+  x += m0 * sx;
+  M -= (int)m0;
   float acc[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) acc[i] = 0.f;
@@ -1055,9 +1057,8 @@ __global__ void __launch_bounds__(kSkinnyThreads)
   float v = 0.f;
 #pragma unroll
   for (int q = 0; q < kSkinnyWarps; ++q) v += part[q][lane];
-  const int m = lane >> 2;
-  const int64_t n = n0 + (lane & 3);
-  if (m >= M || n >= N) return;
+  const int64_t m = m0 + (lane >> 2), n = n0 + (lane & 3);
+  if ((lane >> 2) >= M || n >= N) return;
   if (e.bias) v += get1(e.bias, e.bias_t, n);
   if (e.pre) put1(e.pre, e.pre_t, m * N + n, v);
   v = act_f(e.act, v);
@@ -1330,19 +1331,27 @@ bool in_place(const void* p, int64_t ld, ssd_dtype_t dt) {
   return dt == SSD_DTYPE_BF16 && al(p, 16) && ld % 8 == 0 && ld < (1LL << 38);
 }
 
-// Rows for which the weight is streamed through registers.  Every CTA reads all
-// of x, so beyond 8 rows x has to be small (64 KB): 16 rows x 1024 -> 1024 take
-// 9 us here and 15 in the product kernel, 16 x 2560 -> 10576 take 26 and 23 (both
-// with 5 to 10 us of measuring around them).
-constexpr int kSkinnyBf16 = 32, kSkinnyF32 = 8;
-bool few_rows(int64_t rows, int K, ssd_dtype_t dt) {
-  if (dt == SSD_DTYPE_F32) return rows <= kSkinnyF32;
+// Whether the weight is streamed through registers.  bf16: every CTA reads all of
+// x, so beyond 8 rows x has to be small (64 KB): 16 rows x 1024 -> 1024 take 9 us
+// here and 15 in the product kernel, 16 x 2560 -> 10576 take 26 and 23.  fp32, whose
+// product kernel wants both operands split first: a pass over the weight for each
+// 8 rows, up to 24 rows (16 x 2560 -> 10576: 75 us instead of 112, 32 rows: 132 and
+// 112), or up to 128 where the passes are short, by the cost of their CTAs of four
+// outputs (64 x 1024 -> 1024: 22 and 24, 128 x 512 -> 352: 16 and 26, 96 x 1024 ->
+// 1024: 28 and 24; 1000 x 64 -> 64: 20 and 16).  (All with 5 to 10 us of measuring
+// around them.)
+constexpr int kSkinnyBf16 = 32, kSkinnyF32 = 24, kSkinnyMax = 128;
+bool few_rows(int64_t rows, int K, int64_t N, ssd_dtype_t dt) {
+  if (dt == SSD_DTYPE_F32)
+    return rows <= kSkinnyF32 || (rows <= kSkinnyMax &&
+                                  ((rows + 7) / 8) * ((N + 3) / 4) * (K + 512) <= 3000000);
   return rows <= 8 || (rows <= kSkinnyBf16 && rows * K <= 32768);
 }
 
-bool skinny(const void* x, int64_t sx, const void* w, int64_t rows, int K, ssd_dtype_t dt) {
+bool skinny(const void* x, int64_t sx, const void* w, int64_t rows, int K, int64_t N,
+            ssd_dtype_t dt) {
   const int unit = dt == SSD_DTYPE_BF16 ? 8 : 4;   // elements of a 16-byte load
-  return few_rows(rows, K, dt) && K % unit == 0 && al(x, 16) && al(w, 16) &&
+  return few_rows(rows, K, N, dt) && K % unit == 0 && al(x, 16) && al(w, 16) &&
          (rows == 1 || sx % unit == 0);
 }
 
@@ -1395,7 +1404,7 @@ size_t ssd_linear_fwd_workspace_bytes(int64_t rows, int in_features, int out_fea
                                       ssd_dtype_t dtype, int aligned) {
   if (check_sizes(rows, in_features, out_features, dtype) != SSD_OK) return 0;
   const bool odd = !aligned || in_features % 8 != 0;
-  if (!odd && few_rows(rows, in_features, dtype)) return 0;
+  if (!odd && few_rows(rows, in_features, out_features, dtype)) return 0;
   // (a strided x may be aligned while a weight of odd rows is not: the sum is enough for both)
   const bool pack = dtype == SSD_DTYPE_F32 || odd;
   return fwd_bytes(rows, in_features, out_features, dtype, pack, pack);
@@ -1440,7 +1449,7 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
             (!residual || wide4(residual, ep.res_ld, re));
   ep.wide8 = N % 8 == 0 && al(bias, 16) && al(out, 16) && al(pre, 16) &&
              (!residual || (al(residual, 16) && ep.res_ld % 8 == 0));
-  if (skinny(x, sx, weight, rows, in_features, dtype)) {
+  if (skinny(x, sx, weight, rows, in_features, N, dtype)) {
     if (dtype == SSD_DTYPE_BF16) {
       const auto* xb = static_cast<const __nv_bfloat16*>(x);
       const auto* wb = static_cast<const __nv_bfloat16*>(weight);
@@ -1462,7 +1471,7 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
       }
 #undef SSD_SKINNY
     } else {
-      const unsigned grid = (unsigned)((N + kF32Rows - 1) / kF32Rows);
+      const dim3 grid((unsigned)((N + kF32Rows - 1) / kF32Rows), (unsigned)((rows + 7) / 8));
       skinny_f32_kernel<<<grid, kSkinnyThreads, 0, st>>>(static_cast<const float*>(x), sx,
                                                          static_cast<const float*>(weight),
                                                          (int)rows, N, in_features, ep);

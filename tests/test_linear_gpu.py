@@ -39,6 +39,8 @@ CASES = [
     (300, 1, 5, BF, True, None, None), (257, 7, 130, F32, False, None, None),
     (130, 200, 300, F32, True, "silu", F32), (64, 4096, 24, BF, False, None, None),
     (2000, 72, 640, BF, False, None, F32), (333, 1030, 129, F32, True, "gelu", None),
+    (24, 2564, 101, F32, True, "silu", F32), (61, 1024, 1023, F32, True, "gelu", F32),
+    (1000, 68, 30, F32, False, None, F32), (700, 1024, 520, F32, True, "silu", None),
 ]
 
 
