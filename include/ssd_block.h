@@ -192,7 +192,10 @@ int ssd_clip_grads(const void *const *grads, const int64_t *sizes,
  *             it both activations are flat), for fp32 in fp32.
  * Sums in fp32 (bf16 products on the tensor cores; fp32 operands are split
  * into three bf16 parts each and their six leading products summed, about
- * fp32 accuracy).  SSD_ACT_GELU is v * Phi(v).
+ * fp32 accuracy for operands above 2^-110 in magnitude, whose third part is
+ * still a normal bf16; a result within 2^-7 of the largest fp32 value may
+ * come out infinite).  Infinities and NaN of an operand give the infinities and
+ * NaN of the product in IEEE arithmetic.  SSD_ACT_GELU is v * Phi(v).
  * Any sizes and element-aligned pointers; bf16 operands whose rows are not all
  * 16-byte aligned (x, weight: in_features or the stride not a multiple of 8)
  * and fp32 ones are first laid out in the workspace.

@@ -10,7 +10,9 @@
 // fp32 runs on the same kernel: each operand is split beforehand into three
 // bf16 planes hi + mid + lo, which hold its 24-bit significand exactly, and
 // the six products down to 2^-24 (hi hi, hi mid, mid hi, mid mid, hi lo,
-// lo hi) are more K steps of the same sum, the smallest first.
+// lo hi) are more K steps of the same sum, the smallest first.  Infinities and
+// NaN have no such planes: they are left out of them, and a launch that ends at
+// once where there was none puts their products into the results.
 //
 // The kernel is persistent.  A pair of CTAs on two SMs walks output tiles of
 // 256 x BN (cta_group::2: each SM reads half of B's tile, which the shared
@@ -799,15 +801,27 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Gemm 
 
 // ------------------------------------------------------- operands made ready
 
+// Which rows and columns of an fp32 operand hold an infinity or a NaN, a byte
+// each, and whether any does.
+struct Marks {
+  unsigned char* row;
+  unsigned char* col;
+  int* any;
+};
+
 // src (times act'(pre)) as bf16 planes [planes][R][ld] (planes 0: none), and
 // its column sums over this CTA's rows (colsum: [gridDim.y][C], or null).
-// Three planes hold an fp32 value exactly: each takes the next 8 bits of its
-// significand, rounded, the next one the remainder.
+// Three planes hold a finite fp32 value exactly (above 2^-110, whose third
+// plane is still normal): each takes the next 8 bits of its significand,
+// rounded, the next one the remainder; where rounding would overflow, 8 bits
+// towards zero each (24 in all: exact as well).
+// Infinities and NaN get zeros, and their row and column a mark.
 struct Prep {
   const void* src;
   const void* pre;
   __nv_bfloat16* out;
   float* colsum;
+  Marks marks;   // of three planes
   int64_t R, src_ld, ld, rows_per;
   int C;
   uint8_t src_t, pre_t, act, planes;
@@ -856,6 +870,14 @@ __device__ __forceinline__ void get8_any(const void* p, int t, const void* end, 
   }
 }
 
+// Whether one of eight values rounds to an infinity in bf16, or is not finite.
+__device__ __forceinline__ bool beyond_bf16(const float (&v)[8]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  return most >= 0x7F7F8000u;
+}
+
 // Eight consecutive columns a thread; ANY: rows of any alignment and length.
 template <bool ANY>
 __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep p) {
@@ -896,12 +918,30 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
       if (rb + i >= r1) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[i][j];
+      const bool beyond = p.planes == 3 && beyond_bf16(v[i]);
+      if (beyond) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (isfinite(v[i][j])) continue;
+          v[i][j] = 0.f;
+          if (j < left) {   // (every writer writes the same)
+            p.marks.row[rb + i] = 1;
+            p.marks.col[c + j] = 1;
+            *p.marks.any = 1;
+          }
+        }
+      }
       __nv_bfloat16* o = p.out + (rb + i) * p.ld + c;   // (ld is a multiple of 8: the pad may be written)
       for (int k = 0; k < p.planes; ++k) {
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          u[j] = tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1]);
+          float a = v[i][2 * j], b = v[i][2 * j + 1];
+          if (beyond) {   // towards zero: no sum of the planes is beyond the value
+            a = __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
+            b = __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
+          }
+          u[j] = tc::pack_bf16x2(a, b);
           v[i][2 * j] -= __uint_as_float(u[j] << 16);
           v[i][2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
         }
@@ -914,6 +954,97 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < left) p.colsum[(int64_t)blockIdx.y * p.C + c + j] = sum[j];
+  }
+}
+
+// A side of an fp32 product D[m,n] = sum_k A[m,k] B[n,k] as it was given: element
+// (r, k) is src[r * ld + k], or src[k * ld + r] (mn), times act'(pre) of the same
+// place (rows of pre are pre_ld apart).  mark: its rows with infinities or NaN.
+struct Given {
+  const float* src;
+  const float* pre;
+  const unsigned char* mark;
+  int64_t ld, pre_ld;
+  uint8_t act;
+  bool mn;
+  __device__ __forceinline__ float at(int64_t r, int64_t k) const {
+    const float v = src[mn ? k * ld + r : r * ld + k];
+    return pre ? v * dact_f(act, pre[mn ? k * pre_ld + r : r * pre_ld + k]) : v;
+  }
+};
+struct NonFinite {
+  Given a, b;
+  int64_t M, N, K;
+  const int* any;
+  Epilogue e;
+};
+
+// The results that infinities and NaN of the operands enter (D's rows and columns
+// of marked rows of A and B).  Such a result is an infinity or NaN, whatever the
+// finite terms are, so only the terms with an operand that is not finite are
+// summed; a chunk of K without any costs its loads.  Then the epilogue as in the
+// product kernel, whose result, of the finite terms, stands in `out`: where that
+// was the residual's memory it is taken for the residual, from which it differs
+// by a finite value.  A tile of 32 x 32 results a CTA at a time, four a thread.
+// Nothing marked: 2 us.
+constexpr int kFixTile = 32;
+__global__ void __launch_bounds__(256) nonfinite_kernel(const __grid_constant__ NonFinite p) {
+  if (*p.any == 0) return;
+  __shared__ float sa[kFixTile][kFixTile + 1], sb[kFixTile][kFixTile + 1];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t tiles_n = (p.N + kFixTile - 1) / kFixTile;
+  const int64_t tiles = (p.M + kFixTile - 1) / kFixTile * tiles_n;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t m0 = t / tiles_n * kFixTile, n0 = t % tiles_n * kFixTile;
+    const int64_t n = n0 + tx;
+    const bool col = n < p.N && p.b.mark[n];
+    bool mine[4], open = false;   // results of this thread that are marked
+    float acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + ty + 8 * i;
+      mine[i] = m < p.M && n < p.N && (col || p.a.mark[m]);
+      open |= mine[i];
+      acc[i] = 0.f;
+    }
+    // a NaN stays one: once every marked result is NaN the tile is done
+    for (int64_t k0 = 0; __syncthreads_or(open) && k0 < p.K; k0 += kFixTile) {
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // consecutive threads, consecutive addresses
+        const int y = ty + 8 * i;
+        const int ra = p.a.mn ? tx : y, ka = p.a.mn ? y : tx;
+        const int rb = p.b.mn ? tx : y, kb = p.b.mn ? y : tx;
+        const float a = m0 + ra < p.M && k0 + ka < p.K ? p.a.at(m0 + ra, k0 + ka) : 0.f;
+        const float b = n0 + rb < p.N && k0 + kb < p.K ? p.b.at(n0 + rb, k0 + kb) : 0.f;
+        found |= !isfinite(a) || !isfinite(b);
+        sa[ra][ka] = a;
+        sb[rb][kb] = b;
+      }
+      if (!__syncthreads_or(found)) continue;
+      open = false;
+      for (int k = 0; k < kFixTile && k0 + k < p.K; ++k) {
+        const float b = sb[tx][k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = sa[ty + 8 * i][k];
+          if (!isfinite(a) || !isfinite(b)) acc[i] += a * b;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) open |= mine[i] && !isnan(acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + ty + 8 * i;
+      if (!mine[i] || isfinite(acc[i])) continue;
+      float v = acc[i];
+      if (p.e.bias) v += get1(p.e.bias, p.e.bias_t, n);
+      if (p.e.pre) put1(p.e.pre, p.e.pre_t, m * p.N + n, v);
+      v = act_f(p.e.act, v);
+      if (p.e.res) v += get1(p.e.res, p.e.res_t, m * p.e.res_ld + n);
+      put1(p.e.out, p.e.out_t, m * p.e.out_ld + n, v);
+    }
   }
 }
 
@@ -1289,8 +1420,10 @@ size_t planes_bytes(int64_t R, int64_t C, int planes) {
 
 // src as operand planes at `out`; column sums to colsum if not null.
 cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const void* pre, int pre_t,
-                 int act, int planes, void* out, float* colsum, cudaStream_t st) {
+                 int act, int planes, void* out, float* colsum, const Marks& marks,
+                 cudaStream_t st) {
   Prep p = {};
+  p.marks = marks;
   p.src = src;
   p.pre = pre;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -1312,6 +1445,17 @@ cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const
     prep_kernel<true><<<grid, 128, 0, st>>>(p);
   return cudaGetLastError();
 }
+
+// Puts what infinities and NaN of fp32 operands contribute into a product's results.
+cudaError_t fix_nonfinite(const Given& a, const Given& b, int64_t M, int64_t N, int64_t K,
+                          const int* any, const Epilogue& e, cudaStream_t st) {
+  const NonFinite p = {a, b, M, N, K, any, e};
+  const int64_t tiles = ((M + kFixTile - 1) / kFixTile) * ((N + kFixTile - 1) / kFixTile);
+  nonfinite_kernel<<<(unsigned)std::min<int64_t>(tiles, row::sm_count() * 2), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+// The marks of fp32 operands: `any`, then those of each operand's rows and columns.
+size_t marks_bytes(int64_t n) { return up256(sizeof(int) + (size_t)n); }
 
 int check_sizes(int64_t rows, int in_f, int out_f, ssd_dtype_t dt) {
   if (dt != SSD_DTYPE_F32 && dt != SSD_DTYPE_BF16) return bad(SSD_ERR_ARG, "unknown dtype");
@@ -1363,6 +1507,7 @@ size_t fwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool p
   size_t b = up256(plan_for(rows, N, K, planes == 3 ? 6 : 1, false).partial_bytes());
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
+  if (planes == 3) b += marks_bytes(rows + N + 2 * (int64_t)K);
   return b;
 }
 size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w, bool pack_d) {
@@ -1373,6 +1518,7 @@ size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool p
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
   if (pack_d) b += planes_bytes(rows, N, planes);
+  if (planes == 3) b += marks_bytes(2 * ((int64_t)rows + N + K));
   return b;
 }
 
@@ -1487,21 +1633,37 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
   const int planes = dtype == SSD_DTYPE_F32 ? 3 : 1;
   char* ws = static_cast<char*>(workspace);
   Operand a = {x, rows, K, sx, 1}, b = {weight, N, K, K, 1};
+  Marks mx = {}, mw = {};
+  if (planes == 3) {   // x's rows and columns, the weight's
+    const size_t bytes = marks_bytes(rows + N + 2 * K);
+    const cudaError_t err = cudaMemsetAsync(ws, 0, bytes, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear marks");
+    int* any = reinterpret_cast<int*>(ws);
+    auto* m = reinterpret_cast<unsigned char*>(any + 1);
+    mx = {m, m + rows, any};
+    mw = {m + rows + K, m + rows + K + N, any};
+    ws += bytes;
+  }
   if (pack_x) {
     const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
-                                 nullptr, st);
+                                 nullptr, mx, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     a = {ws, rows, K, padded(K), planes};
     ws += planes_bytes(rows, K, planes);
   }
   if (pack_w) {
     const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
-                                 ws, nullptr, st);
+                                 ws, nullptr, mw, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     b = {ws, N, K, padded(K), planes};
     ws += planes_bytes(N, K, planes);
   }
-  return gemm(a, false, b, false, rows, N, K, ep, reinterpret_cast<float*>(ws), st);
+  const int r = gemm(a, false, b, false, rows, N, K, ep, reinterpret_cast<float*>(ws), st);
+  if (r != SSD_OK || planes != 3) return r;
+  const Given gx = {static_cast<const float*>(x), nullptr, mx.row, sx, 0, 0, false};
+  const Given gw = {static_cast<const float*>(weight), nullptr, mw.row, K, 0, 0, false};
+  const cudaError_t err = fix_nonfinite(gx, gw, rows, N, K, mx.any, ep, st);
+  return err == cudaSuccess ? SSD_OK : cuda_bad(err, "linear launch");
 }
 
 size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int in_features, int out_features,
@@ -1549,11 +1711,23 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   float* colsum = reinterpret_cast<float*>(ws);
   ws += up256((size_t)prep_parts(rows, out_features) * N * sizeof(float));
   Operand d = {dout, rows, N, N, 1}, w = {weight, N, K, K, 1}, xo = {x, rows, K, sx, 1};
+  Marks md = {}, mw = {}, mx = {};
+  if (planes == 3) {   // rows and columns of dpre, of the weight and of x
+    const size_t bytes = marks_bytes(2 * (rows + N + K));
+    const cudaError_t err = cudaMemsetAsync(ws, 0, bytes, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear marks");
+    int* any = reinterpret_cast<int*>(ws);
+    auto* m = reinterpret_cast<unsigned char*>(any + 1);
+    md = {m, m + rows, any};
+    mw = {m + rows + N, m + rows + 2 * N, any};
+    mx = {m + rows + 2 * N + K, m + 2 * rows + 2 * N + K, any};
+    ws += bytes;
+  }
   if (pack_d || dbias) {
     const cudaError_t err =
         prep(dout, type_of(dout_dtype), N, rows, out_features, act ? pre : nullptr,
              dtype == SSD_DTYPE_BF16 ? kF16 : kF32, activation, pack_d ? planes : 0, ws,
-             dbias ? colsum : nullptr, st);
+             dbias ? colsum : nullptr, md, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     if (pack_d) {
       d = {ws, rows, N, padded(N), planes};
@@ -1568,14 +1742,14 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   }
   if (pack_w) {
     const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
-                                 ws, nullptr, st);
+                                 ws, nullptr, mw, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     w = {ws, N, K, padded(K), planes};
     ws += planes_bytes(N, K, planes);
   }
   if (pack_x) {
     const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
-                                 nullptr, st);
+                                 nullptr, mx, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     xo = {ws, rows, K, padded(K), planes};
     ws += planes_bytes(rows, K, planes);
@@ -1584,18 +1758,32 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   ep.out_t = (uint8_t)type_of(dtype);
   ep.out_ld = K;
   float* part = reinterpret_cast<float*>(ws);
+  const float* dpre = act ? static_cast<const float*>(pre) : nullptr;   // (used for fp32)
   if (dx) {
     ep.out = dx;
     ep.wide = K % 4 == 0 && al(dx, 4 * e);
     ep.wide8 = K % 8 == 0 && al(dx, 16);
     const int r = gemm(d, false, w, true, rows, K, N, ep, part, st);
     if (r != SSD_OK) return r;
+    if (planes == 3) {
+      const Given gd = {static_cast<const float*>(dout), dpre, md.row, N, N, (uint8_t)activation, false};
+      const Given gw = {static_cast<const float*>(weight), nullptr, mw.col, K, 0, 0, true};
+      const cudaError_t err = fix_nonfinite(gd, gw, rows, K, N, md.any, ep, st);
+      if (err != cudaSuccess) return cuda_bad(err, "linear launch");
+    }
   }
   if (dweight) {
     ep.out = dweight;
     ep.wide = K % 4 == 0 && al(dweight, 4 * e);
     ep.wide8 = K % 8 == 0 && al(dweight, 16);
-    return gemm(d, true, xo, true, N, K, rows, ep, part, st);
+    const int r = gemm(d, true, xo, true, N, K, rows, ep, part, st);
+    if (r != SSD_OK) return r;
+    if (planes == 3) {
+      const Given gd = {static_cast<const float*>(dout), dpre, md.col, N, N, (uint8_t)activation, true};
+      const Given gx = {static_cast<const float*>(x), nullptr, mx.col, sx, 0, 0, true};
+      const cudaError_t err = fix_nonfinite(gd, gx, N, K, rows, md.any, ep, st);
+      if (err != cudaSuccess) return cuda_bad(err, "linear launch");
+    }
   }
   return SSD_OK;
 }
