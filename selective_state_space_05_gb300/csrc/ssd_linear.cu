@@ -548,11 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       }
       // every MMA has finished before the operands' memory and TMEM are given back
       commit(&s.drain);
+      wait_drain(&s.drain, 0);
+      __syncwarp();
     }
-    // (in a pair the leader's commits arrive at the peer's barriers too: its
-    // memory stays until the last of them has)
-    wait_drain(&s.drain, 0);
-    __syncwarp();
   } else {
     // a quarter of the TMEM lanes and every other 32 columns
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -769,6 +767,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
     }
   }
   __syncthreads();
+  if (CG == 2 && rank == 1 && warp == 1) {
+    // the leader's commits arrive at the peer's barriers too: its memory stays
+    // until the last of them has.  This CTA's other warps are done, so its last
+    // tile is: what is left of the leader's work is short, and so is the wait,
+    // however long the launch was.
+    wait_drain(&s.drain, 0);
+    __syncwarp();
+  }
   tc::fence_after_sync();
   if constexpr (CG == 2) {
     tc::cluster_sync();   // nothing of the peer's is needed or written any more
