@@ -63,6 +63,12 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0: TMA, 1: MMA, then the
 // grows with their number (relative 3.9e-6 after 320 MMAs, K = 5120, measured);
 // sums of 64 MMAs are added up in registers, to nearest, instead.
 constexpr int kExactSteps = 16;
+// Where it is rounded to bf16 afterwards an accumulator takes more: an MMA loses
+// less than 2^-23 of the running sum, which for terms of one sign is half of the
+// total on average, so 1024 MMAs lose at most 2^-14, a 32nd of the least half step
+// of bf16.  (Summed in one accumulator, a dW over 2^24 tokens of one sign was
+// 0.8 % short.)
+constexpr int kBf16Steps = 256;
 constexpr unsigned long long kWaitNs = 2000000000ull;   // limit of any single wait: 2 s
 constexpr uint32_t kSleepNs = 20000;
 
@@ -403,8 +409,8 @@ __device__ __forceinline__ Item item_of(const Gemm& p, int item, int all_steps) 
 // A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
 // leader's `full`; the leader issues the MMAs and signals `empty` and `tfull`
 // of both; both CTAs' epilogues arrive on the leader's `tempty`.
-// EXACT: sums in runs of p.run K steps (fp32 results); PLAIN: no bias, pre,
-// activation or residual.  Apart, because one kernel with all of it was 150 KB
+// EXACT: sums in runs of p.run K steps (fp32 results, long sums); PLAIN: no bias,
+// pre, activation or residual.  Apart, because one kernel with all of it was 150 KB
 // of code and spilled.
 template <int CG, bool AMN, bool BMN, bool EXACT, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
@@ -1377,10 +1383,16 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.bn = pl.bn;
   g.stages = std::min(kMaxStages, kOperandBytes / (kStageA + stage_b(pl.cg, pl.bn, bmn)));
   g.group_m = 8 / pl.cg;
+  // runs of the longest item's K steps
+  const int longest = pl.full > 0 ? g.kblocks * pairs : pl.steps_per;
+  const bool exact = e.out_t == kF32 || longest > kBf16Steps;
   g.run = kExactSteps;
+  if (e.out_t != kF32) {   // as even as they can be
+    const int runs = (longest + kBf16Steps - 1) / kBf16Steps;
+    g.run = (longest + runs - 1) / runs;
+  }
   g.partial = part;
   g.e = e;
-  const bool exact = e.out_t == kF32;
   const bool plain = !e.bias && !e.pre && !e.res && e.act == kActNone;
   cudaError_t err;
   // (the backward's products are plain)
