@@ -464,8 +464,8 @@ bool wide_stride(const ssd_stride_t& s, size_t e) {
 
 }  // namespace norm
 
-cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
-                              int64_t n2, float* out2, cudaStream_t st) {
+void launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
+                       int64_t n2, float* out2, cudaStream_t st) {
   // many rows: more of them at once (1024 rows of 1280 columns: 22 us with 8
   // warps, whose loads wait for one another)
   const unsigned grid = (unsigned)((n + n2 + 31) / 32);
@@ -473,7 +473,6 @@ cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64
     norm::column_sum_kernel<32><<<grid, 1024, 0, st>>>(part, rows, ld, n, out, n2, out2);
   else
     norm::column_sum_kernel<8><<<grid, 256, 0, st>>>(part, rows, ld, n, out, n2, out2);
-  return cudaGetLastError();
 }
 
 }  // namespace ssd

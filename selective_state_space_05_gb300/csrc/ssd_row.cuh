@@ -211,8 +211,9 @@ int sm_count();
 }  // namespace row
 
 // Column sums in a fixed order: s[c] = sum over r < rows of part[r * ld + c] for
-// c < n + n2; the first n go to out, the next n2 to out2.
-cudaError_t launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
-                              int64_t n2, float* out2, cudaStream_t st);
+// c < n + n2; the first n go to out, the next n2 to out2.  Its launch error and
+// those before it are left to the caller's cudaGetLastError.
+void launch_column_sum(const float* part, int64_t rows, int64_t ld, int64_t n, float* out,
+                       int64_t n2, float* out2, cudaStream_t st);
 
 }  // namespace ssd
