@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1)   // (one slot: 6
       for (int j = 0; j < kVec; ++j) {
         const float sg = MODE != kNoGate ? row::sigmoid_f(zv[j]) : 1.f;
         const float e = MODE != kNoGate ? zv[j] * sg : 1.f;
-        const float de = MODE != kNoGate ? fmaf(sg, 1.f - e, e) : 0.f;   // e = z sg
+        // silu' = sg + z sg (1 - sg); not sg (1 - e) + e, which cancels for large z
+        const float de = MODE != kNoGate ? fmaf(e, 1.f - sg, sg) : 0.f;
         const float gw = go[j] * w[j];
         if constexpr (MODE == kNormFirst) {
           const float n = yv[j] * rstd;
