@@ -813,27 +813,19 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Gemm 
 
 // ------------------------------------------------------- operands made ready
 
-// Which rows and columns of an fp32 operand hold an infinity or a NaN, a byte
-// each, and whether any does.
-struct Marks {
-  unsigned char* row;
-  unsigned char* col;
-  int* any;
-};
-
 // src (times act'(pre)) as bf16 planes [planes][R][ld] (planes 0: none), and
 // its column sums over this CTA's rows (colsum: [gridDim.y][C], or null).
 // Three planes hold a finite fp32 value exactly (above 2^-110, whose third
 // plane is still normal): each takes the next 8 bits of its significand,
 // rounded, the next one the remainder; where rounding would overflow, 8 bits
 // towards zero each (24 in all: exact as well).
-// Infinities and NaN get zeros, and their row and column a mark.
+// Infinities and NaN get zeros, and flags tell which CTAs met one.
 struct Prep {
   const void* src;
   const void* pre;
   __nv_bfloat16* out;
   float* colsum;
-  Marks marks;   // of three planes
+  int* flags;   // of three planes: [gridDim.y][gridDim.x]
   int64_t R, src_ld, ld, rows_per;
   int C;
   uint8_t src_t, pre_t, act, planes;
@@ -882,20 +874,26 @@ __device__ __forceinline__ void get8_any(const void* p, int t, const void* end, 
   }
 }
 
-// Whether one of eight values rounds to an infinity in bf16, or is not finite.
-__device__ __forceinline__ bool beyond_bf16(const float (&v)[8]) {
+// Two values to bf16 towards zero (of a value near the end of the range: no sum of
+// its planes is beyond it).
+__device__ __forceinline__ uint32_t chopped(float a, float b) {
+  return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+}
+// Whether one of eight packed bf16 is an infinity or a NaN.
+__device__ __forceinline__ bool beyond(const uint32_t (&u)[4]) {
   uint32_t most = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return most >= 0x7F7F8000u;
+  for (int j = 0; j < 4; ++j) most = __vmaxu2(most, u[j] & 0x7FFF7FFFu);
+  return (most & 0xFFFFu) >= 0x7F80u || most >= 0x7F800000u;
 }
 
 // Eight consecutive columns a thread; ANY: rows of any alignment and length.
 template <bool ANY>
 __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep p) {
   const int c = (blockIdx.x * 128 + threadIdx.x) * 8;
-  if (c >= p.C) return;
-  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per, r1 = min(r0 + p.rows_per, p.R);
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per;
+  const int64_t r1 = c < p.C ? min(r0 + p.rows_per, p.R) : r0;   // past the row: nothing
+  bool met = false;   // an infinity or NaN
   const int se = p.src_t == kF32 ? 4 : 2, pe = p.pre_t == kF32 ? 4 : 2;
   const int left = p.C - c;
   float sum[8];
@@ -930,30 +928,28 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
       if (rb + i >= r1) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[i][j];
-      const bool beyond = p.planes == 3 && beyond_bf16(v[i]);
-      if (beyond) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (isfinite(v[i][j])) continue;
-          v[i][j] = 0.f;
-          if (j < left) {   // (every writer writes the same)
-            p.marks.row[rb + i] = 1;
-            p.marks.col[c + j] = 1;
-            *p.marks.any = 1;
-          }
-        }
-      }
+      bool chop = false;
       __nv_bfloat16* o = p.out + (rb + i) * p.ld + c;   // (ld is a multiple of 8: the pad may be written)
       for (int k = 0; k < p.planes; ++k) {
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float a = v[i][2 * j], b = v[i][2 * j + 1];
-          if (beyond) {   // towards zero: no sum of the planes is beyond the value
-            a = __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
-            b = __uint_as_float(__float_as_uint(b) & 0xFFFF0000u);
-          }
-          u[j] = tc::pack_bf16x2(a, b);
+          if (!chop) u[j] = tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1]);
+          else u[j] = chopped(v[i][2 * j], v[i][2 * j + 1]);
+        }
+        if (k == 0 && p.planes == 3 && beyond(u)) {
+          chop = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!isfinite(v[i][j])) {
+              v[i][j] = 0.f;
+              met |= j < left;
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = chopped(v[i][2 * j], v[i][2 * j + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
           v[i][2 * j] -= __uint_as_float(u[j] << 16);
           v[i][2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
         }
@@ -967,41 +963,65 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
     for (int j = 0; j < 8; ++j)
       if (j < left) p.colsum[(int64_t)blockIdx.y * p.C + c + j] = sum[j];
   }
+  if (p.flags) {
+    met = __syncthreads_or(met);
+    if (threadIdx.x == 0) p.flags[blockIdx.y * gridDim.x + blockIdx.x] = met;
+  }
 }
 
 // A side of an fp32 product D[m,n] = sum_k A[m,k] B[n,k] as it was given: element
 // (r, k) is src[r * ld + k], or src[k * ld + r] (mn), times act'(pre) of the same
-// place (rows of pre are pre_ld apart).  mark: its rows with infinities or NaN.
+// place (rows of pre are pre_ld apart).  flags: of prep_kernel's blocks, flags_y of
+// rows_per rows by flags_x of 1024 columns of src, which hold infinities or NaN.
 struct Given {
   const float* src;
   const float* pre;
-  const unsigned char* mark;
-  int64_t ld, pre_ld;
+  const int* flags;
+  int64_t ld, pre_ld, rows_per;
+  int flags_x, flags_y;
   uint8_t act;
   bool mn;
   __device__ __forceinline__ float at(int64_t r, int64_t k) const {
     const float v = src[mn ? k * ld + r : r * ld + k];
     return pre ? v * dact_f(act, pre[mn ? k * pre_ld + r : r * pre_ld + k]) : v;
   }
+  // This thread's share of: whether a block is flagged, of all or of those that
+  // rows r0 .. r0 + n - 1 of this side lie in.
+  __device__ __forceinline__ bool flagged() const {
+    bool f = false;
+    for (int i = threadIdx.x; i < flags_x * flags_y; i += blockDim.x) f |= flags[i] != 0;
+    return f;
+  }
+  __device__ __forceinline__ bool flagged(int64_t r0, int n) const {
+    const int64_t per = mn ? 1024 : rows_per;
+    const int across = mn ? flags_y : flags_x, blocks = mn ? flags_x : flags_y;
+    const int b0 = (int)(r0 / per), b1 = min((int)((r0 + n - 1) / per), blocks - 1);
+    bool f = false;
+    for (int b = b0; b <= b1; ++b)
+      for (int i = threadIdx.x; i < across; i += blockDim.x)
+        f |= flags[mn ? i * flags_x + b : b * flags_x + i] != 0;
+    return f;
+  }
 };
 struct NonFinite {
   Given a, b;
   int64_t M, N, K;
-  const int* any;
   Epilogue e;
 };
 
-// The results that infinities and NaN of the operands enter (D's rows and columns
-// of marked rows of A and B).  Such a result is an infinity or NaN, whatever the
-// finite terms are, so only the terms with an operand that is not finite are
-// summed; a chunk of K without any costs its loads.  Then the epilogue as in the
-// product kernel, whose result, of the finite terms, stands in `out`: where that
-// was the residual's memory it is taken for the residual, from which it differs
-// by a finite value.  A tile of 32 x 32 results a CTA at a time, four a thread.
-// Nothing marked: 2 us.
+// The results that infinities and NaN of the operands enter.  Such a result is an
+// infinity or NaN, whatever the finite terms are, so only the terms with an operand
+// that is not finite are summed; a chunk of K without any costs its loads.  Then the
+// epilogue as in the product kernel, whose result, of the finite terms, stands in
+// `out`: where that was the residual's memory it is taken for the residual, from
+// which it differs by a finite value.  A tile of 32 x 32 results a CTA at a time,
+// four a thread; blockIdx.y: the product.  Where nothing is flagged it ends at once.
 constexpr int kFixTile = 32;
-__global__ void __launch_bounds__(256) nonfinite_kernel(const __grid_constant__ NonFinite p) {
-  if (*p.any == 0) return;
+__global__ void __launch_bounds__(256)
+    nonfinite_kernel(const __grid_constant__ NonFinite p0, const __grid_constant__ NonFinite p1) {
+  const NonFinite& p = blockIdx.y == 0 ? p0 : p1;
+  const bool some = p.a.flagged() | p.b.flagged();
+  if (!__syncthreads_or(some)) return;
   __shared__ float sa[kFixTile][kFixTile + 1], sb[kFixTile][kFixTile + 1];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int64_t tiles_n = (p.N + kFixTile - 1) / kFixTile;
@@ -1009,17 +1029,10 @@ __global__ void __launch_bounds__(256) nonfinite_kernel(const __grid_constant__ 
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t m0 = t / tiles_n * kFixTile, n0 = t % tiles_n * kFixTile;
     const int64_t n = n0 + tx;
-    const bool col = n < p.N && p.b.mark[n];
-    bool mine[4], open = false;   // results of this thread that are marked
-    float acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + ty + 8 * i;
-      mine[i] = m < p.M && n < p.N && (col || p.a.mark[m]);
-      open |= mine[i];
-      acc[i] = 0.f;
-    }
-    // a NaN stays one: once every marked result is NaN the tile is done
+    const bool here = p.a.flagged(m0, kFixTile) | p.b.flagged(n0, kFixTile);
+    if (!__syncthreads_or(here)) continue;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    bool open = true;   // (a NaN stays one: a tile of them is done)
     for (int64_t k0 = 0; __syncthreads_or(open) && k0 < p.K; k0 += kFixTile) {
       bool found = false;
 #pragma unroll
@@ -1034,7 +1047,6 @@ __global__ void __launch_bounds__(256) nonfinite_kernel(const __grid_constant__ 
         sb[rb][kb] = b;
       }
       if (!__syncthreads_or(found)) continue;
-      open = false;
       for (int k = 0; k < kFixTile && k0 + k < p.K; ++k) {
         const float b = sb[tx][k];
 #pragma unroll
@@ -1043,13 +1055,14 @@ __global__ void __launch_bounds__(256) nonfinite_kernel(const __grid_constant__ 
           if (!isfinite(a) || !isfinite(b)) acc[i] += a * b;
         }
       }
+      open = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) open |= mine[i] && !isnan(acc[i]);
+      for (int i = 0; i < 4; ++i) open |= m0 + ty + 8 * i < p.M && n < p.N && !isnan(acc[i]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t m = m0 + ty + 8 * i;
-      if (!mine[i] || isfinite(acc[i])) continue;
+      if (m >= p.M || n >= p.N || isfinite(acc[i])) continue;
       float v = acc[i];
       if (p.e.bias) v += get1(p.e.bias, p.e.bias_t, n);
       if (p.e.pre) put1(p.e.pre, p.e.pre_t, m * p.N + n, v);
@@ -1438,10 +1451,9 @@ size_t planes_bytes(int64_t R, int64_t C, int planes) {
 
 // src as operand planes at `out`; column sums to colsum if not null.
 cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const void* pre, int pre_t,
-                 int act, int planes, void* out, float* colsum, const Marks& marks,
-                 cudaStream_t st) {
+                 int act, int planes, void* out, float* colsum, int* flags, cudaStream_t st) {
   Prep p = {};
-  p.marks = marks;
+  p.flags = planes == 3 ? flags : nullptr;
   p.src = src;
   p.pre = pre;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -1464,16 +1476,33 @@ cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const
   return cudaGetLastError();
 }
 
-// Puts what infinities and NaN of fp32 operands contribute into a product's results.
-cudaError_t fix_nonfinite(const Given& a, const Given& b, int64_t M, int64_t N, int64_t K,
-                          const int* any, const Epilogue& e, cudaStream_t st) {
-  const NonFinite p = {a, b, M, N, K, any, e};
-  const int64_t tiles = ((M + kFixTile - 1) / kFixTile) * ((N + kFixTile - 1) / kFixTile);
-  nonfinite_kernel<<<(unsigned)std::min<int64_t>(tiles, row::sm_count() * 2), 256, 0, st>>>(p);
+// The flags of an fp32 operand's prep_kernel blocks.
+size_t flags_bytes(int64_t R, int64_t C) {
+  return up256(sizeof(int) * (size_t)prep_parts(R, (int)C) * ((C + 1023) / 1024));
+}
+// An operand of R rows of C for nonfinite_kernel.
+Given given(const void* src, int64_t R, int64_t C, int64_t ld, const int* flags, bool mn) {
+  Given g = {};
+  g.src = static_cast<const float*>(src);
+  g.flags = flags;
+  g.ld = ld;
+  g.rows_per = prep_rows_per(R, (int)C);
+  g.flags_x = (int)((C + 1023) / 1024);
+  g.flags_y = (int)prep_parts(R, (int)C);
+  g.mn = mn;
+  return g;
+}
+// Puts what infinities and NaN of fp32 operands contribute into the results of one
+// product or two.
+cudaError_t fix_nonfinite(const NonFinite* p, int products, cudaStream_t st) {
+  int64_t tiles = 0;
+  for (int i = 0; i < products; ++i)
+    tiles = std::max(tiles, ((p[i].M + kFixTile - 1) / kFixTile) *
+                                ((p[i].N + kFixTile - 1) / kFixTile));
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, row::sm_count()), (unsigned)products);
+  nonfinite_kernel<<<grid, 256, 0, st>>>(p[0], p[products - 1]);
   return cudaGetLastError();
 }
-// The marks of fp32 operands: `any`, then those of each operand's rows and columns.
-size_t marks_bytes(int64_t n) { return up256(sizeof(int) + (size_t)n); }
 
 int check_sizes(int64_t rows, int in_f, int out_f, ssd_dtype_t dt) {
   if (dt != SSD_DTYPE_F32 && dt != SSD_DTYPE_BF16) return bad(SSD_ERR_ARG, "unknown dtype");
@@ -1525,7 +1554,7 @@ size_t fwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool p
   size_t b = up256(plan_for(rows, N, K, planes == 3 ? 6 : 1, false).partial_bytes());
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
-  if (planes == 3) b += marks_bytes(rows + N + 2 * (int64_t)K);
+  if (planes == 3) b += flags_bytes(rows, K) + flags_bytes(N, K);
   return b;
 }
 size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool pack_w, bool pack_d) {
@@ -1536,7 +1565,7 @@ size_t bwd_bytes(int64_t rows, int K, int N, ssd_dtype_t dt, bool pack_x, bool p
   if (pack_x) b += planes_bytes(rows, K, planes);
   if (pack_w) b += planes_bytes(N, K, planes);
   if (pack_d) b += planes_bytes(rows, N, planes);
-  if (planes == 3) b += marks_bytes(2 * ((int64_t)rows + N + K));
+  if (planes == 3) b += flags_bytes(rows, N) + flags_bytes(N, K) + flags_bytes(rows, K);
   return b;
 }
 
@@ -1651,36 +1680,32 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
   const int planes = dtype == SSD_DTYPE_F32 ? 3 : 1;
   char* ws = static_cast<char*>(workspace);
   Operand a = {x, rows, K, sx, 1}, b = {weight, N, K, K, 1};
-  Marks mx = {}, mw = {};
-  if (planes == 3) {   // x's rows and columns, the weight's
-    const size_t bytes = marks_bytes(rows + N + 2 * K);
-    const cudaError_t err = cudaMemsetAsync(ws, 0, bytes, st);
-    if (err != cudaSuccess) return cuda_bad(err, "linear marks");
-    int* any = reinterpret_cast<int*>(ws);
-    auto* m = reinterpret_cast<unsigned char*>(any + 1);
-    mx = {m, m + rows, any};
-    mw = {m + rows + K, m + rows + K + N, any};
-    ws += bytes;
+  int *fx = nullptr, *fw = nullptr;
+  if (planes == 3) {
+    fx = reinterpret_cast<int*>(ws);
+    ws += flags_bytes(rows, K);
+    fw = reinterpret_cast<int*>(ws);
+    ws += flags_bytes(N, K);
   }
   if (pack_x) {
     const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
-                                 nullptr, mx, st);
+                                 nullptr, fx, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     a = {ws, rows, K, padded(K), planes};
     ws += planes_bytes(rows, K, planes);
   }
   if (pack_w) {
     const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
-                                 ws, nullptr, mw, st);
+                                 ws, nullptr, fw, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     b = {ws, N, K, padded(K), planes};
     ws += planes_bytes(N, K, planes);
   }
   const int r = gemm(a, false, b, false, rows, N, K, ep, reinterpret_cast<float*>(ws), st);
   if (r != SSD_OK || planes != 3) return r;
-  const Given gx = {static_cast<const float*>(x), nullptr, mx.row, sx, 0, 0, false};
-  const Given gw = {static_cast<const float*>(weight), nullptr, mw.row, K, 0, 0, false};
-  const cudaError_t err = fix_nonfinite(gx, gw, rows, N, K, mx.any, ep, st);
+  const NonFinite fix = {given(x, rows, K, sx, fx, false), given(weight, N, K, K, fw, false),
+                         rows, N, K, ep};
+  const cudaError_t err = fix_nonfinite(&fix, 1, st);
   return err == cudaSuccess ? SSD_OK : cuda_bad(err, "linear launch");
 }
 
@@ -1729,23 +1754,20 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   float* colsum = reinterpret_cast<float*>(ws);
   ws += up256((size_t)prep_parts(rows, out_features) * N * sizeof(float));
   Operand d = {dout, rows, N, N, 1}, w = {weight, N, K, K, 1}, xo = {x, rows, K, sx, 1};
-  Marks md = {}, mw = {}, mx = {};
-  if (planes == 3) {   // rows and columns of dpre, of the weight and of x
-    const size_t bytes = marks_bytes(2 * (rows + N + K));
-    const cudaError_t err = cudaMemsetAsync(ws, 0, bytes, st);
-    if (err != cudaSuccess) return cuda_bad(err, "linear marks");
-    int* any = reinterpret_cast<int*>(ws);
-    auto* m = reinterpret_cast<unsigned char*>(any + 1);
-    md = {m, m + rows, any};
-    mw = {m + rows + N, m + rows + 2 * N, any};
-    mx = {m + rows + 2 * N + K, m + 2 * rows + 2 * N + K, any};
-    ws += bytes;
+  int *fd = nullptr, *fw = nullptr, *fx = nullptr;
+  if (planes == 3) {
+    fd = reinterpret_cast<int*>(ws);
+    ws += flags_bytes(rows, N);
+    fw = reinterpret_cast<int*>(ws);
+    ws += flags_bytes(N, K);
+    fx = reinterpret_cast<int*>(ws);
+    ws += flags_bytes(rows, K);
   }
   if (pack_d || dbias) {
     const cudaError_t err =
         prep(dout, type_of(dout_dtype), N, rows, out_features, act ? pre : nullptr,
              dtype == SSD_DTYPE_BF16 ? kF16 : kF32, activation, pack_d ? planes : 0, ws,
-             dbias ? colsum : nullptr, md, st);
+             dbias ? colsum : nullptr, fd, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     if (pack_d) {
       d = {ws, rows, N, padded(N), planes};
@@ -1760,14 +1782,14 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   }
   if (pack_w) {
     const cudaError_t err = prep(weight, type_of(dtype), K, N, in_features, nullptr, 0, 0, planes,
-                                 ws, nullptr, mw, st);
+                                 ws, nullptr, fw, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     w = {ws, N, K, padded(K), planes};
     ws += planes_bytes(N, K, planes);
   }
   if (pack_x) {
     const cudaError_t err = prep(x, type_of(dtype), sx, rows, in_features, nullptr, 0, 0, planes, ws,
-                                 nullptr, mx, st);
+                                 nullptr, fx, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     xo = {ws, rows, K, padded(K), planes};
     ws += planes_bytes(rows, K, planes);
@@ -1776,19 +1798,21 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   ep.out_t = (uint8_t)type_of(dtype);
   ep.out_ld = K;
   float* part = reinterpret_cast<float*>(ws);
-  const float* dpre = act ? static_cast<const float*>(pre) : nullptr;   // (used for fp32)
+  NonFinite fix[2];
+  int fixes = 0;
+  Given gd = planes == 3 ? given(dout, rows, N, N, fd, false) : Given{};
+  if (act) {
+    gd.pre = static_cast<const float*>(pre);
+    gd.pre_ld = N;
+    gd.act = (uint8_t)activation;
+  }
   if (dx) {
     ep.out = dx;
     ep.wide = K % 4 == 0 && al(dx, 4 * e);
     ep.wide8 = K % 8 == 0 && al(dx, 16);
     const int r = gemm(d, false, w, true, rows, K, N, ep, part, st);
     if (r != SSD_OK) return r;
-    if (planes == 3) {
-      const Given gd = {static_cast<const float*>(dout), dpre, md.row, N, N, (uint8_t)activation, false};
-      const Given gw = {static_cast<const float*>(weight), nullptr, mw.col, K, 0, 0, true};
-      const cudaError_t err = fix_nonfinite(gd, gw, rows, K, N, md.any, ep, st);
-      if (err != cudaSuccess) return cuda_bad(err, "linear launch");
-    }
+    if (planes == 3) fix[fixes++] = {gd, given(weight, N, K, K, fw, true), rows, K, N, ep};
   }
   if (dweight) {
     ep.out = dweight;
@@ -1796,12 +1820,12 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
     ep.wide8 = K % 8 == 0 && al(dweight, 16);
     const int r = gemm(d, true, xo, true, N, K, rows, ep, part, st);
     if (r != SSD_OK) return r;
-    if (planes == 3) {
-      const Given gd = {static_cast<const float*>(dout), dpre, md.col, N, N, (uint8_t)activation, true};
-      const Given gx = {static_cast<const float*>(x), nullptr, mx.col, sx, 0, 0, true};
-      const cudaError_t err = fix_nonfinite(gd, gx, N, K, rows, md.any, ep, st);
-      if (err != cudaSuccess) return cuda_bad(err, "linear launch");
-    }
+    gd.mn = true;
+    if (planes == 3) fix[fixes++] = {gd, given(x, rows, K, sx, fx, true), N, K, rows, ep};
+  }
+  if (fixes > 0) {
+    const cudaError_t err = fix_nonfinite(fix, fixes, st);
+    if (err != cudaSuccess) return cuda_bad(err, "linear launch");
   }
   return SSD_OK;
 }
