@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads)
         if (silu) {
 #pragma unroll
           for (int i = 0; i < kCh; ++i) {
-            const float s = row::sigmoid_f(pre[i]);
+            const float s = row::sigmoid<T>(pre[i]);
             g[i] *= fmaf(s * pre[i], 1.f - s, s);
           }
         }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (silu) {
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) acc[i] *= row::sigmoid_f(acc[i]);
+    for (int i = 0; i < kCh; ++i) acc[i] *= row::sigmoid<T>(acc[i]);
   }
   put4(out + b * C + c0, acc);
 }

@@ -75,7 +75,11 @@ constexpr uint32_t kSleepNs = 20000;
 // Sticky status of this device: nonzero once a wait gave up (ssd_scan_status).
 __device__ int g_status_linear;
 
-enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+// (of bf16 data: with the exponentials that are exact enough for it, row::sigmoid)
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSiluBf16 = 3, kActGeluBf16 = 4 };
+int act_of(ssd_activation_t a, ssd_dtype_t dtype) {
+  return a == SSD_ACT_NONE || dtype == SSD_DTYPE_F32 ? (int)a : (int)a + 2;
+}
 enum { kNone = 0, kF32 = 1, kBf16 = 2, kF16 = 3 };
 
 // What happens to a sum on its way out: out = act(sum + bias) + res, and pre =
@@ -92,17 +96,21 @@ struct Epilogue {
 };
 
 __device__ __forceinline__ float act_f(int act, float v) {
-  if (act == kActSilu) return v * row::sigmoid_f(v);
-  if (act == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678f));
+  if (act == kActSilu) return v * row::sigmoid<float>(v);
+  if (act == kActSiluBf16) return v * row::sigmoid<__nv_bfloat16>(v);
+  if (act != kActNone) return 0.5f * v * (1.f + erff(v * 0.70710678f));
   return v;
 }
 __device__ __forceinline__ float dact_f(int act, float v) {
-  if (act == kActSilu) {
-    const float s = row::sigmoid_f(v);
+  if (act == kActSilu || act == kActSiluBf16) {
+    const float s = act == kActSilu ? row::sigmoid<float>(v) : row::sigmoid<__nv_bfloat16>(v);
     return s * (1.f + v * (1.f - s));
   }
-  if (act == kActGelu)
-    return 0.5f * (1.f + erff(v * 0.70710678f)) + v * 0.39894228f * __expf(-0.5f * v * v);
+  if (act != kActNone) {
+    const float q = -0.5f * v * v;
+    return 0.5f * (1.f + erff(v * 0.70710678f)) +
+           v * 0.39894228f * (act == kActGelu ? expf(q) : __expf(q));
+  }
   return 1.f;
 }
 
@@ -1636,7 +1644,7 @@ int ssd_linear_fwd(const void* x, int64_t x_row_stride, const void* weight, cons
   ep.out_ld = N;
   ep.pre = pre;
   ep.pre_t = dtype == SSD_DTYPE_BF16 ? kF16 : kF32;
-  ep.act = (uint8_t)activation;
+  ep.act = (uint8_t)act_of(activation, dtype);
   ep.wide = N % 4 == 0 && al(bias, 4 * e) && al(out, 4 * re) &&
             al(pre, dtype == SSD_DTYPE_BF16 ? 8 : 16) &&
             (!residual || wide4(residual, ep.res_ld, re));
@@ -1766,7 +1774,7 @@ int ssd_linear_bwd(const void* dout, ssd_dtype_t dout_dtype, const void* x, int6
   if (pack_d || dbias) {
     const cudaError_t err =
         prep(dout, type_of(dout_dtype), N, rows, out_features, act ? pre : nullptr,
-             dtype == SSD_DTYPE_BF16 ? kF16 : kF32, activation, pack_d ? planes : 0, ws,
+             dtype == SSD_DTYPE_BF16 ? kF16 : kF32, act_of(activation, dtype), pack_d ? planes : 0, ws,
              dbias ? colsum : nullptr, fd, st);
     if (err != cudaSuccess) return cuda_bad(err, "linear operand launch");
     if (pack_d) {

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kMaxThreads)
       if (MODE != kNoGate) {
         zs[s].get(gate[s]);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) gate[s][j] *= row::sigmoid_f(gate[s][j]);
+        for (int j = 0; j < kVec; ++j) gate[s][j] *= row::sigmoid<T>(gate[s][j]);
         if (MODE == kGateFirst) {
 #pragma unroll
           for (int j = 0; j < kVec; ++j) v[s][j] *= gate[s][j];
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1)   // (one slot: 6
         if (MODE != kNoGate) zs[s].get(zv);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
-          const float e = MODE != kNoGate ? zv[j] * row::sigmoid_f(zv[j]) : 1.f;
+          const float e = MODE != kNoGate ? zv[j] * row::sigmoid<T>(zv[j]) : 1.f;
           const float u = MODE == kNormFirst ? yv[j] : yv[j] * e;
           const float g = MODE == kNormFirst ? go[j] * w[j] * e : go[j] * w[j];
           c[0] = fmaf(u, u, c[0]);
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kMaxThreads, S == 1 ? 2 : 1)   // (one slot: 6
       if (MODE != kNoGate) zs[s].get(zv);
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float sg = MODE != kNoGate ? row::sigmoid_f(zv[j]) : 1.f;
+        const float sg = MODE != kNoGate ? row::sigmoid<T>(zv[j]) : 1.f;
         const float e = MODE != kNoGate ? zv[j] * sg : 1.f;
         // silu' = sg + z sg (1 - sg); not sg (1 - e) + e, which cancels for large z
         const float de = MODE != kNoGate ? fmaf(e, 1.f - sg, sg) : 0.f;

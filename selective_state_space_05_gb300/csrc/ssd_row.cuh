@@ -12,16 +12,22 @@ namespace row {
 constexpr int kVec = 8;   // elements per slot: one 16-byte bf16 or two fp32 vectors
 constexpr int kMaxWarps = 16;   // of a CTA of row teams
 
-// 1 / (1 + 2^(-v log2 e)) in four instructions: both SFU operations flush
-// subnormals, where the sigmoid is 0 or 1 to fp32 anyway (relative error of
-// each about 2^-22; with expf and a division the gated backward was bound by
-// its instructions).
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid_f(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
+// The sigmoid for data of type T.  bf16: 1 / (1 + 2^(-v log2 e)) in four
+// instructions, each SFU operation within about 2^-22 and the rounded exponent
+// adding |v| 2^-24, which is nothing beside bf16's 2^-9 (with expf and a division
+// the gated backward was bound by its instructions).  fp32: expf, whose error does
+// not grow with v; its calls move twice the bytes for the same instructions.
+// Subnormals flush, where the sigmoid is 0 to fp32's normal range.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v) {
+  if constexpr (sizeof(T) == 2) return rcp(1.f + ex2(-kLog2e * v));
+  else return rcp(1.f + expf(-v));
+}
 
 __device__ __forceinline__ void unpack(uint4 w, float (&v)[kVec]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
