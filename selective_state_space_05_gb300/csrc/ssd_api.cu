@@ -9,6 +9,7 @@
 
 #include "../../include/ssd_scan.h"
 #include "ssd_common.cuh"
+#include "ssd_status.h"
 
 namespace {
 
@@ -275,27 +276,22 @@ const char* ssd_last_error(void) { return g_err; }
 
 int ssd_scan_status(int reset, void* stream) {
   g_err[0] = 0;
-  int bits = 0;
-  int e = ssd::fused_status(reset, static_cast<cudaStream_t>(stream), &bits);
-  if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
-  int bits32 = 0;
-  e = ssd::tc32_status(reset, static_cast<cudaStream_t>(stream), &bits32);
-  if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
-  bits |= bits32;
-  int bits_linear = 0;
-  e = ssd::linear_status(reset, static_cast<cudaStream_t>(stream), &bits_linear);
-  if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
-  if (bits_linear != 0)
-    return fail(SSD_ERR_TIMEOUT,
-                "a projection's launch gave up a bounded wait (error bits 0x%x: 1 barrier, 2 "
-                "drain); its outputs are not valid",
-                bits_linear);
-  if (bits != 0)
-    return fail(SSD_ERR_TIMEOUT,
-                "a tensor-core scan launch gave up a bounded wait (error bits 0x%x: 1 barrier, "
-                "2 state hand-off, 4 drain, 8 fp32 tensor-core stage); its outputs are not "
-                "valid",
-                bits);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int (*const words[])(int, cudaStream_t, int*) = {ssd::fused_status, ssd::tc32_status,
+                                                   ssd::linear_status};
+  int bits[3] = {};
+  // all are read before any is cleared: an error in between loses none
+  for (int pass = 0; pass < (reset ? 2 : 1); ++pass)
+    for (int i = 0; i < 3; ++i) {
+      if (pass == 1 && bits[i] == 0) continue;
+      int now = 0;
+      const int e = words[i](pass, st, &now);
+      if (e != 0) return cuda_fail(static_cast<cudaError_t>(e), "ssd_scan_status");
+      bits[i] |= now;
+    }
+  char m[sizeof(g_err)];
+  if (ssd::status_message(bits[0] | bits[1], bits[2], m, sizeof(m)))
+    return fail(SSD_ERR_TIMEOUT, "%s", m);
   return SSD_OK;
 }
 
