@@ -9,6 +9,11 @@ Argument marshalling only, as in scan.py.  Each operator comes as
 CUDA graph capture) and as ``<name>``, a differentiable torch function of the
 two.  A backward that is captured into a CUDA graph should call ``<name>_bwd``:
 capturing ``Tensor.backward`` ties the graph to autograd's own streams.
+
+A tensor that is given to be written (out, residual_out, dx, dz, conv_state,
+clipped gradients) has its version counter moved on, as torch's own in-place
+functions do: a backward pass that saved its old value raises.  Replays of a
+captured call are not counted.
 """
 from __future__ import annotations
 
@@ -19,6 +24,7 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .scan import _DT, _need, _ptr
@@ -115,20 +121,25 @@ def add_rmsnorm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: t
     if scale is not None:
         _chk(scale, "scale", _F32, (dim,), dev)
     st = _stream_of(stream, dev)
+    given = []
     if out is None:
         out = _empty(shape, xd, dev, stream)
     else:
         _chk(out, "out", xd, shape, dev)
+        given.append(out)
     if residual_out is None:
         residual_out = _empty(shape, residual_dtype, dev, stream)
     else:
         _chk(residual_out, "residual_out", residual_dtype, shape, dev)
+        given.append(residual_out)
     code = _call("ssd_add_rmsnorm_fwd")(
         x.data_ptr(), _ptr(residual), _ptr(scale), weight.data_ptr(), eps,
         x.numel() // dim if dim else 0, dim, dt, _float_dtype(residual_out, "residual"),
         out.data_ptr(), residual_out.data_ptr(), st)
     if code:
         _lib.check(code)
+    if given:
+        increment_version(given)
     return out, residual_out
 
 
@@ -259,6 +270,7 @@ def gated_rmsnorm_fwd(y: torch.Tensor, z: Optional[torch.Tensor], weight: torch.
         zp = z.data_ptr()
     _chk(weight, "weight", _F32, (dim,), dev)
     st = _stream_of(stream, dev)
+    given = out
     if out is None:
         out = _empty(shape, yd, dev, stream)
     else:
@@ -269,6 +281,8 @@ def gated_rmsnorm_fwd(y: torch.Tensor, z: Optional[torch.Tensor], weight: torch.
         out.data_ptr(), st)
     if code:
         _lib.check(code)
+    if given is not None:
+        increment_version(given)
     return out
 
 
@@ -289,6 +303,7 @@ def gated_rmsnorm_bwd(dout: torch.Tensor, y: torch.Tensor, z: Optional[torch.Ten
     _chk(weight, "weight", _F32, (dim,), dev)
     st = _stream_of(stream, dev)
     sz = sdz = _NO_STRIDE
+    given = dz
     if z is not None:
         sz = _chk_rows(z, "z", yd, shape, dev)[2]
         if dz is None:
@@ -305,6 +320,8 @@ def gated_rmsnorm_bwd(dout: torch.Tensor, y: torch.Tensor, z: Optional[torch.Ten
         dout.data_ptr(), y.data_ptr(), sy, _ptr(z), sz, weight.data_ptr(), eps, B, L, dim, gs,
         1 if norm_before_gate else 0, dt, dy.data_ptr(), _ptr(dz), sdz, dw.data_ptr(), ws,
         ws_bytes, st))
+    if given is not None:
+        increment_version(given)
     return dict(dy=dy, dz=dz, dweight=dw)
 
 
@@ -359,6 +376,7 @@ def causal_conv1d_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     if seq_idx is not None:
         _chk(seq_idx, "seq_idx", torch.int32, (Bsz, L), dev)
     st = _stream_of(stream, dev)
+    given = dx
     if dx is None:
         dx = _empty(shape, xd, dev, stream)
     so = _chk_rows(dx, "dx", xd, shape, dev)[2]
@@ -370,6 +388,8 @@ def causal_conv1d_bwd(dout: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         dout.data_ptr(), sd, x.data_ptr(), sx, weight.data_ptr(), _ptr(bias), _ptr(seq_idx), Bsz,
         L, Cn, W, int(activation == "silu"), dt, dx.data_ptr(), so, dw.data_ptr(), _ptr(db), ws,
         ws_bytes, st))
+    if given is not None:
+        increment_version(given)
     return dict(dx=dx, dweight=dw, dbias=db)
 
 
@@ -396,15 +416,19 @@ def causal_conv1d_step(x: torch.Tensor, conv_state: Optional[torch.Tensor], weig
     if W > 1:
         _chk(conv_state, "conv_state", xd, (Bsz, W - 1, Cn), dev)
     st = _stream_of(stream, dev)
+    given = [conv_state] if W > 1 else []
     if out is None:
         out = _empty(shape, xd, dev, stream)
     else:
         _chk(out, "out", xd, shape, dev)
+        given.append(out)
     code = _call("ssd_causal_conv1d_step")(
         x.data_ptr(), x.stride(0), conv_state.data_ptr() if W > 1 else None, weight.data_ptr(),
         _ptr(bias), Bsz, Cn, W, 1 if activation == "silu" else 0, dt, out.data_ptr(), st)
     if code:
         _lib.check(code)
+    if given:
+        increment_version(given)
     return out
 
 
@@ -491,6 +515,7 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         rt = _float_dtype(residual, "residual")
         sr = _row_stride(residual, "residual")
     od = xd if residual is None else residual.dtype
+    given = out
     if out is None:
         out = _empty(shape, od, dev, stream)
     else:
@@ -507,6 +532,8 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         _ptr(pre), ws, ws_bytes, st)
     if code:
         _lib.check(code)
+    if given is not None:
+        increment_version(given)
     return (out, pre) if save_pre else out
 
 
@@ -696,4 +723,5 @@ def clip_grads(grads, max_norm: float, *, eps: float = 1e-6, out=None,
         _address(ptrs), _address(sizes), _address(codes), n,
         None if outs is None else _address(outs), None if outs is None else _address(out_codes),
         max_norm, eps, norm.data_ptr(), ws, ws_bytes, st))
+    increment_version(grads if out is None else out)
     return norm
