@@ -91,6 +91,13 @@ def _float_dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _no_rows(t: torch.Tensor) -> bool:
+    """An empty batch: the differentiable forms answer it without a launch,
+    with empty results and zero gradients of the parameters (the explicit calls
+    refuse it, as the C ABI does)."""
+    return t.numel() == 0 and t.dim() > 1 and t.shape[-1] > 0
+
+
 def block_abi_version() -> int:
     return _lib.load().ssd_block_abi_version()
 
@@ -185,8 +192,19 @@ class _AddRMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, weight, scale, eps, residual_dtype):
         ctx.set_materialize_grads(False)
-        y, r = add_rmsnorm_fwd(x, residual, weight, scale=scale, eps=eps,
-                               residual_dtype=residual_dtype)
+        if _no_rows(x):
+            _float_dtype(x, "x")
+            _stream_of(None, x.device)
+            if residual is not None:
+                residual_dtype = residual.dtype
+                _chk(residual, "residual", residual_dtype, x.shape, x.device)
+            _chk(weight, "weight", _F32, x.shape[-1:], x.device)
+            if scale is not None:
+                _chk(scale, "scale", _F32, x.shape[-1:], x.device)
+            y, r = torch.empty_like(x), x.new_empty(x.shape, dtype=residual_dtype)
+        else:
+            y, r = add_rmsnorm_fwd(x, residual, weight, scale=scale, eps=eps,
+                                   residual_dtype=residual_dtype)
         ctx.save_for_backward(r, weight, None if scale is None else x, scale)
         ctx.eps, ctx.has_residual, ctx.dtype = eps, residual is not None, x.dtype
         return y, r
@@ -197,6 +215,9 @@ class _AddRMSNorm(torch.autograd.Function):
         r, weight, x, scale = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros(r.shape, dtype=ctx.dtype, device=r.device)
+        if _no_rows(r):
+            return (dy, torch.empty_like(r) if ctx.has_residual else None, torch.zeros_like(weight),
+                    None if scale is None else torch.zeros_like(scale), None, None)
         g = add_rmsnorm_bwd(dy.contiguous(), None if dr is None else dr.contiguous(), r, weight,
                             x=x, scale=scale, eps=ctx.eps, need_dx=ctx.needs_input_grad[0],
                             need_dresidual=ctx.has_residual and ctx.needs_input_grad[1])
@@ -330,12 +351,24 @@ class _GatedRMSNorm(torch.autograd.Function):
     def forward(ctx, y, z, weight, group_size, eps, norm_before_gate):
         ctx.save_for_backward(y, z, weight)
         ctx.opts = dict(group_size=group_size, eps=eps, norm_before_gate=norm_before_gate)
+        if _no_rows(y):
+            _float_dtype(y, "y")
+            _stream_of(None, y.device)
+            if z is not None:
+                _chk_rows(z, "z", y.dtype, y.shape, y.device)
+            _chk(weight, "weight", _F32, y.shape[-1:], y.device)
+            if group_size is not None and (group_size < 1 or y.shape[-1] % group_size):
+                raise ValueError("group_size must divide the channels")
+            return y.new_empty(y.shape)
         return gated_rmsnorm_fwd(y, z, weight, **ctx.opts)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         y, z, weight = ctx.saved_tensors
+        if _no_rows(y):
+            return (y.new_empty(y.shape), None if z is None else y.new_empty(y.shape),
+                    torch.zeros_like(weight), None, None, None)
         g = gated_rmsnorm_bwd(dout.contiguous(), y, z, weight, **ctx.opts)
         return g["dy"], g["dz"], g["dweight"], None, None, None
 
@@ -586,6 +619,9 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, activation):
         save = activation is not None and any(ctx.needs_input_grad[:3])
+        ctx.empty = _no_rows(x)
+        if ctx.empty:
+            return _Linear.no_rows(ctx, x, weight, bias, residual, activation)
         got = linear_fwd(x, weight, bias, activation=activation, residual=residual, save_pre=save)
         out, pre = got if save else (got, None)
         ctx.save_for_backward(x if ctx.needs_input_grad[1] else None,
@@ -594,10 +630,31 @@ class _Linear(torch.autograd.Function):
         return out
 
     @staticmethod
+    def no_rows(ctx, x, weight, bias, residual, activation):
+        _float_dtype(x, "x")
+        _act_code(activation)
+        _stream_of(None, x.device)
+        N = weight.shape[0]
+        shape = x.shape[:-1] + (N,)
+        _chk(weight, "weight", x.dtype, (N, x.shape[-1]), x.device)
+        if bias is not None:
+            _chk(bias, "bias", x.dtype, (N,), x.device)
+        if residual is not None:
+            _float_dtype(residual, "residual")
+            if residual.shape != shape or residual.device != x.device:
+                raise ValueError(f"residual must have shape {tuple(shape)} on {x.device}")
+        ctx.save_for_backward(x, weight, bias)
+        return x.new_empty(shape, dtype=x.dtype if residual is None else residual.dtype)
+
+    @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        x, weight, pre = ctx.saved_tensors
         nx, nw, nb, nr = ctx.needs_input_grad[:4]
+        if ctx.empty:
+            x, weight, bias = ctx.saved_tensors
+            return (x.new_empty(x.shape) if nx else None, torch.zeros_like(weight) if nw else None,
+                    torch.zeros_like(bias) if nb else None, dout if nr else None, None)
+        x, weight, pre = ctx.saved_tensors
         dout = dout.contiguous()
         g = dict(dx=None, dweight=None, dbias=None)
         if nx or nw or nb:
