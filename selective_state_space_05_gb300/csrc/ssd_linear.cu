@@ -882,10 +882,12 @@ __device__ __forceinline__ void get8_any(const void* p, int t, const void* end, 
   }
 }
 
-// Two values to bf16 towards zero (of a value near the end of the range: no sum of
-// its planes is beyond it).
-__device__ __forceinline__ uint32_t chopped(float a, float b) {
-  return (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u);
+// Two values to bf16, to nearest, or towards zero where chop's bit 0 or 1 is set
+// (a value near the end of the range: no sum of its planes is beyond it).
+__device__ __forceinline__ uint32_t pack_chopped(float a, float b, uint32_t chop) {
+  const uint32_t u = tc::pack_bf16x2(a, b);
+  const uint32_t lo = chop & 1 ? __float_as_uint(a) >> 16 : u & 0xFFFFu;
+  return lo | ((chop & 2 ? __float_as_uint(b) : u) & 0xFFFF0000u);
 }
 // Whether one of eight packed bf16 is an infinity or a NaN.
 __device__ __forceinline__ bool beyond(const uint32_t (&u)[4]) {
@@ -936,25 +938,27 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
       if (rb + i >= r1) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[i][j];
-      bool chop = false;
+      uint32_t chop = 0;   // a bit for each of the eight
       __nv_bfloat16* o = p.out + (rb + i) * p.ld + c;   // (ld is a multiple of 8: the pad may be written)
       for (int k = 0; k < p.planes; ++k) {
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (!chop) u[j] = tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1]);
-          else u[j] = chopped(v[i][2 * j], v[i][2 * j + 1]);
+          u[j] = chop == 0 ? tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1])
+                           : pack_chopped(v[i][2 * j], v[i][2 * j + 1], chop >> (2 * j));
         }
         if (k == 0 && p.planes == 3 && beyond(u)) {
-          chop = true;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 8; ++j) {
             if (!isfinite(v[i][j])) {
               v[i][j] = 0.f;
               met |= j < left;
             }
+            if (fabsf(v[i][j]) >= 0x1.FFp127f) chop |= 1u << j;
+          }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = chopped(v[i][2 * j], v[i][2 * j + 1]);
+          for (int j = 0; j < 4; ++j)
+            u[j] = pack_chopped(v[i][2 * j], v[i][2 * j + 1], chop >> (2 * j));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

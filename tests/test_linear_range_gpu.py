@@ -146,3 +146,49 @@ def test_nothing_but_nan():
     w[7, 519] = INF
     g = ssd.linear_bwd(torch.full((700, 300), -INF, device="cuda"), x.nan_to_num(1.0), w)
     assert torch.isinf(g["dweight"]).all() and not torch.isfinite(g["dx"]).any()
+
+
+def test_a_few_places_of_a_large_product():
+    """Their rows and columns only: every other result keeps the bits it has
+    without them."""
+    import selective_state_space_05_gb300 as ssd
+    M, K, N = 2000, 2100, 1500
+    g = torch.Generator("cuda").manual_seed(9)
+
+    def r(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    x, w, do = r(M, K), r(N, K) * K ** -0.5, r(M, N)
+    places = {"x": (x, [(0, 0), (777, 1024), (1999, 2099)]), "w": (w, [(3, 5), (1499, 2099)]),
+              "do": (do, [(1, 1023), (1024, 7), (1998, 1499)])}
+    for t, at in places.values():
+        for i, j in at:
+            t[i, j] = 0.0
+
+    def step():
+        b = ssd.linear_bwd(do, x, w)
+        return ssd.linear_fwd(x, w), b["dx"], b["dweight"]
+
+    clean = step()
+    for n, (t, at) in enumerate(places.values()):
+        for k, (i, j) in enumerate(at):
+            t[i, j] = (INF, -INF, NAN)[(n + k) % 3]
+    got = step()
+    rows = {k: [i for i, _ in at] for k, (_, at) in places.items()}
+    cols = {k: [j for _, j in at] for k, (_, at) in places.items()}
+    # the three products, which rows and columns of each are concerned, and the terms
+    for name, a, b, out, was, ar, bc in (
+            ("out", x, w, got[0], clean[0], rows["x"], rows["w"]),
+            ("dx", do, w.t(), got[1], clean[1], rows["do"], cols["w"]),
+            ("dweight", do.t(), x.t(), got[2], clean[2], cols["do"], cols["x"])):
+        hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+        hit[ar] = True
+        hit[:, bc] = True
+        assert torch.equal(out[~hit], was[~hit]), name
+        for i in ar:
+            ref = (a[i].double() * b.double()).sum(-1).float()
+            assert torch.equal(torch.isnan(out[i]), torch.isnan(ref)), (name, i)
+            assert torch.equal(out[i].nan_to_num(7.0), ref.nan_to_num(7.0)), (name, i)
+        for j in bc:
+            ref = (a.double() * b[j].double()).sum(-1).float()
+            assert torch.equal(torch.isnan(out[:, j]), torch.isnan(ref)), (name, j)
+            assert torch.equal(out[:, j].nan_to_num(7.0), ref.nan_to_num(7.0)), (name, j)
