@@ -192,3 +192,39 @@ def test_a_few_places_of_a_large_product():
             ref = (a.double() * b[j].double()).sum(-1).float()
             assert torch.equal(torch.isnan(out[:, j]), torch.isnan(ref)), (name, j)
             assert torch.equal(out[:, j].nan_to_num(7.0), ref.nan_to_num(7.0)), (name, j)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("rt", [None, F32])
+def test_bf16(shape, rt):
+    """bf16 operands go to the tensor cores as they are."""
+    import selective_state_space_05_gb300 as ssd
+    bf = torch.bfloat16
+    M, K, N = shape
+    x, w = operands(*shape)
+    plant(x, w)
+    big = torch.finfo(bf).max
+
+    def to_bf16(t):   # the largest fp32 values would round to infinities
+        return torch.where(torch.isfinite(t), t.clamp(-big, big), t).to(bf)
+    x, w = to_bf16(x), to_bf16(w)
+    r = torch.randn(M, N, generator=torch.Generator().manual_seed(2)) if rt else None
+    out = ssd.linear_fwd(x.cuda(), w.cuda(), residual=None if r is None else r.cuda())
+    ref, mag = dot(x, w), dot(x.abs(), w.abs())
+    if r is not None:
+        ref, mag = ref + r.double(), mag + r.double().abs()
+    check(out, ref, mag, _ops(K), "out")
+    do = torch.randn(M, N, generator=torch.Generator().manual_seed(3))
+    do[:, 1] *= 1e-3
+    do[15] *= 1e-2
+    do[16] *= 1e-2
+    do[:, 22] *= 1e-3
+    do[:, 24] *= 1e-3
+    do[4, 9], do[6, 30], do[8, 31], do[10, 3] = INF, -INF, NAN, -0.05 * MAX
+    do = do.to(bf)
+    got = ssd.linear_bwd(do.cuda(), x.cuda(), w.cuda(), need_dbias=True)
+    ssd.scan_status()
+    d, a = do.double(), do.double().abs()
+    check(got["dx"], dot(d, w.t()), dot(a, w.t().abs()), _ops(N), "dx")
+    check(got["dweight"], dot(d.t(), x.t()), dot(a.t(), x.t().abs()), _ops(M), "dweight")
+    check(got["dbias"], d.sum(0), a.sum(0), M + 64, "dbias")
