@@ -882,13 +882,6 @@ __device__ __forceinline__ void get8_any(const void* p, int t, const void* end, 
   }
 }
 
-// Two values to bf16, to nearest, or towards zero where chop's bit 0 or 1 is set
-// (a value near the end of the range: no sum of its planes is beyond it).
-__device__ __forceinline__ uint32_t pack_chopped(float a, float b, uint32_t chop) {
-  const uint32_t u = tc::pack_bf16x2(a, b);
-  const uint32_t lo = chop & 1 ? __float_as_uint(a) >> 16 : u & 0xFFFFu;
-  return lo | ((chop & 2 ? __float_as_uint(b) : u) & 0xFFFF0000u);
-}
 // Whether one of eight packed bf16 is an infinity or a NaN.
 __device__ __forceinline__ bool beyond(const uint32_t (&u)[4]) {
   uint32_t most = 0;
@@ -897,13 +890,14 @@ __device__ __forceinline__ bool beyond(const uint32_t (&u)[4]) {
   return (most & 0xFFFFu) >= 0x7F80u || most >= 0x7F800000u;
 }
 
-// Eight consecutive columns a thread; ANY: rows of any alignment and length.
-template <bool ANY>
+// Eight consecutive columns a thread; ANY: rows of any alignment and length; SPLIT:
+// three planes.
+template <bool ANY, bool SPLIT>
 __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep p) {
   const int c = (blockIdx.x * 128 + threadIdx.x) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per;
   const int64_t r1 = c < p.C ? min(r0 + p.rows_per, p.R) : r0;   // past the row: nothing
-  bool met = false;   // an infinity or NaN
+  bool far = false;   // a value that has no first plane
   const int se = p.src_t == kF32 ? 4 : 2, pe = p.pre_t == kF32 ? 4 : 2;
   const int left = p.C - c;
   float sum[8];
@@ -938,35 +932,44 @@ __global__ void __launch_bounds__(128) prep_kernel(const __grid_constant__ Prep 
       if (rb + i >= r1) break;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[i][j];
-      uint32_t chop = 0;   // a bit for each of the eight
+      if (!SPLIT && p.planes == 0) continue;
       __nv_bfloat16* o = p.out + (rb + i) * p.ld + c;   // (ld is a multiple of 8: the pad may be written)
-      for (int k = 0; k < p.planes; ++k) {
-        uint32_t u[4];
+      uint32_t u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[j] = chop == 0 ? tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1])
-                           : pack_chopped(v[i][2 * j], v[i][2 * j + 1], chop >> (2 * j));
-        }
-        if (k == 0 && p.planes == 3 && beyond(u)) {
+      for (int k = 0; k < (SPLIT ? 3 : 1); ++k) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!isfinite(v[i][j])) {
-              v[i][j] = 0.f;
-              met |= j < left;
-            }
-            if (fabsf(v[i][j]) >= 0x1.FFp127f) chop |= 1u << j;
+        for (int j = 0; j < 4; ++j) u[j] = tc::pack_bf16x2(v[i][2 * j], v[i][2 * j + 1]);
+        if (SPLIT && k == 0) far |= beyond(u);
+        if (SPLIT && k < 2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[i][2 * j] -= __uint_as_float(u[j] << 16);
+            v[i][2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            u[j] = pack_chopped(v[i][2 * j], v[i][2 * j + 1], chop >> (2 * j));
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[i][2 * j] -= __uint_as_float(u[j] << 16);
-          v[i][2 * j + 1] -= __uint_as_float(u[j] & 0xFFFF0000u);
+        *reinterpret_cast<uint4*>(o + k * p.R * p.ld) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+  bool met = false;   // an infinity or NaN
+  if (SPLIT && far) {   // the thread's part once more, value by value
+    for (int64_t r = r0; r < r1; ++r) {
+#pragma unroll 1
+      for (int j = 0; j < min(8, left); ++j) {
+        float v = static_cast<const float*>(p.src)[r * p.src_ld + c + j];
+        if (p.pre) v *= dact_f(p.act, static_cast<const float*>(p.pre)[r * p.C + c + j]);
+        if (!isfinite(v)) {
+          v = 0.f;
+          met = true;
         }
-        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-        o += p.R * p.ld;
+        // towards zero where rounding would overflow: no sum of the planes is
+        // beyond the value
+        const bool chop = fabsf(v) >= 0x1.FFp127f;
+        for (int k = 0; k < 3; ++k) {
+          const __nv_bfloat16 h = chop ? __float2bfloat16_rz(v) : __float2bfloat16_rn(v);
+          p.out[(k * p.R + r) * p.ld + c + j] = h;
+          v -= __bfloat162float(h);
+        }
       }
     }
   }
@@ -1482,9 +1485,9 @@ cudaError_t prep(const void* src, int src_t, int64_t ld, int64_t R, int C, const
   const unsigned parts = (unsigned)prep_parts(R, C);
   const dim3 grid((unsigned)((C + 1023) / 1024), parts);
   if (C % 8 == 0 && ld % 8 == 0 && al(src, 16) && al(pre, 16))
-    prep_kernel<false><<<grid, 128, 0, st>>>(p);
+    (planes == 3 ? prep_kernel<false, true> : prep_kernel<false, false>)<<<grid, 128, 0, st>>>(p);
   else
-    prep_kernel<true><<<grid, 128, 0, st>>>(p);
+    (planes == 3 ? prep_kernel<true, true> : prep_kernel<true, false>)<<<grid, 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 
