@@ -37,8 +37,8 @@
 // active in a capture), dx 923-943 us, dW 997-1054 us; 1021 x 5120 -> 2560 into an fp32
 // residual 35 us, where 64 of 76 pairs hold one tile each and its last epilogue
 // has nothing to hide behind; 8 x 2560 -> 10576 10.3 us (5.3 TB/s of weight).
-// fp32, 4095 x 2048 -> 4384: forward 271 us, dx 298, dW 282 with the splitting
-// into planes (six bf16 products: 1.63, 1.48 and 1.56 PFLOP/s of them).
+// fp32, 4095 x 2048 -> 4384: forward 282 us, dx 306, dW 292 with the splitting
+// into planes (six bf16 products: 1.57, 1.44 and 1.51 PFLOP/s of them).
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <stdio.h>
@@ -61,8 +61,15 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0: TMA, 1: MMA, then the
 // K steps that one TMEM accumulator takes where the result is kept in fp32.
 // The tensor core's fp32 sum rounds towards zero at every MMA, an error that
 // grows with their number (relative 3.9e-6 after 320 MMAs, K = 5120, measured);
-// sums of 64 MMAs are added up in registers, to nearest, instead.
-constexpr int kExactSteps = 16;
+// short sums are added up in registers, to nearest, instead.  Relative error of the
+// whole result at K = 512 to 10576, where fp32 FMAs reach 4e-7 to 1.8e-6:
+// fp32 operands 4.8e-7 with 8 steps (16: 1.0e-6); the small products of planes,
+// which come first, add nothing to it and take long sums, which also lets the MMAs
+// run on while the epilogue is busy with the tile before (4095 x 2048 -> 4384 with
+// bias: 304 us; 16 steps throughout 323, 8 throughout 341).  bf16 operands 1.0e-6
+// with 16 steps (8: 4.8e-7, but 8192 x 1024 -> 2560 into a residual 115 us instead
+// of 95).
+constexpr int kExactSteps = 16, kPlanesSteps = 8, kLeadSteps = 64;
 // Where it is rounded to bf16 afterwards an accumulator takes more: an MMA loses
 // less than 2^-23 of the running sum, which for terms of one sign is half of the
 // total on average, so 1024 MMAs lose at most 2^-14, a 32nd of the least half step
@@ -288,7 +295,8 @@ struct Gemm {
   int bn;             // tile width, a multiple of 32 up to 256
   int stages;         // operand tiles in flight
   int group_m;        // tiles of M walked together (L2 reuse)
-  int run;            // K steps an accumulator takes before it is added to the registers'
+  int run;            // K steps an accumulator takes before it is added to the registers',
+  int lead;           // except for the first `lead` steps, the small products of planes:
   float* partial;     // [tail tile][splits][rows of a tile][bn] where splits > 1
   Epilogue e;
 };
@@ -414,6 +422,11 @@ __device__ __forceinline__ Item item_of(const Gemm& p, int item, int all_steps) 
   return w;
 }
 
+// Where the run of K steps ends that begins at r0, of an item that ends at k1.
+__device__ __forceinline__ int run_end(const Gemm& p, int r0, int k1) {
+  return min(r0 < p.lead ? min(r0 + kLeadSteps, p.lead) : r0 + p.run, k1);
+}
+
 // A CTA pair (CG 2): each CTA loads its own operand rows, counted on the
 // leader's `full`; the leader issues the MMAs and signals `empty` and `tfull`
 // of both; both CTAs' epilogues arrive on the leader's `tempty`.
@@ -433,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
   const int first = blockIdx.x / CG, stride = gridDim.x / CG;
   const int items = p.full + (p.tiles_m * p.tiles_n - p.full) * p.splits;
   const int all_steps = p.kblocks * p.pairs;
-  const int run = EXACT ? p.run : all_steps;   // K steps of one accumulator
 
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S; ++i) {
@@ -529,8 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
       for (int it = first; it < items && ok; it += stride) {
         const Item w = item_of(p, it, all_steps);
         const int k0 = w.k0, k1 = w.k1;
-        for (int r0 = k0; r0 < k1 && ok; r0 += run, ++n) {
-          const int r1 = min(r0 + run, k1), buf = n & 1;
+        for (int r0 = k0, r1; r0 < k1 && ok; r0 = r1, ++n) {
+          r1 = EXACT ? run_end(p, r0, k1) : k1;
+          const int buf = n & 1;
           ok = __all_sync(0xffffffffu,
                           wait_phase(&s.tempty[buf], ((n >> 1) & 1) ^ 1, &s.abort));
           tc::fence_after_sync();
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
                   (m * p.e.res_ld + n) * (p.e.res_t == kF32 ? 4 : 2)));
           }
       }
-      if (EXACT && k1 - k0 > p.run) {
+      if (EXACT && run_end(p, k0, k1) < k1) {
         // the runs' sums in registers; their total goes back to the last run's
         // place in TMEM
         float acc[4][32];
@@ -611,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
-        for (int r0 = k0; r0 < k1; r0 += p.run, ++n) {
+        for (int r0 = k0, r1; r0 < k1; r0 = r1, ++n) {
+          r1 = run_end(p, r0, k1);
           ok = filled(n);
           if (!ok) break;
           const uint32_t at = tmem + (n & 1) * 256 + lanes;
@@ -626,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
               for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
             }
           }
-          if (r0 + p.run < k1) release(n);
+          if (r1 < k1) release(n);
         }
         if (!ok) break;
         --n;
@@ -1030,7 +1044,9 @@ struct NonFinite {
 // epilogue as in the product kernel, whose result, of the finite terms, stands in
 // `out`: where that was the residual's memory it is taken for the residual, from
 // which it differs by a finite value.  A tile of 32 x 32 results a CTA at a time,
-// four a thread; blockIdx.y: the product.  Where nothing is flagged it ends at once.
+// four a thread; blockIdx.y: the product.  Where nothing is flagged it ends at once
+// (1 to 4 us of the call); 4095 x 2048 -> 4384 takes 0.64 ms instead of 0.28 with one
+// infinity, 0.94 with nothing but NaN, 12 with an infinity late in every row.
 constexpr int kFixTile = 32;
 __global__ void __launch_bounds__(256)
     nonfinite_kernel(const __grid_constant__ NonFinite p0, const __grid_constant__ NonFinite p1) {
@@ -1414,7 +1430,8 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   // runs of the longest item's K steps
   const int longest = pl.full > 0 ? g.kblocks * pairs : pl.steps_per;
   const bool exact = e.out_t == kF32 || longest > kBf16Steps;
-  g.run = kExactSteps;
+  g.run = pairs == 1 ? kExactSteps : kPlanesSteps;
+  g.lead = (pairs - 1) * g.kblocks;
   if (e.out_t != kF32) {   // as even as they can be
     const int runs = (longest + kBf16Steps - 1) / kBf16Steps;
     g.run = (longest + runs - 1) / runs;

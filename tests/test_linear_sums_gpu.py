@@ -1,7 +1,7 @@
 """Long sums of the projections: the tensor core's fp32 sum rounds towards
 zero at every step, which sums of one sign show.  An accumulator takes 64 MMAs
-(of 16 products each) where the result is kept in fp32 and 1024 where it is
-rounded to bf16; the accumulators' totals are added to nearest."""
+(of 16 products each; fp32 operands 32) where the result is kept in fp32 and 1024
+where it is rounded to bf16; the accumulators' totals are added to nearest."""
 import pytest
 import torch
 
@@ -62,6 +62,22 @@ def test_forward_of_many_features():
         ref += a.double() @ b.double().t()
     ref = ref.cpu()
     bt.assert_within(out, ref, ref.abs(), 0, "out", extra=2.0 ** -14 * ref.abs())
+
+
+@pytest.mark.parametrize("K", [512, 2048, 5120, 10576])
+@pytest.mark.parametrize("dt,units", [(F32, 10), (BF, 20)])
+def test_results_kept_in_fp32_of_both_signs(dt, units, K):
+    """The relative error of the whole result that the kernel's comment states:
+    4.8e-7 (8 * 2^-24) for fp32 operands, 1.0e-6 (17 * 2^-24) for bf16 ones; the
+    bounds fail with sums twice as long."""
+    import selective_state_space_05_gb300 as ssd
+    g = torch.Generator("cuda").manual_seed(K)
+    x = torch.randn(900, K, generator=g, device="cuda").to(dt)
+    w = (torch.randn(1000, K, generator=g, device="cuda") * K ** -0.5).to(dt)
+    ref = x.double() @ w.double().t()
+    out = ssd.linear_fwd(x, w, residual=torch.zeros(900, 1000, device="cuda"))
+    ssd.scan_status()
+    assert float((out.double() - ref).norm() / ref.norm()) <= units * bt.U32
 
 
 def test_equal_bits_on_every_call():
