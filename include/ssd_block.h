@@ -161,9 +161,10 @@ int ssd_causal_conv1d_step(const void *x, int64_t x_row_stride, void *conv_state
  * gradient's own type).  Tensors must not overlap one another.
  * norm: one float on the device (written).  Squares are summed in fp32 within
  * a chunk and in double beyond it, and in double throughout where a square
- * would leave the fp32 range.  A norm that is not finite is not special: an
- * infinite one gives the factor 0 (and NaN where g is infinite), a NaN one
- * gives NaN everywhere.  count may be 0 (norm = 0).  max_norm, eps >= 0. */
+ * would leave the fp32 range; the factor takes the norm in double, so a finite
+ * one that is infinite in *norm still scales.  A norm that is not finite is not
+ * special: an infinite one gives the factor 0 (and NaN where g is infinite), a
+ * NaN one gives NaN everywhere.  count may be 0 (norm = 0).  max_norm, eps >= 0. */
 size_t ssd_clip_grads_workspace_bytes(int count);
 int ssd_grad_norm(const void *const *grads, const int64_t *sizes,
                   const int32_t *dtypes, int count, float *norm,

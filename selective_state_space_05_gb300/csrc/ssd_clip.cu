@@ -155,10 +155,12 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // (g and o may be the same memory: each element is read and written by one thread)
+// The factor is first * coef: first is 1, or 2^-64 where the factor alone would be
+// a subnormal of few bits.
 template <typename T, typename O>
-__device__ __forceinline__ void scale_chunk(const T* p, O* o, int n, float coef) {
+__device__ __forceinline__ void scale_chunk(const T* p, O* o, int n, float first, float coef) {
   const int head = head_of(p, n);
-  if ((int)threadIdx.x < head) o[threadIdx.x] = from_f<O>(to_f(p[threadIdx.x]) * coef);
+  if ((int)threadIdx.x < head) o[threadIdx.x] = from_f<O>(to_f(p[threadIdx.x]) * first * coef);
   const int vecs = (n - head) / row::kVec;
   const bool wide = ((uintptr_t)(o + head) & 15) == 0;
 #pragma unroll 4
@@ -166,7 +168,7 @@ __device__ __forceinline__ void scale_chunk(const T* p, O* o, int n, float coef)
     float v[row::kVec];
     load8(p + head + i * row::kVec, v);
 #pragma unroll
-    for (int j = 0; j < row::kVec; ++j) v[j] *= coef;
+    for (int j = 0; j < row::kVec; ++j) v[j] = v[j] * first * coef;
     O* at = o + head + i * row::kVec;
     if (wide) {
       row::store_slot<true>(at, 0, 0, 1, row::kVec, v);
@@ -176,7 +178,7 @@ __device__ __forceinline__ void scale_chunk(const T* p, O* o, int n, float coef)
     }
   }
   const int rest = head + vecs * row::kVec + threadIdx.x;
-  if (rest < n) o[rest] = from_f<O>(to_f(p[rest]) * coef);
+  if (rest < n) o[rest] = from_f<O>(to_f(p[rest]) * first * coef);
 }
 
 template <int N>
@@ -188,7 +190,9 @@ __global__ void __launch_bounds__(kThreads)
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
   // a NaN norm compares false and is kept
   const double c = (double)max_norm / (v + (double)eps);
-  const float coef = c >= 1.0 ? 1.f : (float)c;
+  const bool tiny = c < 0x1p-100;
+  const float first = tiny ? 0x1p-64f : 1.f;
+  const float coef = c >= 1.0 ? 1.f : (float)(tiny ? c * 0x1p64 : c);
   if (in_place && coef == 1.f) return;
   for (uint32_t i = blockIdx.x; i < t.chunks; i += gridDim.x) {
     const uint32_t ch = t.chunks - 1 - i;
@@ -198,12 +202,12 @@ __global__ void __launch_bounds__(kThreads)
     const int n = (int)(left < kChunk ? left : kChunk);
     if (t.g_bf16[k]) {
       const bf* p = static_cast<const bf*>(t.g[k]) + at;
-      if (t.out_bf16[k]) scale_chunk(p, static_cast<bf*>(t.out[k]) + at, n, coef);
-      else scale_chunk(p, static_cast<float*>(t.out[k]) + at, n, coef);
+      if (t.out_bf16[k]) scale_chunk(p, static_cast<bf*>(t.out[k]) + at, n, first, coef);
+      else scale_chunk(p, static_cast<float*>(t.out[k]) + at, n, first, coef);
     } else {
       const float* p = static_cast<const float*>(t.g[k]) + at;
-      if (t.out_bf16[k]) scale_chunk(p, static_cast<bf*>(t.out[k]) + at, n, coef);
-      else scale_chunk(p, static_cast<float*>(t.out[k]) + at, n, coef);
+      if (t.out_bf16[k]) scale_chunk(p, static_cast<bf*>(t.out[k]) + at, n, first, coef);
+      else scale_chunk(p, static_cast<float*>(t.out[k]) + at, n, first, coef);
     }
   }
 }
