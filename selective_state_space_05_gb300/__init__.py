@@ -13,3 +13,5 @@ from .block import (add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_fwd,  # noqa: F401
                     block_abi_version, causal_conv1d_bwd, causal_conv1d_step, clip_grads,
                     gated_rmsnorm, gated_rmsnorm_bwd, gated_rmsnorm_fwd, grad_norm, linear,
                     linear_bwd, linear_fwd)
+from .delta import (delta_abi_version, delta_decode_step, delta_scan,  # noqa: F401
+                    delta_scan_bwd, delta_scan_fwd)

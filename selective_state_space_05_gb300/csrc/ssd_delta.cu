@@ -1,0 +1,364 @@
+// C ABI of the gated delta rule (include/ssd_delta.h): checks, workspace, the
+// launch sequence and the one-token step.
+#include <math.h>
+#include <stdio.h>
+
+#include "../../include/ssd_delta.h"
+#include "ssd_delta.cuh"
+#include "ssd_row.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+int bad(int code, const char* msg) { return set_error(code, msg); }
+int cuda_bad(cudaError_t e, const char* where) {
+  if (e == cudaSuccess) return SSD_OK;
+  char m[256];
+  snprintf(m, sizeof(m), "%s: %s", where, cudaGetErrorString(e));
+  return set_error(SSD_ERR_CUDA, m);
+}
+bool off(const void* p, size_t align) { return ((uintptr_t)p & (align - 1)) != 0; }
+size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+constexpr int kMaxHeaddim = 2048;
+
+int check_sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
+  if (dtype != SSD_DTYPE_F32 && dtype != SSD_DTYPE_BF16) return bad(SSD_ERR_ARG, "unknown dtype");
+  if (B < 1 || L < 1 || H < 1 || V < 1 || K < 1 || G < 1)
+    return bad(SSD_ERR_ARG, "batch, seqlen, nheads, headdim, dstate and ngroups must be >= 1");
+  if (H % G) return bad(SSD_ERR_ARG, "nheads must be a multiple of ngroups");
+  if (K > 128) return bad(SSD_ERR_UNSUPPORTED, "dstate must be at most 128");
+  if (V > kMaxHeaddim) return bad(SSD_ERR_UNSUPPORTED, "headdim must be at most 2048");
+  const int C = dtype == SSD_DTYPE_BF16 ? Mode<bf16>::C : Mode<float>::C;
+  if (B > 0x7fffffffLL || L > (1LL << 40) ||
+      (double)B * H * ((double)(L + C - 1) / C) >= 2147483648.0)
+    return bad(SSD_ERR_UNSUPPORTED, "batch * nheads * chunks must be below 2^31");
+  return SSD_OK;
+}
+
+Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
+  Args a = {};
+  const int C = dtype == SSD_DTYPE_BF16 ? Mode<bf16>::C : Mode<float>::C;
+  a.L = L;
+  a.B = (int)B;
+  a.H = H;
+  a.G = G;
+  a.K = K;
+  a.V = V;
+  a.nc = (int)((L + C - 1) / C);
+  a.KP = K <= 64 ? 64 : 128;
+  a.VP = (V + 15) / 16 * 16;
+  return a;
+}
+
+// The forward's pieces of a workspace at `base`, and how many bytes they take.
+template <typename T>
+size_t carve(Args& a, void* base, bool keep) {
+  constexpr int C = Mode<T>::C, NT = Mode<T>::NT;
+  const size_t n = (size_t)a.B * a.H * a.nc;
+  char* p = static_cast<char*>(base);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* r = p + at;
+    at += up(bytes);
+    return r;
+  };
+  a.T = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
+  a.P = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
+  a.vec = reinterpret_cast<float*>(take(n * vec_floats<C>() * 4));
+  a.S0 = a.X = nullptr;
+  if (keep) {
+    a.S0 = reinterpret_cast<bf16*>(take(n * NT * a.VP * a.KP * 2));
+    a.X = reinterpret_cast<bf16*>(take(n * NT * C * a.VP * 2));
+  }
+  return at;
+}
+// The backward's own.
+template <typename T>
+size_t carve_bwd(Args& a, void* base) {
+  constexpr int C = Mode<T>::C, NT = Mode<T>::NT;
+  const size_t n = (size_t)a.B * a.H * a.nc;
+  char* p = static_cast<char*>(base);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* r = p + at;
+    at += up(bytes);
+    return r;
+  };
+  a.dS = reinterpret_cast<bf16*>(take(n * NT * a.VP * a.KP * 2));
+  a.dY = reinterpret_cast<bf16*>(take(n * NT * C * a.VP * 2));
+  a.dq_part = a.dk_part = nullptr;
+  if (a.H != a.G) {
+    a.dq_part = reinterpret_cast<float*>(take((size_t)a.B * a.L * a.H * a.K * 4));
+    a.dk_part = reinterpret_cast<float*>(take((size_t)a.B * a.L * a.H * a.K * 4));
+  }
+  return at;
+}
+size_t fwd_bytes(Args& a, int dtype, void* base, bool keep) {
+  return dtype == SSD_DTYPE_BF16 ? carve<bf16>(a, base, keep) : carve<float>(a, base, keep);
+}
+size_t bwd_bytes(Args& a, int dtype, void* base) {
+  return dtype == SSD_DTYPE_BF16 ? carve_bwd<bf16>(a, base) : carve_bwd<float>(a, base);
+}
+
+bool bad_stride(ssd_stride_t s) {
+  return s.batch < 0 || s.token < 0 || s.batch > (1LL << 40) || s.token > (1LL << 40);
+}
+// Whether rows of `n` elements at these strides lie on 16 bytes.
+int wide_rows(const void* p, ssd_stride_t s, int n, int esize) {
+  return !off(p, 16) && (s.batch * esize) % 16 == 0 && (s.token * esize) % 16 == 0 &&
+         (n * esize) % 16 == 0;
+}
+
+int fill_inputs(Args& a, const void* q, ssd_stride_t sq, const void* k, ssd_stride_t sk,
+                const void* v, ssd_stride_t sv, const float* g, const float* beta, float scale,
+                const float* init, const int32_t* seq, int dtype) {
+  const int es = dtype == SSD_DTYPE_BF16 ? 2 : 4;
+  if (!q || !k || !v || !g || !beta) return bad(SSD_ERR_NULL, "q, k, v, g and beta are required");
+  if (bad_stride(sq) || bad_stride(sk) || bad_stride(sv))
+    return bad(SSD_ERR_ARG, "strides must be in [0, 2^40]");
+  if (!(fabsf(scale) <= 3.0e38f)) return bad(SSD_ERR_ARG, "scale must be finite");
+  if (off(q, es) || off(k, es) || off(v, es) || off(g, 4) || off(beta, 4) || off(init, 4) ||
+      off(seq, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.scale = scale;
+  a.init = init;
+  a.seq = seq;
+  a.sq = {sq.batch, sq.token};
+  a.sk = {sk.batch, sk.token};
+  a.sv = {sv.batch, sv.token};
+  a.wide_q = wide_rows(q, sq, a.K, es);
+  a.wide_k = wide_rows(k, sk, a.K, es);
+  a.wide_v = wide_rows(v, sv, a.V, es);
+  return SSD_OK;
+}
+
+template <typename T>
+cudaError_t run_forward(const Args& a, cudaStream_t st) {
+  const cudaError_t e = launch_prepare<T>(a, st);
+  return e != cudaSuccess ? e : launch_forward<T>(a, st);
+}
+
+// One token.  HBM-bound on the fp32 state, read and written once.  A warp takes
+// kRows rows of a head's state, all their loads in flight before the first is
+// used; with a = S q and b = S k of the old state, u = beta (v - e^g b) and
+// out = scale (e^g a + u (k q)), so that both row sums come from one pass.
+constexpr int kStepWarps = 4, kRows = 8;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kStepWarps * 32)
+    step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                const float* __restrict__ g, const float* __restrict__ beta, float scale,
+                float* __restrict__ state, int H, int V, int K, int G, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t bh = blockIdx.x;
+  const int h = (int)(bh % H);
+  const int64_t at = (bh / H * G + h / (H / G)) * K;
+  // this lane's four columns: neighbours where rows are whole float4s
+  float kv[4], qv[4];
+  int col[4];
+  float kq = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    col[j] = VEC ? lane * 4 + j : lane + 32 * j;
+    kv[j] = col[j] < K ? to_f(k[at + col[j]]) : 0.f;
+    qv[j] = col[j] < K ? to_f(q[at + col[j]]) : 0.f;
+    kq = fmaf(kv[j], qv[j], kq);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, o);
+  const float decay = expf(g[bh]), be = beta[bh];
+  const int v0 = (blockIdx.y * kStepWarps + warp) * kRows;
+  if (v0 >= V) return;
+  float* const S = state + (bh * V + v0) * K;
+  float s[kRows][4];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const bool row = v0 + r < V;
+    if (VEC) {
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row && col[0] < K) w = *reinterpret_cast<const float4*>(S + (int64_t)r * K + col[0]);
+      s[r][0] = w.x; s[r][1] = w.y; s[r][2] = w.z; s[r][3] = w.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[r][j] = row && col[j] < K ? S[(int64_t)r * K + col[j]] : 0.f;
+    }
+  }
+  float vv[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) vv[r] = v0 + r < V ? to_f(v[bh * V + v0 + r]) : 0.f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float sa = 0.f, sb = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[r][j] *= decay;
+      sa = fmaf(s[r][j], qv[j], sa);
+      sb = fmaf(s[r][j], kv[j], sb);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sa += __shfl_xor_sync(0xffffffffu, sa, o);
+      sb += __shfl_xor_sync(0xffffffffu, sb, o);
+    }
+    const float u = be * (vv[r] - sb);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[r][j] = fmaf(u, kv[j], s[r][j]);
+    if (v0 + r >= V) continue;
+    if (lane == r) out[bh * V + v0 + r] = from_f<T>(scale * fmaf(u, kq, sa));
+    if (VEC) {
+      if (col[0] < K)
+        *reinterpret_cast<float4*>(S + (int64_t)r * K + col[0]) =
+            make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (col[j] < K) S[(int64_t)r * K + col[j]] = s[r][j];
+    }
+  }
+}
+
+template <typename T>
+cudaError_t run_step(const void* q, const void* k, const void* v, const float* g,
+                     const float* beta, float scale, float* state, int64_t B, int H, int V, int K,
+                     int G, void* out, cudaStream_t st) {
+  const dim3 grid((unsigned)(B * H), (unsigned)((V + kStepWarps * kRows - 1) / (kStepWarps * kRows)));
+  const T *qt = static_cast<const T*>(q), *kt = static_cast<const T*>(k),
+          *vt = static_cast<const T*>(v);
+  if (K % 4 == 0 && !off(state, 16))
+    step_kernel<T, true><<<grid, kStepWarps * 32, 0, st>>>(qt, kt, vt, g, beta, scale, state, H, V,
+                                                           K, G, static_cast<T*>(out));
+  else
+    step_kernel<T, false><<<grid, kStepWarps * 32, 0, st>>>(qt, kt, vt, g, beta, scale, state, H,
+                                                            V, K, G, static_cast<T*>(out));
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace delta
+}  // namespace ssd
+
+using namespace ssd::delta;
+
+extern "C" {
+
+int ssd_delta_abi_version(void) { return SSD_DELTA_ABI_VERSION; }
+
+size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
+                                      int dstate, int ngroups, ssd_dtype_t dtype, int keep) {
+  if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  return fwd_bytes(a, dtype, nullptr, keep != 0);
+}
+
+int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_stride_t k_stride,
+                       const void* v, ssd_stride_t v_stride, const float* g, const float* beta,
+                       float scale, const float* initial_states, const int32_t* seq_idx,
+                       int64_t batch, int64_t seqlen, int nheads, int headdim, int dstate,
+                       int ngroups, ssd_dtype_t dtype, void* out, float* final_states, int keep,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  if (c != SSD_OK) return c;
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
+                  seq_idx, dtype);
+  if (c != SSD_OK) return c;
+  if (!out || !workspace) return bad(SSD_ERR_NULL, "out and workspace are required");
+  if (off(out, dtype == SSD_DTYPE_BF16 ? 2 : 4) || off(final_states, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (off(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < fwd_bytes(a, dtype, workspace, keep != 0))
+    return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  a.out = out;
+  a.wide_out = wide_rows(out, {0, 0}, headdim, dtype == SSD_DTYPE_BF16 ? 2 : 4);
+  a.final = final_states;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_bad(dtype == SSD_DTYPE_BF16 ? run_forward<bf16>(a, st) : run_forward<float>(a, st),
+                  "delta_scan_fwd launch");
+}
+
+size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
+                                          int dstate, int ngroups, ssd_dtype_t dtype, int saved) {
+  if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(a, dtype, nullptr, true));
+}
+
+int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void* q,
+                       ssd_stride_t q_stride, const void* k, ssd_stride_t k_stride, const void* v,
+                       ssd_stride_t v_stride, const float* g, const float* beta, float scale,
+                       const float* initial_states, const int32_t* seq_idx, int64_t batch,
+                       int64_t seqlen, int nheads, int headdim, int dstate, int ngroups,
+                       ssd_dtype_t dtype, const void* saved, size_t saved_bytes, void* dq, void* dk,
+                       void* dv, float* dg, float* dbeta, float* d_initial_states, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  if (c != SSD_OK) return c;
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
+                  seq_idx, dtype);
+  if (c != SSD_OK) return c;
+  if (!dout || !dq || !dk || !dv || !dg || !dbeta || !workspace)
+    return bad(SSD_ERR_NULL, "dout, dq, dk, dv, dg, dbeta and workspace are required");
+  const int es = dtype == SSD_DTYPE_BF16 ? 2 : 4;
+  if (off(dout, es) || off(dv, es) || off(dq, 2 * es) || off(dk, 2 * es) || off(dg, 4) ||
+      off(dbeta, 4) || off(dfinal_states, 4) || off(d_initial_states, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element (dq, dk: to two)");
+  if (off(workspace, 256) || off(saved, 256))
+    return bad(SSD_ERR_ALIGN, "workspace and saved must be 256-byte aligned");
+  const size_t kept = fwd_bytes(a, dtype, nullptr, true), own = bwd_bytes(a, dtype, nullptr);
+  if (saved && saved_bytes < kept)
+    return bad(SSD_ERR_WORKSPACE, "saved is not the workspace of a forward with keep at these sizes");
+  if (workspace_bytes < own + (saved ? 0 : kept)) return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  bwd_bytes(a, dtype, workspace);
+  fwd_bytes(a, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == SSD_DTYPE_BF16;
+  cudaError_t e = cudaSuccess;
+  if (!saved) e = bf ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
+  const int64_t hv = (int64_t)nheads * headdim;
+  a.dout = dout;
+  a.sdo = {seqlen * hv, hv};
+  a.wide_do = wide_rows(dout, {0, 0}, headdim, es);
+  a.dfinal = dfinal_states;
+  a.dinit = d_initial_states;
+  a.dv = dv;
+  a.wide_dv = wide_rows(dv, {0, 0}, headdim, es);
+  a.dq = dq;
+  a.dk = dk;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  if (e == cudaSuccess) e = bf ? launch_reverse<bf16>(a, st) : launch_reverse<float>(a, st);
+  if (e == cudaSuccess) e = bf ? launch_grads<bf16>(a, st) : launch_grads<float>(a, st);
+  return cuda_bad(e, "delta_scan_bwd launch");
+}
+
+int ssd_delta_decode_step(const void* q, const void* k, const void* v, const float* g,
+                          const float* beta, float scale, float* state, int64_t batch, int nheads,
+                          int headdim, int dstate, int ngroups, ssd_dtype_t dtype, void* out,
+                          void* stream) {
+  const int c = check_sizes(batch, 1, nheads, headdim, dstate, ngroups, dtype);
+  if (c != SSD_OK) return c;
+  if (!q || !k || !v || !g || !beta || !state || !out)
+    return bad(SSD_ERR_NULL, "q, k, v, g, beta, state and out are required");
+  const size_t es = dtype == SSD_DTYPE_BF16 ? 2 : 4;
+  if (off(q, es) || off(k, es) || off(v, es) || off(out, es) || off(g, 4) || off(beta, 4) ||
+      off(state, 4))
+    return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
+  if (!(fabsf(scale) <= 3.0e38f)) return bad(SSD_ERR_ARG, "scale must be finite");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_bad(dtype == SSD_DTYPE_BF16
+                      ? run_step<bf16>(q, k, v, g, beta, scale, state, batch, nheads, headdim,
+                                       dstate, ngroups, out, st)
+                      : run_step<float>(q, k, v, g, beta, scale, state, batch, nheads, headdim,
+                                        dstate, ngroups, out, st),
+                  "delta_decode_step launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,307 @@
+"""The gated delta rule on the GPU against its recurrence in 64 bits."""
+import pytest
+import torch
+
+import delta_testutil as du
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import selective_state_space_05_gb300 as m
+    return m
+
+
+def split(d):
+    d = du.to(d, "cuda")
+    return tuple(d[n] for n in du.NAMES), dict(initial_states=d["initial_states"],
+                                               seq_idx=d["seq_idx"])
+
+
+def check(ssd, d, dtype, dfinal=True, scale=None, seed=1):
+    """Forward, gradients with and without what the forward keeps, one input."""
+    ins, kw = split(d)
+    B, L, H, V = d["v"].shape
+    gen = torch.Generator().manual_seed(seed)
+    dout = torch.randn(B, L, H, V, generator=gen).to(dtype)
+    df = torch.randn(B, H, V, d["q"].shape[3], generator=gen) if dfinal else None
+    want, fin, grads = du.reference(d, dout, df, scale)
+    out, final, saved = ssd.delta_scan_fwd(*ins, scale=scale, return_final_states=True, save=True,
+                                           **kw)
+    du.close(out, want, dtype, "out")
+    du.close(final, fin, dtype, "final_states")
+    assert torch.equal(out, ssd.delta_scan_fwd(*ins, scale=scale, **kw))
+    bkw = dict(scale=scale, dfinal_states=None if df is None else df.cuda(), **kw)
+    got = ssd.delta_scan_bwd(dout.cuda(), *ins, saved=saved, **bkw)
+    for n, ref in grads.items():
+        du.close(got[n], ref, dtype, n)
+    again = ssd.delta_scan_bwd(dout.cuda(), *ins, **bkw)
+    for n in got:
+        assert (got[n] is None and again[n] is None) or torch.equal(got[n], again[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,L,G,H,V,K", [
+    (1, 1, 1, 1, 16, 16), (2, 2, 1, 2, 1, 1), (1, 31, 2, 2, 8, 8), (1, 32, 1, 1, 64, 64),
+    (2, 33, 1, 3, 17, 65), (1, 63, 2, 4, 130, 40), (1, 64, 1, 1, 128, 128), (3, 65, 2, 2, 24, 127),
+    (1, 129, 3, 3, 33, 64), (2, 200, 1, 4, 48, 128), (1, 257, 2, 2, 200, 100)])
+def test_sizes(ssd, dtype, B, L, G, H, V, K):
+    check(ssd, du.inputs(B, L, G, H, V, K, dtype, seed=L * 131 + K), dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("docs", [[1] * 40, [31, 1, 1, 31, 1, 70], [64, 64, 7], [3, 130, 2]])
+def test_documents(ssd, dtype, docs):
+    check(ssd, du.inputs(2, sum(docs), 1, 2, 32, 32, dtype, seed=len(docs), docs=docs), dtype)
+    check(ssd, du.inputs(1, sum(docs), 2, 2, 16, 64, dtype, init=False, docs=docs), dtype,
+          dfinal=False, scale=0.7)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_strong_decays(ssd, dtype):
+    """Decays to e^-30 beside weak ones: those of the tokens after them keep
+    their bits.  Below -104 the state starts anew, as in fp32."""
+    check(ssd, du.inputs(1, 150, 2, 2, 32, 32, dtype, seed=5, strong=0.3), dtype)
+    for low in (-105.0, -1e4, -float("inf")):
+        d = du.inputs(1, 100, 1, 2, 32, 32, dtype, seed=6)
+        e = du.inputs(1, 100, 1, 2, 32, 32, dtype, seed=6, docs=[7, 50, 43])
+        d["g"][:, [7, 57]] = low
+        e["g"][:, [7, 57]] = 0.0
+        a, b = (ssd.delta_scan_fwd(*split(x)[0], return_final_states=True, **split(x)[1])
+                for x in (d, e))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        dout = torch.ones_like(a[0])
+        ga, gb = (ssd.delta_scan_bwd(dout, *split(x)[0], **split(x)[1]) for x in (d, e))
+        for n in ga:
+            assert torch.equal(ga[n], gb[n]), n
+        assert (ga["dg"][:, [7, 57]] == 0).all()
+
+
+def test_growing_and_plain_states(ssd):
+    """g above 0 grows the state; beta 0 leaves it; g = 0 and beta = 1 is the
+    rule without gates."""
+    d = du.inputs(1, 90, 1, 2, 32, 48, F32, seed=8)
+    d["g"] = d["g"].abs() * 0.05
+    d["beta"][:, 20:40] = 0.0
+    check(ssd, d, F32)
+    d = du.inputs(1, 90, 1, 2, 32, 48, BF, seed=9)
+    d["g"].zero_()
+    d["beta"].fill_(1.0)
+    check(ssd, d, BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pad", [0, 8, 1])
+def test_views_of_a_projection(ssd, dtype, pad):
+    """q, k and v as slices of one tensor, on and off 16 bytes."""
+    B, L, G, H, V, K = 2, 70, 2, 4, 24, 40
+    d = du.inputs(B, L, G, H, V, K, dtype, seed=11)
+    parts = [d[n].flatten(2) for n in "qkv"]
+    wide = torch.cat([torch.zeros(B, L, pad, dtype=dtype)] + parts, -1).cuda()
+    q, k, v = wide[..., pad:].split([p.shape[-1] for p in parts], -1)
+    q, k, v = q.unflatten(-1, (G, K)), k.unflatten(-1, (G, K)), v.unflatten(-1, (H, V))
+    assert not q.is_contiguous()
+    ins, kw = split(d)
+    dout = torch.randn(B, L, H, V, device="cuda").to(dtype)
+    assert torch.equal(ssd.delta_scan_fwd(q, k, v, *ins[3:], **kw), ssd.delta_scan_fwd(*ins, **kw))
+    a = ssd.delta_scan_bwd(dout, q, k, v, *ins[3:], **kw)
+    b = ssd.delta_scan_bwd(dout, *ins, **kw)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    # a token for all rows, and a batch row for all
+    one = d["k"][:, :1].cuda().expand(-1, L, -1, -1)
+    assert torch.equal(ssd.delta_scan_fwd(ins[0], one, *ins[2:], **kw),
+                       ssd.delta_scan_fwd(ins[0], one.contiguous(), *ins[2:], **kw))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pieces_of_a_sequence(ssd, dtype):
+    """A sequence in pieces from final to initial states, then token by token,
+    is the whole."""
+    B, L, G, H, V, K = 2, 100, 2, 4, 40, 56
+    d = du.inputs(B, L, G, H, V, K, dtype, seed=12)
+    ins, kw = split(d)
+    want, fin = du.reference(d)
+    state, outs = kw["initial_states"], []
+    for a, b in ((0, 1), (1, 30), (30, 80)):
+        o, state = ssd.delta_scan_fwd(*(t[:, a:b].contiguous() for t in ins), initial_states=state,
+                                      return_final_states=True)
+        outs.append(o)
+    state = state.clone()
+    for t in range(80, L):
+        outs.append(ssd.delta_decode_step(*(x[:, t].contiguous() for x in ins), state)[:, None])
+    du.close(torch.cat(outs, 1), want, dtype, "out")
+    du.close(state, fin, dtype, "state")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,G,H,V,K", [(1, 1, 1, 1, 1), (3, 2, 4, 33, 37), (2, 1, 2, 64, 128),
+                                       (9, 3, 3, 100, 126), (1, 1, 1, 300, 4)])
+def test_step(ssd, dtype, B, G, H, V, K):
+    d = du.inputs(B, 1, G, H, V, K, dtype, seed=V + K)
+    want, fin = du.reference(d)
+    ins = [d[n][:, 0].contiguous().cuda() for n in du.NAMES]
+    store = torch.empty(d["initial_states"].numel() + 1, device="cuda")
+    for at in (0, 1):   # on and off 16 bytes
+        state = store[at:at + d["initial_states"].numel()].view(d["initial_states"].shape)
+        state.copy_(d["initial_states"])
+        out = ssd.delta_decode_step(*ins, state)
+        du.close(out, want[:, 0], dtype, "out")
+        du.close(state, fin, F32, "state")
+    assert state._version == 4     # the two copies into its store, and two steps
+
+
+def test_step_keeps_infinities_to_their_rows(ssd):
+    d = du.to(du.inputs(1, 1, 1, 2, 8, 16, F32, seed=3), "cuda")
+    ins = [d[n][:, 0].contiguous() for n in du.NAMES]
+    state, other = d["initial_states"].clone(), d["initial_states"].clone()
+    ins[2][0, 0, 3] = float("nan")
+    out = ssd.delta_decode_step(*ins, state)
+    ins[2][0, 0, 3] = 0.0
+    want = ssd.delta_decode_step(*ins, other)
+    bad = torch.zeros(1, 2, 8, dtype=torch.bool, device="cuda")
+    bad[0, 0, 3] = True
+    assert torch.equal(torch.isnan(out), bad) and torch.equal(out[~bad], want[~bad])
+    assert torch.equal(torch.isnan(state).any(-1), bad) and torch.equal(state[~bad], other[~bad])
+
+
+def test_gradient_against_differences(ssd):
+    """The gradients in fp32 along random directions against central differences
+    of the scan in 64 bits (truncation h^2, far below the bound)."""
+    d = du.inputs(1, 70, 1, 2, 16, 24, F32, seed=21)
+    ins, kw = split(d)
+    dout = torch.randn(1, 70, 2, 16)
+    got = ssd.delta_scan_bwd(dout.cuda(), *ins, **kw)
+    base = {k: v if v is None else v.double() for k, v in d.items()}
+    gen = torch.Generator().manual_seed(2)
+    for n in du.NAMES + ("initial_states",):
+        u = torch.randn(base[n].shape, generator=gen, dtype=torch.float64)
+        h = 1e-5
+        f = [(du.recurrence(dict(base, **{n: base[n] + s * h * u}))[0] * dout.double()).sum()
+             for s in (1, -1)]
+        diff = float(f[0] - f[1]) / (2 * h)
+        g = got[("d_" if n == "initial_states" else "d") + n].double().cpu()
+        assert abs(float((g * u).sum()) - diff) <= du.COMPUTE[F32] * float(g.norm() * u.norm()), n
+
+
+def test_autograd(ssd):
+    d = du.inputs(2, 50, 1, 2, 16, 24, F32, seed=30, docs=[20, 30])
+    dout, df = torch.randn(2, 50, 2, 16), torch.randn(2, 2, 16, 24)
+    _, _, want = du.reference(d, dout, df)
+    c = du.to(d, "cuda")
+    names = du.NAMES + ("initial_states",)
+    ins = {n: c[n].requires_grad_(True) for n in names}
+    out, fin = ssd.delta_scan(*(ins[n] for n in du.NAMES), initial_states=ins["initial_states"],
+                              seq_idx=c["seq_idx"], return_final_states=True)
+    loss = (out * dout.cuda()).sum() + (fin * df.cuda()).sum()
+    for n, g in zip(names, torch.autograd.grad(loss, list(ins.values()), retain_graph=True)):
+        du.close(g, want[("d_" if n == "initial_states" else "d") + n], F32, n)
+    # only the final states, and only some inputs
+    g = torch.autograd.grad((fin * df.cuda()).sum(), [ins["v"], ins["q"]])
+    _, _, want = du.reference(d, torch.zeros_like(dout), df)
+    du.close(g[0], want["dv"], F32, "dv")
+    assert (g[1] == 0).all()
+    with torch.no_grad():
+        assert not ssd.delta_scan(*(ins[n] for n in du.NAMES)).requires_grad
+
+
+def test_no_tokens(ssd):
+    for B, L in ((0, 5), (2, 0)):
+        d = du.inputs(B, L, 1, 2, 8, 16, BF)
+        c = du.to(d, "cuda")
+        ins = {n: c[n].requires_grad_(True) for n in du.NAMES + ("initial_states",)}
+        out, fin = ssd.delta_scan(*(ins[n] for n in du.NAMES), return_final_states=True,
+                                  initial_states=ins["initial_states"])
+        assert out.shape == d["v"].shape and torch.equal(fin, c["initial_states"])
+        (out.sum() + 2 * fin.sum()).backward()
+        assert all(t.grad is not None and t.grad.shape == t.shape for t in ins.values())
+        assert (ins["initial_states"].grad == 2).all()
+        with pytest.raises(RuntimeError, match="ARG"):
+            ssd.delta_scan_fwd(*(c[n] for n in du.NAMES))
+
+
+def test_graph_streams_and_given_tensors(ssd):
+    """A captured forward and backward, replayed on new inputs, two graphs whose
+    workspaces are their own, a side stream, and outputs that are given."""
+    d = [du.inputs(2, 130, 2, 2, 32, 64, BF, seed=s) for s in (40, 41)]
+    (ins, kw), (ins2, kw2) = split(d[0]), split(d[1])
+    dout = torch.randn(2, 130, 2, 32, device="cuda").to(BF)
+
+    def run(i, k):
+        o, f, saved = ssd.delta_scan_fwd(*i, return_final_states=True, save=True, **k)
+        return [o, f] + list(ssd.delta_scan_bwd(dout, *i, saved=saved, **k).values())
+
+    want, want2 = run(ins, kw), run(ins2, kw2)
+    static, skw = [t.clone() for t in ins], {n: None if t is None else t.clone()
+                                             for n, t in kw.items()}
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(run(static, skw))
+        graphs.append(graph)
+    graphs[0].replay()
+    graphs[1].replay()
+    graphs[0].replay()
+    for a, b, c in zip(want, got[0], got[1]):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    for a, b in zip(static, ins2):
+        a.copy_(b)
+    skw["initial_states"].copy_(kw2["initial_states"])
+    graphs[0].replay()
+    for a, b in zip(want2, got[0]):
+        assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, fin = torch.empty_like(want[0]), torch.empty_like(want[1])
+    o, f = ssd.delta_scan_fwd(*ins, out=out, final_states=fin, return_final_states=True,
+                              stream=side, **kw)
+    side.synchronize()
+    assert o is out and f is fin and out._version == 1 and fin._version == 1
+    assert torch.equal(out, want[0]) and torch.equal(fin, want[1])
+    # an output off 16 bytes
+    store = torch.zeros(out.numel() + 2, dtype=BF, device="cuda")
+    view = store[1:-1].view(out.shape)
+    ssd.delta_scan_fwd(*ins, out=view, **kw)
+    assert torch.equal(view, out) and store[0] == 0 and store[-1] == 0
+
+
+def test_long_sequences_keep_their_accuracy(ssd):
+    """5000 tokens that hardly decay: the state's rounding does not add up."""
+    for dtype in (BF, F32):
+        d = du.inputs(1, 5000, 1, 1, 16, 32, dtype, seed=50)
+        d["g"] *= 1e-3
+        ins, kw = split(d)
+        want, fin = du.reference(d)
+        out, final = ssd.delta_scan_fwd(*ins, return_final_states=True, **kw)
+        du.close(out, want, dtype, "out")
+        du.close(final, fin, dtype, "final_states")
+
+
+def test_refusals(ssd):
+    d = du.to(du.inputs(1, 10, 1, 2, 16, 16, F32), "cuda")
+    ins = [d[n] for n in du.NAMES]
+
+    def swap(i, t):
+        return [t if j == i else x for j, x in enumerate(ins)]
+
+    for i, t in ((0, ins[0].half()), (1, ins[1].to(BF)), (2, ins[2].cpu()), (3, ins[3].double()),
+                 (4, ins[4][:, :-1]), (1, ins[1][..., ::2]), (3, ins[3].transpose(1, 2))):
+        with pytest.raises(ValueError):
+            ssd.delta_scan_fwd(*swap(i, t))
+    with pytest.raises(ValueError):
+        ssd.delta_scan_fwd(*ins, initial_states=d["initial_states"].half())
+    with pytest.raises(ValueError):
+        ssd.delta_scan_fwd(*ins, seq_idx=torch.zeros(1, 10, dtype=torch.int64, device="cuda"))
+    with pytest.raises(RuntimeError, match="WORKSPACE"):
+        ssd.delta_scan_fwd(*ins, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    out, saved = ssd.delta_scan_fwd(*ins, save=True)
+    with pytest.raises(RuntimeError, match="WORKSPACE"):
+        ssd.delta_scan_bwd(out, *ins, saved=saved[:-256])
+    with pytest.raises(ValueError):
+        ssd.delta_scan_bwd(out.transpose(1, 2), *ins)
+    with pytest.raises(ValueError):
+        ssd.delta_decode_step(*(x[:, 0] for x in ins), d["initial_states"].transpose(2, 3))
