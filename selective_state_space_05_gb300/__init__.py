@@ -15,3 +15,4 @@ from .block import (add_rmsnorm, add_rmsnorm_bwd, add_rmsnorm_fwd,  # noqa: F401
                     linear_bwd, linear_fwd)
 from .delta import (delta_abi_version, delta_decode_step, delta_scan,  # noqa: F401
                     delta_scan_bwd, delta_scan_fwd)
+from .optim import adamw_moments, adamw_state, adamw_step, optim_abi_version  # noqa: F401

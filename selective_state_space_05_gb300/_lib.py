@@ -111,6 +111,13 @@ SIGNATURES.update({
                                    _vp]),
 })
 
+# include/ssd_optim.h
+SIGNATURES.update({
+    "ssd_optim_abi_version": (_i, []),
+    "ssd_adamw_step": (_i, [_vp] * 10 + [_i, _i, _vp, _vp]),
+    "ssd_adamw_moments": (_i, [_vp] * 7 + [_i, _vp]),
+})
+
 _LIB = None
 
 
