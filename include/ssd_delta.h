@@ -53,10 +53,13 @@ int ssd_delta_abi_version(void);
  * keep: nonzero if the workspace is to hold what ssd_delta_scan_bwd would
  * otherwise compute again (each chunk's triangular inverse and scores, first
  * state and corrections): it is then passed there as `saved`, unchanged.
+ * aligned (workspace queries): nonzero if q, k and v (and for the backward dout)
+ * have every token's rows on 16 bytes (pointer, strides and row lengths) and no
+ * stride of 0 along a length above 1; others may be copied in the workspace.
  * workspace_bytes: 0 on bad sizes. */
 size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int nheads,
                                       int headdim, int dstate, int ngroups,
-                                      ssd_dtype_t dtype, int keep);
+                                      ssd_dtype_t dtype, int keep, int aligned);
 int ssd_delta_scan_fwd(const void *q, ssd_stride_t q_stride, const void *k,
                        ssd_stride_t k_stride, const void *v,
                        ssd_stride_t v_stride, const float *g, const float *beta,

@@ -3,8 +3,10 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <mutex>
+
 #include "../../include/ssd_delta.h"
-#include "ssd_delta.cuh"
+#include "ssd_delta_tc.cuh"
 #include "ssd_row.cuh"
 
 namespace ssd {
@@ -37,7 +39,7 @@ int check_sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   return SSD_OK;
 }
 
-Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
+Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype, bool tcok = true) {
   Args a = {};
   const int C = dtype == SSD_DTYPE_BF16 ? Mode<bf16>::C : Mode<float>::C;
   a.L = L;
@@ -48,8 +50,40 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   a.V = V;
   a.nc = (int)((L + C - 1) / C);
   a.KP = K <= 64 ? 64 : 128;
-  a.VP = (V + 15) / 16 * 16;
+  a.tc = tcok && dtype == SSD_DTYPE_BF16 && V >= kTcHeaddim;
+  a.VP = a.tc ? (V + 127) / 128 * 128 : (V + 15) / 16 * 16;
+  a.qcols = a.kcols = K;
+  a.vcols = a.docols = V;
   return a;
+}
+
+// The tcgen05 kernels read rows by tensor maps: on 16 bytes, strides above 0.
+// Others are first copied to dense rows of a multiple of eight columns.
+int up8(int n) { return (n + 7) & ~7; }
+size_t packed_bytes(const Args& a, int rows, int cols) {
+  return up((size_t)a.B * a.L * rows * up8(cols) * 2);
+}
+__global__ void __launch_bounds__(256)
+    pack_kernel(const bf16* __restrict__ src, TokStride s, int64_t L, int64_t n, int rows, int cols,
+                int wide, bf16* __restrict__ dst) {
+  const int64_t total = n * rows * wide;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int c = (int)(i % wide);
+    const int64_t r = i / wide % rows, t = i / wide / rows;
+    dst[i] = c < cols ? src[toff(s, t / L, t % L) + r * cols + c] : __float2bfloat16_rn(0.f);
+  }
+}
+cudaError_t pack(const Args& a, const void** src, TokStride* s, int* ncols, int rows, char* to,
+                 cudaStream_t st) {
+  const int cols = *ncols, wide = up8(cols);
+  const int64_t n = (int64_t)a.B * a.L, ctas = (n * rows * wide + 255) / 256;
+  pack_kernel<<<(unsigned)(ctas < 16384 ? ctas : 16384), 256, 0, st>>>(
+      static_cast<const bf16*>(*src), *s, a.L, n, rows, cols, wide, reinterpret_cast<bf16*>(to));
+  *src = to;
+  *s = {a.L * rows * wide, (int64_t)rows * wide};
+  *ncols = wide;
+  return cudaGetLastError();
 }
 
 // The forward's pieces of a workspace at `base`, and how many bytes they take.
@@ -64,10 +98,12 @@ size_t carve(Args& a, void* base, bool keep) {
     at += up(bytes);
     return r;
   };
-  a.T = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
-  a.P = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
+  a.T = a.P = a.S0 = a.X = nullptr;
+  a.vec = nullptr;
+  if (a.tc && !keep) return 0;   // T and P stay on the SM
+  a.T = reinterpret_cast<bf16*>(take(n * NT * C * C * 2 * (a.tc ? 2 : 1)));   // (P beside T)
+  if (!a.tc) a.P = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
   a.vec = reinterpret_cast<float*>(take(n * vec_floats<C>() * 4));
-  a.S0 = a.X = nullptr;
   if (keep) {
     a.S0 = reinterpret_cast<bf16*>(take(n * NT * a.VP * a.KP * 2));
     a.X = reinterpret_cast<bf16*>(take(n * NT * C * a.VP * 2));
@@ -105,6 +141,11 @@ size_t bwd_bytes(Args& a, int dtype, void* base) {
 bool bad_stride(ssd_stride_t s) {
   return s.batch < 0 || s.token < 0 || s.batch > (1LL << 40) || s.token > (1LL << 40);
 }
+// Whether a tensor map takes such rows (a stride of 0 only along a length of 1).
+bool mapped(const Args& a, int wide, TokStride s) {
+  const int64_t most = 1LL << 38;
+  return wide && (s.t > 0 || a.L == 1) && (s.b > 0 || a.B == 1) && s.t <= most && s.b <= most;
+}
 // Whether rows of `n` elements at these strides lie on 16 bytes.
 int wide_rows(const void* p, ssd_stride_t s, int n, int esize) {
   return !off(p, 16) && (s.batch * esize) % 16 == 0 && (s.token * esize) % 16 == 0 &&
@@ -141,8 +182,27 @@ int fill_inputs(Args& a, const void* q, ssd_stride_t sq, const void* k, ssd_stri
 
 template <typename T>
 cudaError_t run_forward(const Args& a, cudaStream_t st) {
+  if (a.tc) return launch_tc_forward(a, st);
   const cudaError_t e = launch_prepare<T>(a, st);
   return e != cudaSuccess ? e : launch_forward<T>(a, st);
+}
+
+bool inputs_mapped(const Args& a) {
+  return mapped(a, a.wide_q, a.sq) && mapped(a, a.wide_k, a.sk) && mapped(a, a.wide_v, a.sv);
+}
+size_t pack_bytes(const Args& a, bool aligned) {
+  return !a.tc || aligned
+             ? 0
+             : 2 * packed_bytes(a, a.G, a.K) + packed_bytes(a, a.H, a.V);
+}
+// Copies q, k and v where they are not mapped, to pack_bytes at `at`.
+cudaError_t pack_inputs(Args& a, char* at, cudaStream_t st) {
+  if (!a.tc || inputs_mapped(a)) return cudaSuccess;
+  const size_t n = packed_bytes(a, a.G, a.K);
+  cudaError_t e = pack(a, &a.q, &a.sq, &a.qcols, a.G, at, st);
+  if (e == cudaSuccess) e = pack(a, &a.k, &a.sk, &a.kcols, a.G, at + n, st);
+  if (e == cudaSuccess) e = pack(a, &a.v, &a.sv, &a.vcols, a.H, at + 2 * n, st);
+  return e;
 }
 
 // One token.  HBM-bound on the fp32 state, read and written once.  A warp takes
@@ -241,6 +301,39 @@ cudaError_t run_step(const void* q, const void* k, const void* v, const float* g
 }
 
 }  // namespace
+
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+}  // namespace
+
+bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
+               bool swizzle) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)L, (cuuint64_t)B};
+  // (a stride along a length of 1 is never walked)
+  cuuint64_t strides[3] = {(cuuint64_t)cols * 2, (cuuint64_t)(s.t > 0 ? s.t : cols) * 2,
+                           (cuuint64_t)(s.b > 0 ? s.b : cols) * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)kC, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace delta
 }  // namespace ssd
 
@@ -251,10 +344,11 @@ extern "C" {
 int ssd_delta_abi_version(void) { return SSD_DELTA_ABI_VERSION; }
 
 size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
-                                      int dstate, int ngroups, ssd_dtype_t dtype, int keep) {
+                                      int dstate, int ngroups, ssd_dtype_t dtype, int keep, int aligned) {
   if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
-  return fwd_bytes(a, dtype, nullptr, keep != 0);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, !keep);
+  const size_t n = fwd_bytes(a, dtype, nullptr, keep != 0) + pack_bytes(a, aligned != 0);
+  return n ? n : 256;
 }
 
 int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_stride_t k_stride,
@@ -265,7 +359,7 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
                        void* workspace, size_t workspace_bytes, void* stream) {
   int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   if (c != SSD_OK) return c;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, !keep);
   c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
                   seq_idx, dtype);
   if (c != SSD_OK) return c;
@@ -273,20 +367,23 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
   if (off(out, dtype == SSD_DTYPE_BF16 ? 2 : 4) || off(final_states, 4))
     return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
   if (off(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if (workspace_bytes < fwd_bytes(a, dtype, workspace, keep != 0))
+  const size_t kept = fwd_bytes(a, dtype, workspace, keep != 0);
+  if (workspace_bytes < kept + pack_bytes(a, inputs_mapped(a)))
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
   a.out = out;
   a.wide_out = wide_rows(out, {0, 0}, headdim, dtype == SSD_DTYPE_BF16 ? 2 : 4);
   a.final = final_states;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_bad(dtype == SSD_DTYPE_BF16 ? run_forward<bf16>(a, st) : run_forward<float>(a, st),
-                  "delta_scan_fwd launch");
+  cudaError_t e = pack_inputs(a, static_cast<char*>(workspace) + kept, st);
+  if (e == cudaSuccess)
+    e = dtype == SSD_DTYPE_BF16 ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
+  return cuda_bad(e, "delta_scan_fwd launch");
 }
 
 size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
                                           int dstate, int ngroups, ssd_dtype_t dtype, int saved) {
   if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, false);
   return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(a, dtype, nullptr, true));
 }
 
@@ -300,7 +397,7 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
                        size_t workspace_bytes, void* stream) {
   int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   if (c != SSD_OK) return c;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, false);
   c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
                   seq_idx, dtype);
   if (c != SSD_OK) return c;

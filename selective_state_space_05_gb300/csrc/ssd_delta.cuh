@@ -37,6 +37,9 @@ template <> struct Mode<float> { static constexpr int C = 32, NT = 3, TI = 3; };
 // whose seq_idx changes.
 constexpr float kReset = -104.f;
 
+// From this headdim on bf16 runs on tcgen05, whose MMAs have 128 channels.
+constexpr int kTcHeaddim = 33;
+
 // Per chunk and head: vectors of C floats each, then e^(G_C) alone.
 enum { kGam, kOnto, kBeta, kGhi, kGlo, kSeg, kVecs };   // e^G, e^(G_C - G), beta, G in two floats
 template <int C> constexpr int vec_floats() { return kVecs * C + 4; }
@@ -45,7 +48,9 @@ struct Args {
   int64_t L;
   int B, H, G, K, V, nc, KP, VP;   // KP: dstate padded to 64 or 128; VP: headdim to 16
   TokStride sq, sk, sv, sdo;
+  int qcols, kcols, vcols, docols;   // dstate and headdim as their rows have them (packed: to 8)
   int wide_q, wide_k, wide_v, wide_do, wide_out, wide_dv;   // rows in 16-byte pieces
+  int tc;       // the tcgen05 kernels and their workspace's layout
   float scale;
   const void *q, *k, *v, *dout;
   const float *g, *beta;

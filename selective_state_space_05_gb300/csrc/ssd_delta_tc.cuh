@@ -1,0 +1,398 @@
+// What the gated delta rule's tcgen05 kernels share: bounded waits, tensor maps,
+// operands in TMEM, and a chunk's triangular inverse.
+//
+// These kernels take bf16 tensors whose rows lie on 16 bytes, 128 headdim channels
+// a CTA: the state's rows are TMEM lanes, so that every product of a chunk has its
+// fp32 factor as A operand in TMEM (two bf16 terms) and keys, queries or the
+// chunk's matrices as B operand in shared memory, as 64-column tiles with the
+// 128-byte swizzle.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "ssd_delta.cuh"
+#include "tc_ptx.cuh"
+
+namespace ssd {
+namespace delta {
+
+constexpr int kC = 64;              // tokens a chunk
+constexpr uint32_t kTile = kC * 128;   // bytes of 64 rows of 64 columns
+constexpr unsigned long long kWaitNs = 2000000000ull;   // limit of any single wait: 2 s
+enum { kErrWait = 1, kErrDrain = 4 };   // bits of the status word (ssd_scan_status)
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// A wait for an mbarrier's phase that gives up after two seconds, or at once when
+// the CTA has given up before: it then records that in `gave_up` (shared) and in
+// the device's status word, and the caller goes on without what it waited for
+// (every later wait returns at once, nothing more is issued, and the launch ends).
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up,
+                                         int* status) {
+  if (tc::mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = now_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait_sleep(bar, parity, 20000)) return;
+    if ((i & 15u) == 0) {
+      if (*gave_up) return;
+      if (now_ns() - t0 > kWaitNs) {
+        *gave_up = 1;
+        atomicOr(status, kErrWait);
+        return;
+      }
+    }
+  }
+}
+// At the end of a launch, for copies or MMAs in flight: not cut short.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) {
+  const unsigned long long t0 = now_ns();
+  while (!tc::mbar_try_wait_sleep(bar, parity, 20000))
+    if (now_ns() - t0 > kWaitNs) {
+      atomicOr(status, kErrDrain);
+      return;
+    }
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// A warp's arrival for what all its lanes have done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
+// 16 values as two terms in pairs: words 0-7 the first, 8-15 the second.  A K step
+// of 16 columns of an A operand stands so in 16 TMEM columns.
+__device__ __forceinline__ void two_terms(const float (&v)[16], uint32_t (&t)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t w[2];
+    split2<2>(v[2 * i], v[2 * i + 1], w);
+    t[i] = w[0];
+    t[8 + i] = w[1];
+  }
+}
+// Products with 16 factors in shared memory (16-byte aligned).
+__device__ __forceinline__ void scale_by(float (&x)[16], const float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 w = *reinterpret_cast<const float4*>(f + 4 * i);
+    x[4 * i] *= w.x;
+    x[4 * i + 1] *= w.y;
+    x[4 * i + 2] *= w.z;
+    x[4 * i + 3] *= w.w;
+  }
+}
+// D (+)= A B over A's K steps [0, STEPS), for term `ta` of A and the tile(s) at b: a
+// K-major descriptor (32 bytes a step inside 64 columns, `half` 16-byte units to
+// the next 64) or an MN-major one (16 rows a step).
+template <int STEPS, bool MN>
+__device__ __forceinline__ void mma_chain(uint32_t d, uint32_t a, int ta, uint64_t b, uint32_t half,
+                                          uint32_t idesc, bool fresh) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks)
+    tc::mma_ts(d, a + ks * 16 + ta * 8,
+               b + (MN ? (uint32_t)ks * 128u : (uint32_t)(ks >> 2) * half + (uint32_t)(ks & 3) * 2u),
+               idesc, !(fresh && ks == 0));
+}
+
+// ------------------------------------------------------------------ a chunk's matrices
+// Transposes an 8 x 8 block of bf16 held as an accumulator's packed pairs.
+__device__ __forceinline__ uint32_t trans8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// A 16 x 16 block [m][n] in two accumulator tiles, negated and transposed, as two
+// terms to rows `row` .. and columns `col` .. of a tile's planes.
+__device__ __forceinline__ void store_block_t(const float (&x)[4], const float (&y)[4],
+                                              unsigned char* base, int row, int col, int lane) {
+  const float* v[2] = {x, y};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)        // eight rows of the result
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {    // eight of its columns
+      uint32_t w[2];
+      split2<2>(-v[j][2 * r], -v[j][2 * r + 1], w);
+      const uint32_t at = tile_at<64>(row + 8 * j + (lane >> 2), (col + 8 * r) >> 3) + (lane & 3) * 4;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        *reinterpret_cast<uint32_t*>(base + t * kTile + at) = trans8(w[t]);
+    }
+}
+constexpr int kDiag = 16 * 20;   // floats of a diagonal block's transpose
+
+// T = (I + A)^-1 for strictly lower A [64][64], by four warps (named barrier `id`):
+// A's blocks below the diagonal as planes, its diagonal blocks transposed in fp32;
+// T as planes, whose blocks above the diagonal are zero already.  The diagonal
+// blocks by substitution, a column a lane; then -T_ii A_ij T_jj, doubling the side
+// twice, transposed, so that each product's result is the next one's A operand.
+__device__ __forceinline__ void invert(unsigned char* t, const unsigned char* a,
+                                       const float* diag, int w, int lane, int id) {
+  {
+    const float* d = diag + w * kDiag;
+    const int c = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = i == c ? 1.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < 15; ++j) {
+#pragma unroll
+      for (int q = (j + 1) / 4; q < 4; ++q) {
+        const float4 f = *reinterpret_cast<const float4*>(d + j * 20 + 4 * q);
+        const float col[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * q + e > j) x[4 * q + e] = fmaf(-col[e], x[j], x[4 * q + e]);
+      }
+    }
+    if (lane < 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bf16 h = __float2bfloat16_rn(x[i]);
+        unsigned char* p = t + tile_at<64>(w * 16 + i, (w * 16 + c) >> 3) + (c & 7) * 2;
+        *reinterpret_cast<bf16*>(p) = h;
+        *reinterpret_cast<bf16*>(p + kTile) = __float2bfloat16_rn(x[i] - __bfloat162float(h));
+      }
+    }
+  }
+  named_sync(id, 128);
+  if (w < 2) {
+    const int r = 32 * w;
+    uint32_t f[2][4];
+    float y[2][4], z[2][4];
+    zero(y);
+    zero(z);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a_from_t(f[i], block_at<64>(saddr(t) + i * kTile, r, r, lane));
+    mma_pair<2, 2, false>(y[0], y[1], f, blockn_at<64>(saddr(a), r + 16, r, lane), kTile);
+    a_from<2>(y[0], y[1], f);
+    mma_pair<2, 2, false>(z[0], z[1], f, blockn_at<64>(saddr(t), r + 16, r + 16, lane), kTile);
+    store_block_t(z[0], z[1], t, r + 16, r, lane);
+  }
+  named_sync(id, 128);
+  {
+    const int m = (w & 1) * 16, n = 32 + (w >> 1) * 16;
+    uint32_t f[2][4];
+    float y[4][4], z[2][4];
+    zero(y);
+    zero(z);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a_from_t(f[i], block_at<64>(saddr(t) + i * kTile, ks * 16, m, lane));
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        mma_pair<2, 2, false>(y[2 * p], y[2 * p + 1], f,
+                              blockn_at<64>(saddr(a), 32 + p * 16, ks * 16, lane), kTile);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      a_from<2>(y[2 * ks], y[2 * ks + 1], f);
+      mma_pair<2, 2, false>(z[0], z[1], f, blockn_at<64>(saddr(t), n, 32 + ks * 16, lane), kTile);
+    }
+    store_block_t(z[0], z[1], t, n, m, lane);
+  }
+}
+
+// A chunk's vectors by one warp, two tokens a lane; g0.. are the lane's tokens'.
+struct Gates {
+  float g[2], be[2];
+  int reset[2];
+};
+__device__ __forceinline__ Gates load_gates(const Args& a, int b, int h, int64_t t0, int lane) {
+  Gates x;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int64_t t = t0 + lane * 2 + e;
+    x.g[e] = x.be[e] = 0.f;
+    x.reset[e] = 0;
+    if (t < a.L) {
+      const int64_t at = ((int64_t)b * a.L + t) * a.H + h;
+      x.g[e] = a.g[at];
+      x.be[e] = a.beta[at];
+      if (a.seq && t > 0) {
+        const int32_t* q = a.seq + (int64_t)b * a.L + t;
+        x.reset[e] = q[0] != q[-1];
+      }
+    }
+  }
+  return x;
+}
+// A sum kept as two floats: the larger and what its rounding left (fp64 would be
+// as exact, but its pipe takes ten times as long here).
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo);
+  Sum2 r;
+  r.hi = s + e;
+  r.lo = e - (r.hi - s);
+  return r;
+}
+__device__ __forceinline__ Sum2 shfl_up2(Sum2 a, int off) {
+  return {__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
+}
+// kGhi, kGlo: G log2(e) in two floats, so that a decay is one ex2 of a difference.
+__device__ __forceinline__ void chunk_vectors(Gates x, float* vec, int lane) {
+  Sum2 s[2], run = {0.f, 0.f};
+  int seg[2], cnt = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (x.g[e] < kReset) {
+      x.g[e] = 0.f;
+      x.reset[e] = 1;
+    }
+    run = add2(run, {x.g[e], 0.f});
+    cnt += x.reset[e];
+    s[e] = run;
+    seg[e] = cnt;
+  }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const Sum2 v = shfl_up2(run, off);
+    const int n = __shfl_up_sync(0xffffffffu, cnt, off);
+    if (lane >= off) {
+      run = add2(v, run);
+      cnt += n;
+    }
+  }
+  const Sum2 total = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+  const int segs = __shfl_sync(0xffffffffu, cnt, 31);
+  Sum2 before = shfl_up2(run, 1);
+  int cbefore = __shfl_up_sync(0xffffffffu, cnt, 1);
+  if (lane == 0) {
+    before = {0.f, 0.f};
+    cbefore = 0;
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = lane * 2 + e;
+    const Sum2 G = add2(before, s[e]);
+    const int sg = cbefore + seg[e];
+    const float rest = (total.hi - G.hi) + (total.lo - G.lo);
+    // G log2(e): the product's rounding and the factor's own tail go to the low part
+    const float hi = G.hi * kLog2e;
+    const float lo = fmaf(G.hi, kLog2e, -hi) + fmaf(G.hi, 1.925963033500e-8f, G.lo * kLog2e);
+    vec[kGam * kC + i] = sg == 0 ? expf(G.hi) : 0.f;
+    vec[kOnto * kC + i] = sg == segs ? expf(rest) : 0.f;
+    vec[kBeta * kC + i] = x.be[e];
+    vec[kGhi * kC + i] = hi;
+    vec[kGlo * kC + i] = lo;
+    vec[kSeg * kC + i] = (float)sg;
+  }
+  if (lane == 0) vec[kVecs * kC] = segs == 0 ? expf(total.hi) : 0.f;
+}
+
+// Two warps of four for k k^T, two for q k^T (64 x 64, lower triangles): a warp has
+// the rows of 16 from 3 and 0 (ODD: 2 and 1), five blocks of 16 x 16, block q in
+// x[2q], x[2q + 1].  ba: the first 64 columns' rows of A, bk: keys' (`next` bytes
+// to the next 64 columns).
+template <int KP, bool ODD>
+__device__ __forceinline__ void pair_products(float (&x)[10][4], uint32_t ba, uint32_t bk,
+                                              uint32_t next, int lane) {
+  constexpr int r0 = ODD ? 2 : 3, r1 = ODD ? 1 : 0;
+  zero(x);
+#pragma unroll
+  for (int ks = 0; ks < KP / 16; ++ks) {
+    const uint32_t off = (ks >> 2) * next;
+    uint32_t f0[4], f1[4], k[r0 + 1][4];
+    ldsm(f0, block_at<64>(ba + off, r0 * 16, (ks & 3) * 16, lane));
+    ldsm(f1, block_at<64>(ba + off, r1 * 16, (ks & 3) * 16, lane));
+#pragma unroll
+    for (int n = 0; n <= r0; ++n) ldsm(k[n], blockn_at<64>(bk + off, n * 16, (ks & 3) * 16, lane));
+#pragma unroll
+    for (int n = 0; n <= r0; ++n) {
+      mma(x[2 * n], f0, k[n][0], k[n][1]);
+      mma(x[2 * n + 1], f0, k[n][2], k[n][3]);
+    }
+#pragma unroll
+    for (int n = 0; n <= r1; ++n) {
+      mma(x[2 * (r0 + 1 + n)], f1, k[n][0], k[n][1]);
+      mma(x[2 * (r0 + 1 + n) + 1], f1, k[n][2], k[n][3]);
+    }
+  }
+}
+// Those products with their decays: A = strictly lower D k k^T beta_j into planes
+// (its diagonal blocks into diag), or P = lower D q k^T scale beta_j, as terms.
+template <bool ODD>
+__device__ __forceinline__ void pair_decays(const float (&x)[10][4], const float* vec, bool keys,
+                                            float scale, unsigned char* planes, float* diag,
+                                            int lane) {
+  constexpr int r0 = ODD ? 2 : 3, r1 = ODD ? 1 : 0;
+  const int g = lane >> 2, t = lane & 3;
+  const float neg = __int_as_float(0xff800000);
+  float hi[4], lo[4], sg[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {   // the two rows of r0, the two of r1
+    const int i = (r < 2 ? r0 : r1) * 16 + g + 8 * (r & 1);
+    hi[r] = vec[kGhi * kC + i];
+    lo[r] = vec[kGlo * kC + i];
+    sg[r] = vec[kSeg * kC + i];
+  }
+#pragma unroll
+  for (int n = 0; n < 2 * (r0 + 1); ++n) {
+    const int j = n * 8 + t * 2;
+    const float2 h = *reinterpret_cast<const float2*>(vec + kGhi * kC + j);
+    const float2 l = *reinterpret_cast<const float2*>(vec + kGlo * kC + j);
+    const float2 s = *reinterpret_cast<const float2*>(vec + kSeg * kC + j);
+    float2 be = *reinterpret_cast<const float2*>(vec + kBeta * kC + j);
+    be.x *= keys ? 1.f : scale;
+    be.y *= keys ? 1.f : scale;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int rb = r < 2 ? r0 : r1, i = rb * 16 + g + 8 * (r & 1);
+      if (n >= 2 * (rb + 1)) continue;
+      const float* v = &x[(r < 2 ? 0 : 2 * (r0 + 1)) + n][2 * (r & 1)];
+      const bool last = n >= 2 * rb;   // the diagonal block
+      const bool n0 = s.x == sg[r] && (!last || (keys ? i > j : i >= j));
+      const bool n1 = s.y == sg[r] && (!last || (keys ? i > j + 1 : i >= j + 1));
+      const float d0 = ex2(n0 ? (hi[r] - h.x) + (lo[r] - l.x) : neg);
+      const float d1 = ex2(n1 ? (hi[r] - h.y) + (lo[r] - l.y) : neg);
+      const float y0 = n0 ? v[0] * (d0 * be.x) : 0.f;
+      const float y1 = n1 ? v[1] * (d1 * be.y) : 0.f;
+      if (keys && last) {
+        float* p = diag + rb * kDiag + (j - rb * 16) * 20 + i - rb * 16;
+        p[0] = y0;
+        p[20] = y1;
+      } else {
+        uint32_t m[2];
+        split2<2>(y0, y1, m);
+        unsigned char* p = planes + tile_at<64>(i, j >> 3) + (j & 7) * 2;
+        *reinterpret_cast<uint32_t*>(p) = m[0];
+        *reinterpret_cast<uint32_t*>(p + kTile) = m[1];
+      }
+    }
+  }
+}
+
+// A bf16 tensor [batch, seqlen, rows, cols] as a map of boxes of 64 columns of one
+// row of 64 tokens.
+bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
+               bool swizzle);
+
+// A device's status word (after the stream's work), cleared if asked.
+template <typename W>
+int read_status(W& word, int reset, cudaStream_t st, int* bits) {
+  int h = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&h, word, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && reset && h != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
+  *bits = h;
+  return (int)e;
+}
+
+cudaError_t launch_tc_forward(const Args& a, cudaStream_t st);
+
+}  // namespace delta
+}  // namespace ssd

@@ -59,6 +59,16 @@ def _inputs(q, k, v, g, beta, scale, initial_states, seq_idx):
     return args, (B, L, H, V, K, G), dt, dev
 
 
+def _aligned(*tensors) -> int:
+    """The C calls' `aligned` of [batch, seqlen, rows, columns] tensors."""
+    for t in tensors:
+        e, s, n = t.element_size(), t.stride(), t.shape
+        if (t.data_ptr() | s[0] * e | s[1] * e | n[3] * e) & 15 or (
+                n[0] > 1 and s[0] == 0) or (n[1] > 1 and s[1] == 0):
+            return 0
+    return 1
+
+
 def delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                    beta: torch.Tensor, *, scale: Optional[float] = None,
                    initial_states: Optional[torch.Tensor] = None,
@@ -94,7 +104,8 @@ def delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
         final_states = _empty((B, H, V, K), _F32, dev, stream)
     keep = 1 if save else 0
     ws, ws_bytes, hold = _workspace(
-        _call("ssd_delta_scan_workspace_bytes")(B, L, H, V, K, G, dt, keep), workspace, dev, stream)
+        _call("ssd_delta_scan_workspace_bytes")(B, L, H, V, K, G, dt, keep, _aligned(q, k, v)),
+        workspace, dev, stream)
     code = _call("ssd_delta_scan_fwd")(*args, B, L, H, V, K, G, dt, out.data_ptr(),
                                        _ptr(final_states), keep, ws, ws_bytes, st)
     if code:
