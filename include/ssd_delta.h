@@ -82,7 +82,7 @@ int ssd_delta_scan_fwd(const void *q, ssd_stride_t q_stride, const void *k,
 size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen,
                                           int nheads, int headdim, int dstate,
                                           int ngroups, ssd_dtype_t dtype,
-                                          int saved);
+                                          int saved, int aligned);
 int ssd_delta_scan_bwd(const void *dout, const float *dfinal_states,
                        const void *q, ssd_stride_t q_stride, const void *k,
                        ssd_stride_t k_stride, const void *v,

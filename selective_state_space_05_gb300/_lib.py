@@ -105,7 +105,7 @@ SIGNATURES.update({
     "ssd_delta_abi_version": (_i, []),
     "ssd_delta_scan_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i, _i, _i, _i]),
     "ssd_delta_scan_fwd": (_i, _delta_in + [_vp, _vp, _i, _vp, _sz, _vp]),
-    "ssd_delta_scan_bwd_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i, _i, _i]),
+    "ssd_delta_scan_bwd_workspace_bytes": (_sz, [_i64, _i64, _i, _i, _i, _i, _i, _i, _i]),
     "ssd_delta_scan_bwd": (_i, [_vp, _vp] + _delta_in + [_vp, _sz] + [_vp] * 7 + [_sz, _vp]),
     "ssd_delta_decode_step": (_i, [_vp, _vp, _vp, _vp, _vp, _f, _vp, _i64, _i, _i, _i, _i, _i, _vp,
                                    _vp]),

@@ -278,11 +278,11 @@ int ssd_scan_status(int reset, void* stream) {
   g_err[0] = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int (*const words[])(int, cudaStream_t, int*) = {ssd::fused_status, ssd::tc32_status,
-                                                   ssd::linear_status};
-  int bits[3] = {};
+                                                   ssd::linear_status, ssd::delta::status};
+  int bits[4] = {};
   // all are read before any is cleared: an error in between loses none
   for (int pass = 0; pass < (reset ? 2 : 1); ++pass)
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
       if (pass == 1 && bits[i] == 0) continue;
       int now = 0;
       const int e = words[i](pass, st, &now);
@@ -290,7 +290,7 @@ int ssd_scan_status(int reset, void* stream) {
       bits[i] |= now;
     }
   char m[sizeof(g_err)];
-  if (ssd::status_message(bits[0] | bits[1], bits[2], m, sizeof(m)))
+  if (ssd::status_message(bits[0] | bits[1] | bits[3], bits[2], m, sizeof(m)))
     return fail(SSD_ERR_TIMEOUT, "%s", m);
   return SSD_OK;
 }

@@ -151,6 +151,11 @@ int tc32_status(int reset, cudaStream_t st, int* bits);
 // The same for the projections' product kernel (ssd_linear.cu).
 int linear_status(int reset, cudaStream_t st, int* bits);
 
+namespace delta {
+// The same for the gated delta rule's tensor-core kernels.
+int status(int reset, cudaStream_t st, int* bits);
+}  // namespace delta
+
 // Device-wide status of the fused kernel's bounded waits: the error bits
 // recorded since the last reset into *bits (0: none); synchronises st.
 // Returns 0 or the cudaError_t of a failed copy.

@@ -39,7 +39,7 @@ int check_sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   return SSD_OK;
 }
 
-Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype, bool tcok = true) {
+Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   Args a = {};
   const int C = dtype == SSD_DTYPE_BF16 ? Mode<bf16>::C : Mode<float>::C;
   a.L = L;
@@ -50,7 +50,7 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype, bool tco
   a.V = V;
   a.nc = (int)((L + C - 1) / C);
   a.KP = K <= 64 ? 64 : 128;
-  a.tc = tcok && dtype == SSD_DTYPE_BF16 && V >= kTcHeaddim;
+  a.tc = dtype == SSD_DTYPE_BF16 && V >= kTcHeaddim;
   a.VP = a.tc ? (V + 127) / 128 * 128 : (V + 15) / 16 * 16;
   a.qcols = a.kcols = K;
   a.vcols = a.docols = V;
@@ -100,7 +100,6 @@ size_t carve(Args& a, void* base, bool keep) {
   };
   a.T = a.P = a.S0 = a.X = nullptr;
   a.vec = nullptr;
-  if (a.tc && !keep) return 0;   // T and P stay on the SM
   a.T = reinterpret_cast<bf16*>(take(n * NT * C * C * 2 * (a.tc ? 2 : 1)));   // (P beside T)
   if (!a.tc) a.P = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
   a.vec = reinterpret_cast<float*>(take(n * vec_floats<C>() * 4));
@@ -182,7 +181,10 @@ int fill_inputs(Args& a, const void* q, ssd_stride_t sq, const void* k, ssd_stri
 
 template <typename T>
 cudaError_t run_forward(const Args& a, cudaStream_t st) {
-  if (a.tc) return launch_tc_forward(a, st);
+  if (a.tc) {
+    const cudaError_t e = launch_tc_prepare(a, st);
+    return e != cudaSuccess ? e : launch_tc_forward(a, st);
+  }
   const cudaError_t e = launch_prepare<T>(a, st);
   return e != cudaSuccess ? e : launch_forward<T>(a, st);
 }
@@ -195,6 +197,7 @@ size_t pack_bytes(const Args& a, bool aligned) {
              ? 0
              : 2 * packed_bytes(a, a.G, a.K) + packed_bytes(a, a.H, a.V);
 }
+size_t pack_dout_bytes(const Args& a) { return a.tc ? packed_bytes(a, a.H, a.V) : 0; }
 // Copies q, k and v where they are not mapped, to pack_bytes at `at`.
 cudaError_t pack_inputs(Args& a, char* at, cudaStream_t st) {
   if (!a.tc || inputs_mapped(a)) return cudaSuccess;
@@ -318,6 +321,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 }  // namespace
 
+int status(int reset, cudaStream_t st, int* bits) {
+  int (*const words[])(int, cudaStream_t, int*) = {tc_prepare_status, tc_forward_status,
+                                                   tc_reverse_status, tc_grads_status};
+  int e = 0;
+  *bits = 0;
+  for (auto w : words) {
+    int now = 0;
+    if (e == 0) e = w(reset, st, &now);
+    *bits |= now;
+  }
+  return e;
+}
+
 bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
                bool swizzle) {
   auto enc = encode_fn();
@@ -346,7 +362,7 @@ int ssd_delta_abi_version(void) { return SSD_DELTA_ABI_VERSION; }
 size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
                                       int dstate, int ngroups, ssd_dtype_t dtype, int keep, int aligned) {
   if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, !keep);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   const size_t n = fwd_bytes(a, dtype, nullptr, keep != 0) + pack_bytes(a, aligned != 0);
   return n ? n : 256;
 }
@@ -359,7 +375,7 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
                        void* workspace, size_t workspace_bytes, void* stream) {
   int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   if (c != SSD_OK) return c;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, !keep);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
                   seq_idx, dtype);
   if (c != SSD_OK) return c;
@@ -381,10 +397,11 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
 }
 
 size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int nheads, int headdim,
-                                          int dstate, int ngroups, ssd_dtype_t dtype, int saved) {
+                                          int dstate, int ngroups, ssd_dtype_t dtype, int saved, int aligned) {
   if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, false);
-  return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(a, dtype, nullptr, true));
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
+  return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(a, dtype, nullptr, true)) +
+         (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a));
 }
 
 int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void* q,
@@ -397,7 +414,7 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
                        size_t workspace_bytes, void* stream) {
   int c = check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   if (c != SSD_OK) return c;
-  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype, false);
+  Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
   c = fill_inputs(a, q, q_stride, k, k_stride, v, v_stride, g, beta, scale, initial_states,
                   seq_idx, dtype);
   if (c != SSD_OK) return c;
@@ -412,17 +429,23 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   const size_t kept = fwd_bytes(a, dtype, nullptr, true), own = bwd_bytes(a, dtype, nullptr);
   if (saved && saved_bytes < kept)
     return bad(SSD_ERR_WORKSPACE, "saved is not the workspace of a forward with keep at these sizes");
-  if (workspace_bytes < own + (saved ? 0 : kept)) return bad(SSD_ERR_WORKSPACE, "workspace too small");
-  bwd_bytes(a, dtype, workspace);
-  fwd_bytes(a, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = dtype == SSD_DTYPE_BF16;
-  cudaError_t e = cudaSuccess;
-  if (!saved) e = bf ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
   const int64_t hv = (int64_t)nheads * headdim;
   a.dout = dout;
   a.sdo = {seqlen * hv, hv};
   a.wide_do = wide_rows(dout, {0, 0}, headdim, es);
+  const bool aligned = inputs_mapped(a) && a.wide_do;
+  const size_t used = own + (saved ? 0 : kept);
+  if (workspace_bytes < used + (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a)))
+    return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  bwd_bytes(a, dtype, workspace);
+  fwd_bytes(a, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == SSD_DTYPE_BF16;
+  char* const at = static_cast<char*>(workspace) + used;
+  cudaError_t e = pack_inputs(a, at, st);
+  if (e == cudaSuccess && a.tc && !a.wide_do)
+    e = pack(a, &a.dout, &a.sdo, &a.docols, a.H, at + pack_bytes(a, false), st);
+  if (e == cudaSuccess && !saved) e = bf ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
   a.dfinal = dfinal_states;
   a.dinit = d_initial_states;
   a.dv = dv;
@@ -431,8 +454,13 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   a.dk = dk;
   a.dg = dg;
   a.dbeta = dbeta;
-  if (e == cudaSuccess) e = bf ? launch_reverse<bf16>(a, st) : launch_reverse<float>(a, st);
-  if (e == cudaSuccess) e = bf ? launch_grads<bf16>(a, st) : launch_grads<float>(a, st);
+  if (a.tc) {
+    if (e == cudaSuccess) e = launch_tc_reverse(a, st);
+    if (e == cudaSuccess) e = launch_tc_grads(a, st);
+  } else {
+    if (e == cudaSuccess) e = bf ? launch_reverse<bf16>(a, st) : launch_reverse<float>(a, st);
+    if (e == cudaSuccess) e = bf ? launch_grads<bf16>(a, st) : launch_grads<float>(a, st);
+  }
   return cuda_bad(e, "delta_scan_bwd launch");
 }
 

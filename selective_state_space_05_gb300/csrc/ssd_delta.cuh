@@ -41,7 +41,9 @@ constexpr float kReset = -104.f;
 constexpr int kTcHeaddim = 33;
 
 // Per chunk and head: vectors of C floats each, then e^(G_C) alone.
-enum { kGam, kOnto, kBeta, kGhi, kGlo, kSeg, kVecs };   // e^G, e^(G_C - G), beta, G in two floats
+// e^G, e^(G_C - G), beta, G in two floats, the resets before a token; beta e^(G_C - G)
+// and -e^G
+enum { kGam, kOnto, kBeta, kGhi, kGlo, kSeg, kWrite, kRead, kVecs };
 template <int C> constexpr int vec_floats() { return kVecs * C + 4; }
 
 struct Args {
@@ -295,6 +297,8 @@ template <typename T> cudaError_t launch_prepare(const Args& a, cudaStream_t st)
 template <typename T> cudaError_t launch_forward(const Args& a, cudaStream_t st);
 template <typename T> cudaError_t launch_reverse(const Args& a, cudaStream_t st);
 template <typename T> cudaError_t launch_grads(const Args& a, cudaStream_t st);
+// dq and dk of heads that share them: sums of dq_part and dk_part
+template <typename T> cudaError_t launch_group_sum(const Args& a, cudaStream_t st);
 
 }  // namespace delta
 }  // namespace ssd

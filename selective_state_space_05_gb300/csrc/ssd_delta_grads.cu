@@ -352,6 +352,16 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+template <typename T>
+cudaError_t launch_group_sum(const Args& a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.B * a.L * a.G, ctas = (rows * a.K + 255) / 256;
+  group_sum_kernel<T><<<(unsigned)(ctas < 65536 ? ctas : 65536), 256, 0, st>>>(
+      a.dq_part, a.dk_part, rows, a.H / a.G, a.K, static_cast<T*>(a.dq), static_cast<T*>(a.dk));
+  return cudaGetLastError();
+}
+template cudaError_t launch_group_sum<bf16>(const Args&, cudaStream_t);
+template cudaError_t launch_group_sum<float>(const Args&, cudaStream_t);
+
 template <typename T, int KP>
 cudaError_t grads(const Args& a, cudaStream_t st) {
   using S = GradSmem<T, KP>;
@@ -360,11 +370,7 @@ cudaError_t grads(const Args& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.B * a.H * a.nc;
   grads_kernel<T, KP><<<(unsigned)n, kGradThreads, S::total, st>>>(a);
-  if (a.dq_part) {
-    const int64_t rows = (int64_t)a.B * a.L * a.G, ctas = (rows * a.K + 255) / 256;
-    group_sum_kernel<T><<<(unsigned)(ctas < 65536 ? ctas : 65536), 256, 0, st>>>(
-        a.dq_part, a.dk_part, rows, a.H / a.G, a.K, static_cast<T*>(a.dq), static_cast<T*>(a.dk));
-  }
+  if (a.dq_part) return launch_group_sum<T>(a, st);
   return cudaGetLastError();
 }
 

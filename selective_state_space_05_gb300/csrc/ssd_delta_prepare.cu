@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
       vec[kGam * C + i] = sg == 0 ? expf(hi) : 0.f;
       vec[kOnto * C + i] = sg == segs ? expf((float)(total - G)) : 0.f;
       vec[kBeta * C + i] = be[e];
+      vec[kRead * C + i] = -vec[kGam * C + i];
+      vec[kWrite * C + i] = be[e] * vec[kOnto * C + i];
       vec[kGhi * C + i] = hi;
       vec[kGlo * C + i] = (float)(G - (double)hi);
       vec[kSeg * C + i] = (float)sg;

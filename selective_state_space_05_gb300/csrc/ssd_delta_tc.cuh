@@ -18,39 +18,29 @@ namespace delta {
 
 constexpr int kC = 64;              // tokens a chunk
 constexpr uint32_t kTile = kC * 128;   // bytes of 64 rows of 64 columns
-constexpr unsigned long long kWaitNs = 2000000000ull;   // limit of any single wait: 2 s
 enum { kErrWait = 1, kErrDrain = 4 };   // bits of the status word (ssd_scan_status)
 
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// A wait for an mbarrier's phase that gives up after two seconds, or at once when
-// the CTA has given up before: it then records that in `gave_up` (shared) and in
-// the device's status word, and the caller goes on without what it waited for
-// (every later wait returns at once, nothing more is issued, and the launch ends).
+// A wait for an mbarrier's phase that gives up after kTries polls (each of which
+// suspends the thread for a while: they take seconds, and no wait takes a
+// millisecond), or at once when the CTA has given up before: it then records that
+// in `gave_up` (shared) and in the device's status word, and the caller goes on
+// without what it waited for (every later wait returns at once, nothing more is
+// issued, and the launch ends).  Short, since every role's loop has several.
+constexpr uint32_t kTries = 4000000;
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up,
                                          int* status) {
-  if (tc::mbar_try_wait(bar, parity)) return;
-  const unsigned long long t0 = now_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (tc::mbar_try_wait_sleep(bar, parity, 20000)) return;
-    if ((i & 15u) == 0) {
-      if (*gave_up) return;
-      if (now_ns() - t0 > kWaitNs) {
-        *gave_up = 1;
-        atomicOr(status, kErrWait);
-        return;
-      }
+  for (uint32_t i = 0; !tc::mbar_try_wait(bar, parity); ++i) {
+    if (*gave_up) return;
+    if (i == kTries) {
+      *gave_up = 1;
+      atomicOr(status, kErrWait);
     }
   }
 }
 // At the end of a launch, for copies or MMAs in flight: not cut short.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* status) {
-  const unsigned long long t0 = now_ns();
-  while (!tc::mbar_try_wait_sleep(bar, parity, 20000))
-    if (now_ns() - t0 > kWaitNs) {
+  for (uint32_t i = 0; !tc::mbar_try_wait_sleep(bar, parity, 10000); ++i)
+    if (i == kTries) {
       atomicOr(status, kErrDrain);
       return;
     }
@@ -64,15 +54,42 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d) : "l"(pair_of(a0, a1)), "l"(pair_of(b0, b1)), "l"(pair_of(c0, c1)));
+  unpair(d, x, y);
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float b0, float b1) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(x, y)), "l"(pair_of(b0, b1)));
+  unpair(d, x, y);
+}
+__device__ __forceinline__ void add2p(float& x, float& y, float b0, float b1) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(x, y)), "l"(pair_of(b0, b1)));
+  unpair(d, x, y);
+}
 // 16 values as two terms in pairs: words 0-7 the first, 8-15 the second.  A K step
 // of 16 columns of an A operand stands so in 16 TMEM columns.
 __device__ __forceinline__ void two_terms(const float (&v)[16], uint32_t (&t)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t w[2];
-    split2<2>(v[2 * i], v[2 * i + 1], w);
-    t[i] = w[0];
-    t[8 + i] = w[1];
+    float x = v[2 * i], y = v[2 * i + 1];
+    t[i] = pack2(x, y);
+    add2p(x, y, __uint_as_float((t[i] << 16) ^ 0x80000000u),
+          __uint_as_float((t[i] & 0xFFFF0000u) ^ 0x80000000u));
+    t[8 + i] = pack2(x, y);
   }
 }
 // Products with 16 factors in shared memory (16-byte aligned).
@@ -80,23 +97,91 @@ __device__ __forceinline__ void scale_by(float (&x)[16], const float* f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 w = *reinterpret_cast<const float4*>(f + 4 * i);
-    x[4 * i] *= w.x;
-    x[4 * i + 1] *= w.y;
-    x[4 * i + 2] *= w.z;
-    x[4 * i + 3] *= w.w;
+    mul2(x[4 * i], x[4 * i + 1], w.x, w.y);
+    mul2(x[4 * i + 2], x[4 * i + 3], w.z, w.w);
   }
 }
 // D (+)= A B over A's K steps [0, STEPS), for term `ta` of A and the tile(s) at b: a
 // K-major descriptor (32 bytes a step inside 64 columns, `half` 16-byte units to
 // the next 64) or an MN-major one (16 rows a step).
+// (a_step: TMEM columns a step of A takes, 8 for one with a single term.)
 template <int STEPS, bool MN>
 __device__ __forceinline__ void mma_chain(uint32_t d, uint32_t a, int ta, uint64_t b, uint32_t half,
-                                          uint32_t idesc, bool fresh) {
+                                          uint32_t idesc, bool fresh, int a_step = 16) {
 #pragma unroll
   for (int ks = 0; ks < STEPS; ++ks)
-    tc::mma_ts(d, a + ks * 16 + ta * 8,
+    tc::mma_ts(d, a + ks * a_step + ta * 8,
                b + (MN ? (uint32_t)ks * 128u : (uint32_t)(ks >> 2) * half + (uint32_t)(ks & 3) * 2u),
                idesc, !(fresh && ks == 0));
+}
+
+// SP pieces of 16 of a row of a [B, H, V, K] fp32 state, from column part * SP * 16
+// on; zeros where there is none.
+template <int SP>
+__device__ __forceinline__ void read_row(float (&x)[SP][16], const float* state, int bh, int vr,
+                                         int part, const Args& a) {
+  const float* row = state + ((int64_t)bh * a.V + vr) * a.K;
+  const bool wide = a.K % 4 == 0 && ((uintptr_t)state & 15) == 0;
+#pragma unroll
+  for (int p = 0; p < SP; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (part * SP + p) * 16 + 4 * i;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (state && vr < a.V) {
+        if (wide) {
+          if (k < a.K) f = *reinterpret_cast<const float4*>(row + k);
+        } else {
+          if (k < a.K) f.x = row[k];
+          if (k + 1 < a.K) f.y = row[k + 1];
+          if (k + 2 < a.K) f.z = row[k + 2];
+          if (k + 3 < a.K) f.w = row[k + 3];
+        }
+      }
+      x[p][4 * i] = f.x;
+      x[p][4 * i + 1] = f.y;
+      x[p][4 * i + 2] = f.z;
+      x[p][4 * i + 3] = f.w;
+    }
+}
+template <int SP>
+__device__ __forceinline__ void write_row(const float (&x)[SP][16], float* state, int bh, int vr,
+                                          int part, const Args& a) {
+  if (!state || vr >= a.V) return;
+  float* row = state + ((int64_t)bh * a.V + vr) * a.K;
+  const bool wide = a.K % 4 == 0 && ((uintptr_t)state & 15) == 0;
+#pragma unroll
+  for (int p = 0; p < SP; ++p)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (part * SP + p) * 16 + 4 * i;
+      if (wide) {
+        if (k < a.K)
+          *reinterpret_cast<float4*>(row + k) =
+              make_float4(x[p][4 * i], x[p][4 * i + 1], x[p][4 * i + 2], x[p][4 * i + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (k + e < a.K) row[k + e] = x[p][4 * i + e];
+      }
+    }
+}
+// 16 columns from k on of row vr of chunk id's state, as terms into planes
+// [term][dstate half][row][64] of the workspace, swizzled as the tiles.
+template <int KP>
+__device__ __forceinline__ void keep_row(const uint32_t (&t)[16], bf16* planes, int64_t id, int vr,
+                                         int k, const Args& a) {
+  unsigned char* at = reinterpret_cast<unsigned char*>(planes) +
+                      ((id * 2 * (KP / 64) + (k >> 6)) * a.VP + vr) * 128;
+  const int64_t plane = (int64_t)a.VP * KP * 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int unit = (((k & 63) >> 3) + i) ^ (vr & 7);
+    *reinterpret_cast<uint4*>(at + unit * 16) =
+        make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+    *reinterpret_cast<uint4*>(at + plane + unit * 16) =
+        make_uint4(t[8 + 4 * i], t[9 + 4 * i], t[10 + 4 * i], t[11 + 4 * i]);
+  }
 }
 
 // ------------------------------------------------------------------ a chunk's matrices
@@ -281,8 +366,11 @@ __device__ __forceinline__ void chunk_vectors(Gates x, float* vec, int lane) {
     const float hi = G.hi * kLog2e;
     const float lo = fmaf(G.hi, kLog2e, -hi) + fmaf(G.hi, 1.925963033500e-8f, G.lo * kLog2e);
     vec[kGam * kC + i] = sg == 0 ? expf(G.hi) : 0.f;
-    vec[kOnto * kC + i] = sg == segs ? expf(rest) : 0.f;
+    const float onto = sg == segs ? expf(rest) : 0.f;
+    vec[kOnto * kC + i] = onto;
     vec[kBeta * kC + i] = x.be[e];
+    vec[kRead * kC + i] = sg == 0 ? -expf(G.hi) : 0.f;
+    vec[kWrite * kC + i] = onto * x.be[e];
     vec[kGhi * kC + i] = hi;
     vec[kGlo * kC + i] = lo;
     vec[kSeg * kC + i] = (float)sg;
@@ -320,7 +408,8 @@ __device__ __forceinline__ void pair_products(float (&x)[10][4], uint32_t ba, ui
   }
 }
 // Those products with their decays: A = strictly lower D k k^T beta_j into planes
-// (its diagonal blocks into diag), or P = lower D q k^T scale beta_j, as terms.
+// (its diagonal blocks transposed to diag), or P = lower D q k^T scale beta_j, as
+// terms.
 template <bool ODD>
 __device__ __forceinline__ void pair_decays(const float (&x)[10][4], const float* vec, bool keys,
                                             float scale, unsigned char* planes, float* diag,
@@ -392,7 +481,16 @@ int read_status(W& word, int reset, cudaStream_t st, int* bits) {
   return (int)e;
 }
 
+int tc_prepare_status(int reset, cudaStream_t st, int* bits);
+int tc_forward_status(int reset, cudaStream_t st, int* bits);
+int tc_reverse_status(int reset, cudaStream_t st, int* bits);
+int tc_grads_status(int reset, cudaStream_t st, int* bits);
+
+// The chunks' vectors, T and P; then the chunks one after another.
+cudaError_t launch_tc_prepare(const Args& a, cudaStream_t st);
 cudaError_t launch_tc_forward(const Args& a, cudaStream_t st);
+cudaError_t launch_tc_reverse(const Args& a, cudaStream_t st);
+cudaError_t launch_tc_grads(const Args& a, cudaStream_t st);
 
 }  // namespace delta
 }  // namespace ssd

@@ -2,8 +2,8 @@
 // inputs), one CTA per (batch row, head, 128 channels), chunk after chunk.
 //
 // Transposed as in ssd_delta_fwd.cu: TMEM lane = channel, columns = tokens or
-// dstate.  Per chunk, with S in the registers of eight warps (a row and half of
-// dstate a thread) and as two bf16 terms in TMEM:
+// dstate.  Per chunk, with S in the registers of sixteen warps (a row and a quarter
+// of dstate a thread) and as two bf16 terms in TMEM:
 //   Y | O1 = S [K | Q]^T                 A: S
 //   y = v - e^G Y  -> TMEM               the chain's warps
 //   X = y T^T                            A: y, over Y's columns
@@ -13,11 +13,11 @@
 // and beside it out = scale e^G O1 + O2 (P holds scale and beta).  K^T and K are
 // one tile read in both orders.  Roles, so that only the chain Y - y - X - w - W - S
 // is in a chunk's way:
-//   warps 0-7    the chain, a quarter of the lanes and half of the columns each
-//   warps 8-11   out
-//   warps 12-15  the next chunk's T and P (mma.sync: their operands are 16-row
-//                blocks in registers, and the tcgen05 pipe is the chain's)
-//   warp 16      issues the MMAs;  17: the copies;  18: the chunks' vectors
+//   warps 0-15   the chain, a quarter of the lanes and of the columns each (its
+//                phases are bound by their warps' latency: half as many columns a
+//                warp take about half as long)
+//   warps 16-19  out
+//   warp 20      issues the MMAs;  21: the copies
 // Shared and tensor memory: one CTA an SM.
 #include "ssd_delta_tc.cuh"
 
@@ -25,11 +25,10 @@ namespace ssd {
 namespace delta {
 namespace fwd {
 
-constexpr int kChainWarps = 8, kOutWarp = 8, kPrepWarp = 12, kMmaWarp = 16, kLoadWarp = 17,
-              kVecWarp = 18;
-constexpr int kThreads = 20 * 32;   // (warp 19 fills the last warpgroup)
-// Registers a thread: launched with 96, five warps a quadrant of the SM:
-// 2 x 128 + 104 + 80 + 40 = 480
+constexpr int kChainWarps = 16, kOutWarp = 16, kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kThreads = 24 * 32;   // (warps 22 and 23 fill the last warpgroup)
+// Registers a thread: launched with 80, six warps a quadrant of the SM:
+// 4 x 80 + 104 + 48 = 472 of 480
 #define SSD_SETREG(dir, n) asm volatile("setmaxnreg." dir ".sync.aligned.u32 " n ";")
 constexpr int kKQ = 3, kTP = 2;   // stages
 // TMEM columns: S's terms (and w's), Y / y, O1, X / x, O2, W
@@ -39,13 +38,12 @@ template <int KP>
 struct Smem {
   static constexpr uint32_t kHalf = 2 * kTile;   // 64 columns: 64 rows of K, 64 of Q
   unsigned char kq[kKQ][KP / 64][2][kTile];
-  unsigned char v[2][2][kTile];                  // [channel half][token][64], not swizzled; out
+  unsigned char v[2][2][kTile];                  // [channel half][token][64], not swizzled
+  unsigned char o[2][kTile];                     // out, as v
   unsigned char tp[kTP][4][kTile];               // T's terms, P's terms
-  unsigned char a[2][kTile];                     // the inverse's A, two terms
-  float diag[4][kDiag];
   alignas(16) float vec[kTP][vec_floats<kC>()];
-  uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[2], v_empty[2], tp_ready[kTP], tp_empty[kTP],
-      vec_ready[kTP], vec_empty[kTP];
+  uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[2], v_empty[2], tp_full[kTP], tp_empty[kTP],
+      vec_full[kTP], vec_empty[kTP];
   uint64_t s_ready, y_done, yt_ready, x_done, w_ready, w_done, o_done, o1_read, o2_read,
       mma_drain;
   uint32_t tmem;
@@ -74,10 +72,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.v_full[i], 1);
-      tc::mbar_init(&s.v_empty[i], 1);
-      tc::mbar_init(&s.tp_ready[i], 4);
+      tc::mbar_init(&s.v_empty[i], kChainWarps);
+      tc::mbar_init(&s.tp_full[i], 1);
       tc::mbar_init(&s.tp_empty[i], 1);
-      tc::mbar_init(&s.vec_ready[i], 1);
+      tc::mbar_init(&s.vec_full[i], 1);
       tc::mbar_init(&s.vec_empty[i], kChainWarps + 4);
     }
     tc::mbar_init(&s.s_ready, kChainWarps);
@@ -93,10 +91,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_fence_init();
     s.gave_up = 0;
   }
-  // T's and P's blocks above the diagonal stay zero
-  for (int i = tid; i < kTP * 4 * (int)kTile / 16; i += kThreads)
-    reinterpret_cast<uint4*>(s.tp)[i] = make_uint4(0, 0, 0, 0);
-  tc::fence_proxy_async_smem();
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
@@ -105,56 +99,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto W = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &s.gave_up, &g_status); };
 
   if (warp >= kMmaWarp) {
-    SSD_SETREG("dec", "40");
+    SSD_SETREG("dec", "48");
     if (warp == kLoadWarp) {
-      int nk = 0, nv = 0;   // chunks issued
-      auto keys = [&] {
-        const int st = nk % kKQ;
-        if (nk >= kKQ) W(&s.kq_empty[st], (nk / kKQ - 1) & 1);
-        if (__any_sync(0xffffffffu, s.gave_up)) return false;
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int p = c & 1, kq = c % kKQ;
+        const uint32_t ph = (c / 2 - 1) & 1;
+        const int64_t id = (int64_t)bh * nc + c;
+        if (c >= kKQ) W(&s.kq_empty[kq], (c / kKQ - 1) & 1);
+        if (__any_sync(0xffffffffu, s.gave_up)) break;
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.kq_full[st], KP / 64 * 2 * kTile);
+          tc::mbar_arrive_expect_tx(&s.kq_full[kq], KP / 64 * 2 * kTile);
           for (int i = 0; i < KP / 64; ++i) {
-            tc::tma_load_4d(s.kq[st][i][0], &mk, &s.kq_full[st], i * 64, kg, nk * kC, b);
-            tc::tma_load_4d(s.kq[st][i][1], &mq, &s.kq_full[st], i * 64, kg, nk * kC, b);
+            tc::tma_load_4d(s.kq[kq][i][0], &mk, &s.kq_full[kq], i * 64, kg, c * kC, b);
+            tc::tma_load_4d(s.kq[kq][i][1], &mq, &s.kq_full[kq], i * 64, kg, c * kC, b);
           }
         }
         __syncwarp();
-        ++nk;
-        return true;
-      };
-      bool ok = keys();
-      while (ok && nv < nc) {   // keys one chunk ahead of values
-        if (nk < nc) ok = keys();
-        const int vs = nv & 1;
-        if (nv >= 2) W(&s.v_empty[vs], (nv / 2 - 1) & 1);
-        ok = ok && !__any_sync(0xffffffffu, s.gave_up);
-        if (!ok) break;
+        // (after a wait that gave up, what follows is only waited for)
+        if (c >= 2) W(&s.v_empty[p], ph);
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.v_full[vs], 2 * kTile);
+          tc::mbar_arrive_expect_tx(&s.v_full[p], 2 * kTile);
           for (int i = 0; i < 2; ++i)
-            tc::tma_load_4d(s.v[vs][i], &mv, &s.v_full[vs], v0 + i * 64, h, nv * kC, b);
+            tc::tma_load_4d(s.v[p][i], &mv, &s.v_full[p], v0 + i * 64, h, c * kC, b);
         }
         __syncwarp();
-        ++nv;
+        if (c >= 2) W(&s.vec_empty[p], ph);
+        if (c >= 2) W(&s.tp_empty[p], ph);
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&s.vec_full[p], vec_floats<kC>() * 4);
+          tc::bulk_load(s.vec[p], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4,
+                        &s.vec_full[p]);
+          tc::mbar_arrive_expect_tx(&s.tp_full[p], 4 * kTile);
+          tc::bulk_load(s.tp[p], reinterpret_cast<const unsigned char*>(a.T) + id * 4 * kTile,
+                        4 * kTile, &s.tp_full[p]);
+        }
+        __syncwarp();
       }
       // every copy has landed before the CTA ends
-      for (int i = nk > kKQ ? nk - kKQ : 0; i < nk; ++i)
+      for (int i = c > kKQ ? c - kKQ : 0; i < c; ++i) {
         drain(&s.kq_full[i % kKQ], (i / kKQ) & 1, &g_status);
-      for (int i = nv > 2 ? nv - 2 : 0; i < nv; ++i)
+        if (i < c - 2) continue;
+        drain(&s.tp_full[i & 1], (i / 2) & 1, &g_status);
+        drain(&s.vec_full[i & 1], (i / 2) & 1, &g_status);
         drain(&s.v_full[i & 1], (i / 2) & 1, &g_status);
-    } else if (warp == kVecWarp) {
-      Gates next = load_gates(a, b, h, 0, lane);
-      for (int c = 0; c < nc; ++c) {
-        float* const vec = s.vec[c & 1];
-        if (c >= kTP) W(&s.vec_empty[c & 1], (c / kTP - 1) & 1);
-        chunk_vectors(next, vec, lane);
-        if (c + 1 < nc) next = load_gates(a, b, h, (int64_t)(c + 1) * kC, lane);
-        warp_arrive(&s.vec_ready[c & 1], lane);
-        if (KEEP && blockIdx.y == 0) {
-          float* const to = a.vec + ((int64_t)bh * nc + c) * vec_floats<kC>();
-          for (int i = lane; i < kVecs * kC + 1; i += 32) to[i] = vec[i];
-        }
       }
     } else if (warp == kMmaWarp) {
       // (the warp stays converged, one elected lane issuing: descriptors then live
@@ -173,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t kq_ph = 0;
       for (int c = 0; c < nc; ++c) {
         const uint32_t ph = c & 1, tp = c & 1;
+        const uint32_t fill = (c >> 1) & 1;
         const uint64_t dk = dk0 + st * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dm = dm0 + st * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dt = dt0 + tp * (4 * kTile >> 4), dp = dp0 + tp * (4 * kTile >> 4);
@@ -187,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(&s.y_done);
         }
         __syncwarp();
-        W(&s.tp_ready[tp], (c >> 1) & 1);
+        W(&s.tp_full[tp], fill);
         W(&s.yt_ready, ph);
         if (stop()) break;
         tc::fence_after_sync();
@@ -228,98 +217,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       drain(&s.mma_drain, 0, &g_status);
     }
-  } else if (warp >= kPrepWarp) {
-    // ---------------- the chunks' T and P
-    SSD_SETREG("dec", "80");
-    const int w = warp - kPrepWarp, ptid = tid - kPrepWarp * 32;
-    for (int c = 0; c < nc; ++c) {
-      const int st = c % kKQ, tp = c & 1;
-      const float* const vec = s.vec[tp];
-      const bool keys = w < 2;
-      const uint32_t ba = saddr(s.kq[st][0][keys ? 0 : 1]), bk = saddr(s.kq[st][0][0]);
-      float x[10][4];
-      W(&s.kq_full[st], (c / kKQ) & 1);
-      if (w & 1) pair_products<KP, true>(x, ba, bk, S::kHalf, lane);
-      else pair_products<KP, false>(x, ba, bk, S::kHalf, lane);
-      W(&s.vec_ready[tp], (c >> 1) & 1);
-      if (c >= kTP) W(&s.tp_empty[tp], (c / kTP - 1) & 1);
-      if (KEEP && ptid == 0) tc::bulk_wait_read();
-      named_sync(2, 128);   // all four are past the chunk before
-      unsigned char* const to = keys ? s.a[0] : s.tp[tp][2];
-      if (w & 1) pair_decays<true>(x, vec, keys, a.scale, to, s.diag[0], lane);
-      else pair_decays<false>(x, vec, keys, a.scale, to, s.diag[0], lane);
-      named_sync(2, 128);
-      invert(s.tp[tp][0], s.a[0], s.diag[0], w, lane, 2);
-      tc::fence_proxy_async_smem();
-      if (KEEP) {
-        named_sync(2, 128);
-        if (blockIdx.y == 0 && ptid == 0) {
-          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                           reinterpret_cast<unsigned char*>(a.T) + ((int64_t)bh * nc + c) * 4 * kTile),
-                       "r"(saddr(s.tp[tp][0])), "r"(4 * kTile)
-                       : "memory");
-          tc::bulk_commit();
-        }
-      }
-      warp_arrive(&s.tp_ready[tp], lane);
-    }
-    if (KEEP && ptid == 0) tc::bulk_wait_all();
   } else if (warp >= kOutWarp) {
-    // ---------------- out = scale e^G O1 + O2, over v's tile
+    // ---------------- out = scale e^G O1 + O2
     SSD_SETREG("inc", "104");
     const int qr = warp & 3, row = qr * 32 + lane, vr = v0 + row;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const float* gam = s.vec[ph] + kGam * kC;
-      unsigned char* const vt = s.v[ph][row >> 6] + (row & 63) * 2;
-      uint32_t o1[4][16];
+      unsigned char* const vt = s.o[row >> 6] + (row & 63) * 2;
+      float x[4][16];
       W(&s.x_done, ph);   // O1 is done as X is
       tc::fence_after_sync();
 #pragma unroll
-      for (int p = 0; p < 4; ++p) tc::tmem_ld16(lanes + kO1 + p * 16, o1[p]);
+      for (int p = 0; p < 4; ++p) {
+        uint32_t r[16];
+        tc::tmem_ld16(lanes + kO1 + p * 16, r);
+        tc::tmem_ld_wait_regs(r);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) tc::tmem_ld_wait_regs(o1[p]);
+        for (int i = 0; i < 16; ++i) x[p][i] = __uint_as_float(r[i]) * a.scale;
+      }
       tc::fence_before_sync();
       warp_arrive(&s.o1_read, lane);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) scale_by(x[p], gam + p * 16);
       W(&s.o_done, ph);
       tc::fence_after_sync();
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         uint32_t r[16];
-        float x[16];
         tc::tmem_ld16(lanes + kO2 + p * 16, r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o1[p][i]) * a.scale;
-        scale_by(x, gam + p * 16);
         tc::tmem_ld_wait_regs(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(r[i]);
+        for (int i = 0; i < 16; ++i) x[p][i] += __uint_as_float(r[i]);
+      }
+      tc::fence_before_sync();
+      warp_arrive(&s.o2_read, lane);
+      warp_arrive(&s.vec_empty[ph], lane);
+      if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_read();   // the tile's last store
+      named_sync(1, 128);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
         if (a.wide_out) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<bf16*>(vt + (p * 16 + i) * 128) = __float2bfloat16_rn(x[i]);
+            *reinterpret_cast<bf16*>(vt + (p * 16 + i) * 128) = __float2bfloat16_rn(x[p][i]);
         } else if (a.out && vr < a.V) {   // rows off 16 bytes
           const int64_t t0 = (int64_t)c * kC + p * 16;
           bf16* dst = static_cast<bf16*>(a.out) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vr;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (t0 + i < a.L) dst[(int64_t)i * a.H * a.V] = __float2bfloat16_rn(x[i]);
+            if (t0 + i < a.L) dst[(int64_t)i * a.H * a.V] = __float2bfloat16_rn(x[p][i]);
         }
       }
-      tc::fence_before_sync();
-      warp_arrive(&s.o2_read, lane);
-      warp_arrive(&s.vec_empty[ph], lane);
       tc::fence_proxy_async_smem();
       named_sync(1, 128);
       if (warp == kOutWarp) {
         if (tc::elect_one()) {
           if (a.wide_out && !s.gave_up)
             for (int i = 0; i < 2; ++i)
-              if (v0 + i * 64 < a.V) tc::tma_store_4d(&mo, s.v[ph][i], v0 + i * 64, h, c * kC, b);
+              if (v0 + i * 64 < a.V) tc::tma_store_4d(&mo, s.o[i], v0 + i * 64, h, c * kC, b);
           tc::bulk_commit();
-          tc::bulk_wait_read();
-          tc::mbar_arrive(&s.v_empty[ph]);
         }
         __syncwarp();
       }
@@ -327,43 +285,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_all();
   } else {
     // ---------------- the chain
-    SSD_SETREG("inc", "128");
-    const int qr = warp & 3, hf = warp >> 2, row = qr * 32 + lane, vr = v0 + row;
+    const int qr = warp & 3, part = warp >> 2, row = qr * 32 + lane, vr = v0 + row;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);   // this warp's 32 TMEM lanes
-    constexpr int SP = KP / 32;                           // pieces of 16 of S a thread
-    const bool live = vr < a.V;
+    constexpr int SP = KP / 64;                           // pieces of 16 of S a thread
     float S0[SP][16];
-    {
-      const float* src = a.init ? a.init + ((int64_t)bh * a.V + (live ? vr : 0)) * a.K : nullptr;
-#pragma unroll
-      for (int p = 0; p < SP; ++p)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = (hf * SP + p) * 16 + i;
-          S0[p][i] = src && live && k < a.K ? src[k] : 0.f;
-        }
-    }
+    read_row<SP>(S0, a.init, bh, vr, part, a);
     // A piece of S as terms to TMEM (and to memory, as chunk c's first state)
     auto put_state = [&](int p, int c) {
       uint32_t t[16];
       two_terms(S0[p], t);
-      tc::tmem_st16(lanes + kAS + (hf * SP + p) * 16, t);
-      if (KEEP) {
-        // planes [term][dstate half][row][64], swizzled as the tiles
-        const int k = (hf * SP + p) * 16;
-        unsigned char* at = reinterpret_cast<unsigned char*>(a.S0) +
-                            (((int64_t)bh * nc + c) * 2 * (KP / 64) + (k >> 6)) * a.VP * 128 +
-                            (int64_t)vr * 128;
-        const int64_t plane = (int64_t)a.VP * KP * 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int unit = (((k & 63) >> 3) + i) ^ (vr & 7);
-          *reinterpret_cast<uint4*>(at + unit * 16) =
-              make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
-          *reinterpret_cast<uint4*>(at + plane + unit * 16) =
-              make_uint4(t[8 + 4 * i], t[9 + 4 * i], t[10 + 4 * i], t[11 + 4 * i]);
-        }
-      }
+      tc::tmem_st16(lanes + kAS + (part * SP + p) * 16, t);
+      if (KEEP) keep_row<KP>(t, a.S0, (int64_t)bh * nc + c, vr, (part * SP + p) * 16, a);
     };
     auto told = [&](uint64_t* bar) {   // what this warp wrote to TMEM is there
       tc::tmem_st_wait();
@@ -377,62 +309,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = c & 1;
       const float* vec = s.vec[ph];
       const unsigned char* const vt = s.v[ph][row >> 6] + (row & 63) * 2;
-      uint32_t r[2][16];
+      uint32_t r[16], t[16];
+      float x[16];
+      const int t0 = part * 16;   // the warp's tokens
       // y = v - e^G Y
       W(&s.v_full[ph], (c >> 1) & 1);
-      W(&s.vec_ready[ph], (c >> 1) & 1);
+      W(&s.vec_full[ph], (c >> 1) & 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {   // v's pairs of tokens, while Y is computed
+        const unsigned char* q = vt + (t0 + 2 * i) * 128;
+        t[i] = *reinterpret_cast<const uint16_t*>(q) |
+               (uint32_t)*reinterpret_cast<const uint16_t*>(q + 128) << 16;
+      }
       W(&s.y_done, ph);
       tc::fence_after_sync();
+      tc::tmem_ld16(lanes + kR0 + t0, r);
+      tc::tmem_ld_wait_regs(r);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) tc::tmem_ld16(lanes + kR0 + (hf * 2 + p) * 16, r[p]);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int t0 = (hf * 2 + p) * 16;
-        float x[16];
-        tc::tmem_ld_wait_regs(r[p]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = -__uint_as_float(r[p][i]);
-        scale_by(x, vec + kGam * kC + t0);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          x[i] += __uint_as_float(
-              (uint32_t)*reinterpret_cast<const uint16_t*>(vt + (t0 + i) * 128) << 16);
-        two_terms(x, r[p]);
-        tc::tmem_st16(lanes + kR0 + t0, r[p]);
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(vec + kRead * kC + t0 + 4 * i);
+        fma2(x[4 * i], x[4 * i + 1], __uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), f.x,
+             f.y, lo_of(t[2 * i]), hi_of(t[2 * i]));
+        fma2(x[4 * i + 2], x[4 * i + 3], __uint_as_float(r[4 * i + 2]),
+             __uint_as_float(r[4 * i + 3]), f.z, f.w, lo_of(t[2 * i + 1]), hi_of(t[2 * i + 1]));
       }
+      two_terms(x, r);
+      tc::tmem_st16(lanes + kR0 + t0, r);
       told(&s.yt_ready);
+      warp_arrive(&s.v_empty[ph], lane);
       // x's terms, and w = beta e^(G_C - G) x
       W(&s.x_done, ph);
       tc::fence_after_sync();
+      tc::tmem_ld16(lanes + kR1 + t0, r);
+      tc::tmem_ld_wait_regs(r);
 #pragma unroll
-      for (int p = 0; p < 2; ++p) tc::tmem_ld16(lanes + kR1 + (hf * 2 + p) * 16, r[p]);
+      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+      two_terms(x, t);
+      tc::tmem_st16(lanes + kR1 + t0, t);
+      scale_by(x, vec + kWrite * kC + t0);
+      two_terms(x, r);
+      tc::tmem_st16(lanes + kAS + t0, r);
+      if (KEEP) {
+        // planes [term][channel half][token][64], swizzled
+        unsigned char* base = reinterpret_cast<unsigned char*>(a.X) +
+                              ((int64_t)bh * nc + c) * 2 * kC * a.VP * 2 +
+                              (int64_t)(vr >> 6) * kTile;
+        const int64_t plane = (int64_t)kC * a.VP * 2;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int t0 = (hf * 2 + p) * 16;
-        float x[16];
-        uint32_t t[16];
-        tc::tmem_ld_wait_regs(r[p]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[p][i]);
-        two_terms(x, t);
-        tc::tmem_st16(lanes + kR1 + t0, t);
-        scale_by(x, vec + kBeta * kC + t0);
-        scale_by(x, vec + kOnto * kC + t0);
-        two_terms(x, r[p]);
-        tc::tmem_st16(lanes + kAS + t0, r[p]);
-        if (KEEP) {
-          // planes [term][channel half][token][64], swizzled
-          unsigned char* base = reinterpret_cast<unsigned char*>(a.X) +
-                                ((int64_t)bh * nc + c) * 2 * kC * a.VP * 2 +
-                                (int64_t)(vr >> 6) * kTile;
-          const int64_t plane = (int64_t)kC * a.VP * 2;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            unsigned char* at = base + tile_at<64>(t0 + i, (vr & 63) >> 3) + (vr & 7) * 2;
-            const int sh = 16 * (i & 1);
-            *reinterpret_cast<uint16_t*>(at) = (uint16_t)(t[i >> 1] >> sh);
-            *reinterpret_cast<uint16_t*>(at + plane) = (uint16_t)(t[8 + (i >> 1)] >> sh);
-          }
+        for (int i = 0; i < 16; ++i) {
+          unsigned char* at = base + tile_at<64>(t0 + i, (vr & 63) >> 3) + (vr & 7) * 2;
+          const int sh = 16 * (i & 1);
+          *reinterpret_cast<uint16_t*>(at) = (uint16_t)(t[i >> 1] >> sh);
+          *reinterpret_cast<uint16_t*>(at + plane) = (uint16_t)(t[8 + (i >> 1)] >> sh);
         }
       }
       told(&s.w_ready);
@@ -443,28 +371,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
 #pragma unroll
       for (int p = 0; p < SP; ++p) {
-        if (p % 2 == 0) {
-          tc::tmem_ld16(lanes + kW + (hf * SP + p) * 16, r[0]);
-          if (p + 1 < SP) tc::tmem_ld16(lanes + kW + (hf * SP + p + 1) * 16, r[1]);
-        }
-        tc::tmem_ld_wait_regs(r[p & 1]);
+        tc::tmem_ld16(lanes + kW + (part * SP + p) * 16, r);
+        tc::tmem_ld_wait_regs(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          S0[p][i] = fmaf(through, S0[p][i], __uint_as_float(r[p & 1][i]));
+        for (int i = 0; i < 8; ++i)
+          fma2(S0[p][2 * i], S0[p][2 * i + 1], S0[p][2 * i], S0[p][2 * i + 1], through, through,
+               __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         if (c + 1 < nc) put_state(p, c + 1);
       }
       told(&s.s_ready);
     }
-    if (a.final && live) {
-      float* dst = a.final + ((int64_t)bh * a.V + vr) * a.K;
-#pragma unroll
-      for (int p = 0; p < SP; ++p)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = (hf * SP + p) * 16 + i;
-          if (k < a.K) dst[k] = S0[p][i];
-        }
-    }
+    write_row<SP>(S0, a.final, bh, vr, part, a);
   }
   __syncwarp();
   tc::fence_before_sync();

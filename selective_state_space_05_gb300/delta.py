@@ -142,7 +142,8 @@ def delta_scan_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
         _need(saved, "saved", torch.uint8, device=dev)
     st = _stream_of(stream, dev)
     ws, ws_bytes, hold = _workspace(
-        _call("ssd_delta_scan_bwd_workspace_bytes")(B, L, H, V, K, G, dt, int(saved is not None)),
+        _call("ssd_delta_scan_bwd_workspace_bytes")(
+            B, L, H, V, K, G, dt, int(saved is not None), _aligned(q, k, v, dout)),
         workspace, dev, stream)
     grads = dict(dq=_empty((B, L, G, K), xd, dev, stream), dk=_empty((B, L, G, K), xd, dev, stream),
                  dv=_empty((B, L, H, V), xd, dev, stream), dg=_empty((B, L, H), _F32, dev, stream),

@@ -51,12 +51,12 @@ def test_forward_refusals(lib):
     common(f)
     assert f(out=None) == NULL and f(ws=None) == NULL
     assert f(out=17) == ALIGN and f(final=18) == ALIGN and f(ws=128) == ALIGN
-    ws = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 0)
+    ws = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 0, 1)
     assert f(wsb=ws - 1) == WORKSPACE and b"workspace" in lib.ssd_last_error()
-    kept = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 1)
+    kept = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 1, 1)
     assert kept > ws > 0 and f(keep=1, wsb=kept - 1) == WORKSPACE
-    assert lib.ssd_delta_scan_workspace_bytes(2, 0, 1, 16, 16, 1, BF, 0) == 0
-    assert lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 129, 1, BF, 0) == 0
+    assert lib.ssd_delta_scan_workspace_bytes(2, 0, 1, 16, 16, 1, BF, 0, 1) == 0
+    assert lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 129, 1, BF, 0, 1) == 0
 
 
 def test_backward_refusals(lib):
@@ -68,12 +68,16 @@ def test_backward_refusals(lib):
     assert f(dout=17) == ALIGN and f(dq=18) == ALIGN and f(dinit=2) == ALIGN
     assert f(saved=16) == ALIGN and f(ws=16) == ALIGN
     q = lib.ssd_delta_scan_bwd_workspace_bytes
-    own, whole = (q(2, 4, 1, 16, 16, 1, BF, s) for s in (1, 0))
-    kept = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 1)
+    own, whole = (q(2, 4, 1, 16, 16, 1, BF, s, 1) for s in (1, 0))
+    kept = lib.ssd_delta_scan_workspace_bytes(2, 4, 1, 16, 16, 1, BF, 1, 1)
     assert whole == own + kept
     assert f(sb=kept - 1) == WORKSPACE and f(wsb=own - 1) == WORKSPACE
     assert f(saved=None, wsb=whole - 1) == WORKSPACE
-    assert q(2, 4, 3, 16, 16, 2, BF, 1) == 0
+    assert q(2, 4, 3, 16, 16, 2, BF, 1, 1) == 0
+    # rows off 16 bytes are copied where the kernels read by tensor maps
+    wide = q(2, 4, 1, 64, 16, 1, BF, 1, 1)
+    assert q(2, 4, 1, 64, 16, 1, BF, 1, 0) >= wide + 2 * 4 * (2 * 16 + 2 * 64) * 2
+    assert q(2, 4, 1, 64, 16, 1, F32, 1, 0) == q(2, 4, 1, 64, 16, 1, F32, 1, 1)
 
 
 def test_step_refusals(lib):
