@@ -166,22 +166,25 @@ __device__ __forceinline__ void write_row(const float (&x)[SP][16], float* state
       }
     }
 }
-// 16 columns from k on of row vr of chunk id's state, as terms into planes
-// [term][dstate half][row][64] of the workspace, swizzled as the tiles.
+// 16 columns from k on of row vr of chunk id's state, as terms: planes [block of 128
+// rows][term][8 columns][row], so that a warp's rows lie side by side and a block is
+// an MMA operand's core matrices (no swizzle).
 template <int KP>
 __device__ __forceinline__ void keep_row(const uint32_t (&t)[16], bf16* planes, int64_t id, int vr,
                                          int k, const Args& a) {
-  unsigned char* at = reinterpret_cast<unsigned char*>(planes) +
-                      ((id * 2 * (KP / 64) + (k >> 6)) * a.VP + vr) * 128;
-  const int64_t plane = (int64_t)a.VP * KP * 2;
+  uint4* at = reinterpret_cast<uint4*>(planes) +
+              (((id * (a.VP / 128) + (vr >> 7)) * 2) * (KP / 8) + (k >> 3)) * 128 + (vr & 127);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int unit = (((k & 63) >> 3) + i) ^ (vr & 7);
-    *reinterpret_cast<uint4*>(at + unit * 16) =
-        make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
-    *reinterpret_cast<uint4*>(at + plane + unit * 16) =
-        make_uint4(t[8 + 4 * i], t[9 + 4 * i], t[10 + 4 * i], t[11 + 4 * i]);
+    at[i * 128] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+    at[(KP / 8 + i) * 128] = make_uint4(t[8 + 4 * i], t[9 + 4 * i], t[10 + 4 * i], t[11 + 4 * i]);
   }
+}
+// Descriptor of such a block (MN-major without swizzle): groups of eight rows along
+// K 128 bytes apart, of eight columns along MN 2048.
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 |
+         (uint64_t)(2048 >> 4) << 32 | 1ull << 46;
 }
 
 // ------------------------------------------------------------------ a chunk's matrices

@@ -30,16 +30,18 @@ constexpr int kThreads = 24 * 32;   // (warps 22 and 23 fill the last warpgroup)
 // Registers a thread: launched with 80, six warps a quadrant of the SM:
 // 4 x 80 + 104 + 48 = 472 of 480
 #define SSD_SETREG(dir, n) asm volatile("setmaxnreg." dir ".sync.aligned.u32 " n ";")
-constexpr int kKQ = 3, kTP = 2;   // stages
+constexpr int kTP = 2;   // stages
 // TMEM columns: S's terms (and w's), Y / y, O1, X / x, O2, W
 constexpr uint32_t kAS = 0, kR0 = 128, kO1 = 192, kR1 = 256, kO2 = 320, kW = 384;
 
-template <int KP>
+template <int KP, bool KEEP>
 struct Smem {
+  static constexpr int kKQ = KEEP ? 2 : 3;
   static constexpr uint32_t kHalf = 2 * kTile;   // 64 columns: 64 rows of K, 64 of Q
   unsigned char kq[kKQ][KP / 64][2][kTile];
   unsigned char v[2][2][kTile];                  // [channel half][token][64], not swizzled
   unsigned char o[2][kTile];                     // out, as v
+  unsigned char x[KEEP ? 2 : 0][2][kTile];       // x's terms: [term][channel half][token][64]
   unsigned char tp[kTP][4][kTile];               // T's terms, P's terms
   alignas(16) float vec[kTP][vec_floats<kC>()];
   uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[2], v_empty[2], tp_full[kTP], tp_empty[kTP],
@@ -58,7 +60,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
                       const __grid_constant__ Args a) {
   extern __shared__ unsigned char raw[];
-  using S = Smem<KP>;
+  using S = Smem<KP, KEEP>;
+  constexpr int kKQ = S::kKQ;
   S& s = *reinterpret_cast<S*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
@@ -177,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         W(&s.tp_full[tp], fill);
+        if (c > 0) W(&s.o2_read, ph ^ 1);   // O2 and x's terms of the chunk before
         W(&s.yt_ready, ph);
         if (stop()) break;
         tc::fence_after_sync();
@@ -195,12 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_chain<4, true>(tmem + kW, tmem + kAS, 0, dm, 0, idw, false);
           tc::mma_commit(&s.w_done);
           tc::mma_commit(&s.kq_empty[st]);
-        }
-        __syncwarp();
-        if (c > 0) W(&s.o2_read, ph ^ 1);
-        if (stop()) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) {
           mma_chain<4, false>(tmem + kO2, tmem + kR1, 1, dp, 0, id64, true);
           mma_chain<4, false>(tmem + kO2, tmem + kR1, 0, dp + lo, 0, id64, false);
           mma_chain<4, false>(tmem + kO2, tmem + kR1, 0, dp, 0, id64, false);
@@ -241,6 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&s.o1_read, lane);
 #pragma unroll
       for (int p = 0; p < 4; ++p) scale_by(x[p], gam + p * 16);
+      if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_read();   // the tiles' last copies
+      __syncwarp();
+      named_sync(1, 128);
       W(&s.o_done, ph);
       tc::fence_after_sync();
 #pragma unroll
@@ -250,12 +251,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_ld_wait_regs(r);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[p][i] += __uint_as_float(r[i]);
+        if (KEEP) {
+          tc::tmem_ld16(lanes + kR1 + p * 16, r);
+          tc::tmem_ld_wait_regs(r);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            unsigned char* at =
+                s.x[0][row >> 6] + tile_at<64>(p * 16 + i, (row & 63) >> 3) + (row & 7) * 2;
+            const int sh = 16 * (i & 1);
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)(r[i >> 1] >> sh);
+            *reinterpret_cast<uint16_t*>(at + 2 * kTile) = (uint16_t)(r[8 + (i >> 1)] >> sh);
+          }
+        }
       }
       tc::fence_before_sync();
       warp_arrive(&s.o2_read, lane);
       warp_arrive(&s.vec_empty[ph], lane);
-      if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_read();   // the tile's last store
-      named_sync(1, 128);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         if (a.wide_out) {
@@ -277,6 +288,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a.wide_out && !s.gave_up)
             for (int i = 0; i < 2; ++i)
               if (v0 + i * 64 < a.V) tc::tma_store_4d(&mo, s.o[i], v0 + i * 64, h, c * kC, b);
+          if (KEEP && !s.gave_up) {
+            // planes [term][channel half][token][64] of the workspace
+            unsigned char* to = reinterpret_cast<unsigned char*>(a.X) +
+                                (((int64_t)bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
+            for (int i = 0; i < 2; ++i)
+              asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                               to + (int64_t)i * (a.VP / 64) * kTile),
+                           "r"(saddr(s.x[i][0])), "r"(2 * kTile)
+                           : "memory");
+          }
           tc::bulk_commit();
         }
         __syncwarp();
@@ -349,20 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       scale_by(x, vec + kWrite * kC + t0);
       two_terms(x, r);
       tc::tmem_st16(lanes + kAS + t0, r);
-      if (KEEP) {
-        // planes [term][channel half][token][64], swizzled
-        unsigned char* base = reinterpret_cast<unsigned char*>(a.X) +
-                              ((int64_t)bh * nc + c) * 2 * kC * a.VP * 2 +
-                              (int64_t)(vr >> 6) * kTile;
-        const int64_t plane = (int64_t)kC * a.VP * 2;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          unsigned char* at = base + tile_at<64>(t0 + i, (vr & 63) >> 3) + (vr & 7) * 2;
-          const int sh = 16 * (i & 1);
-          *reinterpret_cast<uint16_t*>(at) = (uint16_t)(t[i >> 1] >> sh);
-          *reinterpret_cast<uint16_t*>(at + plane) = (uint16_t)(t[8 + (i >> 1)] >> sh);
-        }
-      }
       told(&s.w_ready);
       const float through = vec[kVecs * kC];
       warp_arrive(&s.vec_empty[ph], lane);
@@ -404,7 +411,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   mo = mv;
   if (a.wide_out && !token_map(&mo, a.out, a.V, a.H, a.L, a.B, dense, false))
     return cudaErrorInvalidValue;
-  const int smem = (int)sizeof(Smem<KP>) + 1024;
+  const int smem = (int)sizeof(Smem<KP, KEEP>) + 1024;
   const cudaError_t e = cudaFuncSetAttribute(
       tc_forward_kernel<KP, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -412,7 +419,8 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   tc_forward_kernel<KP, KEEP><<<grid, kThreads, smem, st>>>(mq, mk, mv, mo, a);
   return cudaGetLastError();
 }
-static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Smem<128, false>) + 1024 <= 227 * 1024 &&
+              sizeof(Smem<128, true>) + 1024 <= 227 * 1024, "shared memory");
 
 }  // namespace fwd
 

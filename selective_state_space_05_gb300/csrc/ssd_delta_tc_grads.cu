@@ -34,7 +34,7 @@ struct Smem {
     unsigned char out[2][KP / 64][kTile];   // then dq, dk
   };
   unsigned char x[2][2][kTile];          // a channel half: Xhi, Xlo
-  unsigned char s[2][KP / 64][2][kTile]; // a term, 64 dstate columns: 128 channels; S0, then dS
+  unsigned char s[2][KP / 8][128][16];   // a term, 8 dstate columns, 128 channels: S0, then dS
   union {
     unsigned char p[2][2][kTile];        // a channel half: dYhi, do
     float h[128][kHPitch];               // then H's rows of dY, of do
@@ -115,13 +115,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // a state's planes of block v
     auto state = [&](const bf16* planes, int v, uint64_t* bar) {
-      tc::mbar_arrive_expect_tx(bar, 2 * (KP / 64) * 2 * kTile);
-      for (int t = 0; t < 2; ++t)
-        for (int k = 0; k < KP / 64; ++k)
-          bulk(s.s[t][k][0],
-               reinterpret_cast<const unsigned char*>(planes) +
-                   (((id * 2 + t) * (KP / 64) + k) * a.VP + v * 128) * 128,
-               2 * kTile, bar);
+      tc::mbar_arrive_expect_tx(bar, sizeof(s.s));
+      bulk(s.s, reinterpret_cast<const unsigned char*>(planes) + (id * blocks + v) * sizeof(s.s),
+           sizeof(s.s), bar);
     };
     int loaded = 0, ds = 0;
     if (tc::elect_one()) {
@@ -178,17 +174,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t mk64 = tc::idesc_bf16(128, 64, true, false);
     constexpr uint32_t mm64 = tc::idesc_bf16(128, 64, true, true);
     constexpr uint32_t tile = kTile >> 4;
-    // (with 64 dstate columns the MMA's upper 64 rows are the lower ones again)
-    constexpr uint32_t mstate = KP == 128 ? 2 * kTile : 0, mkq = KP == 128 ? S::kHalf : 0;
+    // (with 64 dstate columns the MMA's upper 64 rows are not read)
+    constexpr uint32_t mkq = KP == 128 ? S::kHalf : 0;
     const uint64_t dk = tc::sdesc_sw128(saddr(s.kq[0][0]), 16, 1024);
     const uint64_t dkm = tc::sdesc_sw128(saddr(s.kq[0][0]), mkq, 1024);
     const uint64_t dp = tc::sdesc_sw128(saddr(s.p[0][0]), 16, 1024);
     const uint64_t dq = tc::sdesc_sw128(saddr(s.q[0][0]), 16, 1024);
     const uint64_t dx = tc::sdesc_sw128(saddr(s.x[0][0]), 16, 1024);
-    const uint64_t dsm = tc::sdesc_sw128(saddr(s.s[0][0][0]), mstate, 1024);
+    const uint64_t dsm = sdesc_rows(saddr(s.s));
     const uint64_t dm = tc::sdesc_sw128(saddr(s.m[0][0]), 16, 1024);
     const uint64_t dmm = tc::sdesc_sw128(saddr(s.m[0][0]), kTile, 1024);
-    constexpr uint32_t term = (KP / 64) * 2 * tile;   // a state's second term
+    constexpr uint32_t term = (KP / 8) * 2048 >> 4;   // a state's second term
     auto stop = [&] { return __any_sync(0xffffffffu, s.gave_up) != 0; };
     W(&s.kq_full, 0);
     tc::fence_after_sync();
@@ -217,11 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       if (tc::elect_one()) {
         for (int i = 0; i < nh; ++i) {   // 64 channels: 4 steps of 16 rows
-          const uint32_t at = i * 2 * tile, rows = i * tile;
+          const uint32_t at = i * 2 * tile, rows = i * (64 * 16 >> 4);
           const bool fresh = v == 0 && i == 0;
-          chain<4>(tmem + kD1, dsm + term + rows, 128, dp + at, 2, mk128, fresh);
-          chain<4>(tmem + kD1, dsm + rows, 128, dp + at, 2, mk128, false);
-          chain<4>(tmem + kD1 + 128, dsm + rows, 128, dq + at, 2, mk64, fresh);
+          chain<4>(tmem + kD1, dsm + term + rows, 16, dp + at, 2, mk128, fresh);
+          chain<4>(tmem + kD1, dsm + rows, 16, dp + at, 2, mk128, false);
+          chain<4>(tmem + kD1 + 128, dsm + rows, 16, dq + at, 2, mk64, fresh);
         }
         tc::mma_commit(&s.d1_done);
       }
@@ -246,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       if (tc::elect_one()) {
         for (int i = 0; i < nh; ++i) {
-          const uint32_t at = i * 2 * tile, rows = i * tile;
+          const uint32_t at = i * 2 * tile, rows = i * (64 * 16 >> 4);
           const bool fresh = v == 0 && i == 0;
-          chain<4>(tmem + kD2, dsm + rows, 128, dx + at, 2, mk128, fresh);
-          chain<4>(tmem + kD2, dsm + term + rows, 128, dx + at, 2, mk64, false);
+          chain<4>(tmem + kD2, dsm + rows, 16, dx + at, 2, mk128, fresh);
+          chain<4>(tmem + kD2, dsm + term + rows, 16, dx + at, 2, mk64, false);
         }
         tc::mma_commit(&s.d2_done);
       }
@@ -268,14 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // <S0, dS> of block v: dS from shared memory, S0 again from the L2
     auto inner_of = [&](int v) {
       W(&s.ds_full, v & 1);
-      for (int u = tid; u < KP / 64 * 128 * 8; u += kWarps * 32) {
-        const int k = u / (128 * 8), at = u % (128 * 8) * 16;
-        const unsigned char* g = reinterpret_cast<const unsigned char*>(a.S0) +
-                                 ((id * 2 * (KP / 64) + k) * a.VP + v * 128) * 128 + at;
-        const uint4 x = *reinterpret_cast<const uint4*>(g);
-        const uint4 y = *reinterpret_cast<const uint4*>(g + (int64_t)(KP / 64) * a.VP * 128);
-        const uint4 z = *reinterpret_cast<const uint4*>(s.s[0][k][0] + at);
-        const uint4 w = *reinterpret_cast<const uint4*>(s.s[1][k][0] + at);
+      const uint4* const g = reinterpret_cast<const uint4*>(a.S0) + (id * blocks + v) * (sizeof(s.s) / 16);
+      const uint4* const d = reinterpret_cast<const uint4*>(s.s);
+      constexpr int n = KP / 8 * 128;
+#pragma unroll 2
+      for (int u = tid; u < n; u += kWarps * 32) {
+        const uint4 x = g[u], y = g[n + u], z = d[u], w = d[n + u];
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
         const uint32_t zs[4] = {z.x, z.y, z.z, z.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

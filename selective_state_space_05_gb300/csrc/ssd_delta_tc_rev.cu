@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < nc; ++n) {
       const int c = nc - 1 - n;
       if (warp == kIoWarp && tc::elect_one()) tc::bulk_wait_read();   // the tiles' last copies
+      __syncwarp();
       W(&s.y_done, n & 1);
       tc::fence_after_sync();
       named_sync(1, 128);
