@@ -52,6 +52,20 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   a.KP = K <= 64 ? 64 : 128;
   a.tc = dtype == SSD_DTYPE_BF16 && V >= kTcHeaddim;
   a.VP = a.tc ? (V + 127) / 128 * 128 : (V + 15) / 16 * 16;
+  // Segments only where there are at least as many sequences as SMs: eight or so for
+  // each SM's share (a segment costs the state's way through the L2, about the time of a
+  // chunk), at least eight chunks long.
+  a.segs = 1;
+  a.seg = a.nc;
+  const int64_t lanes = (int64_t)a.B * H * (a.VP / 128), sms = row::sm_count();
+  if (a.tc && lanes > sms) {
+    const int64_t share = lanes * a.nc / sms;
+    int64_t seg = share / 8 > 8 ? share / 8 : 8;
+    if (seg < a.nc) {
+      a.seg = (int)seg;
+      a.segs = (int)((a.nc + seg - 1) / seg);
+    }
+  }
   a.qcols = a.kcols = K;
   a.vcols = a.docols = V;
   return a;
@@ -86,6 +100,14 @@ cudaError_t pack(const Args& a, const void** src, TokStride* s, int* ncols, int 
   return cudaGetLastError();
 }
 
+template <typename F>
+void carve_work(Args& a, F take) {
+  if (!a.tc) return;
+  const size_t lanes = (size_t)a.B * a.H * (a.VP / 128);
+  a.ctrl = reinterpret_cast<int*>(take((1 + lanes) * sizeof(int)));
+  a.slots = reinterpret_cast<float*>(take(a.segs > 1 ? lanes * 128 * a.KP * 4 : 0));
+}
+
 // The forward's pieces of a workspace at `base`, and how many bytes they take.
 template <typename T>
 size_t carve(Args& a, void* base, bool keep) {
@@ -102,6 +124,7 @@ size_t carve(Args& a, void* base, bool keep) {
   a.vec = nullptr;
   a.T = reinterpret_cast<bf16*>(take(n * NT * C * C * 2 * (a.tc ? 2 : 1)));   // (P beside T)
   if (!a.tc) a.P = reinterpret_cast<bf16*>(take(n * NT * C * C * 2));
+  carve_work(a, take);
   a.vec = reinterpret_cast<float*>(take(n * vec_floats<C>() * 4));
   if (keep) {
     a.S0 = reinterpret_cast<bf16*>(take(n * NT * a.VP * a.KP * 2));
@@ -123,6 +146,7 @@ size_t carve_bwd(Args& a, void* base) {
   };
   a.dS = reinterpret_cast<bf16*>(take(n * NT * a.VP * a.KP * 2));
   a.dY = reinterpret_cast<bf16*>(take(n * NT * C * a.VP * 2));
+  carve_work(a, take);
   a.dq_part = a.dk_part = nullptr;
   if (a.H != a.G) {
     a.dq_part = reinterpret_cast<float*>(take((size_t)a.B * a.L * a.H * a.K * 4));
@@ -334,6 +358,12 @@ int status(int reset, cudaStream_t st, int* bits) {
   return e;
 }
 
+cudaError_t start_work(const Args& a, int* grid, cudaStream_t st) {
+  const int lanes = a.B * a.H * (a.VP / 128);
+  *grid = lanes < row::sm_count() ? lanes : row::sm_count();
+  return cudaMemsetAsync(a.ctrl, 0, (1 + lanes) * sizeof(int), st);
+}
+
 bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
                bool swizzle) {
   auto enc = encode_fn();
@@ -437,15 +467,27 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   const size_t used = own + (saved ? 0 : kept);
   if (workspace_bytes < used + (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a)))
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
-  bwd_bytes(a, dtype, workspace);
   fwd_bytes(a, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
+  Args f = a;   // a forward that is computed again has its own work's state
+  bwd_bytes(a, dtype, workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SSD_DTYPE_BF16;
   char* const at = static_cast<char*>(workspace) + used;
   cudaError_t e = pack_inputs(a, at, st);
   if (e == cudaSuccess && a.tc && !a.wide_do)
     e = pack(a, &a.dout, &a.sdo, &a.docols, a.H, at + pack_bytes(a, false), st);
-  if (e == cudaSuccess && !saved) e = bf ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
+  if (e == cudaSuccess && !saved) {
+    f.q = a.q;
+    f.k = a.k;
+    f.v = a.v;
+    f.sq = a.sq;
+    f.sk = a.sk;
+    f.sv = a.sv;
+    f.qcols = a.qcols;
+    f.kcols = a.kcols;
+    f.vcols = a.vcols;
+    e = bf ? run_forward<bf16>(f, st) : run_forward<float>(f, st);
+  }
   a.dfinal = dfinal_states;
   a.dinit = d_initial_states;
   a.dv = dv;

@@ -65,6 +65,11 @@ struct Args {
   float* vec;      // vec_floats
   bf16 *S0, *X;    // [NT][VP][KP], [NT][C][VP]; null in a forward that keeps nothing
   bf16 *dS, *dY;   // the same of the backward
+  // the tcgen05 kernels' work: sequences in `segs` segments of `seg` chunks, a ticket
+  // and one flag for each (head, 128 channels), and its state between segments
+  int segs, seg;
+  int* ctrl;
+  float* slots;
   // gradients; per head [B, L, H, dstate] fp32 where heads share queries and keys
   void *dq, *dk;
   float *dg, *dbeta, *dq_part, *dk_part;

@@ -166,6 +166,88 @@ __device__ __forceinline__ void write_row(const float (&x)[SP][16], float* state
       }
     }
 }
+// ------------------------------------------------------------------ work
+// A CTA takes (segment, head, 128 channels) items by tickets, in segments' order, so
+// that heads that do not divide into the SMs leave none idle: an item's state comes
+// from the one a whole round of heads earlier, through the L2.  The predecessor of a
+// ticket that was taken has been taken too: whatever else runs on the GPU, waiting
+// for it ends.
+struct Item {
+  int bh, v0, first, last;   // head, channel, chunks [first, last)
+};
+__device__ __forceinline__ Item item_of(const Args& a, int ticket) {
+  const int vb = (a.V + 127) / 128, n = a.B * a.H * vb;
+  Item i = {-1, 0, 0, 0};
+  if (ticket < n * a.segs) {
+    const int seg = ticket / n, r = ticket % n;
+    i.bh = r / vb;
+    i.v0 = r % vb * 128;
+    i.first = seg * a.seg;
+    i.last = min(i.first + a.seg, a.nc);
+  }
+  return i;
+}
+// Two items ahead in shared memory.
+struct Items {
+  Item item[2];
+  uint64_t full[2], empty[2];
+};
+// Waits for an item's predecessor (one warp), and lets its successor go on (after a
+// barrier of the warps that wrote its state).
+__device__ __forceinline__ int* flag_of(const Args& a, const Item& i) {
+  return a.ctrl + 1 + i.bh * ((a.V + 127) / 128) + i.v0 / 128;
+}
+__device__ __forceinline__ void wait_flag(const int* flag, int want, volatile int* gave_up,
+                                          int* status) {
+  for (uint32_t n = 0;; ++n) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+    if (v >= want || *gave_up) break;
+    if (n == kTries) {
+      *gave_up = 1;
+      atomicOr(status, kErrWait);
+    }
+    __nanosleep(100);
+  }
+}
+__device__ __forceinline__ void raise_flag(int* flag, int to) {
+  __threadfence();
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(flag), "r"(to) : "memory");
+}
+// A row of a state between segments: [head, 128 channels][16 columns][4 of them][row],
+// a warp's rows side by side.
+template <int SP>
+__device__ __forceinline__ void read_slot(float (&x)[SP][16], const Args& a, const Item& it, int row,
+                                          int part) {
+  const float4* p = reinterpret_cast<const float4*>(a.slots) +
+                    (int64_t)(it.bh * ((a.V + 127) / 128) + it.v0 / 128) * 32 * a.KP + row;
+#pragma unroll
+  for (int k = 0; k < SP; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float4 f;
+      asm volatile("ld.relaxed.gpu.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+                   : "l"(p + ((part * SP + k) * 4 + i) * 128) : "memory");
+      x[k][4 * i] = f.x;
+      x[k][4 * i + 1] = f.y;
+      x[k][4 * i + 2] = f.z;
+      x[k][4 * i + 3] = f.w;
+    }
+}
+template <int SP>
+__device__ __forceinline__ void write_slot(const float (&x)[SP][16], const Args& a, const Item& it,
+                                           int row, int part) {
+  float4* p = reinterpret_cast<float4*>(a.slots) +
+              (int64_t)(it.bh * ((a.V + 127) / 128) + it.v0 / 128) * 32 * a.KP + row;
+#pragma unroll
+  for (int k = 0; k < SP; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[((part * SP + k) * 4 + i) * 128] =
+          make_float4(x[k][4 * i], x[k][4 * i + 1], x[k][4 * i + 2], x[k][4 * i + 3]);
+}
+
 // 16 columns from k on of row vr of chunk id's state, as terms: planes [block of 128
 // rows][term][8 columns][row], so that a warp's rows lie side by side and a block is
 // an MMA operand's core matrices (no swizzle).
@@ -468,6 +550,9 @@ __device__ __forceinline__ void pair_decays(const float (&x)[10][4], const float
 // row of 64 tokens.
 bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
                bool swizzle);
+
+// Clears a.ctrl for a launch of `grid` CTAs.
+cudaError_t start_work(const Args& a, int* grid, cudaStream_t st);
 
 // A device's status word (after the stream's work), cleared if asked.
 template <typename W>

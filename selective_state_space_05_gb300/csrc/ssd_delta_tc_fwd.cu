@@ -1,5 +1,6 @@
 // The gated delta rule's forward on tcgen05 (ssd_delta_tc.cuh says for which
-// inputs), one CTA per (batch row, head, 128 channels), chunk after chunk.
+// inputs), one CTA per SM, each at one (batch row, head, 128 channels), chunk after
+// chunk.
 //
 // Transposed as in ssd_delta_fwd.cu: TMEM lane = channel, columns = tokens or
 // dstate.  Per chunk, with S in the registers of sixteen warps (a row and a quarter
@@ -47,7 +48,8 @@ struct Smem {
   uint64_t kq_full[kKQ], kq_empty[kKQ], v_full[2], v_empty[2], tp_full[kTP], tp_empty[kTP],
       vec_full[kTP], vec_empty[kTP];
   uint64_t s_ready, y_done, yt_ready, x_done, w_ready, w_done, o_done, o1_read, o2_read,
-      mma_drain;
+      o_sync, slot_done, mma_drain;
+  Items items;
   uint32_t tmem;
   volatile int gave_up;
 };
@@ -64,8 +66,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kKQ = S::kKQ;
   S& s = *reinterpret_cast<S*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
-  const int v0 = blockIdx.y * 128;
   const int nc = a.nc;
   if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, 512);
   if (tid == 0) {
@@ -81,11 +81,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&s.vec_full[i], 1);
       tc::mbar_init(&s.vec_empty[i], kChainWarps + 4);
     }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.items.full[i], 1);
+      tc::mbar_init(&s.items.empty[i], kChainWarps + 5);   // ... out's four, the MMAs' one
+    }
     tc::mbar_init(&s.s_ready, kChainWarps);
     tc::mbar_init(&s.yt_ready, kChainWarps);
     tc::mbar_init(&s.w_ready, kChainWarps);
     tc::mbar_init(&s.o1_read, 4);
     tc::mbar_init(&s.o2_read, 4);
+    tc::mbar_init(&s.o_sync, 4);
+    tc::mbar_init(&s.slot_done, kChainWarps);
     tc::mbar_init(&s.y_done, 1);
     tc::mbar_init(&s.x_done, 1);
     tc::mbar_init(&s.w_done, 1);
@@ -100,49 +106,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
   auto W = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &s.gave_up, &g_status); };
+  // the CTA's n-th item, for all lanes of a warp (bh < 0: no more)
+  auto item = [&](int n) {
+    W(&s.items.full[n & 1], (n >> 1) & 1);
+    Item i = s.items.item[n & 1];
+    warp_arrive(&s.items.empty[n & 1], lane);
+    if (__any_sync(0xffffffffu, s.gave_up)) i.bh = -1;
+    return i;
+  };
 
   if (warp >= kMmaWarp) {
     SSD_SETREG("dec", "48");
     if (warp == kLoadWarp) {
-      int c = 0;
-      for (; c < nc; ++c) {
-        const int p = c & 1, kq = c % kKQ;
-        const uint32_t ph = (c / 2 - 1) & 1;
-        const int64_t id = (int64_t)bh * nc + c;
-        if (c >= kKQ) W(&s.kq_empty[kq], (c / kKQ - 1) & 1);
-        if (__any_sync(0xffffffffu, s.gave_up)) break;
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.kq_full[kq], KP / 64 * 2 * kTile);
-          for (int i = 0; i < KP / 64; ++i) {
-            tc::tma_load_4d(s.kq[kq][i][0], &mk, &s.kq_full[kq], i * 64, kg, c * kC, b);
-            tc::tma_load_4d(s.kq[kq][i][1], &mq, &s.kq_full[kq], i * 64, kg, c * kC, b);
+      int n = 0;   // chunks so far
+      bool go = true;
+      for (int k = 0; go; ++k) {
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(a.ctrl, 1);
+        const Item it = item_of(a, __shfl_sync(0xffffffffu, ticket, 0));
+        if (k >= 2) W(&s.items.empty[k & 1], (k / 2 - 1) & 1);
+        if (lane == 0) s.items.item[k & 1] = it;
+        warp_arrive(&s.items.full[k & 1], lane);
+        if (it.bh < 0) break;
+        const int b = it.bh / a.H, h = it.bh % a.H, kg = h / (a.H / a.G);
+        for (int c = it.first; c < it.last; ++c, ++n) {
+          const int p = n & 1, kq = n % kKQ;
+          const uint32_t ph = (n / 2 - 1) & 1;
+          const int64_t id = (int64_t)it.bh * nc + c;
+          if (n >= kKQ) W(&s.kq_empty[kq], (n / kKQ - 1) & 1);
+          if (__any_sync(0xffffffffu, s.gave_up)) {
+            go = false;
+            break;
           }
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&s.kq_full[kq], KP / 64 * 2 * kTile);
+            for (int i = 0; i < KP / 64; ++i) {
+              tc::tma_load_4d(s.kq[kq][i][0], &mk, &s.kq_full[kq], i * 64, kg, c * kC, b);
+              tc::tma_load_4d(s.kq[kq][i][1], &mq, &s.kq_full[kq], i * 64, kg, c * kC, b);
+            }
+          }
+          __syncwarp();
+          // (after a wait that gave up, what follows is only waited for)
+          if (n >= 2) W(&s.v_empty[p], ph);
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&s.v_full[p], 2 * kTile);
+            for (int i = 0; i < 2; ++i)
+              tc::tma_load_4d(s.v[p][i], &mv, &s.v_full[p], it.v0 + i * 64, h, c * kC, b);
+          }
+          __syncwarp();
+          if (n >= 2) W(&s.vec_empty[p], ph);
+          if (n >= 2) W(&s.tp_empty[p], ph);
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&s.vec_full[p], vec_floats<kC>() * 4);
+            tc::bulk_load(s.vec[p], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4,
+                          &s.vec_full[p]);
+            tc::mbar_arrive_expect_tx(&s.tp_full[p], 4 * kTile);
+            tc::bulk_load(s.tp[p], reinterpret_cast<const unsigned char*>(a.T) + id * 4 * kTile,
+                          4 * kTile, &s.tp_full[p]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        // (after a wait that gave up, what follows is only waited for)
-        if (c >= 2) W(&s.v_empty[p], ph);
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.v_full[p], 2 * kTile);
-          for (int i = 0; i < 2; ++i)
-            tc::tma_load_4d(s.v[p][i], &mv, &s.v_full[p], v0 + i * 64, h, c * kC, b);
-        }
-        __syncwarp();
-        if (c >= 2) W(&s.vec_empty[p], ph);
-        if (c >= 2) W(&s.tp_empty[p], ph);
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.vec_full[p], vec_floats<kC>() * 4);
-          tc::bulk_load(s.vec[p], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4,
-                        &s.vec_full[p]);
-          tc::mbar_arrive_expect_tx(&s.tp_full[p], 4 * kTile);
-          tc::bulk_load(s.tp[p], reinterpret_cast<const unsigned char*>(a.T) + id * 4 * kTile,
-                        4 * kTile, &s.tp_full[p]);
-        }
-        __syncwarp();
       }
       // every copy has landed before the CTA ends
-      for (int i = c > kKQ ? c - kKQ : 0; i < c; ++i) {
+      for (int i = n > kKQ ? n - kKQ : 0; i < n; ++i) {
         drain(&s.kq_full[i % kKQ], (i / kKQ) & 1, &g_status);
-        if (i < c - 2) continue;
+        if (i < n - 2) continue;
         drain(&s.tp_full[i & 1], (i / 2) & 1, &g_status);
         drain(&s.vec_full[i & 1], (i / 2) & 1, &g_status);
         drain(&s.v_full[i & 1], (i / 2) & 1, &g_status);
@@ -162,14 +190,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto stop = [&] { return __any_sync(0xffffffffu, s.gave_up) != 0; };
       int st = 0;
       uint32_t kq_ph = 0;
-      for (int c = 0; c < nc; ++c) {
-        const uint32_t ph = c & 1, tp = c & 1;
-        const uint32_t fill = (c >> 1) & 1;
+      int n = 0, end = 0;
+      for (int k = 0;; ++n) {
+        if (n == end) {
+          const Item it = item(k++);
+          if (it.bh < 0) break;
+          end = n + it.last - it.first;
+        }
+        const uint32_t ph = n & 1, tp = n & 1;
+        const uint32_t fill = (n >> 1) & 1;
         const uint64_t dk = dk0 + st * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dm = dm0 + st * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dt = dt0 + tp * (4 * kTile >> 4), dp = dp0 + tp * (4 * kTile >> 4);
         W(&s.kq_full[st], kq_ph);
-        if (c > 0) W(&s.o1_read, ph ^ 1);
+        if (n > 0) W(&s.o1_read, ph ^ 1);
         W(&s.s_ready, ph);
         if (stop()) break;
         tc::fence_after_sync();
@@ -180,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         W(&s.tp_full[tp], fill);
-        if (c > 0) W(&s.o2_read, ph ^ 1);   // O2 and x's terms of the chunk before
+        if (n > 0) W(&s.o2_read, ph ^ 1);   // O2 and x's terms of the chunk before
         W(&s.yt_ready, ph);
         if (stop()) break;
         tc::fence_after_sync();
@@ -218,10 +252,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kOutWarp) {
     // ---------------- out = scale e^G O1 + O2
     SSD_SETREG("inc", "104");
-    const int qr = warp & 3, row = qr * 32 + lane, vr = v0 + row;
+    const int qr = warp & 3, row = qr * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
+    // (the four warps; a wait that gives up, unlike a barrier, lets every warp end)
+    auto together = [&](uint32_t phase) {
+      warp_arrive(&s.o_sync, lane);
+      W(&s.o_sync, phase);
+    };
+    Item it = {};
+    int c = 0;
+    for (int n = 0, k = 0;; ++n, ++c) {
+      if (c == it.last) {
+        it = item(k++);
+        if (it.bh < 0) break;
+        c = it.first;
+      }
+      const int b = it.bh / a.H, h = it.bh % a.H, v0 = it.v0, vr = v0 + row;
+      const uint32_t ph = n & 1;
       const float* gam = s.vec[ph] + kGam * kC;
       unsigned char* const vt = s.o[row >> 6] + (row & 63) * 2;
       float x[4][16];
@@ -240,8 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int p = 0; p < 4; ++p) scale_by(x[p], gam + p * 16);
       if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_read();   // the tiles' last copies
-      __syncwarp();
-      named_sync(1, 128);
+      together(0);
       W(&s.o_done, ph);
       tc::fence_after_sync();
 #pragma unroll
@@ -282,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_proxy_async_smem();
-      named_sync(1, 128);
+      together(1);
       if (warp == kOutWarp) {
         if (tc::elect_one()) {
           if (a.wide_out && !s.gave_up)
@@ -291,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (KEEP && !s.gave_up) {
             // planes [term][channel half][token][64] of the workspace
             unsigned char* to = reinterpret_cast<unsigned char*>(a.X) +
-                                (((int64_t)bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
+                                (((int64_t)it.bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
             for (int i = 0; i < 2; ++i)
               asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
                                to + (int64_t)i * (a.VP / 64) * kTile),
@@ -306,36 +352,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kOutWarp && tc::elect_one()) tc::bulk_wait_all();
   } else {
     // ---------------- the chain
-    const int qr = warp & 3, part = warp >> 2, row = qr * 32 + lane, vr = v0 + row;
+    const int qr = warp & 3, part = warp >> 2, row = qr * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);   // this warp's 32 TMEM lanes
     constexpr int SP = KP / 64;                           // pieces of 16 of S a thread
     float S0[SP][16];
-    read_row<SP>(S0, a.init, bh, vr, part, a);
+    Item it = {};
     // A piece of S as terms to TMEM (and to memory, as chunk c's first state)
     auto put_state = [&](int p, int c) {
       uint32_t t[16];
       two_terms(S0[p], t);
       tc::tmem_st16(lanes + kAS + (part * SP + p) * 16, t);
-      if (KEEP) keep_row<KP>(t, a.S0, (int64_t)bh * nc + c, vr, (part * SP + p) * 16, a);
+      if (KEEP) keep_row<KP>(t, a.S0, (int64_t)it.bh * nc + c, it.v0 + row, (part * SP + p) * 16, a);
     };
     auto told = [&](uint64_t* bar) {   // what this warp wrote to TMEM is there
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(bar, lane);
     };
+    int c = 0, slots = 0;
+    for (int n = 0, k = 0;; ++n, ++c) {
+      if (c == it.last) {
+        it = item(k++);
+        if (it.bh < 0) break;
+        c = it.first;
+        if (c == 0) {
+          read_row<SP>(S0, a.init, it.bh, it.v0 + row, part, a);
+        } else {
+          if (lane == 0) wait_flag(flag_of(a, it), c / a.seg, &s.gave_up, &g_status);
+          __syncwarp();
+          read_slot<SP>(S0, a, it, row, part);
+        }
 #pragma unroll
-    for (int p = 0; p < SP; ++p) put_state(p, 0);
-    told(&s.s_ready);
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
+        for (int p = 0; p < SP; ++p) put_state(p, c);
+        told(&s.s_ready);
+      }
+      const uint32_t ph = n & 1;
       const float* vec = s.vec[ph];
       const unsigned char* const vt = s.v[ph][row >> 6] + (row & 63) * 2;
       uint32_t r[16], t[16];
       float x[16];
       const int t0 = part * 16;   // the warp's tokens
       // y = v - e^G Y
-      W(&s.v_full[ph], (c >> 1) & 1);
-      W(&s.vec_full[ph], (c >> 1) & 1);
+      W(&s.v_full[ph], (n >> 1) & 1);
+      W(&s.vec_full[ph], (n >> 1) & 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {   // v's pairs of tokens, while Y is computed
         const unsigned char* q = vt + (t0 + 2 * i) * 128;
@@ -384,11 +443,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i)
           fma2(S0[p][2 * i], S0[p][2 * i + 1], S0[p][2 * i], S0[p][2 * i + 1], through, through,
                __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        if (c + 1 < nc) put_state(p, c + 1);
+        if (c + 1 < it.last) put_state(p, c + 1);
       }
-      told(&s.s_ready);
+      if (c + 1 < it.last) {
+        told(&s.s_ready);
+      } else if (c + 1 < nc) {   // on to the next segment
+        write_slot<SP>(S0, a, it, row, part);
+        warp_arrive(&s.slot_done, lane);
+        if (warp == 0) {
+          W(&s.slot_done, slots++ & 1);
+          if (lane == 0) raise_flag(flag_of(a, it), (c + 1) / a.seg);
+        }
+      } else {
+        write_row<SP>(S0, a.final, it.bh, it.v0 + row, part, a);
+      }
     }
-    write_row<SP>(S0, a.final, bh, vr, part, a);
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -412,10 +481,12 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   if (a.wide_out && !token_map(&mo, a.out, a.V, a.H, a.L, a.B, dense, false))
     return cudaErrorInvalidValue;
   const int smem = (int)sizeof(Smem<KP, KEEP>) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       tc_forward_kernel<KP, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.V + 127) / 128));
+  int grid = 0;
+  e = start_work(a, &grid, st);
+  if (e != cudaSuccess) return e;
   tc_forward_kernel<KP, KEEP><<<grid, kThreads, smem, st>>>(mq, mk, mv, mo, a);
   return cudaGetLastError();
 }

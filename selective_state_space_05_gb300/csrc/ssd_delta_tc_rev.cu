@@ -1,6 +1,6 @@
 // The gated delta rule's backward along the sequence on tcgen05, last chunk first:
-// one CTA per (batch row, head, 128 channels), transposed as the forward, with the
-// state's gradient dS in registers and as two bf16 terms in TMEM.  Per chunk:
+// one CTA per SM, each at one (batch row, head, 128 channels), transposed as the
+// forward, with the state's gradient dS in registers and as two bf16 terms in TMEM.  Per chunk:
 //   Z = dS K^T                                A: dS
 //   dx = beta e^(G_C - G) Z + do P -> TMEM     (do P ahead: A: do, one term)
 //   dY = dx T                                 A: dx, over Z's columns
@@ -34,7 +34,9 @@ struct Smem {
   alignas(16) float vec[2][vec_floats<kC>()];
   uint64_t kq_full[2], kq_empty[2], d_full[2], d_empty[2], tp_full[2], tp_empty[2], vec_full[2],
       vec_empty[2];
-  uint64_t s_ready, z_done, xt_ready, y_done, w_ready, w_done, in_ready, mma_drain;
+  uint64_t s_ready, z_done, xt_ready, y_done, w_ready, w_done, in_ready, io_sync, slot_done,
+      mma_drain;
+  Items items;
   uint32_t tmem;
   volatile int gave_up;
 };
@@ -50,8 +52,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<KP>;
   S& s = *reinterpret_cast<S*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
-  const int v0 = blockIdx.y * 128;
   const int nc = a.nc;
   if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, 512);
   if (tid == 0) {
@@ -65,10 +65,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&s.vec_full[i], 1);
       tc::mbar_init(&s.vec_empty[i], kChainWarps + 4);
     }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.items.full[i], 1);
+      tc::mbar_init(&s.items.empty[i], kChainWarps + 5);   // ... io's four, the MMAs' one
+    }
     tc::mbar_init(&s.s_ready, kChainWarps);
     tc::mbar_init(&s.xt_ready, kChainWarps);
     tc::mbar_init(&s.w_ready, kChainWarps);
     tc::mbar_init(&s.in_ready, 4);
+    tc::mbar_init(&s.io_sync, 4);
+    tc::mbar_init(&s.slot_done, kChainWarps);
     tc::mbar_init(&s.z_done, 1);
     tc::mbar_init(&s.y_done, 1);
     tc::mbar_init(&s.w_done, 1);
@@ -82,41 +88,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem;
   auto W = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &s.gave_up, &g_status); };
+  // the CTA's n-th item, for all lanes of a warp (bh < 0: no more); its chunks count
+  // from the sequence's end
+  auto item = [&](int n) {
+    W(&s.items.full[n & 1], (n >> 1) & 1);
+    Item i = s.items.item[n & 1];
+    warp_arrive(&s.items.empty[n & 1], lane);
+    if (__any_sync(0xffffffffu, s.gave_up)) i.bh = -1;
+    return i;
+  };
 
   if (warp >= kMmaWarp) {
     SSD_SETREG("dec", "48");
     if (warp == kLoadWarp) {
-      int n = 0;
-      for (; n < nc; ++n) {
-        const int c = nc - 1 - n, p = n & 1;
-        const uint32_t ph = (n / 2 - 1) & 1;
-        const int64_t id = (int64_t)bh * nc + c;
-        if (n >= 2) W(&s.d_empty[p], ph);
-        if (n >= 2) W(&s.vec_empty[p], ph);
-        if (__any_sync(0xffffffffu, s.gave_up)) break;
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.d_full[p], 2 * kTile);
-          for (int i = 0; i < 2; ++i)
-            tc::tma_load_4d(s.d[p][i], &md, &s.d_full[p], v0 + i * 64, h, c * kC, b);
-          tc::mbar_arrive_expect_tx(&s.vec_full[p], vec_floats<kC>() * 4);
-          tc::bulk_load(s.vec[p], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4,
-                        &s.vec_full[p]);
-        }
-        __syncwarp();
-        // (after a wait that gave up, what follows is only waited for)
-        if (n >= 2) W(&s.tp_empty[p], ph);
-        if (n >= 2) W(&s.kq_empty[p], ph);
-        if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&s.tp_full[p], 4 * kTile);
-          tc::bulk_load(s.tp[p], reinterpret_cast<const unsigned char*>(a.T) + id * 4 * kTile,
-                        4 * kTile, &s.tp_full[p]);
-          tc::mbar_arrive_expect_tx(&s.kq_full[p], KP / 64 * 2 * kTile);
-          for (int i = 0; i < KP / 64; ++i) {
-            tc::tma_load_4d(s.kq[p][i][0], &mk, &s.kq_full[p], i * 64, kg, c * kC, b);
-            tc::tma_load_4d(s.kq[p][i][1], &mq, &s.kq_full[p], i * 64, kg, c * kC, b);
+      int n = 0;   // chunks so far
+      bool go = true;
+      for (int k = 0; go; ++k) {
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(a.ctrl, 1);
+        const Item it = item_of(a, __shfl_sync(0xffffffffu, ticket, 0));
+        if (k >= 2) W(&s.items.empty[k & 1], (k / 2 - 1) & 1);
+        if (lane == 0) s.items.item[k & 1] = it;
+        warp_arrive(&s.items.full[k & 1], lane);
+        if (it.bh < 0) break;
+        const int b = it.bh / a.H, h = it.bh % a.H, kg = h / (a.H / a.G);
+        for (int r = it.first; r < it.last; ++r, ++n) {
+          const int c = nc - 1 - r, p = n & 1;
+          const uint32_t ph = (n / 2 - 1) & 1;
+          const int64_t id = (int64_t)it.bh * nc + c;
+          if (n >= 2) W(&s.d_empty[p], ph);
+          if (n >= 2) W(&s.vec_empty[p], ph);
+          if (__any_sync(0xffffffffu, s.gave_up)) {
+            go = false;
+            break;
           }
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&s.d_full[p], 2 * kTile);
+            for (int i = 0; i < 2; ++i)
+              tc::tma_load_4d(s.d[p][i], &md, &s.d_full[p], it.v0 + i * 64, h, c * kC, b);
+            tc::mbar_arrive_expect_tx(&s.vec_full[p], vec_floats<kC>() * 4);
+            tc::bulk_load(s.vec[p], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4,
+                          &s.vec_full[p]);
+          }
+          __syncwarp();
+          // (after a wait that gave up, what follows is only waited for)
+          if (n >= 2) W(&s.tp_empty[p], ph);
+          if (n >= 2) W(&s.kq_empty[p], ph);
+          if (tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(&s.tp_full[p], 4 * kTile);
+            tc::bulk_load(s.tp[p], reinterpret_cast<const unsigned char*>(a.T) + id * 4 * kTile,
+                          4 * kTile, &s.tp_full[p]);
+            tc::mbar_arrive_expect_tx(&s.kq_full[p], KP / 64 * 2 * kTile);
+            for (int i = 0; i < KP / 64; ++i) {
+              tc::tma_load_4d(s.kq[p][i][0], &mk, &s.kq_full[p], i * 64, kg, c * kC, b);
+              tc::tma_load_4d(s.kq[p][i][1], &mq, &s.kq_full[p], i * 64, kg, c * kC, b);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       // every copy has landed before the CTA ends
       for (int i = n > 2 ? n - 2 : 0; i < n; ++i) {
@@ -148,8 +177,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      do_p(0);
-      for (int n = 0; n < nc; ++n) {
+      int n = 0, end = 0, k = 0;
+      // whether there is an n-th chunk (taking the next item for it)
+      auto more = [&] {
+        if (n < end) return true;
+        const Item it = item(k++);
+        end = n + (it.bh < 0 ? 0 : it.last - it.first);
+        return n < end;
+      };
+      bool go = more();
+      if (go) do_p(0);
+      while (go) {
         const uint32_t ph = n & 1, p = n & 1, fill = (n >> 1) & 1;
         const uint64_t dk = dk0 + p * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dm = dm0 + p * ((KP / 64) * S::kHalf >> 4);   // keys; queries a tile on
@@ -187,7 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(&s.tp_empty[p]);
         }
         __syncwarp();
-        if (n + 1 < nc) do_p(n + 1);   // (while dS is on its way)
+        ++n;
+        go = more();
+        if (go) do_p(n);   // (while dS is on its way)
       }
       if (tc::elect_one()) tc::mma_commit(&s.mma_drain);
       __syncwarp();
@@ -196,8 +236,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kIoWarp) {
     // ---------------- do into TMEM, dY out of it
     SSD_SETREG("inc", "104");
-    const int qr = warp & 3, row = qr * 32 + lane, vr = v0 + row;
+    const int qr = warp & 3, row = qr * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);
+    // (the four warps; a wait that gives up, unlike a barrier, lets every warp end)
+    auto together = [&](uint32_t phase) {
+      warp_arrive(&s.io_sync, lane);
+      W(&s.io_sync, phase);
+    };
     auto put_do = [&](int n) {
       const int p = n & 1;
       const unsigned char* const dt = s.d[p][row >> 6] + (row & 63) * 2;
@@ -225,14 +270,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before_sync();
       warp_arrive(&s.in_ready, lane);
     };
-    put_do(0);
-    for (int n = 0; n < nc; ++n) {
-      const int c = nc - 1 - n;
+    int k = 0;
+    Item it = item(k++);
+    int r = it.first;   // the chunk, counted from the end
+    if (it.bh >= 0) put_do(0);
+    for (int n = 0; it.bh >= 0; ++n) {
+      const int c = nc - 1 - r;
+      const int b = it.bh / a.H, h = it.bh % a.H, v0 = it.v0, vr = v0 + row;
       if (warp == kIoWarp && tc::elect_one()) tc::bulk_wait_read();   // the tiles' last copies
       __syncwarp();
       W(&s.y_done, n & 1);
       tc::fence_after_sync();
-      named_sync(1, 128);
+      together(0);
       unsigned char* const yt = s.y[0][row >> 6];
       for (int q = 0; q < 4; ++q) {
         uint32_t r[16];
@@ -257,13 +306,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_before_sync();
       tc::fence_proxy_async_smem();
-      named_sync(1, 128);
+      together(1);
       if (warp == kIoWarp) {
         if (tc::elect_one()) {
           if (!s.gave_up) {
             // planes [term][channel half][token][64] of the workspace; the first is dv
             unsigned char* to = reinterpret_cast<unsigned char*>(a.dY) +
-                                (((int64_t)bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
+                                (((int64_t)it.bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
             for (int i = 0; i < 2; ++i)
               asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
                                to + (int64_t)i * (a.VP / 64) * kTile),
@@ -278,31 +327,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (n + 1 < nc) put_do(n + 1);   // (what the MMAs read of n's is done as dY is)
+      if (++r == it.last) {
+        it = item(k++);
+        r = it.first;
+      }
+      if (it.bh >= 0) put_do(n + 1);   // (what the MMAs read of n's is done as dY is)
     }
     if (warp == kIoWarp && tc::elect_one()) tc::bulk_wait_all();
   } else {
     // ---------------- the chain
-    const int qr = warp & 3, part = warp >> 2, row = qr * 32 + lane, vr = v0 + row;
+    const int qr = warp & 3, part = warp >> 2, row = qr * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);   // this warp's 32 TMEM lanes
     constexpr int SP = KP / 64;                           // pieces of 16 of dS a thread
     float dS[SP][16];
-    read_row<SP>(dS, a.dfinal, bh, vr, part, a);
+    Item it = {};
     auto put_state = [&](int p, int c) {
       uint32_t t[16];
       two_terms(dS[p], t);
       tc::tmem_st16(lanes + kAS + (part * SP + p) * 16, t);
-      keep_row<KP>(t, a.dS, (int64_t)bh * nc + c, vr, (part * SP + p) * 16, a);
+      keep_row<KP>(t, a.dS, (int64_t)it.bh * nc + c, it.v0 + row, (part * SP + p) * 16, a);
     };
     auto told = [&](uint64_t* bar) {   // what this warp wrote to TMEM is there
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(bar, lane);
     };
+    int rc = 0, slots = 0;   // the chunk, counted from the end
+    for (int n = 0, k = 0;; ++n, ++rc) {
+      if (rc == it.last) {
+        it = item(k++);
+        if (it.bh < 0) break;
+        rc = it.first;
+        if (rc == 0) {
+          read_row<SP>(dS, a.dfinal, it.bh, it.v0 + row, part, a);
+        } else {
+          if (lane == 0) wait_flag(flag_of(a, it), rc / a.seg, &s.gave_up, &g_status);
+          __syncwarp();
+          read_slot<SP>(dS, a, it, row, part);
+        }
 #pragma unroll
-    for (int p = 0; p < SP; ++p) put_state(p, nc - 1);
-    told(&s.s_ready);
-    for (int n = 0; n < nc; ++n) {
+        for (int p = 0; p < SP; ++p) put_state(p, nc - 1 - rc);
+        told(&s.s_ready);
+      }
       const uint32_t ph = n & 1;
       const float* vec = s.vec[ph];
       uint32_t r[16], t[16];
@@ -352,11 +418,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i)
           fma2(dS[p][2 * i], dS[p][2 * i + 1], dS[p][2 * i], dS[p][2 * i + 1], through, through,
                __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        if (n + 1 < nc) put_state(p, nc - 2 - n);
+        if (rc + 1 < it.last) put_state(p, nc - 2 - rc);
       }
-      told(&s.s_ready);
+      if (rc + 1 < it.last) {
+        told(&s.s_ready);
+      } else if (rc + 1 < nc) {   // on to the next segment
+        write_slot<SP>(dS, a, it, row, part);
+        warp_arrive(&s.slot_done, lane);
+        if (warp == 0) {
+          W(&s.slot_done, slots++ & 1);
+          if (lane == 0) raise_flag(flag_of(a, it), (rc + 1) / a.seg);
+        }
+      } else {
+        write_row<SP>(dS, a.dinit, it.bh, it.v0 + row, part, a);
+      }
     }
-    write_row<SP>(dS, a.dinit, bh, vr, part, a);
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -380,10 +456,12 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   if (a.wide_dv && !token_map(&mv, a.dv, a.V, a.H, a.L, a.B, dense, true))
     return cudaErrorInvalidValue;
   const int smem = (int)sizeof(Smem<KP>) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       tc_reverse_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.V + 127) / 128));
+  int grid = 0;
+  e = start_work(a, &grid, st);
+  if (e != cudaSuccess) return e;
   tc_reverse_kernel<KP><<<grid, kThreads, smem, st>>>(mq, mk, md, mv, a);
   return cudaGetLastError();
 }

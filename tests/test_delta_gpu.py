@@ -305,3 +305,27 @@ def test_refusals(ssd):
         ssd.delta_scan_bwd(out.transpose(1, 2), *ins)
     with pytest.raises(ValueError):
         ssd.delta_decode_step(*(x[:, 0] for x in ins), d["initial_states"].transpose(2, 3))
+
+
+@pytest.mark.parametrize("V", [40, 130])
+def test_more_sequences_than_sms(ssd, V):
+    """So many heads that the SMs take their sequences in segments: every head is the
+    same scan alone."""
+    B, L, H, K = 4, 1500, 50, 32
+    d = du.inputs(B, L, H, H, V, K, BF, seed=60)
+    ins, kw = split(d)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dout = torch.randn(B, L, H, V, generator=gen, device="cuda").to(BF)
+    df = torch.randn(B, H, V, K, generator=gen, device="cuda")
+    out, fin = ssd.delta_scan_fwd(*ins, return_final_states=True, **kw)
+    got = ssd.delta_scan_bwd(dout, *ins, dfinal_states=df, **kw)
+    for b, h in ((0, 0), (1, 17), (3, 49)):
+        one = [t[b:b + 1, :, h:h + 1].contiguous() for t in ins]
+        init = kw["initial_states"][b:b + 1, h:h + 1].contiguous()
+        o, f = ssd.delta_scan_fwd(*one, initial_states=init, return_final_states=True)
+        assert torch.equal(o[0, :, 0], out[b, :, h]) and torch.equal(f[0, 0], fin[b, h])
+        g = ssd.delta_scan_bwd(dout[b:b + 1, :, h:h + 1].contiguous(), *one, initial_states=init,
+                               dfinal_states=df[b:b + 1, h:h + 1].contiguous())
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(g[n][0, :, 0], got[n][b, :, h]), n
+        assert torch.equal(g["d_initial_states"][0, 0], got["d_initial_states"][b, h])
