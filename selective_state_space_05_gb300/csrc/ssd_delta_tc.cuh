@@ -293,7 +293,7 @@ __device__ __forceinline__ void store_block_t(const float (&x)[4], const float (
         *reinterpret_cast<uint32_t*>(base + t * kTile + at) = trans8(w[t]);
     }
 }
-constexpr int kDiag = 16 * 20;   // floats of a diagonal block's transpose
+constexpr int kDiag = 16 * 16;   // floats of a diagonal block's transpose
 
 // T = (I + A)^-1 for strictly lower A [64][64], by four warps (named barrier `id`):
 // A's blocks below the diagonal as planes, its diagonal blocks transposed in fp32;
@@ -312,7 +312,7 @@ __device__ __forceinline__ void invert(unsigned char* t, const unsigned char* a,
     for (int j = 0; j < 15; ++j) {
 #pragma unroll
       for (int q = (j + 1) / 4; q < 4; ++q) {
-        const float4 f = *reinterpret_cast<const float4*>(d + j * 20 + 4 * q);
+        const float4 f = *reinterpret_cast<const float4*>(d + j * 16 + 4 * q);
         const float col[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -494,47 +494,54 @@ __device__ __forceinline__ void pair_products(float (&x)[10][4], uint32_t ba, ui
 }
 // Those products with their decays: A = strictly lower D k k^T beta_j into planes
 // (its diagonal blocks transposed to diag), or P = lower D q k^T scale beta_j, as
-// terms.
-template <bool ODD>
+// terms.  RESETS: whether a state starts anew within the chunk.
+template <bool ODD, bool RESETS>
 __device__ __forceinline__ void pair_decays(const float (&x)[10][4], const float* vec, bool keys,
                                             float scale, unsigned char* planes, float* diag,
                                             int lane) {
   constexpr int r0 = ODD ? 2 : 3, r1 = ODD ? 1 : 0;
   const int g = lane >> 2, t = lane & 3;
-  const float neg = __int_as_float(0xff800000);
+  const float neg = __int_as_float(0xff800000), f = keys ? 1.f : scale;
   float hi[4], lo[4], sg[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {   // the two rows of r0, the two of r1
     const int i = (r < 2 ? r0 : r1) * 16 + g + 8 * (r & 1);
     hi[r] = vec[kGhi * kC + i];
     lo[r] = vec[kGlo * kC + i];
-    sg[r] = vec[kSeg * kC + i];
+    sg[r] = RESETS ? vec[kSeg * kC + i] : 0.f;
   }
 #pragma unroll
   for (int n = 0; n < 2 * (r0 + 1); ++n) {
     const int j = n * 8 + t * 2;
     const float2 h = *reinterpret_cast<const float2*>(vec + kGhi * kC + j);
     const float2 l = *reinterpret_cast<const float2*>(vec + kGlo * kC + j);
-    const float2 s = *reinterpret_cast<const float2*>(vec + kSeg * kC + j);
+    float2 s = make_float2(0.f, 0.f);
+    if (RESETS) s = *reinterpret_cast<const float2*>(vec + kSeg * kC + j);
     float2 be = *reinterpret_cast<const float2*>(vec + kBeta * kC + j);
-    be.x *= keys ? 1.f : scale;
-    be.y *= keys ? 1.f : scale;
+    mul2(be.x, be.y, f, f);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int rb = r < 2 ? r0 : r1, i = rb * 16 + g + 8 * (r & 1);
       if (n >= 2 * (rb + 1)) continue;
       const float* v = &x[(r < 2 ? 0 : 2 * (r0 + 1)) + n][2 * (r & 1)];
       const bool last = n >= 2 * rb;   // the diagonal block
-      const bool n0 = s.x == sg[r] && (!last || (keys ? i > j : i >= j));
-      const bool n1 = s.y == sg[r] && (!last || (keys ? i > j + 1 : i >= j + 1));
-      const float d0 = ex2(n0 ? (hi[r] - h.x) + (lo[r] - l.x) : neg);
-      const float d1 = ex2(n1 ? (hi[r] - h.y) + (lo[r] - l.y) : neg);
-      const float y0 = n0 ? v[0] * (d0 * be.x) : 0.f;
-      const float y1 = n1 ? v[1] * (d1 * be.y) : 0.f;
+      const bool n0 = (!RESETS || s.x == sg[r]) && (!last || (keys ? i > j : i >= j));
+      const bool n1 = (!RESETS || s.y == sg[r]) && (!last || (keys ? i > j + 1 : i >= j + 1));
+      float e0 = hi[r], e1 = hi[r], c0 = lo[r], c1 = lo[r];
+      add2p(e0, e1, -h.x, -h.y);
+      add2p(c0, c1, -l.x, -l.y);
+      add2p(e0, e1, c0, c1);
+      float y0 = ex2(n0 ? e0 : neg), y1 = ex2(n1 ? e1 : neg);
+      mul2(y0, y1, be.x, be.y);
+      mul2(y0, y1, v[0], v[1]);
+      if (RESETS || last) {   // (a product that is not finite stays out of what it is not part of)
+        y0 = n0 ? y0 : 0.f;
+        y1 = n1 ? y1 : 0.f;
+      }
       if (keys && last) {
-        float* p = diag + rb * kDiag + (j - rb * 16) * 20 + i - rb * 16;
+        float* p = diag + rb * kDiag + (j - rb * 16) * 16 + i - rb * 16;
         p[0] = y0;
-        p[20] = y1;
+        p[16] = y1;
       } else {
         uint32_t m[2];
         split2<2>(y0, y1, m);

@@ -16,12 +16,10 @@ template <int KP>
 struct Smem {
   union {
     unsigned char kq[KP / 64][2][kTile];   // 64 columns: 64 rows of K, 64 of Q
-    struct {
-      unsigned char a[2][kTile];           // afterwards: the inverse's A, two terms
-      float diag[4][kDiag];
-    };
+    unsigned char tp[4][kTile];            // afterwards: T's terms, P's terms
   };
-  unsigned char tp[4][kTile];              // T's terms, P's terms
+  unsigned char a[2][kTile];               // the inverse's A, two terms
+  float diag[4][kDiag];
   alignas(16) float vec[vec_floats<kC>()];
   uint64_t full;
   volatile int gave_up;
@@ -29,7 +27,7 @@ struct Smem {
 __device__ int g_status;
 
 template <int KP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     tc_prepare_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ Args a) {
   extern __shared__ unsigned char raw[];
@@ -49,9 +47,6 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if (w == 0) chunk_vectors(load_gates(a, b, h, (int64_t)c * kC, lane), s.vec, lane);
-  else
-    for (int i = tid - 32; i < 4 * (int)kTile / 16; i += kThreads - 32)
-      reinterpret_cast<uint4*>(s.tp)[i] = make_uint4(0, 0, 0, 0);   // above the diagonal
   __syncthreads();
   wait_for(&s.full, 0, &s.gave_up, &g_status);
   const bool keys = w < 2;
@@ -59,10 +54,21 @@ __global__ void __launch_bounds__(kThreads)
   float x[10][4];
   if (w & 1) pair_products<KP, true>(x, ba, bk, 2 * kTile, lane);
   else pair_products<KP, false>(x, ba, bk, 2 * kTile, lane);
-  __syncthreads();   // K's and Q's memory is A's from here
+  __syncthreads();   // K's and Q's memory is T's and P's from here
+  // zeros above the diagonal: of rows r of 16, the units (of 8 columns) from 2 r + 2 on
+  for (int i = tid; i < 4 * 64 * 6; i += kThreads) {
+    const int row = i / 6 % 64, u = 2 + i % 6;
+    if (u >= 2 * (row >> 4) + 2)
+      *reinterpret_cast<uint4*>(s.tp[i / 384] + tile_at<64>(row, u)) = make_uint4(0, 0, 0, 0);
+  }
   unsigned char* const to = keys ? s.a[0] : s.tp[2];
-  if (w & 1) pair_decays<true>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
-  else pair_decays<false>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
+  if (s.vec[kSeg * kC + kC - 1] != 0.f) {
+    if (w & 1) pair_decays<true, true>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
+    else pair_decays<false, true>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
+  } else {
+    if (w & 1) pair_decays<true, false>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
+    else pair_decays<false, false>(x, s.vec, keys, a.scale, to, s.diag[0], lane);
+  }
   __syncthreads();
   invert(s.tp[0], s.a[0], s.diag[0], w, lane, 1);
   tc::fence_proxy_async_smem();
@@ -75,7 +81,7 @@ __global__ void __launch_bounds__(kThreads)
                  "r"(saddr(s.tp[0])), "r"(4 * kTile)
                  : "memory");
     tc::bulk_commit();
-    tc::bulk_wait_all();
+    tc::bulk_wait_read();   // (the writes end with the kernel)
   }
 }
 
