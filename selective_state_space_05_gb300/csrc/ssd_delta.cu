@@ -66,6 +66,7 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
       a.segs = (int)((a.nc + seg - 1) / seg);
     }
   }
+  a.pass = kWhole;
   a.qcols = a.kcols = K;
   a.vcols = a.docols = V;
   return a;
@@ -104,13 +105,30 @@ template <typename F>
 void carve_work(Args& a, F take) {
   if (!a.tc) return;
   const size_t lanes = (size_t)a.B * a.H * (a.VP / 128);
+  const size_t slots = a.pass == kParts ? lanes * (a.segs - 1) + (size_t)a.B * a.H * (a.segs - 2)
+                       : a.segs > 1     ? lanes
+                                        : 0;
   a.ctrl = reinterpret_cast<int*>(take((1 + lanes) * sizeof(int)));
-  a.slots = reinterpret_cast<float*>(take(a.segs > 1 ? lanes * 128 * a.KP * 4 : 0));
+  a.slots = reinterpret_cast<float*>(take(slots * 128 * a.KP * 4));
+}
+// A few long sequences leave most SMs idle: their segments run all at once, in two
+// passes.  The first has (2 segs - 3) items a sequence of 128 channels, the second
+// segs: with as many as the SMs take in two rounds and in one, both take about
+// nc / segs chunks.  Worth it from four segments of sixteen chunks on.
+void split(Args& a) {
+  const int64_t lanes = (int64_t)a.B * a.H * (a.VP / 128);
+  if (!a.tc || a.segs > 1) return;
+  int64_t segs = row::sm_count() / lanes;
+  if (segs > a.nc / 16) segs = a.nc / 16;
+  if (segs < 4) return;
+  a.seg = (int)((a.nc + segs - 1) / segs);
+  a.segs = (a.nc + a.seg - 1) / a.seg;
+  a.pass = kParts;
 }
 
 // The forward's pieces of a workspace at `base`, and how many bytes they take.
 template <typename T>
-size_t carve(Args& a, void* base, bool keep) {
+size_t carve(Args& a, void* base, bool keep) {   // (the forward's `a`: split)
   constexpr int C = Mode<T>::C, NT = Mode<T>::NT;
   const size_t n = (size_t)a.B * a.H * a.nc;
   char* p = static_cast<char*>(base);
@@ -155,6 +173,7 @@ size_t carve_bwd(Args& a, void* base) {
   return at;
 }
 size_t fwd_bytes(Args& a, int dtype, void* base, bool keep) {
+  split(a);
   return dtype == SSD_DTYPE_BF16 ? carve<bf16>(a, base, keep) : carve<float>(a, base, keep);
 }
 size_t bwd_bytes(Args& a, int dtype, void* base) {
@@ -359,8 +378,11 @@ int status(int reset, cudaStream_t st, int* bits) {
 }
 
 cudaError_t start_work(const Args& a, int* grid, cudaStream_t st) {
-  const int lanes = a.B * a.H * (a.VP / 128);
-  *grid = lanes < row::sm_count() ? lanes : row::sm_count();
+  const int lanes = a.B * a.H * (a.VP / 128), sms = row::sm_count();
+  const int items = a.pass == kParts ? lanes * (a.segs - 1) + a.B * a.H * (a.segs - 2)
+                    : a.pass == kJoined ? lanes * a.segs
+                                        : lanes;
+  *grid = items < sms ? items : sms;
   return cudaMemsetAsync(a.ctrl, 0, (1 + lanes) * sizeof(int), st);
 }
 
@@ -430,7 +452,8 @@ size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int nhe
                                           int dstate, int ngroups, ssd_dtype_t dtype, int saved, int aligned) {
   if (check_sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype) != SSD_OK) return 0;
   Args a = sizes(batch, seqlen, nheads, headdim, dstate, ngroups, dtype);
-  return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(a, dtype, nullptr, true)) +
+  Args f = a;
+  return bwd_bytes(a, dtype, nullptr) + (saved ? 0 : fwd_bytes(f, dtype, nullptr, true)) +
          (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a));
 }
 
@@ -456,7 +479,8 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
     return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element (dq, dk: to two)");
   if (off(workspace, 256) || off(saved, 256))
     return bad(SSD_ERR_ALIGN, "workspace and saved must be 256-byte aligned");
-  const size_t kept = fwd_bytes(a, dtype, nullptr, true), own = bwd_bytes(a, dtype, nullptr);
+  Args f = a;   // the forward's pieces, and its work where it is computed again
+  const size_t kept = fwd_bytes(f, dtype, nullptr, true), own = bwd_bytes(a, dtype, nullptr);
   if (saved && saved_bytes < kept)
     return bad(SSD_ERR_WORKSPACE, "saved is not the workspace of a forward with keep at these sizes");
   const int64_t hv = (int64_t)nheads * headdim;
@@ -467,9 +491,13 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   const size_t used = own + (saved ? 0 : kept);
   if (workspace_bytes < used + (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a)))
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
-  fwd_bytes(a, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
-  Args f = a;   // a forward that is computed again has its own work's state
+  fwd_bytes(f, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
   bwd_bytes(a, dtype, workspace);
+  a.T = f.T;
+  a.P = f.P;
+  a.vec = f.vec;
+  a.S0 = f.S0;
+  a.X = f.X;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == SSD_DTYPE_BF16;
   char* const at = static_cast<char*>(workspace) + used;

@@ -40,6 +40,13 @@ constexpr float kReset = -104.f;
 // From this headdim on bf16 runs on tcgen05, whose MMAs have 128 channels.
 constexpr int kTcHeaddim = 33;
 
+// How the tcgen05 forward takes its segments: one after another, each from the
+// state that the one before left; or all at once, which takes two passes.  The first
+// gives each segment's effect on a state, S -> S M + W: W from a state of zeros, M
+// from the unit rows and without values.  Those are joined, and the second pass
+// starts each segment from its own state.
+enum { kWhole, kParts, kJoined };
+
 // Per chunk and head: vectors of C floats each, then e^(G_C) alone.
 // e^G, e^(G_C - G), beta, G in two floats, the resets before a token; beta e^(G_C - G)
 // and -e^G
@@ -68,6 +75,7 @@ struct Args {
   // the tcgen05 kernels' work: sequences in `segs` segments of `seg` chunks, a ticket
   // and one flag for each (head, 128 channels), and its state between segments
   int segs, seg;
+  int pass;        // kWhole; or of a few long sequences, kParts and then kJoined
   int* ctrl;
   float* slots;
   // gradients; per head [B, L, H, dstate] fp32 where heads share queries and keys

@@ -174,17 +174,31 @@ __device__ __forceinline__ void write_row(const float (&x)[SP][16], float* state
 // for it ends.
 struct Item {
   int bh, v0, first, last;   // head, channel, chunks [first, last)
+  int slot;                  // where its state comes from or goes to (kParts, kJoined)
+  int unit;                  // from unit rows, without values
 };
 __device__ __forceinline__ Item item_of(const Args& a, int ticket) {
   const int vb = (a.V + 127) / 128, n = a.B * a.H * vb;
-  Item i = {-1, 0, 0, 0};
-  if (ticket < n * a.segs) {
-    const int seg = ticket / n, r = ticket % n;
+  Item i = {-1, 0, 0, 0, 0, 0};
+  int seg = 0;
+  if (a.pass == kParts && ticket >= n * (a.segs - 1)) {
+    // M of the segments between the first and the last, behind the W
+    const int t = ticket - n * (a.segs - 1);
+    if (t >= a.B * a.H * (a.segs - 2)) return i;
+    i.bh = t % (a.B * a.H);
+    seg = t / (a.B * a.H) + 1;
+    i.unit = 1;
+    i.slot = ticket;
+  } else {
+    if (ticket >= n * (a.pass == kParts ? a.segs - 1 : a.segs)) return i;
+    const int r = ticket % n;
+    seg = ticket / n;
     i.bh = r / vb;
     i.v0 = r % vb * 128;
-    i.first = seg * a.seg;
-    i.last = min(i.first + a.seg, a.nc);
+    i.slot = a.pass == kJoined ? ticket - n : ticket;
   }
+  i.first = seg * a.seg;
+  i.last = min(i.first + a.seg, a.nc);
   return i;
 }
 // Two items ahead in shared memory.
@@ -216,11 +230,14 @@ __device__ __forceinline__ void raise_flag(int* flag, int to) {
 }
 // A row of a state between segments: [head, 128 channels][16 columns][4 of them][row],
 // a warp's rows side by side.
+__device__ __forceinline__ int slot_of(const Args& a, const Item& it) {
+  return a.pass == kWhole ? it.bh * ((a.V + 127) / 128) + it.v0 / 128 : it.slot;
+}
 template <int SP>
 __device__ __forceinline__ void read_slot(float (&x)[SP][16], const Args& a, const Item& it, int row,
                                           int part) {
-  const float4* p = reinterpret_cast<const float4*>(a.slots) +
-                    (int64_t)(it.bh * ((a.V + 127) / 128) + it.v0 / 128) * 32 * a.KP + row;
+  const float4* p =
+      reinterpret_cast<const float4*>(a.slots) + (int64_t)slot_of(a, it) * 32 * a.KP + row;
 #pragma unroll
   for (int k = 0; k < SP; ++k)
 #pragma unroll
@@ -238,8 +255,7 @@ __device__ __forceinline__ void read_slot(float (&x)[SP][16], const Args& a, con
 template <int SP>
 __device__ __forceinline__ void write_slot(const float (&x)[SP][16], const Args& a, const Item& it,
                                            int row, int part) {
-  float4* p = reinterpret_cast<float4*>(a.slots) +
-              (int64_t)(it.bh * ((a.V + 127) / 128) + it.v0 / 128) * 32 * a.KP + row;
+  float4* p = reinterpret_cast<float4*>(a.slots) + (int64_t)slot_of(a, it) * 32 * a.KP + row;
 #pragma unroll
   for (int k = 0; k < SP; ++k)
 #pragma unroll
@@ -558,6 +574,8 @@ __device__ __forceinline__ void pair_decays(const float (&x)[10][4], const float
 bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, int B, TokStride s,
                bool swizzle);
 
+// After kParts: each segment's first state but the first's, into the slots of W.
+cudaError_t launch_tc_join(const Args& a, cudaStream_t st);
 // Clears a.ctrl for a launch of `grid` CTAs.
 cudaError_t start_work(const Args& a, int* grid, cudaStream_t st);
 

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             *reinterpret_cast<bf16*>(vt + (p * 16 + i) * 128) = __float2bfloat16_rn(x[p][i]);
-        } else if (a.out && vr < a.V) {   // rows off 16 bytes
+        } else if (a.out && vr < a.V && a.pass != kParts) {   // rows off 16 bytes
           const int64_t t0 = (int64_t)c * kC + p * 16;
           bf16* dst = static_cast<bf16*>(a.out) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vr;
 #pragma unroll
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       together(1);
       if (warp == kOutWarp) {
         if (tc::elect_one()) {
-          if (a.wide_out && !s.gave_up)
+          if (a.wide_out && !s.gave_up && a.pass != kParts)
             for (int i = 0; i < 2; ++i)
               if (v0 + i * 64 < a.V) tc::tma_store_4d(&mo, s.o[i], v0 + i * 64, h, c * kC, b);
           if (KEEP && !s.gave_up) {
@@ -377,8 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         c = it.first;
         if (c == 0) {
           read_row<SP>(S0, a.init, it.bh, it.v0 + row, part, a);
+        } else if (a.pass == kParts) {
+#pragma unroll
+          for (int p = 0; p < SP; ++p)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              S0[p][i] = it.unit && row == (part * SP + p) * 16 + i ? 1.f : 0.f;
         } else {
-          if (lane == 0) wait_flag(flag_of(a, it), c / a.seg, &s.gave_up, &g_status);
+          if (lane == 0 && a.pass == kWhole) wait_flag(flag_of(a, it), c / a.seg, &s.gave_up, &g_status);
           __syncwarp();
           read_slot<SP>(S0, a, it, row, part);
         }
@@ -398,8 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {   // v's pairs of tokens, while Y is computed
         const unsigned char* q = vt + (t0 + 2 * i) * 128;
-        t[i] = *reinterpret_cast<const uint16_t*>(q) |
-               (uint32_t)*reinterpret_cast<const uint16_t*>(q + 128) << 16;
+        t[i] = it.unit ? 0u
+                       : *reinterpret_cast<const uint16_t*>(q) |
+                             (uint32_t)*reinterpret_cast<const uint16_t*>(q + 128) << 16;
       }
       W(&s.y_done, ph);
       tc::fence_after_sync();
@@ -447,7 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (c + 1 < it.last) {
         told(&s.s_ready);
+      } else if (a.pass == kParts) {
+        write_slot<SP>(S0, a, it, row, part);
       } else if (c + 1 < nc) {   // on to the next segment
+        if (a.pass == kJoined) continue;
         write_slot<SP>(S0, a, it, row, part);
         warp_arrive(&s.slot_done, lane);
         if (warp == 0) {
@@ -500,7 +510,56 @@ int tc_forward_status(int reset, cudaStream_t st, int* bits) {
   return read_status(fwd::g_status, reset, st, bits);
 }
 
-cudaError_t launch_tc_forward(const Args& a, cudaStream_t st) {
+// S <- S M + W from segment to segment, eight rows a CTA, in fp32: a thread has four
+// columns of a row, and the rows of S stand in shared memory.
+template <int KP>
+__global__ void __launch_bounds__(KP * 2) tc_join_kernel(const __grid_constant__ Args a) {
+  __shared__ float s[2][8][KP];
+  const int vb = (a.V + 127) / 128, n = a.B * a.H * vb;
+  const int lane = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x & 7), col = threadIdx.x >> 3;
+  float4* const slots = reinterpret_cast<float4*>(a.slots);
+  const int64_t size = 32 * KP;   // of a slot, in float4
+  float4 x = slots[(int64_t)lane * size + col * 128 + row];
+  for (int seg = 1; seg + 1 < a.segs; ++seg) {
+    float(&now)[8][KP] = s[seg & 1];
+    *reinterpret_cast<float4*>(&now[threadIdx.x & 7][col * 4]) = x;
+    __syncthreads();
+    const float4* m =
+        slots + ((int64_t)n * (a.segs - 1) + (int64_t)(seg - 1) * a.B * a.H + lane / vb) * size +
+        col * 128;
+    float4* const w = slots + ((int64_t)seg * n + lane) * size + col * 128 + row;
+    x = *w;
+#pragma unroll 16
+    for (int k = 0; k < KP; ++k) {
+      const float4 f = m[k];
+      const float y = now[threadIdx.x & 7][k];
+      x.x = fmaf(y, f.x, x.x);
+      x.y = fmaf(y, f.y, x.y);
+      x.z = fmaf(y, f.z, x.z);
+      x.w = fmaf(y, f.w, x.w);
+    }
+    *w = x;
+  }
+}
+
+cudaError_t launch_tc_join(const Args& a, cudaStream_t st) {
+  const dim3 grid((unsigned)(a.B * a.H * ((a.V + 127) / 128)), 16);
+  if (a.KP == 64) tc_join_kernel<64><<<grid, 128, 0, st>>>(a);
+  else tc_join_kernel<128><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tc_forward(const Args& args, cudaStream_t st) {
+  Args a = args;
+  if (a.pass == kParts) {
+    Args f = a;
+    f.S0 = f.X = nullptr;
+    f.final = nullptr;
+    cudaError_t e = a.KP == 64 ? fwd::run<64, false>(f, st) : fwd::run<128, false>(f, st);
+    if (e == cudaSuccess) e = launch_tc_join(f, st);
+    if (e != cudaSuccess) return e;
+    a.pass = kJoined;
+  }
   if (a.KP == 64) return a.S0 ? fwd::run<64, true>(a, st) : fwd::run<64, false>(a, st);
   return a.S0 ? fwd::run<128, true>(a, st) : fwd::run<128, false>(a, st);
 }

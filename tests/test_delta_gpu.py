@@ -329,3 +329,29 @@ def test_more_sequences_than_sms(ssd, V):
         for n in ("dq", "dk", "dv", "dg", "dbeta"):
             assert torch.equal(g[n][0, :, 0], got[n][b, :, h]), n
         assert torch.equal(g["d_initial_states"][0, 0], got["d_initial_states"][b, h])
+
+
+@pytest.mark.parametrize("B,G,H,V,K,docs", [(1, 1, 1, 128, 128, None), (1, 2, 4, 40, 64, None),
+                                            (2, 1, 1, 200, 100, [2000, 1, 2100]),
+                                            (1, 3, 3, 130, 33, None)])
+def test_a_few_long_sequences(ssd, B, G, H, V, K, docs):
+    """Segments of a sequence all at once, joined by their effect on a state."""
+    L = 4101
+    d = du.inputs(B, L, G, H, V, K, BF, seed=70, docs=docs)
+    d["g"] *= 0.02     # memory over many segments
+    ins, kw = split(d)
+    want, fin = du.reference(d)
+    out, final, saved = ssd.delta_scan_fwd(*ins, return_final_states=True, save=True, **kw)
+    du.close(out, want, BF, "out")
+    du.close(final, fin, BF, "final_states")
+    again = ssd.delta_scan_fwd(*ins, return_final_states=True, **kw)
+    assert torch.equal(again[0], out) and torch.equal(again[1], final)
+    # the backward takes what was kept, or runs it again
+    dout = torch.ones_like(out)
+    a = ssd.delta_scan_bwd(dout, *ins, saved=saved, **kw)
+    b = ssd.delta_scan_bwd(dout, *ins, **kw)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    # and is that of the same sequence after its first tokens' pieces
+    o1, s1 = ssd.delta_scan_fwd(*(t[:, :64].contiguous() for t in ins),
+                                initial_states=kw["initial_states"], return_final_states=True)
+    du.close(o1, want[:, :64], BF, "out of a short one")
