@@ -112,18 +112,25 @@ void carve_work(Args& a, F take) {
   a.slots = reinterpret_cast<float*>(take(slots * 128 * a.KP * 4));
 }
 // A few long sequences leave most SMs idle: their segments run all at once, in two
-// passes.  The first has (2 segs - 3) items a sequence of 128 channels, the second
-// segs: with as many as the SMs take in two rounds and in one, both take about
-// nc / segs chunks.  Worth it from four segments of sixteen chunks on.
+// passes, where that takes fewer chunks one after another than the sequence has.  The
+// first pass has 2 segs - 3 items a sequence (of 128 channels), the second segs; eight
+// chunks' time is what joining them and two launches take.
 void split(Args& a) {
-  const int64_t lanes = (int64_t)a.B * a.H * (a.VP / 128);
-  if (!a.tc || a.segs > 1) return;
-  int64_t segs = row::sm_count() / lanes;
-  if (segs > a.nc / 16) segs = a.nc / 16;
-  if (segs < 4) return;
-  a.seg = (int)((a.nc + segs - 1) / segs);
-  a.segs = (a.nc + a.seg - 1) / a.seg;
-  a.pass = kParts;
+  const int64_t lanes = (int64_t)a.B * a.H * (a.VP / 128), heads = (int64_t)a.B * a.H;
+  const int64_t sms = row::sm_count();
+  if (!a.tc || a.segs > 1 || lanes >= sms) return;
+  int64_t best = a.nc;
+  for (int64_t segs = 2; segs <= 64 && segs * 8 <= a.nc; ++segs) {
+    const int64_t seg = (a.nc + segs - 1) / segs, n = (a.nc + seg - 1) / seg;
+    const int64_t first = lanes * (n - 1) + heads * (n - 2), second = lanes * n;
+    const int64_t steps = ((first + sms - 1) / sms + (second + sms - 1) / sms) * seg + 8;
+    if (steps < best) {
+      best = steps;
+      a.seg = (int)seg;
+      a.segs = (int)n;
+      a.pass = kParts;
+    }
+  }
 }
 
 // The forward's pieces of a workspace at `base`, and how many bytes they take.

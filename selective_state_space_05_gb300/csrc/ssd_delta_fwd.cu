@@ -27,10 +27,9 @@ struct FwdSmem {
   static constexpr uint32_t k = 0, q = M::TI * kPlane, t = 2 * M::TI * kPlane,
                             p = t + M::NT * kMat, vec = p + M::NT * kMat, v = vec + kVec;
   static constexpr uint32_t stage(int nw) { return (v + C * vpitch(nw) + 127) / 128 * 128; }
-  static constexpr int kStages = M::TI == 1 ? 2 : 1;
   // a warp's results on their way out: C rows of 16 values
   static constexpr uint32_t opitch = 16 * sizeof(T) + 16;
-  static constexpr uint32_t total(int nw) { return kStages * stage(nw) + nw * C * opitch; }
+  static constexpr uint32_t total(int nw) { return 2 * stage(nw) + nw * C * opitch; }
 };
 
 // One chunk's operands into a stage.
@@ -80,38 +79,33 @@ __device__ __forceinline__ void load_chunk(const Args& a, uint32_t st, int b, in
 }
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(kMaxWarps * 32) forward_kernel(const Args a) {
+__global__ void __launch_bounds__(256) forward_kernel(const Args a) {
   using S = FwdSmem<T, KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, NC = C / 8, NK = KP / 8;
   extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nw = (blockDim.x >> 5) - load_warps<T>();   // those with rows
+  // the loading threads: the warps behind them, or all
+  const int ltid = tid - (load_warps<T>() ? nw * 32 : 0);
+  const int nth = load_warps<T>() ? load_warps<T>() * 32 : blockDim.x;
   const int g = lane >> 2, t = lane & 3;
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
   const int v0 = blockIdx.y * nw * 16, vw = v0 + warp * 16;   // the CTA's, the warp's channels
   const uint32_t base = saddr(smem);
-  unsigned char* const obuf = smem + S::kStages * S::stage(nw) + warp * C * S::opitch;
+  unsigned char* const obuf = smem + 2 * S::stage(nw) + warp * C * S::opitch;
 
   float s[NK][4];
   read_state<KP>(s, a.init ? a.init + (int64_t)bh * a.V * a.K : nullptr, vw, a.V, a.K, lane);
-  if (S::kStages == 2) {
-    load_chunk<T, KP>(a, base, b, h, kg, 0, v0, nw, tid, nth);
-    cp_commit();
-  }
+  if (ltid >= 0) load_chunk<T, KP>(a, base, b, h, kg, 0, v0, nw, ltid, nth);
+  cp_commit();
   for (int c = 0; c < a.nc; ++c) {
-    const uint32_t off = S::kStages == 2 ? (c & 1) * S::stage(nw) : 0;
-    if (S::kStages == 2) {
-      cp_wait<0>();
-      __syncthreads();   // the chunk is there, and all warps are done with the one before
-      if (c + 1 < a.nc)
-        load_chunk<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c + 1, v0, nw, tid, nth);
-      cp_commit();
-    } else {
-      __syncthreads();
-      load_chunk<T, KP>(a, base, b, h, kg, c, v0, nw, tid, nth);
-      cp_commit();
-      cp_wait<0>();
-      __syncthreads();
-    }
+    const uint32_t off = (c & 1) * S::stage(nw);
+    cp_wait<0>();
+    __syncthreads();   // the chunk is there, and all warps are done with the one before
+    if (ltid >= 0 && c + 1 < a.nc)
+      load_chunk<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c + 1, v0, nw, ltid, nth);
+    cp_commit();
+    if (warp >= nw) continue;   // (it only loads)
     if (vw >= a.VP) continue;   // (it only helps to load)
     const uint32_t st = base + off;
     const float* vec = reinterpret_cast<const float*>(smem + off + S::vec);
@@ -125,6 +119,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) forward_kernel(const Args a) {
     zero(o);
 #pragma unroll
     for (int ks = 0; ks < KP / 16; ++ks) {
+      if (ks * 16 >= a.K) break;
       uint32_t f[NT][4];
       a_from<NT>(s[2 * ks], s[2 * ks + 1], f);
 #pragma unroll
@@ -179,6 +174,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) forward_kernel(const Args a) {
     const float through = vec[kVecs * C];
 #pragma unroll
     for (int n = 0; n < NK / 2; ++n) {
+      if (n * 16 >= a.K) break;
       float w[2][4];
       zero(w);
 #pragma unroll
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) forward_kernel(const Args a) {
     }
   }
   cp_wait<0>();
-  if (a.final && vw < a.VP)
+  if (a.final && warp < nw && vw < a.VP)
     write_state<KP>(s, a.final + (int64_t)bh * a.V * a.K, vw, a.V, a.K, lane);
 }
 
@@ -201,13 +197,13 @@ template <typename T, int KP>
 cudaError_t forward(const Args& a, cudaStream_t st) {
   using S = FwdSmem<T, KP>;
   int nw = 0;
-  cudaError_t e = warps_for(a, &nw);
+  cudaError_t e = warps_for<T>(a, &nw);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(forward_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::total(kMaxWarps));
+                             S::total(max_warps<T>()));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.VP / 16 + nw - 1) / nw));
-  forward_kernel<T, KP><<<grid, nw * 32, S::total(nw), st>>>(a);
+  forward_kernel<T, KP><<<grid, (nw + load_warps<T>()) * 32, S::total(nw), st>>>(a);
   return cudaGetLastError();
 }
 

@@ -20,9 +20,8 @@ struct RevSmem {
   static constexpr uint32_t k = 0, q = M::TI * kPlane, t = 2 * M::TI * kPlane,
                             p = t + M::NT * kMat, vec = p + M::NT * kMat, d = vec + kVec;
   static constexpr uint32_t stage(int nw) { return d + nw * M::TI * kOut; }
-  static constexpr int kStages = M::TI == 1 ? 2 : 1;
   static constexpr uint32_t opitch = 16 * sizeof(T) + 16;
-  static constexpr uint32_t total(int nw) { return kStages * stage(nw) + nw * C * opitch; }
+  static constexpr uint32_t total(int nw) { return 2 * stage(nw) + nw * C * opitch; }
 };
 
 template <typename T, int KP>
@@ -52,39 +51,34 @@ __device__ __forceinline__ void load_reverse(const Args& a, uint32_t st, int b, 
 }
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(kMaxWarps * 32) reverse_kernel(const Args a) {
+__global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
   using S = RevSmem<T, KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, NC = C / 8, NK = KP / 8;
   extern __shared__ __align__(128) unsigned char smem[];
-  const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nth >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nw = (blockDim.x >> 5) - load_warps<T>();   // those with rows
+  // the loading threads: the warps behind them, or all
+  const int ltid = tid - (load_warps<T>() ? nw * 32 : 0);
+  const int nth = load_warps<T>() ? load_warps<T>() * 32 : blockDim.x;
   const int t = lane & 3;
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
   const int v0 = blockIdx.y * nw * 16, vw = v0 + warp * 16;
   const uint32_t base = saddr(smem);
-  unsigned char* const obuf = smem + S::kStages * S::stage(nw) + warp * C * S::opitch;
+  unsigned char* const obuf = smem + 2 * S::stage(nw) + warp * C * S::opitch;
 
   float s[NK][4];
   read_state<KP>(s, a.dfinal ? a.dfinal + (int64_t)bh * a.V * a.K : nullptr, vw, a.V, a.K, lane);
-  if (S::kStages == 2) {
-    load_reverse<T, KP>(a, base, b, h, kg, a.nc - 1, v0, nw, tid, nth);
-    cp_commit();
-  }
+  if (ltid >= 0) load_reverse<T, KP>(a, base, b, h, kg, a.nc - 1, v0, nw, ltid, nth);
+  cp_commit();
   for (int n0 = 0; n0 < a.nc; ++n0) {
     const int c = a.nc - 1 - n0;
-    const uint32_t off = S::kStages == 2 ? (n0 & 1) * S::stage(nw) : 0;
-    if (S::kStages == 2) {
-      cp_wait<0>();
-      __syncthreads();   // the chunk is there, and all warps are done with the one before
-      if (c > 0)
-        load_reverse<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c - 1, v0, nw, tid, nth);
-      cp_commit();
-    } else {
-      __syncthreads();
-      load_reverse<T, KP>(a, base, b, h, kg, c, v0, nw, tid, nth);
-      cp_commit();
-      cp_wait<0>();
-      __syncthreads();
-    }
+    const uint32_t off = (n0 & 1) * S::stage(nw);
+    cp_wait<0>();
+    __syncthreads();   // the chunk is there, and all warps are done with the one before
+    if (ltid >= 0 && c > 0)
+      load_reverse<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c - 1, v0, nw, ltid, nth);
+    cp_commit();
+    if (warp >= nw) continue;   // (it only loads)
     if (vw >= a.VP) continue;   // (it only helps to load)
     const uint32_t st = base + off;
     const float* vec = reinterpret_cast<const float*>(smem + off + S::vec);
@@ -97,6 +91,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) reverse_kernel(const Args a) {
     zero(x);
 #pragma unroll
     for (int ks = 0; ks < KP / 16; ++ks) {
+      if (ks * 16 >= a.K) break;
       uint32_t f[NT][4];
       a_from<NT>(s[2 * ks], s[2 * ks + 1], f);
 #pragma unroll
@@ -171,6 +166,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) reverse_kernel(const Args a) {
     const float through = vec[kVecs * C];
 #pragma unroll
     for (int n = 0; n < NK / 2; ++n) {
+      if (n * 16 >= a.K) break;
       float w[2][4];
       zero(w);
 #pragma unroll
@@ -188,7 +184,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) reverse_kernel(const Args a) {
     }
   }
   cp_wait<0>();
-  if (a.dinit && vw < a.VP)
+  if (a.dinit && warp < nw && vw < a.VP)
     write_state<KP>(s, a.dinit + (int64_t)bh * a.V * a.K, vw, a.V, a.K, lane);
 }
 
@@ -196,13 +192,13 @@ template <typename T, int KP>
 cudaError_t reverse(const Args& a, cudaStream_t st) {
   using S = RevSmem<T, KP>;
   int nw = 0;
-  cudaError_t e = warps_for(a, &nw);
+  cudaError_t e = warps_for<T>(a, &nw);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(reverse_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::total(kMaxWarps));
+                             S::total(max_warps<T>()));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.VP / 16 + nw - 1) / nw));
-  reverse_kernel<T, KP><<<grid, nw * 32, S::total(nw), st>>>(a);
+  reverse_kernel<T, KP><<<grid, (nw + load_warps<T>()) * 32, S::total(nw), st>>>(a);
   return cudaGetLastError();
 }
 

@@ -7,7 +7,10 @@
 namespace ssd {
 namespace delta {
 
-constexpr int kMaxWarps = 8;   // of a CTA
+// Warps of a CTA that have rows of the state, and those that only load (fp32: rows
+// have to be split into terms on their way, which takes the former's time otherwise).
+template <typename T> constexpr int max_warps() { return sizeof(T) == 2 ? 8 : 4; }
+template <typename T> constexpr int load_warps() { return sizeof(T) == 2 ? 0 : 4; }
 
 __device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
@@ -118,15 +121,16 @@ __device__ __forceinline__ void write_state(const float (&s)[KP / 8][4], float* 
     }
 }
 
-// Warps of a CTA: eight share a chunk's tiles where the heads alone fill the SMs,
-// fewer (and more CTAs) where they do not.
-inline cudaError_t warps_for(const Args& a, int* warps) {
+// How many have rows: all that a CTA can have share a chunk's tiles where the heads
+// alone fill the SMs, fewer (and more CTAs) where they do not.
+template <typename T>
+cudaError_t warps_for(const Args& a, int* warps) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int slices = a.VP / 16;
-  int nw = slices < kMaxWarps ? slices : kMaxWarps;
+  int nw = slices < max_warps<T>() ? slices : max_warps<T>();
   while (nw > 1 && (int64_t)a.B * a.H * ((slices + nw - 1) / nw) < sms) nw = (nw + 1) / 2;
   *warps = nw;
   return cudaSuccess;

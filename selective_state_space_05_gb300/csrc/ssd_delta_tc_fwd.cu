@@ -511,42 +511,69 @@ int tc_forward_status(int reset, cudaStream_t st, int* bits) {
 }
 
 // S <- S M + W from segment to segment, eight rows a CTA, in fp32: a thread has four
-// columns of a row, and the rows of S stand in shared memory.
+// columns of a row; S's rows and M stand in shared memory, the next M on its way.
 template <int KP>
 __global__ void __launch_bounds__(KP * 2) tc_join_kernel(const __grid_constant__ Args a) {
-  __shared__ float s[2][8][KP];
-  const int vb = (a.V + 127) / 128, n = a.B * a.H * vb;
-  const int lane = blockIdx.x, row = blockIdx.y * 8 + (threadIdx.x & 7), col = threadIdx.x >> 3;
+  extern __shared__ __align__(16) unsigned char raw[];
+  // rows a bank group apart: M [2][KP / 4][KP], S [2][8][KP]
+  constexpr int PM = KP + 1, PS = KP + 4;
+  float4* const m = reinterpret_cast<float4*>(raw);
+  float* const s = reinterpret_cast<float*>(m + 2 * (KP / 4) * PM);
+  const int vb = (a.V + 127) / 128, n = a.B * a.H * vb, tid = threadIdx.x;
+  const int lane = blockIdx.x, r = tid & 7, row = blockIdx.y * 8 + r, col = tid >> 3;
   float4* const slots = reinterpret_cast<float4*>(a.slots);
   const int64_t size = 32 * KP;   // of a slot, in float4
+  auto load = [&](int seg) {
+    const float4* src =
+        slots + ((int64_t)n * (a.segs - 1) + (int64_t)(seg - 1) * a.B * a.H + lane / vb) * size;
+    float4* dst = m + (seg & 1) * (KP / 4) * PM;
+    for (int i = tid; i < KP / 4 * KP; i += KP * 2)   // rows below KP of 128
+      cp16(saddr(dst + i / KP * PM + i % KP), src + i / KP * 128 + i % KP, 16);
+    cp_commit();
+  };
+  load(1);
   float4 x = slots[(int64_t)lane * size + col * 128 + row];
   for (int seg = 1; seg + 1 < a.segs; ++seg) {
-    float(&now)[8][KP] = s[seg & 1];
-    *reinterpret_cast<float4*>(&now[threadIdx.x & 7][col * 4]) = x;
-    __syncthreads();
-    const float4* m =
-        slots + ((int64_t)n * (a.segs - 1) + (int64_t)(seg - 1) * a.B * a.H + lane / vb) * size +
-        col * 128;
+    float* const now = s + (seg & 1) * 8 * PS;
+    *reinterpret_cast<float4*>(now + r * PS + col * 4) = x;
     float4* const w = slots + ((int64_t)seg * n + lane) * size + col * 128 + row;
     x = *w;
-#pragma unroll 16
-    for (int k = 0; k < KP; ++k) {
-      const float4 f = m[k];
-      const float y = now[threadIdx.x & 7][k];
-      x.x = fmaf(y, f.x, x.x);
-      x.y = fmaf(y, f.y, x.y);
-      x.z = fmaf(y, f.z, x.z);
-      x.w = fmaf(y, f.w, x.w);
+    if (seg + 2 < a.segs) load(seg + 1);
+    else cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const float4* const f = m + ((seg & 1) * (KP / 4) + col) * PM;
+#pragma unroll 4
+    for (int k = 0; k < KP; k += 4) {
+      const float4 y4 = *reinterpret_cast<const float4*>(now + r * PS + k);
+      const float y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 g = f[k + e];
+        x.x = fmaf(y[e], g.x, x.x);
+        x.y = fmaf(y[e], g.y, x.y);
+        x.z = fmaf(y[e], g.z, x.z);
+        x.w = fmaf(y[e], g.w, x.w);
+      }
     }
     *w = x;
+    __syncthreads();   // this M's place is the one after the next's
   }
+  cp_wait<0>();
 }
 
-cudaError_t launch_tc_join(const Args& a, cudaStream_t st) {
+template <int KP>
+cudaError_t join(const Args& a, cudaStream_t st) {
+  const int smem = 2 * (KP / 4) * (KP + 1) * 16 + 2 * 8 * (KP + 4) * 4;
+  const cudaError_t e =
+      cudaFuncSetAttribute(tc_join_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.B * a.H * ((a.V + 127) / 128)), 16);
-  if (a.KP == 64) tc_join_kernel<64><<<grid, 128, 0, st>>>(a);
-  else tc_join_kernel<128><<<grid, 256, 0, st>>>(a);
+  tc_join_kernel<KP><<<grid, KP * 2, smem, st>>>(a);
   return cudaGetLastError();
+}
+cudaError_t launch_tc_join(const Args& a, cudaStream_t st) {
+  return a.KP == 64 ? join<64>(a, st) : join<128>(a, st);
 }
 
 cudaError_t launch_tc_forward(const Args& args, cudaStream_t st) {
