@@ -123,7 +123,7 @@ void split(Args& a) {
   for (int64_t segs = 2; segs <= 64 && segs * 8 <= a.nc; ++segs) {
     const int64_t seg = (a.nc + segs - 1) / segs, n = (a.nc + seg - 1) / seg;
     const int64_t first = lanes * (n - 1) + heads * (n - 2), second = lanes * n;
-    const int64_t steps = ((first + sms - 1) / sms + (second + sms - 1) / sms) * seg + 8;
+    const int64_t steps = ((first + sms - 1) / sms + (second + sms - 1) / sms) * (seg + 3) + n + 8;
     if (steps < best) {
       best = steps;
       a.seg = (int)seg;
