@@ -27,7 +27,8 @@ constexpr int kChunk = 8192;                // elements
 constexpr int kBlock = SSD_ADAMW_BLOCK;
 static_assert(kBlock == 32 * kVec, "a warp holds a block");
 constexpr int kSmall = 40, kLarge = 360;    // tensors a launch: 3 KB or 28 KB of parameters
-constexpr int kCtas = 4;                    // an SM
+template <int BITS>
+constexpr int kCtas = BITS == 8 ? 3 : 4;    // an SM
 
 enum { kParamBf16 = 1, kGradBf16 = 2, kMaster = 4 };
 struct Entry {
@@ -81,7 +82,8 @@ __device__ __forceinline__ Factors factors(const Opt& o) {
   f.keep = (float)(1.0 - lr * o.decay);
   f.coef = 1.f;
   if (o.norm) {
-    const float c = __fdiv_rn(o.max_norm, __fadd_rn(*o.norm, 1e-6f));
+    // (a product with the reciprocal: what a tensor under a number is elsewhere)
+    const float c = __fmul_rn(__frcp_rn(__fadd_rn(*o.norm, 1e-6f)), o.max_norm);
     f.coef = c >= 1.f ? 1.f : c;   // a NaN norm gives NaN
   }
   f.key = mix(mix(o.seed) + low);
@@ -190,6 +192,23 @@ __device__ __forceinline__ void chunk32(const Entry& e, int64_t at, int n, const
 }
 
 // ------------------------------------------------------------------ 8 bits
+// Small whole numbers and floats, through the bits of 2^23 + n (conversion
+// instructions run at a quarter of the rate).
+__device__ __forceinline__ float float_of(uint32_t word, int byte) {
+  return __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u + byte)) - 8388608.f;
+}
+// A word of four whole n in [0, 256], 256 as 0.
+__device__ __forceinline__ uint32_t word_of(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c + 8388608.f), __float_as_uint(d + 8388608.f), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+__device__ __forceinline__ float floor_of(float x) {   // of 0 <= x < 2^22
+  return __fadd_rz(x, 8388608.f) - 8388608.f;
+}
+__device__ __forceinline__ float share(uint32_t n) {   // (n + 1/2) 2^-16, n < 2^16
+  return (__uint_as_float(0x4B000000u | n) - 8388607.5f) * 0x1p-16f;
+}
 __device__ __forceinline__ float m_unit(float c) {   // of a code's size
   const float t = __fmul_rn(c, 1.0f / 127.0f);
   return __fmul_rn(t, t);
@@ -198,8 +217,14 @@ __device__ __forceinline__ float v_unit(float c) {
   const float t = __fmul_rn(c, 1.0f / 255.0f), s = __fmul_rn(t, t);
   return __fmul_rn(s, s);
 }
-// The code of x >= 0 below the largest, `big`: the one below it, or the next
-// with the odds that keep its value; u in (0, 1).
+// A signed code's value; `word` has 128 added to each.
+__device__ __forceinline__ float m_of(uint32_t word, int byte) {
+  const float t = __fmul_rn(float_of(word, byte) - 128.f, 1.0f / 127.0f);
+  return __fmul_rn(t, fabsf(t));
+}
+// The code of x >= 0 below the largest: the one below it, or the next with the odds
+// that keep its value, u in (0, 1); x's quotient by the largest, the place of its
+// root among the codes and the odds are each rounded to nearest.
 template <bool SQUARE>
 __device__ __forceinline__ float code_of(float x, float big, float u) {
   constexpr float top = SQUARE ? 127.f : 255.f;
@@ -209,6 +234,31 @@ __device__ __forceinline__ float code_of(float x, float big, float u) {
   const float lo = SQUARE ? m_unit(c) : v_unit(c), hi = SQUARE ? m_unit(c + 1.f) : v_unit(c + 1.f);
   return u < __fdiv_rn(__fsub_rn(r, lo), __fsub_rn(hi, lo)) ? c + 1.f : c;
 }
+// The same without its divisions and roots, u = (2 n + 1) 2^-17 with n < 2^16.  The
+// quotient is Markstein's correction of the product with the largest's rounded
+// reciprocal (largest and quotient well within the normal range).  The odds round to
+// more than u where they are above it by more than half of u's last place, which the
+// sign of n - u d tells.  The approximate root, within 2^-13 of its place among the
+// codes, is on the wrong side of one only where x is next to that code's value; then
+// both sides give the same code but for u next to 0 or 1: `unsure` is above 0.499
+// there (four in a million), and code_of is asked.
+__device__ __forceinline__ float quick_root(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool SQUARE>
+__device__ __forceinline__ float quick_code(float x, float big, float inv, float u, float& unsure) {
+  constexpr float top = SQUARE ? 127.f : 255.f;
+  const float q = x * inv, r = fmaf(fmaf(-q, big, x), inv, q);
+  const float y = fminf((SQUARE ? quick_root(r) : quick_root(quick_root(r))) * top, top);
+  const float c = fminf(floor_of(y), top - 1.f);
+  unsure = fmaxf(unsure, fminf(fabsf(y - c - 0.5f), fabsf(u - 0.5f)));
+  const float lo = SQUARE ? m_unit(c) : v_unit(c), hi = SQUARE ? m_unit(c + 1.f) : v_unit(c + 1.f);
+  const float step = __fsub_rn(hi, lo);
+  const float half = __uint_as_float((__float_as_uint(u) & 0x7F800000u) - (24u << 23));
+  return fmaf(-half, step, fmaf(-u, step, __fsub_rn(r, lo))) > 0.f ? c + 1.f : c;
+}
 // The largest of 256 magnitudes (a NaN is larger than all).
 __device__ __forceinline__ float warp_max(const float (&x)[kVec]) {
   uint32_t b = 0;
@@ -217,32 +267,23 @@ __device__ __forceinline__ float warp_max(const float (&x)[kVec]) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, b));
 }
 
-__device__ __forceinline__ void load_codes(const uint8_t* p, bool wide, int n, uint8_t (&c)[kVec]) {
+__device__ __forceinline__ void load_codes(const uint8_t* p, bool wide, int n, uint2& w) {
   if (wide) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c[j] = (uint8_t)(w.x >> (8 * j));
-      c[j + 4] = (uint8_t)(w.y >> (8 * j));
-    }
+    w = *reinterpret_cast<const uint2*>(p);
   } else {
+    w = make_uint2(0, 0);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) c[j] = j < n ? p[j] : 0;
+    for (int j = 0; j < kVec; ++j)
+      if (j < n) (j < 4 ? w.x : w.y) |= (uint32_t)p[j] << (j % 4 * 8);
   }
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, bool wide, int n, const uint8_t (&c)[kVec]) {
+__device__ __forceinline__ void store_codes(uint8_t* p, bool wide, int n, uint2 w) {
   if (wide) {
-    uint2 w = make_uint2(0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w.x |= (uint32_t)c[j] << (8 * j);
-      w.y |= (uint32_t)c[j + 4] << (8 * j);
-    }
     *reinterpret_cast<uint2*>(p) = w;
   } else {
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-      if (j < n) p[j] = c[j];
+      if (j < n) p[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (j % 4 * 8));
   }
 }
 __device__ __forceinline__ bool on8(const void* p) { return ((uintptr_t)p & 7) == 0; }
@@ -282,41 +323,67 @@ __device__ __forceinline__ void chunk8(const Entry& e, int64_t at, int n, const 
     uint8_t* const vc = static_cast<uint8_t*>(e.v) + i;
     const float ms = e.ms[blk], vs = e.vs[blk];
     float gv[kVec], pv[kVec], mv[kVec], vv[kVec];
-    uint8_t cm[kVec], cv[kVec];
+    uint2 cm, cv;
     const bool full = left == kVec;
     load_some(static_cast<const G*>(e.g) + i, left, gv);
     load_codes(mc, full && on8(mc), left, cm);
     load_codes(vc, full && on8(vc), left, cv);
+    cm.x ^= 0x80808080u;
+    cm.y ^= 0x80808080u;
     if (MASTER) load_some(w, left, pv);
     else load_some(p, left, pv);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const float c = (float)(int8_t)cm[j];
-      mv[j] = __fmul_rn(copysignf(m_unit(c), c), ms);
-      vv[j] = __fmul_rn(v_unit((float)cv[j]), vs);
+      mv[j] = __fmul_rn(m_of(j < 4 ? cm.x : cm.y, j % 4), ms);
+      vv[j] = __fmul_rn(v_unit(float_of(j < 4 ? cv.x : cv.y, j % 4)), vs);
       if (j >= left) mv[j] = vv[j] = 0.f;   // (a scale that is not finite stays out of the rest)
       moments(__fmul_rn(gv[j], f.coef), mv[j], vv[j], o);
       if (j >= left) mv[j] = vv[j] = 0.f;
       pv[j] = update(pv[j], mv[j], vv[j], f, o);
     }
+    if (MASTER) store_some(w, left, pv);
+    store_some(p, left, pv);
     const float mb = warp_max(mv), vb = warp_max(vv);
+    const float mi = __frcp_rn(mb), vi = __frcp_rn(vb);
+    const bool plain = mb > 0x1p-90f && mb < 0x1p90f && vb > 0x1p-90f && vb < 0x1p90f;
+    float unsure = plain ? 0.f : 1.f;
     uint32_t key = mix(f.key + e.num);
     if (i >> 32) key = mix(key + (uint32_t)(i >> 32));
+    float a[kVec], b[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       const uint32_t h = mix(key + (uint32_t)i + j);
-      const float um = ((float)(h >> 16) + 0.5f) * 0x1p-16f,
-                  uv = ((float)(h & 0xFFFFu) + 0.5f) * 0x1p-16f;
-      const float a = code_of<true>(fabsf(mv[j]), mb, um);
-      float b = code_of<false>(vv[j], vb, uv);
-      if (vv[j] > 0.f) b = fmaxf(b, 1.f);
-      cm[j] = (uint8_t)(int8_t)(int)copysignf(a, mv[j]);
-      cv[j] = (uint8_t)(int)b;
+      a[j] = quick_code<true>(fabsf(mv[j]), mb, mi, share(h >> 16), unsure);
+      b[j] = quick_code<false>(vv[j], vb, vi, share(h & 0xFFFFu), unsure);
     }
+    if (unsure > 0.499f) {
+#pragma unroll 1
+      for (int k = 0; k < kVec; ++k) {   // (a loop, and picks, for few registers)
+        float x = mv[0], z = vv[0];
+#pragma unroll
+        for (int j = 1; j < kVec; ++j) {
+          x = j == k ? mv[j] : x;
+          z = j == k ? vv[j] : z;
+        }
+        const uint32_t h = mix(key + (uint32_t)i + k);
+        x = code_of<true>(fabsf(x), mb, share(h >> 16));
+        z = code_of<false>(z, vb, share(h & 0xFFFFu));
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          a[j] = j == k ? x : a[j];
+          b[j] = j == k ? z : b[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      a[j] = mv[j] < 0.f ? 256.f - a[j] : a[j];
+      b[j] = vv[j] > 0.f ? fmaxf(b[j], 1.f) : b[j];
+    }
+    cm = make_uint2(word_of(a[0], a[1], a[2], a[3]), word_of(a[4], a[5], a[6], a[7]));
+    cv = make_uint2(word_of(b[0], b[1], b[2], b[3]), word_of(b[4], b[5], b[6], b[7]));
     store_codes(mc, full && on8(mc), left, cm);
     store_codes(vc, full && on8(vc), left, cv);
-    if (MASTER) store_some(w, left, pv);
-    store_some(p, left, pv);
     if (lane == 0) {
       e.ms[blk] = mb;
       e.vs[blk] = vb;
@@ -332,7 +399,7 @@ __device__ __forceinline__ void chunk(const Entry& e, int64_t at, int n, const F
 }
 
 template <int N, int BITS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas<BITS>)
     step_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Opt o) {
   __shared__ Factors sf;
   if (threadIdx.x == 0) sf = factors(o);
@@ -372,15 +439,16 @@ __global__ void __launch_bounds__(kThreads) values_kernel(const __grid_constant_
       const uint8_t *mc = static_cast<const uint8_t*>(e.m) + i,
                     *vc = static_cast<const uint8_t*>(e.v) + i;
       const float ms = e.ms[i / kBlock], vs = e.vs[i / kBlock];
-      uint8_t cm[kVec], cv[kVec];
+      uint2 cm, cv;
       load_codes(mc, left == kVec && on8(mc), left, cm);
       load_codes(vc, left == kVec && on8(vc), left, cv);
+      cm.x ^= 0x80808080u;
+      cm.y ^= 0x80808080u;
       float mv[kVec], vv[kVec];
 #pragma unroll
       for (int j = 0; j < kVec; ++j) {
-        const float k = (float)(int8_t)cm[j];
-        mv[j] = __fmul_rn(copysignf(m_unit(k), k), ms);
-        vv[j] = __fmul_rn(v_unit((float)cv[j]), vs);
+        mv[j] = __fmul_rn(m_of(j < 4 ? cm.x : cm.y, j % 4), ms);
+        vv[j] = __fmul_rn(v_unit(float_of(j < 4 ? cv.x : cv.y, j % 4)), vs);
       }
       store_some(static_cast<float*>(e.p) + i, left, mv);
       store_some(e.master + i, left, vv);
@@ -408,8 +476,8 @@ int fill(Table<N>& t, int k, int count, const int64_t* n, F entry) {
   }
   return k;
 }
-int grid_of(uint32_t chunks) {
-  return (int)std::min<int64_t>(chunks, (int64_t)row::sm_count() * kCtas);
+int grid_of(uint32_t chunks, int ctas) {
+  return (int)std::min<int64_t>(chunks, (int64_t)row::sm_count() * ctas);
 }
 int launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
@@ -425,8 +493,8 @@ int run_step(const int64_t* n, int count, int bits, const Opt& o, F entry, cudaS
   for (int k = 0; k < count;) {
     k = fill(t, k, count, n, entry);
     if (t.chunks == 0) break;
-    if (bits == 32) step_kernel<N, 32><<<grid_of(t.chunks), kThreads, 0, st>>>(t, o);
-    else step_kernel<N, 8><<<grid_of(t.chunks), kThreads, 0, st>>>(t, o);
+    if (bits == 32) step_kernel<N, 32><<<grid_of(t.chunks, kCtas<32>), kThreads, 0, st>>>(t, o);
+    else step_kernel<N, 8><<<grid_of(t.chunks, kCtas<8>), kThreads, 0, st>>>(t, o);
   }
   return launched("adamw_step");
 }
@@ -436,7 +504,7 @@ int run_values(const int64_t* n, int count, F entry, cudaStream_t st) {
   for (int k = 0; k < count;) {
     k = fill(t, k, count, n, entry);
     if (t.chunks == 0) break;
-    values_kernel<N><<<grid_of(t.chunks), kThreads, 0, st>>>(t);
+    values_kernel<N><<<grid_of(t.chunks, kCtas<32>), kThreads, 0, st>>>(t);
   }
   return launched("adamw_moments");
 }
