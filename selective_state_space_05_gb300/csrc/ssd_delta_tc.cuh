@@ -16,6 +16,9 @@
 namespace ssd {
 namespace delta {
 
+// A role's registers: the roles' sum stays within what the CTA was launched with.
+#define SSD_SETREG(dir, n) asm volatile("setmaxnreg." dir ".sync.aligned.u32 " n ";")
+
 constexpr int kC = 64;              // tokens a chunk
 constexpr uint32_t kTile = kC * 128;   // bytes of 64 rows of 64 columns
 enum { kErrWait = 1, kErrDrain = 4 };   // bits of the status word (ssd_scan_status)

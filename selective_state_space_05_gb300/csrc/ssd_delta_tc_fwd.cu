@@ -30,7 +30,6 @@ constexpr int kChainWarps = 16, kOutWarp = 16, kMmaWarp = 20, kLoadWarp = 21;
 constexpr int kThreads = 24 * 32;   // (warps 22 and 23 fill the last warpgroup)
 // Registers a thread: launched with 80, six warps a quadrant of the SM:
 // 4 x 80 + 104 + 48 = 472 of 480
-#define SSD_SETREG(dir, n) asm volatile("setmaxnreg." dir ".sync.aligned.u32 " n ";")
 constexpr int kTP = 2;   // stages
 // TMEM columns: S's terms (and w's), Y / y, O1, X / x, O2, W
 constexpr uint32_t kAS = 0, kR0 = 128, kO1 = 192, kR1 = 256, kO2 = 320, kW = 384;

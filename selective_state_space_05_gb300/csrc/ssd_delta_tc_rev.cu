@@ -20,7 +20,6 @@ namespace rev {
 constexpr int kChainWarps = 16, kIoWarp = 16, kMmaWarp = 20, kLoadWarp = 21;
 constexpr int kThreads = 24 * 32;   // (warps 22 and 23 fill the last warpgroup)
 // Registers a thread: as the forward's, 4 x 80 + 104 + 48 of 480 a quadrant
-#define SSD_SETREG(dir, n) asm volatile("setmaxnreg." dir ".sync.aligned.u32 " n ";")
 // TMEM columns: dS's terms (and dY's), Z / dx, do P / dY, W, scale e^G do, do
 constexpr uint32_t kAS = 0, kZ = 128, kY = 192, kW = 256, kA1 = 384, kAD = 448;
 
