@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<KP>;
   S& s = *reinterpret_cast<S*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t chunks = (int64_t)a.B * a.H * a.nc;
+  const int chunks = a.B * a.H * a.nc;         // (each has 64 KB and more: an int)
   const int blocks = a.VP / 128;               // of 128 channels
   if (warp == kMmaWarp) tc::tmem_alloc(&s.tmem, 512);
   if (tid == 0) {
@@ -112,26 +112,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto halves = [&](int v) { return a.V - v * 128 > 64 ? 2 : 1; };
 
   if (warp >= kMmaWarp) {
-    SSD_SETREG("dec", "48");
+    SSD_SETREG("dec", "64");
     if (warp == kLoadWarp) {
       auto bulk = [&](void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
         tc::bulk_load(dst, src, bytes, bar);
       };
       auto stop = [&] { return __any_sync(0xffffffffu, s.gave_up) != 0; };
+      auto block_of = [&](const bf16* planes, int id, int v) {
+        return reinterpret_cast<const unsigned char*>(planes) +
+               ((int64_t)id * blocks + v) * sizeof(s.s);
+      };
       // how many of each have been asked for
       int kqs = 0, xs = 0, ps = 0, qs = 0, ss = 0, dss = 0, it = 0, n = 0;
-      for (int64_t id = blockIdx.x; id < chunks && !stop(); id += gridDim.x, ++it) {
-        const int c = (int)(id % a.nc), h = (int)(id / a.nc % a.H), b = (int)(id / a.nc / a.H);
+      for (int id = blockIdx.x; id < chunks && !stop(); id += gridDim.x, ++it) {
+        const int c = id % a.nc, h = id / a.nc % a.H, b = id / a.nc / a.H;
         const int kg = h / (a.H / a.G);
         // a state's planes of block v
         auto state = [&](const bf16* planes, int v, uint64_t* bar) {
           tc::mbar_arrive_expect_tx(bar, sizeof(s.s));
-          bulk(s.s, reinterpret_cast<const unsigned char*>(planes) + (id * blocks + v) * sizeof(s.s),
-               sizeof(s.s), bar);
+          bulk(s.s, block_of(planes, id, v), sizeof(s.s), bar);
         };
         for (int v = 0; v < blocks; ++v, ++n) {
           const int nh = halves(v);
-          const int64_t tile = id * 2 * (a.VP / 64) + v * 2;   // the first term's
+          const int64_t tile = (int64_t)id * 2 * (a.VP / 64) + v * 2;   // the first term's
           const unsigned char* y = reinterpret_cast<const unsigned char*>(a.dY) + tile * kTile;
           const unsigned char* x = reinterpret_cast<const unsigned char*>(a.X) + tile * kTile;
           const int64_t next = (int64_t)(a.VP / 64) * kTile;
@@ -147,8 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               bulk(s.x[i][1], x + next + i * kTile, kTile, &s.x_full);
             }
             state(a.S0, v, &s.s_full);
-            prefetch(reinterpret_cast<const unsigned char*>(a.dS) + (id * blocks + v) * sizeof(s.s),
-                     sizeof(s.s));
+            prefetch(block_of(a.dS, id, v), sizeof(s.s));
           }
           __syncwarp();
           ++xs;
@@ -165,7 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tma_load_4d(s.kq[i][0], &mk, &s.kq_full, i * 64, kg, c * kC, b);
                 tc::tma_load_4d(s.kq[i][1], &mq, &s.kq_full, i * 64, kg, c * kC, b);
               }
-              bulk(s.vec[it & 1], a.vec + id * vec_floats<kC>(), vec_floats<kC>() * 4, &s.kq_full);
+              bulk(s.vec[it & 1], a.vec + (int64_t)id * vec_floats<kC>(), vec_floats<kC>() * 4,
+                   &s.kq_full);
             }
             __syncwarp();
             ++kqs;
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t term = (KP / 8) * 2048 >> 4;   // a state's second term
       auto stop = [&] { return __any_sync(0xffffffffu, s.gave_up) != 0; };
       int it = 0, n = 0;
-      for (int64_t id = blockIdx.x; id < chunks && !stop(); id += gridDim.x, ++it) {
+      for (int id = blockIdx.x; id < chunks && !stop(); id += gridDim.x, ++it) {
         W(&s.kq_full, it & 1);
         if (stop()) break;
         tc::fence_after_sync();
@@ -311,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)qr << 21);
     const int t0 = part * 16;
     int it = 0, n = 0;
-    for (int64_t id = blockIdx.x; id < chunks; id += gridDim.x, ++it, ++n) {
-      const int c = (int)(id % a.nc), h = (int)(id / a.nc % a.H), b = (int)(id / a.nc / a.H);
+    for (int id = blockIdx.x; id < chunks; id += gridDim.x, ++it, ++n) {
+      const int c = id % a.nc, h = id / a.nc % a.H, b = id / a.nc / a.H;
       const int kg = h / (a.H / a.G);
       const int rows = (int)(a.L - (int64_t)c * kC < kC ? a.L - (int64_t)c * kC : kC);
       const float* const vec = s.vec[it & 1];
@@ -404,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             unsigned char* p = s.m[0][reads ? 1 : 0] + tile_at<64>(i, (t0 >> 3) + e);
-            *reinterpret_cast<uint4*>(p) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+            *reinterpret_cast<uint4*>(p) =
+                make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
             *reinterpret_cast<uint4*>(p + 2 * kTile) =
                 make_uint4(r[8 + 4 * e], r[9 + 4 * e], r[10 + 4 * e], r[11 + 4 * e]);
           }
@@ -520,12 +524,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t tok = (int64_t)b * a.L + (int64_t)c * kC + t0;
       if (tma_out) {   // M's memory is dq's and dk's now
         if (live) {
-          unsigned char* base = s.out[0][row >> 6] + (row & 7) * 2;
+          // two lanes' columns side by side, the even lane's of token e, the odd one's of
+          // e + 4 (whose swizzle is in other banks)
+          const bool odd = lane & 1;
+          unsigned char* base = s.out[0][row >> 6] + (row & 6) * 2;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            unsigned char* p = base + tile_at<64>(t0 + e, (row & 63) >> 3);
-            *reinterpret_cast<bf16*>(p) = __float2bfloat16_rn(dq[e]);
-            *reinterpret_cast<bf16*>(p + (KP / 64) * kTile) = __float2bfloat16_rn(dk[e]);
+          for (int i = 0; i < 8; ++i) {
+            const int e = (i & 3) + 2 * (i & 4);
+            const uint32_t w0 = pack2(dq[e], dk[e]), w1 = pack2(dq[e + 4], dk[e + 4]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1);
+            const uint32_t lo = odd ? got : w0, hi = odd ? w1 : got;
+            unsigned char* p = base + tile_at<64>(t0 + e + (odd ? 4 : 0), (row & 63) >> 3);
+            *reinterpret_cast<uint32_t*>(p) = __byte_perm(lo, hi, 0x5410);
+            *reinterpret_cast<uint32_t*>(p + (KP / 64) * kTile) = __byte_perm(lo, hi, 0x7632);
           }
         }
         tc::fence_proxy_async_smem();
@@ -589,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             w1 += z1;
           }
         }
-        const float r1all = __shfl_sync(0xffffffffu, r1, 0), w0all = __shfl_sync(0xffffffffu, w0, 31);
+        const float r1all = __shfl_sync(0xffffffffu, r1, 0);
+        const float w0all = __shfl_sync(0xffffffffu, w0, 31);
         const float from = warp == 1 ? r0 + r1all : r1;
         const float before = (warp == 1 ? w0 : w0all + w1) - mine;
         if (t < rows) {
