@@ -50,7 +50,7 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   a.V = V;
   a.nc = (int)((L + C - 1) / C);
   a.KP = K <= 64 ? 64 : 128;
-  a.tc = dtype == SSD_DTYPE_BF16 && V >= kTcHeaddim;
+  a.tc = dtype == SSD_DTYPE_BF16;
   a.VP = a.tc ? (V + 127) / 128 * 128 : (V + 15) / 16 * 16;
   // Segments only where there are at least as many sequences as SMs: eight or so for
   // each SM's share (a segment costs the state's way through the L2, about the time of a
@@ -229,14 +229,13 @@ int fill_inputs(Args& a, const void* q, ssd_stride_t sq, const void* k, ssd_stri
   return SSD_OK;
 }
 
-template <typename T>
 cudaError_t run_forward(const Args& a, cudaStream_t st) {
   if (a.tc) {
     const cudaError_t e = launch_tc_prepare(a, st);
     return e != cudaSuccess ? e : launch_tc_forward(a, st);
   }
-  const cudaError_t e = launch_prepare<T>(a, st);
-  return e != cudaSuccess ? e : launch_forward<T>(a, st);
+  const cudaError_t e = launch_prepare(a, st);
+  return e != cudaSuccess ? e : launch_forward(a, st);
 }
 
 bool inputs_mapped(const Args& a) {
@@ -450,8 +449,7 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
   a.final = final_states;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = pack_inputs(a, static_cast<char*>(workspace) + kept, st);
-  if (e == cudaSuccess)
-    e = dtype == SSD_DTYPE_BF16 ? run_forward<bf16>(a, st) : run_forward<float>(a, st);
+  if (e == cudaSuccess) e = run_forward(a, st);
   return cuda_bad(e, "delta_scan_fwd launch");
 }
 
@@ -506,7 +504,6 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   a.S0 = f.S0;
   a.X = f.X;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = dtype == SSD_DTYPE_BF16;
   char* const at = static_cast<char*>(workspace) + used;
   cudaError_t e = pack_inputs(a, at, st);
   if (e == cudaSuccess && a.tc && !a.wide_do)
@@ -521,7 +518,7 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
     f.qcols = a.qcols;
     f.kcols = a.kcols;
     f.vcols = a.vcols;
-    e = bf ? run_forward<bf16>(f, st) : run_forward<float>(f, st);
+    e = run_forward(f, st);
   }
   a.dfinal = dfinal_states;
   a.dinit = d_initial_states;
@@ -535,8 +532,8 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
     if (e == cudaSuccess) e = launch_tc_reverse(a, st);
     if (e == cudaSuccess) e = launch_tc_grads(a, st);
   } else {
-    if (e == cudaSuccess) e = bf ? launch_reverse<bf16>(a, st) : launch_reverse<float>(a, st);
-    if (e == cudaSuccess) e = bf ? launch_grads<bf16>(a, st) : launch_grads<float>(a, st);
+    if (e == cudaSuccess) e = launch_reverse(a, st);
+    if (e == cudaSuccess) e = launch_grads(a, st);
   }
   return cuda_bad(e, "delta_scan_bwd launch");
 }

@@ -8,16 +8,22 @@
 //   x = T (v - e^G S0 k),  u = beta x,  out = scale e^G S0 q + P u
 //   S_C = e^(G_C) S0 + sum_j e^(G_C - G_j) u_j k_j^T
 //
-// Products run on mma.sync m16n8k16 with bf16 operands and fp32 sums.  Inputs in
-// bf16 are one term; what is computed in fp32 (the state, x, u, T, P and their
-// gradients) is split into NT bf16 terms, each the rounding of what the ones
-// before leave, and the products a_i b_j with i + j < NT are summed: two terms
-// leave 2^-18 of each factor, three (for fp32 inputs, themselves three terms)
-// about 2^-26.  mma.sync and not tcgen05, because each product's result is the
-// next one's operand: a warp owns 16 of the state's rows, and its accumulators
-// are, register by register, the A operand of the next mma, so that a chunk's
-// chain of five products meets no memory and no other warp.  (mma.sync runs
-// bf16 at 593 TFLOP/s on all SMs, one m16n8k16 per 8 cycles and quadrant.)
+// Products have bf16 operands and fp32 sums.  Inputs in bf16 are one term; what is
+// computed in fp32 (the state, x, u, T, P and their gradients) is split into NT bf16
+// terms, each the rounding of what the ones before leave, and the products a_i b_j
+// with i + j < NT are summed: two terms leave 2^-18 of each factor, which is nothing
+// beside what bf16 inputs and outputs round; three (for fp32 inputs, themselves three
+// terms) about 2^-26.
+//
+// bf16 runs on tcgen05 (ssd_delta_tc*): for 8 x 1024 tokens of 128 heads of 32
+// channels and a dstate of 32 the forward takes 0.59 ms there and 0.95 with mma.sync,
+// forward and backward 1.82 and 2.74, and no size was found where it is the slower one by
+// more than a microsecond.  fp32 runs on mma.sync m16n8k16: six products a pair of
+// factors, whose three terms would not fit TMEM beside the results; a warp owns 16 of
+// the state's rows, and its accumulators are, register by register, the A operand of
+// the next mma, so that a chunk's chain of five products meets no memory and no other
+// warp.  (mma.sync runs bf16 at 593 TFLOP/s on all SMs, one m16n8k16 per 8 cycles and
+// quadrant.)
 #pragma once
 
 #include "ssd_common.cuh"
@@ -30,15 +36,12 @@ using bf16 = __nv_bfloat16;
 // Chunk length and terms: bf16 inputs 64 tokens, two terms; fp32 32 and three
 // (their tiles take three times the shared memory).
 template <typename T> struct Mode;
-template <> struct Mode<bf16> { static constexpr int C = 64, NT = 2, TI = 1; };
+template <> struct Mode<bf16> { static constexpr int C = 64, NT = 2; };
 template <> struct Mode<float> { static constexpr int C = 32, NT = 3, TI = 3; };
 
 // e^g is 0 in fp32 below this: such a token starts the state anew, as one
 // whose seq_idx changes.
 constexpr float kReset = -104.f;
-
-// From this headdim on bf16 runs on tcgen05, whose MMAs have 128 channels.
-constexpr int kTcHeaddim = 33;
 
 // How the tcgen05 forward takes its segments: one after another, each from the
 // state that the one before left; or all at once, which takes two passes.  The first
@@ -55,11 +58,11 @@ template <int C> constexpr int vec_floats() { return kVecs * C + 4; }
 
 struct Args {
   int64_t L;
-  int B, H, G, K, V, nc, KP, VP;   // KP: dstate padded to 64 or 128; VP: headdim to 16
+  int B, H, G, K, V, nc, KP, VP;   // KP: dstate padded to 64 or 128; VP: headdim to 16 or 128
   TokStride sq, sk, sv, sdo;
   int qcols, kcols, vcols, docols;   // dstate and headdim as their rows have them (packed: to 8)
   int wide_q, wide_k, wide_v, wide_do, wide_out, wide_dv;   // rows in 16-byte pieces
-  int tc;       // the tcgen05 kernels and their workspace's layout
+  int tc;       // bf16: the tcgen05 kernels and their workspace's layout
   float scale;
   const void *q, *k, *v, *dout;
   const float *g, *beta;
@@ -216,33 +219,9 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
-// ROWS rows of a tile of W columns: row r is src + r * ld for r < rows, columns
-// below cols; zeros elsewhere.  bf16 as it is (wide: with cp.async), fp32 as
-// three planes, `plane` bytes apart.
-template <int W, int ROWS>
-__device__ __forceinline__ void load_tile(uint32_t dst, uint32_t, const bf16* src, int64_t ld,
-                                          int rows, int cols, int wide, int tid, int nth) {
-  constexpr int U = W / 8;
-  for (int i = tid; i < ROWS * U; i += nth) {
-    const int r = i / U, u = i % U;
-    const uint32_t at = dst + tile_at<W>(r, u);
-    const bf16* p = src + r * ld + u * 8;
-    if (wide) {
-      const bool in = r < rows && u * 8 < cols;   // cols is a multiple of 8
-      cp16(at, in ? p : src, in ? 16 : 0);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = u * 8 + 2 * j;
-        const uint32_t x = r < rows && c < cols ? __bfloat16_as_ushort(p[2 * j]) : 0;
-        const uint32_t y = r < rows && c + 1 < cols ? __bfloat16_as_ushort(p[2 * j + 1]) : 0;
-        w[j] = x | y << 16;
-      }
-      sts16(at, w[0], w[1], w[2], w[3]);
-    }
-  }
-}
+// ROWS rows of a tile of W columns as three planes, `plane` bytes apart: row r is
+// src + r * ld for r < rows, columns below cols; zeros elsewhere (wide: rows lie on
+// 16 bytes).
 template <int W, int ROWS>
 __device__ __forceinline__ void load_tile(uint32_t dst, uint32_t plane, const float* src,
                                           int64_t ld, int rows, int cols, int wide, int tid,
@@ -304,12 +283,12 @@ __device__ __forceinline__ float2 tile_pair(const unsigned char* base, uint32_t 
 }
 
 // ------------------------------------------------------------------ launches
-// (each returns the launch's error; T: the x dtype)
-template <typename T> cudaError_t launch_prepare(const Args& a, cudaStream_t st);
+// (each returns the launch's error; the first four: fp32)
+cudaError_t launch_prepare(const Args& a, cudaStream_t st);
 // out and final may be null; S0 and X are written where they are given
-template <typename T> cudaError_t launch_forward(const Args& a, cudaStream_t st);
-template <typename T> cudaError_t launch_reverse(const Args& a, cudaStream_t st);
-template <typename T> cudaError_t launch_grads(const Args& a, cudaStream_t st);
+cudaError_t launch_forward(const Args& a, cudaStream_t st);
+cudaError_t launch_reverse(const Args& a, cudaStream_t st);
+cudaError_t launch_grads(const Args& a, cudaStream_t st);
 // dq and dk of heads that share them: sums of dq_part and dk_part
 template <typename T> cudaError_t launch_group_sum(const Args& a, cudaStream_t st);
 

@@ -16,37 +16,37 @@
 namespace ssd {
 namespace delta {
 
-template <typename T, int KP>
+template <int KP>
 struct FwdSmem {
-  using M = Mode<T>;
+  using M = Mode<float>;
   static constexpr int C = M::C;
   static constexpr uint32_t kPlane = C * KP * 2;        // of K and Q
   static constexpr uint32_t kMat = C * C * 2;           // of T and P
-  static constexpr uint32_t vpitch(int nw) { return nw * 16 * sizeof(T) + 16; }
+  static constexpr uint32_t vpitch(int nw) { return nw * 16 * sizeof(float) + 16; }
   static constexpr uint32_t kVec = (vec_floats<C>() * 4 + 15) / 16 * 16;
   static constexpr uint32_t k = 0, q = M::TI * kPlane, t = 2 * M::TI * kPlane,
                             p = t + M::NT * kMat, vec = p + M::NT * kMat, v = vec + kVec;
   static constexpr uint32_t stage(int nw) { return (v + C * vpitch(nw) + 127) / 128 * 128; }
   // a warp's results on their way out: C rows of 16 values
-  static constexpr uint32_t opitch = 16 * sizeof(T) + 16;
+  static constexpr uint32_t opitch = 16 * sizeof(float) + 16;
   static constexpr uint32_t total(int nw) { return 2 * stage(nw) + nw * C * opitch; }
 };
 
 // One chunk's operands into a stage.
-template <typename T, int KP>
+template <int KP>
 __device__ __forceinline__ void load_chunk(const Args& a, uint32_t st, int b, int h, int kg, int c,
                                            int v0, int nw, int tid, int nth) {
-  using S = FwdSmem<T, KP>;
+  using S = FwdSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT;
   const int64_t t0 = (int64_t)c * C;
   const int rows = (int)(a.L - t0 < C ? a.L - t0 : C);
   const int64_t id = ((int64_t)b * a.H + h) * a.nc + c;
   load_tile<KP, C>(st + S::k, S::kPlane,
-                   static_cast<const T*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
+                   static_cast<const float*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
                    a.K, a.wide_k, tid, nth);
   if (a.out)
     load_tile<KP, C>(st + S::q, S::kPlane,
-                     static_cast<const T*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t,
+                     static_cast<const float*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t,
                      rows, a.K, a.wide_q, tid, nth);
   load_planes<C, C, NT>(st + S::t, S::kMat, a.T + id * NT * C * C, C, C * C, C, C, tid, nth);
   if (a.out)
@@ -54,19 +54,19 @@ __device__ __forceinline__ void load_chunk(const Args& a, uint32_t st, int b, in
   const float* gv = a.vec + id * vec_floats<C>();
   for (int i = tid; i < vec_floats<C>() / 4; i += nth) cp16(st + S::vec + i * 16, gv + i * 4, 16);
   // v: rows of nw * 16 channels from v0 on
-  const T* src = static_cast<const T*>(a.v) + toff(a.sv, b, t0) + (int64_t)h * a.V + v0;
-  constexpr int E = 16 / sizeof(T);
+  const float* src = static_cast<const float*>(a.v) + toff(a.sv, b, t0) + (int64_t)h * a.V + v0;
+  constexpr int E = 16 / sizeof(float);
   const int cols = a.V - v0 < nw * 16 ? a.V - v0 : nw * 16, units = nw * 16 / E;
   for (int i = tid; i < C * units; i += nth) {
     const int r = i / units, u = i % units;
     const uint32_t at = st + S::v + r * S::vpitch(nw) + u * 16;
-    const T* p = src + r * a.sv.t + u * E;
+    const float* p = src + r * a.sv.t + u * E;
     if (a.wide_v) {
       const bool in = r < rows && u * E < cols;
       cp16(at, in ? p : src, in ? 16 : 0);
     } else {
       union {
-        T e[E];
+        float e[E];
         uint4 w;
       } x;
       x.w = make_uint4(0, 0, 0, 0);
@@ -78,16 +78,16 @@ __device__ __forceinline__ void load_chunk(const Args& a, uint32_t st, int b, in
   }
 }
 
-template <typename T, int KP>
+template <int KP>
 __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
-  using S = FwdSmem<T, KP>;
+  using S = FwdSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, NC = C / 8, NK = KP / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nw = (blockDim.x >> 5) - load_warps<T>();   // those with rows
+  const int nw = (blockDim.x >> 5) - kLoadWarps;   // those with rows
   // the loading threads: the warps behind them, or all
-  const int ltid = tid - (load_warps<T>() ? nw * 32 : 0);
-  const int nth = load_warps<T>() ? load_warps<T>() * 32 : blockDim.x;
+  const int ltid = tid - nw * 32;
+  constexpr int nth = kLoadWarps * 32;
   const int g = lane >> 2, t = lane & 3;
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
   const int v0 = blockIdx.y * nw * 16, vw = v0 + warp * 16;   // the CTA's, the warp's channels
@@ -96,14 +96,14 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
 
   float s[NK][4];
   read_state<KP>(s, a.init ? a.init + (int64_t)bh * a.V * a.K : nullptr, vw, a.V, a.K, lane);
-  if (ltid >= 0) load_chunk<T, KP>(a, base, b, h, kg, 0, v0, nw, ltid, nth);
+  if (ltid >= 0) load_chunk<KP>(a, base, b, h, kg, 0, v0, nw, ltid, nth);
   cp_commit();
   for (int c = 0; c < a.nc; ++c) {
     const uint32_t off = (c & 1) * S::stage(nw);
     cp_wait<0>();
     __syncthreads();   // the chunk is there, and all warps are done with the one before
     if (ltid >= 0 && c + 1 < a.nc)
-      load_chunk<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c + 1, v0, nw, ltid, nth);
+      load_chunk<KP>(a, base + (S::stage(nw) - off), b, h, kg, c + 1, v0, nw, ltid, nth);
     cp_commit();
     if (warp >= nw) continue;   // (it only loads)
     if (vw >= a.VP) continue;   // (it only helps to load)
@@ -131,15 +131,15 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
                                   blockn_at<KP>(st + S::q, n * 16, ks * 16, lane), S::kPlane);
       }
     }
-    const unsigned char* vt = smem + off + S::v + (warp * 16 + g) * sizeof(T);
+    const unsigned char* vt = smem + off + S::v + (warp * 16 + g) * sizeof(float);
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int i = n * 8 + t * 2;
       const float2 gam = ld2(vec + kGam * C + i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float v = to_f(*reinterpret_cast<const T*>(vt + (i + (e & 1)) * S::vpitch(nw) +
-                                                         8 * (e >> 1) * sizeof(T)));
+        const float v = to_f(*reinterpret_cast<const float*>(vt + (i + (e & 1)) * S::vpitch(nw) +
+                                                         8 * (e >> 1) * sizeof(float)));
         const float ge = e & 1 ? gam.y : gam.x;
         y[n][e] = fmaf(-ge, y[n][e], v);
         o[n][e] *= a.scale * ge;
@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
     }
     if (a.out) {
       mma_lower<C, NT>(o, x, st + S::p, lane);
-      store_rows<T, C>(o, obuf, S::opitch,
-                       static_cast<T*>(a.out) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vw,
+      store_rows<float, C>(o, obuf, S::opitch,
+                       static_cast<float*>(a.out) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vw,
                        (int64_t)a.H * a.V, rows, a.V - vw, a.wide_out, lane);
     }
 #pragma unroll
@@ -193,26 +193,23 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
     write_state<KP>(s, a.final + (int64_t)bh * a.V * a.K, vw, a.V, a.K, lane);
 }
 
-template <typename T, int KP>
+template <int KP>
 cudaError_t forward(const Args& a, cudaStream_t st) {
-  using S = FwdSmem<T, KP>;
+  using S = FwdSmem<KP>;
   int nw = 0;
-  cudaError_t e = warps_for<T>(a, &nw);
+  cudaError_t e = warps_for(a, &nw);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(forward_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::total(max_warps<T>()));
+    e = cudaFuncSetAttribute(forward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::total(kRowWarps));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.VP / 16 + nw - 1) / nw));
-  forward_kernel<T, KP><<<grid, (nw + load_warps<T>()) * 32, S::total(nw), st>>>(a);
+  forward_kernel<KP><<<grid, (nw + kLoadWarps) * 32, S::total(nw), st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t launch_forward(const Args& a, cudaStream_t st) {
-  return a.KP == 64 ? forward<T, 64>(a, st) : forward<T, 128>(a, st);
+  return a.KP == 64 ? forward<64>(a, st) : forward<128>(a, st);
 }
-template cudaError_t launch_forward<bf16>(const Args&, cudaStream_t);
-template cudaError_t launch_forward<float>(const Args&, cudaStream_t);
 
 }  // namespace delta
 }  // namespace ssd

@@ -21,9 +21,9 @@ namespace delta {
 
 constexpr int kGradThreads = 256, kVT = 32;   // kVT: channels a tile
 
-template <typename T, int KP>
+template <int KP>
 struct GradSmem {
-  using M = Mode<T>;
+  using M = Mode<float>;
   static constexpr int C = M::C, RG = C / 16, CG = 8 / RG;   // row and column groups of warps
   static constexpr uint32_t kPlane = C * KP * 2;             // K, Q
   static constexpr uint32_t kTok = C * kVT * 2;              // dout, x, dy
@@ -41,14 +41,14 @@ struct GradSmem {
   static constexpr uint32_t total = st + 2 * stage > end ? st + 2 * stage : end;
 };
 
-template <typename T, int KP>
+template <int KP>
 __device__ __forceinline__ void load_channels(const Args& a, uint32_t st, int b, int h, int64_t id,
                                               int64_t t0, int rows, int v0, int tid) {
-  using S = GradSmem<T, KP>;
+  using S = GradSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT;
   const int cols = a.V - v0 < kVT ? a.V - v0 : kVT, pad = a.VP - v0 < kVT ? a.VP - v0 : kVT;
   load_tile<kVT, C>(st + S::d, S::kTok,
-                    static_cast<const T*>(a.dout) + toff(a.sdo, b, t0) + (int64_t)h * a.V + v0,
+                    static_cast<const float*>(a.dout) + toff(a.sdo, b, t0) + (int64_t)h * a.V + v0,
                     a.sdo.t, rows, cols, a.wide_do, tid, kGradThreads);
   load_planes<kVT, C, NT>(st + S::x, S::kTok, a.X + id * NT * C * a.VP + v0, a.VP,
                           (int64_t)C * a.VP, C, pad, tid, kGradThreads);
@@ -61,20 +61,18 @@ __device__ __forceinline__ void load_channels(const Args& a, uint32_t st, int b,
 }
 
 // A row's pair of columns in a result of `cols` columns.
-template <typename T>
-__device__ __forceinline__ void put2(T* row, int c, int cols, bool pairs, float x, float y) {
+__device__ __forceinline__ void put2(float* row, int c, int cols, bool pairs, float x, float y) {
   if (pairs && c + 1 < cols) {
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(row + c) = pack2(x, y);
-    else *reinterpret_cast<float2*>(row + c) = make_float2(x, y);
+    *reinterpret_cast<float2*>(row + c) = make_float2(x, y);
   } else {
-    if (c < cols) row[c] = from_f<T>(x);
-    if (c + 1 < cols) row[c + 1] = from_f<T>(y);
+    if (c < cols) row[c] = x;
+    if (c + 1 < cols) row[c + 1] = y;
   }
 }
 
-template <typename T, int KP>
+template <int KP>
 __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
-  using S = GradSmem<T, KP>;
+  using S = GradSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, RG = S::RG, CG = S::CG;
   constexpr int NW = KP / CG / 16;                     // 16-column blocks of a warp's results
   constexpr int PB = RG / CG > 0 ? RG / CG : 1;        // 16-column blocks of its pair matrices
@@ -94,14 +92,14 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   float* const part = acc + C;
 
   load_tile<KP, C>(base + S::k, S::kPlane,
-                   static_cast<const T*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
+                   static_cast<const float*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
                    a.K, a.wide_k, tid, kGradThreads);
   load_tile<KP, C>(base + S::q, S::kPlane,
-                   static_cast<const T*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
+                   static_cast<const float*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
                    a.K, a.wide_q, tid, kGradThreads);
   for (int i = tid; i < vec_floats<C>() / 4; i += kGradThreads)
     cp16(base + S::vec + i * 16, a.vec + id * vec_floats<C>() + i * 4, 16);
-  load_channels<T, KP>(a, base + S::st, b, h, id, t0, rows, 0, tid);
+  load_channels<KP>(a, base + S::st, b, h, id, t0, rows, 0, tid);
   cp_commit();
 
   float dq[2 * NW][4], dk[2 * NW][4], w0[2 * NW][4], dp[2 * PB][4], da[2 * PB][4];
@@ -117,7 +115,7 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
     cp_wait<0>();
     __syncthreads();
     if (v + 1 < tiles)
-      load_channels<T, KP>(a, base + S::st + ((v + 1) & 1) * S::stage, b, h, id, t0, rows,
+      load_channels<KP>(a, base + S::st + ((v + 1) & 1) * S::stage, b, h, id, t0, rows,
                            (v + 1) * kVT, tid);
     cp_commit();
 #pragma unroll
@@ -295,8 +293,8 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
         put2(a.dk_part + row, col, a.K, pairs, dk[n][2 * r], dk[n][2 * r + 1]);
       } else {
         const int64_t row = (tok * a.G + kg) * a.K;
-        put2(static_cast<T*>(a.dq) + row, col, a.K, pairs, dq[n][2 * r], dq[n][2 * r + 1]);
-        put2(static_cast<T*>(a.dk) + row, col, a.K, pairs, dk[n][2 * r], dk[n][2 * r + 1]);
+        put2(static_cast<float*>(a.dq) + row, col, a.K, pairs, dq[n][2 * r], dq[n][2 * r + 1]);
+        put2(static_cast<float*>(a.dk) + row, col, a.K, pairs, dk[n][2 * r], dk[n][2 * r + 1]);
       }
     }
   }
@@ -362,24 +360,21 @@ cudaError_t launch_group_sum(const Args& a, cudaStream_t st) {
 template cudaError_t launch_group_sum<bf16>(const Args&, cudaStream_t);
 template cudaError_t launch_group_sum<float>(const Args&, cudaStream_t);
 
-template <typename T, int KP>
+template <int KP>
 cudaError_t grads(const Args& a, cudaStream_t st) {
-  using S = GradSmem<T, KP>;
-  cudaError_t e = cudaFuncSetAttribute(grads_kernel<T, KP>,
+  using S = GradSmem<KP>;
+  cudaError_t e = cudaFuncSetAttribute(grads_kernel<KP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::total);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.B * a.H * a.nc;
-  grads_kernel<T, KP><<<(unsigned)n, kGradThreads, S::total, st>>>(a);
-  if (a.dq_part) return launch_group_sum<T>(a, st);
+  grads_kernel<KP><<<(unsigned)n, kGradThreads, S::total, st>>>(a);
+  if (a.dq_part) return launch_group_sum<float>(a, st);
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t launch_grads(const Args& a, cudaStream_t st) {
-  return a.KP == 64 ? grads<T, 64>(a, st) : grads<T, 128>(a, st);
+  return a.KP == 64 ? grads<64>(a, st) : grads<128>(a, st);
 }
-template cudaError_t launch_grads<bf16>(const Args&, cudaStream_t);
-template cudaError_t launch_grads<float>(const Args&, cudaStream_t);
 
 }  // namespace delta
 }  // namespace ssd

@@ -42,9 +42,9 @@ __device__ __forceinline__ void block_product(float* dst, const float* a, const 
   }
 }
 
-template <typename T, int KP>
+template <int KP>
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
-  using M = Mode<T>;
+  using M = Mode<float>;
   constexpr int C = M::C, NT = M::NT, TI = M::TI;
   constexpr int LD = C + 2;                    // of the fp32 matrices
   constexpr uint32_t kPlane = C * KP * 2;
@@ -63,10 +63,10 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
   const int64_t t0 = (int64_t)c * C;
   const int rows = (int)(a.L - t0 < C ? a.L - t0 : C);
   load_tile<KP, C>(saddr(tk), kPlane,
-                   static_cast<const T*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
+                   static_cast<const float*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
                    a.K, a.wide_k, tid, kPrepThreads);
   load_tile<KP, C>(saddr(tq), kPlane,
-                   static_cast<const T*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
+                   static_cast<const float*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
                    a.K, a.wide_q, tid, kPrepThreads);
   cp_commit();
   if (warp == 0) {   // the vectors: C / 32 neighbouring tokens a lane
@@ -234,26 +234,23 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
   }
 }
 
-template <typename T, int KP>
+template <int KP>
 cudaError_t prepare(const Args& a, cudaStream_t st) {
-  using M = Mode<T>;
+  using M = Mode<float>;
   constexpr int C = M::C;
   const int tiles = 2 * M::TI * C * KP * 2, mats = 3 * C * (C + 2) * 4;
   const int smem = (vec_floats<C>() * 4 + 127) / 128 * 128 + (tiles > mats ? tiles : mats);
-  cudaError_t e = cudaFuncSetAttribute(prepare_kernel<T, KP>,
+  cudaError_t e = cudaFuncSetAttribute(prepare_kernel<KP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t n = (int64_t)a.B * a.H * a.nc;
-  prepare_kernel<T, KP><<<(unsigned)n, kPrepThreads, smem, st>>>(a);
+  prepare_kernel<KP><<<(unsigned)n, kPrepThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t launch_prepare(const Args& a, cudaStream_t st) {
-  return a.KP == 64 ? prepare<T, 64>(a, st) : prepare<T, 128>(a, st);
+  return a.KP == 64 ? prepare<64>(a, st) : prepare<128>(a, st);
 }
-template cudaError_t launch_prepare<bf16>(const Args&, cudaStream_t);
-template cudaError_t launch_prepare<float>(const Args&, cudaStream_t);
 
 }  // namespace delta
 }  // namespace ssd

@@ -9,9 +9,9 @@
 namespace ssd {
 namespace delta {
 
-template <typename T, int KP>
+template <int KP>
 struct RevSmem {
-  using M = Mode<T>;
+  using M = Mode<float>;
   static constexpr int C = M::C;
   static constexpr uint32_t kPlane = C * KP * 2;
   static constexpr uint32_t kMat = C * C * 2;
@@ -20,29 +20,29 @@ struct RevSmem {
   static constexpr uint32_t k = 0, q = M::TI * kPlane, t = 2 * M::TI * kPlane,
                             p = t + M::NT * kMat, vec = p + M::NT * kMat, d = vec + kVec;
   static constexpr uint32_t stage(int nw) { return d + nw * M::TI * kOut; }
-  static constexpr uint32_t opitch = 16 * sizeof(T) + 16;
+  static constexpr uint32_t opitch = 16 * sizeof(float) + 16;
   static constexpr uint32_t total(int nw) { return 2 * stage(nw) + nw * C * opitch; }
 };
 
-template <typename T, int KP>
+template <int KP>
 __device__ __forceinline__ void load_reverse(const Args& a, uint32_t st, int b, int h, int kg,
                                              int c, int v0, int nw, int tid, int nth) {
-  using S = RevSmem<T, KP>;
+  using S = RevSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT;
   const int64_t t0 = (int64_t)c * C;
   const int rows = (int)(a.L - t0 < C ? a.L - t0 : C);
   const int64_t id = ((int64_t)b * a.H + h) * a.nc + c;
   load_tile<KP, C>(st + S::k, S::kPlane,
-                   static_cast<const T*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
+                   static_cast<const float*>(a.k) + toff(a.sk, b, t0) + (int64_t)kg * a.K, a.sk.t, rows,
                    a.K, a.wide_k, tid, nth);
   load_tile<KP, C>(st + S::q, S::kPlane,
-                   static_cast<const T*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
+                   static_cast<const float*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
                    a.K, a.wide_q, tid, nth);
   load_planes<C, C, NT>(st + S::t, S::kMat, a.T + id * NT * C * C, C, C * C, C, C, tid, nth);
   load_planes<C, C, NT>(st + S::p, S::kMat, a.P + id * NT * C * C, C, C * C, C, C, tid, nth);
   const float* gv = a.vec + id * vec_floats<C>();
   for (int i = tid; i < vec_floats<C>() / 4; i += nth) cp16(st + S::vec + i * 16, gv + i * 4, 16);
-  const T* src = static_cast<const T*>(a.dout) + toff(a.sdo, b, t0) + (int64_t)h * a.V;
+  const float* src = static_cast<const float*>(a.dout) + toff(a.sdo, b, t0) + (int64_t)h * a.V;
   for (int w = 0; w < nw; ++w) {
     const int v = v0 + w * 16, cols = a.V - v < 16 ? a.V - v : 16;
     load_tile<16, C>(st + S::d + w * S::M::TI * S::kOut, S::kOut, src + (cols > 0 ? v : 0), a.sdo.t,
@@ -50,16 +50,16 @@ __device__ __forceinline__ void load_reverse(const Args& a, uint32_t st, int b, 
   }
 }
 
-template <typename T, int KP>
+template <int KP>
 __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
-  using S = RevSmem<T, KP>;
+  using S = RevSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, NC = C / 8, NK = KP / 8;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nw = (blockDim.x >> 5) - load_warps<T>();   // those with rows
+  const int nw = (blockDim.x >> 5) - kLoadWarps;   // those with rows
   // the loading threads: the warps behind them, or all
-  const int ltid = tid - (load_warps<T>() ? nw * 32 : 0);
-  const int nth = load_warps<T>() ? load_warps<T>() * 32 : blockDim.x;
+  const int ltid = tid - nw * 32;
+  constexpr int nth = kLoadWarps * 32;
   const int t = lane & 3;
   const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, kg = h / (a.H / a.G);
   const int v0 = blockIdx.y * nw * 16, vw = v0 + warp * 16;
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
 
   float s[NK][4];
   read_state<KP>(s, a.dfinal ? a.dfinal + (int64_t)bh * a.V * a.K : nullptr, vw, a.V, a.K, lane);
-  if (ltid >= 0) load_reverse<T, KP>(a, base, b, h, kg, a.nc - 1, v0, nw, ltid, nth);
+  if (ltid >= 0) load_reverse<KP>(a, base, b, h, kg, a.nc - 1, v0, nw, ltid, nth);
   cp_commit();
   for (int n0 = 0; n0 < a.nc; ++n0) {
     const int c = a.nc - 1 - n0;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
     cp_wait<0>();
     __syncthreads();   // the chunk is there, and all warps are done with the one before
     if (ltid >= 0 && c > 0)
-      load_reverse<T, KP>(a, base + (S::stage(nw) - off), b, h, kg, c - 1, v0, nw, ltid, nth);
+      load_reverse<KP>(a, base + (S::stage(nw) - off), b, h, kg, c - 1, v0, nw, ltid, nth);
     cp_commit();
     if (warp >= nw) continue;   // (it only loads)
     if (vw >= a.VP) continue;   // (it only helps to load)
@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
     }
     store_terms<C, NT>(y, obuf, S::opitch, a.dY + id * NT * C * a.VP + vw, a.VP, (int64_t)C * a.VP,
                        lane);
-    store_rows<T, C>(y, obuf, S::opitch,
-                     static_cast<T*>(a.dv) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vw,
+    store_rows<float, C>(y, obuf, S::opitch,
+                     static_cast<float*>(a.dv) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vw,
                      (int64_t)a.H * a.V, rows, a.V - vw, a.wide_dv, lane);
     uint32_t fq[C / 16][NT][4], fk[C / 16][NT][4];
 #pragma unroll
@@ -188,26 +188,23 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
     write_state<KP>(s, a.dinit + (int64_t)bh * a.V * a.K, vw, a.V, a.K, lane);
 }
 
-template <typename T, int KP>
+template <int KP>
 cudaError_t reverse(const Args& a, cudaStream_t st) {
-  using S = RevSmem<T, KP>;
+  using S = RevSmem<KP>;
   int nw = 0;
-  cudaError_t e = warps_for<T>(a, &nw);
+  cudaError_t e = warps_for(a, &nw);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(reverse_kernel<T, KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::total(max_warps<T>()));
+    e = cudaFuncSetAttribute(reverse_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::total(kRowWarps));
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.VP / 16 + nw - 1) / nw));
-  reverse_kernel<T, KP><<<grid, (nw + load_warps<T>()) * 32, S::total(nw), st>>>(a);
+  reverse_kernel<KP><<<grid, (nw + kLoadWarps) * 32, S::total(nw), st>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t launch_reverse(const Args& a, cudaStream_t st) {
-  return a.KP == 64 ? reverse<T, 64>(a, st) : reverse<T, 128>(a, st);
+  return a.KP == 64 ? reverse<64>(a, st) : reverse<128>(a, st);
 }
-template cudaError_t launch_reverse<bf16>(const Args&, cudaStream_t);
-template cudaError_t launch_reverse<float>(const Args&, cudaStream_t);
 
 }  // namespace delta
 }  // namespace ssd

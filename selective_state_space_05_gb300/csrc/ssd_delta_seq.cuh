@@ -7,10 +7,9 @@
 namespace ssd {
 namespace delta {
 
-// Warps of a CTA that have rows of the state, and those that only load (fp32: rows
-// have to be split into terms on their way, which takes the former's time otherwise).
-template <typename T> constexpr int max_warps() { return sizeof(T) == 2 ? 8 : 4; }
-template <typename T> constexpr int load_warps() { return sizeof(T) == 2 ? 0 : 4; }
+// Warps of a CTA that have rows of the state (at most), and those that only load: rows
+// have to be split into terms on their way, which took the former's time otherwise.
+constexpr int kRowWarps = 4, kLoadWarps = 4;
 
 __device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
@@ -123,14 +122,13 @@ __device__ __forceinline__ void write_state(const float (&s)[KP / 8][4], float* 
 
 // How many have rows: all that a CTA can have share a chunk's tiles where the heads
 // alone fill the SMs, fewer (and more CTAs) where they do not.
-template <typename T>
-cudaError_t warps_for(const Args& a, int* warps) {
+inline cudaError_t warps_for(const Args& a, int* warps) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int slices = a.VP / 16;
-  int nw = slices < max_warps<T>() ? slices : max_warps<T>();
+  int nw = slices < kRowWarps ? slices : kRowWarps;
   while (nw > 1 && (int64_t)a.B * a.H * ((slices + nw - 1) / nw) < sms) nw = (nw + 1) / 2;
   *warps = nw;
   return cudaSuccess;
