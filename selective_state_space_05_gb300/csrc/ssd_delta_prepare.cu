@@ -1,5 +1,5 @@
-// The gated delta rule's first launch: what each chunk needs of its keys, queries
-// and gates and not of a state, for all chunks at once.
+// The gated delta rule's first launch in fp32: what each chunk needs of its keys,
+// queries and gates and not of a state, for all chunks at once.
 //
 // One CTA of four warps per (chunk, head, batch row):
 //   - G, the running sum of g in 64 bits, kept as two floats, so that the decays
@@ -8,7 +8,9 @@
 //   - T = (I + N diag(beta))^-1 in fp32: the 16 x 16 blocks of the diagonal by
 //     substitution, a column a lane, then the blocks below them as
 //     -T_ii A_ij T_jj, doubling the side twice.
-// T and P are written as bf16 terms, the vectors as fp32.
+// T and P are written as bf16 terms, the vectors as fp32.  Bound by the latency of
+// the substitution and of the block products in one CTA, of which four or so share an
+// SM: 600 chunks of 72 columns in 14.6 us, a twenty-fifth of the call.
 #include <math.h>
 
 #include "ssd_delta.cuh"

@@ -1,17 +1,22 @@
 // The gated delta rule's backward within each chunk on tcgen05 (its formulas:
-// ssd_delta_grads.cu), one CTA per (chunk, head, batch row).  With the state S0
-// before the chunk, dS after it, x and dY as terms (hi, lo) and dout:
+// ssd_delta_grads.cu), one CTA per SM, a chunk of a (head, batch row) after another.
+// With the state S0 before the chunk, dS after it, x and dY as terms (hi, lo) and dout:
 //   D5 = [K; Q] K^T                                lanes: rows of K, of Q
-//   D3 = [dYhi; do] [Xhi; Xlo]^T + [dYlo; 0] Xhi^T  lanes: rows of dY, of do
-//   from both, a row a thread:  M2 = -D da beta, M1 = scale D dp beta as terms, and H
-//   D1 = S0^T [dYhi | do | dYlo],  D2 = dS^T [Xhi | Xlo]   lanes: dstate
+//   D3 = [dYhi; do] [Xhi; Xlo]^T,  D3lo = dYlo Xhi^T  lanes: rows of dY, of do
+//   from them, a row a thread:  M2 = -D da beta, M1 = scale D dp beta as terms, and H
+//   D1 = S0^T [dY | do],  D2 = dS^T [Xhi | Xlo]    lanes: dstate
 //   D4 = K^T [M2; M1]^T,  its first half += Q^T M1 + K^T M2
 //   dq = scale e^G D1[do] + D4[1],  dk = -e^G D1[dY] + beta e^(G_C - G) D2 + D4[0]
 // A tile serves in the order in which it is needed: K and Q by tokens and by
 // dstate, M by rows and by columns; the terms of B's rows stand side by side in N, so
-// that an MMA has 128 columns.  Bound by HBM: S0, dS, x and dY (192 KB a chunk and
-// head) come once, K, Q and dout too.  dS takes S0's place in shared memory as soon
-// as D1 is done; sums over dstate run over the lanes with shuffles.
+// that an MMA has 128 columns.  S0, dS, x and dY (192 KB a chunk and head) come once,
+// K, Q and dout too: dS takes S0's place in shared memory as soon as D1 is done and
+// the warps have S0 in registers for <S0, dS>; every buffer's next load starts as soon
+// as it is free.  Sums over dstate run over the lanes with shuffles.
+// Bound by the sixteen warps' own work, phase after phase (7000 instructions a chunk
+// and quadrant, one every 2.8 cycles): 10240 chunks in 682 us, 4.1 TB/s.  (A CTA a
+// chunk, with S0 read again: 752 us.)  The idle MMA and copy time beside them would take
+// a second chunk's buffers, which shared memory (209 KB) has no room for.
 #include "ssd_delta_tc.cuh"
 #include "ssd_row.cuh"
 
@@ -524,19 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t tok = (int64_t)b * a.L + (int64_t)c * kC + t0;
       if (tma_out) {   // M's memory is dq's and dk's now
         if (live) {
-          // two lanes' columns side by side, the even lane's of token e, the odd one's of
-          // e + 4 (whose swizzle is in other banks)
-          const bool odd = lane & 1;
-          unsigned char* base = s.out[0][row >> 6] + (row & 6) * 2;
+          unsigned char* base = s.out[0][row >> 6] + (row & 7) * 2;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = (i & 3) + 2 * (i & 4);
-            const uint32_t w0 = pack2(dq[e], dk[e]), w1 = pack2(dq[e + 4], dk[e + 4]);
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w0 : w1, 1);
-            const uint32_t lo = odd ? got : w0, hi = odd ? w1 : got;
-            unsigned char* p = base + tile_at<64>(t0 + e + (odd ? 4 : 0), (row & 63) >> 3);
-            *reinterpret_cast<uint32_t*>(p) = __byte_perm(lo, hi, 0x5410);
-            *reinterpret_cast<uint32_t*>(p + (KP / 64) * kTile) = __byte_perm(lo, hi, 0x7632);
+          for (int e = 0; e < 16; ++e) {
+            unsigned char* p = base + tile_at<64>(t0 + e, (row & 63) >> 3);
+            *reinterpret_cast<bf16*>(p) = __float2bfloat16_rn(dq[e]);
+            *reinterpret_cast<bf16*>(p + (KP / 64) * kTile) = __float2bfloat16_rn(dk[e]);
           }
         }
         tc::fence_proxy_async_smem();
