@@ -72,6 +72,23 @@ __device__ __forceinline__ void put2(float* row, int c, int cols, bool pairs, fl
   }
 }
 
+// mma_pair from zero, added with one rounding to nearest: the tensor cores' sums truncate,
+// and a gradient is a sum of up to a dozen steps of products (dk was off by 1.1e-6
+// of its norm without that).
+template <int NA, int NB, bool TR>
+__device__ __forceinline__ void mma_apart(float (&d0)[4], float (&d1)[4],
+                                          const uint32_t (&a)[NA][4], uint32_t addr,
+                                          uint32_t plane) {
+  float x[2][4];
+  zero(x);
+  mma_pair<NA, NB, TR>(x[0], x[1], a, addr, plane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    d0[i] += x[0][i];
+    d1[i] += x[1][i];
+  }
+}
+
 template <int KP>
 __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   using S = GradSmem<KP>;
@@ -118,7 +135,7 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
     __syncthreads();
     if (v + 1 < tiles)
       load_channels<KP>(a, base + S::st + ((v + 1) & 1) * S::stage, b, h, id, t0, rows,
-                           (v + 1) * kVT, tid);
+                        (v + 1) * kVT, tid);
     cp_commit();
 #pragma unroll
     for (int ks = 0; ks < kVT / 16; ++ks) {
@@ -135,17 +152,17 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
       for (int n = 0; n < NW; ++n) {
         const int col = (cg * NW + n) * 16;
         const uint32_t s0 = block_at<KP>(st + S::s0, ks * 16, col, lane);
-        mma_pair<TI, NT, true>(dq[2 * n], dq[2 * n + 1], fd, s0, S::kState);
-        mma_pair<NT, NT, true>(dk[2 * n], dk[2 * n + 1], fy, s0, S::kState);
-        mma_pair<NT, NT, true>(w0[2 * n], w0[2 * n + 1], fx,
+        mma_apart<TI, NT, true>(dq[2 * n], dq[2 * n + 1], fd, s0, S::kState);
+        mma_apart<NT, NT, true>(dk[2 * n], dk[2 * n + 1], fy, s0, S::kState);
+        mma_apart<NT, NT, true>(w0[2 * n], w0[2 * n + 1], fx,
                                block_at<KP>(st + S::ds, ks * 16, col, lane), S::kState);
       }
 #pragma unroll
       for (int n = 0; n < PB; ++n)
         if (cg * PB + n <= rg) {
           const uint32_t xt = blockn_at<kVT>(st + S::x, (cg * PB + n) * 16, ks * 16, lane);
-          mma_pair<TI, NT, false>(dp[2 * n], dp[2 * n + 1], fd, xt, S::kTok);
-          mma_pair<NT, NT, false>(da[2 * n], da[2 * n + 1], fy, xt, S::kTok);
+          mma_apart<TI, NT, false>(dp[2 * n], dp[2 * n + 1], fd, xt, S::kTok);
+          mma_apart<NT, NT, false>(da[2 * n], da[2 * n + 1], fy, xt, S::kTok);
         }
     }
     for (int i = tid; i < kVT * KP / 2; i += kGradThreads) {
@@ -209,8 +226,8 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
     for (int n = 0; n < PB; ++n)
       if (cg * PB + n <= rg) {
         const uint32_t kt = blockn_at<KP>(base + S::k, (cg * PB + n) * 16, ks * 16, lane);
-        mma_pair<TI, TI, false>(qk[2 * n], qk[2 * n + 1], fq, kt, S::kPlane);
-        mma_pair<TI, TI, false>(kk[2 * n], kk[2 * n + 1], fk, kt, S::kPlane);
+        mma_apart<TI, TI, false>(qk[2 * n], qk[2 * n + 1], fq, kt, S::kPlane);
+        mma_apart<TI, TI, false>(kk[2 * n], kk[2 * n + 1], fk, kt, S::kPlane);
       }
   }
   __syncthreads();   // the tiles' memory is M1's, M2's and H's from here
@@ -259,8 +276,8 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
 #pragma unroll
       for (int n = 0; n < NW; ++n) {
         const uint32_t kt = block_at<KP>(base + S::k, ks * 16, (cg * NW + n) * 16, lane);
-        mma_pair<NT, TI, true>(dq[2 * n], dq[2 * n + 1], f1, kt, S::kPlane);
-        mma_pair<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f2, kt, S::kPlane);
+        mma_apart<NT, TI, true>(dq[2 * n], dq[2 * n + 1], f1, kt, S::kPlane);
+        mma_apart<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f2, kt, S::kPlane);
       }
     }
     if (ks >= rg) {   // columns rg, queries and keys ks
@@ -273,9 +290,9 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
 #pragma unroll
       for (int n = 0; n < NW; ++n) {
         const int col = (cg * NW + n) * 16;
-        mma_pair<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f1,
+        mma_apart<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f1,
                                block_at<KP>(base + S::q, ks * 16, col, lane), S::kPlane);
-        mma_pair<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f2,
+        mma_apart<NT, TI, true>(dk[2 * n], dk[2 * n + 1], f2,
                                block_at<KP>(base + S::k, ks * 16, col, lane), S::kPlane);
       }
     }

@@ -5,10 +5,16 @@
 // chunks that CTAs take a grid apart; a thread has eight elements of every tensor
 // in flight.
 //
+// 161 M bf16 parameters with masters take 3.1 to 3.3 ms for 18 GB, 5.5 to 5.8 TB/s; four
+// CTAs of 256 threads an SM were the fastest of 128 to 512 threads (3.2, 3.1, 3.1), and
+// two groups of eight elements in flight a thread slower (3.4).
+//
 // 8-bit moments: a warp holds one block of 256 elements, eight a lane, so that the
 // new scales are two reductions over the warp.  The arithmetic of m, v and their
 // codes is in single rounded operations (no contraction), so that a code depends
-// on nothing but its inputs.
+// on nothing but its inputs.  Bound by instruction issue, a hundred an element: 161 M
+// parameters take 0.85 ms (1.7 with divisions, exact roots and conversions), and their
+// moments' values, which are HBM's, 0.28.
 #include <math.h>
 #include <stdio.h>
 
@@ -199,9 +205,9 @@ __device__ __forceinline__ float float_of(uint32_t word, int byte) {
 }
 // A word of four whole n in [0, 256], 256 as 0.
 __device__ __forceinline__ uint32_t word_of(float a, float b, float c, float d) {
-  const uint32_t lo = __byte_perm(__float_as_uint(a + 8388608.f), __float_as_uint(b + 8388608.f), 0x0040);
-  const uint32_t hi = __byte_perm(__float_as_uint(c + 8388608.f), __float_as_uint(d + 8388608.f), 0x0040);
-  return __byte_perm(lo, hi, 0x5410);
+  auto bits = [](float x) { return __float_as_uint(x + 8388608.f); };
+  return __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(d), 0x0040),
+                     0x5410);
 }
 __device__ __forceinline__ float floor_of(float x) {   // of 0 <= x < 2^22
   return __fadd_rz(x, 8388608.f) - 8388608.f;
@@ -344,8 +350,9 @@ __device__ __forceinline__ void chunk8(const Entry& e, int64_t at, int n, const 
     if (MASTER) store_some(w, left, pv);
     store_some(p, left, pv);
     const float mb = warp_max(mv), vb = warp_max(vv);
-    const float mi = __frcp_rn(mb), vi = __frcp_rn(vb);
-    const bool plain = mb > 0x1p-90f && mb < 0x1p90f && vb > 0x1p-90f && vb < 0x1p90f;
+    const float mi = mb > 0.f ? __frcp_rn(mb) : 0.f, vi = vb > 0.f ? __frcp_rn(vb) : 0.f;
+    auto usual = [](float x) { return x == 0.f || (x > 0x1p-90f && x < 0x1p90f); };
+    const bool plain = usual(mb) && usual(vb);
     float unsure = plain ? 0.f : 1.f;
     uint32_t key = mix(f.key + e.num);
     if (i >> 32) key = mix(key + (uint32_t)(i >> 32));

@@ -355,3 +355,117 @@ def test_a_few_long_sequences(ssd, B, G, H, V, K, docs):
     o1, s1 = ssd.delta_scan_fwd(*(t[:, :64].contiguous() for t in ins),
                                 initial_states=kw["initial_states"], return_final_states=True)
     du.close(o1, want[:, :64], BF, "out of a short one")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_value_for_many(ssd, dtype):
+    """Inputs expanded along the batch or the tokens (strides of 0)."""
+    d = du.inputs(3, 70, 2, 4, 40, 48, dtype, seed=80)
+    d["k"] = d["k"][:1].expand(3, -1, -1, -1)
+    d["v"] = d["v"][:, :1].expand(-1, 70, -1, -1)
+    ins, kw = split(d)
+    ins = (ins[0], d["k"][:1].cuda().expand(3, -1, -1, -1),
+           d["v"][:, :1].cuda().expand(-1, 70, -1, -1), *ins[3:])
+    dout = torch.randn(3, 70, 4, 40, generator=torch.Generator().manual_seed(1)).to(dtype)
+    want, fin, grads = du.reference(d, dout)
+    out, saved = ssd.delta_scan_fwd(*ins, save=True, **kw)
+    du.close(out, want, dtype, "out")
+    got = ssd.delta_scan_bwd(dout.cuda(), *ins, saved=saved, **kw)
+    for n, ref in grads.items():
+        du.close(got[n], ref, dtype, n)
+    # through autograd the leaf's gradient is the sum over what it was expanded along:
+    # three (70) rounded gradients' sum, itself rounded
+    leaf = [d["k"][:1].cuda().requires_grad_(), d["v"][:, :1].contiguous().cuda().requires_grad_()]
+    o = ssd.delta_scan(ins[0], leaf[0].expand(3, -1, -1, -1), leaf[1].expand(-1, 70, -1, -1),
+                       *ins[3:], **kw)
+    o.backward(dout.cuda())
+    for t, n, dim in ((leaf[0], "dk", 0), (leaf[1], "dv", 1)):
+        ref = grads[n].sum(dim, keepdim=True)
+        step = torch.finfo(dtype).eps / 2 * grads[n].abs().sum(dim, keepdim=True)
+        off = (t.grad.double().cpu() - ref).abs()
+        assert (off <= 72 * step + du.COMPUTE[dtype] * float(grads[n].norm())).all(), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [24, 130])
+def test_values_that_are_not_finite_stay_in_their_head(ssd, dtype, V):
+    """A head with a NaN and one with an infinity leave every other head's results as
+    they are, whichever SM took them after the other."""
+    B, L, H, K = 3, 200, 80, 40
+    d = du.inputs(B, L, H, H, V, K, dtype, seed=81)
+    ins, kw = split(d)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dout = torch.randn(B, L, H, V, generator=gen, device="cuda").to(dtype)
+
+    def both(ins):
+        out, fin, saved = ssd.delta_scan_fwd(*ins, return_final_states=True, save=True, **kw)
+        return dict(ssd.delta_scan_bwd(dout, *ins, saved=saved, **kw), out=out, fin=fin)
+
+    clean = both(ins)
+    bad = [t.clone() for t in ins]
+    bad[2][0, 70, 7] = float("nan")
+    bad[1][1, 130, 33] = float("inf")
+    bad[3][2, 5, 60] = float("nan")
+    got = both(bad)
+    mask = torch.ones(B, H, dtype=torch.bool, device="cuda")
+    for b, h in ((0, 7), (1, 33), (2, 60)):
+        mask[b, h] = False
+    for n, t in got.items():
+        by_head = t if n in ("fin", "d_initial_states") else t.transpose(1, 2)
+        ref = clean[n] if n in ("fin", "d_initial_states") else clean[n].transpose(1, 2)
+        assert torch.equal(by_head[mask], ref[mask]), n
+    assert not torch.isfinite(got["out"][0, 70:, 7]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_streams_at_once(ssd, dtype):
+    """Two calls in flight beside each other, as often as it takes to meet."""
+    jobs = []
+    for seed, (B, L, H, V, K) in enumerate(((2, 900, 100, 64, 64), (1, 3000, 3, 40, 128))):
+        ins, kw = split(du.inputs(B, L, H, H, V, K, dtype, seed=82 + seed))
+        dout = torch.ones(B, L, H, V, device="cuda", dtype=dtype)
+        jobs.append((ins, kw, dout))
+
+    def run(ins, kw, dout):
+        out, saved = ssd.delta_scan_fwd(*ins, save=True, **kw)
+        return [out, *(t for t in ssd.delta_scan_bwd(dout, *ins, saved=saved, **kw).values())]
+
+    want = [run(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = []
+        for st, j in zip(streams, jobs):
+            with torch.cuda.stream(st):
+                got.append(run(*j))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_past_2_31_elements(ssd, dtype):
+    """The last batch row of tensors of 2.35e9 elements is that row alone."""
+    B, L, H, V, K = 7, 16384, 160, 128, 128
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def rnd(*s):
+        return torch.empty(s, dtype=dtype, device="cuda").normal_(generator=gen)
+
+    q, k, v = rnd(B, L, H, K).mul_(K ** -0.5), rnd(B, L, H, K).mul_(K ** -0.5), rnd(B, L, H, V)
+    g = -torch.rand(B, L, H, generator=gen, device="cuda")
+    beta = torch.rand(B, L, H, generator=gen, device="cuda")
+    ins = (q, k, v, g, beta)
+    one = tuple(t[B - 1:].contiguous() for t in ins)
+    o1, f1 = ssd.delta_scan_fwd(*one, return_final_states=True)
+    out, fin = ssd.delta_scan_fwd(*ins, return_final_states=True)
+    assert torch.isfinite(o1).all() and float(o1.abs().max()) > 0
+    assert torch.equal(out[B - 1], o1[0]) and torch.equal(fin[B - 1], f1[0])
+    if dtype is F32:
+        return
+    d1 = ssd.delta_scan_bwd(one[2], *one)
+    got = ssd.delta_scan_bwd(v, *ins)
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(got[n][B - 1], d1[n][0]), n
