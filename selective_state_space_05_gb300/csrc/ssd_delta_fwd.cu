@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
       a_from<NT>(s[2 * ks], s[2 * ks + 1], f);
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) {
-        mma_pair<NT, TI, false>(y[2 * n], y[2 * n + 1], f,
+        mma_apart<NT, TI, false>(y[2 * n], y[2 * n + 1], f,
                                 blockn_at<KP>(st + S::k, n * 16, ks * 16, lane), S::kPlane);
         if (a.out)
-          mma_pair<NT, TI, false>(o[2 * n], o[2 * n + 1], f,
+          mma_apart<NT, TI, false>(o[2 * n], o[2 * n + 1], f,
                                   blockn_at<KP>(st + S::q, n * 16, ks * 16, lane), S::kPlane);
       }
     }
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) forward_kernel(const Args a) {
       zero(w);
 #pragma unroll
       for (int ks = 0; ks < C / 16; ++ks)
-        mma_pair<NT, TI, true>(w[0], w[1], f[ks], block_at<KP>(st + S::k, ks * 16, n * 16, lane),
+        mma_apart<NT, TI, true>(w[0], w[1], f[ks], block_at<KP>(st + S::k, ks * 16, n * 16, lane),
                                S::kPlane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

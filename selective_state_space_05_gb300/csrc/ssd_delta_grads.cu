@@ -72,23 +72,6 @@ __device__ __forceinline__ void put2(float* row, int c, int cols, bool pairs, fl
   }
 }
 
-// mma_pair from zero, added with one rounding to nearest: the tensor cores' sums truncate,
-// and a gradient is a sum of up to a dozen steps of products (dk was off by 1.1e-6
-// of its norm without that).
-template <int NA, int NB, bool TR>
-__device__ __forceinline__ void mma_apart(float (&d0)[4], float (&d1)[4],
-                                          const uint32_t (&a)[NA][4], uint32_t addr,
-                                          uint32_t plane) {
-  float x[2][4];
-  zero(x);
-  mma_pair<NA, NB, TR>(x[0], x[1], a, addr, plane);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d0[i] += x[0][i];
-    d1[i] += x[1][i];
-  }
-}
-
 template <int KP>
 __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   using S = GradSmem<KP>;

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
       a_from<NT>(s[2 * ks], s[2 * ks + 1], f);
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n)
-        mma_pair<NT, TI, false>(x[2 * n], x[2 * n + 1], f,
+        mma_apart<NT, TI, false>(x[2 * n], x[2 * n + 1], f,
                                 blockn_at<KP>(st + S::k, n * 16, ks * 16, lane), S::kPlane);
     }
 #pragma unroll
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
         a_from_t(d[ks][i], block_at<16>(dt + i * S::kOut, ks * 16, 0, lane));
 #pragma unroll
       for (int n = 0; n <= ks; ++n)
-        mma_pair<TI, NT, true>(x[2 * n], x[2 * n + 1], d[ks],
+        mma_apart<TI, NT, true>(x[2 * n], x[2 * n + 1], d[ks],
                                block_at<C>(st + S::p, ks * 16, n * 16, lane), S::kMat);
     }
 #pragma unroll
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
       a_from<NT>(x[2 * ks], x[2 * ks + 1], f);
 #pragma unroll
       for (int n = 0; n <= ks; ++n)
-        mma_pair<NT, NT, true>(y[2 * n], y[2 * n + 1], f,
+        mma_apart<NT, NT, true>(y[2 * n], y[2 * n + 1], f,
                                block_at<C>(st + S::t, ks * 16, n * 16, lane), S::kMat);
     }
     store_terms<C, NT>(y, obuf, S::opitch, a.dY + id * NT * C * a.VP + vw, a.VP, (int64_t)C * a.VP,
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
       zero(w);
 #pragma unroll
       for (int ks = 0; ks < C / 16; ++ks) {
-        mma_pair<NT, TI, true>(w[0], w[1], fq[ks], block_at<KP>(st + S::q, ks * 16, n * 16, lane),
+        mma_apart<NT, TI, true>(w[0], w[1], fq[ks], block_at<KP>(st + S::q, ks * 16, n * 16, lane),
                                S::kPlane);
-        mma_pair<NT, TI, true>(w[0], w[1], fk[ks], block_at<KP>(st + S::k, ks * 16, n * 16, lane),
+        mma_apart<NT, TI, true>(w[0], w[1], fk[ks], block_at<KP>(st + S::k, ks * 16, n * 16, lane),
                                S::kPlane);
       }
 #pragma unroll

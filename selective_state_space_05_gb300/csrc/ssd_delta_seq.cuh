@@ -24,7 +24,7 @@ __device__ __forceinline__ void mma_lower(float (&d)[C / 8][4], const float (&s)
     a_from<NT>(s[2 * ks], s[2 * ks + 1], f);
 #pragma unroll
     for (int n = ks; n < C / 16; ++n)
-      mma_pair<NT, NT, false>(d[2 * n], d[2 * n + 1], f, blockn_at<C>(base, n * 16, ks * 16, lane),
+      mma_apart<NT, NT, false>(d[2 * n], d[2 * n + 1], f, blockn_at<C>(base, n * 16, ks * 16, lane),
                               C * C * 2);
   }
 }
