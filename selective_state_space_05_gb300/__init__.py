@@ -1,8 +1,10 @@
 """GB300-native (sm_103a) Mamba-2 SSD chunked scan: forward, backward,
-decode step and the block's conv1d and grouped norm.
+decode step and the block's conv1d and grouped norm; the block's other
+operators, the gated delta rule and the optimizer's step.
 
 The computation lives in ``libssd_gb300.so`` (CUDA kernels behind the C ABI
-of include/ssd_scan.h); this package only marshals torch tensors into it.
+of include/ssd_scan.h and the headers beside it); this package only marshals
+torch tensors into it.
 """
 from .scan import (abi_version, bwd_workspace_bytes, causal_conv1d,  # noqa: F401
                    group_rmsnorm_, host_workspace_bytes, scan_status, ssd_chunk_fused,

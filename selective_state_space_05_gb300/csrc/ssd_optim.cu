@@ -5,7 +5,7 @@
 // chunks that CTAs take a grid apart; a thread has eight elements of every tensor
 // in flight.
 //
-// 161 M bf16 parameters with masters take 3.1 to 3.3 ms for 18 GB, 5.5 to 5.8 TB/s; four
+// 643 M bf16 parameters with masters take 3.1 to 3.3 ms for 18 GB, 5.5 to 5.8 TB/s; four
 // CTAs of 256 threads an SM were the fastest of 128 to 512 threads (3.2, 3.1, 3.1), and
 // two groups of eight elements in flight a thread slower (3.4).
 //
