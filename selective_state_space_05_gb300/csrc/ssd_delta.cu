@@ -184,6 +184,7 @@ size_t fwd_bytes(Args& a, int dtype, void* base, bool keep) {
   return dtype == SSD_DTYPE_BF16 ? carve<bf16>(a, base, keep) : carve<float>(a, base, keep);
 }
 size_t bwd_bytes(Args& a, int dtype, void* base) {
+  split(a);
   return dtype == SSD_DTYPE_BF16 ? carve_bwd<bf16>(a, base) : carve_bwd<float>(a, base);
 }
 

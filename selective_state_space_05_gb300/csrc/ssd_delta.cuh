@@ -43,11 +43,12 @@ template <> struct Mode<float> { static constexpr int C = 32, NT = 3, TI = 3; };
 // whose seq_idx changes.
 constexpr float kReset = -104.f;
 
-// How the tcgen05 forward takes its segments: one after another, each from the
+// How the tcgen05 passes take a sequence's segments: one after another, each from the
 // state that the one before left; or all at once, which takes two passes.  The first
 // gives each segment's effect on a state, S -> S M + W: W from a state of zeros, M
 // from the unit rows and without values.  Those are joined, and the second pass
-// starts each segment from its own state.
+// starts each segment from its own state.  (Backward: segments from the sequence's end,
+// the state's gradient in S's place and dout in the values'.)
 enum { kWhole, kParts, kJoined };
 
 // Per chunk and head: vectors of C floats each, then e^(G_C) alone.

@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i)
               S0[p][i] = it.unit && row == (part * SP + p) * 16 + i ? 1.f : 0.f;
         } else {
-          if (lane == 0 && a.pass == kWhole) wait_flag(flag_of(a, it), c / a.seg, &s.gave_up, &g_status);
+          if (lane == 0 && a.pass == kWhole)
+            wait_flag(flag_of(a, it), c / a.seg, &s.gave_up, &g_status);
           __syncwarp();
           read_slot<SP>(S0, a, it, row, part);
         }
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(KP * 2) tc_join_kernel(const __grid_constant__
       cp16(saddr(dst + i / KP * PM + i % KP), src + i / KP * 128 + i % KP, 16);
     cp_commit();
   };
-  load(1);
+  if (a.segs > 2) load(1);
   float4 x = slots[(int64_t)lane * size + col * 128 + row];
   for (int seg = 1; seg + 1 < a.segs; ++seg) {
     float* const now = s + (seg & 1) * 8 * PS;

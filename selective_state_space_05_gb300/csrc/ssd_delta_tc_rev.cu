@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&s.io_sync, lane);
       W(&s.io_sync, phase);
     };
-    auto put_do = [&](int n) {
+    auto put_do = [&](int n, int none) {   // (none: of unit rows, nothing comes in)
       const int p = n & 1;
       const unsigned char* const dt = s.d[p][row >> 6] + (row & 63) * 2;
       W(&s.d_full[p], (n >> 1) & 1);
@@ -256,8 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {   // pairs of tokens
           const unsigned char* at = dt + (q * 16 + 2 * i) * 128;
-          u[i] = *reinterpret_cast<const uint16_t*>(at) |
-                 (uint32_t)*reinterpret_cast<const uint16_t*>(at + 128) << 16;
+          u[i] = none ? 0u
+                      : *reinterpret_cast<const uint16_t*>(at) |
+                            (uint32_t)*reinterpret_cast<const uint16_t*>(at + 128) << 16;
           x[2 * i] = lo_of(u[i]) * a.scale;
           x[2 * i + 1] = hi_of(u[i]) * a.scale;
         }
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0;
     Item it = item(k++);
     int r = it.first;   // the chunk, counted from the end
-    if (it.bh >= 0) put_do(0);
+    if (it.bh >= 0) put_do(0, it.unit);
     for (int n = 0; it.bh >= 0; ++n) {
       const int c = nc - 1 - r;
       const int b = it.bh / a.H, h = it.bh % a.H, v0 = it.v0, vr = v0 + row;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<bf16*>(at) = hi;
           *reinterpret_cast<bf16*>(at + 2 * kTile) = __float2bfloat16_rn(f - __bfloat162float(hi));
         }
-        if (!a.wide_dv && vr < a.V) {   // rows off 16 bytes
+        if (!a.wide_dv && vr < a.V && a.pass != kParts) {   // rows off 16 bytes
           const int64_t t0 = (int64_t)c * kC + q * 16;
           bf16* dst = static_cast<bf16*>(a.dv) + (((int64_t)b * a.L + t0) * a.H + h) * a.V + vr;
 #pragma unroll
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       together(1);
       if (warp == kIoWarp) {
         if (tc::elect_one()) {
-          if (!s.gave_up) {
+          if (!s.gave_up && a.pass != kParts) {
             // planes [term][channel half][token][64] of the workspace; the first is dv
             unsigned char* to = reinterpret_cast<unsigned char*>(a.dY) +
                                 (((int64_t)it.bh * nc + c) * 2 * (a.VP / 64) + v0 / 64) * kTile;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it = item(k++);
         r = it.first;
       }
-      if (it.bh >= 0) put_do(n + 1);   // (what the MMAs read of n's is done as dY is)
+      if (it.bh >= 0) put_do(n + 1, it.unit);   // (what the MMAs read of n's is done as dY is)
     }
     if (warp == kIoWarp && tc::elect_one()) tc::bulk_wait_all();
   } else {
@@ -347,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t[16];
       two_terms(dS[p], t);
       tc::tmem_st16(lanes + kAS + (part * SP + p) * 16, t);
-      keep_row<KP>(t, a.dS, (int64_t)it.bh * nc + c, it.v0 + row, (part * SP + p) * 16, a);
+      if (a.pass != kParts)
+        keep_row<KP>(t, a.dS, (int64_t)it.bh * nc + c, it.v0 + row, (part * SP + p) * 16, a);
     };
     auto told = [&](uint64_t* bar) {   // what this warp wrote to TMEM is there
       tc::tmem_st_wait();
@@ -362,8 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         rc = it.first;
         if (rc == 0) {
           read_row<SP>(dS, a.dfinal, it.bh, it.v0 + row, part, a);
+        } else if (a.pass == kParts) {
+#pragma unroll
+          for (int p = 0; p < SP; ++p)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              dS[p][i] = it.unit && row == (part * SP + p) * 16 + i ? 1.f : 0.f;
         } else {
-          if (lane == 0) wait_flag(flag_of(a, it), rc / a.seg, &s.gave_up, &g_status);
+          if (lane == 0 && a.pass == kWhole)
+            wait_flag(flag_of(a, it), rc / a.seg, &s.gave_up, &g_status);
           __syncwarp();
           read_slot<SP>(dS, a, it, row, part);
         }
@@ -424,7 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (rc + 1 < it.last) {
         told(&s.s_ready);
+      } else if (a.pass == kParts) {
+        write_slot<SP>(dS, a, it, row, part);
       } else if (rc + 1 < nc) {   // on to the next segment
+        if (a.pass == kJoined) continue;
         write_slot<SP>(dS, a, it, row, part);
         warp_arrive(&s.slot_done, lane);
         if (warp == 0) {
@@ -474,7 +486,14 @@ static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
 int tc_reverse_status(int reset, cudaStream_t st, int* bits) {
   return read_status(rev::g_status, reset, st, bits);
 }
-cudaError_t launch_tc_reverse(const Args& a, cudaStream_t st) {
+cudaError_t launch_tc_reverse(const Args& args, cudaStream_t st) {
+  Args a = args;
+  if (a.pass == kParts) {
+    cudaError_t e = a.KP == 64 ? rev::run<64>(a, st) : rev::run<128>(a, st);
+    if (e == cudaSuccess) e = launch_tc_join(a, st);
+    if (e != cudaSuccess) return e;
+    a.pass = kJoined;
+  }
   return a.KP == 64 ? rev::run<64>(a, st) : rev::run<128>(a, st);
 }
 

@@ -469,3 +469,23 @@ def test_past_2_31_elements(ssd, dtype):
     got = ssd.delta_scan_bwd(v, *ins)
     for n in ("dq", "dk", "dv", "dg", "dbeta"):
         assert torch.equal(got[n][B - 1], d1[n][0]), n
+
+
+@pytest.mark.parametrize("B,G,H,V,K,docs", [(1, 1, 2, 128, 128, None), (1, 2, 4, 40, 64, None),
+                                            (2, 1, 1, 200, 100, [2000, 1, 1100])])
+def test_gradients_of_a_few_long_sequences(ssd, B, G, H, V, K, docs):
+    """The backward's segments all at once, with what was kept and without."""
+    L = 3101
+    d = du.inputs(B, L, G, H, V, K, BF, seed=90, docs=docs)
+    d["g"] *= 0.02     # gradients from many segments away
+    ins, kw = split(d)
+    gen = torch.Generator().manual_seed(2)
+    dout = torch.randn(B, L, H, V, generator=gen).to(BF)
+    df = torch.randn(B, H, V, K, generator=gen)
+    _, _, grads = du.reference(d, dout, df)
+    _, saved = ssd.delta_scan_fwd(*ins, save=True, **kw)
+    got = ssd.delta_scan_bwd(dout.cuda(), *ins, saved=saved, dfinal_states=df.cuda(), **kw)
+    for n, ref in grads.items():
+        du.close(got[n], ref, BF, n)
+    again = ssd.delta_scan_bwd(dout.cuda(), *ins, dfinal_states=df.cuda(), **kw)
+    assert all(torch.equal(got[n], again[n]) for n in got)
