@@ -184,6 +184,39 @@ def test_codes_bit_by_bit(ssd, seed, step):
         assert torch.equal(out[1][i].cpu().flatten(), v)
 
 
+def test_codes_at_their_edges(ssd):
+    """A first step's codes, bit by bit, for gradients of all sizes that fp32 squares
+    hold and past them, for values that are a code's own and next to it, for blocks of
+    zeros, and for four million values in all."""
+    gen = torch.Generator().manual_seed(9)
+    blocks = 16384
+    n = blocks * 256 - 100
+    g = torch.randn(blocks, 256, generator=gen)
+    g *= 10.0 ** (torch.rand(blocks, 1, generator=gen) * 38 - 21)     # 1e-21 to 1e17
+    m_code = torch.randint(0, 128, (blocks, 256), generator=gen).float() / 127
+    v_code = torch.randint(0, 256, (blocks, 256), generator=gen).float() / 255
+    near = 1 + (torch.randint(-2, 3, (blocks, 256), generator=gen)).float() * 2.0 ** -23
+    size = 10.0 ** (torch.rand(blocks, 1, generator=gen) * 8 - 6)
+    kind = torch.arange(blocks)[:, None] % 4
+    g = torch.where(kind == 1, m_code ** 2 * near * size, g)
+    g = torch.where(kind == 2, -v_code ** 2 * near * size, g)
+    g[3::64] = 0.0
+    g = g.flatten()[:n].contiguous()
+    m, v = g * (1.0 - 0.9) + 0.0, (g * g) * (1.0 - 0.999)
+    low = 0xFFFFFFFF
+    key = mix((mix((mix(torch.tensor(21)) + 1) & low) + 0) & low)
+    h = mix((key + torch.arange(n)) & low)
+    cm, ms = encode(m.abs(), ((h >> 16).float() + 0.5) * 2.0 ** -16, 127.0, 2)
+    cv, vs = encode(v, ((h & 0xFFFF).float() + 0.5) * 2.0 ** -16, 255.0, 4)
+    p = [torch.zeros(n, device="cuda")]
+    state = ssd.adamw_state(p, bits=8)
+    ssd.adamw_step(p, [g.cuda()], state, step=1, lr=1e-3, betas=(0.9, 0.999), seed=21)
+    assert torch.equal(state["exp_avg_scale"][0].cpu(), ms)
+    assert torch.equal(state["exp_avg_sq_scale"][0].cpu(), vs)
+    assert torch.equal(state["exp_avg"][0].cpu().float(), cm * torch.sign(m))
+    assert torch.equal(state["exp_avg_sq"][0].cpu().float(), torch.where(v > 0, cv.clamp(min=1), cv))
+
+
 def test_rounded_averages_keep_moving(ssd):
     """Each new moment's steps are below half a code's, yet the averages arrive:
     with gradients of one size v tends to their square as 1 - beta2^t.  The mean
