@@ -4,7 +4,7 @@
 // Transposed as in ssd_delta_fwd.cu: TMEM lane = channel, columns = tokens or
 // dstate.  Per chunk, with S in the registers of sixteen warps (a row and a quarter
 // of dstate a thread) and as two bf16 terms in TMEM:
-//   Y | O1 = S [K | Q]^T                 A: S
+//   Y = S K^T, then O1 = S Q^T           A: S
 //   y = v - e^G Y  -> TMEM               the chain's warps
 //   X = y T^T                            A: y, over Y's columns
 //   w = beta e^(G_C - G) X -> TMEM
@@ -19,9 +19,10 @@
 //   warps 16-19  out
 //   warp 20      issues the MMAs;  21: the copies
 // Shared and tensor memory: one CTA an SM.
-// Bound by that chain: of a chunk's 5400 to 6100 cycles the MMAs take 2100 (Y 1024,
-// X 528, W 512) and their commits 600, the three steps between them 600 to 1000 each.
-// 8 x 4096 tokens of 40 heads (20480 chunks): 480 us; with S0 and X kept for a
+// Bound by that chain: of a chunk's 5200 to 5900 cycles its MMAs take 1750 (Y 704, X
+// 528, W 512) and their commits 600, the three steps between them 600 to 1000 each.
+// 8 x 4096 tokens of 40 heads (20480 chunks): 463 us (480 with Y and O1 in one product,
+// which is the shorter of the two, but all of it in the chain's way); with S0 and X kept for a
 // backward (96 KB a chunk and head more) 4 x 4096 tokens take 396 us, half of it HBM's time.
 #include "ssd_delta_tc.cuh"
 
@@ -181,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the warp stays converged, one elected lane issuing: descriptors then live
       // in uniform registers)
       constexpr uint32_t id64 = tc::idesc_bf16(128, 64, false, false);
-      constexpr uint32_t id128 = tc::idesc_bf16(128, 128, false, false);
       constexpr uint32_t idw = tc::idesc_bf16(128, KP, false, true);
       constexpr uint32_t half = S::kHalf >> 4;
       constexpr uint32_t lo = kTile >> 4;   // a tile's second term
@@ -205,14 +205,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dm = dm0 + st * ((KP / 64) * S::kHalf >> 4);
         const uint64_t dt = dt0 + tp * (4 * kTile >> 4), dp = dp0 + tp * (4 * kTile >> 4);
         W(&s.kq_full[st], kq_ph);
-        if (n > 0) W(&s.o1_read, ph ^ 1);
         W(&s.s_ready, ph);
         if (stop()) break;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          mma_chain<KP / 16, false>(tmem + kR0, tmem + kAS, 1, dk, half, id128, true);
-          mma_chain<KP / 16, false>(tmem + kR0, tmem + kAS, 0, dk, half, id128, false);
+          mma_chain<KP / 16, false>(tmem + kR0, tmem + kAS, 1, dk, half, id64, true);
+          mma_chain<KP / 16, false>(tmem + kR0, tmem + kAS, 0, dk, half, id64, false);
           tc::mma_commit(&s.y_done);
+        }
+        __syncwarp();
+        if (n > 0) W(&s.o1_read, ph ^ 1);
+        if (stop()) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) {   // (while the chain's warps are at y)
+          mma_chain<KP / 16, false>(tmem + kO1, tmem + kAS, 1, dk + lo, half, id64, true);
+          mma_chain<KP / 16, false>(tmem + kO1, tmem + kAS, 0, dk + lo, half, id64, false);
         }
         __syncwarp();
         W(&s.tp_full[tp], fill);
