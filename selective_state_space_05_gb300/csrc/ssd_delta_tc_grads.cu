@@ -14,9 +14,9 @@
 // the warps have S0 in registers for <S0, dS>; every buffer's next load starts as soon
 // as it is free.  Sums over dstate run over the lanes with shuffles.
 // Bound by the sixteen warps' own work, phase after phase (7000 instructions a chunk
-// and quadrant, one every 2.8 cycles): 10240 chunks in 682 us, 4.1 TB/s.  (A CTA a
-// chunk, with S0 read again: 752 us.)  The idle MMA and copy time beside them would take
-// a second chunk's buffers, which shared memory (209 KB) has no room for.
+// and quadrant): 10240 chunks in 502 us, 5.5 TB/s.  Before the next chunk's D3 was computed
+// while this one's tokens are summed, for which D1 and D3 change places in TMEM, it took
+// 682; a CTA a chunk, with S0 read again for <S0, dS>, 752.
 #include "ssd_delta_tc.cuh"
 #include "ssd_row.cuh"
 
@@ -26,17 +26,20 @@ namespace grd {
 
 constexpr int kWarps = 16, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kThreads = 20 * 32;   // (two idle, for the register split)
-// TMEM columns: D1 (dY, do), D3lo, D2 (Xhi, Xlo), D3 then D4, D5
-constexpr uint32_t kD1 = 0, kD3lo = 128, kD2 = 192, kD3 = 320, kD5 = 448;
+// TMEM columns: D3lo, D2 (Xhi, Xlo), D5; D1 (dY, do) and D3 (then D4), which change places
+// with each chunk: D3 is computed as soon as the D1 before it is read
+constexpr uint32_t kD3lo = 128, kD2 = 192, kD5 = 448;
+__device__ __forceinline__ uint32_t d1_at(int it) { return it & 1 ? 320 : 0; }
+__device__ __forceinline__ uint32_t d3_at(int it) { return it & 1 ? 0 : 320; }
 constexpr int kHPitch = 65;
 
 template <int KP>
 struct Smem {
   static constexpr uint32_t kHalf = 2 * kTile;
   unsigned char kq[KP / 64][2][kTile];   // 64 dstate columns: K, Q
+  unsigned char q[2][kTile];             // a channel half: dYlo
   union {
-    unsigned char q[2][kTile];           // a channel half: dYlo
-    unsigned char m[2][2][kTile];        // then a term: M2, M1
+    unsigned char m[2][2][kTile];        // a term: M2, M1 (D3lo reads what stands there too)
     unsigned char out[2][KP / 64][kTile];   // then dq, dk
   };
   unsigned char x[2][2][kTile];          // a channel half: Xhi, Xlo
@@ -51,7 +54,7 @@ struct Smem {
   // copies that have landed, products done, and what the warps are through with
   uint64_t kq_full, x_full, p_full, q_full, s_full, ds_full;
   uint64_t d3_done, d1_done, d2_done, d4_done, drain_bar;
-  uint64_t m_ready, s_read, s_free, kq_free, p_free, q_free, d_free;
+  uint64_t m_ready, s_read, s_free, kq_free, p_free, out_free, d1_read, d_free;
   uint32_t tmem;
   volatile int gave_up;
 };
@@ -100,9 +103,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     uint64_t* const one[] = {&s.kq_full, &s.x_full,  &s.p_full,  &s.q_full,
                              &s.s_full,  &s.ds_full, &s.d3_done, &s.d1_done,
-                             &s.d2_done, &s.d4_done, &s.q_free,  &s.drain_bar};
+                             &s.d2_done, &s.d4_done, &s.out_free, &s.drain_bar};
     for (uint64_t* p : one) tc::mbar_init(p, 1);
-    uint64_t* const all[] = {&s.m_ready, &s.s_read, &s.s_free, &s.kq_free, &s.p_free, &s.d_free};
+    uint64_t* const all[] = {&s.m_ready, &s.s_read,  &s.s_free, &s.kq_free,
+                             &s.p_free,  &s.d1_read, &s.d_free};
     for (uint64_t* p : all) tc::mbar_init(p, kWarps);
     tc::mbar_fence_init();
     s.gave_up = 0;
@@ -191,9 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           ++ps;
-          if (v == 0 && it > 0) W(&s.q_free, (it - 1) & 1);
-          if (stop()) break;
-          if (tc::elect_one()) {
+          if (tc::elect_one()) {   // (D1 of the block before is done)
             tc::mbar_arrive_expect_tx(&s.q_full, nh * kTile);
             for (int i = 0; i < nh; ++i) bulk(s.q[i], y + next + i * kTile, kTile, &s.q_full);
           }
@@ -246,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             chain<4>(tmem + kD5, dk + i * 2 * tile, 2, dk + i * 2 * tile, 2, kk64, i == 0);
         }
         __syncwarp();
-        if (it > 0) W(&s.d_free, (it - 1) & 1);
+        const uint32_t kD1 = d1_at(it), kD3 = d3_at(it);
+        if (it > 0) W(&s.d1_read, (it - 1) & 1);
         for (int v = 0; v < blocks; ++v, ++n) {
           const uint32_t ph = n & 1;
           const int nh = halves(v);
@@ -265,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mma_commit(&s.d3_done);
           }
           __syncwarp();
+          if (v == 0 && it > 0) W(&s.d_free, (it - 1) & 1);
           W(&s.s_full, ph);
           if (stop()) break;
           tc::fence_after_sync();
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kg = h / (a.H / a.G);
       const int rows = (int)(a.L - (int64_t)c * kC < kC ? a.L - (int64_t)c * kC : kC);
       const float* const vec = s.vec[it & 1];
+      const uint32_t kD1 = d1_at(it), kD3 = d3_at(it);
       // <S0, dS>: a thread's pieces of S0 wait in registers for dS, which takes its place
       constexpr int pieces = KP / 8 * 128, mine = pieces / (kWarps * 32);
       float inner = 0.f, s0[mine][8];
@@ -408,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           scale_by(u, vec + kBeta * kC + t0);
           two_terms(u, r);
           tc::fence_before_sync();
-          W(&s.d1_done, n & 1);   // dY's and do's memory is M's and H's from here
+          W(&s.d1_done, n & 1);   // dY's and do's memory is H's from here
+          if (it > 0) W(&s.out_free, (it - 1) & 1);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             unsigned char* p = s.m[0][reads ? 1 : 0] + tile_at<64>(i, (t0 >> 3) + e);
@@ -484,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tmem_ld_wait_regs(r);
 #pragma unroll
       for (int e = 0; e < 16; ++e) dk[e] = __uint_as_float(r[e]);
+      tc::fence_before_sync();
+      warp_arrive(&s.d1_read, lane);
       scale_by(dk, vec + kRead * kC + t0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::bulk_commit();
           tc::bulk_wait_read();
         }
-        tc::mbar_arrive(&s.q_free);
+        tc::mbar_arrive(&s.out_free);
       }
       __syncwarp();
       // ---------------- beta's and the decays' gradients: a token a lane of two warps
