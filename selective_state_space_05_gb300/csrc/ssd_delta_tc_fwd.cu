@@ -22,8 +22,8 @@
 // Bound by that chain: of a chunk's 5200 to 5900 cycles its MMAs take 1750 (Y 704, X
 // 528, W 512) and their commits 600, the three steps between them 600 to 1000 each.
 // 8 x 4096 tokens of 40 heads (20480 chunks): 463 us (480 with Y and O1 in one product,
-// which is the shorter of the two, but all of it in the chain's way); with S0 and X kept for a
-// backward (96 KB a chunk and head more) 4 x 4096 tokens take 396 us, half of it HBM's time.
+// which is the shorter of the two, but all of it in the chain's way).  With S0 and X kept
+// for a backward 4 x 4096 tokens take 400 us: 192 KB a chunk and head, 4.9 TB/s.
 #include "ssd_delta_tc.cuh"
 
 namespace ssd {

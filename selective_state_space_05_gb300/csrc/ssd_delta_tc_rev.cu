@@ -12,8 +12,8 @@
 // Roles: warps 0-15 the chain, 16-19 do into TMEM for the next chunk and dY out of
 // it, 20 issues the MMAs, 21 the copies.  dS after each chunk and dY are kept as
 // terms for the chunks' own gradients.
-// Bound as the forward by the chain dS - Z - dx - dY - W - dS: 10240 chunks of 4 x 4096
-// tokens and 40 heads in 406 us.
+// Bound by the chain dS - Z - dx - dY - W - dS as the forward, and by HBM: 10240 chunks of
+// 4 x 4096 tokens and 40 heads in 406 us, 4.9 TB/s (96 KB of 192 a chunk are kept).
 #include "ssd_delta_tc.cuh"
 
 namespace ssd {
