@@ -52,9 +52,10 @@ Args sizes(int64_t B, int64_t L, int H, int V, int K, int G, int dtype) {
   a.KP = K <= 64 ? 64 : 128;
   a.tc = dtype == SSD_DTYPE_BF16;
   a.VP = a.tc ? (V + 127) / 128 * 128 : (V + 15) / 16 * 16;
-  // Segments only where there are at least as many sequences as SMs: eight or so for
+  // Segments one after another only where there are more sequences than SMs: eight or so for
   // each SM's share (a segment costs the state's way through the L2, about the time of a
-  // chunk), at least eight chunks long.
+  // chunk), at least eight chunks long.  Measured: 320 sequences of 64 chunks in whole 863
+  // us, in segments 800; with as many as SMs or fewer every one has its own SM.
   a.segs = 1;
   a.seg = a.nc;
   const int64_t lanes = (int64_t)a.B * H * (a.VP / 128), sms = row::sm_count();
@@ -112,9 +113,11 @@ void carve_work(Args& a, F take) {
   a.slots = reinterpret_cast<float*>(take(slots * 128 * a.KP * 4));
 }
 // A few long sequences leave most SMs idle: their segments run all at once, in two
-// passes, where that takes fewer chunks one after another than the sequence has.  The
-// first pass has 2 segs - 3 items a sequence (of 128 channels), the second segs; eight
-// chunks' time is what joining them and two launches take.
+// passes, where that takes fewer chunks' time than the sequence has chunks.  The first
+// pass has 2 segs - 3 items a sequence (of 128 channels), the second segs; an item takes
+// three chunks' time to start, joining one a segment, two launches eight.  Measured: 512
+// chunks of 16 heads in one pass 1.56 ms, in two of 6 segments 0.63, of 19 (no time to
+// start counted) 0.70; 16 chunks stay in one pass.
 void split(Args& a) {
   const int64_t lanes = (int64_t)a.B * a.H * (a.VP / 128), heads = (int64_t)a.B * a.H;
   const int64_t sms = row::sm_count();
