@@ -75,6 +75,14 @@ def _table(tensors, name, dtypes, dev, sizes):
     return ptrs, None
 
 
+def _scales(tensors, name, dev, blocks):
+    """Addresses of the 8-bit moments' scales: dense, one for each block."""
+    ptrs, _ = _table(tensors, name, _F32, dev, blocks)
+    if not all(map(_dense_of, tensors)):
+        raise ValueError(f"{name}: tensors must be dense")
+    return ptrs
+
+
 def _same_layout(first, others) -> None:
     """The lists' tensors agree element by element: all contiguous, or dense with
     the first's strides."""
@@ -174,9 +182,7 @@ def adamw_step(params, grads, state: dict, *, step, lr, betas=(0.9, 0.999), eps:
     if bits == 8:
         blocks = array.array("q", [-(-k // BLOCK) for k in sizes])
         for name, ts in (("exp_avg_scale", ms), ("exp_avg_sq_scale", vs)):
-            tables.append(_table(ts, name, _F32, dev, blocks)[0])
-            if not all(map(_dense_of, ts)):
-                raise ValueError(f"{name}: tensors must be dense")
+            tables.append(_scales(ts, name, dev, blocks))
             written += ts
     if master is not None:
         given = [i for i, w in enumerate(master) if w is not None]
@@ -242,10 +248,11 @@ def adamw_moments(state: dict, *, out=None, stream=None):
     om, ov = map(_list, out)
     sizes = array.array("q", map(_numel_of, m))
     blocks = array.array("q", [-(-k // BLOCK) for k in sizes])
-    tables = [_table(ts, name, dtype, dev, want)[0] for ts, name, dtype, want in (
-        (m, "exp_avg", torch.int8, sizes), (v, "exp_avg_sq", torch.uint8, sizes),
-        (ms, "exp_avg_scale", _F32, blocks), (vs, "exp_avg_sq_scale", _F32, blocks),
-        (om, "out", _F32, sizes), (ov, "out", _F32, sizes))]
+    tables = [_table(m, "exp_avg", torch.int8, dev, sizes)[0],
+              _table(v, "exp_avg_sq", torch.uint8, dev, sizes)[0],
+              _scales(ms, "exp_avg_scale", dev, blocks),
+              _scales(vs, "exp_avg_sq_scale", dev, blocks),
+              _table(om, "out", _F32, dev, sizes)[0], _table(ov, "out", _F32, dev, sizes)[0]]
     _same_layout(m, [("exp_avg_sq", v), ("out", om), ("out", ov)])
     code = _call("ssd_adamw_moments")(*map(_address, tables), _address(sizes), len(m), st)
     if code:
