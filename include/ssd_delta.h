@@ -16,7 +16,10 @@
  * atomics on values (equal inputs give equal bits).  "x dtype" is the dtype
  * argument, fp32 or bf16; every sum, the states and the decays are held in
  * fp32 or more, and each output is rounded once.  Pointers are aligned to their
- * element (rows on 16 bytes take wide accesses); the workspace to 256 bytes.
+ * element (dq and dk to two; rows on 16 bytes take wide accesses), the workspace to
+ * 256 bytes.  An output (and the workspace) may share no memory with an input or
+ * another output, but final_states may be initial_states, d_initial_states may be
+ * dfinal_states, and the step's out its v: others are refused (SSD_ERR_ARG).
  *
  * Tensors:
  *   q, k          [batch, seqlen, ngroups, dstate] x dtype
@@ -48,8 +51,8 @@ extern "C" {
 #define SSD_DELTA_ABI_VERSION 1
 int ssd_delta_abi_version(void);
 
-/* The scan.  out [batch, seqlen, nheads, headdim] x dtype, dense (written; may
- * be no input's memory); final_states written, or NULL.
+/* The scan.  out [batch, seqlen, nheads, headdim] x dtype, dense (written);
+ * final_states written, or NULL.
  * keep: nonzero if the workspace is to hold what ssd_delta_scan_bwd would
  * otherwise compute again (each chunk's triangular inverse and scores, first
  * state and corrections): it is then passed there as `saved`, unchanged.

@@ -261,6 +261,30 @@ cudaError_t pack_inputs(Args& a, char* at, cudaStream_t st) {
   return e;
 }
 
+// Memory that a call reads or writes.
+struct Span {
+  const void* p;
+  unsigned __int128 n;   // bytes
+};
+Span dense(const void* p, int64_t n, int size) { return {p, (unsigned __int128)n * size}; }
+Span tokens(const void* p, ssd_stride_t s, int64_t B, int64_t L, int64_t n, int size) {
+  return {p, ((unsigned __int128)(B - 1) * s.batch + (unsigned __int128)(L - 1) * s.token + n) * size};
+}
+bool meet(Span a, Span b) {
+  return a.p && b.p && (uintptr_t)a.p < (uintptr_t)b.p + b.n && (uintptr_t)b.p < (uintptr_t)a.p + a.n;
+}
+// Whether one of the outputs meets an input or another output.
+template <int NO, int NI>
+bool any_meet(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (const Span& x : in)
+      if (meet(out[i], x)) return true;
+  }
+  return false;
+}
+
 // One token.  HBM-bound on the fp32 state, read and written once.  A warp takes
 // kRows rows of a head's state, all their loads in flight before the first is
 // used; with a = S q and b = S k of the old state, u = beta (v - e^g b) and
@@ -448,8 +472,21 @@ int ssd_delta_scan_fwd(const void* q, ssd_stride_t q_stride, const void* k, ssd_
     return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
   if (off(workspace, 256)) return bad(SSD_ERR_ALIGN, "workspace must be 256-byte aligned");
   const size_t kept = fwd_bytes(a, dtype, workspace, keep != 0);
-  if (workspace_bytes < kept + pack_bytes(a, inputs_mapped(a)))
+  const size_t used = kept + pack_bytes(a, inputs_mapped(a));
+  if (workspace_bytes < used)
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const int es = dtype == SSD_DTYPE_BF16 ? 2 : 4;
+  const int64_t hs = batch * seqlen * nheads, states = batch * nheads * headdim * dstate;
+  const Span outs[] = {dense(out, hs * headdim, es), dense(final_states, states, 4),
+                       dense(workspace, (int64_t)used, 1)};
+  const Span ins[] = {tokens(q, q_stride, batch, seqlen, (int64_t)ngroups * dstate, es),
+                      tokens(k, k_stride, batch, seqlen, (int64_t)ngroups * dstate, es),
+                      tokens(v, v_stride, batch, seqlen, (int64_t)nheads * headdim, es),
+                      dense(g, hs, 4), dense(beta, hs, 4), dense(seq_idx, batch * seqlen, 4),
+                      dense(initial_states == final_states ? nullptr : initial_states, states, 4)};
+  if (any_meet(outs, ins))
+    return bad(SSD_ERR_ARG, "an output overlaps an input or another output "
+                            "(final_states may be initial_states)");
   a.out = out;
   a.wide_out = wide_rows(out, {0, 0}, headdim, dtype == SSD_DTYPE_BF16 ? 2 : 4);
   a.final = final_states;
@@ -500,8 +537,24 @@ int ssd_delta_scan_bwd(const void* dout, const float* dfinal_states, const void*
   a.wide_do = wide_rows(dout, {0, 0}, headdim, es);
   const bool aligned = inputs_mapped(a) && a.wide_do;
   const size_t used = own + (saved ? 0 : kept);
-  if (workspace_bytes < used + (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a)))
+  const size_t need = used + (aligned ? 0 : pack_bytes(a, false) + pack_dout_bytes(a));
+  if (workspace_bytes < need)
     return bad(SSD_ERR_WORKSPACE, "workspace too small");
+  const int64_t rows = batch * seqlen, states = batch * nheads * headdim * dstate;
+  const int64_t gk = (int64_t)ngroups * dstate;
+  const Span outs[] = {dense(dq, rows * gk, es), dense(dk, rows * gk, es), dense(dv, rows * hv, es),
+                       dense(dg, rows * nheads, 4), dense(dbeta, rows * nheads, 4),
+                       dense(d_initial_states, states, 4), dense(workspace, (int64_t)need, 1)};
+  const Span ins[] = {tokens(q, q_stride, batch, seqlen, gk, es),
+                      tokens(k, k_stride, batch, seqlen, gk, es),
+                      tokens(v, v_stride, batch, seqlen, hv, es), dense(dout, rows * hv, es),
+                      dense(g, rows * nheads, 4), dense(beta, rows * nheads, 4),
+                      dense(seq_idx, rows, 4), dense(initial_states, states, 4),
+                      dense(saved, (int64_t)kept, 1),
+                      dense(dfinal_states == d_initial_states ? nullptr : dfinal_states, states, 4)};
+  if (any_meet(outs, ins))
+    return bad(SSD_ERR_ARG, "an output overlaps an input or another output "
+                            "(d_initial_states may be dfinal_states)");
   fwd_bytes(f, dtype, saved ? const_cast<void*>(saved) : static_cast<char*>(workspace) + own, true);
   bwd_bytes(a, dtype, workspace);
   a.T = f.T;
@@ -557,6 +610,12 @@ int ssd_delta_decode_step(const void* q, const void* k, const void* v, const flo
       off(state, 4))
     return bad(SSD_ERR_ALIGN, "a pointer is not aligned to its element");
   if (!(fabsf(scale) <= 3.0e38f)) return bad(SSD_ERR_ARG, "scale must be finite");
+  const int64_t hs = batch * nheads, gk = batch * ngroups * dstate;
+  const Span outs[] = {dense(out, hs * headdim, (int)es), dense(state, hs * headdim * dstate, 4)};
+  const Span ins[] = {dense(q, gk, (int)es), dense(k, gk, (int)es), dense(g, hs, 4),
+                      dense(beta, hs, 4), dense(v == out ? nullptr : v, hs * headdim, (int)es)};
+  if (any_meet(outs, ins))
+    return bad(SSD_ERR_ARG, "out or state overlaps an input or the other (out may be v)");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_bad(dtype == SSD_DTYPE_BF16
                       ? run_step<bf16>(q, k, v, g, beta, scale, state, batch, nheads, headdim,

@@ -87,7 +87,8 @@ def delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     headdim, dstate] fp32; seq_idx [batch, seqlen] int32; scale defaults to
     dstate ** -0.5.  Returns out, or a tuple of out, with return_final_states
     the final states, and with save what delta_scan_bwd takes as `saved` (the
-    workspace, which then must not be used for anything else)."""
+    workspace, which then must not be used for anything else).  final_states may
+    be initial_states; otherwise outputs share no memory with inputs."""
     args, sizes, dt, dev = _inputs(q, k, v, g, beta, scale, initial_states, seq_idx)
     B, L, H, V, K, G = sizes
     st = _stream_of(stream, dev)
@@ -213,7 +214,7 @@ def delta_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torc
     """One token per batch row of the gated delta rule (ssd_delta_decode_step):
     q, k [batch, ngroups, dstate], v [batch, nheads, headdim]; g, beta [batch,
     nheads] fp32; state [batch, nheads, headdim, dstate] fp32, moved on in
-    place.  Returns out [batch, nheads, headdim]."""
+    place; out may be v.  Returns out [batch, nheads, headdim]."""
     dt = _float_dtype(q, "q")
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [batch, ngroups, dstate] and v [batch, nheads, headdim]")
