@@ -21,7 +21,7 @@ from .scan import _DT
 _F32, _I64 = torch.float32, torch.int64
 BLOCK = 256   # values that share a scale of 8-bit moments
 
-_ptr_of, _numel_of = torch.Tensor.data_ptr, torch.Tensor.numel
+_ptr_of, _numel_of, _shape_of = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.size
 _dev_of, _dense_of = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
@@ -54,14 +54,15 @@ def adamw_state(params, *, bits: int = 32, master: bool = False) -> dict:
     return state
 
 
-def _table(tensors, name, dtypes, dev, sizes):
-    """Addresses of the tensors, after checks of their sizes, device and type
-    (dtypes: a type, or a dict of codes; then also the codes)."""
+def _table(tensors, name, dtypes, dev, sizes, of=_numel_of):
+    """Addresses of the tensors, after checks of their sizes (None: any; of: what
+    `sizes` lists, elements or shapes), device and type (dtypes: a type, or a dict
+    of codes; then also the codes)."""
     if tensors is None:
         raise ValueError(f"{name} is required")
-    if array.array("q", map(_numel_of, tensors)) != sizes:
+    if sizes is not None and list(map(of, tensors)) != sizes:
         raise ValueError(f"{name}: the tensors' number or sizes do not match the parameters'")
-    if sizes and set(map(_dev_of, tensors)) != {dev.index}:
+    if tensors and set(map(_dev_of, tensors)) != {dev.index}:
         raise ValueError(f"{name}: the tensors must be on {dev}")
     ptrs = array.array("Q", map(_ptr_of, tensors))
     if isinstance(dtypes, dict):
@@ -70,7 +71,7 @@ def _table(tensors, name, dtypes, dev, sizes):
         except KeyError as e:
             raise ValueError(f"{name}: tensors must be float32 or bfloat16, got "
                              f"{e.args[0]}") from None
-    if sizes and set(map(_dtype_of, tensors)) != {dtypes}:
+    if tensors and set(map(_dtype_of, tensors)) != {dtypes}:
         raise ValueError(f"{name}: the tensors must be {dtypes}")
     return ptrs, None
 
@@ -84,17 +85,17 @@ def _scales(tensors, name, dev, blocks):
 
 
 def _same_layout(first, others) -> None:
-    """The lists' tensors agree element by element: all contiguous, or dense with
-    the first's strides."""
+    """The lists' tensors, of the same shapes, agree element by element: all
+    contiguous, or dense with the first's strides."""
     if all(map(_dense_of, first)) and all(all(map(_dense_of, ts)) for _, ts in others):
         return
     for i, p in enumerate(first):
         if not (p.is_contiguous() or p.numel() == 0 or _storage_dense(p)):
             raise ValueError("the tensors must be dense")
         for name, ts in others:
-            if not (ts[i].is_contiguous() and p.is_contiguous()) and (
-                    ts[i].shape != p.shape or ts[i].stride() != p.stride()):
-                raise ValueError(f"{name}: tensors must have their parameter's shape and strides")
+            if not (ts[i].is_contiguous() and p.is_contiguous()) and \
+                    ts[i].stride() != p.stride():
+                raise ValueError(f"{name}: tensors must have their parameter's strides")
 
 
 def _spread(values, places, n):
@@ -142,11 +143,11 @@ def adamw_step(params, grads, state: dict, *, step, lr, betas=(0.9, 0.999), eps:
         p = p (1 - lr weight_decay)
             - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
 
-    params and grads: lists of fp32 or bf16 tensors (a gradient None leaves its
-    parameter as it is); state: adamw_state's dict, whose moments (and masters)
-    move on.  step: this step's number from 1, an int or one int64 value on the
-    device, which a captured graph reads again at each replay; lr: a number or one
-    fp32 value on the device.  With grad_norm (what grad_norm() returned) and
+    params and grads: lists of fp32 or bf16 tensors of the same shapes (a gradient
+    None leaves its parameter as it is); state: adamw_state's dict, whose moments
+    (and masters) move on.  step: this step's number from 1, an int or one int64
+    value on the device, which a captured graph reads again at each replay; lr: a
+    number or one fp32 value on the device.  With grad_norm (what grad_norm() returned) and
     max_norm the gradients count as clip_grads would leave them, times min(1,
     max_norm / (grad_norm + 1e-6)), but are not written.  seed: of the 8-bit
     moments' rounding."""
@@ -171,23 +172,23 @@ def adamw_step(params, grads, state: dict, *, step, lr, betas=(0.9, 0.999), eps:
     st = _stream_of(stream, dev)
     m, v, master, ms, vs = lists.values()
     bits = 32 if ms is None and vs is None else 8
-    sizes = array.array("q", map(_numel_of, params))
-    pp, pc = _table(params, "params", _DT, dev, sizes)
-    gp, gc = _table(grads, "grads", _DT, dev, sizes)
-    mp, _ = _table(m, "exp_avg", _F32 if bits == 32 else torch.int8, dev, sizes)
-    vp, _ = _table(v, "exp_avg_sq", _F32 if bits == 32 else torch.uint8, dev, sizes)
+    sizes, shapes = array.array("q", map(_numel_of, params)), list(map(_shape_of, params))
+    pp, pc = _table(params, "params", _DT, dev, None)
+    gp, gc = _table(grads, "grads", _DT, dev, shapes, _shape_of)
+    mp, _ = _table(m, "exp_avg", _F32 if bits == 32 else torch.int8, dev, shapes, _shape_of)
+    vp, _ = _table(v, "exp_avg_sq", _F32 if bits == 32 else torch.uint8, dev, shapes, _shape_of)
     written = [*params, *m, *v]
     alike = [("grads", grads), ("exp_avg", m), ("exp_avg_sq", v)]
     tables, codes = [pp, gp, mp, vp], [pc, gc]
     if bits == 8:
-        blocks = array.array("q", [-(-k // BLOCK) for k in sizes])
+        blocks = [-(-k // BLOCK) for k in sizes]
         for name, ts in (("exp_avg_scale", ms), ("exp_avg_sq_scale", vs)):
             tables.append(_scales(ts, name, dev, blocks))
             written += ts
     if master is not None:
         given = [i for i, w in enumerate(master) if w is not None]
         some = [master[i] for i in given]
-        wp, _ = _table(some, "master", _F32, dev, array.array("q", [sizes[i] for i in given]))
+        wp, _ = _table(some, "master", _F32, dev, [shapes[i] for i in given], _shape_of)
         alike.append(("master", some if len(given) == len(params) else
                       [params[i] if w is None else w for i, w in enumerate(master)]))
         tables.append(_spread(wp, given, len(params)))
@@ -246,13 +247,13 @@ def adamw_moments(state: dict, *, out=None, stream=None):
     if not given:
         out = tuple([_empty_like(t, dev, stream) for t in ts] for ts in (m, v))
     om, ov = map(_list, out)
-    sizes = array.array("q", map(_numel_of, m))
-    blocks = array.array("q", [-(-k // BLOCK) for k in sizes])
-    tables = [_table(m, "exp_avg", torch.int8, dev, sizes)[0],
-              _table(v, "exp_avg_sq", torch.uint8, dev, sizes)[0],
+    sizes, shapes = array.array("q", map(_numel_of, m)), list(map(_shape_of, m))
+    blocks = [-(-k // BLOCK) for k in sizes]
+    tables = [_table(m, "exp_avg", torch.int8, dev, shapes, _shape_of)[0],
+              _table(v, "exp_avg_sq", torch.uint8, dev, shapes, _shape_of)[0],
               _scales(ms, "exp_avg_scale", dev, blocks),
               _scales(vs, "exp_avg_sq_scale", dev, blocks),
-              _table(om, "out", _F32, dev, sizes)[0], _table(ov, "out", _F32, dev, sizes)[0]]
+              *(_table(ts, "out", _F32, dev, shapes, _shape_of)[0] for ts in (om, ov))]
     _same_layout(m, [("exp_avg_sq", v), ("out", om), ("out", ov)])
     code = _call("ssd_adamw_moments")(*map(_address, tables), _address(sizes), len(m), st)
     if code:

@@ -25,3 +25,24 @@ def test_scales_that_are_not_dense(ssd):
             with pytest.raises(ValueError, match="dense"):
                 ssd.adamw_moments(state)
     assert (p[0] == 0).all()
+
+
+def test_another_shape(ssd):
+    """A gradient, moment or master of as many elements in another shape."""
+    def dense(*shape):
+        return torch.ones(shape, device="cuda")
+    p, g = [dense(8, 4).to(torch.bfloat16), dense(3)], [dense(8, 4), dense(3)]
+    for bits in (32, 8):
+        good = ssd.adamw_state(p, bits=bits, master=True)
+        with pytest.raises(ValueError, match="grads"):
+            ssd.adamw_step(p, [dense(4, 8), g[1]], good, step=1, lr=1e-3)
+        for name in ("exp_avg", "exp_avg_sq", "master"):
+            bad = dict(good, **{name: [good[name][0].view(4, 8), good[name][1]]})
+            with pytest.raises(ValueError, match=name):
+                ssd.adamw_step(p, g, bad, step=1, lr=1e-3)
+        if bits == 8:
+            with pytest.raises(ValueError, match="out"):
+                ssd.adamw_moments(good, out=([dense(4, 8), dense(3)], [dense(8, 4), dense(3)]))
+        assert all((t == 1).all() for t in p)
+        ssd.adamw_step(p, g, good, step=1, lr=0.0)
+        assert all((t == 1).all() for t in p)
