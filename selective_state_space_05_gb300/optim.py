@@ -194,10 +194,13 @@ def adamw_step(params, grads, state: dict, *, step, lr, betas=(0.9, 0.999), eps:
         tables.append(_spread(wp, given, len(params)))
         written += some
     _same_layout(params, alike)
-    if len(set(pp)) != len(params):
-        full = [a for a, k in zip(pp, sizes) if k]
+    once = [pp, *tables[2:]]   # what is written
+    if master is not None:
+        once[-1] = wp
+    if len(set().union(*once)) != sum(map(len, once)):
+        full = [a for t in once for a in t if a]   # (0: no elements)
         if len(set(full)) != len(full):
-            raise ValueError("a parameter is given twice")
+            raise ValueError("a parameter or a tensor of the state is given twice")
     if have is not None:   # the others' places keep their numbers, with no elements
         tables = [_spread(t, have, n) for t in tables]
         codes = [_spread(t, have, n) for t in codes]

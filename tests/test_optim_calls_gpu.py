@@ -46,3 +46,25 @@ def test_another_shape(ssd):
         assert all((t == 1).all() for t in p)
         ssd.adamw_step(p, g, good, step=1, lr=0.0)
         assert all((t == 1).all() for t in p)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_of_the_state_twice(ssd, bits):
+    """Two parameters with one moment, scale or master, or one tensor for both moments:
+    two threads would write the same element."""
+    p = [torch.zeros(300, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    g = [torch.ones(300, device="cuda") for _ in range(2)]
+    good = ssd.adamw_state(p, bits=bits, master=True)
+    for name, ts in good.items():
+        with pytest.raises(ValueError, match="twice"):
+            ssd.adamw_step(p, g, dict(good, **{name: [ts[0], ts[0]]}), step=1, lr=1e-3)
+    if bits == 32:
+        with pytest.raises(ValueError, match="twice"):
+            ssd.adamw_step(p, g, dict(good, exp_avg_sq=good["exp_avg"]), step=1, lr=1e-3)
+        with pytest.raises(ValueError, match="twice"):
+            ssd.adamw_step(p, g, dict(good, master=good["exp_avg"][::-1]), step=1, lr=1e-3)
+    assert all((t == 0).all() for t in p)
+    # without elements, or without masters, nothing is written twice
+    none = [torch.zeros(0, device="cuda") for _ in range(2)]
+    ssd.adamw_step(none, none, ssd.adamw_state(none, bits=bits), step=1, lr=1e-3)
+    ssd.adamw_step(p, g, dict(good, master=[None, None]), step=1, lr=0.0)
