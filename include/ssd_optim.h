@@ -40,7 +40,9 @@ typedef struct {
  *   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
- * in fp32.  params, grads: fp32 or bf16, each tensor of its own dtype.  masters
+ * in fp32 (g' too: not rounded to the gradients' type, as where ssd_clip_grads writes
+ * it).  The factor keeps its bits where it is below the normal fp32 range; a norm that
+ * is infinite in fp32 makes it 0, a NaN one makes everything NaN.  params, grads: fp32 or bf16, each tensor of its own dtype.  masters
  * NULL, or an array whose entry is NULL or the parameter's fp32 master: the step
  * is then the master's, and the parameter its rounded copy.
  * bits 32: exp_avgs, exp_avg_sqs are float, the scales NULL.

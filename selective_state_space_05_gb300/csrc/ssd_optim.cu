@@ -62,7 +62,10 @@ struct Opt {
 };
 // What each thread needs of it.
 struct Factors {
-  float size, keep, root, coef;   // lr / (1 - beta1^t), 1 - lr decay, (1 - beta2^t)^-1/2, clipping
+  float size, keep, root;   // lr / (1 - beta1^t), 1 - lr decay, (1 - beta2^t)^-1/2
+  // clipping: coef * first, where first is 1, or 2^-64 where the factor alone would be a
+  // subnormal of few bits (ssd_clip.cu)
+  float coef, first;
   uint32_t key;
 };
 
@@ -86,10 +89,17 @@ __device__ __forceinline__ Factors factors(const Opt& o) {
   f.size = (float)(lr / -expm1(t * o.log_b1));
   f.root = (float)(1.0 / sqrt(-expm1(t * o.log_b2)));
   f.keep = (float)(1.0 - lr * o.decay);
-  f.coef = 1.f;
+  f.coef = f.first = 1.f;
   if (o.norm) {
     // (a product with the reciprocal: what a tensor under a number is elsewhere)
-    const float c = __fmul_rn(__frcp_rn(__fadd_rn(*o.norm, 1e-6f)), o.max_norm);
+    const float r = __frcp_rn(__fadd_rn(*o.norm, 1e-6f));
+    float c = __fmul_rn(r, o.max_norm);
+    if (r < 0x1p-126f || c < 0x1p-100f) {   // near the end of the range: as clip_grads
+      const double d = (double)o.max_norm / ((double)*o.norm + 1e-6);
+      const bool tiny = d < 0x1p-100;
+      f.first = tiny ? 0x1p-64f : 1.f;
+      c = (float)(tiny ? d * 0x1p64 : d);
+    }
     f.coef = c >= 1.f ? 1.f : c;   // a NaN norm gives NaN
   }
   f.key = mix(mix(o.seed) + low);
@@ -134,6 +144,15 @@ __device__ __forceinline__ void store8(T* p, bool wide, const float (&v)[kVec]) 
 }
 __device__ __forceinline__ bool on16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+// Gradients as clipping leaves them.
+__device__ __forceinline__ void clip(float (&g)[kVec], const Factors& f) {
+  if (f.first != 1.f) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) g[j] = __fmul_rn(g[j], f.first);
+  }
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) g[j] = __fmul_rn(g[j], f.coef);
+}
 __device__ __forceinline__ void moments(float g, float& m, float& v, const Opt& o) {
   m = __fadd_rn(__fmul_rn(m, o.b1), __fmul_rn(g, o.c1));
   v = __fadd_rn(__fmul_rn(v, o.b2), __fmul_rn(__fmul_rn(g, g), o.c2));
@@ -173,9 +192,10 @@ __device__ __forceinline__ void chunk32(const Entry& e, int64_t at, int n, const
     load8(v + k, wv, vv);
     if (MASTER) load8(w + k, ww, pv);
     else load8(p + k, wp, pv);
+    clip(gv, f);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      moments(__fmul_rn(gv[j], f.coef), mv[j], vv[j], o);
+      moments(gv[j], mv[j], vv[j], o);
       pv[j] = update(pv[j], mv[j], vv[j], f, o);
     }
     store8(m + k, true, mv);
@@ -188,7 +208,7 @@ __device__ __forceinline__ void chunk32(const Entry& e, int64_t at, int n, const
   if ((int)threadIdx.x < head + tail) {
     const int k = (int)threadIdx.x < head ? threadIdx.x : threadIdx.x + vecs * kVec;
     float mv = m[k], vv = v[k];
-    moments(__fmul_rn(to_f(g[k]), f.coef), mv, vv, o);
+    moments(__fmul_rn(__fmul_rn(to_f(g[k]), f.first), f.coef), mv, vv, o);
     const float pv = update(MASTER ? w[k] : to_f(p[k]), mv, vv, f, o);
     m[k] = mv;
     v[k] = vv;
@@ -338,12 +358,13 @@ __device__ __forceinline__ void chunk8(const Entry& e, int64_t at, int n, const 
     cm.y ^= 0x80808080u;
     if (MASTER) load_some(w, left, pv);
     else load_some(p, left, pv);
+    clip(gv, f);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       mv[j] = __fmul_rn(m_of(j < 4 ? cm.x : cm.y, j % 4), ms);
       vv[j] = __fmul_rn(v_unit(float_of(j < 4 ? cv.x : cv.y, j % 4)), vs);
       if (j >= left) mv[j] = vv[j] = 0.f;   // (a scale that is not finite stays out of the rest)
-      moments(__fmul_rn(gv[j], f.coef), mv[j], vv[j], o);
+      moments(gv[j], mv[j], vv[j], o);
       if (j >= left) mv[j] = vv[j] = 0.f;
       pv[j] = update(pv[j], mv[j], vv[j], f, o);
     }

@@ -148,8 +148,9 @@ def adamw_step(params, grads, state: dict, *, step, lr, betas=(0.9, 0.999), eps:
     (and masters) move on.  step: this step's number from 1, an int or one int64
     value on the device, which a captured graph reads again at each replay; lr: a
     number or one fp32 value on the device.  With grad_norm (what grad_norm() returned) and
-    max_norm the gradients count as clip_grads would leave them, times min(1,
-    max_norm / (grad_norm + 1e-6)), but are not written.  seed: of the 8-bit
+    max_norm the gradients count as clip_grads would leave them in fp32, times
+    min(1, max_norm / (grad_norm + 1e-6)), but are not written (an infinite norm
+    makes that 0; clip_grads knows norms past fp32's range).  seed: of the 8-bit
     moments' rounding."""
     params, grads = _list(params), _list(grads)
     n = len(params)

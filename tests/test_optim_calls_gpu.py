@@ -68,3 +68,34 @@ def test_a_tensor_of_the_state_twice(ssd, bits):
     none = [torch.zeros(0, device="cuda") for _ in range(2)]
     ssd.adamw_step(none, none, ssd.adamw_state(none, bits=bits), step=1, lr=1e-3)
     ssd.adamw_step(p, g, dict(good, master=[None, None]), step=1, lr=0.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("size,max_norm", [(3e36, 1e-3), (3e36, 1e-10), (9e36, 30.0),
+                                           (9e36, 1e37), (1e-3, 1e-38), (1.0, 1e-3)])
+def test_clipping_at_the_end_of_the_range(ssd, bits, size, max_norm):
+    """The step clips as clip_grads does where the factor or the norm's reciprocal is
+    below the normal fp32 range (a norm of 1.6e38 at most here).  Its factor is off by
+    three roundings, clip_grads' by one, each of their products by another (two with
+    the power of two that keeps its bits); the moment m = (1 - beta1) g' by one more
+    each: 9 of 2^-24, where m is a normal number."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    g = [(torch.rand(1000, generator=gen, device="cuda") * 0.9 + 0.1) * size]
+    g[0][::2] *= -1
+    norm = ssd.grad_norm(g)
+    assert torch.isfinite(norm) and float(norm) > max_norm
+    clipped = [t.clone() for t in g]
+    ssd.clip_grads(clipped, max_norm)
+    res = []
+    for grads, kw in ((g, dict(grad_norm=norm, max_norm=max_norm)), (clipped, {})):
+        p = [torch.zeros(1000, device="cuda")]
+        state = ssd.adamw_state(p, bits=bits)
+        ssd.adamw_step(p, grads, state, step=1, lr=1.0, betas=(0.5, 0.5), eps=0.0, seed=3, **kw)
+        m, v = ssd.adamw_moments(state)
+        res.append((m[0].double(), p[0].double(), state))
+    (m, p, state), (want, q, other) = res
+    if bits == 8:   # (codes are rounded up or down by chance: the blocks' largest are not)
+        m, want = (s["exp_avg_scale"][0].double() for s in (state, other))
+    small = 2.0 ** -149 if max_norm < 1e-30 else 0.0     # results that are subnormal
+    assert ((m - want).abs() <= 9 * 2.0 ** -24 * want.abs() + 4 * small).all(), \
+        float(((m - want).abs() / want.abs()).max())
