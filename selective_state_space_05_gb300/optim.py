@@ -66,7 +66,10 @@ def _table(tensors, name, dtypes, dev, sizes, of=_numel_of):
         raise ValueError(f"{name}: the tensors must be on {dev}")
     ptrs = array.array("Q", map(_ptr_of, tensors))
     if isinstance(dtypes, dict):
+        kinds = set(map(_dtype_of, tensors))
         try:
+            if len(kinds) == 1:
+                return ptrs, array.array("i", [dtypes[kinds.pop()]]) * len(tensors)
             return ptrs, array.array("i", map(dtypes.__getitem__, map(_dtype_of, tensors)))
         except KeyError as e:
             raise ValueError(f"{name}: tensors must be float32 or bfloat16, got "
