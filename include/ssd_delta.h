@@ -37,7 +37,9 @@
  * batch * nheads * chunks < 2^31 (chunks of 64 tokens for bf16, 32 for fp32).
  * Keys of unit length (and beta in [0, 2]) keep the recurrence stable; the call
  * does not normalise them.  An infinity or NaN spreads, as in any chunked form,
- * to its chunk's other tokens of its head, and to those after it.
+ * to its chunk's other tokens of its head, and to those after it.  Finite values do
+ * not count as such up to the end of the fp32 range, but for a bf16 dv that rounds to
+ * an infinity: the other gradients of its chunk are then not finite.
  */
 #ifndef SSD_DELTA_H
 #define SSD_DELTA_H

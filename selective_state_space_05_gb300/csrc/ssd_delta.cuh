@@ -146,6 +146,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The same for a term that others follow: what is beyond bf16's largest value (finite
+// ones within half a place of 2^128, and infinities) becomes that, and the rest is left
+// to the next term, so that a finite value's terms are finite.
+__device__ __forceinline__ uint32_t pack2_part(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 // Two values as NT packed pairs of terms.
@@ -153,7 +161,7 @@ template <int NT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[NT]) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    t[i] = pack2(x, y);
+    t[i] = i + 1 < NT ? pack2_part(x, y) : pack2(x, y);
     if (i + 1 < NT) {
       x -= lo_of(t[i]);
       y -= hi_of(t[i]);

@@ -73,11 +73,18 @@ __device__ __forceinline__ void store_terms(const float (&s)[C / 8][4], unsigned
     for (int e = 0; e < 4; ++e) r[n][e] = s[n][e];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    store_rows<bf16, C>(r, buf, pitch, dst + i * plane, ld, C, 16, true, lane);
+    float h[C / 8][4];   // the term
 #pragma unroll
     for (int n = 0; n < C / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[n][e] -= __bfloat162float(__float2bfloat16_rn(r[n][e]));
+      for (int e = 0; e < 4; e += 2) {
+        const uint32_t w = i + 1 < NT ? pack2_part(r[n][e], r[n][e + 1]) : pack2(r[n][e], r[n][e + 1]);
+        h[n][e] = lo_of(w);
+        h[n][e + 1] = hi_of(w);
+        r[n][e] -= h[n][e];
+        r[n][e + 1] -= h[n][e + 1];
+      }
+    store_rows<bf16, C>(h, buf, pitch, dst + i * plane, ld, C, 16, true, lane);
   }
 }
 // A warp's 16 rows of a state as terms into planes [VP][KP].

@@ -91,7 +91,7 @@ __device__ __forceinline__ void two_terms(const float (&v)[16], uint32_t (&t)[16
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float x = v[2 * i], y = v[2 * i + 1];
-    t[i] = pack2(x, y);
+    t[i] = pack2_part(x, y);
     add2p(x, y, __uint_as_float((t[i] << 16) ^ 0x80000000u),
           __uint_as_float((t[i] & 0xFFFF0000u) ^ 0x80000000u));
     t[8 + i] = pack2(x, y);
@@ -343,10 +343,11 @@ __device__ __forceinline__ void invert(unsigned char* t, const unsigned char* a,
     if (lane < 16) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const bf16 h = __float2bfloat16_rn(x[i]);
+        uint32_t h[2];
+        split2<2>(x[i], 0.f, h);
         unsigned char* p = t + tile_at<64>(w * 16 + i, (w * 16 + c) >> 3) + (c & 7) * 2;
-        *reinterpret_cast<bf16*>(p) = h;
-        *reinterpret_cast<bf16*>(p + kTile) = __float2bfloat16_rn(x[i] - __bfloat162float(h));
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)h[0];
+        *reinterpret_cast<uint16_t*>(p + kTile) = (uint16_t)h[1];
       }
     }
   }

@@ -79,3 +79,83 @@ def test_step_over_its_values(ssd, dtype):
     assert got is ins[2] and torch.equal(got, want) and torch.equal(a, b)
     with pytest.raises(RuntimeError, match="overlaps"):
         ssd.delta_decode_step(*ins, b, out=b.view(dtype).flatten()[:3 * 4 * 70].view(3, 4, 70))
+
+
+TOP = 3.4e38    # finite in fp32, an infinity where it is rounded to bf16
+
+
+def large(dtype, L, where):
+    """Keys and queries along the axes in turn, a weak decay, and one value of TOP (the
+    largest of bf16 for tensors of that type): in v, the initial states or a gradient."""
+    B, H, V, K = 1, 1, 24, 16
+    d = du.inputs(B, L, 1, H, V, K, dtype, seed=110)
+    axes = torch.eye(K)[torch.arange(L) % K].view(B, L, 1, K)
+    d["q"], d["k"] = axes.to(dtype), axes.roll(1, 1).to(dtype).contiguous()
+    d["g"], d["beta"] = torch.full((B, L, H), -1e-3), torch.full((B, L, H), 0.5)
+    dout, df = torch.zeros(B, L, H, V), torch.zeros(B, H, V, K)
+    top = TOP if dtype is F32 else torch.finfo(BF).max
+    if where in ("v", "initial_states"):
+        d["v"].zero_()
+        d["initial_states"].zero_()
+        dout[:, ::7] = 1e-3
+        df.fill_(1e-3)
+    if where == "v":
+        d["v"][0, 5, 0, 3] = top
+    elif where == "initial_states":
+        d["initial_states"][0, 0, 4, 6] = -TOP
+    elif where == "dout":
+        dout[0, L - 4, 0, 2] = top
+    else:
+        df[0, 0, 5, 7] = -TOP
+    return d, dout.to(dtype), df
+
+
+def through(got, ref, dtype, L, what):
+    """A state, or its gradient, that has gone through all chunks: with beta = 1/2 each
+    visit of an axis halves it, so that a chunk of C tokens leaves 2^-(C / 16) of it,
+    by subtracting the rest.  What is subtracted is off by COMPUTE of what the state was
+    before, which is 2^(C / 16) times as much of what it is after, in every chunk."""
+    C = 64 if dtype is BF else 32
+    bound = du.COMPUTE[dtype] * (1 + 2.0 ** (C // 16) * -(-L // C)) * float(ref.norm()) + 1e-30
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), what
+    assert float((got - ref).norm()) <= bound, (what, float((got - ref).norm() / ref.norm()))
+
+
+@pytest.mark.parametrize("dtype,L", [(F32, 40), (F32, 100), (BF, 40), (BF, 150), (BF, 3000)])
+@pytest.mark.parametrize("where", ["v", "initial_states", "dout", "dfinal_states"])
+def test_finite_values_next_to_infinity(ssd, dtype, L, where):
+    """Values that bf16 rounds to an infinity, but fp32 holds, stay finite and keep their
+    bits in the states, their gradients and what is computed of them."""
+    d, dout, df = large(dtype, L, where)
+    if where in ("dout", "dfinal_states"):      # products of two such would overflow
+        d["v"] *= 1e-3
+        d["initial_states"] *= 1e-3
+    ins, kw = split(d)
+    want, fin, grads = du.reference(d, dout, df)
+    assert max(float(t.abs().max()) for t in (fin, *grads.values())) < 3.4028e38
+    out, final, saved = ssd.delta_scan_fwd(*ins, return_final_states=True, save=True, **kw)
+    du.close(out, want, dtype, "out")
+    through(final, fin, dtype, L, "final_states")
+    got = ssd.delta_scan_bwd(dout.cuda(), *ins, saved=saved, dfinal_states=df.cuda(), **kw)
+    for n, ref in grads.items():
+        if n == "d_initial_states":
+            through(got[n], ref, dtype, L, n)
+        else:
+            du.close(got[n], ref, dtype, n)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_infinities_stay_infinite(ssd, dtype):
+    """An infinite state or value is no large finite one."""
+    for where in ("v", "initial_states"):
+        d, _, _ = large(dtype, 100, where)
+        for n in ("v", "initial_states"):
+            d[n][d[n].abs() > 1e30] = float("inf")
+        ins, kw = split(d)
+        out, fin = ssd.delta_scan_fwd(*ins, return_final_states=True, **kw)
+        row = 3 if where == "v" else 4
+        assert not torch.isfinite(fin[0, 0, row]).all()
+        assert not torch.isfinite(out[0, 64:, 0, row]).any()
+        rest = torch.arange(24, device="cuda") != row
+        assert (out[0, :, 0, rest] == 0).all() and (fin[0, 0, rest] == 0).all()
