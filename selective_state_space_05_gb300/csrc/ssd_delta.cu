@@ -102,6 +102,8 @@ cudaError_t pack(const Args& a, const void** src, TokStride* s, int* ncols, int 
   return cudaGetLastError();
 }
 
+size_t state_bytes(const Args& a) { return (size_t)a.B * a.H * a.V * a.K * 4; }
+
 template <typename F>
 void carve_work(Args& a, F take) {
   if (!a.tc) return;
@@ -111,6 +113,7 @@ void carve_work(Args& a, F take) {
                                         : 0;
   a.ctrl = reinterpret_cast<int*>(take((1 + lanes) * sizeof(int)));
   a.slots = reinterpret_cast<float*>(take(slots * 128 * a.KP * 4));
+  a.first = reinterpret_cast<float*>(take(a.pass == kParts ? state_bytes(a) : 0));
 }
 // A few long sequences leave most SMs idle: their segments run all at once, in two
 // passes, where that takes fewer chunks' time than the sequence has chunks.  The first
@@ -410,6 +413,14 @@ int status(int reset, cudaStream_t st, int* bits) {
     if (e == 0) e = w(reset, st, &now);
     *bits |= now;
   }
+  return e;
+}
+
+cudaError_t copy_first(const Args& a, const float** from, const float* to, cudaStream_t st) {
+  if (!to || *from != to) return cudaSuccess;
+  const cudaError_t e =
+      cudaMemcpyAsync(a.first, *from, state_bytes(a), cudaMemcpyDeviceToDevice, st);
+  *from = a.first;
   return e;
 }
 

@@ -81,7 +81,7 @@ struct Args {
   int segs, seg;
   int pass;        // kWhole; or of a few long sequences, kParts and then kJoined
   int* ctrl;
-  float* slots;
+  float *slots, *first;   // first: a copy of the first state (kParts)
   // gradients; per head [B, L, H, dstate] fp32 where heads share queries and keys
   void *dq, *dk;
   float *dg, *dbeta, *dq_part, *dk_part;

@@ -582,6 +582,9 @@ bool token_map(CUtensorMap* m, const void* base, int cols, int rows, int64_t L, 
 
 // After kParts: each segment's first state but the first's, into the slots of W.
 cudaError_t launch_tc_join(const Args& a, cudaStream_t st);
+// Of segments all at once the last one may write its state (to) where the first one
+// still reads (*from): the first state is then taken from a copy.
+cudaError_t copy_first(const Args& a, const float** from, const float* to, cudaStream_t st);
 // Clears a.ctrl for a launch of `grid` CTAs.
 cudaError_t start_work(const Args& a, int* grid, cudaStream_t st);
 

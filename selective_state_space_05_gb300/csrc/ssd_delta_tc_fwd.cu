@@ -378,8 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before_sync();
       warp_arrive(bar, lane);
     };
-    // (segments all at once, with the final states in the initial ones' memory)
-    const bool shared = a.pass == kJoined && a.final && a.final == a.init;
     int c = 0, slots = 0;
     for (int n = 0, k = 0;; ++n, ++c) {
       if (c == it.last) {
@@ -403,13 +401,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int p = 0; p < SP; ++p) put_state(p, c);
         told(&s.s_ready);
-        if (c == 0 && shared) {   // the last segment may write over it
-          warp_arrive(&s.slot_done, lane);
-          if (warp == 0) {
-            W(&s.slot_done, slots++ & 1);
-            if (lane == 0) raise_flag(flag_of(a, it), 1);
-          }
-        }
       }
       const uint32_t ph = n & 1;
       const float* vec = s.vec[ph];
@@ -484,10 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) raise_flag(flag_of(a, it), (c + 1) / a.seg);
         }
       } else {
-        if (shared) {
-          if (lane == 0) wait_flag(flag_of(a, it), 1, &s.gave_up, &g_status);
-          __syncwarp();
-        }
         write_row<SP>(S0, a.final, it.bh, it.v0 + row, part, a);
       }
     }
@@ -609,6 +596,7 @@ cudaError_t launch_tc_forward(const Args& args, cudaStream_t st) {
     f.final = nullptr;
     cudaError_t e = a.KP == 64 ? fwd::run<64, false>(f, st) : fwd::run<128, false>(f, st);
     if (e == cudaSuccess) e = launch_tc_join(f, st);
+    if (e == cudaSuccess) e = copy_first(a, &a.init, a.final, st);
     if (e != cudaSuccess) return e;
     a.pass = kJoined;
   }

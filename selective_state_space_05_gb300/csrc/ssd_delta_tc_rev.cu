@@ -356,8 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_before_sync();
       warp_arrive(bar, lane);
     };
-    // (segments all at once, with the initial states' gradient in the final ones' memory)
-    const bool shared = a.pass == kJoined && a.dinit && a.dinit == a.dfinal;
     int rc = 0, slots = 0;   // the chunk, counted from the end
     for (int n = 0, k = 0;; ++n, ++rc) {
       if (rc == it.last) {
@@ -381,13 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int p = 0; p < SP; ++p) put_state(p, nc - 1 - rc);
         told(&s.s_ready);
-        if (rc == 0 && shared) {   // the last segment may write over it
-          warp_arrive(&s.slot_done, lane);
-          if (warp == 0) {
-            W(&s.slot_done, slots++ & 1);
-            if (lane == 0) raise_flag(flag_of(a, it), 1);
-          }
-        }
       }
       const uint32_t ph = n & 1;
       const float* vec = s.vec[ph];
@@ -453,10 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) raise_flag(flag_of(a, it), (rc + 1) / a.seg);
         }
       } else {
-        if (shared) {
-          if (lane == 0) wait_flag(flag_of(a, it), 1, &s.gave_up, &g_status);
-          __syncwarp();
-        }
         write_row<SP>(dS, a.dinit, it.bh, it.v0 + row, part, a);
       }
     }
@@ -504,6 +491,7 @@ cudaError_t launch_tc_reverse(const Args& args, cudaStream_t st) {
   if (a.pass == kParts) {
     cudaError_t e = a.KP == 64 ? rev::run<64>(a, st) : rev::run<128>(a, st);
     if (e == cudaSuccess) e = launch_tc_join(a, st);
+    if (e == cudaSuccess) e = copy_first(a, &a.dfinal, a.dinit, st);
     if (e != cudaSuccess) return e;
     a.pass = kJoined;
   }
