@@ -590,7 +590,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         float r0 = read(lane), r1 = read(lane + 32);
         const float p0 = put(lane), p1 = put(lane + 32);
         float w0 = p0 * vec[kBeta * kC + lane], w1 = p1 * vec[kBeta * kC + lane + 32];
-        const float mine = warp == 1 ? w0 : w1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float y0 = __shfl_down_sync(0xffffffffu, r0, o);
@@ -609,7 +608,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float r1all = __shfl_sync(0xffffffffu, r1, 0);
         const float w0all = __shfl_sync(0xffffffffu, w0, 31);
         const float from = warp == 1 ? r0 + r1all : r1;
-        const float before = (warp == 1 ? w0 : w0all + w1) - mine;
+        // (what t writes may be large, and is not part of it)
+        float before = __shfl_up_sync(0xffffffffu, warp == 1 ? w0 : w1, 1);
+        if (lane == 0) before = 0.f;
+        if (warp == 2) before += w0all;
         if (t < rows) {
           const int64_t at = ((int64_t)b * a.L + (int64_t)c * kC + t) * a.H + h;
           a.dbeta[at] = (warp == 1 ? p0 : p1) + s.total[t];

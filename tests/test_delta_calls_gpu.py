@@ -159,3 +159,25 @@ def test_infinities_stay_infinite(ssd, dtype):
         assert not torch.isfinite(out[0, 64:, 0, row]).any()
         rest = torch.arange(24, device="cuda") != row
         assert (out[0, :, 0, rest] == 0).all() and (fin[0, 0, rest] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("at", [1, 40])
+def test_decays_beside_a_large_write(ssd, dtype, at):
+    """A token whose own write into the final state weighs 2^27 times as much as all
+    before it: its decay's gradient is of those before it alone.  Along two axes, in
+    powers of two: every product and sum is exact."""
+    L = at + 1
+    q, k = torch.zeros(1, L, 1, 16), torch.zeros(1, L, 1, 16)
+    v, df = torch.zeros(1, L, 1, 8), torch.zeros(1, 1, 8, 16)
+    k[0, 0, 0, 0], k[0, at, 0, 1] = 1, 1
+    v[0, 0, 0, 0], v[0, at, 0, 0] = 1, 1
+    df[0, 0, 0, 0], df[0, 0, 0, 1] = 1, 2.0 ** 27
+    g, beta = torch.zeros(1, L, 1), torch.ones(1, L, 1)
+    d = dict(q=q, k=k, v=v, g=g, beta=beta, initial_states=None, seq_idx=None)
+    _, _, want = du.reference(d, torch.zeros_like(v), df)
+    ins = tuple(d[n].to(dtype if n in "qkv" else F32).cuda() for n in du.NAMES)
+    got = ssd.delta_scan_bwd(torch.zeros_like(ins[2]), *ins, dfinal_states=df.cuda())
+    assert (want["dg"][0, 1:] == 1).all() and want["dg"][0, 0] == 0
+    for n in ("dg", "dbeta", "dv"):
+        assert torch.equal(got[n].double().cpu(), want[n]), n
