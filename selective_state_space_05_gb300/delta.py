@@ -139,8 +139,8 @@ def delta_scan_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     _chk(dout, "dout", xd, (B, L, H, V), dev)
     if dfinal_states is not None:
         _chk(dfinal_states, "dfinal_states", _F32, (B, H, V, K), dev)
-    if saved is not None:
-        _need(saved, "saved", torch.uint8, device=dev)
+    if saved is not None:   # (of any type, as a workspace)
+        _need(saved, "saved", device=dev)
     st = _stream_of(stream, dev)
     ws, ws_bytes, hold = _workspace(
         _call("ssd_delta_scan_bwd_workspace_bytes")(
@@ -153,7 +153,7 @@ def delta_scan_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
                  else _empty((B, H, V, K), _F32, dev, stream))
     code = _call("ssd_delta_scan_bwd")(
         dout.data_ptr(), _ptr(dfinal_states), *args, B, L, H, V, K, G, dt, _ptr(saved),
-        0 if saved is None else saved.numel(), *map(_ptr, grads.values()), ws, ws_bytes, st)
+        0 if saved is None else saved.numel() * saved.element_size(), *map(_ptr, grads.values()), ws, ws_bytes, st)
     if code:
         _lib.check(code)
     return grads

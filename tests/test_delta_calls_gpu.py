@@ -181,3 +181,20 @@ def test_decays_beside_a_large_write(ssd, dtype, at):
     assert (want["dg"][0, 1:] == 1).all() and want["dg"][0, 0] == 0
     for n in ("dg", "dbeta", "dv"):
         assert torch.equal(got[n].double().cpu(), want[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_workspace_of_another_type_is_kept(ssd, dtype):
+    """What the forward returns with save is what the backward takes, when it is the
+    caller's own workspace too."""
+    ins, kw = split(du.inputs(1, 100, 1, 2, 40, 48, dtype, seed=120))
+    out, own = ssd.delta_scan_fwd(*ins, save=True, **kw)
+    dout = torch.ones_like(out)
+    want = ssd.delta_scan_bwd(dout, *ins, saved=own, **kw)
+    ws = torch.empty(-(-own.numel() // 4), device="cuda")
+    _, saved = ssd.delta_scan_fwd(*ins, save=True, workspace=ws, **kw)
+    assert saved is ws
+    got = ssd.delta_scan_bwd(dout, *ins, saved=saved, **kw)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    with pytest.raises(RuntimeError, match="WORKSPACE"):
+        ssd.delta_scan_bwd(dout, *ins, saved=saved[:-64], **kw)
