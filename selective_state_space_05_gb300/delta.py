@@ -161,9 +161,9 @@ def delta_scan_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
 
 class _DeltaScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, initial_states, seq_idx, scale):
+    def forward(ctx, q, k, v, g, beta, initial_states, seq_idx, scale, grad):
         ctx.set_materialize_grads(False)
-        keep = any(ctx.needs_input_grad)
+        keep = grad and any(ctx.needs_input_grad)   # (set for leaves without grad mode too)
         ctx.empty = q.dim() == v.dim() == 4 and q.shape[0] * q.shape[1] == 0
         if ctx.empty:   # no token: answered without a launch (the explicit calls refuse it)
             _, (B, _, H, V, K, _), _, dev = _inputs(q, k, v, g, beta, scale, initial_states, seq_idx)
@@ -187,14 +187,14 @@ class _DeltaScan(torch.autograd.Function):
             if init is not None and dfinal is None:
                 dfinal = torch.zeros_like(init)
             return (*(t.new_empty(t.shape) for t in ins), None if init is None else dfinal, None,
-                    None)
+                    None, None)
         q, k, v, g, beta, init, seq_idx, saved = ctx.saved_tensors
         dout = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if dout is None \
             else dout.contiguous()
         d = delta_scan_bwd(dout, q, k, v, g, beta, scale=ctx.scale, initial_states=init,
                            seq_idx=seq_idx, saved=saved,
                            dfinal_states=None if dfinal is None else dfinal.contiguous())
-        return (*d.values(), None, None)
+        return (*d.values(), None, None, None)
 
 
 def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -204,7 +204,8 @@ def delta_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     """delta_scan_fwd as a differentiable torch function: gradients for q, k,
     v, g, beta and initial_states, through out and the final states.  Returns
     out, or (out, final_states)."""
-    out, final = _DeltaScan.apply(q, k, v, g, beta, initial_states, seq_idx, scale)
+    out, final = _DeltaScan.apply(q, k, v, g, beta, initial_states, seq_idx, scale,
+                                  torch.is_grad_enabled())
     return (out, final) if return_final_states else out
 
 
