@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import delta_testutil as du
+from test_delta_gpu import check
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -198,3 +199,13 @@ def test_a_workspace_of_another_type_is_kept(ssd, dtype):
     assert all(torch.equal(got[n], want[n]) for n in want)
     with pytest.raises(RuntimeError, match="WORKSPACE"):
         ssd.delta_scan_bwd(dout, *ins, saved=saved[:-64], **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,L,G,H,V,K", [
+    (1, 70, 2, 2, 257, 40), (1, 130, 1, 2, 384, 100), (2, 200, 30, 60, 384, 16),
+    (2, 129, 40, 40, 300, 70), (1, 65, 1, 2, 2048, 16), (1, 130, 2, 2, 2048, 128)])
+def test_wide_heads(ssd, dtype, B, L, G, H, V, K):
+    """More than two blocks of 128 channels, up to the most that is taken; a chunk a CTA
+    and several."""
+    check(ssd, du.inputs(B, L, G, H, V, K, dtype, seed=V + K), dtype)
