@@ -310,7 +310,8 @@ __device__ __forceinline__ float2 tile_pair(const unsigned char* base, uint32_t 
 // ------------------------------------------------------------------ launches
 // (each returns the launch's error; the first four: fp32)
 cudaError_t launch_prepare(const Args& a, cudaStream_t st);
-// out and final may be null; S0 and X are written where they are given
+// out (a backward that runs the forward again) and final may be null; S0 and X are written
+// where they are given
 cudaError_t launch_forward(const Args& a, cudaStream_t st);
 cudaError_t launch_reverse(const Args& a, cudaStream_t st);
 cudaError_t launch_grads(const Args& a, cudaStream_t st);

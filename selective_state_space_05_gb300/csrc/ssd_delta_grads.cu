@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   using S = GradSmem<KP>;
   constexpr int C = S::C, NT = S::M::NT, TI = S::M::TI, RG = S::RG, CG = S::CG;
   constexpr int NW = KP / CG / 16;                     // 16-column blocks of a warp's results
-  constexpr int PB = RG / CG > 0 ? RG / CG : 1;        // 16-column blocks of its pair matrices
+  static_assert(RG <= CG, "a warp has one 16-column block of the pair matrices: cg's");
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3, rg = warp % RG, cg = warp / RG;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   load_channels<KP>(a, base + S::st, b, h, id, t0, rows, 0, tid);
   cp_commit();
 
-  float dq[2 * NW][4], dk[2 * NW][4], w0[2 * NW][4], dp[2 * PB][4], da[2 * PB][4];
+  float dq[2 * NW][4], dk[2 * NW][4], w0[2 * NW][4], dp[2][4], da[2][4];
   zero(dq);
   zero(dk);
   zero(w0);
@@ -140,13 +140,11 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
         mma_apart<NT, NT, true>(w0[2 * n], w0[2 * n + 1], fx,
                                block_at<KP>(st + S::ds, ks * 16, col, lane), S::kState);
       }
-#pragma unroll
-      for (int n = 0; n < PB; ++n)
-        if (cg * PB + n <= rg) {
-          const uint32_t xt = blockn_at<kVT>(st + S::x, (cg * PB + n) * 16, ks * 16, lane);
-          mma_apart<TI, NT, false>(dp[2 * n], dp[2 * n + 1], fd, xt, S::kTok);
-          mma_apart<NT, NT, false>(da[2 * n], da[2 * n + 1], fy, xt, S::kTok);
-        }
+      if (cg <= rg) {
+        const uint32_t xt = blockn_at<kVT>(st + S::x, cg * 16, ks * 16, lane);
+        mma_apart<TI, NT, false>(dp[0], dp[1], fd, xt, S::kTok);
+        mma_apart<NT, NT, false>(da[0], da[1], fy, xt, S::kTok);
+      }
     }
     for (int i = tid; i < kVT * KP / 2; i += kGradThreads) {
       const int r = i / (KP / 2), col = i % (KP / 2) * 2;
@@ -194,7 +192,7 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
   if (lane == 0) part[warp] = inner;
 
   // the chunk's scores again, for the pairs' gradients
-  float qk[2 * PB][4], kk[2 * PB][4];
+  float qk[2][4], kk[2][4];
   zero(qk);
   zero(kk);
 #pragma unroll 2
@@ -205,22 +203,20 @@ __global__ void __launch_bounds__(kGradThreads) grads_kernel(const Args a) {
       ldsm(fq[i], block_at<KP>(base + S::q + i * S::kPlane, rg * 16, ks * 16, lane));
       ldsm(fk[i], block_at<KP>(base + S::k + i * S::kPlane, rg * 16, ks * 16, lane));
     }
-#pragma unroll
-    for (int n = 0; n < PB; ++n)
-      if (cg * PB + n <= rg) {
-        const uint32_t kt = blockn_at<KP>(base + S::k, (cg * PB + n) * 16, ks * 16, lane);
-        mma_apart<TI, TI, false>(qk[2 * n], qk[2 * n + 1], fq, kt, S::kPlane);
-        mma_apart<TI, TI, false>(kk[2 * n], kk[2 * n + 1], fk, kt, S::kPlane);
-      }
+    if (cg <= rg) {
+      const uint32_t kt = blockn_at<KP>(base + S::k, cg * 16, ks * 16, lane);
+      mma_apart<TI, TI, false>(qk[0], qk[1], fq, kt, S::kPlane);
+      mma_apart<TI, TI, false>(kk[0], kk[1], fk, kt, S::kPlane);
+    }
   }
   __syncthreads();   // the tiles' memory is M1's, M2's and H's from here
   float* const hm = reinterpret_cast<float*>(smem + S::hm);
 #pragma unroll
-  for (int n = 0; n < 2 * PB; ++n) {
-    if (cg * PB + n / 2 > rg) continue;
+  for (int n = 0; n < 2; ++n) {
+    if (cg > rg) continue;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int i = rg * 16 + g + 8 * r, j = cg * PB * 16 + n * 8 + t * 2;
+      const int i = rg * 16 + g + 8 * r, j = cg * 16 + n * 8 + t * 2;
       float u1[2], u2[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {

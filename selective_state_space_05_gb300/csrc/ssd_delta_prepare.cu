@@ -5,9 +5,8 @@
 //   - G, the running sum of g in 64 bits, kept as two floats, so that the decays
 //     e^(G_i - G_j) of late tokens do not lose bits to strong earlier ones;
 //   - k k^T and q k^T on the tensor cores (lower triangles);
-//   - T = (I + N diag(beta))^-1 in fp32: the 16 x 16 blocks of the diagonal by
-//     substitution, a column a lane, then the blocks below them as
-//     -T_ii A_ij T_jj, doubling the side twice.
+//   - T = (I + N diag(beta))^-1 in fp32: the two 16 x 16 blocks of the diagonal by
+//     substitution, a column a lane, then the one below them as -T_11 A_10 T_00.
 // T and P are written as bf16 terms, the vectors as fp32.  Bound by the latency of
 // the substitution and of the block products in one CTA, of which four or so share an
 // SM: 600 chunks of 72 columns in 14.6 us, a twenty-fifth of the call.
@@ -20,16 +19,15 @@ namespace delta {
 
 constexpr int kPrepThreads = 128;
 
-// dst = sgn a b for N x N blocks in fp32 (row strides LD), 128 threads; 2 x 2
-// outputs a thread and pass.
-template <int N, int LD>
+// dst = sgn a b for 16 x 16 blocks in fp32 (row strides LD); 2 x 2 outputs a thread.
+template <int LD>
 __device__ __forceinline__ void block_product(float* dst, const float* a, const float* b, float sgn,
-                                              int tid, int nth) {
-  for (int o = tid; o < N * N / 4; o += nth) {
-    const int r = o / (N / 2) * 2, c = o % (N / 2) * 2;
+                                              int tid) {
+  if (tid < 64) {
+    const int r = tid / 8 * 2, c = tid % 8 * 2;
     float s00 = 0.f, s01 = 0.f, s10 = 0.f, s11 = 0.f;
 #pragma unroll 8
-    for (int k = 0; k < N; ++k) {
+    for (int k = 0; k < 16; ++k) {
       const float x0 = a[r * LD + k], x1 = a[(r + 1) * LD + k];
       const float y0 = b[k * LD + c], y1 = b[k * LD + c + 1];
       s00 = fmaf(x0, y0, s00);
@@ -48,6 +46,7 @@ template <int KP>
 __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
   using M = Mode<float>;
   constexpr int C = M::C, NT = M::NT, TI = M::TI;
+  static_assert(C == 32, "a token a lane, two blocks a side");
   constexpr int LD = C + 2;                    // of the fp32 matrices
   constexpr uint32_t kPlane = C * KP * 2;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -70,75 +69,47 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
   load_tile<KP, C>(saddr(tq), kPlane,
                    static_cast<const float*>(a.q) + toff(a.sq, b, t0) + (int64_t)kg * a.K, a.sq.t, rows,
                    a.K, a.wide_q, tid, kPrepThreads);
-  cp_commit();
-  if (warp == 0) {   // the vectors: C / 32 neighbouring tokens a lane
-    constexpr int E = C / 32;
-    double s[E];
-    int seg[E];
-    float be[E];
-    double run = 0.0;
-    int cnt = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int64_t t = t0 + lane * E + e;
-      float g = 0.f;
-      int reset = 0;
-      be[e] = 0.f;
-      if (t < a.L) {
-        const int64_t at = ((int64_t)b * a.L + t) * a.H + h;
-        g = a.g[at];
-        be[e] = a.beta[at];
-        if (g < kReset) {
-          g = 0.f;
-          reset = 1;
-        }
-        if (a.seq && t > 0) {
-          const int32_t* q = a.seq + (int64_t)b * a.L + t;
-          if (q[0] != q[-1]) reset = 1;
-        }
+  if (warp == 0) {   // the vectors: a token a lane
+    const int i = lane;
+    const int64_t t = t0 + i;
+    float g = 0.f, be = 0.f;
+    int sg = 0;   // resets so far
+    if (t < a.L) {
+      const int64_t at = ((int64_t)b * a.L + t) * a.H + h;
+      g = a.g[at];
+      be = a.beta[at];
+      if (g < kReset) {
+        g = 0.f;
+        sg = 1;
       }
-      run += (double)g;
-      cnt += reset;
-      s[e] = run;
-      seg[e] = cnt;
+      if (a.seq && t > 0) {
+        const int32_t* q = a.seq + (int64_t)b * a.L + t;
+        if (q[0] != q[-1]) sg = 1;
+      }
     }
-    double before = run;
-    int cbefore = cnt;
+    double G = (double)g;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const double v = __shfl_up_sync(0xffffffffu, before, off);
-      const int n = __shfl_up_sync(0xffffffffu, cbefore, off);
+      const double v = __shfl_up_sync(0xffffffffu, G, off);
+      const int n = __shfl_up_sync(0xffffffffu, sg, off);
       if (lane >= off) {
-        before += v;
-        cbefore += n;
+        G += v;
+        sg += n;
       }
     }
-    const double total = __shfl_sync(0xffffffffu, before, 31);
-    const int segs = __shfl_sync(0xffffffffu, cbefore, 31);
-    before = __shfl_up_sync(0xffffffffu, before, 1);
-    cbefore = __shfl_up_sync(0xffffffffu, cbefore, 1);
-    if (lane == 0) {
-      before = 0.0;
-      cbefore = 0;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = lane * E + e;
-      const double G = before + s[e];
-      const int sg = cbefore + seg[e];
-      const float hi = (float)G;
-      vec[kGam * C + i] = sg == 0 ? expf(hi) : 0.f;
-      vec[kOnto * C + i] = sg == segs ? expf((float)(total - G)) : 0.f;
-      vec[kBeta * C + i] = be[e];
-      vec[kRead * C + i] = -vec[kGam * C + i];
-      vec[kWrite * C + i] = be[e] * vec[kOnto * C + i];
-      vec[kGhi * C + i] = hi;
-      vec[kGlo * C + i] = (float)(G - (double)hi);
-      vec[kSeg * C + i] = (float)sg;
-    }
+    const double total = __shfl_sync(0xffffffffu, G, 31);
+    const int segs = __shfl_sync(0xffffffffu, sg, 31);
+    const float hi = (float)G;
+    vec[kGam * C + i] = sg == 0 ? expf(hi) : 0.f;
+    vec[kOnto * C + i] = sg == segs ? expf((float)(total - G)) : 0.f;
+    vec[kBeta * C + i] = be;
+    vec[kRead * C + i] = -vec[kGam * C + i];
+    vec[kWrite * C + i] = be * vec[kOnto * C + i];
+    vec[kGhi * C + i] = hi;
+    vec[kGlo * C + i] = (float)(G - (double)hi);
+    vec[kSeg * C + i] = (float)sg;
     if (lane == 0) vec[kVecs * C] = segs == 0 ? expf((float)total) : 0.f;
   }
-  cp_wait<0>();
   __syncthreads();
   float* const gvec = a.vec + id * vec_floats<C>();
   for (int i = tid; i < kVecs * C + 1; i += kPrepThreads) gvec[i] = vec[i];
@@ -207,24 +178,11 @@ __global__ void __launch_bounds__(kPrepThreads) prepare_kernel(const Args a) {
     }
   }
   __syncthreads();
-  // pairs of 16 (64 threads a pair where there are two), then of 32
-  constexpr int kTeam = kPrepThreads / (C / 32);
-  {
-    const int r = tid / kTeam * 32, ti = tid % kTeam;
-    block_product<16, LD>(Y + (r + 16) * LD, A + (r + 16) * LD + r, Tm + r * LD + r, 1.f, ti, kTeam);
-    __syncthreads();
-    block_product<16, LD>(Tm + (r + 16) * LD + r, Tm + (r + 16) * LD + r + 16, Y + (r + 16) * LD,
-                          -1.f, ti, kTeam);
-    // above the diagonal blocks of 32
-    for (int o = ti; o < 256; o += kTeam) Tm[(r + o / 16) * LD + r + 16 + o % 16] = 0.f;
-  }
+  // the block below them (what is above them is not read)
+  block_product<LD>(Y + 16 * LD, A + 16 * LD, Tm, 1.f, tid);
   __syncthreads();
-  if constexpr (C == 64) {
-    block_product<32, LD>(Y, A + 32 * LD, Tm, 1.f, tid, kPrepThreads);
-    __syncthreads();
-    block_product<32, LD>(Tm + 32 * LD, Tm + 32 * LD + 32, Y, -1.f, tid, kPrepThreads);
-    __syncthreads();
-  }
+  block_product<LD>(Tm + 16 * LD, Tm + 16 * LD + 16, Y + 16 * LD, -1.f, tid);
+  __syncthreads();
   bf16* const gT = a.T + id * NT * C * C;
   for (int o = tid; o < C * C / 2; o += kPrepThreads) {
     const int i = o / (C / 2), j = o % (C / 2) * 2;

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) reverse_kernel(const Args a) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nw = (blockDim.x >> 5) - kLoadWarps;   // those with rows
-  // the loading threads: the warps behind them, or all
+  // the loading threads: the warps behind them
   const int ltid = tid - nw * 32;
   constexpr int nth = kLoadWarps * 32;
   const int t = lane & 3;
