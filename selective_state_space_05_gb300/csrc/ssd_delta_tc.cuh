@@ -12,6 +12,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "ssd_delta.cuh"
 #include "tc_ptx.cuh"
 
@@ -588,10 +590,13 @@ cudaError_t copy_first(const Args& a, const float** from, const float* to, cudaS
 // Clears a.ctrl for a launch of `grid` CTAs.
 cudaError_t start_work(const Args& a, int* grid, cudaStream_t st);
 
-// A device's status word (after the stream's work), cleared if asked.
+// A device's status word (after the stream's work), cleared if asked.  Each word is a
+// copy and a wait of 10 us, which processes that never launched its kernels are spared.
 template <typename W>
-int read_status(W& word, int reset, cudaStream_t st, int* bits) {
+int read_status(W& word, const std::atomic<bool>& launched, int reset, cudaStream_t st, int* bits) {
   int h = 0;
+  *bits = 0;
+  if (!launched.load()) return 0;
   cudaError_t e = cudaMemcpyFromSymbolAsync(&h, word, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && reset && h != 0) {

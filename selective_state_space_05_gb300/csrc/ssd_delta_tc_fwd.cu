@@ -58,6 +58,7 @@ struct Smem {
 };
 
 __device__ int g_status;
+std::atomic<bool> g_launched{false};
 
 template <int KP, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -507,6 +508,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   int grid = 0;
   e = start_work(a, &grid, st);
   if (e != cudaSuccess) return e;
+  g_launched = true;
   tc_forward_kernel<KP, KEEP><<<grid, kThreads, smem, st>>>(mq, mk, mv, mo, a);
   return cudaGetLastError();
 }
@@ -517,7 +519,7 @@ static_assert(sizeof(Smem<128, false>) + 1024 <= 227 * 1024 &&
 
 // Status bits of the launches that gave up a wait (host; ssd_scan_status).
 int tc_forward_status(int reset, cudaStream_t st, int* bits) {
-  return read_status(fwd::g_status, reset, st, bits);
+  return read_status(fwd::g_status, fwd::g_launched, reset, st, bits);
 }
 
 // S <- S M + W from segment to segment, eight rows a CTA, in fp32: a thread has four

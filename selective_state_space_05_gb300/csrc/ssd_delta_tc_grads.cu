@@ -60,6 +60,7 @@ struct Smem {
 };
 
 __device__ int g_status;
+std::atomic<bool> g_launched{false};
 
 // D (+)= A B over STEPS steps of 16 along K: descriptors and what a step adds.
 template <int STEPS>
@@ -650,6 +651,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t chunks = (int64_t)a.B * a.H * a.nc;
   const int grid = (int)(chunks < row::sm_count() ? chunks : row::sm_count());
+  g_launched = true;
   tc_grads_kernel<KP><<<grid, kThreads, smem, st>>>(mq, mk, md, moq, mok, tma_out, a);
   return cudaGetLastError();
 }
@@ -658,7 +660,7 @@ static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
 }  // namespace grd
 
 int tc_grads_status(int reset, cudaStream_t st, int* bits) {
-  return read_status(grd::g_status, reset, st, bits);
+  return read_status(grd::g_status, grd::g_launched, reset, st, bits);
 }
 cudaError_t launch_tc_grads(const Args& a, cudaStream_t st) {
   const cudaError_t e = a.KP == 64 ? grd::run<64>(a, st) : grd::run<128>(a, st);

@@ -29,6 +29,7 @@ struct Smem {
   volatile int gave_up;
 };
 __device__ int g_status;
+std::atomic<bool> g_launched{false};
 
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -99,6 +100,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(
       tc_prepare_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  g_launched = true;
   tc_prepare_kernel<KP><<<(unsigned)((int64_t)a.B * a.H * a.nc), kThreads, smem, st>>>(mq, mk, a);
   return cudaGetLastError();
 }
@@ -106,7 +108,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
 }  // namespace prep
 
 int tc_prepare_status(int reset, cudaStream_t st, int* bits) {
-  return read_status(prep::g_status, reset, st, bits);
+  return read_status(prep::g_status, prep::g_launched, reset, st, bits);
 }
 cudaError_t launch_tc_prepare(const Args& a, cudaStream_t st) {
   return a.KP == 64 ? prep::run<64>(a, st) : prep::run<128>(a, st);

@@ -44,6 +44,7 @@ struct Smem {
 };
 
 __device__ int g_status;
+std::atomic<bool> g_launched{false};
 
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -476,6 +477,7 @@ cudaError_t run(const Args& a, cudaStream_t st) {
   int grid = 0;
   e = start_work(a, &grid, st);
   if (e != cudaSuccess) return e;
+  g_launched = true;
   tc_reverse_kernel<KP><<<grid, kThreads, smem, st>>>(mq, mk, md, mv, a);
   return cudaGetLastError();
 }
@@ -484,7 +486,7 @@ static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory");
 }  // namespace rev
 
 int tc_reverse_status(int reset, cudaStream_t st, int* bits) {
-  return read_status(rev::g_status, reset, st, bits);
+  return read_status(rev::g_status, rev::g_launched, reset, st, bits);
 }
 cudaError_t launch_tc_reverse(const Args& args, cudaStream_t st) {
   Args a = args;
