@@ -15,9 +15,16 @@
  * arguments validated before anything is launched, no host synchronisation, no
  * atomics on values (equal inputs give equal bits).  "x dtype" is the dtype
  * argument, fp32 or bf16; every sum, the states and the decays are held in
- * fp32 or more, and each output is rounded once.  Pointers are aligned to their
- * element (dq and dk to two; rows on 16 bytes take wide accesses), the workspace to
- * 256 bytes.  An output (and the workspace) may share no memory with an input or
+ * fp32 or more, and each output is rounded once.  The tensor cores' factors that are
+ * computed (the state, the corrections u, the chunks' matrices, their gradients)
+ * enter the products as sums of bf16 terms: three for fp32 tensors, whose results are
+ * off by 1e-7 to 6e-7 of their norm as fp32 arithmetic is; two for bf16 ones, 2^-18
+ * of a factor, and so is what the workspace keeps for the backward.  With bf16
+ * tensors the fp32 results (final_states, dg, dbeta, d_initial_states) are therefore
+ * off by 2e-6 to 6e-6 of their norm: far less than the tensors' own rounding, but not
+ * an fp32 computation's, which the same values as fp32 tensors give.
+ * Pointers are aligned to their element (dq and dk to two; rows on 16 bytes take wide
+ * accesses), the workspace to 256 bytes.  An output (and the workspace) may share no memory with an input or
  * another output, but final_states may be initial_states, d_initial_states may be
  * dfinal_states, and the step's out its v: others are refused (SSD_ERR_ARG).
  *
@@ -31,15 +38,17 @@
  *                 -104 (exp is 0 in fp32) the state starts anew, and g has no
  *                 gradient there
  *   seq_idx       [batch, seqlen] int32 or NULL: the state is set to zero before
- *                 token t whenever seq_idx[b,t] != seq_idx[b,t-1]
+ *                 token t whenever seq_idx[b,t] != seq_idx[b,t-1] (times a decay of
+ *                 0: a state that is not finite stays so)
  *   initial_states, final_states  [batch, nheads, headdim, dstate] float
  * Sizes: dstate in [1, 128], headdim in [1, 2048], nheads a multiple of ngroups,
  * batch * nheads * chunks < 2^31 (chunks of 64 tokens for bf16, 32 for fp32).
  * Keys of unit length (and beta in [0, 2]) keep the recurrence stable; the call
  * does not normalise them.  An infinity or NaN spreads, as in any chunked form,
- * to its chunk's other tokens of its head, and to those after it.  Finite values do
- * not count as such up to the end of the fp32 range, but for a bf16 dv that rounds to
- * an infinity: the other gradients of its chunk are then not finite.
+ * to its chunk's other tokens of its head, and to those after it, past starts of
+ * documents too (its products with zeros are NaN).  Finite values do not count as such
+ * up to the end of the fp32 range, but for a bf16 dv that rounds to an infinity: the
+ * other gradients of its chunk are then not finite.
  */
 #ifndef SSD_DELTA_H
 #define SSD_DELTA_H

@@ -10,9 +10,10 @@
 // warps load and split one chunk ahead; one barrier a chunk is all that the warps
 // wait for each other.  The write into S is summed apart from S and added with one
 // rounding, since the tensor cores' sums truncate and S lives for many chunks.
-// Bound by a warp's own chain of products (six mma a pair of factors, one warp a
-// quadrant): 24 sequences of 25 chunks, 64 channels and 72 columns take 144 us, 5.8
-// a chunk.  Columns past dstate are not multiplied, which is 3/8 of them there.
+// Bound by a warp's own chain of products, six mma a pair of factors.  24 sequences of 25
+// chunks, 64 channels and 72 columns take 144 us, 5.8 a chunk: with fewer heads than SMs a
+// CTA has one warp with rows, so that 96 SMs have one such warp each, and one quadrant of
+// the four at work.  Columns past dstate are not multiplied, which is 3/8 of them there.
 #include "ssd_delta_seq.cuh"
 
 namespace ssd {

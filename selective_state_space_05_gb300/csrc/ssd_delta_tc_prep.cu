@@ -5,9 +5,9 @@
 // time between them.  T's and P's terms go out as swizzled tiles, which the chunks'
 // kernels copy as they are.  (As a role of the forward's own CTAs this work was in its
 // chunks' way: 1.16 ms for the two against 0.94 apart.)
-// 20480 chunks of 128 columns take 277 us, 3.4 TB/s with what goes out: bound by the
-// warps' latency, four CTAs an SM, which is why decays and terms are computed two
-// values an instruction (323 us before).
+// 20480 chunks of 128 columns take 277 us for 66 KB each, in and out, 5.0 TB/s: half of it
+// is T and P on their way to the chunks' kernels.  Four CTAs an SM: their warps' latency
+// counts too (323 us before decays and terms were computed two values an instruction).
 #include "ssd_delta_tc.cuh"
 
 namespace ssd {

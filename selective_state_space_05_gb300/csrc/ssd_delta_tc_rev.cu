@@ -1,6 +1,7 @@
 // The gated delta rule's backward along the sequence on tcgen05, last chunk first:
-// one CTA per SM, each at one (batch row, head, 128 channels), transposed as the
-// forward, with the state's gradient dS in registers and as two bf16 terms in TMEM.
+// one CTA per SM, which takes (segment, head, 128 channels) items by tickets as the
+// forward's do, transposed as there, with the state's gradient dS in registers and as two
+// bf16 terms in TMEM.
 // Per chunk:
 //   Z = dS K^T                                A: dS
 //   dx = beta e^(G_C - G) Z + do P -> TMEM     (do P ahead: A: do, one term)

@@ -85,7 +85,8 @@ def delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     fp32 or bf16, may be strided views whose tokens are dense; g (the decay's
     logarithm) and beta [batch, seqlen, nheads] fp32; states [batch, nheads,
     headdim, dstate] fp32; seq_idx [batch, seqlen] int32; scale defaults to
-    dstate ** -0.5.  Returns out, or a tuple of out, with return_final_states
+    dstate ** -0.5.  With bf16 tensors the fp32 results are off by 2e-6 to 6e-6 of
+    their norm (two bf16 terms a factor; include/ssd_delta.h).  Returns out, or a tuple of out, with return_final_states
     the final states, and with save what delta_scan_bwd takes as `saved` (the
     workspace, which then must not be used for anything else).  final_states may
     be initial_states; otherwise outputs share no memory with inputs."""
