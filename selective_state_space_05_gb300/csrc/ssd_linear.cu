@@ -294,6 +294,7 @@ struct Gemm {
   int splits, steps_per_split;   // splits of K each, joined afterwards where splits > 1
   int bn;             // tile width, a multiple of 32 up to 256
   int stages;         // operand tiles in flight
+  int tx;             // bytes that a stage's loads bring
   int group_m;        // tiles of M walked together (L2 reuse)
   int run;            // K steps an accumulator takes before it is added to the registers',
   int lead;           // except for the first `lead` steps, the small products of planes:
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(CG, 1, 1)
         if (!ok) break;
         if (tc::elect_one()) {
           if (rank == 0)
-            tc::mbar_arrive_expect_tx(&s.full[st], CG * stage);
+            tc::mbar_arrive_expect_tx(&s.full[st], p.tx);
           const uint32_t bar = CG == 2 ? tc::mapa(&s.full[st], 0) : 0;
           unsigned char* at = s.operands + st * stage;
           load_tile<CG, kBM, AMN>(at, &ma, &s.full[st], bar, kBM, (tm * CG + rank) * kBM, kk, pa);
@@ -1286,19 +1287,15 @@ struct Operand {
   int planes;
 };
 
-// box: kBK x tile rows of a K-major operand, 64 x kBK of an MN-major one.
+// box: kBK x tile rows of a K-major operand, 64 x kBK of an MN-major one.  The map is
+// of the operand's own memory and no more: with a second plane declared behind a small
+// one, that no load's coordinates reached, launches faulted where nothing was mapped there.
 bool make_map(CUtensorMap* m, const Operand& o, bool mn, int tile_rows) {
   auto enc = encode_fn();
   if (!enc) return false;
-  // Loads from a map of less than 128 KB are slower (M = 17, K = 2560, N = 10576:
-  // 31 us instead of 24), so a small operand's map is given a second plane past
-  // that size, which no load's coordinates reach.
-  const bool small = o.planes == 1 && o.rows * o.ld * 2 < 131072;
-  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows,
-                              (cuuint64_t)(small ? 2 : o.planes)};
-  const cuuint64_t strides[2] = {
-      (cuuint64_t)o.ld * 2,
-      (cuuint64_t)(small ? 131072 : o.planes > 1 ? o.rows * o.ld * 2 : o.ld * 2)};
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2,
+                                 (cuuint64_t)(o.planes > 1 ? o.rows * o.ld * 2 : o.ld * 2)};
   const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? kBK : tile_rows), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p), dims, strides, box, es,
@@ -1412,7 +1409,12 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   const int pairs = a.planes == 3 ? 6 : 1;
   const Plan pl = plan_for(M, N, K, pairs, bmn);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a, amn, kBM) || !make_map(&mb, b, bmn, rows_b(pl.cg, pl.bn, bmn)))
+  // A few rows are loaded without those behind them, whose place in the tile keeps what
+  // it has: they are rows of the result that are not stored.  (Rows past the end of a
+  // small operand are slow to be filled with zeros: 17 x 2560 -> 10576 takes 24 us with
+  // 128 of them loaded, 14.6 with 24.)
+  const int rows_a = !amn && M < kBM ? (int)((M + 7) / 8 * 8) : kBM;
+  if (!make_map(&ma, a, amn, rows_a) || !make_map(&mb, b, bmn, rows_b(pl.cg, pl.bn, bmn)))
     return bad(SSD_ERR_CUDA, "linear: a tensor map could not be made");
   Gemm g = {};
   g.M = M;
@@ -1425,6 +1427,7 @@ int gemm(const Operand& a, bool amn, const Operand& b, bool bmn, int64_t M, int6
   g.splits = pl.splits;
   g.steps_per_split = pl.steps_per;
   g.bn = pl.bn;
+  g.tx = pl.cg * (rows_a * kBK * 2 + stage_b(pl.cg, pl.bn, bmn));
   g.stages = std::min(kMaxStages, kOperandBytes / (kStageA + stage_b(pl.cg, pl.bn, bmn)));
   g.group_m = 8 / pl.cg;
   // runs of the longest item's K steps
