@@ -85,11 +85,12 @@ def delta_scan_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     fp32 or bf16, may be strided views whose tokens are dense; g (the decay's
     logarithm) and beta [batch, seqlen, nheads] fp32; states [batch, nheads,
     headdim, dstate] fp32; seq_idx [batch, seqlen] int32; scale defaults to
-    dstate ** -0.5.  With bf16 tensors the fp32 results are off by 2e-6 to 6e-6 of
-    their norm (two bf16 terms a factor; include/ssd_delta.h).  Returns out, or a tuple of out, with return_final_states
+    dstate ** -0.5.  Returns out, or a tuple of out, with return_final_states
     the final states, and with save what delta_scan_bwd takes as `saved` (the
     workspace, which then must not be used for anything else).  final_states may
-    be initial_states; otherwise outputs share no memory with inputs."""
+    be initial_states; otherwise outputs share no memory with inputs.  With bf16
+    tensors the fp32 results (final states, dg, dbeta, d_initial_states) are off
+    by 2e-6 to 6e-6 of their norm: factors are two bf16 terms."""
     args, sizes, dt, dev = _inputs(q, k, v, g, beta, scale, initial_states, seq_idx)
     B, L, H, V, K, G = sizes
     st = _stream_of(stream, dev)
@@ -154,7 +155,8 @@ def delta_scan_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
                  else _empty((B, H, V, K), _F32, dev, stream))
     code = _call("ssd_delta_scan_bwd")(
         dout.data_ptr(), _ptr(dfinal_states), *args, B, L, H, V, K, G, dt, _ptr(saved),
-        0 if saved is None else saved.numel() * saved.element_size(), *map(_ptr, grads.values()), ws, ws_bytes, st)
+        0 if saved is None else saved.numel() * saved.element_size(), *map(_ptr, grads.values()),
+        ws, ws_bytes, st)
     if code:
         _lib.check(code)
     return grads
